@@ -42,6 +42,13 @@ DEVERR_PAGE_RANGE = 2
 DEVERR_INDEX_RANGE = 4
 DEVERR_TIMEOUT = 8
 DEVERR_FP16_RANGE = 16
+DEVERR_PAGE_POOL = 32
+DEVERR_PAGE_COUNT = 64
+
+CACHE_KV = 0
+CACHE_IDXK = 1
+CACHE_IDXK_MXFP4 = 2
+_CACHE_PAGE_BYTES = {CACHE_KV: KV_PAGE_BYTES, CACHE_IDXK: IDXK_PAGE_BYTES, CACHE_IDXK_MXFP4: IDXK_MXFP4_PAGE_BYTES}
 
 ERR = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARGUMENT", 2: "DSA_ERR_ALIGNMENT", 3: "DSA_ERR_UNSUPPORTED",
        4: "DSA_ERR_WORKSPACE_TOO_SMALL", 5: "DSA_ERR_NO_TOPK_SOURCE", 6: "DSA_ERR_CUDA", 7: "DSA_ERR_DEVICE",
@@ -69,6 +76,10 @@ class DsaBatch(ctypes.Structure):
     _fields_ = [("batch", c_int32), ("max_pages", c_int32), ("max_seq_len", c_int32),
                 ("max_q_len", c_int32), ("total_q", c_int64), ("num_pages", c_int64),
                 ("seq_len", c_void_p), ("q_start", c_void_p), ("page_table", c_void_p)]
+
+
+class DsaCache(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("kind", c_int32), ("reserved", c_int32)]
 
 
 _lib = None
@@ -122,6 +133,19 @@ _SIGS = {
                                            POINTER(c_int32)]),
     "dsa_topk_share_needs_scoring": (c_int32, [c_void_p, POINTER(c_int32)]),
     "dsa_topk_share_mtp_end": (c_int32, [c_void_p]),
+    "dsa_dense_mla_workspace_size": (c_int32, [POINTER(DsaBatch), POINTER(c_size_t)]),
+    "dsa_window_mla": (c_int32, [c_void_p, c_void_p, POINTER(DsaBatch), c_int32, c_int32, c_float, c_void_p, c_int32,
+                                 c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "dsa_tree_mla": (c_int32, [c_void_p, c_void_p, c_void_p, POINTER(DsaBatch), c_float, c_void_p, c_int32, c_void_p,
+                               c_void_p, c_size_t, c_void_p, c_void_p]),
+    "dsa_tree_commit": (c_int32, [c_void_p, c_int32, POINTER(DsaBatch), POINTER(DsaCache), c_int32, c_void_p, c_void_p,
+                                  c_void_p]),
+    "dsa_pages_reserve": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                    c_void_p, c_void_p]),
+    "dsa_pages_release": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                    c_void_p, c_void_p]),
+    "dsa_pages_fork": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                 POINTER(DsaCache), c_int32, c_void_p, c_void_p]),
     "dsa_cp_topk_merge": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p,
                                     c_void_p]),
     "dsa_cp_topk_localize": (c_int32, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -505,6 +529,141 @@ def dsa_sparse_mla_prefill(q, topk, kv_cache, batch: Batch, *, softmax_scale=1.0
                            out_dtype=DTYPE_BF16, lse=None, share=None, ws=None, dev_status=None, stream=None):
     return _mla("dsa_sparse_mla_prefill", q, topk, kv_cache, batch, softmax_scale, out, out_dtype, lse,
                 share, ws, dev_status, stream)
+
+
+# ---------------------------------------------------------------------------
+# MLA over a whole context: sliding window with sinks, draft trees.
+def dsa_dense_mla_workspace_size(batch: Batch) -> int:
+    return _ws_size("dsa_dense_mla_workspace_size", batch)
+
+
+def _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status):
+    _need(q, torch.bfloat16, "q")
+    T, dev = batch.total_q, q.device
+    _need(q, torch.bfloat16, "q", dev, T * MLA_HEADS * QK_DIM)
+    _need(kv_cache, torch.uint8, "kv_cache", dev, batch.c.num_pages * KV_PAGE_BYTES)
+    _need(batch.seq_len, torch.int32, "batch.seq_len", dev)
+    out_t = torch.float32 if out_dtype == DTYPE_F32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((T, MLA_HEADS, LATENT_DIM), dtype=out_t, device=dev)
+    _need(out, out_t, "out", dev, T * MLA_HEADS * LATENT_DIM)
+    _opt(lse, torch.float32, "lse", dev, T * MLA_HEADS)
+    _opt(dev_status, torch.int32, "dev_status", dev, 4)
+    if ws is None:
+        with torch.cuda.device(dev):
+            ws = workspace(dsa_dense_mla_workspace_size(batch), dev)
+    return out, _need(ws, torch.uint8, "ws", dev)
+
+
+def dsa_window_mla(q, kv_cache, batch: Batch, *, window: int, sinks: int = 0, softmax_scale=1.0 / 16, out=None,
+                   out_dtype=DTYPE_BF16, lse=None, ws=None, dev_status=None, stream=None):
+    """Attention of every row over the last `window` positions up to its own and
+    the context's first `sinks`.  Returns out [T, 64, 512] (allocated if not given)."""
+    out, ws = _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status)
+    _call("dsa_window_mla", q.device,
+          _ptr(q), _ptr(kv_cache), batch.ref(), window, sinks, softmax_scale, _ptr(out), out_dtype, _ptr(lse), _ptr(ws),
+          ws.numel(), _ptr(dev_status), _stream(stream, q.device))
+    return out
+
+
+def dsa_tree_mla(q, tree_mask, kv_cache, batch: Batch, *, softmax_scale=1.0 / 16, out=None, out_dtype=DTYPE_BF16,
+                 lse=None, ws=None, dev_status=None, stream=None):
+    """Attention of a draft tree's rows: the cached prefix and the new tokens whose
+    bit is set in the row's mask (int64 [T], taken as 64 bits)."""
+    out, ws = _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status)
+    _need(tree_mask, torch.int64, "tree_mask", q.device, batch.total_q)
+    _call("dsa_tree_mla", q.device,
+          _ptr(q), _ptr(tree_mask), _ptr(kv_cache), batch.ref(), softmax_scale, _ptr(out), out_dtype, _ptr(lse), _ptr(ws),
+          ws.numel(), _ptr(dev_status), _stream(stream, q.device))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Tokens and pages of the caches.
+class CacheSet:
+    """Every layer's caches that one page table of `num_pages` pages serves:
+    (uint8 tensor, CACHE_* kind) pairs, kept alive and checked here."""
+
+    def __init__(self, caches, num_pages: int):
+        self.num_pages = int(num_pages)
+        self.tensors = [t for t, _ in caches]
+        self.device = self.tensors[0].device if self.tensors else None
+        self.c = (DsaCache * max(len(caches), 1))()
+        for i, (t, kind) in enumerate(caches):
+            if kind not in _CACHE_PAGE_BYTES:
+                raise ValueError(f"cache {i} has unknown kind {kind}")
+            _need(t, torch.uint8, f"cache {i}", self.device, self.num_pages * _CACHE_PAGE_BYTES[kind])
+            self.c[i] = DsaCache(t.data_ptr(), kind, 0)
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+
+def _caches(caches: CacheSet, num_pages: int, dev):
+    if len(caches) and (caches.device != dev or caches.num_pages < num_pages):
+        raise ValueError(f"the caches hold {caches.num_pages} pages on {caches.device}, the call needs {num_pages} on {dev}")
+    return caches.c, len(caches)
+
+
+def dsa_tree_commit(accept, batch: Batch, caches: CacheSet, *, new_seq_len=None, dev_status=None, stream=None):
+    """Move the accepted path's tokens (accept int32 [B, width], -1 ends a row) to the
+    front of each request's new tokens in every cache.  Returns new_seq_len int32 [B]."""
+    _need(accept, torch.int32, "accept")
+    dev, B = accept.device, batch.c.batch
+    if accept.dim() != 2 or accept.shape[0] != B:
+        raise ValueError(f"accept must be [{B}, width], got {tuple(accept.shape)}")
+    _need(batch.seq_len, torch.int32, "batch.seq_len", dev)
+    c, n = _caches(caches, batch.c.num_pages, dev)
+    if new_seq_len is None:
+        new_seq_len = torch.empty(B, dtype=torch.int32, device=dev)
+    _need(new_seq_len, torch.int32, "new_seq_len", dev, B)
+    _opt(dev_status, torch.int32, "dev_status", dev, 4)
+    _call("dsa_tree_commit", dev, _ptr(accept), accept.shape[1], batch.ref(), c, n, _ptr(new_seq_len), _ptr(dev_status),
+          _stream(stream, dev))
+    return new_seq_len
+
+
+def _pool_args(page_ref, page_table, lists, dev_status):
+    """Checks a pool call's tensors; returns (device, rows, max_pages, n)."""
+    _need(page_ref, torch.int32, "page_ref")
+    dev = page_ref.device
+    _need(page_table, torch.int32, "page_table", dev)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [rows, max_pages], got {tuple(page_table.shape)}")
+    n = None
+    for name, t in lists:
+        _need(t, torch.int32, name, dev)
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{name} holds {t.numel()} entries, the call's other lists {n}")
+        n = t.numel()
+    _opt(dev_status, torch.int32, "dev_status", dev, 4)
+    return dev, page_table.shape[0], page_table.shape[1], n
+
+
+def dsa_pages_reserve(page_ref, page_table, row, have_len, want_len, *, dev_status=None, stream=None):
+    """Free pages, lowest first, for request row[i] to hold want_len[i] tokens where it holds have_len[i]."""
+    dev, rows, max_pages, n = _pool_args(page_ref, page_table, (("row", row), ("have_len", have_len), ("want_len", want_len)),
+                                         dev_status)
+    _call("dsa_pages_reserve", dev, _ptr(page_ref), page_ref.numel(), _ptr(page_table), rows, max_pages, _ptr(row),
+          _ptr(have_len), _ptr(want_len), n, _ptr(dev_status), _stream(stream, dev))
+
+
+def dsa_pages_release(page_ref, page_table, row, first_page, end_page, *, dev_status=None, stream=None):
+    """Entries [first_page[i], end_page[i]) of request row[i] give their pages back."""
+    dev, rows, max_pages, n = _pool_args(page_ref, page_table,
+                                         (("row", row), ("first_page", first_page), ("end_page", end_page)), dev_status)
+    _call("dsa_pages_release", dev, _ptr(page_ref), page_ref.numel(), _ptr(page_table), rows, max_pages, _ptr(row),
+          _ptr(first_page), _ptr(end_page), n, _ptr(dev_status), _stream(stream, dev))
+
+
+def dsa_pages_fork(page_ref, page_table, src_row, dst_row, length, caches: CacheSet, *, dev_status=None, stream=None):
+    """Request dst_row[i] becomes a copy of the first length[i] tokens of src_row[i]: full
+    pages shared, the last partial one copied in every cache."""
+    dev, rows, max_pages, n = _pool_args(page_ref, page_table,
+                                         (("src_row", src_row), ("dst_row", dst_row), ("length", length)), dev_status)
+    c, n_caches = _caches(caches, page_ref.numel(), dev)
+    _call("dsa_pages_fork", dev, _ptr(page_ref), page_ref.numel(), _ptr(page_table), rows, max_pages, _ptr(src_row),
+          _ptr(dst_row), _ptr(length), n, c, n_caches, _ptr(dev_status), _stream(stream, dev))
 
 
 # ---------------------------------------------------------------------------

@@ -100,14 +100,16 @@ typedef int32_t dsa_status;
 #define DSA_DEVERR_PAGE_RANGE    2   /* page_table entry outside [0, num_pages)    */
 #define DSA_DEVERR_INDEX_RANGE   4   /* top-k index >= seq_len of its request      */
 #define DSA_DEVERR_TIMEOUT       8   /* a bounded wait inside a kernel gave up     */
-#define DSA_DEVERR_FP16_RANGE   16   /* sparse MLA computes in fp16: a latent
+#define DSA_DEVERR_FP16_RANGE   16   /* MLA computes in fp16: a latent
                                         scale outside [2^-15, 2^7], a key RoPE
                                         value with |r| >= 2^16 (clamped) or an
                                         inf / NaN in q makes an operand inexact.
                                         q itself is scaled per row by a power of
                                         two, so any finite q is in range        */
+#define DSA_DEVERR_PAGE_POOL    32   /* no free page was left for a request       */
+#define DSA_DEVERR_PAGE_COUNT   64   /* a released page's count was not positive  */
 
-/* Output dtypes of the sparse MLA calls. */
+/* Output dtypes of the MLA calls. */
 #define DSA_DTYPE_BF16 0
 #define DSA_DTYPE_F32  1
 
@@ -464,6 +466,121 @@ dsa_status dsa_topk_share_mtp_begin(dsa_topk_share* s, int32_t enabled, int32_t 
                                     int32_t seed_width, int32_t* reuse_on);
 dsa_status dsa_topk_share_needs_scoring(const dsa_topk_share* s, int32_t* needs);
 dsa_status dsa_topk_share_mtp_end(dsa_topk_share* s);
+
+/* ---- MLA over a whole context: sliding window with sinks, draft trees ----------
+ * The pages have no counterpart of these calls.  They are the attention of
+ * dsa_sparse_mla_* without a top-k list, for what reads a latent cache densely:
+ * windowed layers and draft models, draft steps with several candidates, and
+ * contexts short enough that the top-2048 is everything.  For query row i
+ * (request r, position p = seq_len - q_len + t) and head h < 64, over the
+ * visible positions j:
+ *   S_hj = softmax_scale * <q_ih, k_j>,  k_j = [c_j * scale | rope_j] (576 dims)
+ *   out_ih = sum_j softmax_j(S_hj) c_j,  lse_ih = log sum_j exp(S_hj)
+ * A row that sees nothing gives out = 0 and lse = -inf.  Softmax statistics and
+ * accumulation are fp32; probabilities are rounded to fp16 for the product with
+ * the latents, as in sparse MLA.
+ * dsa_window_mla: j <= p and (j < sinks or j > p - window): the last `window`
+ *   positions up to the row's own, and the context's first `sinks`.
+ *   window >= 1, sinks >= 0; window >= max_seq_len is causal attention over the
+ *   whole context.  q_len is 1 for decoding, any for verify and prefill.
+ * dsa_tree_mla: the request's q_len <= 64 new tokens are the nodes of a draft
+ *   tree (or any other pattern).  Row i sees every position of the cached
+ *   prefix, j < seq_len - q_len, and new token u (position seq_len - q_len + u)
+ *   when bit u of tree_mask[i] is set: its ancestors and itself, in a tree.
+ *   Bits at and above q_len are ignored.  max_q_len above 64 returns
+ *   DSA_ERR_UNSUPPORTED.
+ * Only pages that hold a visible position are read: the others' page-table
+ * entries may be -1 (given back).  Cache rows that a row does not see may hold
+ * anything.  A page id outside the cache is recorded and its positions are not
+ * seen; positions at and above 64 * max_pages likewise (DSA_DEVERR_INDEX_RANGE).
+ * Rows at and above q_start[B] (a padded batch) are left as they were.
+ *   q         device bf16 [T,64,576];  tree_mask device uint64 [T], 8-byte aligned
+ *   kv_cache  device uint8 [num_pages * 41984], 16-byte aligned
+ *   out       device [T,64,512], bf16 or fp32 per out_dtype
+ *   lse       device fp32 [T,64] or NULL
+ *   ws        device workspace of dsa_dense_mla_workspace_size() bytes, sized for
+ *             the SM count of the device current at the size call; nothing in
+ *             it has to start at zero or is kept between calls               */
+dsa_status dsa_dense_mla_workspace_size(const dsa_batch* b, size_t* bytes);
+dsa_status dsa_window_mla(const void* q, const uint8_t* kv_cache, const dsa_batch* b, int32_t window,
+                          int32_t sinks, float softmax_scale, void* out, int32_t out_dtype, float* lse,
+                          void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+dsa_status dsa_tree_mla(const void* q, const uint64_t* tree_mask, const uint8_t* kv_cache, const dsa_batch* b,
+                        float softmax_scale, void* out, int32_t out_dtype, float* lse,
+                        void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ---- Tokens and pages of the caches -------------------------------------------
+ * The pages have no counterpart of these calls.  They keep what a step leaves
+ * in the paged caches in order without the host reading anything back, so that
+ * they can be captured into the same graph as the step.
+ *
+ * A cache list names every layer's caches that one page table serves; a call
+ * treats them all alike, in one launch per 128 caches.  The list itself lives
+ * on the host and is read before the call returns.
+ *
+ * dsa_tree_commit: after a verify step, the tokens of the accepted path move to
+ *   the front of the request's new tokens: with P = seq_len[r] - q_len[r], the
+ *   cache rows of position P + accept[r, k] are copied to position P + k, for
+ *   k = 0, 1, .. up to the first negative entry of accept[r].  Every row is read
+ *   before any is written, so accept[r] may be in any order.  An entry at or
+ *   above q_len[r] ends the list and is recorded (DSA_DEVERR_INDEX_RANGE).
+ *   new_seq_len[r] = P + (entries kept).  The new tokens' pages must belong to
+ *   one request only.  A position without a page is skipped and recorded.
+ *     accept      device int32 [B, width], 0 <= width <= 64
+ *     new_seq_len device int32 [B] or NULL
+ *
+ * The pool of pages is an array of counts, one per page: how many page-table
+ * entries hold it.  A page whose count is 0 is free.  A pool starts as zeros and
+ * is changed by the three calls below alone (or by the caller, to set pages
+ * aside).  Free pages are taken in ascending order, for the call's requests in
+ * their order, so a call's result depends on nothing but its inputs.
+ *     page_ref   device int32 [num_pages], 16-byte aligned
+ *     page_table device int32 [rows, max_pages]; free entries hold -1
+ * dsa_pages_reserve: pages for request row[i] to hold want_len[i] tokens where
+ *   it holds have_len[i]: the entries from ceil(have_len / 64) up to
+ *   ceil(want_len / 64).  Entry e of the call (counted over its requests in
+ *   order) takes the e-th free page; one that already holds a page keeps it.
+ *   When the pool is used up the entry stays -1 and is recorded
+ *   (DSA_DEVERR_PAGE_POOL).  Only the first mention of a row counts; others,
+ *   rows outside [0, rows) and lengths above 64 * max_pages are recorded
+ *   (DSA_DEVERR_INDEX_RANGE; a length is cut to 64 * max_pages).
+ * dsa_pages_release: entries [first_page[i], end_page[i]) of request row[i] give
+ *   their pages back and become -1; entries that are -1 already, or lie outside
+ *   [0, max_pages), are passed over.  Whole requests, a rejected tail and the
+ *   pages that a window has left behind are all such ranges.  A page whose count
+ *   is not positive is recorded (DSA_DEVERR_PAGE_COUNT) and stays free.
+ * dsa_pages_fork: request dst_row[i] becomes a copy of the first length[i]
+ *   tokens of request src_row[i]: the full pages are shared (their counts go
+ *   up), a last, partial page is copied into a free page, rows [0, length % 64)
+ *   in every cache of the list, and every further entry becomes -1.  dst rows
+ *   must be released before: what they hold is overwritten.  An entry of the
+ *   source that is -1 gives -1.  A dst row that is named twice keeps its first
+ *   mention; one that is also a source of the call, and rows outside [0, rows),
+ *   are passed over; both are recorded (DSA_DEVERR_INDEX_RANGE).  Lengths are
+ *   cut to 64 * max_pages and recorded likewise.
+ *     row, have_len, want_len, first_page, end_page, src_row, dst_row, length
+ *                device int32 [n]; n <= 4096 for reserve and fork
+ *                (DSA_ERR_UNSUPPORTED beyond)                                  */
+#define DSA_CACHE_KV         0      /* latent rows,  DSA_KV_PAGE_BYTES             */
+#define DSA_CACHE_IDXK       1      /* FP8 index-K,  DSA_IDXK_PAGE_BYTES           */
+#define DSA_CACHE_IDXK_MXFP4 2      /* MXFP4 index-K, DSA_IDXK_MXFP4_PAGE_BYTES    */
+typedef struct dsa_cache {
+    uint8_t* data;              /* device, 16-byte aligned, num_pages pages         */
+    int32_t  kind;              /* DSA_CACHE_*                                      */
+    int32_t  reserved;          /* 0                                                */
+} dsa_cache;
+dsa_status dsa_tree_commit(const int32_t* accept, int32_t width, const dsa_batch* b, const dsa_cache* caches,
+                           int32_t n_caches, int32_t* new_seq_len, int32_t* dev_status, void* stream);
+dsa_status dsa_pages_reserve(int32_t* page_ref, int64_t num_pages, int32_t* page_table, int32_t rows,
+                             int32_t max_pages, const int32_t* row, const int32_t* have_len,
+                             const int32_t* want_len, int32_t n, int32_t* dev_status, void* stream);
+dsa_status dsa_pages_release(int32_t* page_ref, int64_t num_pages, int32_t* page_table, int32_t rows,
+                             int32_t max_pages, const int32_t* row, const int32_t* first_page,
+                             const int32_t* end_page, int32_t n, int32_t* dev_status, void* stream);
+dsa_status dsa_pages_fork(int32_t* page_ref, int64_t num_pages, int32_t* page_table, int32_t rows,
+                          int32_t max_pages, const int32_t* src_row, const int32_t* dst_row,
+                          const int32_t* length, int32_t n, const dsa_cache* caches, int32_t n_caches,
+                          int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

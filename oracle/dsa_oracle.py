@@ -749,3 +749,118 @@ def latent_prepare(kv_c: np.ndarray, k_pe: np.ndarray, pos: np.ndarray, gamma=No
     r = rope_interleaved(np.asarray(k_pe, dtype=np.float64), pos, rope_base, ROPE_DIM)
     codes, scales = latent_quantize(c)
     return codes, scales, f64_to_bf16_bits(r)
+
+
+# ----------------------------------------------------------------------------
+# MLA over a whole context (sliding window with sinks, draft trees), the tokens
+# of an accepted path, and the pool of pages: plain definitions, one request,
+# entry and page at a time.  The pages have no counterpart of these steps.
+# ----------------------------------------------------------------------------
+def window_positions(p: int, window: int, sinks: int) -> np.ndarray:
+    """Positions that a row at position p sees: the last `window` up to its own
+    and the context's first `sinks`."""
+    return np.array([j for j in range(max(p, -1) + 1) if j < sinks or j > p - window], dtype=np.int64)
+
+
+def tree_positions(prefix: int, mask: int, q_len: int) -> np.ndarray:
+    """The cached prefix and the new tokens whose bit is set (bits at and above q_len are ignored)."""
+    return np.array(list(range(prefix)) + [prefix + u for u in range(q_len) if mask >> u & 1], dtype=np.int64)
+
+
+def tree_commit(rows: np.ndarray, prefix: int, q_len: int, accept) -> tuple:
+    """rows [n, ...]: one request's cache rows by position.  Returns (rows after
+    the move, kept): row prefix + accept[k] at prefix + k, read before any write."""
+    kept = []
+    for a in accept:
+        if a < 0 or a >= q_len:
+            break
+        kept.append(int(a))
+    out = rows.copy()
+    for k, a in enumerate(kept):
+        out[prefix + k] = rows[prefix + a]
+    return out, len(kept)
+
+
+def pool_free(ref) -> list:
+    return [p for p, c in enumerate(ref) if c == 0]
+
+
+def pages_reserve(ref, table, row, have_len, want_len):
+    """Entries in the call's order against the free pages in ascending order; returns the errors' count."""
+    entries, errors, named = [], 0, set()
+    for r, h, w in zip(row, have_len, want_len):
+        if not 0 <= r < table.shape[0] or r in named:
+            errors += 1
+            named.add(r)
+            continue
+        named.add(r)
+        hi = -(-max(w, 0) // PAGE_TOKENS)
+        if hi > table.shape[1]:
+            errors += 1
+            hi = table.shape[1]
+        entries += [(r, k) for k in range(-(-max(h, 0) // PAGE_TOKENS), hi)]
+    free = pool_free(ref)
+    for e, (r, k) in enumerate(entries):
+        if table[r, k] >= 0:
+            continue
+        if e >= len(free):
+            errors += 1
+            continue
+        table[r, k] = free[e]
+        ref[free[e]] = 1
+    return errors
+
+
+def pages_release(ref, table, row, first, end):
+    errors = 0
+    for r, a, b in zip(row, first, end):
+        if not 0 <= r < table.shape[0]:
+            errors += 1
+            continue
+        for k in range(max(a, 0), min(b, table.shape[1])):
+            p, table[r, k] = table[r, k], -1
+            if p < 0:
+                continue
+            if p >= len(ref) or ref[p] <= 0:
+                errors += 1
+            else:
+                ref[p] -= 1
+    return errors
+
+
+def pages_fork(ref, table, src, dst, length):
+    """Returns (errors, copies): copies holds (src page, dst page, rows) of the partial pages."""
+    errors, wanted, counts = 0, [], []
+    for f, (s, d, n) in enumerate(zip(src, dst, length)):
+        ok = 0 <= s < table.shape[0] and 0 <= d < table.shape[0] and d not in src and d not in dst[:f]
+        counts.append(ok)
+        if not ok:
+            errors += 1
+            continue
+        cut = min(max(n, 0), table.shape[1] * PAGE_TOKENS)
+        errors += cut != n
+        if cut % PAGE_TOKENS and table[s, cut // PAGE_TOKENS] >= len(ref):
+            errors += 1
+        elif cut % PAGE_TOKENS and table[s, cut // PAGE_TOKENS] >= 0:
+            wanted.append(f)
+    free, copies, taken = pool_free(ref), [], {}
+    for f, p in zip(wanted, free):
+        taken[f] = p
+        ref[p] = 1
+    errors += max(0, len(wanted) - len(free))
+    for f, (s, d, n) in enumerate(zip(src, dst, length)):
+        if not counts[f]:
+            continue
+        full, part = divmod(min(max(n, 0), table.shape[1] * PAGE_TOKENS), PAGE_TOKENS)
+        old = table[s].copy()
+        table[d] = -1
+        for k in range(full):
+            if old[k] >= len(ref):
+                errors += 1
+            elif old[k] >= 0:
+                table[d, k] = old[k]
+                ref[old[k]] += 1
+        if f in taken:
+            table[d, full] = taken[f]
+            copies.append((int(old[full]), taken[f], part))
+    return errors, copies

@@ -1,0 +1,308 @@
+"""GPU parity of dsa_window_mla and dsa_tree_mla with the fp64 oracle.
+
+Cache rows that no row of their request sees hold NaN codes, infinite scales
+and NaN RoPE dims, and pages without a visible position are -1, so a read in a
+masked place shows.
+
+Tolerances, per row and head (weights p_j, latents c_j, scores S_j):
+* scores: 576 products summed in fp32 in steps of 16 (36 additions, each off by
+  at most 2^-23 of the largest partial sum, which sum |q_d k_d| bounds) and one
+  fp32 product with the scale: dS = 40 * 2^-23 * scale * max_j sum_d |q_d k_d|;
+* lse: dS, the exponentials and their fp32 sums (2^-20), the logarithm and the
+  final sum (2^-22 of the value);
+* out: sum_j p_j |c_j| times the rounding of p_j to fp16 (2^-11), twice dS (in
+  p_j and in the sum) and 2^-18 for exponentials, sums and the division; a p_j below
+  fp16's smallest step is off by at most 2^-25 of the largest: 2^-25 sum_j |c_j|;
+* bf16 outputs add half a step, 2^-8 of the value.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import dsa_sparse_attention_indexer_gb300 as D
+from oracle import dsa_oracle as O
+from tests.oracle_side import bf16_bits, check_attention, f64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SENTINEL = -77.0
+
+
+def make_case(seed, seq, q_len, sees, *, q_scale=1.0, pad_rows=0, spare_pages=3, full_table=False):
+    """sees(r, t) -> positions that row t of request r sees.  Latent caches, batch
+    descriptor and queries on the device; per row its positions and latent rows."""
+    g = torch.Generator().manual_seed(seed)
+    B = len(seq)
+    width = max(1, max((L + 63) // 64 for L in seq))
+    vis = [[np.asarray(sees(r, t), dtype=np.int64) for t in range(q_len[r])] for r in range(B)]
+    need = np.zeros((B, width), bool)
+    for r in range(B):
+        for v in vis[r]:
+            need[r, v // 64] = True
+        if full_table:
+            need[r, :(seq[r] + 63) // 64] = True
+    pages = int(need.sum()) + spare_pages
+    perm = torch.randperm(pages, generator=g).numpy()
+    table = np.full((B, width), -1, np.int32)
+    table[need] = perm[:need.sum()]
+    cache = np.zeros((pages * 64, 656), np.uint8)
+    cache[:, :512] = 0x7f                                            # E4M3 NaN
+    cache[:, 512:528] = np.frombuffer(np.array([np.inf] * 4, np.float32).tobytes(), np.uint8)
+    cache[:, 528:] = np.frombuffer(np.array([0x7fc0] * 64, np.uint16).tobytes(), np.uint8)
+    cache = cache.reshape(pages, -1)
+    rows = []
+    for r in range(B):
+        seen = np.unique(np.concatenate([np.zeros(0, np.int64)] + vis[r]))
+        c = f64((torch.randn(len(seen), 512, generator=g) * torch.exp(torch.randn(len(seen), 1, generator=g))).to(torch.bfloat16))
+        codes, scales = O.latent_quantize(c)
+        rope = torch.randn(len(seen), 64, generator=g).to(torch.bfloat16)
+        slots = table[r, seen // 64].astype(np.int64) * 64 + seen % 64
+        if len(seen):
+            O.latent_cache_write(cache, slots, codes, scales, bf16_bits(rope))
+        for v in vis[r]:
+            rows.append((v, O.latent_cache_read_rows(cache, table[r], v) if len(v) else np.zeros((0, 576))))
+    T = len(rows)
+    q = (torch.randn(T + pad_rows, 64, 576, generator=g) * q_scale).to(torch.bfloat16)
+    start = np.concatenate([[0], np.cumsum(q_len)]).astype(np.int32)
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(DEV)  # noqa: E731
+    batch = D.Batch(dev(np.array(seq, np.int32)), dev(start), dev(table), pages, max_seq_len=max(max(seq), 1),
+                    max_q_len=max(max(q_len), -(-(T + pad_rows) // B)), total_q=T + pad_rows)
+    return dict(T=T, rows=rows, q=q, dq=q.to(DEV), kv=dev(cache.reshape(-1)), batch=batch, pages=pages, table=table)
+
+
+def reference(q, kv, scale=1.0 / 16):
+    """(out, lse, bound of an fp32 output, bound of lse) of one row, in 64 bits."""
+    if len(kv) == 0:
+        return np.zeros((64, 512)), np.full(64, -np.inf), np.zeros((64, 512)), np.zeros(64)
+    out, lse = O.sparse_mla(q, np.arange(len(kv)), kv, len(kv), scale)
+    s = (q @ kv.T) * scale
+    p = np.exp(s - lse[:, None])
+    dS = 40 * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(kv).T).max(1)
+    c = np.abs(kv[:, :512])
+    bound = (p @ c) * (2.0 ** -11 + 2 * dS[:, None] + 2.0 ** -18) + 2.0 ** -25 * p.max(1)[:, None] * c.sum(0)
+    return out, lse, bound + 1e-30, dS + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse)
+
+
+def compare(c, out, lse, scale=1.0 / 16, kv_of=lambda i, kv: kv):
+    out, lse = f64(out), f64(lse) if lse is not None else None
+    bf16 = 2.0 ** -8
+    for i, (_, kv) in enumerate(c["rows"]):
+        ref, z, tol, ztol = reference(f64(c["q"][i]), kv_of(i, kv), scale)
+        if c["bf16"]:
+            tol = tol + bf16 * (np.abs(ref) + tol)
+        err = np.abs(out[i] - ref)
+        assert (err <= tol).all(), f"row {i}: {(err > tol).sum()} values off, worst {np.max(err / np.maximum(tol, 1e-30)):.2f} of the bound"
+        if not c["bf16"] and len(kv):
+            check_attention(out[i], ref, what=f"row {i}")
+        if lse is not None:
+            assert np.array_equal(np.isinf(lse[i]), np.isinf(z)), f"row {i}"
+            f = np.isfinite(z)
+            assert (np.abs(lse[i][f] - z[f]) <= ztol[f]).all(), f"row {i}: lse off by {np.max(np.abs(lse[i][f] - z[f])):.2e}"
+
+
+def run(c, call, f32=True, stream=None, ws=None, want_status=0, scale=1.0 / 16):
+    n = c["batch"].total_q
+    out = torch.full((n, 64, 512), SENTINEL, dtype=torch.float32 if f32 else torch.bfloat16, device=DEV)
+    lse = torch.full((n, 64), SENTINEL, dtype=torch.float32, device=DEV)
+    st = D.new_device_status(DEV)
+    kw = dict(out=out, lse=lse, out_dtype=D.DTYPE_F32 if f32 else D.DTYPE_BF16, dev_status=st, stream=stream, ws=ws,
+              softmax_scale=scale)
+    call(c, kw)
+    c["bf16"] = not f32
+    got = D.dsa_device_status_read(st, stream)
+    assert got[0] == want_status, got
+    return out, lse
+
+
+def window_call(window, sinks):
+    return lambda c, kw: D.dsa_window_mla(c["dq"], c["kv"], c["batch"], window=window, sinks=sinks, **kw)
+
+
+def tree_call(masks):
+    m = torch.tensor([x - (1 << 64) if x >> 63 else x for x in masks], dtype=torch.int64).to(DEV)
+    return lambda c, kw: D.dsa_tree_mla(c["dq"], m, c["kv"], c["batch"], **kw)
+
+
+def window_case(seed, seq, q_len, window, sinks, **kw):
+    return make_case(seed, seq, q_len, lambda r, t: O.window_positions(seq[r] - q_len[r] + t, window, sinks), **kw)
+
+
+WINDOW = [
+    # contexts and windows around the page and tile edges, one row each
+    ([1], [1], 1, 0), ([1], [1], 64, 9), ([63, 64, 65, 128, 129], [1] * 5, 64, 0), ([63, 64, 65, 128, 129], [1] * 5, 65, 1),
+    ([200, 257], [1, 1], 1, 0), ([200, 257], [1, 1], 1, 1), ([200, 257], [1, 1], 63, 64), ([500, 130], [1, 1], 70, 65),
+    # the sinks reach into the window, or past the row
+    ([300], [1], 100, 250), ([300, 40], [1, 1], 10, 1000), ([300], [1], 2 ** 31 - 1, 0), ([300], [1], 2 ** 31 - 1, 2 ** 31 - 1),
+    # several rows a request, requests without rows, requests that are all new
+    ([130, 64, 7, 0, 900], [5, 64, 7, 0, 3], 50, 3), ([700], [150], 129, 17), ([1, 0, 2], [1, 0, 2], 8, 8),
+    # many tiles and a gap, ragged; more rows than SMs
+    ([5000, 1717, 3001], [1, 2, 1], 2500, 100), ([90 + 3 * r for r in range(200)], [1] * 200, 40, 5),
+]
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("seq,q_len,window,sinks", WINDOW)
+def test_window(seq, q_len, window, sinks, f32):
+    c = window_case(len(seq) * 1000 + window % 997, seq, q_len, window, sinks)
+    compare(c, *run(c, window_call(window, sinks), f32))
+
+
+def rand_tree(rng, n):
+    masks = []
+    for u in range(n):
+        p = rng.integers(-1, u) if u else -1
+        masks.append((masks[p] if p >= 0 else 0) | 1 << u)
+    return masks
+
+
+def tree_case(seed, seq, masks, **kw):
+    q_len = [len(m) for m in masks]
+    c = make_case(seed, seq, q_len, lambda r, t: O.tree_positions(seq[r] - q_len[r], masks[r][t], q_len[r]), **kw)
+    return c, tree_call([x for m in masks for x in m])
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("seq,nodes", [([9], [8]), ([1], [1]), ([64, 65, 190], [1, 1, 64]), ([64], [64]), ([1000, 77, 300], [16, 7, 33]),
+                                       ([2500, 2600], [64, 20]), ([40 + r for r in range(30)], [8] * 30)])
+def test_tree(seq, nodes, f32):
+    rng = np.random.default_rng(sum(seq))
+    c, call = tree_case(sum(nodes), seq, [rand_tree(rng, n) for n in nodes])
+    compare(c, *run(c, call, f32))
+
+
+def test_tree_masks_that_are_no_tree():
+    """Any pattern: rows that see nothing, only the prefix, later nodes, not themselves; bits beyond the request's tokens."""
+    full = (1 << 64) - 1
+    masks = [[0, 0, 1], [full, 0, full & ~7, 1 << 63], [full] * 64, [1 << 63 | 5] * 64]
+    seq = [3, 100, 64, 130]
+    c, call = tree_case(5, seq, masks)
+    compare(c, *run(c, call))
+
+
+def test_chain_of_drafts_is_causal_attention():
+    """A tree that is a chain sees what causal rows see: the two calls agree."""
+    seq, n = [300, 1000], [6, 6]
+    c, call = tree_case(8, seq, [[(2 << u) - 1 for u in range(k)] for k in n])
+    a, za = run(c, call)
+    b, zb = run(c, window_call(1 << 20, 0))
+    compare(c, a, za)
+    assert torch.allclose(a, b, rtol=0, atol=0) and torch.equal(za, zb)
+
+
+def test_rows_with_no_visible_position_and_a_padded_batch():
+    """Rows behind q_start[B] keep what was there; a request shorter than its new tokens sees nothing."""
+    c = window_case(11, [70, 130], [2, 1], 40, 2, pad_rows=5)
+    out, lse = run(c, window_call(40, 2))
+    compare(c, out, lse)
+    assert (out[3:] == SENTINEL).all() and (lse[3:] == SENTINEL).all()
+    c["batch"].seq_len[0] = 1                                        # q_len 2 > seq_len 1
+    out, lse = run(c, window_call(40, 2))
+    assert (out[:2] == 0).all() and torch.isinf(lse[:2]).all() and (lse[:2] < 0).all()
+
+
+@pytest.mark.parametrize("scale,q_scale", [(1.0 / 16, 3e4), (1.0 / 16, 1e-6), (4.0, 1.0), (1e-3, 1e3), (1e-30, 1.0)])
+def test_magnitudes(scale, q_scale):
+    """Queries far outside fp16's range and sharp or flat softmaxes."""
+    c = window_case(3, [400, 90], [1, 2], 300, 3, q_scale=q_scale)
+    compare(c, *run(c, window_call(300, 3), scale=scale), scale=scale)
+
+
+def test_bad_pages_are_recorded_and_not_seen():
+    c = window_case(21, [400, 700], [1, 3], 250, 70, full_table=True)
+    table = c["batch"].page_table
+    for r, k, bad in ((0, 4, -1), (1, 0, c["pages"]), (1, 10, 2 ** 31 - 1)):
+        table[r, k] = bad
+    out, lse = run(c, window_call(250, 70), want_status=D.DEVERR_PAGE_RANGE)
+    bad = {0: [4], 1: [0, 10]}
+
+    def kept(i, kv):
+        return kv[~np.isin(c["rows"][i][0] // 64, bad[0 if i == 0 else 1])]
+
+    compare(c, out, lse, kv_of=kept)
+
+
+def test_a_row_whose_only_page_is_bad_sees_nothing():
+    c = window_case(22, [40, 40], [1, 1], 64, 0)
+    c["batch"].page_table[1, 0] = -1
+    out, lse = run(c, window_call(64, 0), want_status=D.DEVERR_PAGE_RANGE)
+    compare(c, out, lse, kv_of=lambda i, kv: kv if i == 0 else kv[:0])
+
+
+def test_contexts_longer_than_the_table_are_cut():
+    c = window_case(23, [128, 100], [1, 1], 100, 0)
+    c["batch"].seq_len[0] = 200                                      # the table holds 128 positions
+    out, lse = run(c, window_call(172, 0), want_status=D.DEVERR_INDEX_RANGE)
+    ok = window_case(23, [128, 100], [1, 1], 100, 0)
+    good, z = run(ok, window_call(100, 0))
+    assert torch.equal(out, good) and torch.equal(lse, z)
+
+
+def test_cache_beyond_32_bits():
+    """A pool of 4.6 GB with the pages of the call at its far end."""
+    c = window_case(31, [500], [2], 400, 10)
+    far, off = 110_000, 110_000 - c["pages"]
+    kv = torch.empty(far * D.KV_PAGE_BYTES, dtype=torch.uint8, device=DEV)
+    kv[off * D.KV_PAGE_BYTES:] = c["kv"]
+    t = c["batch"].page_table
+    t[t >= 0] += off
+    b = c["batch"].c
+    c["kv"], c["batch"] = kv, D.Batch(c["batch"].seq_len, c["batch"].q_start, t, far, max_seq_len=b.max_seq_len, max_q_len=2, total_q=2)
+    compare(c, *run(c, window_call(400, 10)))
+
+
+def test_other_streams_dirty_workspaces_and_graphs_that_share_one():
+    a = window_case(51, [900, 333], [1, 1], 700, 9)
+    b, call_b = tree_case(52, [2000, 100], [rand_tree(np.random.default_rng(1), 20), [1, 3]])
+    call_a = window_call(700, 9)
+    ws = torch.empty(max(D.dsa_dense_mla_workspace_size(x["batch"]) for x in (a, b)), dtype=torch.uint8, device=DEV)
+    want_a, want_b = run(a, call_a), run(b, call_b)
+    compare(a, *want_a)
+    compare(b, *want_b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for fill in (0, 0xAB, 0xFF):
+        with torch.cuda.stream(side):
+            ws.fill_(fill)
+        got = run(a, call_a, stream=side, ws=ws)
+        assert torch.equal(got[0], want_a[0]) and torch.equal(got[1], want_a[1])
+    # two captured graphs on one workspace, replayed in turn with the inputs changed in between
+    side.synchronize()
+    outs = {}
+    graphs = {}
+    for name, x, call in (("a", a, call_a), ("b", b, call_b)):
+        n = x["batch"].total_q
+        outs[name] = (torch.zeros(n, 64, 512, device=DEV), torch.zeros(n, 64, device=DEV))
+        graphs[name] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[name]):
+            call(x, dict(out=outs[name][0], lse=outs[name][1], out_dtype=D.DTYPE_F32, ws=ws))
+    for name, want in (("a", want_a), ("b", want_b), ("b", want_b), ("a", want_a)):
+        outs[name][0].zero_()
+        graphs[name].replay()
+        assert torch.equal(outs[name][0], want[0]) and torch.equal(outs[name][1], want[1])
+    a["dq"].neg_()
+    neg = run(a, call_a)
+    graphs["a"].replay()
+    assert torch.equal(outs["a"][0], neg[0]) and not torch.equal(neg[0], want_a[0])
+
+
+def test_results_do_not_change_from_call_to_call():
+    c = window_case(61, [3000, 50, 1200], [2, 1, 9], 1100, 30)
+    first = run(c, window_call(1100, 30))
+    for _ in range(5):
+        again = run(c, window_call(1100, 30))
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_binding_refuses_short_and_foreign_tensors():
+    c = window_case(71, [100], [1], 100, 0)
+    with pytest.raises(ValueError):
+        D.dsa_window_mla(c["dq"], c["kv"][:-1], c["batch"], window=4)
+    with pytest.raises(ValueError):
+        D.dsa_window_mla(c["dq"].transpose(1, 2), c["kv"], c["batch"], window=4)
+    with pytest.raises(TypeError):
+        D.dsa_tree_mla(c["dq"], torch.zeros(1, dtype=torch.int32, device=DEV), c["kv"], c["batch"])
+    with pytest.raises(ValueError):
+        D.dsa_tree_mla(c["dq"], torch.zeros(0, dtype=torch.int64, device=DEV), c["kv"], c["batch"])
+    with pytest.raises(D.DsaError):
+        D.dsa_window_mla(c["dq"], c["kv"], c["batch"], window=0)
