@@ -1,15 +1,54 @@
 // MLA over a whole context of the paged latent cache: a sliding window with the
 // context's first tokens (sinks), and trees of drafted tokens.
 //   S_hj = scale * <q_h, [c_j * s_j | r_j]>,  out_h = sum_j softmax_j(S_hj) c_j
-// over the positions j that the query row sees, 64 heads of 576 dims.
+// over the positions j that the query row sees, 64 heads of 576 dims, in one
+// pass over the pages with a running maximum and sum per head.
+//
+// Work split: a row's visible pages are taken two at a time, as tiles of 128
+// tokens.  The tiles of all rows form one line that is cut into equal shares,
+// one per CTA, so ragged contexts and any number of rows fill the GPU alike;
+// every CTA counts the tiles itself (a block scan over the rows).  A row that
+// several shares hold leaves one partial (O, running max, sum) per share, and a
+// second kernel merges them by their log-sum-exp.
+//
+// Per tile, in transposed form so that tokens are the MMA rows:
+//   S^T = K Q^T      tcgen05.mma kind::f16, M = 128 tokens, N = 64 heads, K = 576
+//   O^T += V^T P^T   M = 4 x 128 latent dims, N = 64 heads, K = 128 tokens,
+//                    A = the same tile read MN-major; 256 TMEM columns stay
+//                    resident for the row
+// The tile in fp16 (147 KB) and the row's Q (74 KB) fill shared memory, so the
+// tile is recycled group by group: the loaders write 128 latent dims of the
+// next tile as soon as the P.V MMAs of those dims have completed, and S^T of
+// the next tile starts behind the last P.V.  P^T takes the place of the tile's
+// RoPE block, which S^T has read by then.
+//
+// Roles (17 warps):
+//   warps 0-7   softmax and epilogue: a thread owns one token (TMEM lane) and 32
+//               heads.  P is formed against a reference that lags the maximum by
+//               up to 2^8 before O^T is rescaled, and shifted up by 2^7 so that
+//               fp16 holds probabilities down to 2^-32 of the largest.
+//   warps 8-15  loaders: read the pages into registers two groups ahead (whole pages
+//               are prefetched into L2 two tiles ahead), dequantise into the
+//               128-byte-swizzled tile (exact for scales in [2^-15, 2^7]) and
+//               convert each row's Q, scaled by the power of two that puts its
+//               largest |q| in [2^14, 2^15).  Rows that are not seen become zeros.
+//   warp 16     issues the MMAs.
+// Every wait is time-bounded; a timeout is recorded and the CTA winds down.
+#include <algorithm>
+
 #include "dsa_internal.cuh"
 #include "indexer_common.cuh"
+#include "mla_common.cuh"
+#include "select_common.cuh"
+#include "sm100.cuh"
 
 namespace dsa {
 
 int device_sm_count();
 
 namespace mld {
+
+struct Meta;
 
 // Which positions a launch's rows see: window form (tree == NULL) or tree form.
 struct View {
@@ -22,23 +61,26 @@ struct Args {
     const uint8_t* kv;          // latent cache
     BatchDev b;
     View view;
-    float scale;
+    float scale_log2;
     void* out;
     int out_f32;
     float* lse;
+    float* part_o;              // [2 G, 64, 512]: unnormalised outputs of cut rows, two pieces per share
+    float2* part_ml;            // [2 G, 64]: reference (log2 units), sum
+    Meta* meta;          // [G]
     int32_t* st;
 };
 
 // One row's visible positions: j < sink_end or first <= j < end, and new token
-// u at position prefix + u when bit u of mask is set.  They lie in `tiles`
+// u at position prefix + u when bit u of mask is set.  They lie in `pages`
 // pages: the first sink_pages, then those from first_page on.
 struct Row {
     int32_t r;                  // request
     int32_t sink_end, first, end;
     int32_t prefix;
     uint64_t mask;
-    int32_t sink_pages, first_page, tiles;
-    __device__ __forceinline__ int page(int tile) const { return tile < sink_pages ? tile : first_page + tile - sink_pages; }
+    int32_t sink_pages, first_page, pages;
+    __device__ __forceinline__ int page(int u) const { return u < sink_pages ? u : first_page + u - sink_pages; }
     __device__ __forceinline__ bool sees(int j) const {
         if (j < sink_end || (j >= first && j < end)) return true;
         const unsigned u = (unsigned)(j - prefix);
@@ -46,7 +88,7 @@ struct Row {
     }
 };
 
-// Row `row` of the batch.  A row that sees nothing keeps one (empty) tile, so
+// Row `row` of the batch.  A row that sees nothing keeps one (empty) page, so
 // that every row of a request is written; rows behind the last request have none.
 __device__ __forceinline__ Row row_view(const BatchDev& b, const View& v, int64_t row, int32_t* st) {
     Row w = {};
@@ -60,7 +102,7 @@ __device__ __forceinline__ Row row_view(const BatchDev& b, const View& v, int64_
         L = (int)room;
     }
     w.prefix = b.seq_len[w.r] - qn;
-    w.tiles = 1;
+    w.pages = 1;
     if (L <= 0 || w.prefix < 0) return w;
     if (v.tree) {
         const int known = min(qn, 64);
@@ -68,7 +110,7 @@ __device__ __forceinline__ Row row_view(const BatchDev& b, const View& v, int64_
         w.end = min(w.prefix, L);
         const int64_t last = w.mask ? (int64_t)w.prefix + 64 - __clzll((long long)w.mask) : w.end;
         if (last > L) w.mask = L > w.prefix ? w.mask & ((1ull << (L - w.prefix)) - 1) : 0;
-        w.tiles = max(1, (int)((min(last, (int64_t)L) + kPage - 1) / kPage));
+        w.pages = max(1, (int)((min(last, (int64_t)L) + kPage - 1) / kPage));
         return w;
     }
     const int end = (int)min((int64_t)w.prefix + (row - qs) + 1, (int64_t)L);
@@ -77,83 +119,695 @@ __device__ __forceinline__ Row row_view(const BatchDev& b, const View& v, int64_
     w.sink_end = min(v.sinks, end);
     w.sink_pages = w.sink_end / kPage + (w.sink_end % kPage != 0);
     w.first_page = max(w.sink_pages, w.first / kPage);
-    w.tiles = max(1, w.sink_pages + max(0, (end + kPage - 1) / kPage - w.first_page));
+    w.pages = max(1, w.sink_pages + max(0, (end + kPage - 1) / kPage - w.first_page));
     return w;
 }
 
-// The plain kernel: one block per (row, 8 heads), a warp per head.  16 tokens at a
-// time are dequantised into shared memory; each warp keeps its head's query and
-// output in registers with a running maximum and sum.
-constexpr int kThreads = 256;
-constexpr int kTok = 16;
+using namespace sm100;
+using namespace mlc;
 
-__global__ void __launch_bounds__(kThreads)
-dense_mla_kernel(Args a) {
-    __shared__ float k[kTok][576];
-    __shared__ int seen[kTok];
-    const int64_t row = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y * 8 + warp;
-    const BatchDev& b = a.b;
-    const Row w = row_view(b, a.view, row, blockIdx.y == 0 && threadIdx.x == 0 ? a.st : nullptr);
-    if (w.tiles == 0) return;
-    float q[18], o[16] = {}, m = -INFINITY, l = 0.f;
-    for (int i = 0; i < 18; ++i) q[i] = bf16_bits_to_f32(a.q[(row * 64 + h) * 576 + lane + 32 * i]) * a.scale;
-    for (int t = 0; t < w.tiles; ++t) {
-        const int lp = w.page(t);
-        const int64_t pg = lp < b.max_pages ? b.page_table[(int64_t)w.r * b.max_pages + lp] : -1;
-        for (int base = 0; base < kPage; base += kTok) {
-            __syncthreads();
-            if (threadIdx.x < kTok) {
-                const int j = lp * kPage + base + threadIdx.x;
-                int s = w.sees(j) ? 1 : 0;
-                if (s && (pg < 0 || pg >= b.num_pages)) {
-                    if (blockIdx.y == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
-                    s = 0;
-                }
-                seen[threadIdx.x] = s;
+constexpr int kTok = 128;                                  // tokens per tile: two pages
+constexpr int kBlk = kTok * 128;                           // one 64-dim K-block of the tile
+constexpr int kSoftWarps = 8;                              // two per TMEM lane quarter, 32 heads each
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kLoadWarp0 = kSoftWarps;
+constexpr int kLoadWarps = 8;
+constexpr int kLoadThreads = kLoadWarps * 32;
+constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kPlanThreads = 512;                          // threads that count the rows' tiles
+constexpr int kSoftBar = 1, kLoadBar = 2, kPlanBar = 3;
+constexpr int kSteps = kTok / kLoadWarps / 4;              // a loader warp's 16 tokens, four at a time
+constexpr float kTau = 8.0f;                               // lazy-rescale threshold, log2 units
+constexpr float kShift = 7.0f;                             // P is scaled by 2^7: P <= 2^(kTau + kShift)
+constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
+constexpr uint32_t kIdescPV = idesc_f16_f32(128, 64, true, true);
+constexpr uint32_t kColS = 0;                              // TMEM: S^T [128 x 64]
+constexpr uint32_t kColO = 64;                             // TMEM: O^T 4 x [128 x 64]
+
+constexpr int kOffKV = 0;                                  // 8 latent K-blocks and the RoPE block (later P^T), [128 tokens x 128 B]
+constexpr int kOffP = kOffKV + 8 * kBlk;
+constexpr int kOffQ = kOffKV + 9 * kBlk;                   // 9 K-blocks of [64 heads x 128 B]
+constexpr int kOffRed = kOffQ + 9 * 8192;                  // [2][4 lane quarters][64 heads] fp32
+constexpr int kOffStat = kOffRed + 2 * 4 * 64 * 4;         // m_ref, l_acc, alpha [64]
+constexpr int kOffBars = kOffStat + 3 * 64 * 4;
+constexpr int kOffMisc = kOffBars + 16 * 8;
+constexpr int kSmemUsed = kOffMisc + 512;
+constexpr int kSmemAlloc = kSmemUsed + 1024;
+static_assert(kSmemAlloc <= 232448, "shared memory budget");
+static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kBlk % 1024 == 0, "swizzle atoms need 1 KB alignment");
+static_assert(kOffStat % 16 == 0, "reference maxima are read as float4");
+
+enum { B_QFULL = 0, B_FULL0, B_FULL4 = B_FULL0 + 4, B_SFULL, B_PREADY, B_PV0, B_PV3 = B_PV0 + 3, B_DRAIN, B_COUNT };
+static_assert(B_COUNT <= 16, "barrier block");
+
+struct Misc {
+    uint32_t tmem_base;
+    int32_t abort;
+    uint32_t qmax[kLoadWarps];  // per loader warp: largest bf16 magnitude of the row's q
+    float q_unscale[2];         // 2^-kq of the row's Q, by piece parity
+    int32_t bad[2];             // the tile's page (first, second half) is outside the cache
+    int32_t scratch[32];
+    int64_t total;              // tiles of the whole batch
+    int64_t row0;               // where this CTA's share begins
+    int32_t tile0;
+};
+static_assert(sizeof(Misc) <= 512, "misc block");
+
+// Where a CTA's share begins, for the merge: its first row (-1: no share) and
+// whether that row began in an earlier share.
+struct Meta {
+    int32_t row;
+    int32_t inside;
+};
+
+__device__ __forceinline__ bool soft_any(bool pred) { return bar_any<kSoftBar, kSoftThreads>(pred); }
+__device__ __forceinline__ void soft_sync() { bar_sync<kSoftBar, kSoftThreads>(); }
+__device__ __forceinline__ bool load_any(bool pred) { return bar_any<kLoadBar, kLoadThreads>(pred); }
+__device__ __forceinline__ void load_sync() { bar_sync<kLoadBar, kLoadThreads>(); }
+
+__device__ __forceinline__ int tiles_of(const Row& w) { return (w.pages + 1) >> 1; }
+
+// Counts the tiles of all rows (kPlanThreads threads, consecutive rows each)
+// and finds where share g of G begins.  Returns the share's tiles.
+__device__ __forceinline__ void plan_share(const Args& a, Misc* misc, int tid) {
+    const int64_t T = a.b.total_q;
+    const int64_t per = (T + kPlanThreads - 1) / kPlanThreads;
+    const int64_t r0 = min(T, tid * per), r1 = min(T, r0 + per);
+    int64_t mine = 0;
+    for (int64_t r = r0; r < r1; ++r) mine += tiles_of(row_view(a.b, a.view, r, nullptr));
+    // block scan in 64 bits: warps, then their totals
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((tid & 31) >= o) x += y;
+    }
+    int64_t* tot = reinterpret_cast<int64_t*>(misc->scratch);     // 16 warps
+    if ((tid & 31) == 31) tot[tid >> 5] = x;
+    bar_sync<kPlanBar, kPlanThreads>();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < (tid >> 5)) before += tot[w];
+        all += tot[w];
+    }
+    before += x - mine;
+    if (tid == 0) misc->total = all;
+    const int64_t G = min((int64_t)gridDim.x, all);
+    if ((int64_t)blockIdx.x < G) {
+        int64_t at = (int64_t)blockIdx.x * all / G;
+        if (at >= before && at < before + mine) {
+            at -= before;
+            int64_t r = r0;
+            for (;; ++r) {
+                const int n = tiles_of(row_view(a.b, a.view, r, nullptr));
+                if (at < n) break;
+                at -= n;
             }
-            __syncthreads();
-            for (int e = threadIdx.x; e < kTok * 576; e += kThreads) {
-                const int tk = e / 576, d = e % 576;
-                float x = 0.f;
-                if (seen[tk]) {
-                    const uint8_t* rp = a.kv + pg * kKvPageBytes + (int64_t)(base + tk) * kKvTokenBytes;
-                    if (d < 512) {
-                        const float sc = reinterpret_cast<const float*>(rp + 512)[d >> 7];
-                        x = e4m3x2_to_f32x2(rp[d]).x * sc;
-                    } else {
-                        x = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(rp + 528)[d - 512]);
-                    }
-                }
-                k[tk][d] = x;
-            }
-            __syncthreads();
-            for (int tk = 0; tk < kTok; ++tk) {
-                if (!seen[tk]) continue;
-                float s = 0.f;
-                for (int i = 0; i < 18; ++i) s += q[i] * k[tk][lane + 32 * i];
-                s = warp_sum(s);
-                const float mn = fmaxf(m, s);
-                const float al = expf(m - mn), p = expf(s - mn);
-                l = l * al + p;
-                for (int i = 0; i < 16; ++i) o[i] = o[i] * al + p * k[tk][lane + 32 * i];
-                m = mn;
-            }
+            misc->row0 = r;
+            misc->tile0 = (int32_t)at;
         }
     }
-    for (int i = 0; i < 16; ++i) {
-        const float v = l > 0.f ? o[i] / l : 0.f;
-        const int64_t at = (row * 64 + h) * 512 + lane + 32 * i;
-        if (a.out_f32) static_cast<float*>(a.out)[at] = v;
-        else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+}
+
+// S^T += K-blocks [B0, B0 + NB) of the tile x the same blocks of Q, four K = 16
+// steps per 64-dim block; the first MMA of a tile overwrites.
+template <int B0, int NB>
+__device__ __forceinline__ void qk_blocks(uint32_t d_tmem, uint64_t d_kv, uint64_t d_q) {
+#pragma unroll
+    for (int bk = B0; bk < B0 + NB; ++bk)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+            mma_f16(d_tmem, d_kv + (uint64_t)((bk * kBlk + kk * 32) >> 4), d_q + (uint64_t)((bk * 8192 + kk * 32) >> 4),
+                    kIdescQK, (bk == 0 && kk == 0) ? 0u : 1u);
+}
+// O^T rows of latent block MB += V^T P^T over the tile's eight 16-token steps,
+// then a commit that releases the block's part of the tile.
+template <int MB>
+__device__ __forceinline__ void pv_block(uint32_t o_tmem, uint64_t d_v, uint64_t d_p, bool acc0, uint64_t* bar) {
+#pragma unroll
+    for (int kt = 0; kt < kTok / 16; ++kt)
+        mma_f16(o_tmem + MB * 64, d_v + (uint64_t)((2 * MB * kBlk + kt * 2048) >> 4), d_p + (uint64_t)((kt * 2048) >> 4),
+                kIdescPV, (acc0 || kt > 0) ? 1u : 0u);
+    mma_commit(bar);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+dense_mla_kernel(Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
+    Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc);
+    float* red = reinterpret_cast<float*>(smem + kOffRed);
+    float* m_ref = reinterpret_cast<float*>(smem + kOffStat);
+    float* l_acc = m_ref + 64;
+    float* alpha = l_acc + 64;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const BatchDev& b = a.b;
+    volatile int32_t* abort_flag = &misc->abort;
+
+    if (tid == 0) {
+        mbar_init(&bars[B_QFULL], kLoadWarps);
+        for (int i = 0; i < 5; ++i) mbar_init(&bars[B_FULL0 + i], kLoadWarps);
+        mbar_init(&bars[B_SFULL], 1);
+        mbar_init(&bars[B_PREADY], kSoftWarps);
+        for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PV0 + i], 1);
+        mbar_init(&bars[B_DRAIN], 1);
+        misc->abort = 0;
+        fence_barrier_init();
     }
-    if (a.lse && lane == 0) a.lse[row * 64 + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    if (warp == 0) {
+        tmem_alloc(&misc->tmem_base, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    if (tid < kPlanThreads) plan_share(a, misc, tid);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem_base;
+    const int64_t g = blockIdx.x;
+    const int64_t N = misc->total, G = min((int64_t)gridDim.x, N);
+    const int64_t row_begin = misc->row0;
+    const int tile_begin = misc->tile0;
+    const int64_t n_mine = g < G ? (g + 1) * N / G - g * N / G : 0;
+    if (tid == 0) a.meta[g] = n_mine > 0 ? Meta{(int32_t)row_begin, tile_begin > 0 ? 1 : 0} : Meta{-1, 0};
+
+    auto timeout = [&](int where) {
+        record_error(a.st, DSA_DEVERR_TIMEOUT, where);
+        *abort_flag = 1;
+    };
+
+    if (warp == kMmaWarp) {
+        // ================================================================ MMA issue (one thread)
+        if (lane == 0) {
+            const uint32_t kv0 = smem_addr(smem + kOffKV), q0 = smem_addr(smem + kOffQ), p0 = smem_addr(smem + kOffP);
+            const uint64_t d_kv = desc_kmajor_sw128(kv0), d_q = desc_kmajor_sw128(q0);
+            const uint64_t d_v = desc_mnmajor_sw128(kv0, kBlk), d_p = desc_mnmajor_sw128(p0, 8192);
+            bool ok = true;
+            int64_t gt = 0, left = n_mine;
+            int t0 = tile_begin;
+            for (int64_t row = row_begin, k = 0; left > 0 && ok; ++row) {
+                const int n_row = tiles_of(row_view(b, a.view, row, nullptr)) - t0;
+                const int n = (int)min((int64_t)n_row, left);
+                left -= n;
+                t0 = 0;
+                if (n == 0) continue;
+                if (!(ok = wait_ab(&bars[B_QFULL], (uint32_t)(k & 1), abort_flag))) break;
+                ++k;
+                for (int t = 0; t < n && ok; ++t, ++gt) {
+                    const uint32_t ph = (uint32_t)(gt & 1);
+                    if (!(ok = wait_ab(&bars[B_FULL0], ph, abort_flag))) break;
+                    tc_fence_after();
+                    qk_blocks<0, 2>(tmem + kColS, d_kv, d_q);
+                    if (!(ok = wait_ab(&bars[B_FULL0 + 1], ph, abort_flag))) break;
+                    tc_fence_after();
+                    qk_blocks<2, 2>(tmem + kColS, d_kv, d_q);
+                    if (!(ok = wait_ab(&bars[B_FULL0 + 2], ph, abort_flag))) break;
+                    tc_fence_after();
+                    qk_blocks<4, 2>(tmem + kColS, d_kv, d_q);
+                    if (!(ok = wait_ab(&bars[B_FULL0 + 3], ph, abort_flag))) break;
+                    tc_fence_after();
+                    qk_blocks<6, 2>(tmem + kColS, d_kv, d_q);
+                    if (!(ok = wait_ab(&bars[B_FULL4], ph, abort_flag))) break;
+                    tc_fence_after();
+                    qk_blocks<8, 1>(tmem + kColS, d_kv, d_q);
+                    mma_commit(&bars[B_SFULL]);
+                    if (!(ok = wait_ab(&bars[B_PREADY], ph, abort_flag))) break;
+                    tc_fence_after();
+                    pv_block<0>(tmem + kColO, d_v, d_p, t > 0, &bars[B_PV0]);
+                    pv_block<1>(tmem + kColO, d_v, d_p, t > 0, &bars[B_PV0 + 1]);
+                    pv_block<2>(tmem + kColO, d_v, d_p, t > 0, &bars[B_PV0 + 2]);
+                    pv_block<3>(tmem + kColO, d_v, d_p, t > 0, &bars[B_PV0 + 3]);
+                }
+            }
+            if (!ok) timeout(61);
+            if (n_mine > 0) {                              // no MMA may be in flight when the TMEM is released
+                mma_commit(&bars[B_DRAIN]);
+                mbar_wait(&bars[B_DRAIN], 0, 500000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kLoadWarp0) {
+        // ================================================================ loaders
+        const int lt = tid - kLoadWarp0 * 32;              // 0..255
+        const int lw = lt >> 5;                            // warps 0-3 the tile's first page, 4-7 its second
+        const int half = lw >> 2;
+        const int tok0 = (lw & 3) * 16 + (lane >> 3);      // token of the page at step 0; step i adds 4 i
+        const int c8 = lane & 7;                           // 16-byte piece of a 128-byte group
+        uint4 raw[2][kSteps], rope[kSteps];
+        float scale[2][kSteps];
+        int64_t gt = 0, left = n_mine;
+        int t0 = tile_begin, k = 0;
+        bool ok = true;
+        for (int64_t row = row_begin; left > 0; ++row) {
+            const Row w = row_view(b, a.view, row, lt == 0 ? a.st : nullptr);
+            const int n_row = tiles_of(w) - t0;
+            const int n = (int)min((int64_t)n_row, left);
+            const int tb = t0;                             // first tile of the piece
+            left -= n;
+            t0 = 0;
+            if (n == 0) continue;
+            if (load_any(!ok || *abort_flag)) break;      // one decision for all loader warps
+            // page ids of this warp's half of the next 32 tiles, one tile per lane, and of the 32 after
+            auto ids_from = [&](int t) -> int32_t {
+                const int u = 2 * (t + lane) + half;
+                return t + lane < tb + n && u < w.pages && w.page(u) < b.max_pages
+                           ? b.page_table[(int64_t)w.r * b.max_pages + w.page(u)] : -1;
+            };
+            int32_t ids = ids_from(tb), ids_next = ids_from(tb + 32);
+            int base_t = tb;                               // tile of lane 0's id
+            auto page_of = [&](int t) -> int32_t {         // t in [base_t, base_t + 64)
+                const int rel = t - base_t;
+                const int32_t x = __shfl_sync(0xffffffffu, ids, rel & 31), y = __shfl_sync(0xffffffffu, ids_next, rel & 31);
+                return rel < 32 ? x : y;
+            };
+            // the tile being prefetched: its page, and which of this lane's four tokens are seen
+            const uint8_t* src = nullptr;
+            uint32_t seen = 0;
+            bool bad = false;
+            auto aim = [&](int t) {
+                const int32_t pg = page_of(t);
+                const int u = 2 * t + half;
+                seen = 0;
+                bad = false;
+                if (u < w.pages) {
+                    const int j0 = w.page(u) * kPage + tok0;
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) seen |= w.sees(j0 + 4 * i) ? 1u << i : 0u;
+                    bad = pg < 0 || pg >= b.num_pages;
+                    if (bad) {
+                        if (__any_sync(0xffffffffu, seen != 0) && lane == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
+                        seen = 0;
+                    }
+                }
+                src = a.kv + (int64_t)(bad || u >= w.pages ? 0 : pg) * kKvPageBytes + tok0 * kKvTokenBytes;
+            };
+            auto fetch = [&](uint4 (&dst)[kSteps], int piece) {
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+                    dst[i] = seen >> i & 1u ? ldg_pinned(reinterpret_cast<const uint4*>(src + i * 4 * kKvTokenBytes) + piece)
+                                            : make_uint4(0, 0, 0, 0);
+            };
+            auto fetch_group = [&](int gg) {               // 128 latent dims of the four tokens and their scales
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+                    scale[gg & 1][i] = seen >> i & 1u
+                                           ? ldg_pinned(reinterpret_cast<const float*>(src + i * 4 * kKvTokenBytes + 512) + gg) : 1.f;
+                fetch(raw[gg & 1], gg * 8 + c8);
+            };
+            auto warm_l2 = [&](int t) {                    // the whole page, by one thread per half
+                if (t < tb + n) {
+                    const int32_t pg = page_of(t);
+                    if ((lw & 3) == 0 && lane == 0 && pg >= 0 && pg < b.num_pages)
+                        prefetch_l2(a.kv + (int64_t)pg * kKvPageBytes, kKvPageBytes);
+                }
+            };
+            warm_l2(tb + 1);
+            aim(tb);
+            fetch_group(0);
+            fetch_group(1);
+            fetch(rope, 33 + c8);
+            // ---- Q of the row -> fp16, K-major, 128-byte swizzle, once the previous row's
+            //      last S^T has read the one before
+            if (gt > 0 && ok) ok = wait_ab(&bars[B_SFULL], (uint32_t)((gt - 1) & 1), abort_flag);
+            {
+                static_assert(64 * 72 == 18 * kLoadThreads, "18 16-byte pieces of q per thread");
+                const uint4* qrow = reinterpret_cast<const uint4*>(a.q + row * (64 * 576));
+                uint32_t mx = 0;                           // two bf16 magnitudes, compared as integers
+#pragma unroll 1
+                for (int u0 = 0; u0 < 18; u0 += 6) {
+                    uint4 qv[6];
+#pragma unroll
+                    for (int u = 0; u < 6; ++u) qv[u] = __ldg(qrow + lt + (u0 + u) * kLoadThreads);
+#pragma unroll
+                    for (int u = 0; u < 6; ++u)
+                        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(qv[u].x & 0x7fff7fffu, qv[u].y & 0x7fff7fffu),
+                                                   __vmaxu2(qv[u].z & 0x7fff7fffu, qv[u].w & 0x7fff7fffu)));
+                }
+                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+                if (lane == 0) misc->qmax[lw] = mx;
+                load_sync();
+                uint32_t amax = 0;
+#pragma unroll
+                for (int v = 0; v < kLoadWarps; ++v) amax = max(amax, misc->qmax[v]);
+                const int eq = amax == 0 ? 14 : (int)(amax >> 7) - 127;
+                const int kq = min(126, max(-126, 14 - eq));
+                const float sc = __int_as_float((127 + kq) << 23);
+                if (lt == 0) misc->q_unscale[k & 1] = __int_as_float((127 - kq) << 23);
+#pragma unroll 1
+                for (int u0 = 0; u0 < 18; u0 += 6) {
+                    uint4 qv[6];
+#pragma unroll
+                    for (int u = 0; u < 6; ++u) qv[u] = __ldg(qrow + lt + (u0 + u) * kLoadThreads);
+#pragma unroll
+                    for (int u = 0; u < 6; ++u) {
+                        const int c = lt + (u0 + u) * kLoadThreads;
+                        const int h = c / 72, cq = c % 72;
+                        const int blk = cq >> 3, ch = cq & 7;
+                        *reinterpret_cast<uint4*>(smem + kOffQ + blk * 8192 + h * 128 + ((ch ^ (h & 7)) * 16)) =
+                            make_uint4(bf16x2_scaled_to_h2(qv[u].x, sc), bf16x2_scaled_to_h2(qv[u].y, sc),
+                                       bf16x2_scaled_to_h2(qv[u].z, sc), bf16x2_scaled_to_h2(qv[u].w, sc));
+                    }
+                }
+                if (lt == 0 && amax >= 0x7f80u) record_error(a.st, DSA_DEVERR_FP16_RANGE, row);   // inf / NaN in q
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_QFULL]);
+                load_sync();                               // qmax may be written again
+            }
+            ++k;
+            // ---- tiles: latent groups 0..3 (free once the previous tile's P.V of the group is
+            //      done), then the RoPE block (free, as P^T, with the last group)
+            for (int t = tb; t < tb + n && ok; ++t, ++gt) {
+                const uint32_t ph = (uint32_t)((gt - 1) & 1);
+                uint32_t off_range = 0;                    // a latent scale or a RoPE value fp16 cannot hold
+                const uint32_t seen_now = seen;
+                if (t - base_t == 31) {                    // the next tile opens the next batch of ids
+                    base_t += 32;
+                    ids = ids_next;
+                    ids_next = ids_from(base_t + 32);
+                }
+                warm_l2(t + 2);
+                const bool bad_now = bad;
+                const bool more = t + 1 < tb + n;
+#pragma unroll
+                for (int gg = 0; gg < 4; ++gg) {
+                    if (gt > 0 && !(ok = wait_ab(&bars[B_PV0 + gg], ph, abort_flag))) break;
+                    if (gg == 0 && (lw & 3) == 0 && lane == 0) misc->bad[half] = bad_now ? 1 : 0;
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        const int tk = half * kPage + tok0 + 4 * i;
+                        const float sc = scale[gg & 1][i];
+                        off_range |= (sc >= 0x1p-15f && sc <= 0x1p7f) ? 0u : 1u;
+                        const __half2 sc2 = __float2half2_rn(sc);           // a power of two: exact
+                        const uint4 x = raw[gg & 1][i];
+                        // 16 FP8 dims 128 gg + 16 c8 .. -> K-block 2 gg + c8 / 4, 16-byte chunks 2 (c8 % 4), +1
+                        uint8_t* blkp = smem + kOffKV + (2 * gg + (c8 >> 2)) * kBlk + tk * 128;
+                        const int ch = 2 * (c8 & 3), sw = tk & 7;
+                        *reinterpret_cast<uint4*>(blkp + ((ch ^ sw) * 16)) =
+                            make_uint4(e4m3x2_scaled_h2(x.x & 0xffffu, sc2), e4m3x2_scaled_h2(x.x >> 16, sc2),
+                                       e4m3x2_scaled_h2(x.y & 0xffffu, sc2), e4m3x2_scaled_h2(x.y >> 16, sc2));
+                        *reinterpret_cast<uint4*>(blkp + (((ch + 1) ^ sw) * 16)) =
+                            make_uint4(e4m3x2_scaled_h2(x.z & 0xffffu, sc2), e4m3x2_scaled_h2(x.z >> 16, sc2),
+                                       e4m3x2_scaled_h2(x.w & 0xffffu, sc2), e4m3x2_scaled_h2(x.w >> 16, sc2));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[B_FULL0 + gg]);
+                    // the registers just emptied take the group two ahead
+                    if (gg < 2) {
+                        fetch_group(gg + 2);
+                    } else if (more) {
+                        if (gg == 2) aim(t + 1);
+                        fetch_group(gg - 2);
+                    }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const int tk = half * kPage + tok0 + 4 * i;
+                    *reinterpret_cast<uint4*>(smem + kOffP + tk * 128 + ((c8 ^ (tk & 7)) * 16)) =
+                        make_uint4(rope_bf16x2_to_h2(rope[i].x, off_range), rope_bf16x2_to_h2(rope[i].y, off_range),
+                                   rope_bf16x2_to_h2(rope[i].z, off_range), rope_bf16x2_to_h2(rope[i].w, off_range));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_FULL4]);
+                if (off_range && seen_now) record_error(a.st, DSA_DEVERR_FP16_RANGE, lane);
+                if (more) fetch(rope, 33 + c8);
+            }
+            if (!ok && lane == 0) timeout(62);
+        }
+    } else {
+        // ================================================================ softmax + epilogue
+        // Warp w reads TMEM lane quarter w % 4 (token / latent row st) and
+        // heads [32 hh, 32 hh + 32), hh = w / 4.
+        const int q4 = warp & 3, hh = warp >> 2;
+        const int st = q4 * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
+        int64_t gt = 0, left = n_mine;
+        int t0 = tile_begin, k = 0;
+        for (int64_t row = row_begin; left > 0; ++row) {
+            const Row w = row_view(b, a.view, row, nullptr);
+            const int n_row = tiles_of(w) - t0;
+            const int n = (int)min((int64_t)n_row, left);
+            const int tb = t0;
+            const bool whole = tb == 0 && n == n_row;
+            left -= n;
+            t0 = 0;
+            if (n == 0) continue;
+            if (tid < 64) m_ref[tid] = -INFINITY;
+            soft_sync();
+            float lsum[32];                                // this token lane's running sums of its 32 heads
+#pragma unroll
+            for (int c = 0; c < 32; ++c) lsum[c] = 0.f;
+            float sl2 = 0.f;
+            bool failed = false;
+            const float4* mr4 = reinterpret_cast<const float4*>(m_ref + hh * 32);
+            for (int t = tb; t < tb + n; ++t, ++gt) {
+                const bool ok = wait_ab(&bars[B_SFULL], (uint32_t)(gt & 1), abort_flag);
+                if (t == tb) sl2 = a.scale_log2 * misc->q_unscale[k & 1];
+                const int u = 2 * t + (st >> 6);
+                const bool valid = u < w.pages && w.sees(w.page(u) * kPage + (st & 63)) && misc->bad[st >> 6] == 0;
+                // S^T row of this token for the warp's 32 heads, in log2 units; tokens not seen -> -inf
+                auto load_s = [&](float (&v)[32]) {
+                    uint32_t x[32];
+                    tmem_ld_32x32b_x32(lane_addr + kColS + hh * 32, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) v[h] = valid ? __uint_as_float(x[h]) * sl2 : -INFINITY;
+                };
+                // P of the current references, and its P^T row (heads 32 hh.. as fp16, MN-major swizzle)
+                auto write_p = [&](float (&v)[32]) {
+#pragma unroll
+                    for (int c4 = 0; c4 < 8; ++c4) {
+                        const float4 m = mr4[c4];
+                        v[4 * c4] = valid ? ex2_approx(v[4 * c4] - m.x) : 0.f;
+                        v[4 * c4 + 1] = valid ? ex2_approx(v[4 * c4 + 1] - m.y) : 0.f;
+                        v[4 * c4 + 2] = valid ? ex2_approx(v[4 * c4 + 2] - m.z) : 0.f;
+                        v[4 * c4 + 3] = valid ? ex2_approx(v[4 * c4 + 3] - m.w) : 0.f;
+                    }
+                    uint8_t* prow = smem + kOffP + st * 128;
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc) {
+                        const int c = hh * 4 + cc;
+                        *reinterpret_cast<uint4*>(prow + ((c ^ (st & 7)) * 16)) =
+                            make_uint4(pack_h2(v[8 * cc], v[8 * cc + 1]), pack_h2(v[8 * cc + 2], v[8 * cc + 3]),
+                                       pack_h2(v[8 * cc + 4], v[8 * cc + 5]), pack_h2(v[8 * cc + 6], v[8 * cc + 7]));
+                    }
+                    fence_proxy_async_smem();
+                };
+                float v[32];
+                tc_fence_after();
+                load_s(v);
+                // ---- a score above its head's reference by more than 2^(kTau + kShift) makes every
+                //      warp take new references first (always on the piece's first tile)
+                bool over = false;
+#pragma unroll
+                for (int c4 = 0; c4 < 8; ++c4) {
+                    const float4 m = mr4[c4];
+                    over |= v[4 * c4] > m.x + (kTau + kShift) || v[4 * c4 + 1] > m.y + (kTau + kShift) ||
+                            v[4 * c4 + 2] > m.z + (kTau + kShift) || v[4 * c4 + 3] > m.w + (kTau + kShift);
+                }
+                write_p(v);
+                if (soft_any(over || !ok)) {
+                    if (soft_any(!ok)) {
+                        failed = true;
+                        break;
+                    }
+                    load_s(v);
+                    xreduce32<true>(v, lane);                   // per-head tile max (consumes v)
+                    red[q4 * 64 + hh * 32 + lane] = v[0];
+                    soft_sync();
+                    if (tid < 64) {
+                        const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid])) - kShift;
+                        const float mo = m_ref[tid];
+                        const bool need = tm > mo + kTau;
+                        alpha[tid] = need ? (mo == -INFINITY ? 0.f : exp2f(mo - tm)) : 1.f;
+                        if (need) m_ref[tid] = tm;
+                    }
+                    soft_sync();
+                    if (t > tb) {                               // rescale the resident O^T columns of these heads
+#pragma unroll 1
+                        for (int mb = 0; mb < 4; ++mb) {
+                            uint32_t o[32];
+                            const uint32_t addr = lane_addr + kColO + mb * 64 + hh * 32;
+                            tmem_ld_32x32b_x32(addr, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[hh * 32 + c]);
+                            tmem_st_32x32b_x32(addr, o);
+                        }
+                        tmem_st_wait();
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) lsum[c] *= alpha[hh * 32 + c];
+                    load_s(v);
+                    write_p(v);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_PREADY]);    // P^T written, S^T read, O^T rescaled
+#pragma unroll
+                for (int c = 0; c < 32; ++c) lsum[c] += v[c];
+            }
+            if (failed) {
+                if (tid == 0) timeout(63);
+                break;
+            }
+            ++k;
+            // ---- per-head sums over the piece: the lanes' running sums reduced
+            xreduce32<false>(lsum, lane);
+            red[256 + q4 * 64 + hh * 32 + lane] = lsum[0];
+            // ---- piece end: O^T is final once the last P.V completes
+            const bool ok = wait_ab(&bars[B_PV3], (uint32_t)((gt - 1) & 1), abort_flag);
+            if (soft_any(!ok)) {
+                if (tid == 0) timeout(64);
+                break;
+            }
+            tc_fence_after();
+            if (tid < 64) l_acc[tid] = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
+            soft_sync();
+            const int64_t unit = 2 * g + (k == 1 ? 0 : 1);      // a share's first piece, or its last
+#pragma unroll 1
+            for (int mb = 0; mb < 4; ++mb) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(lane_addr + kColO + mb * 64 + hh * 32, o);
+                tmem_ld_wait();
+                const int d = mb * 128 + st;                           // latent dim of this TMEM lane
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {                         // a warp stores 32 consecutive dims
+                    const int h = hh * 32 + c;
+                    const float ov = __uint_as_float(o[c]);
+                    if (whole) {
+                        const float l = l_acc[h];
+                        const float val = l > 0.f ? ov / l : 0.f;
+                        const int64_t oi = (row * 64 + h) * 512 + d;
+                        if (a.out_f32) static_cast<float*>(a.out)[oi] = val;
+                        else static_cast<__nv_bfloat16*>(a.out)[oi] = __float2bfloat16_rn(val);
+                    } else {
+                        a.part_o[(unit * 64 + h) * 512 + d] = ov;
+                    }
+                }
+            }
+            tc_fence_before();
+            if (tid < 64) {
+                const float l = l_acc[tid];
+                if (!whole) a.part_ml[unit * 64 + tid] = make_float2(m_ref[tid], l);
+                else if (a.lse) a.lse[row * 64 + tid] = l > 0.f ? (m_ref[tid] + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            }
+            soft_sync();                                    // O^T and the references may be reused
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    pdl_trigger();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- merge
+// Block (x, y): share boundary x + 1 and its heads y, y + gridDim.y, ..  The
+// boundary's row was cut when share x + 1 begins inside it; the first such
+// boundary of a row merges its pieces.  Per head over the pieces u:
+//   M = max m_u,  w_u = 2^(m_u - M),  L = sum w_u l_u,
+//   out = sum_u w_u O_u / L,  lse = (M + log2 L) ln 2.
+constexpr int kMergeThreads = 128;                         // 512 dims, four per thread
+constexpr int kMaxPieces = 1024;
+
+__global__ void __launch_bounds__(kMergeThreads)
+dense_merge_kernel(Args a, int G) {
+    __shared__ float w_s[kMaxPieces];
+    __shared__ float red_s[8];
+    __shared__ int np_s;
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int bd = blockIdx.x + 1;
+    const Meta me = a.meta[bd], prev = a.meta[bd - 1];
+    if (!me.inside || (prev.inside && prev.row == me.row)) return;
+    const int64_t row = me.row;
+    // the row's pieces: the last piece of share bd - 1, then the first ones of bd, bd + 1, .. while they begin inside the row
+    if (tid == 0) np_s = 1 + G - bd;
+    __syncthreads();
+    for (int i = tid; bd + i < G; i += kMergeThreads) {
+        const Meta m = a.meta[bd + i];
+        if (!m.inside || m.row != me.row) {
+            atomicMin(&np_s, 1 + i);
+            break;
+        }
+    }
+    __syncthreads();
+    const int np = np_s;
+    const int64_t unit0 = 2 * (int64_t)(bd - 1) + (prev.row == me.row ? 0 : 1);
+    for (int h = blockIdx.y; h < 64; h += gridDim.y) {
+        auto unit = [&](int i) { return i == 0 ? unit0 : 2 * (int64_t)(bd - 1 + i); };
+        float M = -INFINITY;
+        for (int i = tid; i < np; i += kMergeThreads) {
+            const float2 ml = __ldcg(a.part_ml + unit(i) * 64 + h);
+            if (ml.y > 0.f) M = fmaxf(M, ml.x);
+        }
+        M = warp_max(M);
+        if (lane == 0) red_s[warp] = M;
+        __syncthreads();
+        M = fmaxf(fmaxf(red_s[0], red_s[1]), fmaxf(red_s[2], red_s[3]));
+        float L = 0.f;
+        for (int i = tid; i < np; i += kMergeThreads) {
+            const float2 ml = __ldcg(a.part_ml + unit(i) * 64 + h);
+            const float w = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
+            w_s[i] = w;
+            L += w * ml.y;
+        }
+        L = warp_sum(L);
+        if (lane == 0) red_s[4 + warp] = L;
+        __syncthreads();
+        L = red_s[4] + red_s[5] + red_s[6] + red_s[7];
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q0 = 0; q0 < np; q0 += 8) {                // eight pieces' loads in flight
+            float4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = q0 + j < np ? __ldcg(reinterpret_cast<const float4*>(a.part_o + (unit(q0 + j) * 64 + h) * 512) + tid)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float w = q0 + j < np ? w_s[q0 + j] : 0.f;
+                if (w == 0.f) continue;                    // a piece that saw nothing holds no numbers
+                acc.x += w * v[j].x;
+                acc.y += w * v[j].y;
+                acc.z += w * v[j].z;
+                acc.w += w * v[j].w;
+            }
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int64_t o = (row * 64 + h) * 512 + tid * 4;
+        if (a.out_f32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) =
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        } else {
+            __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+            __nv_bfloat162 hi2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) =
+                make_uint2(*reinterpret_cast<uint32_t*>(&lo2), *reinterpret_cast<uint32_t*>(&hi2));
+        }
+        if (a.lse && tid == 0) a.lse[row * 64 + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        __syncthreads();                                    // w_s and red_s may be reused
+    }
 }
 
 static size_t ws_bytes(int G) {
-    const size_t n = (size_t)2 * G * 64 * (512 + 2) * 4 + (size_t)G * 16;
+    const size_t n = (size_t)2 * G * 64 * (512 + 2) * 4 + (size_t)G * sizeof(Meta);
     return (n + 255) / 256 * 256;
+}
+
+// Tiles that one row can have, at most.
+static int64_t most_tiles(const dsa_batch* b, const View& v) {
+    int64_t pages = ((int64_t)b->max_seq_len + kPage - 1) / kPage;
+    if (!v.tree) pages = std::min(pages, (int64_t)v.sinks / kPage + 1 + (int64_t)v.window / kPage + 2);
+    return (pages + 1) / 2;
 }
 
 static dsa_status launch(const void* q, const uint8_t* kv, const dsa_batch* b, View view, float softmax_scale, void* out,
@@ -167,18 +821,30 @@ static dsa_status launch(const void* q, const uint8_t* kv, const dsa_batch* b, V
     if (!ws) return DSA_ERR_INVALID_ARGUMENT;
     if (bytes < ws_bytes(device_sm_count())) return DSA_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned16(ws)) return DSA_ERR_ALIGNMENT;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(&dense_mla_kernel), kSmemAlloc) != DSA_OK) return DSA_ERR_CUDA;
+    const int sms = device_sm_count();
+    const int G = (int)std::min<int64_t>(sms, b->total_q * most_tiles(b, view));
     Args a = {};
     a.q = static_cast<const uint16_t*>(q);
     a.kv = kv;
     a.b = to_dev(b);
     a.view = view;
-    a.scale = softmax_scale;
+    a.scale_log2 = softmax_scale * 1.4426950408889634f;
     a.out = out;
     a.out_f32 = out_dtype == DSA_DTYPE_F32;
     a.lse = lse;
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * sms * 64 * 512);
+    a.meta = reinterpret_cast<Meta*>(a.part_ml + (size_t)2 * sms * 64);
     a.st = st;
-    dense_mla_kernel<<<dim3((unsigned)b->total_q, 8), kThreads, 0, as_stream(stream)>>>(a);
-    DSA_CHECK_LAUNCH();
+    const cudaStream_t s = as_stream(stream);
+    DSA_CHECK(launch_pdl(dense_mla_kernel, dim3((unsigned)G), dim3(kThreads), kSmemAlloc, s, 1, a));
+    if (G > 1) {
+        // boundaries x heads: a block per head where few rows can be cut (each may have many
+        // pieces), four heads a block where many can (most blocks then have nothing to merge)
+        const unsigned cuts = (unsigned)(G - 1);
+        DSA_CHECK(launch_pdl(dense_merge_kernel, dim3(cuts, b->total_q < 32 ? 64 : 16), dim3(kMergeThreads), 0, s, 1, a, G));
+    }
     return DSA_OK;
 }
 

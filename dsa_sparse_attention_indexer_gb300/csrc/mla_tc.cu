@@ -63,12 +63,14 @@
 
 #include "dsa_internal.cuh"
 #include "indexer_common.cuh"
+#include "mla_common.cuh"
 #include "sm100.cuh"
 
 namespace dsa {
 namespace mtc {
 
 using namespace sm100;
+using namespace mlc;
 
 constexpr int kTok = 96;                                   // tokens per tile
 constexpr int kBlk = kTok * 128;                           // one 64-dim K-block of the KV tile
@@ -196,80 +198,6 @@ __device__ __forceinline__ bool load_any(bool pred) {
                  " selp.u32 %0, 1, 0, q;\n}"
                  : "=r"(r) : "r"((uint32_t)pred), "n"(kLoadBar), "n"(kLoadThreads) : "memory");
     return r != 0;
-}
-
-// mbarrier wait that also gives up when another role has set the abort flag.
-__device__ __forceinline__ bool wait_ab(uint64_t* bar, uint32_t parity, const volatile int32_t* abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-        if ((it & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > 2000000000ull)) return false;
-    }
-}
-
-// 16-byte read-only load that stays where it is written (a prefetch a tile
-// ahead must not be sunk to its first use).
-__device__ __forceinline__ uint4 ldg_pinned(const uint4* p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-    return r;
-}
-
-// 2^x by the hardware approximation (subnormal results flush to 0): its error
-// is far below the fp16 rounding that P gets next.
-__device__ __forceinline__ float ex2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-    __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t e4m3x2_scaled_h2(uint32_t two, __half2 sc2) {
-    __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);   // exact
-    const __half2 p = __hmul2(*reinterpret_cast<__half2*>(&h), sc2);                     // * 2^e: exact
-    return *reinterpret_cast<const uint32_t*>(&p);
-}
-__device__ __forceinline__ uint32_t bf16x2_to_h2(uint32_t w) {
-    return pack_h2(bf16_bits_to_f32(w & 0xffffu), bf16_bits_to_f32(w >> 16));
-}
-// Two bf16 key RoPE values -> two fp16.  A magnitude of 2^16 or more (inf and
-// NaN included) does not fit fp16: it is clamped to +-65280 (the largest bf16
-// below fp16's maximum), so the scores stay finite, and bad is set.  Every
-// other bf16 value converts exactly, except those below 2^-17, whose error
-// (under 2^-25 absolute) is far below the attention tolerance.
-__device__ __forceinline__ uint32_t rope_bf16x2_to_h2(uint32_t w, uint32_t& bad) {
-    const uint32_t over = __vcmpgeu2(w & 0x7fff7fffu, 0x47804780u);   // per half: |x| >= 2^16
-    bad |= over;
-    return bf16x2_to_h2((w & ~over) | (over & ((w & 0x80008000u) | 0x477f477fu)));
-}
-// A query pair multiplied by the row's power of two `sc` (exact in fp32) ->
-// two fp16.  After that scaling no |value| reaches 2^15, so nothing
-// overflows; values more than 2^39 below the row's largest are rounded to
-// fp16's subnormal grid (absolute error under 2^-25 after the scaling).
-__device__ __forceinline__ uint32_t bf16x2_scaled_to_h2(uint32_t w, float sc) {
-    return pack_h2(bf16_bits_to_f32(w & 0xffffu) * sc, bf16_bits_to_f32(w >> 16) * sc);
-}
-
-// Reduce 32 values across the 32 lanes of a warp: afterwards lane l holds the
-// result for index l in v[0] (31 shuffles instead of 160).
-template <bool kMax>
-__device__ __forceinline__ void xreduce32(float (&v)[32], int lane) {
-#pragma unroll
-    for (int s = 16, n = 16; s >= 1; s >>= 1, n >>= 1) {
-        const bool up = (lane & s) != 0;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float send = up ? v[i] : v[i + n];
-            const float keep = up ? v[i + n] : v[i];
-            const float recv = __shfl_xor_sync(0xffffffffu, send, s);
-            v[i] = kMax ? fmaxf(keep, recv) : keep + recv;
-        }
-    }
 }
 
 // S^T += K-blocks [B0, B0 + NB) of the KV tile x the same blocks of Q, four

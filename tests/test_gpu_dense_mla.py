@@ -22,7 +22,7 @@ import torch
 
 import dsa_sparse_attention_indexer_gb300 as D
 from oracle import dsa_oracle as O
-from tests.oracle_side import bf16_bits, check_attention, f64
+from tests.oracle_side import ATTN_REL_L2, bf16_bits, f64
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -94,7 +94,9 @@ def compare(c, out, lse, scale=1.0 / 16, kv_of=lambda i, kv: kv):
         err = np.abs(out[i] - ref)
         assert (err <= tol).all(), f"row {i}: {(err > tol).sum()} values off, worst {np.max(err / np.maximum(tol, 1e-30)):.2f} of the bound"
         if not c["bf16"] and len(kv):
-            check_attention(out[i], ref, what=f"row {i}")
+            # the library's relative bar.  Its absolute one, 1e-2, is for latents ~N(0, 1): half an fp16 step of p
+            # times |c| alone passes it from |c| = 20.5 on (2^-11 * 20.5 = 1e-2), and these reach 4 exp(3) = 80
+            assert np.linalg.norm(out[i] - ref) <= ATTN_REL_L2 * np.linalg.norm(ref), f"row {i}"
         if lse is not None:
             assert np.array_equal(np.isinf(lse[i]), np.isinf(z)), f"row {i}"
             f = np.isfinite(z)
@@ -249,6 +251,16 @@ def test_cache_beyond_32_bits():
     b = c["batch"].c
     c["kv"], c["batch"] = kv, D.Batch(c["batch"].seq_len, c["batch"].q_start, t, far, max_seq_len=b.max_seq_len, max_q_len=2, total_q=2)
     compare(c, *run(c, window_call(400, 10)))
+
+
+def test_latents_out_of_range_are_recorded():
+    c = window_case(41, [100], [1], 100, 0)
+    kv = c["kv"].view(-1, 64, 656)
+    kv[int(c["table"][0, 1]), 3, 512:516] = torch.tensor([2.0 ** -20]).view(torch.uint8).to(DEV)
+    run(c, window_call(100, 0), want_status=D.DEVERR_FP16_RANGE)
+    c["dq"][0, 0, 0] = float("inf")
+    kv[int(c["table"][0, 1]), 3, 512:516] = torch.tensor([1.0]).view(torch.uint8).to(DEV)
+    run(c, window_call(100, 0), want_status=D.DEVERR_FP16_RANGE)
 
 
 def test_other_streams_dirty_workspaces_and_graphs_that_share_one():
