@@ -103,5 +103,24 @@ __device__ __forceinline__ void xreduce32(float (&v)[32], int lane) {
     }
 }
 
+// Reduce 16 values across the 32 lanes of a warp: afterwards lanes l and l + 16
+// hold the result for index l in v[0].
+template <bool kMax>
+__device__ __forceinline__ void xreduce16(float (&v)[16], int lane) {
+#pragma unroll
+    for (int s = 8, n = 8; s >= 1; s >>= 1, n >>= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = up ? v[i] : v[i + n];
+            const float keep = up ? v[i + n] : v[i];
+            const float recv = __shfl_xor_sync(0xffffffffu, send, s);
+            v[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+        }
+    }
+    const float recv = __shfl_xor_sync(0xffffffffu, v[0], 16);
+    v[0] = kMax ? fmaxf(v[0], recv) : v[0] + recv;
+}
+
 }  // namespace mlc
 }  // namespace dsa

@@ -22,17 +22,17 @@
 // the next tile starts behind the last P.V.  P^T takes the place of the tile's
 // RoPE block, which S^T has read by then.
 //
-// Roles (17 warps):
-//   warps 0-7   softmax and epilogue: a thread owns one token (TMEM lane) and 32
+// Roles (seven warpgroups):
+//   warps 0-15  softmax and epilogue: a thread owns one token (TMEM lane) and 16
 //               heads.  P is formed against a reference that lags the maximum by
 //               up to 2^8 before O^T is rescaled, and shifted up by 2^7 so that
 //               fp16 holds probabilities down to 2^-32 of the largest.
-//   warps 8-15  loaders: read the pages into registers two groups ahead (whole pages
+//   warps 16-23 loaders: read the pages into registers two groups ahead (whole pages
 //               are prefetched into L2 two tiles ahead), dequantise into the
 //               128-byte-swizzled tile (exact for scales in [2^-15, 2^7]) and
 //               convert each row's Q, scaled by the power of two that puts its
 //               largest |q| in [2^14, 2^15).  Rows that are not seen become zeros.
-//   warp 16     issues the MMAs.
+//   warp 24     issues the MMAs (its warpgroup hands its registers to the others).
 // Every wait is time-bounded; a timeout is recorded and the CTA winds down.
 #include <algorithm>
 
@@ -80,8 +80,8 @@ struct Row {
     int32_t prefix;
     uint64_t mask;
     int32_t sink_pages, first_page, pages;
-    __device__ __forceinline__ int page(int u) const { return u < sink_pages ? u : first_page + u - sink_pages; }
-    __device__ __forceinline__ bool sees(int j) const {
+    __device__ __forceinline__ int page(int u) const volatile { return u < sink_pages ? u : first_page + u - sink_pages; }
+    __device__ __forceinline__ bool sees(int j) const volatile {
         if (j < sink_end || (j >= first && j < end)) return true;
         const unsigned u = (unsigned)(j - prefix);
         return u < 64u && (mask >> u & 1u);
@@ -128,13 +128,14 @@ using namespace mlc;
 
 constexpr int kTok = 128;                                  // tokens per tile: two pages
 constexpr int kBlk = kTok * 128;                           // one 64-dim K-block of the tile
-constexpr int kSoftWarps = 8;                              // two per TMEM lane quarter, 32 heads each
+constexpr int kSoftWarps = 16;                             // four per TMEM lane quarter, 16 heads each
+constexpr int kHeads = 16;                                 // heads of a softmax warp
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kLoadWarp0 = kSoftWarps;
 constexpr int kLoadWarps = 8;
 constexpr int kLoadThreads = kLoadWarps * 32;
 constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kThreads = (kMmaWarp + 4) * 32;              // seven warpgroups; the last one's first warp issues the MMAs
 constexpr int kPlanThreads = 512;                          // threads that count the rows' tiles
 constexpr int kSoftBar = 1, kLoadBar = 2, kPlanBar = 3;
 constexpr int kSteps = kTok / kLoadWarps / 4;              // a loader warp's 16 tokens, four at a time
@@ -152,7 +153,9 @@ constexpr int kOffRed = kOffQ + 9 * 8192;                  // [2][4 lane quarter
 constexpr int kOffStat = kOffRed + 2 * 4 * 64 * 4;         // m_ref, l_acc, alpha [64]
 constexpr int kOffBars = kOffStat + 3 * 64 * 4;
 constexpr int kOffMisc = kOffBars + 16 * 8;
-constexpr int kSmemUsed = kOffMisc + 512;
+constexpr int kOffRows = kOffMisc + 512;                   // every warp's current row, re-read instead of held in registers
+constexpr int kSmemUsed = kOffRows + (kThreads / 32) * (int)sizeof(Row);
+static_assert(sizeof(Row) % 8 == 0, "rows are 8-byte aligned");
 constexpr int kSmemAlloc = kSmemUsed + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kBlk % 1024 == 0, "swizzle atoms need 1 KB alignment");
@@ -169,8 +172,7 @@ struct Misc {
     int32_t bad[2];             // the tile's page (first, second half) is outside the cache
     int32_t scratch[32];
     int64_t total;              // tiles of the whole batch
-    int64_t row0;               // where this CTA's share begins
-    int32_t tile0;
+    int32_t row0, tile0;        // where this CTA's share begins
 };
 static_assert(sizeof(Misc) <= 512, "misc block");
 
@@ -224,16 +226,32 @@ __device__ __forceinline__ void plan_share(const Args& a, Misc* misc, int tid) {
                 if (at < n) break;
                 at -= n;
             }
-            misc->row0 = r;
+            misc->row0 = (int32_t)r;
             misc->tile0 = (int32_t)at;
         }
     }
 }
 
+// The roles' registers per thread: 72 at launch (65,536 / 896 threads, in
+// eights), of which the MMA warpgroup gives most to the loaders:
+// 512 x 72 + 256 x 88 + 128 x 40 = 896 x 72.
+constexpr int kLaunchRegs = 72, kLoadRegs = 88, kMmaRegs = 40;
+static_assert(kSoftThreads * kLaunchRegs + kLoadThreads * kLoadRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs,
+              "more registers than the launch holds");
+template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// The descriptors of an MMA are a base plus a constant.  Formed from a value the
+// compiler cannot see through, they are not kept across the tile loop, where
+// 68 pairs of them would spill.
+__device__ __forceinline__ void keep_here(uint64_t& d) { asm volatile("" : "+l"(d)); }
+
 // S^T += K-blocks [B0, B0 + NB) of the tile x the same blocks of Q, four K = 16
 // steps per 64-dim block; the first MMA of a tile overwrites.
 template <int B0, int NB>
 __device__ __forceinline__ void qk_blocks(uint32_t d_tmem, uint64_t d_kv, uint64_t d_q) {
+    keep_here(d_kv);
+    keep_here(d_q);
 #pragma unroll
     for (int bk = B0; bk < B0 + NB; ++bk)
 #pragma unroll
@@ -245,6 +263,8 @@ __device__ __forceinline__ void qk_blocks(uint32_t d_tmem, uint64_t d_kv, uint64
 // then a commit that releases the block's part of the tile.
 template <int MB>
 __device__ __forceinline__ void pv_block(uint32_t o_tmem, uint64_t d_v, uint64_t d_p, bool acc0, uint64_t* bar) {
+    keep_here(d_v);
+    keep_here(d_p);
 #pragma unroll
     for (int kt = 0; kt < kTok / 16; ++kt)
         mma_f16(o_tmem + MB * 64, d_v + (uint64_t)((2 * MB * kBlk + kt * 2048) >> 4), d_p + (uint64_t)((kt * 2048) >> 4),
@@ -265,6 +285,24 @@ dense_mla_kernel(Args a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const BatchDev& b = a.b;
     volatile int32_t* abort_flag = &misc->abort;
+    volatile Row& w = reinterpret_cast<Row*>(smem + kOffRows)[warp];
+    auto enter_row = [&](int row, int32_t* st) -> int {     // this warp's row; returns its tiles
+        const Row r = row_view(a.b, a.view, row, st);
+        __syncwarp();
+        if ((tid & 31) == 0) {
+            w.r = r.r;
+            w.sink_end = r.sink_end;
+            w.first = r.first;
+            w.end = r.end;
+            w.prefix = r.prefix;
+            w.mask = r.mask;
+            w.sink_pages = r.sink_pages;
+            w.first_page = r.first_page;
+            w.pages = r.pages;
+        }
+        __syncwarp();
+        return tiles_of(r);
+    };
 
     if (tid == 0) {
         mbar_init(&bars[B_QFULL], kLoadWarps);
@@ -288,28 +326,30 @@ dense_mla_kernel(Args a) {
     const uint32_t tmem = misc->tmem_base;
     const int64_t g = blockIdx.x;
     const int64_t N = misc->total, G = min((int64_t)gridDim.x, N);
-    const int64_t row_begin = misc->row0;
+    const int row_begin = misc->row0;
     const int tile_begin = misc->tile0;
-    const int64_t n_mine = g < G ? (g + 1) * N / G - g * N / G : 0;
-    if (tid == 0) a.meta[g] = n_mine > 0 ? Meta{(int32_t)row_begin, tile_begin > 0 ? 1 : 0} : Meta{-1, 0};
+    const int n_mine = g < G ? (int)((g + 1) * N / G - g * N / G) : 0;   // the host bounds it
+    if (tid == 0) a.meta[g] = n_mine > 0 ? Meta{row_begin, tile_begin > 0 ? 1 : 0} : Meta{-1, 0};
 
     auto timeout = [&](int where) {
         record_error(a.st, DSA_DEVERR_TIMEOUT, where);
         *abort_flag = 1;
     };
 
-    if (warp == kMmaWarp) {
+    if (warp >= kMmaWarp) {
         // ================================================================ MMA issue (one thread)
-        if (lane == 0) {
+        fewer_registers<kMmaRegs>();
+        if (warp == kMmaWarp && lane == 0) {
             const uint32_t kv0 = smem_addr(smem + kOffKV), q0 = smem_addr(smem + kOffQ), p0 = smem_addr(smem + kOffP);
             const uint64_t d_kv = desc_kmajor_sw128(kv0), d_q = desc_kmajor_sw128(q0);
             const uint64_t d_v = desc_mnmajor_sw128(kv0, kBlk), d_p = desc_mnmajor_sw128(p0, 8192);
             bool ok = true;
-            int64_t gt = 0, left = n_mine;
+            int gt = 0, left = n_mine;
             int t0 = tile_begin;
-            for (int64_t row = row_begin, k = 0; left > 0 && ok; ++row) {
+            int k = 0;
+            for (int row = row_begin; left > 0 && ok; ++row) {
                 const int n_row = tiles_of(row_view(b, a.view, row, nullptr)) - t0;
-                const int n = (int)min((int64_t)n_row, left);
+                const int n = min(n_row, left);
                 left -= n;
                 t0 = 0;
                 if (n == 0) continue;
@@ -350,80 +390,75 @@ dense_mla_kernel(Args a) {
         __syncwarp();
     } else if (warp >= kLoadWarp0) {
         // ================================================================ loaders
+        more_registers<kLoadRegs>();
         const int lt = tid - kLoadWarp0 * 32;              // 0..255
         const int lw = lt >> 5;                            // warps 0-3 the tile's first page, 4-7 its second
         const int half = lw >> 2;
-        const int tok0 = (lw & 3) * 16 + (lane >> 3);      // token of the page at step 0; step i adds 4 i
-        const int c8 = lane & 7;                           // 16-byte piece of a 128-byte group
+        // A warp's 16 tokens go four at a time.  Eight consecutive lanes hold four 16-byte
+        // pieces of two tokens whose numbers differ in bits 0 and 2, so that their
+        // swizzled 16-byte stores fall into 32 different banks.
+        const int par = lane >> 2 & 1;
+        const int tok0 = (lw & 3) * 16 + par + (lane >> 4) * 8;
+        const int c8 = (lane & 3) | (lane >> 3 & 1) << 2;  // 16-byte piece of a 128-byte group
+        auto tok_of = [&](int i) { return tok0 + ((2 * i) ^ (4 * par)); };   // token of the page at step i
         uint4 raw[2][kSteps], rope[kSteps];
         float scale[2][kSteps];
-        int64_t gt = 0, left = n_mine;
+        int gt = 0, left = n_mine;
         int t0 = tile_begin, k = 0;
         bool ok = true;
-        for (int64_t row = row_begin; left > 0; ++row) {
-            const Row w = row_view(b, a.view, row, lt == 0 ? a.st : nullptr);
-            const int n_row = tiles_of(w) - t0;
-            const int n = (int)min((int64_t)n_row, left);
+        for (int row = row_begin; left > 0; ++row) {
+            const int n_row = enter_row(row, lt == 0 ? a.st : nullptr) - t0;
+            const int n = min(n_row, left);
             const int tb = t0;                             // first tile of the piece
             left -= n;
             t0 = 0;
             if (n == 0) continue;
             if (load_any(!ok || *abort_flag)) break;      // one decision for all loader warps
-            // page ids of this warp's half of the next 32 tiles, one tile per lane, and of the 32 after
-            auto ids_from = [&](int t) -> int32_t {
-                const int u = 2 * (t + lane) + half;
-                return t + lane < tb + n && u < w.pages && w.page(u) < b.max_pages
-                           ? b.page_table[(int64_t)w.r * b.max_pages + w.page(u)] : -1;
+            // page id of this warp's half of tile t, -1 beyond the piece (loaded two tiles ahead)
+            auto page_of = [&](int t) -> int32_t {
+                const int u = 2 * t + half;
+                if (t >= tb + n || u >= w.pages) return -1;
+                const int lp = w.page(u);
+                return lp < b.max_pages ? __ldg(b.page_table + (int64_t)w.r * b.max_pages + lp) : -1;
             };
-            int32_t ids = ids_from(tb), ids_next = ids_from(tb + 32);
-            int base_t = tb;                               // tile of lane 0's id
-            auto page_of = [&](int t) -> int32_t {         // t in [base_t, base_t + 64)
-                const int rel = t - base_t;
-                const int32_t x = __shfl_sync(0xffffffffu, ids, rel & 31), y = __shfl_sync(0xffffffffu, ids_next, rel & 31);
-                return rel < 32 ? x : y;
-            };
+            int32_t pg = page_of(tb), pg1 = page_of(tb + 1);   // the tile being fetched and the one after
             // the tile being prefetched: its page, and which of this lane's four tokens are seen
             const uint8_t* src = nullptr;
             uint32_t seen = 0;
             bool bad = false;
             auto aim = [&](int t) {
-                const int32_t pg = page_of(t);
                 const int u = 2 * t + half;
                 seen = 0;
                 bad = false;
                 if (u < w.pages) {
-                    const int j0 = w.page(u) * kPage + tok0;
+                    const int j0 = w.page(u) * kPage;
 #pragma unroll
-                    for (int i = 0; i < kSteps; ++i) seen |= w.sees(j0 + 4 * i) ? 1u << i : 0u;
+                    for (int i = 0; i < kSteps; ++i) seen |= w.sees(j0 + tok_of(i)) ? 1u << i : 0u;
                     bad = pg < 0 || pg >= b.num_pages;
                     if (bad) {
                         if (__any_sync(0xffffffffu, seen != 0) && lane == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
                         seen = 0;
                     }
                 }
-                src = a.kv + (int64_t)(bad || u >= w.pages ? 0 : pg) * kKvPageBytes + tok0 * kKvTokenBytes;
+                src = a.kv + (int64_t)(bad || u >= w.pages ? 0 : pg) * kKvPageBytes;
             };
             auto fetch = [&](uint4 (&dst)[kSteps], int piece) {
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i)
-                    dst[i] = seen >> i & 1u ? ldg_pinned(reinterpret_cast<const uint4*>(src + i * 4 * kKvTokenBytes) + piece)
+                    dst[i] = seen >> i & 1u ? ldg_pinned(reinterpret_cast<const uint4*>(src + tok_of(i) * kKvTokenBytes) + piece)
                                             : make_uint4(0, 0, 0, 0);
             };
             auto fetch_group = [&](int gg) {               // 128 latent dims of the four tokens and their scales
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i)
                     scale[gg & 1][i] = seen >> i & 1u
-                                           ? ldg_pinned(reinterpret_cast<const float*>(src + i * 4 * kKvTokenBytes + 512) + gg) : 1.f;
+                                           ? ldg_pinned(reinterpret_cast<const float*>(src + tok_of(i) * kKvTokenBytes + 512) + gg) : 1.f;
                 fetch(raw[gg & 1], gg * 8 + c8);
             };
-            auto warm_l2 = [&](int t) {                    // the whole page, by one thread per half
-                if (t < tb + n) {
-                    const int32_t pg = page_of(t);
-                    if ((lw & 3) == 0 && lane == 0 && pg >= 0 && pg < b.num_pages)
-                        prefetch_l2(a.kv + (int64_t)pg * kKvPageBytes, kKvPageBytes);
-                }
+            auto warm_l2 = [&](int32_t p) {                // the whole page, by one thread per half
+                if ((lw & 3) == 0 && lane == 0 && p >= 0 && p < b.num_pages)
+                    prefetch_l2(a.kv + (int64_t)p * kKvPageBytes, kKvPageBytes);
             };
-            warm_l2(tb + 1);
             aim(tb);
             fetch_group(0);
             fetch_group(1);
@@ -433,7 +468,7 @@ dense_mla_kernel(Args a) {
             if (gt > 0 && ok) ok = wait_ab(&bars[B_SFULL], (uint32_t)((gt - 1) & 1), abort_flag);
             {
                 static_assert(64 * 72 == 18 * kLoadThreads, "18 16-byte pieces of q per thread");
-                const uint4* qrow = reinterpret_cast<const uint4*>(a.q + row * (64 * 576));
+                const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (int64_t)row * (64 * 576));
                 uint32_t mx = 0;                           // two bf16 magnitudes, compared as integers
 #pragma unroll 1
                 for (int u0 = 0; u0 < 18; u0 += 6) {
@@ -483,12 +518,9 @@ dense_mla_kernel(Args a) {
                 const uint32_t ph = (uint32_t)((gt - 1) & 1);
                 uint32_t off_range = 0;                    // a latent scale or a RoPE value fp16 cannot hold
                 const uint32_t seen_now = seen;
-                if (t - base_t == 31) {                    // the next tile opens the next batch of ids
-                    base_t += 32;
-                    ids = ids_next;
-                    ids_next = ids_from(base_t + 32);
-                }
-                warm_l2(t + 2);
+                warm_l2(pg1);
+                pg = pg1;
+                pg1 = page_of(t + 2);
                 const bool bad_now = bad;
                 const bool more = t + 1 < tb + n;
 #pragma unroll
@@ -497,7 +529,7 @@ dense_mla_kernel(Args a) {
                     if (gg == 0 && (lw & 3) == 0 && lane == 0) misc->bad[half] = bad_now ? 1 : 0;
 #pragma unroll
                     for (int i = 0; i < kSteps; ++i) {
-                        const int tk = half * kPage + tok0 + 4 * i;
+                        const int tk = half * kPage + tok_of(i);
                         const float sc = scale[gg & 1][i];
                         off_range |= (sc >= 0x1p-15f && sc <= 0x1p7f) ? 0u : 1u;
                         const __half2 sc2 = __float2half2_rn(sc);           // a power of two: exact
@@ -526,7 +558,7 @@ dense_mla_kernel(Args a) {
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
-                    const int tk = half * kPage + tok0 + 4 * i;
+                    const int tk = half * kPage + tok_of(i);
                     *reinterpret_cast<uint4*>(smem + kOffP + tk * 128 + ((c8 ^ (tk & 7)) * 16)) =
                         make_uint4(rope_bf16x2_to_h2(rope[i].x, off_range), rope_bf16x2_to_h2(rope[i].y, off_range),
                                    rope_bf16x2_to_h2(rope[i].z, off_range), rope_bf16x2_to_h2(rope[i].w, off_range));
@@ -542,16 +574,15 @@ dense_mla_kernel(Args a) {
     } else {
         // ================================================================ softmax + epilogue
         // Warp w reads TMEM lane quarter w % 4 (token / latent row st) and
-        // heads [32 hh, 32 hh + 32), hh = w / 4.
+        // heads [16 hh, 16 hh + 16), hh = w / 4.
         const int q4 = warp & 3, hh = warp >> 2;
         const int st = q4 * 32 + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
-        int64_t gt = 0, left = n_mine;
+        int gt = 0, left = n_mine;
         int t0 = tile_begin, k = 0;
-        for (int64_t row = row_begin; left > 0; ++row) {
-            const Row w = row_view(b, a.view, row, nullptr);
-            const int n_row = tiles_of(w) - t0;
-            const int n = (int)min((int64_t)n_row, left);
+        for (int row = row_begin; left > 0; ++row) {
+            const int n_row = enter_row(row, nullptr) - t0;
+            const int n = min(n_row, left);
             const int tb = t0;
             const bool whole = tb == 0 && n == n_row;
             left -= n;
@@ -559,29 +590,29 @@ dense_mla_kernel(Args a) {
             if (n == 0) continue;
             if (tid < 64) m_ref[tid] = -INFINITY;
             soft_sync();
-            float lsum[32];                                // this token lane's running sums of its 32 heads
+            float lsum[kHeads];                            // this token lane's running sums of its heads
 #pragma unroll
-            for (int c = 0; c < 32; ++c) lsum[c] = 0.f;
+            for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
             float sl2 = 0.f;
             bool failed = false;
-            const float4* mr4 = reinterpret_cast<const float4*>(m_ref + hh * 32);
+            const float4* mr4 = reinterpret_cast<const float4*>(m_ref + hh * kHeads);
             for (int t = tb; t < tb + n; ++t, ++gt) {
                 const bool ok = wait_ab(&bars[B_SFULL], (uint32_t)(gt & 1), abort_flag);
                 if (t == tb) sl2 = a.scale_log2 * misc->q_unscale[k & 1];
                 const int u = 2 * t + (st >> 6);
                 const bool valid = u < w.pages && w.sees(w.page(u) * kPage + (st & 63)) && misc->bad[st >> 6] == 0;
-                // S^T row of this token for the warp's 32 heads, in log2 units; tokens not seen -> -inf
-                auto load_s = [&](float (&v)[32]) {
-                    uint32_t x[32];
-                    tmem_ld_32x32b_x32(lane_addr + kColS + hh * 32, x);
+                // S^T row of this token for the warp's heads, in log2 units; tokens not seen -> -inf
+                auto load_s = [&](float (&v)[kHeads]) {
+                    uint32_t x[kHeads];
+                    tmem_ld_32x32b_x16(lane_addr + kColS + hh * kHeads, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 32; ++h) v[h] = valid ? __uint_as_float(x[h]) * sl2 : -INFINITY;
+                    for (int h = 0; h < kHeads; ++h) v[h] = valid ? __uint_as_float(x[h]) * sl2 : -INFINITY;
                 };
-                // P of the current references, and its P^T row (heads 32 hh.. as fp16, MN-major swizzle)
-                auto write_p = [&](float (&v)[32]) {
+                // P of the current references, and its P^T row (heads 16 hh.. as fp16, MN-major swizzle)
+                auto write_p = [&](float (&v)[kHeads]) {
 #pragma unroll
-                    for (int c4 = 0; c4 < 8; ++c4) {
+                    for (int c4 = 0; c4 < kHeads / 4; ++c4) {
                         const float4 m = mr4[c4];
                         v[4 * c4] = valid ? ex2_approx(v[4 * c4] - m.x) : 0.f;
                         v[4 * c4 + 1] = valid ? ex2_approx(v[4 * c4 + 1] - m.y) : 0.f;
@@ -590,22 +621,22 @@ dense_mla_kernel(Args a) {
                     }
                     uint8_t* prow = smem + kOffP + st * 128;
 #pragma unroll
-                    for (int cc = 0; cc < 4; ++cc) {
-                        const int c = hh * 4 + cc;
+                    for (int cc = 0; cc < kHeads / 8; ++cc) {
+                        const int c = hh * (kHeads / 8) + cc;
                         *reinterpret_cast<uint4*>(prow + ((c ^ (st & 7)) * 16)) =
                             make_uint4(pack_h2(v[8 * cc], v[8 * cc + 1]), pack_h2(v[8 * cc + 2], v[8 * cc + 3]),
                                        pack_h2(v[8 * cc + 4], v[8 * cc + 5]), pack_h2(v[8 * cc + 6], v[8 * cc + 7]));
                     }
                     fence_proxy_async_smem();
                 };
-                float v[32];
+                float v[kHeads];
                 tc_fence_after();
                 load_s(v);
                 // ---- a score above its head's reference by more than 2^(kTau + kShift) makes every
                 //      warp take new references first (always on the piece's first tile)
                 bool over = false;
 #pragma unroll
-                for (int c4 = 0; c4 < 8; ++c4) {
+                for (int c4 = 0; c4 < kHeads / 4; ++c4) {
                     const float4 m = mr4[c4];
                     over |= v[4 * c4] > m.x + (kTau + kShift) || v[4 * c4 + 1] > m.y + (kTau + kShift) ||
                             v[4 * c4 + 2] > m.z + (kTau + kShift) || v[4 * c4 + 3] > m.w + (kTau + kShift);
@@ -617,8 +648,8 @@ dense_mla_kernel(Args a) {
                         break;
                     }
                     load_s(v);
-                    xreduce32<true>(v, lane);                   // per-head tile max (consumes v)
-                    red[q4 * 64 + hh * 32 + lane] = v[0];
+                    xreduce16<true>(v, lane);                   // per-head tile max (consumes v)
+                    if (lane < kHeads) red[q4 * 64 + hh * kHeads + lane] = v[0];
                     soft_sync();
                     if (tid < 64) {
                         const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid])) - kShift;
@@ -631,18 +662,18 @@ dense_mla_kernel(Args a) {
                     if (t > tb) {                               // rescale the resident O^T columns of these heads
 #pragma unroll 1
                         for (int mb = 0; mb < 4; ++mb) {
-                            uint32_t o[32];
-                            const uint32_t addr = lane_addr + kColO + mb * 64 + hh * 32;
-                            tmem_ld_32x32b_x32(addr, o);
+                            uint32_t o[kHeads];
+                            const uint32_t addr = lane_addr + kColO + mb * 64 + hh * kHeads;
+                            tmem_ld_32x32b_x16(addr, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[hh * 32 + c]);
-                            tmem_st_32x32b_x32(addr, o);
+                            for (int c = 0; c < kHeads; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[hh * kHeads + c]);
+                            tmem_st_32x32b_x16(addr, o);
                         }
                         tmem_st_wait();
                     }
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) lsum[c] *= alpha[hh * 32 + c];
+                    for (int c = 0; c < kHeads; ++c) lsum[c] *= alpha[hh * kHeads + c];
                     load_s(v);
                     write_p(v);
                 }
@@ -650,7 +681,7 @@ dense_mla_kernel(Args a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_PREADY]);    // P^T written, S^T read, O^T rescaled
 #pragma unroll
-                for (int c = 0; c < 32; ++c) lsum[c] += v[c];
+                for (int c = 0; c < kHeads; ++c) lsum[c] += v[c];
             }
             if (failed) {
                 if (tid == 0) timeout(63);
@@ -658,8 +689,8 @@ dense_mla_kernel(Args a) {
             }
             ++k;
             // ---- per-head sums over the piece: the lanes' running sums reduced
-            xreduce32<false>(lsum, lane);
-            red[256 + q4 * 64 + hh * 32 + lane] = lsum[0];
+            xreduce16<false>(lsum, lane);
+            if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];
             // ---- piece end: O^T is final once the last P.V completes
             const bool ok = wait_ab(&bars[B_PV3], (uint32_t)((gt - 1) & 1), abort_flag);
             if (soft_any(!ok)) {
@@ -669,21 +700,21 @@ dense_mla_kernel(Args a) {
             tc_fence_after();
             if (tid < 64) l_acc[tid] = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
             soft_sync();
-            const int64_t unit = 2 * g + (k == 1 ? 0 : 1);      // a share's first piece, or its last
+            const int64_t unit = 2 * (int64_t)blockIdx.x + (k == 1 ? 0 : 1);      // a share's first piece, or its last
 #pragma unroll 1
             for (int mb = 0; mb < 4; ++mb) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(lane_addr + kColO + mb * 64 + hh * 32, o);
+                uint32_t o[kHeads];
+                tmem_ld_32x32b_x16(lane_addr + kColO + mb * 64 + hh * kHeads, o);
                 tmem_ld_wait();
                 const int d = mb * 128 + st;                           // latent dim of this TMEM lane
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {                         // a warp stores 32 consecutive dims
-                    const int h = hh * 32 + c;
+                for (int c = 0; c < kHeads; ++c) {                     // a warp stores 32 consecutive dims
+                    const int h = hh * kHeads + c;
                     const float ov = __uint_as_float(o[c]);
                     if (whole) {
                         const float l = l_acc[h];
                         const float val = l > 0.f ? ov / l : 0.f;
-                        const int64_t oi = (row * 64 + h) * 512 + d;
+                        const int64_t oi = ((int64_t)row * 64 + h) * 512 + d;
                         if (a.out_f32) static_cast<float*>(a.out)[oi] = val;
                         else static_cast<__nv_bfloat16*>(a.out)[oi] = __float2bfloat16_rn(val);
                     } else {
@@ -695,7 +726,7 @@ dense_mla_kernel(Args a) {
             if (tid < 64) {
                 const float l = l_acc[tid];
                 if (!whole) a.part_ml[unit * 64 + tid] = make_float2(m_ref[tid], l);
-                else if (a.lse) a.lse[row * 64 + tid] = l > 0.f ? (m_ref[tid] + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                else if (a.lse) a.lse[(int64_t)row * 64 + tid] = l > 0.f ? (m_ref[tid] + log2f(l)) * 0.69314718055994531f : -INFINITY;
             }
             soft_sync();                                    // O^T and the references may be reused
         }
@@ -818,6 +849,7 @@ static dsa_status launch(const void* q, const uint8_t* kv, const dsa_batch* b, V
     if (b->total_q == 0) return DSA_OK;
     if (!q || !kv || !out) return DSA_ERR_INVALID_ARGUMENT;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(out)) return DSA_ERR_ALIGNMENT;
+    if (b->total_q * most_tiles(b, view) / device_sm_count() > 0x7ffffff0LL) return DSA_ERR_UNSUPPORTED;   // 32-bit tile counts of a share
     if (!ws) return DSA_ERR_INVALID_ARGUMENT;
     if (bytes < ws_bytes(device_sm_count())) return DSA_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned16(ws)) return DSA_ERR_ALIGNMENT;
