@@ -22,17 +22,20 @@
 // the next tile starts behind the last P.V.  P^T takes the place of the tile's
 // RoPE block, which S^T has read by then.
 //
-// Roles (seven warpgroups):
-//   warps 0-15  softmax and epilogue: a thread owns one token (TMEM lane) and 16
-//               heads.  P is formed against a reference that lags the maximum by
-//               up to 2^8 before O^T is rescaled, and shifted up by 2^7 so that
-//               fp16 holds probabilities down to 2^-32 of the largest.
-//   warps 16-23 loaders: read the pages into registers two groups ahead (whole pages
-//               are prefetched into L2 two tiles ahead), dequantise into the
-//               128-byte-swizzled tile (exact for scales in [2^-15, 2^7]) and
-//               convert each row's Q, scaled by the power of two that puts its
-//               largest |q| in [2^14, 2^15).  Rows that are not seen become zeros.
-//   warp 24     issues the MMAs (its warpgroup hands its registers to the others).
+// Warps 0-15 do everything but issue the MMAs; a tile's phases follow one another,
+// so the same warps take them in turn:
+//   softmax     a thread owns one token (TMEM lane) and 16 heads.  P is formed
+//               against a reference that lags the maximum by up to 2^12 before
+//               O^T is rescaled, and shifted up by 2^3, so that fp16 holds
+//               probabilities down to 2^-28 of the reference;
+//   next tile   its rows, read into registers a tile ahead (whole pages are
+//               prefetched into L2 before that), are dequantised into the
+//               128-byte-swizzled tile (exact for scales in [2^-15, 2^7]), each
+//               part as soon as it is free.  Rows that are not seen become zeros;
+//   next row    its Q, scaled by the power of two that puts its largest |q| in
+//               [2^14, 2^15), while the last P.V runs; then the epilogue, while
+//               the first S^T of the next row runs.
+// Warp 16 issues the MMAs.
 // Every wait is time-bounded; a timeout is recorded and the CTA winds down.
 #include <algorithm>
 
@@ -81,11 +84,15 @@ struct Row {
     uint64_t mask;
     int32_t sink_pages, first_page, pages;
     __device__ __forceinline__ int page(int u) const volatile { return u < sink_pages ? u : first_page + u - sink_pages; }
-    __device__ __forceinline__ bool sees(int j) const volatile {
-        if (j < sink_end || (j >= first && j < end)) return true;
-        const unsigned u = (unsigned)(j - prefix);
-        return u < 64u && (mask >> u & 1u);
+    // The positions of logical page lp that the row sees, one bit each.
+    __device__ __forceinline__ uint64_t seen(int lp) const volatile {
+        const int j = lp * kPage;
+        const uint64_t sinks = below(sink_end - j), from = below(end - j) & ~below(first - j);
+        const int sh = prefix - j;
+        const uint64_t news = sh >= 64 || sh <= -64 ? 0ull : sh >= 0 ? mask << sh : mask >> -sh;
+        return sinks | from | news;
     }
+    static __device__ __forceinline__ uint64_t below(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 };
 
 // Row `row` of the batch.  A row that sees nothing keeps one (empty) page, so
@@ -128,19 +135,16 @@ using namespace mlc;
 
 constexpr int kTok = 128;                                  // tokens per tile: two pages
 constexpr int kBlk = kTok * 128;                           // one 64-dim K-block of the tile
-constexpr int kSoftWarps = 16;                             // four per TMEM lane quarter, 16 heads each
-constexpr int kHeads = 16;                                 // heads of a softmax warp
-constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kLoadWarp0 = kSoftWarps;
-constexpr int kLoadWarps = 8;
-constexpr int kLoadThreads = kLoadWarps * 32;
-constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;
-constexpr int kThreads = (kMmaWarp + 4) * 32;              // seven warpgroups; the last one's first warp issues the MMAs
-constexpr int kPlanThreads = 512;                          // threads that count the rows' tiles
-constexpr int kSoftBar = 1, kLoadBar = 2, kPlanBar = 3;
-constexpr int kSteps = kTok / kLoadWarps / 4;              // a loader warp's 16 tokens, four at a time
-constexpr float kTau = 8.0f;                               // lazy-rescale threshold, log2 units
-constexpr float kShift = 7.0f;                             // P is scaled by 2^7: P <= 2^(kTau + kShift)
+constexpr int kWorkWarps = 16;
+constexpr int kWorkThreads = kWorkWarps * 32;
+constexpr int kHeads = 16;                                 // heads of a warp in the softmax: four warps a TMEM lane quarter
+constexpr int kMmaWarp = kWorkWarps;
+constexpr int kThreads = (kMmaWarp + 4) * 32;              // five warpgroups; the last one's first warp issues the MMAs
+constexpr int kWorkBar = 1;
+constexpr int kSteps = kTok / kWorkWarps / 4;              // a warp's 8 tokens of a tile, four at a time
+constexpr float kTau = 12.0f;                              // lazy-rescale threshold, log2 units
+constexpr float kShift = 3.0f;                             // P is scaled by 2^3 ..
+constexpr float kPMax = 0x1p15f;                           // .. so at most 2^(kTau + kShift): inside fp16
 constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
 constexpr uint32_t kIdescPV = idesc_f16_f32(128, 64, true, true);
 constexpr uint32_t kColS = 0;                              // TMEM: S^T [128 x 64]
@@ -167,8 +171,7 @@ static_assert(B_COUNT <= 16, "barrier block");
 struct Misc {
     uint32_t tmem_base;
     int32_t abort;
-    uint32_t qmax[kLoadWarps];  // per loader warp: largest bf16 magnitude of the row's q
-    float q_unscale[2];         // 2^-kq of the row's Q, by piece parity
+    uint32_t qmax[kWorkWarps];  // per warp: largest bf16 magnitude of the row's q
     int32_t bad[2];             // the tile's page (first, second half) is outside the cache
     int32_t scratch[32];
     int64_t total;              // tiles of the whole batch
@@ -183,18 +186,16 @@ struct Meta {
     int32_t inside;
 };
 
-__device__ __forceinline__ bool soft_any(bool pred) { return bar_any<kSoftBar, kSoftThreads>(pred); }
-__device__ __forceinline__ void soft_sync() { bar_sync<kSoftBar, kSoftThreads>(); }
-__device__ __forceinline__ bool load_any(bool pred) { return bar_any<kLoadBar, kLoadThreads>(pred); }
-__device__ __forceinline__ void load_sync() { bar_sync<kLoadBar, kLoadThreads>(); }
+__device__ __forceinline__ bool work_any(bool pred) { return bar_any<kWorkBar, kWorkThreads>(pred); }
+__device__ __forceinline__ void work_sync() { bar_sync<kWorkBar, kWorkThreads>(); }
 
 __device__ __forceinline__ int tiles_of(const Row& w) { return (w.pages + 1) >> 1; }
 
-// Counts the tiles of all rows (kPlanThreads threads, consecutive rows each)
+// Counts the tiles of all rows (the workers' threads, consecutive rows each)
 // and finds where share g of G begins.  Returns the share's tiles.
 __device__ __forceinline__ void plan_share(const Args& a, Misc* misc, int tid) {
     const int64_t T = a.b.total_q;
-    const int64_t per = (T + kPlanThreads - 1) / kPlanThreads;
+    const int64_t per = (T + kWorkThreads - 1) / kWorkThreads;
     const int64_t r0 = min(T, tid * per), r1 = min(T, r0 + per);
     int64_t mine = 0;
     for (int64_t r = r0; r < r1; ++r) mine += tiles_of(row_view(a.b, a.view, r, nullptr));
@@ -207,9 +208,9 @@ __device__ __forceinline__ void plan_share(const Args& a, Misc* misc, int tid) {
     }
     int64_t* tot = reinterpret_cast<int64_t*>(misc->scratch);     // 16 warps
     if ((tid & 31) == 31) tot[tid >> 5] = x;
-    bar_sync<kPlanBar, kPlanThreads>();
+    work_sync();
     int64_t before = 0, all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
+    for (int w = 0; w < kWorkThreads / 32; ++w) {
         if (w < (tid >> 5)) before += tot[w];
         all += tot[w];
     }
@@ -232,12 +233,10 @@ __device__ __forceinline__ void plan_share(const Args& a, Misc* misc, int tid) {
     }
 }
 
-// The roles' registers per thread: 72 at launch (65,536 / 896 threads, in
-// eights), of which the MMA warpgroup gives most to the loaders:
-// 512 x 72 + 256 x 88 + 128 x 40 = 896 x 72.
-constexpr int kLaunchRegs = 72, kLoadRegs = 88, kMmaRegs = 40;
-static_assert(kSoftThreads * kLaunchRegs + kLoadThreads * kLoadRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs,
-              "more registers than the launch holds");
+// Registers per thread: 96 at launch (65,536 / 640 threads, in eights), of which
+// the MMA warpgroup gives most to the others: 512 x 112 + 128 x 32 = 640 x 96.
+constexpr int kLaunchRegs = 96, kWorkRegs = 112, kMmaRegs = 32;
+static_assert(kWorkThreads * kWorkRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "more registers than the launch holds");
 template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
@@ -305,10 +304,10 @@ dense_mla_kernel(Args a) {
     };
 
     if (tid == 0) {
-        mbar_init(&bars[B_QFULL], kLoadWarps);
-        for (int i = 0; i < 5; ++i) mbar_init(&bars[B_FULL0 + i], kLoadWarps);
+        mbar_init(&bars[B_QFULL], kWorkWarps);
+        for (int i = 0; i < 5; ++i) mbar_init(&bars[B_FULL0 + i], kWorkWarps);
         mbar_init(&bars[B_SFULL], 1);
-        mbar_init(&bars[B_PREADY], kSoftWarps);
+        mbar_init(&bars[B_PREADY], kWorkWarps);
         for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PV0 + i], 1);
         mbar_init(&bars[B_DRAIN], 1);
         misc->abort = 0;
@@ -319,7 +318,7 @@ dense_mla_kernel(Args a) {
         tmem_relinquish();
     }
     pdl_wait();
-    if (tid < kPlanThreads) plan_share(a, misc, tid);
+    if (tid < kWorkThreads) plan_share(a, misc, tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -388,219 +387,182 @@ dense_mla_kernel(Args a) {
             }
         }
         __syncwarp();
-    } else if (warp >= kLoadWarp0) {
-        // ================================================================ loaders
-        more_registers<kLoadRegs>();
-        const int lt = tid - kLoadWarp0 * 32;              // 0..255
-        const int lw = lt >> 5;                            // warps 0-3 the tile's first page, 4-7 its second
-        const int half = lw >> 2;
-        // A warp's 16 tokens go four at a time.  Eight consecutive lanes hold four 16-byte
-        // pieces of two tokens whose numbers differ in bits 0 and 2, so that their
-        // swizzled 16-byte stores fall into 32 different banks.
+    } else if (n_mine > 0) {
+        // ================================================================ workers
+        more_registers<kWorkRegs>();
+        // ---- rows of a tile: warps 0-7 its first page, 8-15 its second, 8 tokens each.
+        // Eight consecutive lanes hold four 16-byte pieces of two tokens whose numbers
+        // differ in bits 0 and 2, so that their swizzled 16-byte stores fall into 32
+        // different banks.
+        const int half = warp >> 3;
         const int par = lane >> 2 & 1;
-        const int tok0 = (lw & 3) * 16 + par + (lane >> 4) * 8;
+        const int tok0 = (warp & 7) * 8 + par + (lane >> 4) * 2;
         const int c8 = (lane & 3) | (lane >> 3 & 1) << 2;  // 16-byte piece of a 128-byte group
-        auto tok_of = [&](int i) { return tok0 + ((2 * i) ^ (4 * par)); };   // token of the page at step i
-        uint4 raw[2][kSteps], rope[kSteps];
-        float scale[2][kSteps];
-        int gt = 0, left = n_mine;
-        int t0 = tile_begin, k = 0;
-        bool ok = true;
-        for (int row = row_begin; left > 0; ++row) {
-            const int n_row = enter_row(row, lt == 0 ? a.st : nullptr) - t0;
-            const int n = min(n_row, left);
-            const int tb = t0;                             // first tile of the piece
-            left -= n;
-            t0 = 0;
-            if (n == 0) continue;
-            if (load_any(!ok || *abort_flag)) break;      // one decision for all loader warps
-            // page id of this warp's half of tile t, -1 beyond the piece (loaded two tiles ahead)
-            auto page_of = [&](int t) -> int32_t {
-                const int u = 2 * t + half;
-                if (t >= tb + n || u >= w.pages) return -1;
-                const int lp = w.page(u);
-                return lp < b.max_pages ? __ldg(b.page_table + (int64_t)w.r * b.max_pages + lp) : -1;
-            };
-            int32_t pg = page_of(tb), pg1 = page_of(tb + 1);   // the tile being fetched and the one after
-            // the tile being prefetched: its page, and which of this lane's four tokens are seen
-            const uint8_t* src = nullptr;
-            uint32_t seen = 0;
-            bool bad = false;
-            auto aim = [&](int t) {
-                const int u = 2 * t + half;
-                seen = 0;
-                bad = false;
-                if (u < w.pages) {
-                    const int j0 = w.page(u) * kPage;
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) seen |= w.sees(j0 + tok_of(i)) ? 1u << i : 0u;
-                    bad = pg < 0 || pg >= b.num_pages;
-                    if (bad) {
-                        if (__any_sync(0xffffffffu, seen != 0) && lane == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
-                        seen = 0;
-                    }
-                }
-                src = a.kv + (int64_t)(bad || u >= w.pages ? 0 : pg) * kKvPageBytes;
-            };
-            auto fetch = [&](uint4 (&dst)[kSteps], int piece) {
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-                    dst[i] = seen >> i & 1u ? ldg_pinned(reinterpret_cast<const uint4*>(src + tok_of(i) * kKvTokenBytes) + piece)
-                                            : make_uint4(0, 0, 0, 0);
-            };
-            auto fetch_group = [&](int gg) {               // 128 latent dims of the four tokens and their scales
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-                    scale[gg & 1][i] = seen >> i & 1u
-                                           ? ldg_pinned(reinterpret_cast<const float*>(src + tok_of(i) * kKvTokenBytes + 512) + gg) : 1.f;
-                fetch(raw[gg & 1], gg * 8 + c8);
-            };
-            auto warm_l2 = [&](int32_t p) {                // the whole page, by one thread per half
-                if ((lw & 3) == 0 && lane == 0 && p >= 0 && p < b.num_pages)
-                    prefetch_l2(a.kv + (int64_t)p * kKvPageBytes, kKvPageBytes);
-            };
-            aim(tb);
-            fetch_group(0);
-            fetch_group(1);
-            fetch(rope, 33 + c8);
-            // ---- Q of the row -> fp16, K-major, 128-byte swizzle, once the previous row's
-            //      last S^T has read the one before
-            if (gt > 0 && ok) ok = wait_ab(&bars[B_SFULL], (uint32_t)((gt - 1) & 1), abort_flag);
-            {
-                static_assert(64 * 72 == 18 * kLoadThreads, "18 16-byte pieces of q per thread");
-                const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (int64_t)row * (64 * 576));
-                uint32_t mx = 0;                           // two bf16 magnitudes, compared as integers
-#pragma unroll 1
-                for (int u0 = 0; u0 < 18; u0 += 6) {
-                    uint4 qv[6];
-#pragma unroll
-                    for (int u = 0; u < 6; ++u) qv[u] = __ldg(qrow + lt + (u0 + u) * kLoadThreads);
-#pragma unroll
-                    for (int u = 0; u < 6; ++u)
-                        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(qv[u].x & 0x7fff7fffu, qv[u].y & 0x7fff7fffu),
-                                                   __vmaxu2(qv[u].z & 0x7fff7fffu, qv[u].w & 0x7fff7fffu)));
-                }
-                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-                if (lane == 0) misc->qmax[lw] = mx;
-                load_sync();
-                uint32_t amax = 0;
-#pragma unroll
-                for (int v = 0; v < kLoadWarps; ++v) amax = max(amax, misc->qmax[v]);
-                const int eq = amax == 0 ? 14 : (int)(amax >> 7) - 127;
-                const int kq = min(126, max(-126, 14 - eq));
-                const float sc = __int_as_float((127 + kq) << 23);
-                if (lt == 0) misc->q_unscale[k & 1] = __int_as_float((127 - kq) << 23);
-#pragma unroll 1
-                for (int u0 = 0; u0 < 18; u0 += 6) {
-                    uint4 qv[6];
-#pragma unroll
-                    for (int u = 0; u < 6; ++u) qv[u] = __ldg(qrow + lt + (u0 + u) * kLoadThreads);
-#pragma unroll
-                    for (int u = 0; u < 6; ++u) {
-                        const int c = lt + (u0 + u) * kLoadThreads;
-                        const int h = c / 72, cq = c % 72;
-                        const int blk = cq >> 3, ch = cq & 7;
-                        *reinterpret_cast<uint4*>(smem + kOffQ + blk * 8192 + h * 128 + ((ch ^ (h & 7)) * 16)) =
-                            make_uint4(bf16x2_scaled_to_h2(qv[u].x, sc), bf16x2_scaled_to_h2(qv[u].y, sc),
-                                       bf16x2_scaled_to_h2(qv[u].z, sc), bf16x2_scaled_to_h2(qv[u].w, sc));
-                    }
-                }
-                if (lt == 0 && amax >= 0x7f80u) record_error(a.st, DSA_DEVERR_FP16_RANGE, row);   // inf / NaN in q
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_QFULL]);
-                load_sync();                               // qmax may be written again
-            }
-            ++k;
-            // ---- tiles: latent groups 0..3 (free once the previous tile's P.V of the group is
-            //      done), then the RoPE block (free, as P^T, with the last group)
-            for (int t = tb; t < tb + n && ok; ++t, ++gt) {
-                const uint32_t ph = (uint32_t)((gt - 1) & 1);
-                uint32_t off_range = 0;                    // a latent scale or a RoPE value fp16 cannot hold
-                const uint32_t seen_now = seen;
-                warm_l2(pg1);
-                pg = pg1;
-                pg1 = page_of(t + 2);
-                const bool bad_now = bad;
-                const bool more = t + 1 < tb + n;
-#pragma unroll
-                for (int gg = 0; gg < 4; ++gg) {
-                    if (gt > 0 && !(ok = wait_ab(&bars[B_PV0 + gg], ph, abort_flag))) break;
-                    if (gg == 0 && (lw & 3) == 0 && lane == 0) misc->bad[half] = bad_now ? 1 : 0;
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        const int tk = half * kPage + tok_of(i);
-                        const float sc = scale[gg & 1][i];
-                        off_range |= (sc >= 0x1p-15f && sc <= 0x1p7f) ? 0u : 1u;
-                        const __half2 sc2 = __float2half2_rn(sc);           // a power of two: exact
-                        const uint4 x = raw[gg & 1][i];
-                        // 16 FP8 dims 128 gg + 16 c8 .. -> K-block 2 gg + c8 / 4, 16-byte chunks 2 (c8 % 4), +1
-                        uint8_t* blkp = smem + kOffKV + (2 * gg + (c8 >> 2)) * kBlk + tk * 128;
-                        const int ch = 2 * (c8 & 3), sw = tk & 7;
-                        *reinterpret_cast<uint4*>(blkp + ((ch ^ sw) * 16)) =
-                            make_uint4(e4m3x2_scaled_h2(x.x & 0xffffu, sc2), e4m3x2_scaled_h2(x.x >> 16, sc2),
-                                       e4m3x2_scaled_h2(x.y & 0xffffu, sc2), e4m3x2_scaled_h2(x.y >> 16, sc2));
-                        *reinterpret_cast<uint4*>(blkp + (((ch + 1) ^ sw) * 16)) =
-                            make_uint4(e4m3x2_scaled_h2(x.z & 0xffffu, sc2), e4m3x2_scaled_h2(x.z >> 16, sc2),
-                                       e4m3x2_scaled_h2(x.w & 0xffffu, sc2), e4m3x2_scaled_h2(x.w >> 16, sc2));
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[B_FULL0 + gg]);
-                    // the registers just emptied take the group two ahead
-                    if (gg < 2) {
-                        fetch_group(gg + 2);
-                    } else if (more) {
-                        if (gg == 2) aim(t + 1);
-                        fetch_group(gg - 2);
-                    }
-                }
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const int tk = half * kPage + tok_of(i);
-                    *reinterpret_cast<uint4*>(smem + kOffP + tk * 128 + ((c8 ^ (tk & 7)) * 16)) =
-                        make_uint4(rope_bf16x2_to_h2(rope[i].x, off_range), rope_bf16x2_to_h2(rope[i].y, off_range),
-                                   rope_bf16x2_to_h2(rope[i].z, off_range), rope_bf16x2_to_h2(rope[i].w, off_range));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_FULL4]);
-                if (off_range && seen_now) record_error(a.st, DSA_DEVERR_FP16_RANGE, lane);
-                if (more) fetch(rope, 33 + c8);
-            }
-            if (!ok && lane == 0) timeout(62);
-        }
-    } else {
-        // ================================================================ softmax + epilogue
-        // Warp w reads TMEM lane quarter w % 4 (token / latent row st) and
-        // heads [16 hh, 16 hh + 16), hh = w / 4.
+        auto tok_of = [&](int i) { return tok0 + 4 * (i ^ par); };   // token of the page at step i
+        // ---- softmax: warp w reads TMEM lane quarter w % 4 (token / latent row st) and
+        // heads [16 hh, 16 hh + 16), hh = w / 4
         const int q4 = warp & 3, hh = warp >> 2;
         const int st = q4 * 32 + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
-        int gt = 0, left = n_mine;
-        int t0 = tile_begin, k = 0;
-        for (int row = row_begin; left > 0; ++row) {
-            const int n_row = enter_row(row, nullptr) - t0;
-            const int n = min(n_row, left);
-            const int tb = t0;
-            const bool whole = tb == 0 && n == n_row;
-            left -= n;
-            t0 = 0;
-            if (n == 0) continue;
-            if (tid < 64) m_ref[tid] = -INFINITY;
-            soft_sync();
-            float lsum[kHeads];                            // this token lane's running sums of its heads
+        const float4* mr4 = reinterpret_cast<const float4*>(m_ref + hh * kHeads);
+
+        int row = row_begin, t = tile_begin, left = n_mine, gt = 0;
+        int t_end = 0;                                     // end of the row's piece
+        bool ok = true;
+        uint4 raw[2][kSteps], rope[kSteps], scv[kSteps];   // rows in flight: two latent groups, RoPE dims, scales
+        uint32_t seen = 0;                                 // which of this lane's tokens of the fetched tile are seen
+        bool bad = false;                                  // its page is outside the cache
+        const uint8_t* src = nullptr;
+        int32_t pg = -1, pg1 = -1;                         // pages of the tile to fetch next and the one after
+        // page id of this warp's half of tile x, -1 beyond the piece
+        auto page_of = [&](int x) -> int32_t {
+            const int u = 2 * x + half;
+            if (x >= t_end || u >= w.pages) return -1;
+            const int lp = w.page(u);
+            return lp < b.max_pages ? __ldg(b.page_table + (int64_t)w.r * b.max_pages + lp) : -1;
+        };
+        auto aim = [&](int x) {                            // fetches are for tile x from here on
+            const int u = 2 * x + half;
+            uint64_t m = u < w.pages ? w.seen(w.page(u)) : 0ull;
+            bad = pg < 0 || pg >= b.num_pages;
+            if (bad && m) {
+                if (lane == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
+                m = 0;
+            }
+            seen = 0;
 #pragma unroll
-            for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
-            float sl2 = 0.f;
-            bool failed = false;
-            const float4* mr4 = reinterpret_cast<const float4*>(m_ref + hh * kHeads);
-            for (int t = tb; t < tb + n; ++t, ++gt) {
-                const bool ok = wait_ab(&bars[B_SFULL], (uint32_t)(gt & 1), abort_flag);
-                if (t == tb) sl2 = a.scale_log2 * misc->q_unscale[k & 1];
+            for (int i = 0; i < kSteps; ++i) seen |= (uint32_t)(m >> tok_of(i) & 1u) << i;
+            src = a.kv + (int64_t)(bad ? 0 : pg) * kKvPageBytes;
+            pg = pg1;
+            pg1 = page_of(x + 2);
+            if ((warp & 7) == 0 && lane == 0 && pg >= 0 && pg < b.num_pages)      // the next tile's page
+                prefetch_l2(a.kv + (int64_t)pg * kKvPageBytes, kKvPageBytes);
+        };
+        auto fetch = [&](uint4 (&dst)[kSteps], int piece, uint32_t fill) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+                dst[i] = seen >> i & 1u ? ldg_pinned(reinterpret_cast<const uint4*>(src + tok_of(i) * kKvTokenBytes) + piece)
+                                        : make_uint4(fill, fill, fill, fill);
+        };
+        // The fetched tile into shared memory, latent groups 0..3 (free once tile gt's P.V of
+        // the group is done; `first`: nothing to wait for), then the RoPE block (free, as
+        // P^T, with the last group).  The registers emptied take the group two ahead.
+        auto put_tile = [&](int x, bool first) {
+            const uint32_t ph = (uint32_t)(gt & 1);
+            const bool more = x + 1 < t_end;
+            uint32_t off_range = 0;                        // a latent scale or a RoPE value fp16 cannot hold
+#pragma unroll
+            for (int gg = 0; gg < 4; ++gg) {
+                if (!first && ok) ok = wait_ab(&bars[B_PV0 + gg], ph, abort_flag);
+                if (gg == 0 && (warp & 7) == 0 && lane == 0) misc->bad[half] = bad ? 1 : 0;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const int tk = half * kPage + tok_of(i);
+                    const float sc = __uint_as_float(gg == 0 ? scv[i].x : gg == 1 ? scv[i].y : gg == 2 ? scv[i].z : scv[i].w);
+                    off_range |= sc >= 0x1p-15f && sc <= 0x1p7f ? 0u : 1u;
+                    const __half2 sc2 = __float2half2_rn(sc);   // a power of two: exact
+                    const uint4 v = raw[gg & 1][i];
+                    // 16 FP8 dims 128 gg + 16 c8 .. -> K-block 2 gg + c8 / 4, 16-byte chunks 2 (c8 % 4), +1
+                    uint8_t* blkp = smem + kOffKV + (2 * gg + (c8 >> 2)) * kBlk + tk * 128;
+                    const int ch = 2 * (c8 & 3), sw = tk & 7;
+                    *reinterpret_cast<uint4*>(blkp + ((ch ^ sw) * 16)) =
+                        make_uint4(e4m3x2_scaled_h2(v.x & 0xffffu, sc2), e4m3x2_scaled_h2(v.x >> 16, sc2),
+                                   e4m3x2_scaled_h2(v.y & 0xffffu, sc2), e4m3x2_scaled_h2(v.y >> 16, sc2));
+                    *reinterpret_cast<uint4*>(blkp + (((ch + 1) ^ sw) * 16)) =
+                        make_uint4(e4m3x2_scaled_h2(v.z & 0xffffu, sc2), e4m3x2_scaled_h2(v.z >> 16, sc2),
+                                   e4m3x2_scaled_h2(v.w & 0xffffu, sc2), e4m3x2_scaled_h2(v.w >> 16, sc2));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_FULL0 + gg]);
+                if (gg < 2) {
+                    fetch(raw[gg], (gg + 2) * 8 + c8, 0u);
+                } else if (more) {
+                    if (gg == 2) aim(x + 1);
+                    fetch(raw[gg - 2], (gg - 2) * 8 + c8, 0u);
+                }
+            }
+            if (more) fetch(scv, 32, 0x3f800000u);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int tk = half * kPage + tok_of(i);
+                *reinterpret_cast<uint4*>(smem + kOffP + tk * 128 + ((c8 ^ (tk & 7)) * 16)) =
+                    make_uint4(rope_bf16x2_to_h2(rope[i].x, off_range), rope_bf16x2_to_h2(rope[i].y, off_range),
+                               rope_bf16x2_to_h2(rope[i].z, off_range), rope_bf16x2_to_h2(rope[i].w, off_range));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_FULL4]);
+            if (off_range) record_error(a.st, DSA_DEVERR_FP16_RANGE, lane);
+            if (more) fetch(rope, 33 + c8, 0u);
+        };
+        // Fetches the first tile of the current piece and lays out the row's Q (fp16,
+        // K-major, 128-byte swizzle): every S^T issued so far has completed, so Q is
+        // free.  Returns the softmax scale in log2 units times 2^-kq of the row's Q.
+        auto open_piece = [&]() -> float {
+            pg = page_of(t);
+            pg1 = page_of(t + 1);
+            aim(t);
+            fetch(scv, 32, 0x3f800000u);
+            fetch(raw[0], c8, 0u);
+            fetch(raw[1], 8 + c8, 0u);
+            fetch(rope, 33 + c8, 0u);
+            static_assert(64 * 72 == 9 * kWorkThreads, "nine 16-byte pieces of q per thread");
+            const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (int64_t)row * (64 * 576));
+            uint32_t mx = 0;                               // two bf16 magnitudes, compared as integers
+#pragma unroll 1
+            for (int u0 = 0; u0 < 9; u0 += 3) {
+                uint4 qv[3];
+#pragma unroll
+                for (int u = 0; u < 3; ++u) qv[u] = __ldg(qrow + tid + (u0 + u) * kWorkThreads);
+#pragma unroll
+                for (int u = 0; u < 3; ++u)
+                    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(qv[u].x & 0x7fff7fffu, qv[u].y & 0x7fff7fffu),
+                                               __vmaxu2(qv[u].z & 0x7fff7fffu, qv[u].w & 0x7fff7fffu)));
+            }
+            mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+            if (lane == 0) misc->qmax[warp] = mx;
+            work_sync();
+            mx = __reduce_max_sync(0xffffffffu, misc->qmax[lane & (kWorkWarps - 1)]);
+            const int eq = mx == 0 ? 14 : (int)(mx >> 7) - 127;
+            const int kq = min(126, max(-126, 14 - eq));
+            const float sc = __int_as_float((127 + kq) << 23);
+#pragma unroll 1
+            for (int u0 = 0; u0 < 9; u0 += 3) {
+                uint4 qv[3];
+#pragma unroll
+                for (int u = 0; u < 3; ++u) qv[u] = __ldg(qrow + tid + (u0 + u) * kWorkThreads);
+#pragma unroll
+                for (int u = 0; u < 3; ++u) {
+                    const int c = tid + (u0 + u) * kWorkThreads;
+                    const int h = c / 72, cq = c % 72;
+                    const int blk = cq >> 3, ch = cq & 7;
+                    *reinterpret_cast<uint4*>(smem + kOffQ + blk * 8192 + h * 128 + ((ch ^ (h & 7)) * 16)) =
+                        make_uint4(bf16x2_scaled_to_h2(qv[u].x, sc), bf16x2_scaled_to_h2(qv[u].y, sc),
+                                   bf16x2_scaled_to_h2(qv[u].z, sc), bf16x2_scaled_to_h2(qv[u].w, sc));
+                }
+            }
+            if (tid == 0 && mx >= 0x7f80u) record_error(a.st, DSA_DEVERR_FP16_RANGE, row);   // inf / NaN in q
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_QFULL]);
+            return a.scale_log2 * __int_as_float((127 - kq) << 23);
+        };
+
+        float lsum[kHeads];                                // this token lane's running sums of its heads
+#pragma unroll
+        for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
+        if (tid < 64) m_ref[tid] = -INFINITY;              // seen by all behind open_piece's barrier
+        float sl2 = 0.f;
+        bool fresh = true;                                 // the next softmax is its piece's first
+        int k = 0;                                         // pieces opened
+        for (;;) {
+            bool ended = false;
+            if (k > 0) {
+                // ---- softmax of tile t
+                if (ok) ok = wait_ab(&bars[B_SFULL], (uint32_t)(gt & 1), abort_flag);
                 const int u = 2 * t + (st >> 6);
-                const bool valid = u < w.pages && w.sees(w.page(u) * kPage + (st & 63)) && misc->bad[st >> 6] == 0;
+                const bool valid = u < w.pages && (w.seen(w.page(u)) >> (st & 63) & 1u) && misc->bad[st >> 6] == 0;
                 // S^T row of this token for the warp's heads, in log2 units; tokens not seen -> -inf
                 auto load_s = [&](float (&v)[kHeads]) {
                     uint32_t x[kHeads];
@@ -632,25 +594,21 @@ dense_mla_kernel(Args a) {
                 float v[kHeads];
                 tc_fence_after();
                 load_s(v);
-                // ---- a score above its head's reference by more than 2^(kTau + kShift) makes every
-                //      warp take new references first (always on the piece's first tile)
+                write_p(v);
+                // ---- a score above its head's reference by more than 2^kTau (P above 2^(kTau + kShift))
+                //      makes every warp take new references (always on the piece's first tile)
                 bool over = false;
 #pragma unroll
-                for (int c4 = 0; c4 < kHeads / 4; ++c4) {
-                    const float4 m = mr4[c4];
-                    over |= v[4 * c4] > m.x + (kTau + kShift) || v[4 * c4 + 1] > m.y + (kTau + kShift) ||
-                            v[4 * c4 + 2] > m.z + (kTau + kShift) || v[4 * c4 + 3] > m.w + (kTau + kShift);
-                }
-                write_p(v);
-                if (soft_any(over || !ok)) {
-                    if (soft_any(!ok)) {
-                        failed = true;
+                for (int c = 0; c < kHeads; ++c) over |= v[c] > kPMax;
+                if (work_any(over || !ok)) {
+                    if (work_any(!ok)) {
+                        if (tid == 0) timeout(63);
                         break;
                     }
                     load_s(v);
                     xreduce16<true>(v, lane);                   // per-head tile max (consumes v)
                     if (lane < kHeads) red[q4 * 64 + hh * kHeads + lane] = v[0];
-                    soft_sync();
+                    work_sync();
                     if (tid < 64) {
                         const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid])) - kShift;
                         const float mo = m_ref[tid];
@@ -658,22 +616,27 @@ dense_mla_kernel(Args a) {
                         alpha[tid] = need ? (mo == -INFINITY ? 0.f : exp2f(mo - tm)) : 1.f;
                         if (need) m_ref[tid] = tm;
                     }
-                    soft_sync();
-                    if (t > tb) {                               // rescale the resident O^T columns of these heads
+                    work_sync();
+                    bool mine = false;                          // does a head of this warp have a new reference
+#pragma unroll
+                    for (int c = 0; c < kHeads; ++c) mine |= alpha[hh * kHeads + c] != 1.f;
+                    if (mine) {
+                        if (!fresh) {                           // rescale the resident O^T columns of these heads
 #pragma unroll 1
-                        for (int mb = 0; mb < 4; ++mb) {
-                            uint32_t o[kHeads];
-                            const uint32_t addr = lane_addr + kColO + mb * 64 + hh * kHeads;
-                            tmem_ld_32x32b_x16(addr, o);
-                            tmem_ld_wait();
+                            for (int mb = 0; mb < 4; ++mb) {
+                                uint32_t o[kHeads];
+                                const uint32_t addr = lane_addr + kColO + mb * 64 + hh * kHeads;
+                                tmem_ld_32x32b_x16(addr, o);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int c = 0; c < kHeads; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[hh * kHeads + c]);
-                            tmem_st_32x32b_x16(addr, o);
+                                for (int c = 0; c < kHeads; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[hh * kHeads + c]);
+                                tmem_st_32x32b_x16(addr, o);
+                            }
+                            tmem_st_wait();
                         }
-                        tmem_st_wait();
-                    }
 #pragma unroll
-                    for (int c = 0; c < kHeads; ++c) lsum[c] *= alpha[hh * kHeads + c];
+                        for (int c = 0; c < kHeads; ++c) lsum[c] *= alpha[hh * kHeads + c];
+                    }
                     load_s(v);
                     write_p(v);
                 }
@@ -682,53 +645,83 @@ dense_mla_kernel(Args a) {
                 if (lane == 0) mbar_arrive(&bars[B_PREADY]);    // P^T written, S^T read, O^T rescaled
 #pragma unroll
                 for (int c = 0; c < kHeads; ++c) lsum[c] += v[c];
+                fresh = false;
+                --left;
+                ended = ++t == t_end;
             }
-            if (failed) {
-                if (tid == 0) timeout(63);
-                break;
+            // ---- the piece's sums; the next row
+            int done = row;
+            bool whole = false;
+            float sl2_next = sl2;
+            if (ended) {
+                xreduce16<false>(lsum, lane);
+                if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];
+                whole = (k > 1 || tile_begin == 0) && w.pages <= 2 * t_end;
+                __syncwarp();
             }
-            ++k;
-            // ---- per-head sums over the piece: the lanes' running sums reduced
-            xreduce16<false>(lsum, lane);
-            if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];
-            // ---- piece end: O^T is final once the last P.V completes
-            const bool ok = wait_ab(&bars[B_PV3], (uint32_t)((gt - 1) & 1), abort_flag);
-            if (soft_any(!ok)) {
-                if (tid == 0) timeout(64);
-                break;
+            if (left > 0 && (ended || k == 0)) {
+                if (ended) {
+                    ++row;
+                    t = 0;
+                }
+                t_end = enter_row(row, tid == 0 ? a.st : nullptr);
+                t_end = min(t_end, t + left);
+                sl2_next = open_piece();
+                ++k;
             }
-            tc_fence_after();
-            if (tid < 64) l_acc[tid] = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
-            soft_sync();
-            const int64_t unit = 2 * (int64_t)blockIdx.x + (k == 1 ? 0 : 1);      // a share's first piece, or its last
+            // ---- the next tile
+            if (left > 0) put_tile(t, k == 1 && fresh);
+            if (k == 1 && fresh) {
+                sl2 = sl2_next;
+                continue;
+            }
+            if (ended) {
+                // ---- the piece's output
+                if (ok) ok = wait_ab(&bars[B_PV3], (uint32_t)(gt & 1), abort_flag);   // O^T is final
+                if (work_any(!ok)) {
+                    if (tid == 0) timeout(64);
+                    break;
+                }
+                tc_fence_after();
+                if (tid < 64) l_acc[tid] = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
+                work_sync();
+                const int64_t unit = 2 * (int64_t)blockIdx.x + (done == row_begin ? 0 : 1);   // a share's first piece, or its last
 #pragma unroll 1
-            for (int mb = 0; mb < 4; ++mb) {
-                uint32_t o[kHeads];
-                tmem_ld_32x32b_x16(lane_addr + kColO + mb * 64 + hh * kHeads, o);
-                tmem_ld_wait();
-                const int d = mb * 128 + st;                           // latent dim of this TMEM lane
+                for (int mb = 0; mb < 4; ++mb) {
+                    uint32_t o[kHeads];
+                    tmem_ld_32x32b_x16(lane_addr + kColO + mb * 64 + hh * kHeads, o);
+                    tmem_ld_wait();
+                    const int d = mb * 128 + st;                           // latent dim of this TMEM lane
 #pragma unroll
-                for (int c = 0; c < kHeads; ++c) {                     // a warp stores 32 consecutive dims
-                    const int h = hh * kHeads + c;
-                    const float ov = __uint_as_float(o[c]);
-                    if (whole) {
-                        const float l = l_acc[h];
-                        const float val = l > 0.f ? ov / l : 0.f;
-                        const int64_t oi = ((int64_t)row * 64 + h) * 512 + d;
-                        if (a.out_f32) static_cast<float*>(a.out)[oi] = val;
-                        else static_cast<__nv_bfloat16*>(a.out)[oi] = __float2bfloat16_rn(val);
-                    } else {
-                        a.part_o[(unit * 64 + h) * 512 + d] = ov;
+                    for (int c = 0; c < kHeads; ++c) {                     // a warp stores 32 consecutive dims
+                        const int h = hh * kHeads + c;
+                        const float ov = __uint_as_float(o[c]);
+                        if (whole) {
+                            const float l = l_acc[h];
+                            const float val = l > 0.f ? ov / l : 0.f;
+                            const int64_t oi = ((int64_t)done * 64 + h) * 512 + d;
+                            if (a.out_f32) static_cast<float*>(a.out)[oi] = val;
+                            else static_cast<__nv_bfloat16*>(a.out)[oi] = __float2bfloat16_rn(val);
+                        } else {
+                            a.part_o[(unit * 64 + h) * 512 + d] = ov;
+                        }
                     }
                 }
+                tc_fence_before();
+                if (tid < 64) {
+                    const float l = l_acc[tid];
+                    if (!whole) a.part_ml[unit * 64 + tid] = make_float2(m_ref[tid], l);
+                    else if (a.lse) a.lse[(int64_t)done * 64 + tid] = l > 0.f ? (m_ref[tid] + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                    m_ref[tid] = -INFINITY;
+                }
+                if (left == 0) break;
+                sl2 = sl2_next;
+                fresh = true;
+#pragma unroll
+                for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
+                work_sync();                                // O^T and the references may be reused
             }
-            tc_fence_before();
-            if (tid < 64) {
-                const float l = l_acc[tid];
-                if (!whole) a.part_ml[unit * 64 + tid] = make_float2(m_ref[tid], l);
-                else if (a.lse) a.lse[(int64_t)row * 64 + tid] = l > 0.f ? (m_ref[tid] + log2f(l)) * 0.69314718055994531f : -INFINITY;
-            }
-            soft_sync();                                    // O^T and the references may be reused
+            ++gt;
         }
     }
     tc_fence_before();
