@@ -410,10 +410,15 @@ dense_mla_kernel(Args a) {
         int t_end = 0;                                     // end of the row's piece
         bool ok = true;
         uint4 raw[2][kSteps], rope[kSteps], scv[kSteps];   // rows in flight: two latent groups, RoPE dims, scales
-        uint32_t seen = 0;                                 // which of this lane's tokens of the fetched tile are seen
-        bool bad = false;                                  // its page is outside the cache
-        const uint8_t* src = nullptr;
-        int32_t pg = -1, pg1 = -1;                         // pages of the tile to fetch next and the one after
+        // a tile as this warp fetches it: its half's page, and which of the lane's tokens are seen
+        struct Aim {
+            const uint8_t* src;
+            uint32_t seen;
+            bool bad;                                      // the page is outside the cache
+        };
+        Aim now = {}, next = {};                           // the tile in flight, and the one after it
+        bool valid_now = false, valid_next = false;        // softmax: is this lane's token of those tiles seen
+        int32_t pg = -1, pg1 = -1;                         // pages of the tile to aim at next and the one after
         // page id of this warp's half of tile x, -1 beyond the piece
         auto page_of = [&](int x) -> int32_t {
             const int u = 2 * x + half;
@@ -421,27 +426,28 @@ dense_mla_kernel(Args a) {
             const int lp = w.page(u);
             return lp < b.max_pages ? __ldg(b.page_table + (int64_t)w.r * b.max_pages + lp) : -1;
         };
-        auto aim = [&](int x) {                            // fetches are for tile x from here on
-            const int u = 2 * x + half;
+        auto aim = [&](int x) {                            // sets `next` to tile x
+            const int u = 2 * x + half, us = 2 * x + (st >> 6);
             uint64_t m = u < w.pages ? w.seen(w.page(u)) : 0ull;
-            bad = pg < 0 || pg >= b.num_pages;
-            if (bad && m) {
+            next.bad = pg < 0 || pg >= b.num_pages;
+            if (next.bad && m) {
                 if (lane == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
                 m = 0;
             }
-            seen = 0;
+            next.seen = 0;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) seen |= (uint32_t)(m >> tok_of(i) & 1u) << i;
-            src = a.kv + (int64_t)(bad ? 0 : pg) * kKvPageBytes;
+            for (int i = 0; i < kSteps; ++i) next.seen |= (uint32_t)(m >> tok_of(i) & 1u) << i;
+            next.src = a.kv + (int64_t)(next.bad ? 0 : pg) * kKvPageBytes;
+            valid_next = us < w.pages && (w.seen(w.page(us)) >> (st & 63) & 1u);
             pg = pg1;
             pg1 = page_of(x + 2);
-            if ((warp & 7) == 0 && lane == 0 && pg >= 0 && pg < b.num_pages)      // the next tile's page
+            if ((warp & 7) == 0 && lane == 0 && pg >= 0 && pg < b.num_pages)      // the page of the tile after
                 prefetch_l2(a.kv + (int64_t)pg * kKvPageBytes, kKvPageBytes);
         };
         auto fetch = [&](uint4 (&dst)[kSteps], int piece, uint32_t fill) {
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
-                dst[i] = seen >> i & 1u ? ldg_pinned(reinterpret_cast<const uint4*>(src + tok_of(i) * kKvTokenBytes) + piece)
+                dst[i] = now.seen >> i & 1u ? ldg_pinned(reinterpret_cast<const uint4*>(now.src + tok_of(i) * kKvTokenBytes) + piece)
                                         : make_uint4(fill, fill, fill, fill);
         };
         // The fetched tile into shared memory, latent groups 0..3 (free once tile gt's P.V of
@@ -449,7 +455,9 @@ dense_mla_kernel(Args a) {
         // P^T, with the last group).  The registers emptied take the group two ahead.
         auto put_tile = [&](int x, bool first) {
             const uint32_t ph = (uint32_t)(gt & 1);
-            const bool more = x + 1 < t_end;
+            const bool more = x + 1 < t_end, bad = now.bad;
+            valid_now = valid_next;
+            if (more) aim(x + 1);                          // while the first P.V runs
             uint32_t off_range = 0;                        // a latent scale or a RoPE value fp16 cannot hold
 #pragma unroll
             for (int gg = 0; gg < 4; ++gg) {
@@ -478,7 +486,7 @@ dense_mla_kernel(Args a) {
                 if (gg < 2) {
                     fetch(raw[gg], (gg + 2) * 8 + c8, 0u);
                 } else if (more) {
-                    if (gg == 2) aim(x + 1);
+                    if (gg == 2) now = next;
                     fetch(raw[gg - 2], (gg - 2) * 8 + c8, 0u);
                 }
             }
@@ -503,6 +511,7 @@ dense_mla_kernel(Args a) {
             pg = page_of(t);
             pg1 = page_of(t + 1);
             aim(t);
+            now = next;
             fetch(scv, 32, 0x3f800000u);
             fetch(raw[0], c8, 0u);
             fetch(raw[1], 8 + c8, 0u);
@@ -549,9 +558,7 @@ dense_mla_kernel(Args a) {
             return a.scale_log2 * __int_as_float((127 - kq) << 23);
         };
 
-        float lsum[kHeads];                                // this token lane's running sums of its heads
-#pragma unroll
-        for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
+        float lsum = 0.f;                                  // head 16 hh + lane % 16: sum over the lane quarter's tokens
         if (tid < 64) m_ref[tid] = -INFINITY;              // seen by all behind open_piece's barrier
         float sl2 = 0.f;
         bool fresh = true;                                 // the next softmax is its piece's first
@@ -561,8 +568,7 @@ dense_mla_kernel(Args a) {
             if (k > 0) {
                 // ---- softmax of tile t
                 if (ok) ok = wait_ab(&bars[B_SFULL], (uint32_t)(gt & 1), abort_flag);
-                const int u = 2 * t + (st >> 6);
-                const bool valid = u < w.pages && (w.seen(w.page(u)) >> (st & 63) & 1u) && misc->bad[st >> 6] == 0;
+                const bool valid = valid_now && misc->bad[st >> 6] == 0;
                 // S^T row of this token for the warp's heads, in log2 units; tokens not seen -> -inf
                 auto load_s = [&](float (&v)[kHeads]) {
                     uint32_t x[kHeads];
@@ -634,8 +640,7 @@ dense_mla_kernel(Args a) {
                             }
                             tmem_st_wait();
                         }
-#pragma unroll
-                        for (int c = 0; c < kHeads; ++c) lsum[c] *= alpha[hh * kHeads + c];
+                        lsum *= alpha[hh * kHeads + (lane & (kHeads - 1))];
                     }
                     load_s(v);
                     write_p(v);
@@ -643,8 +648,8 @@ dense_mla_kernel(Args a) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_PREADY]);    // P^T written, S^T read, O^T rescaled
-#pragma unroll
-                for (int c = 0; c < kHeads; ++c) lsum[c] += v[c];
+                xreduce16<false>(v, lane);
+                lsum += v[0];
                 fresh = false;
                 --left;
                 ended = ++t == t_end;
@@ -654,8 +659,7 @@ dense_mla_kernel(Args a) {
             bool whole = false;
             float sl2_next = sl2;
             if (ended) {
-                xreduce16<false>(lsum, lane);
-                if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];
+                if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum;
                 whole = (k > 1 || tile_begin == 0) && w.pages <= 2 * t_end;
                 __syncwarp();
             }
@@ -717,8 +721,7 @@ dense_mla_kernel(Args a) {
                 if (left == 0) break;
                 sl2 = sl2_next;
                 fresh = true;
-#pragma unroll
-                for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
+                lsum = 0.f;
                 work_sync();                                // O^T and the references may be reused
             }
             ++gt;
