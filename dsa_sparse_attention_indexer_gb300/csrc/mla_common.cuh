@@ -78,6 +78,16 @@ __device__ __forceinline__ uint32_t rope_bf16x2_to_h2(uint32_t w, uint32_t& bad)
     bad |= over;
     return bf16x2_to_h2((w & ~over) | (over & ((w & 0x80008000u) | 0x477f477fu)));
 }
+// The same with cvt's saturation to the largest finite fp16 (a caller that checks
+// the magnitudes itself).
+__device__ __forceinline__ uint32_t bf16x2_to_h2_sat(uint32_t w) {
+    uint32_t h;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(__uint_as_float(w & 0xffff0000u)), "f"(__uint_as_float(w << 16)));
+    return h;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 // A query pair multiplied by the row's power of two `sc` (exact in fp32) ->
 // two fp16.  After that scaling no |value| reaches 2^15, so nothing
 // overflows; values more than 2^39 below the row's largest are rounded to

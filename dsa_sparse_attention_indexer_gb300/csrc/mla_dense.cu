@@ -144,7 +144,8 @@ constexpr int kWorkBar = 1;
 constexpr int kSteps = kTok / kWorkWarps / 4;              // a warp's 8 tokens of a tile, four at a time
 constexpr float kTau = 12.0f;                              // lazy-rescale threshold, log2 units
 constexpr float kShift = 3.0f;                             // P is scaled by 2^3 ..
-constexpr float kPMax = 0x1p15f;                           // .. so at most 2^(kTau + kShift): inside fp16
+constexpr uint32_t kPMaxH = 0x7800;                        // .. so at most 2^(kTau + kShift) = 2^15, as fp16 bits
+constexpr float kNoRef = 0x1p100f;                         // minus the reference of a head without one: P of any score is inf
 constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
 constexpr uint32_t kIdescPV = idesc_f16_f32(128, 64, true, true);
 constexpr uint32_t kColS = 0;                              // TMEM: S^T [128 x 64]
@@ -154,8 +155,8 @@ constexpr int kOffKV = 0;                                  // 8 latent K-blocks 
 constexpr int kOffP = kOffKV + 8 * kBlk;
 constexpr int kOffQ = kOffKV + 9 * kBlk;                   // 9 K-blocks of [64 heads x 128 B]
 constexpr int kOffRed = kOffQ + 9 * 8192;                  // [2][4 lane quarters][64 heads] fp32
-constexpr int kOffStat = kOffRed + 2 * 4 * 64 * 4;         // m_ref, l_acc, alpha [64]
-constexpr int kOffBars = kOffStat + 3 * 64 * 4;
+constexpr int kOffStat = kOffRed + 2 * 4 * 64 * 4;         // neg_ref, l_acc, alpha [64], 16 times -inf
+constexpr int kOffBars = kOffStat + (3 * 64 + 16) * 4;
 constexpr int kOffMisc = kOffBars + 16 * 8;
 constexpr int kOffRows = kOffMisc + 512;                   // every warp's current row, re-read instead of held in registers
 constexpr int kSmemUsed = kOffRows + (kThreads / 32) * (int)sizeof(Row);
@@ -172,7 +173,6 @@ struct Misc {
     uint32_t tmem_base;
     int32_t abort;
     uint32_t qmax[kWorkWarps];  // per warp: largest bf16 magnitude of the row's q
-    int32_t bad[2];             // the tile's page (first, second half) is outside the cache
     int32_t scratch[32];
     int64_t total;              // tiles of the whole batch
     int32_t row0, tile0;        // where this CTA's share begins
@@ -278,9 +278,10 @@ dense_mla_kernel(Args a) {
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
     Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc);
     float* red = reinterpret_cast<float*>(smem + kOffRed);
-    float* m_ref = reinterpret_cast<float*>(smem + kOffStat);
-    float* l_acc = m_ref + 64;
+    float* neg_ref = reinterpret_cast<float*>(smem + kOffStat);   // minus the heads' references, log2 units
+    float* l_acc = neg_ref + 64;
     float* alpha = l_acc + 64;
+    float* neg_inf = alpha + 64;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const BatchDev& b = a.b;
     volatile int32_t* abort_flag = &misc->abort;
@@ -390,31 +391,35 @@ dense_mla_kernel(Args a) {
     } else if (n_mine > 0) {
         // ================================================================ workers
         more_registers<kWorkRegs>();
-        // ---- rows of a tile: warps 0-7 its first page, 8-15 its second, 8 tokens each.
-        // Eight consecutive lanes hold four 16-byte pieces of two tokens whose numbers
-        // differ in bits 0 and 2, so that their swizzled 16-byte stores fall into 32
-        // different banks.
-        const int half = warp >> 3;
-        const int par = lane >> 2 & 1;
-        const int tok0 = (warp & 7) * 8 + par + (lane >> 4) * 2;
-        const int c8 = (lane & 3) | (lane >> 3 & 1) << 2;  // 16-byte piece of a 128-byte group
-        auto tok_of = [&](int i) { return tok0 + 4 * (i ^ par); };   // token of the page at step i
         // ---- softmax: warp w reads TMEM lane quarter w % 4 (token / latent row st) and
         // heads [16 hh, 16 hh + 16), hh = w / 4
         const int q4 = warp & 3, hh = warp >> 2;
         const int st = q4 * 32 + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
-        const float4* mr4 = reinterpret_cast<const float4*>(m_ref + hh * kHeads);
+        // ---- rows of a tile: the quarters of a page's tokens fetch that page, 8 tokens a
+        // warp in two steps.  Eight consecutive lanes hold four 16-byte pieces of two tokens
+        // whose numbers differ in bits 0 and 2, so that their swizzled 16-byte stores fall
+        // into 32 different banks.  The lane's token of step 1 is that of step 0 with bit 2
+        // flipped: in a tile block's address that flips bit 9 and, through the swizzle, bit 6.
+        const int half = q4 >> 1;
+        const int par = lane >> 2 & 1;
+        const int tok0 = ((warp >> 2) * 2 + (warp & 1)) * 8 + par * 5 + (lane >> 4) * 2;
+        const int c8 = (lane & 3) | (lane >> 3 & 1) << 2;  // 16-byte piece of a 128-byte group
+        constexpr uint32_t kFlip = 512 + 64;
+        const uint32_t row_at = (uint32_t)(half * kPage + tok0) * 128;
+        const uint32_t put_at = smem_addr(smem + kOffKV) + (c8 >> 2) * kBlk + row_at + (((2 * (c8 & 3)) ^ (tok0 & 7)) << 4);
+        const uint32_t rope_at = smem_addr(smem + kOffP) + row_at + ((c8 ^ (tok0 & 7)) << 4);
+        const uint32_t p_at = smem_addr(smem + kOffP) + st * 128 + (((2 * hh) ^ (st & 7)) << 4);   // P^T row st, heads 16 hh ..
 
         int row = row_begin, t = tile_begin, left = n_mine, gt = 0;
         int t_end = 0;                                     // end of the row's piece
         bool ok = true;
         uint4 raw[2][kSteps], rope[kSteps], scv[kSteps];   // rows in flight: two latent groups, RoPE dims, scales
-        // a tile as this warp fetches it: its half's page, and which of the lane's tokens are seen
+        // A tile as this warp fetches it: the lane's rows of step 0 and 1 in its half's page.
+        // A token that is not seen takes a row of the page that is (its probability is 0, and
+        // the product needs a finite latent); a page without any gives zeros (row0 = NULL).
         struct Aim {
-            const uint8_t* src;
-            uint32_t seen;
-            bool bad;                                      // the page is outside the cache
+            const uint8_t *row0, *row1;
         };
         Aim now = {}, next = {};                           // the tile in flight, and the one after it
         bool valid_now = false, valid_next = false;        // softmax: is this lane's token of those tiles seen
@@ -427,82 +432,90 @@ dense_mla_kernel(Args a) {
             return lp < b.max_pages ? __ldg(b.page_table + (int64_t)w.r * b.max_pages + lp) : -1;
         };
         auto aim = [&](int x) {                            // sets `next` to tile x
-            const int u = 2 * x + half, us = 2 * x + (st >> 6);
-            uint64_t m = u < w.pages ? w.seen(w.page(u)) : 0ull;
-            next.bad = pg < 0 || pg >= b.num_pages;
-            if (next.bad && m) {
-                if (lane == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
+            const int u = 2 * x + half;
+            uint64_t m = 0;
+            if (u < w.pages) {
+                const int lp = w.page(u);
+                m = w.first <= lp * kPage && (lp + 1) * kPage <= w.end ? ~0ull : w.seen(lp);
+            }
+            if (m && (pg < 0 || pg >= b.num_pages)) {
+                if (lane == 0 && (warp & ~2) == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
                 m = 0;
             }
-            next.seen = 0;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) next.seen |= (uint32_t)(m >> tok_of(i) & 1u) << i;
-            next.src = a.kv + (int64_t)(next.bad ? 0 : pg) * kKvPageBytes;
-            valid_next = us < w.pages && (w.seen(w.page(us)) >> (st & 63) & 1u);
+            valid_next = m >> (st & 63) & 1u;
+            next.row0 = next.row1 = nullptr;
+            if (m) {
+                const int some = __ffsll((long long)m) - 1;
+                const uint8_t* page = a.kv + (int64_t)pg * kKvPageBytes + c8 * 16;
+                next.row0 = page + ((m >> tok0 & 1u) ? tok0 : some) * kKvTokenBytes;
+                next.row1 = page + ((m >> (tok0 ^ 4) & 1u) ? tok0 ^ 4 : some) * kKvTokenBytes;
+            }
             pg = pg1;
             pg1 = page_of(x + 2);
-            if ((warp & 7) == 0 && lane == 0 && pg >= 0 && pg < b.num_pages)      // the page of the tile after
+            if ((warp & ~2) == 0 && lane == 0 && pg >= 0 && pg < b.num_pages)     // the page of the tile after
                 prefetch_l2(a.kv + (int64_t)pg * kKvPageBytes, kKvPageBytes);
         };
-        auto fetch = [&](uint4 (&dst)[kSteps], int piece, uint32_t fill) {
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i)
-                dst[i] = now.seen >> i & 1u ? ldg_pinned(reinterpret_cast<const uint4*>(now.src + tok_of(i) * kKvTokenBytes) + piece)
-                                        : make_uint4(fill, fill, fill, fill);
+        auto fetch = [&](uint4 (&dst)[kSteps], int at) {   // the 16 bytes at `at` + 16 c8 of the lane's rows
+            if (now.row0 != nullptr) {
+                dst[0] = ldg_pinned(reinterpret_cast<const uint4*>(now.row0 + at));
+                dst[1] = ldg_pinned(reinterpret_cast<const uint4*>(now.row1 + at));
+            } else {
+                dst[0] = dst[1] = make_uint4(0, 0, 0, 0);
+            }
         };
+        auto fetch_scales = [&]() { fetch(scv, 512 - c8 * 16); };
+        static_assert(kSteps == 2, "two rows a lane");
         // The fetched tile into shared memory, latent groups 0..3 (free once tile gt's P.V of
         // the group is done; `first`: nothing to wait for), then the RoPE block (free, as
         // P^T, with the last group).  The registers emptied take the group two ahead.
         auto put_tile = [&](int x, bool first) {
             const uint32_t ph = (uint32_t)(gt & 1);
-            const bool more = x + 1 < t_end, bad = now.bad;
+            const bool more = x + 1 < t_end, zeros = now.row0 == nullptr;
             valid_now = valid_next;
             if (more) aim(x + 1);                          // while the first P.V runs
             uint32_t off_range = 0;                        // a latent scale or a RoPE value fp16 cannot hold
 #pragma unroll
             for (int gg = 0; gg < 4; ++gg) {
                 if (!first && ok) ok = wait_ab(&bars[B_PV0 + gg], ph, abort_flag);
-                if (gg == 0 && (warp & 7) == 0 && lane == 0) misc->bad[half] = bad ? 1 : 0;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
-                    const int tk = half * kPage + tok_of(i);
-                    const float sc = __uint_as_float(gg == 0 ? scv[i].x : gg == 1 ? scv[i].y : gg == 2 ? scv[i].z : scv[i].w);
-                    off_range |= sc >= 0x1p-15f && sc <= 0x1p7f ? 0u : 1u;
-                    const __half2 sc2 = __float2half2_rn(sc);   // a power of two: exact
+                    const uint32_t scb = gg == 0 ? scv[i].x : gg == 1 ? scv[i].y : gg == 2 ? scv[i].z : scv[i].w;
+                    off_range |= scb - 0x38000000u > 0x43000000u - 0x38000000u ? 1u : 0u;   // outside [2^-15, 2^7]
+                    const __half2 sc2 = __float2half2_rn(__uint_as_float(scb));              // a power of two: exact
                     const uint4 v = raw[gg & 1][i];
                     // 16 FP8 dims 128 gg + 16 c8 .. -> K-block 2 gg + c8 / 4, 16-byte chunks 2 (c8 % 4), +1
-                    uint8_t* blkp = smem + kOffKV + (2 * gg + (c8 >> 2)) * kBlk + tk * 128;
-                    const int ch = 2 * (c8 & 3), sw = tk & 7;
-                    *reinterpret_cast<uint4*>(blkp + ((ch ^ sw) * 16)) =
-                        make_uint4(e4m3x2_scaled_h2(v.x & 0xffffu, sc2), e4m3x2_scaled_h2(v.x >> 16, sc2),
-                                   e4m3x2_scaled_h2(v.y & 0xffffu, sc2), e4m3x2_scaled_h2(v.y >> 16, sc2));
-                    *reinterpret_cast<uint4*>(blkp + (((ch + 1) ^ sw) * 16)) =
-                        make_uint4(e4m3x2_scaled_h2(v.z & 0xffffu, sc2), e4m3x2_scaled_h2(v.z >> 16, sc2),
-                                   e4m3x2_scaled_h2(v.w & 0xffffu, sc2), e4m3x2_scaled_h2(v.w >> 16, sc2));
+                    const uint32_t at = (put_at ^ (i ? kFlip : 0u)) + 2 * gg * kBlk;
+                    st_shared_v4(at, e4m3x2_scaled_h2(v.x & 0xffffu, sc2), e4m3x2_scaled_h2(v.x >> 16, sc2),
+                                 e4m3x2_scaled_h2(v.y & 0xffffu, sc2), e4m3x2_scaled_h2(v.y >> 16, sc2));
+                    st_shared_v4(at ^ 16, e4m3x2_scaled_h2(v.z & 0xffffu, sc2), e4m3x2_scaled_h2(v.z >> 16, sc2),
+                                 e4m3x2_scaled_h2(v.w & 0xffffu, sc2), e4m3x2_scaled_h2(v.w >> 16, sc2));
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_FULL0 + gg]);
                 if (gg < 2) {
-                    fetch(raw[gg], (gg + 2) * 8 + c8, 0u);
+                    fetch(raw[gg], (gg + 2) * 128);
                 } else if (more) {
                     if (gg == 2) now = next;
-                    fetch(raw[gg - 2], (gg - 2) * 8 + c8, 0u);
+                    fetch(raw[gg - 2], (gg - 2) * 128);
                 }
             }
-            if (more) fetch(scv, 32, 0x3f800000u);
+            if (more) fetch_scales();
+            uint32_t rope_max = 0;                         // two bf16 magnitudes, compared as integers
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int tk = half * kPage + tok_of(i);
-                *reinterpret_cast<uint4*>(smem + kOffP + tk * 128 + ((c8 ^ (tk & 7)) * 16)) =
-                    make_uint4(rope_bf16x2_to_h2(rope[i].x, off_range), rope_bf16x2_to_h2(rope[i].y, off_range),
-                               rope_bf16x2_to_h2(rope[i].z, off_range), rope_bf16x2_to_h2(rope[i].w, off_range));
+                const uint4 v = rope[i];
+                rope_max = __vmaxu2(rope_max, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                st_shared_v4(rope_at ^ (i ? kFlip : 0u), bf16x2_to_h2_sat(v.x), bf16x2_to_h2_sat(v.y), bf16x2_to_h2_sat(v.z),
+                             bf16x2_to_h2_sat(v.w));
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_FULL4]);
-            if (off_range) record_error(a.st, DSA_DEVERR_FP16_RANGE, lane);
-            if (more) fetch(rope, 33 + c8, 0u);
+            off_range |= (rope_max & 0xffffu) >= 0x4780u || rope_max >= 0x47800000u ? 1u : 0u;   // |r| >= 2^16
+            if (off_range && !zeros) record_error(a.st, DSA_DEVERR_FP16_RANGE, lane);
+            if (more) fetch(rope, 528);
         };
         // Fetches the first tile of the current piece and lays out the row's Q (fp16,
         // K-major, 128-byte swizzle): every S^T issued so far has completed, so Q is
@@ -512,10 +525,10 @@ dense_mla_kernel(Args a) {
             pg1 = page_of(t + 1);
             aim(t);
             now = next;
-            fetch(scv, 32, 0x3f800000u);
-            fetch(raw[0], c8, 0u);
-            fetch(raw[1], 8 + c8, 0u);
-            fetch(rope, 33 + c8, 0u);
+            fetch_scales();
+            fetch(raw[0], 0);
+            fetch(raw[1], 128);
+            fetch(rope, 528);
             static_assert(64 * 72 == 9 * kWorkThreads, "nine 16-byte pieces of q per thread");
             const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (int64_t)row * (64 * 576));
             uint32_t mx = 0;                               // two bf16 magnitudes, compared as integers
@@ -558,8 +571,11 @@ dense_mla_kernel(Args a) {
             return a.scale_log2 * __int_as_float((127 - kq) << 23);
         };
 
-        float lsum = 0.f;                                  // head 16 hh + lane % 16: sum over the lane quarter's tokens
-        if (tid < 64) m_ref[tid] = -INFINITY;              // seen by all behind open_piece's barrier
+        float lsum[kHeads];                                // this token lane's running sums of its heads
+#pragma unroll
+        for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
+        if (tid < 16) neg_inf[tid] = -INFINITY;
+        if (tid < 64) neg_ref[tid] = kNoRef;               // seen by all behind open_piece's barrier
         float sl2 = 0.f;
         bool fresh = true;                                 // the next softmax is its piece's first
         int k = 0;                                         // pieces opened
@@ -568,33 +584,34 @@ dense_mla_kernel(Args a) {
             if (k > 0) {
                 // ---- softmax of tile t
                 if (ok) ok = wait_ab(&bars[B_SFULL], (uint32_t)(gt & 1), abort_flag);
-                const bool valid = valid_now && misc->bad[st >> 6] == 0;
-                // S^T row of this token for the warp's heads, in log2 units; tokens not seen -> -inf
+                // a token that is not seen takes -inf for its references: every P is 0
+                const float4* nr4 = reinterpret_cast<const float4*>(valid_now ? neg_ref + hh * kHeads : neg_inf);
+                uint32_t most;                              // largest P of the thread, as two fp16
+                // S^T row of this token for the warp's heads
                 auto load_s = [&](float (&v)[kHeads]) {
                     uint32_t x[kHeads];
                     tmem_ld_32x32b_x16(lane_addr + kColS + hh * kHeads, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < kHeads; ++h) v[h] = valid ? __uint_as_float(x[h]) * sl2 : -INFINITY;
+                    for (int h = 0; h < kHeads; ++h) v[h] = __uint_as_float(x[h]);
                 };
                 // P of the current references, and its P^T row (heads 16 hh.. as fp16, MN-major swizzle)
                 auto write_p = [&](float (&v)[kHeads]) {
 #pragma unroll
                     for (int c4 = 0; c4 < kHeads / 4; ++c4) {
-                        const float4 m = mr4[c4];
-                        v[4 * c4] = valid ? ex2_approx(v[4 * c4] - m.x) : 0.f;
-                        v[4 * c4 + 1] = valid ? ex2_approx(v[4 * c4 + 1] - m.y) : 0.f;
-                        v[4 * c4 + 2] = valid ? ex2_approx(v[4 * c4 + 2] - m.z) : 0.f;
-                        v[4 * c4 + 3] = valid ? ex2_approx(v[4 * c4 + 3] - m.w) : 0.f;
+                        const float4 m = nr4[c4];
+                        v[4 * c4] = ex2_approx(fmaf(v[4 * c4], sl2, m.x));
+                        v[4 * c4 + 1] = ex2_approx(fmaf(v[4 * c4 + 1], sl2, m.y));
+                        v[4 * c4 + 2] = ex2_approx(fmaf(v[4 * c4 + 2], sl2, m.z));
+                        v[4 * c4 + 3] = ex2_approx(fmaf(v[4 * c4 + 3], sl2, m.w));
                     }
-                    uint8_t* prow = smem + kOffP + st * 128;
+                    uint32_t h[kHeads / 2];
 #pragma unroll
-                    for (int cc = 0; cc < kHeads / 8; ++cc) {
-                        const int c = hh * (kHeads / 8) + cc;
-                        *reinterpret_cast<uint4*>(prow + ((c ^ (st & 7)) * 16)) =
-                            make_uint4(pack_h2(v[8 * cc], v[8 * cc + 1]), pack_h2(v[8 * cc + 2], v[8 * cc + 3]),
-                                       pack_h2(v[8 * cc + 4], v[8 * cc + 5]), pack_h2(v[8 * cc + 6], v[8 * cc + 7]));
-                    }
+                    for (int c = 0; c < kHeads / 2; ++c) h[c] = pack_h2(v[2 * c], v[2 * c + 1]);
+                    st_shared_v4(p_at, h[0], h[1], h[2], h[3]);
+                    st_shared_v4(p_at ^ 16, h[4], h[5], h[6], h[7]);
+                    most = __vmaxu2(__vmaxu2(__vmaxu2(h[0], h[1]), __vmaxu2(h[2], h[3])),
+                                    __vmaxu2(__vmaxu2(h[4], h[5]), __vmaxu2(h[6], h[7])));
                     fence_proxy_async_smem();
                 };
                 float v[kHeads];
@@ -603,24 +620,24 @@ dense_mla_kernel(Args a) {
                 write_p(v);
                 // ---- a score above its head's reference by more than 2^kTau (P above 2^(kTau + kShift))
                 //      makes every warp take new references (always on the piece's first tile)
-                bool over = false;
-#pragma unroll
-                for (int c = 0; c < kHeads; ++c) over |= v[c] > kPMax;
+                const bool over = (most & 0xffffu) > kPMaxH || most >> 16 > kPMaxH;
                 if (work_any(over || !ok)) {
                     if (work_any(!ok)) {
                         if (tid == 0) timeout(63);
                         break;
                     }
                     load_s(v);
+#pragma unroll
+                    for (int c = 0; c < kHeads; ++c) v[c] = valid_now ? v[c] * sl2 : -INFINITY;
                     xreduce16<true>(v, lane);                   // per-head tile max (consumes v)
                     if (lane < kHeads) red[q4 * 64 + hh * kHeads + lane] = v[0];
                     work_sync();
                     if (tid < 64) {
                         const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid])) - kShift;
-                        const float mo = m_ref[tid];
+                        const float mo = -neg_ref[tid];
                         const bool need = tm > mo + kTau;
-                        alpha[tid] = need ? (mo == -INFINITY ? 0.f : exp2f(mo - tm)) : 1.f;
-                        if (need) m_ref[tid] = tm;
+                        alpha[tid] = need ? exp2f(mo - tm) : 1.f;          // 0 for a first reference
+                        if (need) neg_ref[tid] = -tm;
                     }
                     work_sync();
                     bool mine = false;                          // does a head of this warp have a new reference
@@ -640,7 +657,8 @@ dense_mla_kernel(Args a) {
                             }
                             tmem_st_wait();
                         }
-                        lsum *= alpha[hh * kHeads + (lane & (kHeads - 1))];
+#pragma unroll
+                        for (int c = 0; c < kHeads; ++c) lsum[c] *= alpha[hh * kHeads + c];
                     }
                     load_s(v);
                     write_p(v);
@@ -648,8 +666,8 @@ dense_mla_kernel(Args a) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_PREADY]);    // P^T written, S^T read, O^T rescaled
-                xreduce16<false>(v, lane);
-                lsum += v[0];
+#pragma unroll
+                for (int c = 0; c < kHeads; ++c) lsum[c] += v[c];
                 fresh = false;
                 --left;
                 ended = ++t == t_end;
@@ -659,7 +677,8 @@ dense_mla_kernel(Args a) {
             bool whole = false;
             float sl2_next = sl2;
             if (ended) {
-                if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum;
+                xreduce16<false>(lsum, lane);
+                if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];
                 whole = (k > 1 || tile_begin == 0) && w.pages <= 2 * t_end;
                 __syncwarp();
             }
@@ -714,14 +733,15 @@ dense_mla_kernel(Args a) {
                 tc_fence_before();
                 if (tid < 64) {
                     const float l = l_acc[tid];
-                    if (!whole) a.part_ml[unit * 64 + tid] = make_float2(m_ref[tid], l);
-                    else if (a.lse) a.lse[(int64_t)done * 64 + tid] = l > 0.f ? (m_ref[tid] + log2f(l)) * 0.69314718055994531f : -INFINITY;
-                    m_ref[tid] = -INFINITY;
+                    if (!whole) a.part_ml[unit * 64 + tid] = make_float2(-neg_ref[tid], l);
+                    else if (a.lse) a.lse[(int64_t)done * 64 + tid] = l > 0.f ? (log2f(l) - neg_ref[tid]) * 0.69314718055994531f : -INFINITY;
+                    neg_ref[tid] = kNoRef;
                 }
                 if (left == 0) break;
                 sl2 = sl2_next;
                 fresh = true;
-                lsum = 0.f;
+#pragma unroll
+                for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
                 work_sync();                                // O^T and the references may be reused
             }
             ++gt;
