@@ -85,8 +85,15 @@ __device__ __forceinline__ uint32_t bf16x2_to_h2_sat(uint32_t w) {
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(__uint_as_float(w & 0xffff0000u)), "f"(__uint_as_float(w << 16)));
     return h;
 }
+template <int OFF = 0>
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+    asm volatile("st.shared.v4.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d), "n"(OFF) : "memory");
+}
+// Four E4M3 codes times a power of two (as two equal fp16), exact: (lo, hi) pairs of fp16.
+__device__ __forceinline__ void e4m3x4_scaled_h2(uint32_t four, uint32_t sc2, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 a, b;\n .reg .b32 x, y;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 x, a;\n cvt.rn.f16x2.e4m3x2 y, b;\n"
+        " mul.rn.f16x2 %0, x, %3;\n mul.rn.f16x2 %1, y, %3;\n}"
+        : "=r"(lo), "=r"(hi) : "r"(four), "r"(sc2));
 }
 // A query pair multiplied by the row's power of two `sc` (exact in fp32) ->
 // two fp16.  After that scaling no |value| reaches 2^15, so nothing

@@ -22,22 +22,24 @@
 // the next tile starts behind the last P.V.  P^T takes the place of the tile's
 // RoPE block, which S^T has read by then.
 //
-// Warps 0-15 do everything but issue the MMAs; a tile's phases follow one another,
-// so the same warps take them in turn:
+// Warps 0-15 (workers) do what a tile's phases ask for one after the other:
 //   softmax     a thread owns one token (TMEM lane) and 16 heads.  P is formed
 //               against a reference that lags the maximum by up to 2^12 before
 //               O^T is rescaled, and shifted up by 2^3, so that fp16 holds
 //               probabilities down to 2^-28 of the reference;
-//   next tile   its rows, read into registers a tile ahead (whole pages are
-//               prefetched into L2 before that), are dequantised into the
+//   next tile   its rows, read into registers two groups ahead, are dequantised into the
 //               128-byte-swizzled tile (exact for scales in [2^-15, 2^7]), each
-//               part as soon as it is free.  Rows that are not seen become zeros;
+//               part as soon as it is free.  Rows that are not seen become zeros or
+//               another row, with probability 0;
 //   next row    its Q, scaled by the power of two that puts its largest |q| in
 //               [2^14, 2^15), while the last P.V runs; then the epilogue, while
 //               the first S^T of the next row runs.
-// Warp 16 issues the MMAs.
+// Warp 16 issues the MMAs.  Warp 17 lays out the tiles of the CTA's share up to four
+// ahead: pages, masks of what is seen, where a row's piece begins and ends; it also
+// prefetches the pages into L2.
 // Every wait is time-bounded; a timeout is recorded and the CTA winds down.
 #include <algorithm>
+#include <type_traits>
 
 #include "dsa_internal.cuh"
 #include "indexer_common.cuh"
@@ -83,9 +85,9 @@ struct Row {
     int32_t prefix;
     uint64_t mask;
     int32_t sink_pages, first_page, pages;
-    __device__ __forceinline__ int page(int u) const volatile { return u < sink_pages ? u : first_page + u - sink_pages; }
+    __device__ __forceinline__ int page(int u) const { return u < sink_pages ? u : first_page + u - sink_pages; }
     // The positions of logical page lp that the row sees, one bit each.
-    __device__ __forceinline__ uint64_t seen(int lp) const volatile {
+    __device__ __forceinline__ uint64_t seen(int lp) const {
         const int j = lp * kPage;
         const uint64_t sinks = below(sink_end - j), from = below(end - j) & ~below(first - j);
         const int sh = prefix - j;
@@ -139,9 +141,10 @@ constexpr int kWorkWarps = 16;
 constexpr int kWorkThreads = kWorkWarps * 32;
 constexpr int kHeads = 16;                                 // heads of a warp in the softmax: four warps a TMEM lane quarter
 constexpr int kMmaWarp = kWorkWarps;
-constexpr int kThreads = (kMmaWarp + 4) * 32;              // five warpgroups; the last one's first warp issues the MMAs
-constexpr int kWorkBar = 1;
-constexpr int kSteps = kTok / kWorkWarps / 4;              // a warp's 8 tokens of a tile, four at a time
+constexpr int kAimWarp = kMmaWarp + 1;
+constexpr int kThreads = (kWorkWarps + 4) * 32;            // five warpgroups; the last one issues the MMAs and lays out the tiles
+constexpr int kWorkBar = 1, kVoteBar = 2;                  // workers; workers and the MMA warp
+constexpr int kAhead = 4;                                  // tiles laid out ahead
 constexpr float kTau = 12.0f;                              // lazy-rescale threshold, log2 units
 constexpr float kShift = 3.0f;                             // P is scaled by 2^3 ..
 constexpr uint32_t kPMaxH = 0x7800;                        // .. so at most 2^(kTau + kShift) = 2^15, as fp16 bits
@@ -155,25 +158,34 @@ constexpr int kOffKV = 0;                                  // 8 latent K-blocks 
 constexpr int kOffP = kOffKV + 8 * kBlk;
 constexpr int kOffQ = kOffKV + 9 * kBlk;                   // 9 K-blocks of [64 heads x 128 B]
 constexpr int kOffRed = kOffQ + 9 * 8192;                  // [2][4 lane quarters][64 heads] fp32
-constexpr int kOffStat = kOffRed + 2 * 4 * 64 * 4;         // neg_ref, l_acc, alpha [64], 16 times -inf
-constexpr int kOffBars = kOffStat + (3 * 64 + 16) * 4;
-constexpr int kOffMisc = kOffBars + 16 * 8;
-constexpr int kOffRows = kOffMisc + 512;                   // every warp's current row, re-read instead of held in registers
-constexpr int kSmemUsed = kOffRows + (kThreads / 32) * (int)sizeof(Row);
-static_assert(sizeof(Row) % 8 == 0, "rows are 8-byte aligned");
+constexpr int kOffStat = kOffRed + 2 * 4 * 64 * 4;         // neg_ref, l_acc, alpha [64], 32 times -inf
+constexpr int kOffBars = kOffStat + (3 * 64 + 32) * 4;
+constexpr int kOffMisc = kOffBars + 24 * 8;
+constexpr int kSmemUsed = kOffMisc + 512;
 constexpr int kSmemAlloc = kSmemUsed + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kBlk % 1024 == 0, "swizzle atoms need 1 KB alignment");
 static_assert(kOffStat % 16 == 0, "reference maxima are read as float4");
 
-enum { B_QFULL = 0, B_FULL0, B_FULL4 = B_FULL0 + 4, B_SFULL, B_PREADY, B_PV0, B_PV3 = B_PV0 + 3, B_DRAIN, B_COUNT };
-static_assert(B_COUNT <= 16, "barrier block");
+enum { B_QFULL = 0, B_FULL0, B_FULL4 = B_FULL0 + 4, B_SFULL, B_PV0, B_PV3 = B_PV0 + 3, B_DRAIN, B_AIM0,
+       B_FREE0 = B_AIM0 + kAhead, B_COUNT = B_FREE0 + kAhead };
+static_assert(B_COUNT <= 24, "barrier block");
+
+// A tile of the share, as the aim warp lays it out: its two pages, which of their
+// positions the row sees, and where it stands in the row's piece.
+struct Tile {
+    uint64_t seen[2];
+    int32_t page[2];            // -1: no position of the page is seen, or it is outside the cache
+    uint32_t row;               // row x 8 + FIRST, LAST tile of the piece; WHOLE: the piece is the whole row
+};
+enum { T_FIRST = 1, T_LAST = 2, T_WHOLE = 4 };
 
 struct Misc {
     uint32_t tmem_base;
     int32_t abort;
+    Tile tile[kAhead];          // by tile of the share, modulo kAhead
     uint32_t qmax[kWorkWarps];  // per warp: largest bf16 magnitude of the row's q
-    int32_t scratch[32];
+    int64_t scratch[kWorkWarps];
     int64_t total;              // tiles of the whole batch
     int32_t row0, tile0;        // where this CTA's share begins
 };
@@ -186,14 +198,15 @@ struct Meta {
     int32_t inside;
 };
 
-__device__ __forceinline__ bool work_any(bool pred) { return bar_any<kWorkBar, kWorkThreads>(pred); }
+// Has any worker, or the MMA warp, `pred` set?  (All of them call it.)
+__device__ __forceinline__ bool vote(bool pred) { return bar_any<kVoteBar, kWorkThreads + 32>(pred); }
 __device__ __forceinline__ void work_sync() { bar_sync<kWorkBar, kWorkThreads>(); }
 
 __device__ __forceinline__ int tiles_of(const Row& w) { return (w.pages + 1) >> 1; }
 
 // Counts the tiles of all rows (the workers' threads, consecutive rows each)
 // and finds where share g of G begins.  Returns the share's tiles.
-__device__ __forceinline__ void plan_share(const Args& a, Misc* misc, int tid) {
+__device__ __noinline__ void plan_share(const Args& a, Misc* misc, int tid) {
     const int64_t T = a.b.total_q;
     const int64_t per = (T + kWorkThreads - 1) / kWorkThreads;
     const int64_t r0 = min(T, tid * per), r1 = min(T, r0 + per);
@@ -206,7 +219,7 @@ __device__ __forceinline__ void plan_share(const Args& a, Misc* misc, int tid) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if ((tid & 31) >= o) x += y;
     }
-    int64_t* tot = reinterpret_cast<int64_t*>(misc->scratch);     // 16 warps
+    int64_t* tot = misc->scratch;                                 // one per warp
     if ((tid & 31) == 31) tot[tid >> 5] = x;
     work_sync();
     int64_t before = 0, all = 0;
@@ -234,7 +247,7 @@ __device__ __forceinline__ void plan_share(const Args& a, Misc* misc, int tid) {
 }
 
 // Registers per thread: 96 at launch (65,536 / 640 threads, in eights), of which
-// the MMA warpgroup gives most to the others: 512 x 112 + 128 x 32 = 640 x 96.
+// the last warpgroup gives some to the workers: 512 x 112 + 128 x 32 = 640 x 96.
 constexpr int kLaunchRegs = 96, kWorkRegs = 112, kMmaRegs = 32;
 static_assert(kWorkThreads * kWorkRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "more registers than the launch holds");
 template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
@@ -272,7 +285,7 @@ __device__ __forceinline__ void pv_block(uint32_t o_tmem, uint64_t d_v, uint64_t
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-dense_mla_kernel(Args a) {
+dense_mla_kernel(const __grid_constant__ Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
@@ -285,31 +298,16 @@ dense_mla_kernel(Args a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const BatchDev& b = a.b;
     volatile int32_t* abort_flag = &misc->abort;
-    volatile Row& w = reinterpret_cast<Row*>(smem + kOffRows)[warp];
-    auto enter_row = [&](int row, int32_t* st) -> int {     // this warp's row; returns its tiles
-        const Row r = row_view(a.b, a.view, row, st);
-        __syncwarp();
-        if ((tid & 31) == 0) {
-            w.r = r.r;
-            w.sink_end = r.sink_end;
-            w.first = r.first;
-            w.end = r.end;
-            w.prefix = r.prefix;
-            w.mask = r.mask;
-            w.sink_pages = r.sink_pages;
-            w.first_page = r.first_page;
-            w.pages = r.pages;
-        }
-        __syncwarp();
-        return tiles_of(r);
-    };
 
     if (tid == 0) {
         mbar_init(&bars[B_QFULL], kWorkWarps);
         for (int i = 0; i < 5; ++i) mbar_init(&bars[B_FULL0 + i], kWorkWarps);
         mbar_init(&bars[B_SFULL], 1);
-        mbar_init(&bars[B_PREADY], kWorkWarps);
         for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PV0 + i], 1);
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(&bars[B_AIM0 + i], 1);
+            mbar_init(&bars[B_FREE0 + i], kWorkWarps + 1);
+        }
         mbar_init(&bars[B_DRAIN], 1);
         misc->abort = 0;
         fence_barrier_init();
@@ -337,55 +335,102 @@ dense_mla_kernel(Args a) {
     };
 
     if (warp >= kMmaWarp) {
-        // ================================================================ MMA issue (one thread)
         fewer_registers<kMmaRegs>();
-        if (warp == kMmaWarp && lane == 0) {
+        if (warp == kMmaWarp && n_mine > 0) {
+            // ============================================================ MMA issue (lane 0; the warp joins the votes)
             const uint32_t kv0 = smem_addr(smem + kOffKV), q0 = smem_addr(smem + kOffQ), p0 = smem_addr(smem + kOffP);
             const uint64_t d_kv = desc_kmajor_sw128(kv0), d_q = desc_kmajor_sw128(q0);
             const uint64_t d_v = desc_mnmajor_sw128(kv0, kBlk), d_p = desc_mnmajor_sw128(p0, 8192);
-            bool ok = true;
-            int gt = 0, left = n_mine;
-            int t0 = tile_begin;
-            int k = 0;
-            for (int row = row_begin; left > 0 && ok; ++row) {
-                const int n_row = tiles_of(row_view(b, a.view, row, nullptr)) - t0;
-                const int n = min(n_row, left);
-                left -= n;
-                t0 = 0;
-                if (n == 0) continue;
-                if (!(ok = wait_ab(&bars[B_QFULL], (uint32_t)(k & 1), abort_flag))) break;
-                ++k;
-                for (int t = 0; t < n && ok; ++t, ++gt) {
-                    const uint32_t ph = (uint32_t)(gt & 1);
-                    if (!(ok = wait_ab(&bars[B_FULL0], ph, abort_flag))) break;
-                    tc_fence_after();
-                    qk_blocks<0, 2>(tmem + kColS, d_kv, d_q);
-                    if (!(ok = wait_ab(&bars[B_FULL0 + 1], ph, abort_flag))) break;
-                    tc_fence_after();
-                    qk_blocks<2, 2>(tmem + kColS, d_kv, d_q);
-                    if (!(ok = wait_ab(&bars[B_FULL0 + 2], ph, abort_flag))) break;
-                    tc_fence_after();
-                    qk_blocks<4, 2>(tmem + kColS, d_kv, d_q);
-                    if (!(ok = wait_ab(&bars[B_FULL0 + 3], ph, abort_flag))) break;
-                    tc_fence_after();
-                    qk_blocks<6, 2>(tmem + kColS, d_kv, d_q);
-                    if (!(ok = wait_ab(&bars[B_FULL4], ph, abort_flag))) break;
-                    tc_fence_after();
-                    qk_blocks<8, 1>(tmem + kColS, d_kv, d_q);
-                    mma_commit(&bars[B_SFULL]);
-                    if (!(ok = wait_ab(&bars[B_PREADY], ph, abort_flag))) break;
-                    tc_fence_after();
-                    pv_block<0>(tmem + kColO, d_v, d_p, t > 0, &bars[B_PV0]);
-                    pv_block<1>(tmem + kColO, d_v, d_p, t > 0, &bars[B_PV0 + 1]);
-                    pv_block<2>(tmem + kColO, d_v, d_p, t > 0, &bars[B_PV0 + 2]);
-                    pv_block<3>(tmem + kColO, d_v, d_p, t > 0, &bars[B_PV0 + 3]);
+            bool ok = true;                                // of lane 0
+            int k = 0;                                     // rows' Qs so far
+            for (int n = 0; n < n_mine; ++n) {
+                const uint32_t ph = (uint32_t)(n & 1);
+                bool first = false;
+                if (lane == 0) {
+                    ok = wait_ab(&bars[B_AIM0 + n % kAhead], (uint32_t)(n / kAhead & 1), abort_flag);
+                    first = reinterpret_cast<volatile Tile*>(misc->tile)[n % kAhead].row & T_FIRST;
+                    mbar_arrive(&bars[B_FREE0 + n % kAhead]);
+                    if (ok && first) ok = wait_ab(&bars[B_QFULL], (uint32_t)(k++ & 1), abort_flag);
+                    auto next = [&](int bar) {
+                        if (ok) ok = wait_ab(&bars[bar], ph, abort_flag);
+                        tc_fence_after();
+                        return ok;
+                    };
+                    if (next(B_FULL0)) qk_blocks<0, 2>(tmem + kColS, d_kv, d_q);
+                    if (next(B_FULL0 + 1)) qk_blocks<2, 2>(tmem + kColS, d_kv, d_q);
+                    if (next(B_FULL0 + 2)) qk_blocks<4, 2>(tmem + kColS, d_kv, d_q);
+                    if (next(B_FULL0 + 3)) qk_blocks<6, 2>(tmem + kColS, d_kv, d_q);
+                    if (next(B_FULL4)) {
+                        qk_blocks<8, 1>(tmem + kColS, d_kv, d_q);
+                        mma_commit(&bars[B_SFULL]);
+                    }
                 }
+                __syncwarp();
+                if (vote(!ok)) {                           // P^T is written; or new references, or a timeout
+                    if (vote(!ok)) break;
+                    vote(false);                           // P^T is written again, O^T rescaled
+                }
+                if (lane == 0) {
+                    tc_fence_after();
+                    pv_block<0>(tmem + kColO, d_v, d_p, !first, &bars[B_PV0]);
+                    pv_block<1>(tmem + kColO, d_v, d_p, !first, &bars[B_PV0 + 1]);
+                    pv_block<2>(tmem + kColO, d_v, d_p, !first, &bars[B_PV0 + 2]);
+                    pv_block<3>(tmem + kColO, d_v, d_p, !first, &bars[B_PV0 + 3]);
+                }
+                __syncwarp();
             }
-            if (!ok) timeout(61);
-            if (n_mine > 0) {                              // no MMA may be in flight when the TMEM is released
-                mma_commit(&bars[B_DRAIN]);
+            if (lane == 0) {
+                if (!ok) timeout(61);
+                mma_commit(&bars[B_DRAIN]);                // no MMA may be in flight when the TMEM is released
                 mbar_wait(&bars[B_DRAIN], 0, 500000000ull);
             }
+        } else if (warp == kAimWarp && n_mine > 0) {
+            // ============================================================ tiles of the share, one after the other
+            bool ok = true;
+            int row = row_begin, t = tile_begin;
+            Row w = row_view(b, a.view, row, lane == 0 ? a.st : nullptr);
+            bool first = true, cut = t > 0;                // the piece's first tile; the row began in an earlier share
+            for (int n = 0; n < n_mine; ++n) {
+                // until the workers and the MMA warp have read the slot's last tile (a phase that
+                // counts as over the first time round)
+                ok = __all_sync(0xffffffffu, wait_ab(&bars[B_FREE0 + n % kAhead], (uint32_t)(n / kAhead + 1 & 1), abort_flag));
+                if (!ok) break;
+                Tile* tile = &misc->tile[n % kAhead];
+                const int u = 2 * t + lane;
+                const bool end_of_row = t + 1 == tiles_of(w);
+                if (lane < 2) {                            // page u of the row
+                    const int lp = w.page(u);
+                    uint64_t m = u < w.pages ? w.seen(lp) : 0ull;
+                    int32_t page = -1;
+                    if (m) {
+                        const int64_t pg = lp < b.max_pages ? b.page_table[(int64_t)w.r * b.max_pages + lp] : -1;
+                        if (pg >= 0 && pg < b.num_pages) {
+                            page = (int32_t)pg;
+                            prefetch_l2(a.kv + pg * kKvPageBytes, kKvPageBytes);
+                        } else {
+                            record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
+                            m = 0;
+                        }
+                    }
+                    tile->page[lane] = page;
+                    tile->seen[lane] = m;
+                }
+                if (lane == 0) {
+                    const bool last = end_of_row || n + 1 == n_mine;
+                    tile->row = (uint32_t)row << 3 | (first ? T_FIRST : 0) | (last ? T_LAST : 0) | (last && end_of_row && !cut ? T_WHOLE : 0);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_AIM0 + n % kAhead]);
+                first = end_of_row;
+                ++t;
+                if (end_of_row && n + 1 < n_mine) {
+                    ++row;
+                    t = 0;
+                    cut = false;
+                    w = row_view(b, a.view, row, lane == 0 ? a.st : nullptr);
+                }
+            }
+            if (!ok && lane == 0) timeout(65);
         }
         __syncwarp();
     } else if (n_mine > 0) {
@@ -396,141 +441,130 @@ dense_mla_kernel(Args a) {
         const int q4 = warp & 3, hh = warp >> 2;
         const int st = q4 * 32 + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
-        // ---- rows of a tile: the quarters of a page's tokens fetch that page, 8 tokens a
-        // warp in two steps.  Eight consecutive lanes hold four 16-byte pieces of two tokens
-        // whose numbers differ in bits 0 and 2, so that their swizzled 16-byte stores fall
-        // into 32 different banks.  The lane's token of step 1 is that of step 0 with bit 2
-        // flipped: in a tile block's address that flips bit 9 and, through the swizzle, bit 6.
-        const int half = q4 >> 1;
-        const int par = lane >> 2 & 1;
-        const int tok0 = ((warp >> 2) * 2 + (warp & 1)) * 8 + par * 5 + (lane >> 4) * 2;
-        const int c8 = (lane & 3) | (lane >> 3 & 1) << 2;  // 16-byte piece of a 128-byte group
-        constexpr uint32_t kFlip = 512 + 64;
-        const uint32_t row_at = (uint32_t)(half * kPage + tok0) * 128;
-        const uint32_t put_at = smem_addr(smem + kOffKV) + (c8 >> 2) * kBlk + row_at + (((2 * (c8 & 3)) ^ (tok0 & 7)) << 4);
-        const uint32_t rope_at = smem_addr(smem + kOffP) + row_at + ((c8 ^ (tok0 & 7)) << 4);
         const uint32_t p_at = smem_addr(smem + kOffP) + st * 128 + (((2 * hh) ^ (st & 7)) << 4);   // P^T row st, heads 16 hh ..
+        // ---- rows of a tile: a warp takes four tokens of each page, a lane token tok of
+        // both.  Eight consecutive lanes hold four 16-byte pieces of two tokens whose
+        // numbers differ in bits 0 and 2, so that their swizzled 16-byte stores fall into 32
+        // different banks.
+        const int par = lane >> 2 & 1;
+        const int tok = (warp >> 1) * 8 + (par ^ (warp & 1)) * 4 + (lane >> 4) * 2 + par;
+        const int c8 = (lane & 3) | (lane >> 3 & 1) << 2;  // 16-byte piece of a 128-byte group
+        const uint32_t put = smem_addr(smem + kOffKV) + (c8 >> 2) * kBlk + tok * 128 + (((2 * (c8 & 3)) ^ (tok & 7)) << 4);
+        const uint32_t putx = put ^ 16;
+        const uint32_t put_rope = smem_addr(smem + kOffP) + tok * 128 + ((c8 ^ (tok & 7)) << 4);
 
-        int row = row_begin, t = tile_begin, left = n_mine, gt = 0;
-        int t_end = 0;                                     // end of the row's piece
         bool ok = true;
-        uint4 raw[2][kSteps], rope[kSteps], scv[kSteps];   // rows in flight: two latent groups, RoPE dims, scales
-        // A tile as this warp fetches it: the lane's rows of step 0 and 1 in its half's page.
-        // A token that is not seen takes a row of the page that is (its probability is 0, and
-        // the product needs a finite latent); a page without any gives zeros (row0 = NULL).
-        struct Aim {
-            const uint8_t *row0, *row1;
-        };
-        Aim now = {}, next = {};                           // the tile in flight, and the one after it
-        bool valid_now = false, valid_next = false;        // softmax: is this lane's token of those tiles seen
-        int32_t pg = -1, pg1 = -1;                         // pages of the tile to aim at next and the one after
-        // page id of this warp's half of tile x, -1 beyond the piece
-        auto page_of = [&](int x) -> int32_t {
-            const int u = 2 * x + half;
-            if (x >= t_end || u >= w.pages) return -1;
-            const int lp = w.page(u);
-            return lp < b.max_pages ? __ldg(b.page_table + (int64_t)w.r * b.max_pages + lp) : -1;
-        };
-        auto aim = [&](int x) {                            // sets `next` to tile x
-            const int u = 2 * x + half;
-            uint64_t m = 0;
-            if (u < w.pages) {
-                const int lp = w.page(u);
-                m = w.first <= lp * kPage && (lp + 1) * kPage <= w.end ? ~0ull : w.seen(lp);
+        int n = 0;                                         // the tile whose softmax comes next
+        uint32_t row = 0, row_next = 0;                    // row and flags of tile n and the one after it
+        bool valid = false, valid_next = false;            // softmax: is the lane's token of those tiles seen
+        uint4 raw[2][2] = {}, rope[2] = {}, scv[2] = {};   // rows of the tile after tile n in flight: two latent groups, RoPE dims, scales
+        // Where the rows are, one per page.  A token that is not seen takes a row of its page
+        // that is (its probability is 0, and the product needs a finite latent); a page without
+        // any gives zeros (NULL, slot -1).
+        const uint8_t* src[2] = {};                        // of the tile in flight
+        int32_t slot_next[2] = {};                         // of the one after it, as cache slots
+        auto aim = [&](int x) {                            // lays slot_next, row_next, .. on tile x
+            ok = wait_ab(&bars[B_AIM0 + x % kAhead], (uint32_t)(x / kAhead & 1), abort_flag) && ok;
+            const Tile* tile = &misc->tile[x % kAhead];
+            row_next = tile->row;
+            valid_next = tile->seen[q4 >> 1] >> (st & 63) & 1u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint64_t m = tile->seen[h];
+                slot_next[h] = tile->page[h] * kPage + tok;
+                if (m != ~0ull) slot_next[h] = m == 0 ? -1 : (m >> tok & 1u) ? slot_next[h] : slot_next[h] - tok + __ffsll((long long)m) - 1;
             }
-            if (m && (pg < 0 || pg >= b.num_pages)) {
-                if (lane == 0 && (warp & ~2) == 0) record_error(a.st, DSA_DEVERR_PAGE_RANGE, pg);
-                m = 0;
-            }
-            valid_next = m >> (st & 63) & 1u;
-            next.row0 = next.row1 = nullptr;
-            if (m) {
-                const int some = __ffsll((long long)m) - 1;
-                const uint8_t* page = a.kv + (int64_t)pg * kKvPageBytes + c8 * 16;
-                next.row0 = page + ((m >> tok0 & 1u) ? tok0 : some) * kKvTokenBytes;
-                next.row1 = page + ((m >> (tok0 ^ 4) & 1u) ? tok0 ^ 4 : some) * kKvTokenBytes;
-            }
-            pg = pg1;
-            pg1 = page_of(x + 2);
-            if ((warp & ~2) == 0 && lane == 0 && pg >= 0 && pg < b.num_pages)     // the page of the tile after
-                prefetch_l2(a.kv + (int64_t)pg * kKvPageBytes, kKvPageBytes);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_FREE0 + x % kAhead]);
         };
-        auto fetch = [&](uint4 (&dst)[kSteps], int at) {   // the 16 bytes at `at` + 16 c8 of the lane's rows
-            if (now.row0 != nullptr) {
-                dst[0] = ldg_pinned(reinterpret_cast<const uint4*>(now.row0 + at));
-                dst[1] = ldg_pinned(reinterpret_cast<const uint4*>(now.row1 + at));
-            } else {
-                dst[0] = dst[1] = make_uint4(0, 0, 0, 0);
+        auto follow = [&]() {                              // fetches are for the tile aimed at from here on
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                src[h] = slot_next[h] < 0 ? nullptr : a.kv + (int64_t)slot_next[h] * kKvTokenBytes + c8 * 16;
+        };
+        static_assert(kKvPageBytes == kPage * kKvTokenBytes, "slots are rows");
+        auto fetch = [&](uint4 (&dst)[2], int at, uint32_t fill) {   // the 16 bytes at `at` + 16 c8 of the lane's rows
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (src[h] != nullptr) dst[h] = ldg_pinned(reinterpret_cast<const uint4*>(src[h] + at));
+                else dst[h] = make_uint4(fill, fill, fill, fill);
             }
         };
-        auto fetch_scales = [&]() { fetch(scv, 512 - c8 * 16); };
-        static_assert(kSteps == 2, "two rows a lane");
-        // The fetched tile into shared memory, latent groups 0..3 (free once tile gt's P.V of
-        // the group is done; `first`: nothing to wait for), then the RoPE block (free, as
-        // P^T, with the last group).  The registers emptied take the group two ahead.
-        auto put_tile = [&](int x, bool first) {
-            const uint32_t ph = (uint32_t)(gt & 1);
-            const bool more = x + 1 < t_end, zeros = now.row0 == nullptr;
-            valid_now = valid_next;
+        // The fetched tile x into shared memory, latent groups 0..3 as soon as the P.V of the
+        // group has completed for tile x - 1 (for x = 0 that is a phase that counts as over),
+        // then the RoPE block (free, as P^T, with the last group).  The registers emptied take
+        // the group two ahead.
+        auto put_tile = [&](int x) {
+            const uint32_t ph = (uint32_t)((x - 1) & 1);
+            const bool more = x + 1 < n_mine;
+            row = row_next;
+            valid = valid_next;
             if (more) aim(x + 1);                          // while the first P.V runs
-            uint32_t off_range = 0;                        // a latent scale or a RoPE value fp16 cannot hold
-#pragma unroll
-            for (int gg = 0; gg < 4; ++gg) {
-                if (!first && ok) ok = wait_ab(&bars[B_PV0 + gg], ph, abort_flag);
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const uint32_t scb = gg == 0 ? scv[i].x : gg == 1 ? scv[i].y : gg == 2 ? scv[i].z : scv[i].w;
-                    off_range |= scb - 0x38000000u > 0x43000000u - 0x38000000u ? 1u : 0u;   // outside [2^-15, 2^7]
-                    const __half2 sc2 = __float2half2_rn(__uint_as_float(scb));              // a power of two: exact
-                    const uint4 v = raw[gg & 1][i];
-                    // 16 FP8 dims 128 gg + 16 c8 .. -> K-block 2 gg + c8 / 4, 16-byte chunks 2 (c8 % 4), +1
-                    const uint32_t at = (put_at ^ (i ? kFlip : 0u)) + 2 * gg * kBlk;
-                    st_shared_v4(at, e4m3x2_scaled_h2(v.x & 0xffffu, sc2), e4m3x2_scaled_h2(v.x >> 16, sc2),
-                                 e4m3x2_scaled_h2(v.y & 0xffffu, sc2), e4m3x2_scaled_h2(v.y >> 16, sc2));
-                    st_shared_v4(at ^ 16, e4m3x2_scaled_h2(v.z & 0xffffu, sc2), e4m3x2_scaled_h2(v.z >> 16, sc2),
-                                 e4m3x2_scaled_h2(v.w & 0xffffu, sc2), e4m3x2_scaled_h2(v.w >> 16, sc2));
-                }
+            // the scales as fp16 (exact), two blocks a word: every one in [2^-15, 2^7] = [0x0200, 0x5800]
+            const uint32_t sc[2][2] = {{pack_h2(__uint_as_float(scv[0].x), __uint_as_float(scv[0].y)),
+                                        pack_h2(__uint_as_float(scv[0].z), __uint_as_float(scv[0].w))},
+                                       {pack_h2(__uint_as_float(scv[1].x), __uint_as_float(scv[1].y)),
+                                        pack_h2(__uint_as_float(scv[1].z), __uint_as_float(scv[1].w))}};
+            uint32_t bad = __vcmpgtu2(__vmaxu2(__vmaxu2(sc[0][0], sc[0][1]), __vmaxu2(sc[1][0], sc[1][1])), 0x58005800u) |
+                           __vcmpltu2(__vminu2(__vminu2(sc[0][0], sc[0][1]), __vminu2(sc[1][0], sc[1][1])), 0x02000200u);
+            auto hand_over = [&](int bar) {
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_FULL0 + gg]);
+                if (lane == 0) mbar_arrive(&bars[bar]);
+            };
+            auto group = [&](auto gi) {
+                constexpr int gg = decltype(gi)::value;
+                ok = wait_ab(&bars[B_PV0 + gg], ph, abort_flag) && ok;
+                auto put_row = [&](auto hi) {
+                    // 16 FP8 dims 128 gg + 16 c8 .. -> K-block 2 gg + c8 / 4, 16-byte chunks 2 (c8 % 4), +1
+                    constexpr int h = decltype(hi)::value, kOff = 2 * gg * kBlk + h * kPage * 128;
+                    const uint32_t sc2 = __byte_perm(sc[h][gg >> 1], 0, (gg & 1) ? 0x3232 : 0x1010);
+                    const uint4 v = raw[gg & 1][h];
+                    uint32_t o[8];
+                    e4m3x4_scaled_h2(v.x, sc2, o[0], o[1]);
+                    e4m3x4_scaled_h2(v.y, sc2, o[2], o[3]);
+                    e4m3x4_scaled_h2(v.z, sc2, o[4], o[5]);
+                    e4m3x4_scaled_h2(v.w, sc2, o[6], o[7]);
+                    st_shared_v4<kOff>(put, o[0], o[1], o[2], o[3]);
+                    st_shared_v4<kOff>(putx, o[4], o[5], o[6], o[7]);
+                };
+                put_row(std::integral_constant<int, 0>{});
+                put_row(std::integral_constant<int, 1>{});
+                hand_over(B_FULL0 + gg);
                 if (gg < 2) {
-                    fetch(raw[gg], (gg + 2) * 128);
+                    fetch(raw[gg], (gg + 2) * 128, 0u);
                 } else if (more) {
-                    if (gg == 2) now = next;
-                    fetch(raw[gg - 2], (gg - 2) * 128);
+                    if (gg == 2) {
+                        follow();
+                        fetch(scv, 512 - c8 * 16, 0x3f800000u);
+                    }
+                    fetch(raw[gg - 2], (gg - 2) * 128, 0u);
                 }
-            }
-            if (more) fetch_scales();
-            uint32_t rope_max = 0;                         // two bf16 magnitudes, compared as integers
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const uint4 v = rope[i];
-                rope_max = __vmaxu2(rope_max, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-                st_shared_v4(rope_at ^ (i ? kFlip : 0u), bf16x2_to_h2_sat(v.x), bf16x2_to_h2_sat(v.y), bf16x2_to_h2_sat(v.z),
-                             bf16x2_to_h2_sat(v.w));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_FULL4]);
-            off_range |= (rope_max & 0xffffu) >= 0x4780u || rope_max >= 0x47800000u ? 1u : 0u;   // |r| >= 2^16
-            if (off_range && !zeros) record_error(a.st, DSA_DEVERR_FP16_RANGE, lane);
-            if (more) fetch(rope, 528);
+            };
+            group(std::integral_constant<int, 0>{});
+            group(std::integral_constant<int, 1>{});
+            group(std::integral_constant<int, 2>{});
+            group(std::integral_constant<int, 3>{});
+            uint32_t rope_max = 0;                         // bf16 magnitudes, compared as integers: |r| < 2^16
+            auto rope_row = [&](auto hi) {
+                constexpr int h = decltype(hi)::value;
+                const uint4 r = rope[h];
+                rope_max = __vmaxu2(rope_max, __vmaxu2(__vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu),
+                                                       __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu)));
+                st_shared_v4<h * kPage * 128>(put_rope, bf16x2_to_h2_sat(r.x), bf16x2_to_h2_sat(r.y), bf16x2_to_h2_sat(r.z),
+                                              bf16x2_to_h2_sat(r.w));
+            };
+            rope_row(std::integral_constant<int, 0>{});
+            rope_row(std::integral_constant<int, 1>{});
+            hand_over(B_FULL4);
+            if (more) fetch(rope, 528, 0u);
+            if (bad | __vcmpgtu2(rope_max, 0x477f477fu)) record_error(a.st, DSA_DEVERR_FP16_RANGE, lane);
         };
-        // Fetches the first tile of the current piece and lays out the row's Q (fp16,
-        // K-major, 128-byte swizzle): every S^T issued so far has completed, so Q is
-        // free.  Returns the softmax scale in log2 units times 2^-kq of the row's Q.
-        auto open_piece = [&]() -> float {
-            pg = page_of(t);
-            pg1 = page_of(t + 1);
-            aim(t);
-            now = next;
-            fetch_scales();
-            fetch(raw[0], 0);
-            fetch(raw[1], 128);
-            fetch(rope, 528);
+        // The row's Q (fp16, K-major, 128-byte swizzle): every S^T issued so far has completed,
+        // so its place is free.  Returns the softmax scale in log2 units times 2^-kq of the Q.
+        auto put_q = [&](int q_row) -> float {
             static_assert(64 * 72 == 9 * kWorkThreads, "nine 16-byte pieces of q per thread");
-            const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (int64_t)row * (64 * 576));
+            const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (int64_t)q_row * (64 * 576));
             uint32_t mx = 0;                               // two bf16 magnitudes, compared as integers
 #pragma unroll 1
             for (int u0 = 0; u0 < 9; u0 += 3) {
@@ -564,7 +598,7 @@ dense_mla_kernel(Args a) {
                                    bf16x2_scaled_to_h2(qv[u].z, sc), bf16x2_scaled_to_h2(qv[u].w, sc));
                 }
             }
-            if (tid == 0 && mx >= 0x7f80u) record_error(a.st, DSA_DEVERR_FP16_RANGE, row);   // inf / NaN in q
+            if (tid == 0 && mx >= 0x7f80u) record_error(a.st, DSA_DEVERR_FP16_RANGE, q_row);   // inf / NaN in q
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_QFULL]);
@@ -574,177 +608,162 @@ dense_mla_kernel(Args a) {
         float lsum[kHeads];                                // this token lane's running sums of its heads
 #pragma unroll
         for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
-        if (tid < 16) neg_inf[tid] = -INFINITY;
-        if (tid < 64) neg_ref[tid] = kNoRef;               // seen by all behind open_piece's barrier
-        float sl2 = 0.f;
-        bool fresh = true;                                 // the next softmax is its piece's first
-        int k = 0;                                         // pieces opened
-        for (;;) {
-            bool ended = false;
-            if (k > 0) {
-                // ---- softmax of tile t
-                if (ok) ok = wait_ab(&bars[B_SFULL], (uint32_t)(gt & 1), abort_flag);
-                // a token that is not seen takes -inf for its references: every P is 0
-                const float4* nr4 = reinterpret_cast<const float4*>(valid_now ? neg_ref + hh * kHeads : neg_inf);
-                uint32_t most;                              // largest P of the thread, as two fp16
-                // S^T row of this token for the warp's heads
-                auto load_s = [&](float (&v)[kHeads]) {
-                    uint32_t x[kHeads];
-                    tmem_ld_32x32b_x16(lane_addr + kColS + hh * kHeads, x);
-                    tmem_ld_wait();
+        if (tid < 32) neg_inf[tid] = -INFINITY;
+        if (tid < 64) neg_ref[tid] = kNoRef;               // seen by all behind put_q's barrier
+        aim(0);
+        follow();
+        fetch(scv, 512 - c8 * 16, 0x3f800000u);
+        fetch(raw[0], 0, 0u);
+        fetch(raw[1], 128, 0u);
+        fetch(rope, 528, 0u);
+        float sl2 = put_q((int)(row_next >> 3));
+        put_tile(0);
+        int piece = 0;
+        for (;; ++n) {
+            const uint32_t done = row;                      // row and flags of this tile
+            // ---- softmax of tile n
+            ok = wait_ab(&bars[B_SFULL], (uint32_t)(n & 1), abort_flag) && ok;
+            // a token that is not seen takes -inf for its references: every P is 0
+            const float4* nr4 = reinterpret_cast<const float4*>(valid ? neg_ref + hh * kHeads : neg_inf);
+            uint32_t most;                                  // largest P of the thread, as two fp16
+            // S^T row of this token for the warp's heads
+            auto load_s = [&](float (&v)[kHeads]) {
+                uint32_t x[kHeads];
+                tmem_ld_32x32b_x16(lane_addr + kColS + hh * kHeads, x);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < kHeads; ++h) v[h] = __uint_as_float(x[h]);
+                for (int h = 0; h < kHeads; ++h) v[h] = __uint_as_float(x[h]);
+            };
+            // P of the current references, and its P^T row (heads 16 hh.. as fp16, MN-major swizzle)
+            auto write_p = [&](float (&v)[kHeads]) {
+                most = 0;
+                auto eight = [&](auto ci) {
+                    constexpr int c = decltype(ci)::value * 8;
+                    const float4 m0 = nr4[c / 4], m1 = nr4[c / 4 + 1];
+                    v[c] = ex2_approx(fmaf(v[c], sl2, m0.x));
+                    v[c + 1] = ex2_approx(fmaf(v[c + 1], sl2, m0.y));
+                    v[c + 2] = ex2_approx(fmaf(v[c + 2], sl2, m0.z));
+                    v[c + 3] = ex2_approx(fmaf(v[c + 3], sl2, m0.w));
+                    v[c + 4] = ex2_approx(fmaf(v[c + 4], sl2, m1.x));
+                    v[c + 5] = ex2_approx(fmaf(v[c + 5], sl2, m1.y));
+                    v[c + 6] = ex2_approx(fmaf(v[c + 6], sl2, m1.z));
+                    v[c + 7] = ex2_approx(fmaf(v[c + 7], sl2, m1.w));
+                    const uint32_t h0 = pack_h2(v[c], v[c + 1]), h1 = pack_h2(v[c + 2], v[c + 3]);
+                    const uint32_t h2 = pack_h2(v[c + 4], v[c + 5]), h3 = pack_h2(v[c + 6], v[c + 7]);
+                    st_shared_v4(p_at ^ (c * 2), h0, h1, h2, h3);
+                    most = __vmaxu2(most, __vmaxu2(__vmaxu2(h0, h1), __vmaxu2(h2, h3)));
                 };
-                // P of the current references, and its P^T row (heads 16 hh.. as fp16, MN-major swizzle)
-                auto write_p = [&](float (&v)[kHeads]) {
-#pragma unroll
-                    for (int c4 = 0; c4 < kHeads / 4; ++c4) {
-                        const float4 m = nr4[c4];
-                        v[4 * c4] = ex2_approx(fmaf(v[4 * c4], sl2, m.x));
-                        v[4 * c4 + 1] = ex2_approx(fmaf(v[4 * c4 + 1], sl2, m.y));
-                        v[4 * c4 + 2] = ex2_approx(fmaf(v[4 * c4 + 2], sl2, m.z));
-                        v[4 * c4 + 3] = ex2_approx(fmaf(v[4 * c4 + 3], sl2, m.w));
-                    }
-                    uint32_t h[kHeads / 2];
-#pragma unroll
-                    for (int c = 0; c < kHeads / 2; ++c) h[c] = pack_h2(v[2 * c], v[2 * c + 1]);
-                    st_shared_v4(p_at, h[0], h[1], h[2], h[3]);
-                    st_shared_v4(p_at ^ 16, h[4], h[5], h[6], h[7]);
-                    most = __vmaxu2(__vmaxu2(__vmaxu2(h[0], h[1]), __vmaxu2(h[2], h[3])),
-                                    __vmaxu2(__vmaxu2(h[4], h[5]), __vmaxu2(h[6], h[7])));
-                    fence_proxy_async_smem();
-                };
-                float v[kHeads];
+                eight(std::integral_constant<int, 0>{});
+                eight(std::integral_constant<int, 1>{});
+                fence_proxy_async_smem();
+            };
+            float v[kHeads];
+            tc_fence_after();
+            load_s(v);
+            write_p(v);
+            // ---- a score above its head's reference by more than 2^kTau (P above 2^(kTau + kShift))
+            //      makes every warp take new references (always on the piece's first tile)
+            const bool over = (most & 0xffffu) > kPMaxH || most >> 16 > kPMaxH;
+            tc_fence_before();
+            if (vote(over || !ok)) {
                 tc_fence_after();
-                load_s(v);
-                write_p(v);
-                // ---- a score above its head's reference by more than 2^kTau (P above 2^(kTau + kShift))
-                //      makes every warp take new references (always on the piece's first tile)
-                const bool over = (most & 0xffffu) > kPMaxH || most >> 16 > kPMaxH;
-                if (work_any(over || !ok)) {
-                    if (work_any(!ok)) {
-                        if (tid == 0) timeout(63);
-                        break;
-                    }
-                    load_s(v);
-#pragma unroll
-                    for (int c = 0; c < kHeads; ++c) v[c] = valid_now ? v[c] * sl2 : -INFINITY;
-                    xreduce16<true>(v, lane);                   // per-head tile max (consumes v)
-                    if (lane < kHeads) red[q4 * 64 + hh * kHeads + lane] = v[0];
-                    work_sync();
-                    if (tid < 64) {
-                        const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid])) - kShift;
-                        const float mo = -neg_ref[tid];
-                        const bool need = tm > mo + kTau;
-                        alpha[tid] = need ? exp2f(mo - tm) : 1.f;          // 0 for a first reference
-                        if (need) neg_ref[tid] = -tm;
-                    }
-                    work_sync();
-                    bool mine = false;                          // does a head of this warp have a new reference
-#pragma unroll
-                    for (int c = 0; c < kHeads; ++c) mine |= alpha[hh * kHeads + c] != 1.f;
-                    if (mine) {
-                        if (!fresh) {                           // rescale the resident O^T columns of these heads
-#pragma unroll 1
-                            for (int mb = 0; mb < 4; ++mb) {
-                                uint32_t o[kHeads];
-                                const uint32_t addr = lane_addr + kColO + mb * 64 + hh * kHeads;
-                                tmem_ld_32x32b_x16(addr, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int c = 0; c < kHeads; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[hh * kHeads + c]);
-                                tmem_st_32x32b_x16(addr, o);
-                            }
-                            tmem_st_wait();
-                        }
-#pragma unroll
-                        for (int c = 0; c < kHeads; ++c) lsum[c] *= alpha[hh * kHeads + c];
-                    }
-                    load_s(v);
-                    write_p(v);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_PREADY]);    // P^T written, S^T read, O^T rescaled
-#pragma unroll
-                for (int c = 0; c < kHeads; ++c) lsum[c] += v[c];
-                fresh = false;
-                --left;
-                ended = ++t == t_end;
-            }
-            // ---- the piece's sums; the next row
-            int done = row;
-            bool whole = false;
-            float sl2_next = sl2;
-            if (ended) {
-                xreduce16<false>(lsum, lane);
-                if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];
-                whole = (k > 1 || tile_begin == 0) && w.pages <= 2 * t_end;
-                __syncwarp();
-            }
-            if (left > 0 && (ended || k == 0)) {
-                if (ended) {
-                    ++row;
-                    t = 0;
-                }
-                t_end = enter_row(row, tid == 0 ? a.st : nullptr);
-                t_end = min(t_end, t + left);
-                sl2_next = open_piece();
-                ++k;
-            }
-            // ---- the next tile
-            if (left > 0) put_tile(t, k == 1 && fresh);
-            if (k == 1 && fresh) {
-                sl2 = sl2_next;
-                continue;
-            }
-            if (ended) {
-                // ---- the piece's output
-                if (ok) ok = wait_ab(&bars[B_PV3], (uint32_t)(gt & 1), abort_flag);   // O^T is final
-                if (work_any(!ok)) {
-                    if (tid == 0) timeout(64);
+                if (vote(!ok)) {
+                    if (tid == 0) timeout(63);
                     break;
                 }
-                tc_fence_after();
-                if (tid < 64) l_acc[tid] = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
-                work_sync();
-                const int64_t unit = 2 * (int64_t)blockIdx.x + (done == row_begin ? 0 : 1);   // a share's first piece, or its last
-#pragma unroll 1
-                for (int mb = 0; mb < 4; ++mb) {
-                    uint32_t o[kHeads];
-                    tmem_ld_32x32b_x16(lane_addr + kColO + mb * 64 + hh * kHeads, o);
-                    tmem_ld_wait();
-                    const int d = mb * 128 + st;                           // latent dim of this TMEM lane
+                load_s(v);
 #pragma unroll
-                    for (int c = 0; c < kHeads; ++c) {                     // a warp stores 32 consecutive dims
-                        const int h = hh * kHeads + c;
-                        const float ov = __uint_as_float(o[c]);
-                        if (whole) {
-                            const float l = l_acc[h];
-                            const float val = l > 0.f ? ov / l : 0.f;
-                            const int64_t oi = ((int64_t)done * 64 + h) * 512 + d;
-                            if (a.out_f32) static_cast<float*>(a.out)[oi] = val;
-                            else static_cast<__nv_bfloat16*>(a.out)[oi] = __float2bfloat16_rn(val);
-                        } else {
-                            a.part_o[(unit * 64 + h) * 512 + d] = ov;
+                for (int c = 0; c < kHeads; ++c) v[c] = valid ? v[c] * sl2 : -INFINITY;
+                xreduce16<true>(v, lane);                   // per-head tile max (consumes v)
+                if (lane < kHeads) red[q4 * 64 + hh * kHeads + lane] = v[0];
+                work_sync();
+                if (tid < 64) {
+                    const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid])) - kShift;
+                    const float mo = -neg_ref[tid];
+                    const bool need = tm > mo + kTau;
+                    alpha[tid] = need ? exp2f(mo - tm) : 1.f;          // 0 for a first reference
+                    if (need) neg_ref[tid] = -tm;
+                }
+                work_sync();
+                bool mine = false;                          // does a head of this warp have a new reference
+#pragma unroll
+                for (int c = 0; c < kHeads; ++c) mine |= alpha[hh * kHeads + c] != 1.f;
+                if (mine) {
+                    if (!(done & T_FIRST)) {                           // rescale the resident O^T columns of these heads
+#pragma unroll 1
+                        for (int mb = 0; mb < 4; ++mb) {
+                            uint32_t o[kHeads];
+                            const uint32_t addr = lane_addr + kColO + mb * 64 + hh * kHeads;
+                            tmem_ld_32x32b_x16(addr, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < kHeads; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[hh * kHeads + c]);
+                            tmem_st_32x32b_x16(addr, o);
                         }
+                        tmem_st_wait();
+                    }
+#pragma unroll
+                    for (int c = 0; c < kHeads; ++c) lsum[c] *= alpha[hh * kHeads + c];
+                }
+                load_s(v);
+                write_p(v);
+                tc_fence_before();
+                vote(false);
+            }
+#pragma unroll
+            for (int c = 0; c < kHeads; ++c) lsum[c] += v[c];
+            // ---- the next row's Q and the next tile
+            float sl2_next = sl2;
+            if (n + 1 < n_mine) {
+                if (row_next & T_FIRST) sl2_next = put_q((int)(row_next >> 3));
+                put_tile(n + 1);
+            }
+            if (!(done & T_LAST)) continue;
+            // ---- the piece's output: O^T is final when its last P.V has completed
+            ok = wait_ab(&bars[B_PV3], (uint32_t)(n & 1), abort_flag) && ok;
+            xreduce16<false>(lsum, lane);
+            if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];
+            work_sync();                                    // a timeout here is seen by the next vote, or is the end
+            tc_fence_after();
+            if (tid < 64) l_acc[tid] = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
+            work_sync();
+            const int64_t unit = 2 * (int64_t)blockIdx.x + (piece++ == 0 ? 0 : 1);   // a share's first piece, or its last
+#pragma unroll 1
+            for (int mb = 0; mb < 4; ++mb) {
+                uint32_t o[kHeads];
+                tmem_ld_32x32b_x16(lane_addr + kColO + mb * 64 + hh * kHeads, o);
+                tmem_ld_wait();
+                const int d = mb * 128 + st;                           // latent dim of this TMEM lane
+#pragma unroll
+                for (int c = 0; c < kHeads; ++c) {                     // a warp stores 32 consecutive dims
+                    const int h = hh * kHeads + c;
+                    const float ov = __uint_as_float(o[c]);
+                    if (done & T_WHOLE) {
+                        const float l = l_acc[h];
+                        const float val = l > 0.f ? ov / l : 0.f;
+                        const int64_t oi = ((int64_t)(done >> 3) * 64 + h) * 512 + d;
+                        if (a.out_f32) static_cast<float*>(a.out)[oi] = val;
+                        else static_cast<__nv_bfloat16*>(a.out)[oi] = __float2bfloat16_rn(val);
+                    } else {
+                        a.part_o[(unit * 64 + h) * 512 + d] = ov;
                     }
                 }
-                tc_fence_before();
-                if (tid < 64) {
-                    const float l = l_acc[tid];
-                    if (!whole) a.part_ml[unit * 64 + tid] = make_float2(-neg_ref[tid], l);
-                    else if (a.lse) a.lse[(int64_t)done * 64 + tid] = l > 0.f ? (log2f(l) - neg_ref[tid]) * 0.69314718055994531f : -INFINITY;
-                    neg_ref[tid] = kNoRef;
-                }
-                if (left == 0) break;
-                sl2 = sl2_next;
-                fresh = true;
-#pragma unroll
-                for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
-                work_sync();                                // O^T and the references may be reused
             }
-            ++gt;
+            tc_fence_before();
+            if (tid < 64) {
+                const float l = l_acc[tid];
+                if (!(done & T_WHOLE)) a.part_ml[unit * 64 + tid] = make_float2(-neg_ref[tid], l);
+                else if (a.lse) a.lse[(int64_t)(done >> 3) * 64 + tid] = l > 0.f ? (log2f(l) - neg_ref[tid]) * 0.69314718055994531f : -INFINITY;
+                neg_ref[tid] = kNoRef;
+            }
+            if (n + 1 == n_mine) {
+                if (!ok && lane == 0) timeout(64);
+                break;
+            }
+            sl2 = sl2_next;
+#pragma unroll
+            for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
+            work_sync();                                    // O^T and the references may be reused
         }
     }
     tc_fence_before();
@@ -865,7 +884,8 @@ static dsa_status launch(const void* q, const uint8_t* kv, const dsa_batch* b, V
     if (b->total_q == 0) return DSA_OK;
     if (!q || !kv || !out) return DSA_ERR_INVALID_ARGUMENT;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(out)) return DSA_ERR_ALIGNMENT;
-    if (b->total_q * most_tiles(b, view) / device_sm_count() > 0x7ffffff0LL) return DSA_ERR_UNSUPPORTED;   // 32-bit tile counts of a share
+    // 32-bit tile counts of a share, rows with three flags in a word
+    if (b->total_q * most_tiles(b, view) / device_sm_count() > 0x7ffffff0LL || b->total_q > 0x1fffffffLL) return DSA_ERR_UNSUPPORTED;
     if (!ws) return DSA_ERR_INVALID_ARGUMENT;
     if (bytes < ws_bytes(device_sm_count())) return DSA_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned16(ws)) return DSA_ERR_ALIGNMENT;
