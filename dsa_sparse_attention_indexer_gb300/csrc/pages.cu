@@ -5,9 +5,12 @@
 // All of it is copying and counting: a move is bound by HBM (row bytes read and
 // written once), the pool calls by latency (one pass over the counts up to the
 // last page taken).
+#include <algorithm>
+
 #include "dsa_internal.cuh"
 #include "indexer_common.cuh"
 #include "select_common.cuh"
+#include "sm100.cuh"
 
 namespace dsa {
 namespace pages {
@@ -17,6 +20,7 @@ constexpr int kMaxRows = 4096;                             // requests of one re
 constexpr int kMaxAccept = 64;
 constexpr int kCopyThreads = 256;
 constexpr int kPoolThreads = 1024;
+constexpr int kPerThread = kMaxRows / kPoolThreads;         // requests of a thread of the pool calls
 
 struct CacheList {
     uint8_t* data[kMaxCaches];
@@ -38,31 +42,39 @@ __device__ __forceinline__ Layout layout_of(int kind) {
 }
 
 // ---------------------------------------------------------------- commit
-// One block per (request, cache).  Every row that moves is read into registers
-// (at most 64 rows x 41 pieces, 11 per thread, all loads in flight) before the
-// barrier and written after it, so a row may be another row's target.
-constexpr int kRowPieces = (kMaxAccept * (DSA_KV_TOKEN_BYTES / 16) + kCopyThreads - 1) / kCopyThreads;
+// One block per (request, run of caches): the moves are worked out once, by a chain
+// of dependent loads (lengths, list, page table), and then applied cache by cache.
+// A warp moves one row at a time, 41 (KV) or 8 / 4 (index-K) pieces of 16 bytes; a
+// round reads up to 64 rows of as many whole caches as they make into registers, all
+// loads in flight, before the barrier and writes them after it, so a row may be
+// another row's target.  (A block per cache spent most of its time on the chain:
+// 128 requests x 99 caches took 45 us.)
+constexpr int kCommitWarps = kCopyThreads / 32;
+constexpr int kRowsPerWarp = kMaxAccept / kCommitWarps;    // of a round
+constexpr int kCommitBlocks = 1216;                        // about one resident wave of blocks
 
 __global__ void __launch_bounds__(kCopyThreads)
-commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheList cl, int n_caches,
+commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheList cl, int n_caches, int per_block,
               int32_t* __restrict__ new_len, int32_t* __restrict__ st) {
     __shared__ int32_t s_src[kMaxAccept], s_dst[kMaxAccept];
     __shared__ int32_t s_n;
     pdl_wait();
     pdl_trigger();
-    const int r = blockIdx.x, c = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-    if (tid < 32) {
-        const int qn = b.q_start[r + 1] - b.q_start[r];
-        const int P = b.seq_len[r] - qn;
-        int a[2], kept = 0;
+    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool speaks = blockIdx.y == 0;                   // one block per request records and writes the length
+    if (warp == 0) {
+        const int qs = b.q_start[r], qe = b.q_start[r + 1], L = b.seq_len[r];
+        int a[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a[h] = h * 32 + lane < width ? accept[(int64_t)r * width + h * 32 + lane] : -1;
+        const int qn = qe - qs, P = L - qn;
+        int kept = 0;
         bool open = true;                                  // the list has not ended yet
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int k = h * 32 + lane;
-            a[h] = k < width ? accept[(int64_t)r * width + k] : -1;
             const unsigned end = __ballot_sync(0xffffffffu, a[h] < 0 || a[h] >= qn);
             const int n = !open ? 0 : end ? __ffs(end) - 1 : 32;
-            if (open && end && c == 0) {
+            if (open && end && speaks) {
                 const int bad = __shfl_sync(0xffffffffu, a[h], __ffs(end) - 1);
                 if (lane == 0 && bad >= 0) record_error(st, DSA_DEVERR_INDEX_RANGE, bad);
             }
@@ -70,10 +82,10 @@ commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheLi
             open = open && !end;
         }
         if (P < 0 && kept > 0) {                           // more new tokens than the request holds
-            if (lane == 0 && c == 0) record_error(st, DSA_DEVERR_INDEX_RANGE, P);
+            if (lane == 0 && speaks) record_error(st, DSA_DEVERR_INDEX_RANGE, P);
             kept = 0;
         }
-        if (c == 0 && lane == 0 && new_len) new_len[r] = P + kept;
+        if (speaks && lane == 0 && new_len) new_len[r] = P + kept;
         int n_moves = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -82,12 +94,12 @@ commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheLi
             if (k < kept && a[h] != k) {                   // a token already in place stays
                 const int js = P + a[h], jd = P + k;
                 if (js / kPage >= b.max_pages || jd / kPage >= b.max_pages) {
-                    if (c == 0) record_error(st, DSA_DEVERR_INDEX_RANGE, js);
+                    if (speaks) record_error(st, DSA_DEVERR_INDEX_RANGE, js);
                 } else {
                     const int64_t ps = b.page_table[(int64_t)r * b.max_pages + js / kPage];
                     const int64_t pd = b.page_table[(int64_t)r * b.max_pages + jd / kPage];
                     if (ps < 0 || ps >= b.num_pages || pd < 0 || pd >= b.num_pages) {
-                        if (c == 0) record_error(st, DSA_DEVERR_PAGE_RANGE, ps < 0 || ps >= b.num_pages ? ps : pd);
+                        if (speaks) record_error(st, DSA_DEVERR_PAGE_RANGE, ps < 0 || ps >= b.num_pages ? ps : pd);
                     } else {
                         src = (int32_t)(ps * kPage + js % kPage);
                         dst = (int32_t)(pd * kPage + jd % kPage);
@@ -106,39 +118,41 @@ commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheLi
     }
     __syncthreads();
     const int n = s_n;
-    if (n == 0 || c >= n_caches) return;
-    const Layout lo = layout_of(cl.kind[c]);
-    uint8_t* base = cl.data[c];
-    const int total = n * lo.row16;
-    uint4 v[kRowPieces];
-    uint32_t word = 0;
+    if (n == 0) return;
+    const int c_end = min(n_caches, (int)(blockIdx.y + 1) * per_block);
+    const int round = kMaxAccept / n;                      // caches of a round, at least one
+    for (int c0 = blockIdx.y * per_block; c0 < c_end; c0 += round) {
+        const int rows = min(round, c_end - c0) * n;
+        uint4 v0[kRowsPerWarp], v1[kRowsPerWarp];          // a lane's pieces of a row: lane and, in KV rows, 32 + lane
+        uint32_t word[kRowsPerWarp];                       // an index key's scale word
 #pragma unroll
-    for (int u = 0; u < kRowPieces; ++u) {
-        const int e = tid + u * kCopyThreads;
-        if (e < total) {
-            const int m = e / lo.row16, piece = e - m * lo.row16;
-            const int32_t s = s_src[m];
-            v[u] = *reinterpret_cast<const uint4*>(base + (int64_t)(s / kPage) * lo.page_bytes +
-                                                   ((s % kPage) * lo.row16 + piece) * 16);
+        for (int u = 0; u < kRowsPerWarp; ++u) {
+            const int x = u * kCommitWarps + warp;
+            if (x < rows) {
+                const int c = c0 + x / n, s = s_src[x % n];
+                const Layout lo = layout_of(cl.kind[c]);
+                const uint8_t* page = cl.data[c] + (int64_t)(s / kPage) * lo.page_bytes;
+                const uint4* from = reinterpret_cast<const uint4*>(page) + (s % kPage) * lo.row16;
+                if (lane < lo.row16) v0[u] = from[lane];
+                if (lane + 32 < lo.row16) v1[u] = from[lane + 32];
+                if (lo.scale_at && lane == 0) word[u] = *reinterpret_cast<const uint32_t*>(page + lo.scale_at + (s % kPage) * 4);
+            }
+        }
+        __syncthreads();                                   // every source row of these caches has been read
+#pragma unroll
+        for (int u = 0; u < kRowsPerWarp; ++u) {
+            const int x = u * kCommitWarps + warp;
+            if (x < rows) {
+                const int c = c0 + x / n, d = s_dst[x % n];
+                const Layout lo = layout_of(cl.kind[c]);
+                uint8_t* page = cl.data[c] + (int64_t)(d / kPage) * lo.page_bytes;
+                uint4* to = reinterpret_cast<uint4*>(page) + (d % kPage) * lo.row16;
+                if (lane < lo.row16) to[lane] = v0[u];
+                if (lane + 32 < lo.row16) to[lane + 32] = v1[u];
+                if (lo.scale_at && lane == 0) *reinterpret_cast<uint32_t*>(page + lo.scale_at + (d % kPage) * 4) = word[u];
+            }
         }
     }
-    if (lo.scale_at && tid < n)
-        word = *reinterpret_cast<const uint32_t*>(base + (int64_t)(s_src[tid] / kPage) * lo.page_bytes + lo.scale_at +
-                                                  (s_src[tid] % kPage) * 4);
-    __syncthreads();                                       // every source row has been read
-#pragma unroll
-    for (int u = 0; u < kRowPieces; ++u) {
-        const int e = tid + u * kCopyThreads;
-        if (e < total) {
-            const int m = e / lo.row16, piece = e - m * lo.row16;
-            const int32_t d = s_dst[m];
-            *reinterpret_cast<uint4*>(base + (int64_t)(d / kPage) * lo.page_bytes + ((d % kPage) * lo.row16 + piece) * 16) =
-                v[u];
-        }
-    }
-    if (lo.scale_at && tid < n)
-        *reinterpret_cast<uint32_t*>(base + (int64_t)(s_dst[tid] / kPage) * lo.page_bytes + lo.scale_at +
-                                     (s_dst[tid] % kPage) * 4) = word;
 }
 
 // ---------------------------------------------------------------- release
@@ -174,11 +188,12 @@ release_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
 }
 
 // ---------------------------------------------------------------- taking pages
-// Walks the free pages in ascending order and calls take(rank, page) for the
-// first `want` of them; returns how many there were (at most want).  One block:
-// each step covers 16 counts per thread, the next step's loads in flight while
-// this one's ranks are scanned.
-constexpr int kStep = 16 * kPoolThreads;
+// One cluster of up to eight blocks walks the counts.  Each round covers 16 counts
+// per thread and block, a block's next round in flight while the blocks tell one
+// another how many free pages they hold; the ranks follow from a scan inside the
+// block, so every block knows where its pages belong and takes them at once.
+constexpr int kPoolBlocks = 8;                             // the largest cluster every launch may have
+constexpr int kStep = 16 * kPoolThreads;                   // counts of a block's round
 
 struct Counts {
     int4 v[4];
@@ -196,39 +211,67 @@ __device__ __forceinline__ void load_counts(Counts& c, const int32_t* ref, int64
         }
     }
 }
+// Where this thread's counts of the block's first round begin.
+__device__ __forceinline__ int64_t first_count() { return (int64_t)blockIdx.x * kStep + (int64_t)threadIdx.x * 16; }
 
+// Calls take(rank, page) for the first `want` free pages in ascending order and
+// returns how many there were (at most want), the same in every block.  c: the
+// counts from first_count() on, loaded by the caller.
 template <typename Take>
-__device__ __forceinline__ int walk_free(const int32_t* ref, int64_t num_pages, int want, int* scratch, Take take) {
-    const int tid = threadIdx.x;
-    int found = 0;
-    Counts next;
-    load_counts(next, ref, num_pages, (int64_t)tid * 16);
-    for (int64_t base = 0; base < num_pages && found < want; base += kStep) {
-        const Counts c = next;
-        if (base + kStep < num_pages) load_counts(next, ref, num_pages, base + kStep + (int64_t)tid * 16);
+__device__ __forceinline__ int walk_free(Counts c, const int32_t* ref, int64_t num_pages, int want, int* scratch, Take take) {
+    __shared__ int s_tot[2][kPoolBlocks];                  // free pages of each block's round
+    const int tid = threadIdx.x, blocks = gridDim.x;
+    const int64_t round = (int64_t)blocks * kStep;
+    int found = 0, turn = 0;
+    int64_t at = first_count();
+    for (int64_t base = 0; base < num_pages && found < want; base += round, at += round, turn ^= 1) {
+        Counts next;
+        if (base + round < num_pages) load_counts(next, ref, num_pages, at + round);
         int n = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) n += (c.v[u].x == 0) + (c.v[u].y == 0) + (c.v[u].z == 0) + (c.v[u].w == 0);
-        int tot;
-        int rank = found + sel::excl_scan<kPoolThreads, 0>(n, tid, scratch, &tot);
+        int tot, rank = found + sel::excl_scan<kPoolThreads, 0>(n, tid, scratch, &tot), all = tot;
+        if (blocks > 1) {
+            if (tid < blocks) sm100::st_cluster_u32(sm100::mapa_shared(sm100::smem_addr(&s_tot[turn][blockIdx.x]), tid), (uint32_t)tot);
+            sm100::cluster_sync();                         // a block is never two rounds ahead: two sets of slots do
+            all = 0;
+            for (int b = 0; b < blocks; ++b) {
+                if (b == (int)blockIdx.x) rank += all;
+                all += s_tot[turn][b];
+            }
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int x[4] = {c.v[u].x, c.v[u].y, c.v[u].z, c.v[u].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (x[e] == 0) {
-                    if (rank < want) take(rank, base + (int64_t)tid * 16 + 4 * u + e);
+                    if (rank < want) take(rank, at + 4 * u + e);
                     ++rank;
                 }
         }
-        found += tot;
+        found += all;
+        c = next;
     }
     return min(found, want);
 }
 
+// Whether d is among s[0 .. n); s is 16-byte aligned.
+__device__ __forceinline__ bool among(const int32_t* s, int n, int d) {
+    bool hit = false;
+    int j = 0;
+#pragma unroll 4
+    for (; j + 4 <= n; j += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(s + j);
+        hit |= (v.x == d) | (v.y == d) | (v.z == d) | (v.w == d);
+    }
+    for (; j < n; ++j) hit |= s[j] == d;
+    return hit;
+}
+
 // Exclusive prefix sums of cnt[0 .. n) in place, cnt[n] = their total; n <= kMaxRows.
 __device__ __forceinline__ int prefix_in_place(int32_t* cnt, int n, int* scratch) {
-    constexpr int kPer = kMaxRows / kPoolThreads;
+    constexpr int kPer = kPerThread;
     const int tid = threadIdx.x;
     int x[kPer], sum = 0;
 #pragma unroll
@@ -262,57 +305,72 @@ __device__ __forceinline__ int owner_of(const int32_t* cnt, int n, int e) {
 
 __device__ __forceinline__ int pages_of(int len) { return len / kPage + (len % kPage != 0); }
 
+// The e-th entry of the call takes the e-th free page, unless it holds one already.
 __global__ void __launch_bounds__(kPoolThreads)
 reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict__ table, int rows, int max_pages,
                const int32_t* __restrict__ row, const int32_t* __restrict__ have, const int32_t* __restrict__ want, int n,
                int32_t* __restrict__ st) {
-    __shared__ int32_t s_row[kMaxRows], s_cnt[kMaxRows + 1];
-    __shared__ int scratch[64];
+    // s_at: the requests' rows, then their first entries in the table; s_cnt: entries before each
+    __shared__ __align__(16) int32_t s_at[kMaxRows], s_cnt[kMaxRows + 1];
+    __shared__ int scratch[32];
+    if (gridDim.x > 1) sm100::cluster_sync();              // the others' shared memory is there from here on
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x;
-    for (int i = tid; i < n; i += kPoolThreads) s_row[i] = row[i];
-    __syncthreads();
-    for (int i = tid; i < n; i += kPoolThreads) {
-        const int r = s_row[i];
-        bool ok = r >= 0 && r < rows;
-        for (int j = 0; j < i && ok; ++j) ok = s_row[j] != r;
-        if (!ok) record_error(st, DSA_DEVERR_INDEX_RANGE, r);
-        int hi = pages_of(max(want[i], 0));
-        if (ok && hi > max_pages) {
-            record_error(st, DSA_DEVERR_INDEX_RANGE, want[i]);
-            hi = max_pages;
-        }
-        s_cnt[i] = ok ? max(0, hi - pages_of(max(have[i], 0))) : 0;
+    const bool speaks = blockIdx.x == 0;                   // every block works the same requests out, one records
+    Counts c;
+    load_counts(c, ref, num_pages, first_count());
+    int at[kPerThread], cnt[kPerThread];
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u) {
+        const int i = tid + u * kPoolThreads;
+        if (i >= n) continue;
+        s_at[i] = at[u] = row[i];
+        const int w = want[i], lo = pages_of(max(have[i], 0));
+        int hi = pages_of(max(w, 0));
+        cnt[u] = hi > max_pages ? -1 - w : max(0, hi - lo);
+        if (hi > max_pages) hi = max_pages;
+        s_cnt[i] = max(0, hi - lo);
+        at[u] = lo;
     }
     __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u) {
+        const int i = tid + u * kPoolThreads;
+        if (i >= n) continue;
+        const int r = s_at[i];
+        const bool ok = r >= 0 && r < rows && !among(s_at, i, r);   // a row's first mention counts
+        if (!ok) s_cnt[i] = 0;
+        if (speaks && !ok) record_error(st, DSA_DEVERR_INDEX_RANGE, r);
+        if (speaks && ok && cnt[u] < 0) record_error(st, DSA_DEVERR_INDEX_RANGE, -1 - cnt[u]);
+        at[u] = ok && s_cnt[i] > 0 ? r * max_pages + at[u] : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u)
+        if (tid + u * kPoolThreads < n) s_at[tid + u * kPoolThreads] = at[u];
     const int total = prefix_in_place(s_cnt, n, scratch);
     auto entry = [&](int e) {
         const int i = owner_of(s_cnt, n, e);
-        return table + (int64_t)s_row[i] * max_pages + pages_of(max(have[i], 0)) + (e - s_cnt[i]);
+        return table + s_at[i] + (e - s_cnt[i]);
     };
-    const int found = walk_free(ref, num_pages, total, scratch, [&](int rank, int64_t page) {
+    const int found = walk_free(c, ref, num_pages, total, scratch, [&](int rank, int64_t page) {
         int32_t* t = entry(rank);
         if (*t < 0) {
             *t = (int32_t)page;
             ref[page] = 1;
         }
     });
-    for (int e = found + tid; e < total; e += kPoolThreads)
-        if (*entry(e) < 0) record_error(st, DSA_DEVERR_PAGE_POOL, s_row[owner_of(s_cnt, n, e)]);
+    if (speaks)                                            // what the pool does not hold
+        for (int e = found + tid; e < total; e += kPoolThreads)
+            if (*entry(e) < 0) record_error(st, DSA_DEVERR_PAGE_POOL, row[owner_of(s_cnt, n, e)]);
 }
 
 // ---------------------------------------------------------------- fork
-// Whether mention f of a fork call counts: rows in range, the first to name its
-// dst row, and that row no source.  One thread looks at every other mention.
-__device__ __forceinline__ bool fork_counts(const int32_t* __restrict__ src, const int32_t* dst, int n, int f, int rows) {
-    const int s = src[f], d = dst[f];
-    bool ok = s >= 0 && s < rows && d >= 0 && d < rows;
-    for (int j = 0; j < n && ok; ++j) ok = src[j] != d && (j >= f || dst[j] != d);
-    return ok;
-}
-// The same with a whole block's threads (every thread gets the answer).
-__device__ __forceinline__ bool fork_counts_block(const int32_t* src, const int32_t* dst, int n, int f, int rows) {
+// A mention of a fork call counts if its rows are in range, it is the first to name
+// its dst row, and that row is no source.  Asked of a whole block, which gets the
+// answer in every thread.
+__device__ __forceinline__ bool fork_counts(const int32_t* src, const int32_t* dst, int n, int f, int rows) {
     const int s = src[f], d = dst[f];
     bool ok = s >= 0 && s < rows && d >= 0 && d < rows;
     for (int j = threadIdx.x; j < n; j += blockDim.x) ok = ok && src[j] != d && (j >= f || dst[j] != d);
@@ -328,43 +386,62 @@ __global__ void __launch_bounds__(kPoolThreads)
 fork_take_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict__ table, int rows, int max_pages,
                  const int32_t* __restrict__ src, const int32_t* __restrict__ dst, const int32_t* __restrict__ length,
                  int n, int32_t* __restrict__ st) {
-    __shared__ int32_t s_dst[kMaxRows], s_cnt[kMaxRows + 1];
-    __shared__ int scratch[64];
+    // s_cnt: the source rows, then the pages taken before each child
+    __shared__ __align__(16) int32_t s_dst[kMaxRows], s_cnt[kMaxRows + 1];
+    __shared__ int scratch[32];
+    if (gridDim.x > 1) sm100::cluster_sync();              // the others' shared memory is there from here on
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x;
-    for (int i = tid; i < n; i += kPoolThreads) s_dst[i] = dst[i];
-    __syncthreads();
+    const bool speaks = blockIdx.x == 0;                   // every block works the same children out, one records
+    Counts c;
+    load_counts(c, ref, num_pages, first_count());
     for (int i = tid; i < n; i += kPoolThreads) {
-        int take = 0;
-        if (!fork_counts(src, s_dst, n, i, rows)) {
-            record_error(st, DSA_DEVERR_INDEX_RANGE, s_dst[i]);
-        } else {
-            const int len = fork_len(length[i], max_pages);
-            if (len != length[i]) record_error(st, DSA_DEVERR_INDEX_RANGE, length[i]);
-            if (len % kPage) {
-                const int32_t pg = table[(int64_t)src[i] * max_pages + len / kPage];
-                take = pg >= 0 && pg < num_pages;
-                table[(int64_t)s_dst[i] * max_pages + len / kPage] = -1;   // until a page is found for it
-                if (pg >= num_pages) record_error(st, DSA_DEVERR_PAGE_RANGE, pg);
-            }
-        }
-        s_cnt[i] = take;
+        s_dst[i] = dst[i];
+        s_cnt[i] = src[i];
     }
     __syncthreads();
+    int take[kPerThread];
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u) {
+        const int i = tid + u * kPoolThreads;
+        take[u] = 0;
+        if (i >= n) continue;
+        const int s = s_cnt[i], d = s_dst[i];
+        if (s < 0 || s >= rows || d < 0 || d >= rows || among(s_cnt, n, d) || among(s_dst, i, d)) {
+            if (speaks) record_error(st, DSA_DEVERR_INDEX_RANGE, d);
+            continue;
+        }
+        const int len = fork_len(length[i], max_pages);
+        if (len != length[i] && speaks) record_error(st, DSA_DEVERR_INDEX_RANGE, length[i]);
+        if (len % kPage == 0) continue;
+        const int32_t pg = table[(int64_t)s * max_pages + len / kPage];
+        take[u] = pg >= 0 && pg < num_pages;
+        if (pg >= num_pages && speaks) record_error(st, DSA_DEVERR_PAGE_RANGE, pg);
+        if (!take[u] && speaks) table[(int64_t)d * max_pages + len / kPage] = -1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u)
+        if (tid + u * kPoolThreads < n) s_cnt[tid + u * kPoolThreads] = take[u];
+    __syncthreads();
     const int total = prefix_in_place(s_cnt, n, scratch);
-    const int found = walk_free(ref, num_pages, total, scratch, [&](int rank, int64_t page) {
-        const int i = owner_of(s_cnt, n, rank);
-        table[(int64_t)s_dst[i] * max_pages + fork_len(length[i], max_pages) / kPage] = (int32_t)page;
+    auto last = [&](int i) { return table + (int64_t)s_dst[i] * max_pages + fork_len(length[i], max_pages) / kPage; };
+    const int found = walk_free(c, ref, num_pages, total, scratch, [&](int rank, int64_t page) {
+        *last(owner_of(s_cnt, n, rank)) = (int32_t)page;
         ref[page] = 1;
     });
-    for (int e = found + tid; e < total; e += kPoolThreads)
-        record_error(st, DSA_DEVERR_PAGE_POOL, s_dst[owner_of(s_cnt, n, e)]);
+    if (speaks)                                            // children that the pool holds no page for
+        for (int e = found + tid; e < total; e += kPoolThreads) {
+            const int i = owner_of(s_cnt, n, e);
+            *last(i) = -1;
+            record_error(st, DSA_DEVERR_PAGE_POOL, s_dst[i]);
+        }
 }
 
 // Second step, one block per (child, job): jobs 0 .. n_caches - 1 copy the last
-// page's rows in one cache, the others share a chunk of the full pages and
-// clear the entries behind the last.
+// page's rows in one cache, the others share a chunk of the full pages and clear
+// the entries behind the last.
 __global__ void __launch_bounds__(kCopyThreads)
 fork_copy_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict__ table, int rows, int max_pages,
                  const int32_t* __restrict__ src, const int32_t* __restrict__ dst, const int32_t* __restrict__ length,
@@ -372,7 +449,7 @@ fork_copy_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restri
     pdl_wait();
     pdl_trigger();
     const int f = blockIdx.x, job = blockIdx.y, tid = threadIdx.x;
-    if (!fork_counts_block(src, dst, n, f, rows)) return;
+    if (!fork_counts(src, dst, n, f, rows)) return;
     const int len = fork_len(length[f], max_pages), full = len / kPage, part = len % kPage;
     const int32_t* ts = table + (int64_t)src[f] * max_pages;
     int32_t* td = table + (int64_t)dst[f] * max_pages;
@@ -399,6 +476,7 @@ fork_copy_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restri
     const Layout lo = layout_of(cl.kind[job]);
     const uint4* from = reinterpret_cast<const uint4*>(cl.data[job] + ps * lo.page_bytes);
     uint4* to = reinterpret_cast<uint4*>(cl.data[job] + pd * lo.page_bytes);
+    constexpr int kRowPieces = (kPage * (DSA_KV_TOKEN_BYTES / 16) + kCopyThreads - 1) / kCopyThreads;
     const int total = part * lo.row16;                     // rows are contiguous from the page's start
     uint4 v[kRowPieces];
 #pragma unroll
@@ -437,12 +515,20 @@ static CacheList list_of(const dsa_cache* caches, int32_t at, int32_t n) {
 static dsa_status check_pool(const int32_t* page_ref, int64_t num_pages, const int32_t* page_table, int32_t rows,
                              int32_t max_pages, int32_t n) {
     if (n < 0 || num_pages < 1 || rows < 1 || max_pages < 1) return DSA_ERR_INVALID_ARGUMENT;
-    if (num_pages * kPage > 0x7fffffffLL || max_pages > 0x7fffffff / kPage) return DSA_ERR_UNSUPPORTED;
+    if (num_pages * kPage > 0x7fffffffLL || (int64_t)rows * max_pages > 0x7fffffffLL || max_pages > 0x7fffffff / kPage)
+        return DSA_ERR_UNSUPPORTED;                        // 32-bit slots, table entries and lengths
     if (n == 0) return DSA_OK;
     if (!page_ref || !page_table) return DSA_ERR_INVALID_ARGUMENT;
     if (!aligned16(page_ref)) return DSA_ERR_ALIGNMENT;
     return DSA_OK;
 }
+
+// Blocks that walk the counts (one cluster): as many as have a count to look at.
+static unsigned pool_blocks(int64_t num_pages) {
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((num_pages + kStep - 1) / kStep, kPoolBlocks));
+}
+// Blocks for a request's table entries: a thread takes one each up to 64 blocks (16K entries), then goes round again.
+static unsigned entry_blocks(int32_t max_pages) { return (unsigned)std::min((max_pages + kReleaseThreads - 1) / kReleaseThreads, 64); }
 
 }  // namespace pages
 }  // namespace dsa
@@ -462,9 +548,12 @@ extern "C" dsa_status dsa_tree_commit(const int32_t* accept, int32_t width, cons
     int32_t at = 0;
     do {                                                   // 128 caches a launch; the first writes the lengths
         const int32_t n = n_caches - at < pages::kMaxCaches ? n_caches - at : pages::kMaxCaches;
-        DSA_CHECK(launch_pdl(pages::commit_kernel, dim3((unsigned)b->batch, (unsigned)(n > 0 ? n : 1)),
+        // enough blocks to fill the GPU once, but no more than caches
+        const int32_t want = std::min(std::max(1, pages::kCommitBlocks / b->batch), std::max(1, n));
+        const int32_t per = std::max(1, (n + want - 1) / want);
+        DSA_CHECK(launch_pdl(pages::commit_kernel, dim3((unsigned)b->batch, (unsigned)std::max(1, (n + per - 1) / per)),
                              dim3(pages::kCopyThreads), 0, as_stream(stream), 1, accept, (int)width, to_dev(b),
-                             pages::list_of(caches, at, n), (int)n, at == 0 ? new_seq_len : nullptr,
+                             pages::list_of(caches, at, n), (int)n, (int)per, at == 0 ? new_seq_len : nullptr,
                              at == 0 ? dev_status : nullptr));
         at += n;
     } while (at < n_caches);
@@ -477,9 +566,11 @@ extern "C" dsa_status dsa_pages_reserve(int32_t* page_ref, int64_t num_pages, in
     const dsa_status vs = pages::check_pool(page_ref, num_pages, page_table, rows, max_pages, n);
     if (vs != DSA_OK || n == 0) return vs;
     if (!row || !have_len || !want_len) return DSA_ERR_INVALID_ARGUMENT;
-    if (n > pages::kMaxRows || (int64_t)n * max_pages > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
-    DSA_CHECK(launch_pdl(pages::reserve_kernel, dim3(1), dim3(pages::kPoolThreads), 0, as_stream(stream), 1, page_ref,
-                         num_pages, page_table, (int)rows, (int)max_pages, row, have_len, want_len, (int)n, dev_status));
+    if (n > pages::kMaxRows) return DSA_ERR_UNSUPPORTED;
+    const unsigned blocks = pages::pool_blocks(num_pages);
+    DSA_CHECK(launch_pdl(pages::reserve_kernel, dim3(blocks), dim3(pages::kPoolThreads), 0, as_stream(stream), blocks,
+                         page_ref, num_pages, page_table, (int)rows, (int)max_pages, row, have_len, want_len, (int)n,
+                         dev_status));
     return DSA_OK;
 }
 
@@ -489,9 +580,7 @@ extern "C" dsa_status dsa_pages_release(int32_t* page_ref, int64_t num_pages, in
     const dsa_status vs = pages::check_pool(page_ref, num_pages, page_table, rows, max_pages, n);
     if (vs != DSA_OK || n == 0) return vs;
     if (!row || !first_page || !end_page) return DSA_ERR_INVALID_ARGUMENT;
-    // a block's threads take one entry each up to 64 blocks a request (16K entries), then go round again
-    const int chunks = (max_pages + pages::kReleaseThreads - 1) / pages::kReleaseThreads;
-    DSA_CHECK(launch_pdl(pages::release_kernel, dim3((unsigned)n, (unsigned)(chunks < 64 ? chunks : 64)),
+    DSA_CHECK(launch_pdl(pages::release_kernel, dim3((unsigned)n, pages::entry_blocks(max_pages)),
                          dim3(pages::kReleaseThreads), 0, as_stream(stream), 1, page_ref, num_pages, page_table, (int)rows,
                          (int)max_pages, row, first_page, end_page, dev_status));
     return DSA_OK;
@@ -507,8 +596,10 @@ extern "C" dsa_status dsa_pages_fork(int32_t* page_ref, int64_t num_pages, int32
     if (vs != DSA_OK || n == 0) return vs;
     if (!src_row || !dst_row || !length) return DSA_ERR_INVALID_ARGUMENT;
     if (n > pages::kMaxRows) return DSA_ERR_UNSUPPORTED;
-    DSA_CHECK(launch_pdl(pages::fork_take_kernel, dim3(1), dim3(pages::kPoolThreads), 0, as_stream(stream), 1, page_ref,
-                         num_pages, page_table, (int)rows, (int)max_pages, src_row, dst_row, length, (int)n, dev_status));
+    const unsigned blocks = pages::pool_blocks(num_pages);
+    DSA_CHECK(launch_pdl(pages::fork_take_kernel, dim3(blocks), dim3(pages::kPoolThreads), 0, as_stream(stream), blocks,
+                         page_ref, num_pages, page_table, (int)rows, (int)max_pages, src_row, dst_row, length, (int)n,
+                         dev_status));
     const int chunks = (max_pages + pages::kCopyThreads - 1) / pages::kCopyThreads;
     int32_t at = 0;
     do {                                                   // the first launch shares the full pages too

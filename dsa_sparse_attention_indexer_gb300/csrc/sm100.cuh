@@ -241,6 +241,9 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // Bulk copy from this CTA's shared memory to a cluster peer's; dst and bar are
 // shared::cluster addresses (mapa_shared), the peer's barrier receives the bytes.
 // Addresses 16-byte aligned, bytes a multiple of 16.
