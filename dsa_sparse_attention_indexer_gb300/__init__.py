@@ -180,7 +180,7 @@ def _check(fn: str, code: int):
 
 
 def _ptr(t):
-    return None if t is None else c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, device=None):
@@ -188,18 +188,23 @@ def _stream(stream, device=None):
     `device`).  A stream on another device than the call's tensors is refused:
     the kernels would run there with this device's pointers."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        stream = torch.cuda.current_stream(None if device is None else device.index)
     elif device is not None and stream.device != torch.device(device):
         raise ValueError(f"stream is on {stream.device}, the call's tensors on {device}")
-    return c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _call(fn: str, device, *args):
     """Run C entry point `fn` with `device` current, so that the library's
     per-device set-up, its device queries and a default stream all refer to the
     device that holds the call's tensors."""
-    with torch.cuda.device(device):
-        _check(fn, getattr(lib(), fn)(*args))
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == device.index:        # switching costs more than a small call's launch
+        code = f(*args)
+    else:
+        with torch.cuda.device(device):
+            code = f(*args)
+    _check(fn, code)
 
 
 def _need(t: torch.Tensor, dtype, name: str, device=None, numel=None):
@@ -215,7 +220,7 @@ def _need(t: torch.Tensor, dtype, name: str, device=None, numel=None):
         raise ValueError(f"{name} must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
-    if device is not None and t.device != torch.device(device):
+    if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
     if numel is not None and t.numel() < numel:
         raise ValueError(f"{name} holds {t.numel()} elements, the call needs {numel}")

@@ -70,7 +70,7 @@ struct Args {
     void* out;
     int out_f32;
     float* lse;
-    float* part_o;              // [2 G, 64, 512]: unnormalised outputs of cut rows, two pieces per share
+    float* part_o;              // [2 G, 16, 512, 4]: unnormalised outputs of cut rows, two pieces per share, four heads side by side
     float2* part_ml;            // [2 G, 64]: reference (log2 units), sum
     Meta* meta;          // [G]
     int32_t* st;
@@ -101,21 +101,35 @@ struct Row {
 // that every row of a request is written; rows behind the last request have none.
 __device__ __forceinline__ Row row_view(const BatchDev& b, const View& v, int64_t row, int32_t* st) {
     Row w = {};
-    if (row >= b.q_start[b.batch]) return w;
-    w.r = row_request(b.q_start, b.batch, row);
-    const int qs = b.q_start[w.r], qn = b.q_start[w.r + 1] - qs;
+    // In a batch of equal query lengths the row's request is this one.  Its loads depend on
+    // nothing and are one round trip; any other batch searches.
+    w.r = min(b.batch - 1, (int)(((float)row + 0.5f) * (float)b.batch / (float)b.total_q));
+    const int rows = b.q_start[b.batch];
+    int qs = b.q_start[w.r], qe = b.q_start[w.r + 1], len = b.seq_len[w.r];
+    const uint64_t bits = v.tree ? v.tree[row] : 0;
+    if (row >= rows) {
+        w.r = 0;
+        return w;
+    }
+    if (row < qs || row >= qe) {
+        w.r = row_request(b.q_start, b.batch, row);
+        qs = b.q_start[w.r];
+        qe = b.q_start[w.r + 1];
+        len = b.seq_len[w.r];
+    }
+    const int qn = qe - qs;
     const int64_t room = (int64_t)b.max_pages * kPage;
-    int L = b.seq_len[w.r];
+    int L = len;
     if (L > room) {
         record_error(st, DSA_DEVERR_INDEX_RANGE, L);
         L = (int)room;
     }
-    w.prefix = b.seq_len[w.r] - qn;
+    w.prefix = len - qn;
     w.pages = 1;
     if (L <= 0 || w.prefix < 0) return w;
     if (v.tree) {
         const int known = min(qn, 64);
-        w.mask = v.tree[row] & (known >= 64 ? ~0ull : (1ull << known) - 1);
+        w.mask = bits & (known >= 64 ? ~0ull : (1ull << known) - 1);
         w.end = min(w.prefix, L);
         const int64_t last = w.mask ? (int64_t)w.prefix + 64 - __clzll((long long)w.mask) : w.end;
         if (last > L) w.mask = L > w.prefix ? w.mask & ((1ull << (L - w.prefix)) - 1) : 0;
@@ -186,8 +200,7 @@ struct Misc {
     Tile tile[kAhead];          // by tile of the share, modulo kAhead
     uint32_t qmax[kWorkWarps];  // per warp: largest bf16 magnitude of the row's q
     int64_t scratch[kWorkWarps];
-    int64_t total;              // tiles of the whole batch
-    int32_t row0, tile0;        // where this CTA's share begins
+    int32_t mine, row0, tile0;  // tiles of this CTA's share, and where it begins
 };
 static_assert(sizeof(Misc) <= 512, "misc block");
 
@@ -204,8 +217,8 @@ __device__ __forceinline__ void work_sync() { bar_sync<kWorkBar, kWorkThreads>()
 
 __device__ __forceinline__ int tiles_of(const Row& w) { return (w.pages + 1) >> 1; }
 
-// Counts the tiles of all rows (the workers' threads, consecutive rows each)
-// and finds where share g of G begins.  Returns the share's tiles.
+// Counts the tiles of all rows (the workers' threads, consecutive rows each) and
+// finds this CTA's share of them.
 __device__ __noinline__ void plan_share(const Args& a, Misc* misc, int tid) {
     const int64_t T = a.b.total_q;
     const int64_t per = (T + kWorkThreads - 1) / kWorkThreads;
@@ -228,21 +241,21 @@ __device__ __noinline__ void plan_share(const Args& a, Misc* misc, int tid) {
         all += tot[w];
     }
     before += x - mine;
-    if (tid == 0) misc->total = all;
-    const int64_t G = min((int64_t)gridDim.x, all);
-    if ((int64_t)blockIdx.x < G) {
-        int64_t at = (int64_t)blockIdx.x * all / G;
-        if (at >= before && at < before + mine) {
-            at -= before;
-            int64_t r = r0;
-            for (;; ++r) {
-                const int n = tiles_of(row_view(a.b, a.view, r, nullptr));
-                if (at < n) break;
-                at -= n;
-            }
-            misc->row0 = (int32_t)r;
-            misc->tile0 = (int32_t)at;
+    // shares of n or n + 1 tiles, the longer ones first
+    const int64_t n = all >> 32 ? all / gridDim.x : (uint32_t)all / gridDim.x;
+    const int64_t longer = all - n * gridDim.x, g = blockIdx.x;
+    if (tid == 0) misc->mine = (int32_t)n + (g < longer);  // the host bounds it
+    int64_t at = g * n + min(g, longer);
+    if (at >= before && at < before + mine) {
+        at -= before;
+        int64_t r = r0;
+        for (; r + 1 < r1; ++r) {
+            const int t = tiles_of(row_view(a.b, a.view, r, nullptr));
+            if (at < t) break;
+            at -= t;
         }
+        misc->row0 = (int32_t)r;
+        misc->tile0 = (int32_t)at;
     }
 }
 
@@ -316,19 +329,25 @@ dense_mla_kernel(const __grid_constant__ Args a) {
         tmem_alloc(&misc->tmem_base, 512);
         tmem_relinquish();
     }
-    pdl_wait();
-    if (tid < kWorkThreads) plan_share(a, misc, tid);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = misc->tmem_base;
-    const int64_t g = blockIdx.x;
-    const int64_t N = misc->total, G = min((int64_t)gridDim.x, N);
-    const int row_begin = misc->row0;
-    const int tile_begin = misc->tile0;
-    const int n_mine = g < G ? (int)((g + 1) * N / G - g * N / G) : 0;   // the host bounds it
-    if (tid == 0) a.meta[g] = n_mine > 0 ? Meta{row_begin, tile_begin > 0 ? 1 : 0} : Meta{-1, 0};
-
+    uint32_t tmem = 0;
+    int row_begin = 0, tile_begin = 0, n_mine = 0;         // this CTA's share
+    auto share = [&]() {                                   // every thread, the workers behind plan_share
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tmem = misc->tmem_base;
+        row_begin = misc->row0;
+        tile_begin = misc->tile0;
+        n_mine = misc->mine;
+        if (tid == 0) a.meta[blockIdx.x] = n_mine > 0 ? Meta{row_begin, tile_begin > 0 ? 1 : 0} : Meta{-1, 0};
+    };
+    auto start_worker = [&]() {
+        more_registers<kWorkRegs>();
+        pdl_wait();
+        plan_share(a, misc, tid);
+        share();
+        return n_mine > 0;
+    };
     auto timeout = [&](int where) {
         record_error(a.st, DSA_DEVERR_TIMEOUT, where);
         *abort_flag = 1;
@@ -336,6 +355,8 @@ dense_mla_kernel(const __grid_constant__ Args a) {
 
     if (warp >= kMmaWarp) {
         fewer_registers<kMmaRegs>();
+        pdl_wait();
+        share();
         if (warp == kMmaWarp && n_mine > 0) {
             // ============================================================ MMA issue (lane 0; the warp joins the votes)
             const uint32_t kv0 = smem_addr(smem + kOffKV), q0 = smem_addr(smem + kOffQ), p0 = smem_addr(smem + kOffP);
@@ -433,9 +454,8 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             if (!ok && lane == 0) timeout(65);
         }
         __syncwarp();
-    } else if (n_mine > 0) {
+    } else if (start_worker()) {
         // ================================================================ workers
-        more_registers<kWorkRegs>();
         // ---- softmax: warp w reads TMEM lane quarter w % 4 (token / latent row st) and
         // heads [16 hh, 16 hh + 16), hh = w / 4
         const int q4 = warp & 3, hh = warp >> 2;
@@ -560,21 +580,25 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             if (more) fetch(rope, 528, 0u);
             if (bad | __vcmpgtu2(rope_max, 0x477f477fu)) record_error(a.st, DSA_DEVERR_FP16_RANGE, lane);
         };
-        // The row's Q (fp16, K-major, 128-byte swizzle): every S^T issued so far has completed,
-        // so its place is free.  Returns the softmax scale in log2 units times 2^-kq of the Q.
+        // The row's Q (fp16, K-major, 128-byte swizzle) in two steps: its bf16 on the way into
+        // the place of the last one, which every S^T has read by then, and, a softmax later,
+        // the same pieces as fp16.  put_q returns the softmax scale in log2 units times 2^-kq
+        // of the Q.  Eight threads a head, a thread one 16-byte piece of each K-block.
+        static_assert(64 * 8 == kWorkThreads, "a thread has piece tid % 8 of head tid / 8");
+        uint8_t* const q_at = smem + kOffQ + (tid >> 3) * 128 + (((tid ^ tid >> 3) & 7) * 16);   // + 8192 per K-block
+        auto fetch_q = [&](int q_row) {
+            const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (int64_t)q_row * (64 * 576)) + (tid >> 3) * 72 + (tid & 7);
+#pragma unroll
+            for (int u = 0; u < 9; ++u) cp_async_16(smem_addr(q_at) + u * 8192, qrow + u * 8);
+        };
         auto put_q = [&](int q_row) -> float {
-            static_assert(64 * 72 == 9 * kWorkThreads, "nine 16-byte pieces of q per thread");
-            const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (int64_t)q_row * (64 * 576));
+            cp_async_wait_all();
             uint32_t mx = 0;                               // two bf16 magnitudes, compared as integers
-#pragma unroll 1
-            for (int u0 = 0; u0 < 9; u0 += 3) {
-                uint4 qv[3];
 #pragma unroll
-                for (int u = 0; u < 3; ++u) qv[u] = __ldg(qrow + tid + (u0 + u) * kWorkThreads);
-#pragma unroll
-                for (int u = 0; u < 3; ++u)
-                    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(qv[u].x & 0x7fff7fffu, qv[u].y & 0x7fff7fffu),
-                                               __vmaxu2(qv[u].z & 0x7fff7fffu, qv[u].w & 0x7fff7fffu)));
+            for (int u = 0; u < 9; ++u) {
+                const uint4 qv = *reinterpret_cast<const uint4*>(q_at + u * 8192);
+                mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(qv.x & 0x7fff7fffu, qv.y & 0x7fff7fffu),
+                                           __vmaxu2(qv.z & 0x7fff7fffu, qv.w & 0x7fff7fffu)));
             }
             mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
             if (lane == 0) misc->qmax[warp] = mx;
@@ -583,20 +607,12 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             const int eq = mx == 0 ? 14 : (int)(mx >> 7) - 127;
             const int kq = min(126, max(-126, 14 - eq));
             const float sc = __int_as_float((127 + kq) << 23);
-#pragma unroll 1
-            for (int u0 = 0; u0 < 9; u0 += 3) {
-                uint4 qv[3];
 #pragma unroll
-                for (int u = 0; u < 3; ++u) qv[u] = __ldg(qrow + tid + (u0 + u) * kWorkThreads);
-#pragma unroll
-                for (int u = 0; u < 3; ++u) {
-                    const int c = tid + (u0 + u) * kWorkThreads;
-                    const int h = c / 72, cq = c % 72;
-                    const int blk = cq >> 3, ch = cq & 7;
-                    *reinterpret_cast<uint4*>(smem + kOffQ + blk * 8192 + h * 128 + ((ch ^ (h & 7)) * 16)) =
-                        make_uint4(bf16x2_scaled_to_h2(qv[u].x, sc), bf16x2_scaled_to_h2(qv[u].y, sc),
-                                   bf16x2_scaled_to_h2(qv[u].z, sc), bf16x2_scaled_to_h2(qv[u].w, sc));
-                }
+            for (int u = 0; u < 9; ++u) {
+                uint4* at = reinterpret_cast<uint4*>(q_at + u * 8192);
+                const uint4 qv = *at;
+                *at = make_uint4(bf16x2_scaled_to_h2(qv.x, sc), bf16x2_scaled_to_h2(qv.y, sc), bf16x2_scaled_to_h2(qv.z, sc),
+                                 bf16x2_scaled_to_h2(qv.w, sc));
             }
             if (tid == 0 && mx >= 0x7f80u) record_error(a.st, DSA_DEVERR_FP16_RANGE, q_row);   // inf / NaN in q
             fence_proxy_async_smem();
@@ -610,13 +626,14 @@ dense_mla_kernel(const __grid_constant__ Args a) {
         for (int c = 0; c < kHeads; ++c) lsum[c] = 0.f;
         if (tid < 32) neg_inf[tid] = -INFINITY;
         if (tid < 64) neg_ref[tid] = kNoRef;               // seen by all behind put_q's barrier
+        fetch_q(row_begin);
         aim(0);
         follow();
         fetch(scv, 512 - c8 * 16, 0x3f800000u);
         fetch(raw[0], 0, 0u);
         fetch(raw[1], 128, 0u);
         fetch(rope, 528, 0u);
-        float sl2 = put_q((int)(row_next >> 3));
+        float sl2 = put_q(row_begin);
         put_tile(0);
         int piece = 0;
         for (;; ++n) {
@@ -659,6 +676,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             };
             float v[kHeads];
             tc_fence_after();
+            if (n + 1 < n_mine && (row_next & T_FIRST)) fetch_q((int)(row_next >> 3));
             load_s(v);
             write_p(v);
             // ---- a score above its head's reference by more than 2^kTau (P above 2^(kTau + kShift))
@@ -721,11 +739,16 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             if (!(done & T_LAST)) continue;
             // ---- the piece's output: O^T is final when its last P.V has completed
             ok = wait_ab(&bars[B_PV3], (uint32_t)(n & 1), abort_flag) && ok;
+            if (n + 1 == n_mine) pdl_trigger();             // the merge's blocks may take their places
             xreduce16<false>(lsum, lane);
             if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];
             work_sync();                                    // a timeout here is seen by the next vote, or is the end
             tc_fence_after();
-            if (tid < 64) l_acc[tid] = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
+            if (tid < 64) {
+                const float l = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
+                l_acc[tid] = l;
+                alpha[tid] = l > 0.f ? 1.f / l : 0.f;
+            }
             work_sync();
             const int64_t unit = 2 * (int64_t)blockIdx.x + (piece++ == 0 ? 0 : 1);   // a share's first piece, or its last
 #pragma unroll 1
@@ -734,19 +757,43 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                 tmem_ld_32x32b_x16(lane_addr + kColO + mb * 64 + hh * kHeads, o);
                 tmem_ld_wait();
                 const int d = mb * 128 + st;                           // latent dim of this TMEM lane
+                if (!(done & T_WHOLE)) {                               // a warp stores 32 dims of four heads at a time
+                    float4* to = reinterpret_cast<float4*>(a.part_o) + (unit * 16 + hh * (kHeads / 4)) * 512 + d;
 #pragma unroll
-                for (int c = 0; c < kHeads; ++c) {                     // a warp stores 32 consecutive dims
-                    const int h = hh * kHeads + c;
-                    const float ov = __uint_as_float(o[c]);
-                    if (done & T_WHOLE) {
-                        const float l = l_acc[h];
-                        const float val = l > 0.f ? ov / l : 0.f;
-                        const int64_t oi = ((int64_t)(done >> 3) * 64 + h) * 512 + d;
-                        if (a.out_f32) static_cast<float*>(a.out)[oi] = val;
-                        else static_cast<__nv_bfloat16*>(a.out)[oi] = __float2bfloat16_rn(val);
-                    } else {
-                        a.part_o[(unit * 64 + h) * 512 + d] = ov;
-                    }
+                    for (int c = 0; c < kHeads; c += 4)
+                        to[c / 4 * 512] = make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
+                                                      __uint_as_float(o[c + 3]));
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < kHeads; ++c) {
+                    const float inv = alpha[hh * kHeads + c];
+                    o[c] = inv > 0.f ? __float_as_uint(__uint_as_float(o[c]) * inv) : 0u;
+                }
+                const int64_t at = ((int64_t)(done >> 3) * 64 + hh * kHeads) * 512;
+                if (a.out_f32) {
+                    float* to = static_cast<float*>(a.out) + at + d;
+#pragma unroll
+                    for (int c = 0; c < kHeads; ++c) to[c * 512] = __uint_as_float(o[c]);
+                    continue;
+                }
+                // bf16: four lanes turn their 16 heads x 1 dim into 4 heads x 4 dims each, so
+                // that a store is 8 bytes (2 bytes a store were bound by their number)
+                uint32_t x[8], y[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) x[c] = pack_bf16x2(__uint_as_float(o[c]), __uint_as_float(o[c + 8]));   // heads c, c + 8
+                const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {                          // dims of an even lane and the next: heads 0-7 | 8-15
+                    const uint32_t z = __shfl_xor_sync(0xffffffffu, x[c], 1);
+                    y[c] = odd ? __byte_perm(z, x[c], 0x7632) : __byte_perm(x[c], z, 0x5410);
+                }
+                uint16_t* to = static_cast<uint16_t*>(a.out) + at + (mb * 128 + q4 * 32 + (lane & ~3)) +
+                               ((odd ? 8 : 0) + (high ? 4 : 0)) * 512;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {                          // dims of four lanes: heads 0-3 | 4-7 of those
+                    const uint32_t z = __shfl_xor_sync(0xffffffffu, high ? y[c] : y[c + 4], 2);
+                    *reinterpret_cast<uint2*>(to + c * 512) = high ? make_uint2(z, y[c + 4]) : make_uint2(y[c], z);
                 }
             }
             tc_fence_before();
@@ -768,7 +815,6 @@ dense_mla_kernel(const __grid_constant__ Args a) {
     }
     tc_fence_before();
     __syncthreads();
-    pdl_trigger();
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -776,91 +822,111 @@ dense_mla_kernel(const __grid_constant__ Args a) {
 }
 
 // ---------------------------------------------------------------- merge
-// Block (x, y): share boundary x + 1 and its heads y, y + gridDim.y, ..  The
-// boundary's row was cut when share x + 1 begins inside it; the first such
-// boundary of a row merges its pieces.  Per head over the pieces u:
+// Blocks of a row that was cut, four heads and 128 dims at a time.  Where there are
+// more shares than rows, block x looks after row x; else after the row that share
+// x + 1 begins inside, if it is the first to do so.  Per head over the pieces u:
 //   M = max m_u,  w_u = 2^(m_u - M),  L = sum w_u l_u,
 //   out = sum_u w_u O_u / L,  lse = (M + log2 L) ln 2.
-constexpr int kMergeThreads = 128;                         // 512 dims, four per thread
-constexpr int kMaxPieces = 1024;
+// Every warp works the weights out by itself, eight pieces x four heads a step, the
+// outputs of eight pieces in flight meanwhile: two round trips behind the shares'
+// beginnings.
+constexpr int kMergeThreads = 128;
 
-__global__ void __launch_bounds__(kMergeThreads)
-dense_merge_kernel(Args a, int G) {
-    __shared__ float w_s[kMaxPieces];
-    __shared__ float red_s[8];
-    __shared__ int np_s;
+__global__ void __launch_bounds__(kMergeThreads, 4)
+dense_merge_kernel(const __grid_constant__ Args a, int G, int by_row) {
+    __shared__ int32_t s_first[4], s_more[4], s_whole[4];
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int bd = blockIdx.x + 1;
-    const Meta me = a.meta[bd], prev = a.meta[bd - 1];
-    if (!me.inside || (prev.inside && prev.row == me.row)) return;
-    const int64_t row = me.row;
-    // the row's pieces: the last piece of share bd - 1, then the first ones of bd, bd + 1, .. while they begin inside the row
-    if (tid == 0) np_s = 1 + G - bd;
-    __syncthreads();
-    for (int i = tid; bd + i < G; i += kMergeThreads) {
-        const Meta m = a.meta[bd + i];
-        if (!m.inside || m.row != me.row) {
-            atomicMin(&np_s, 1 + i);
-            break;
+    int row = blockIdx.x;
+    if (!by_row) {
+        const Meta me = a.meta[blockIdx.x + 1], prev = a.meta[blockIdx.x];
+        if (!me.inside || (prev.inside && prev.row == me.row)) return;
+        row = me.row;
+    }
+    // the shares that begin inside the row follow one another; the row's first piece is in
+    // the one before them: its first if it begins with the row, else its last
+    int first = INT32_MAX, more = 0, begins = 0;
+    for (int i = tid; i < G; i += kMergeThreads) {
+        const Meta m = a.meta[i];
+        if (m.row != row) continue;
+        if (m.inside) {
+            first = min(first, i);
+            ++more;
+        } else {
+            begins = 1;
         }
     }
+    first = __reduce_min_sync(0xffffffffu, first);
+    more = __reduce_add_sync(0xffffffffu, more);
+    begins = __reduce_or_sync(0xffffffffu, begins);
+    if (lane == 0) {
+        s_first[warp] = first;
+        s_more[warp] = more;
+        s_whole[warp] = begins;
+    }
     __syncthreads();
-    const int np = np_s;
-    const int64_t unit0 = 2 * (int64_t)(bd - 1) + (prev.row == me.row ? 0 : 1);
-    for (int h = blockIdx.y; h < 64; h += gridDim.y) {
-        auto unit = [&](int i) { return i == 0 ? unit0 : 2 * (int64_t)(bd - 1 + i); };
-        float M = -INFINITY;
-        for (int i = tid; i < np; i += kMergeThreads) {
-            const float2 ml = __ldcg(a.part_ml + unit(i) * 64 + h);
-            if (ml.y > 0.f) M = fmaxf(M, ml.x);
-        }
-        M = warp_max(M);
-        if (lane == 0) red_s[warp] = M;
-        __syncthreads();
-        M = fmaxf(fmaxf(red_s[0], red_s[1]), fmaxf(red_s[2], red_s[3]));
-        float L = 0.f;
-        for (int i = tid; i < np; i += kMergeThreads) {
-            const float2 ml = __ldcg(a.part_ml + unit(i) * 64 + h);
-            const float w = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
-            w_s[i] = w;
-            L += w * ml.y;
-        }
-        L = warp_sum(L);
-        if (lane == 0) red_s[4 + warp] = L;
-        __syncthreads();
-        L = red_s[4] + red_s[5] + red_s[6] + red_s[7];
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q0 = 0; q0 < np; q0 += 8) {                // eight pieces' loads in flight
-            float4 v[8];
+    const int np = 1 + s_more[0] + s_more[1] + s_more[2] + s_more[3];
+    if (np == 1) return;
+    first = min(min(s_first[0], s_first[1]), min(s_first[2], s_first[3]));
+    const int64_t unit0 = 2 * (int64_t)(first - 1) + (s_whole[0] | s_whole[1] | s_whole[2] | s_whole[3] ? 0 : 1);
+    auto unit = [&](int i) { return i == 0 ? unit0 : 2 * (int64_t)(first - 1 + i); };
+    for (int part = blockIdx.y; part < 64; part += gridDim.y) {
+        const int h0 = part >> 2 << 2, d = (part & 3) * kMergeThreads + tid;   // heads h0 .. h0 + 3, dim d
+        float4 v[8], next[8];
+        auto load_o = [&](float4 (&v)[8], int q0) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] = q0 + j < np ? __ldcg(reinterpret_cast<const float4*>(a.part_o + (unit(q0 + j) * 64 + h) * 512) + tid)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q0 + j < np) v[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (unit(q0 + j) * 16 + (h0 >> 2)) * 512 + d);
+        };
+        // lane: piece q0 + lane / 4, head h0 + lane % 4; {-inf, 0} of a piece that saw nothing
+        auto load_ml = [&](int q0) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (q0 + (lane >> 2) < np) ml = __ldcg(a.part_ml + unit(q0 + (lane >> 2)) * 64 + h0 + (lane & 3));
+            if (!(ml.y > 0.f)) ml = make_float2(-INFINITY, 0.f);
+            return ml;
+        };
+        load_o(v, 0);
+        float2 ml = load_ml(0), ml_next;
+        float M = ml.x;
+#pragma unroll 4
+        for (int q0 = 8; q0 < np; q0 += 8) M = fmaxf(M, load_ml(q0).x);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q0 = 0; q0 < np; q0 += 8) {
+            load_o(next, q0 + 8);
+            ml_next = load_ml(q0 + 8);
+            const float w = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
+            L += w * ml.y;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float w = q0 + j < np ? w_s[q0 + j] : 0.f;
-                if (w == 0.f) continue;                    // a piece that saw nothing holds no numbers
-                acc.x += w * v[j].x;
-                acc.y += w * v[j].y;
-                acc.z += w * v[j].z;
-                acc.w += w * v[j].w;
+                if (q0 + j >= np) break;
+                const float w0 = __shfl_sync(0xffffffffu, w, 4 * j), w1 = __shfl_sync(0xffffffffu, w, 4 * j + 1);
+                const float w2 = __shfl_sync(0xffffffffu, w, 4 * j + 2), w3 = __shfl_sync(0xffffffffu, w, 4 * j + 3);
+                if (w0 != 0.f) acc.x = fmaf(w0, v[j].x, acc.x);   // a piece that saw nothing holds no numbers
+                if (w1 != 0.f) acc.y = fmaf(w1, v[j].y, acc.y);
+                if (w2 != 0.f) acc.z = fmaf(w2, v[j].z, acc.z);
+                if (w3 != 0.f) acc.w = fmaf(w3, v[j].w, acc.w);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = next[j];
+            ml = ml_next;
         }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        const int64_t o = (row * 64 + h) * 512 + tid * 4;
-        if (a.out_f32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        } else {
-            __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            __nv_bfloat162 hi2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) =
-                make_uint2(*reinterpret_cast<uint32_t*>(&lo2), *reinterpret_cast<uint32_t*>(&hi2));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        const float inv = L > 0.f ? 1.f / L : 0.f;         // lane % 4: head
+        const int64_t at = ((int64_t)row * 64 + h0) * 512 + d;
+        const float x[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float val = x[e] * __shfl_sync(0xffffffffu, inv, e);
+            if (a.out_f32) static_cast<float*>(a.out)[at + e * 512] = val;
+            else static_cast<__nv_bfloat16*>(a.out)[at + e * 512] = __float2bfloat16_rn(val);
         }
-        if (a.lse && tid == 0) a.lse[row * 64 + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
-        __syncthreads();                                    // w_s and red_s may be reused
+        if (a.lse && (part & 3) == 0 && tid < 4)
+            a.lse[(int64_t)row * 64 + h0 + tid] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     }
 }
 
@@ -908,10 +974,9 @@ static dsa_status launch(const void* q, const uint8_t* kv, const dsa_batch* b, V
     const cudaStream_t s = as_stream(stream);
     DSA_CHECK(launch_pdl(dense_mla_kernel, dim3((unsigned)G), dim3(kThreads), kSmemAlloc, s, 1, a));
     if (G > 1) {
-        // boundaries x heads: a block per head where few rows can be cut (each may have many
-        // pieces), four heads a block where many can (most blocks then have nothing to merge)
-        const unsigned cuts = (unsigned)(G - 1);
-        DSA_CHECK(launch_pdl(dense_merge_kernel, dim3(cuts, b->total_q < 32 ? 64 : 16), dim3(kMergeThreads), 0, s, 1, a, G));
+        const bool by_row = b->total_q < G;
+        DSA_CHECK(launch_pdl(dense_merge_kernel, dim3(by_row ? (unsigned)b->total_q : (unsigned)(G - 1), b->total_q < 32 ? 64 : 16),
+                             dim3(kMergeThreads), 0, s, 1, a, G, (int)by_row));
     }
     return DSA_OK;
 }

@@ -51,7 +51,11 @@ __device__ __forceinline__ Layout layout_of(int kind) {
 // 128 requests x 99 caches took 45 us.)
 constexpr int kCommitWarps = kCopyThreads / 32;
 constexpr int kRowsPerWarp = kMaxAccept / kCommitWarps;    // of a round
-constexpr int kCommitBlocks = 1216;                        // about one resident wave of blocks
+// Blocks of a launch: three times what is resident (two a SM).  A block with more
+// caches takes more rounds one after another, a block with fewer repeats the chain:
+// 128 requests x 99 caches took 32.8 / 24.2 / 20.9 / 21.6 / 22.9 us with 304 / 608 /
+// 912 / 1216 / 2432 blocks.
+constexpr int kCommitBlocks = 912;
 
 __global__ void __launch_bounds__(kCopyThreads)
 commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheList cl, int n_caches, int per_block,
@@ -548,7 +552,6 @@ extern "C" dsa_status dsa_tree_commit(const int32_t* accept, int32_t width, cons
     int32_t at = 0;
     do {                                                   // 128 caches a launch; the first writes the lengths
         const int32_t n = n_caches - at < pages::kMaxCaches ? n_caches - at : pages::kMaxCaches;
-        // enough blocks to fill the GPU once, but no more than caches
         const int32_t want = std::min(std::max(1, pages::kCommitBlocks / b->batch), std::max(1, n));
         const int32_t per = std::max(1, (n + want - 1) / want);
         DSA_CHECK(launch_pdl(pages::commit_kernel, dim3((unsigned)b->batch, (unsigned)std::max(1, (n + per - 1) / per)),
