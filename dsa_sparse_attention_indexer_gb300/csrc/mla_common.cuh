@@ -42,10 +42,13 @@ __device__ __forceinline__ uint4 ldg_pinned(const uint4* p) {
     return r;
 }
 
-// 16 bytes from global to shared memory without a register; the thread that issued
-// them sees them after cp_async_wait_all.
+// 16 (4) bytes from global to shared memory without a register; the thread that
+// issued them sees them after cp_async_wait_all.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ float ldg_pinned(const float* p) {

@@ -9,6 +9,7 @@
 
 #include "dsa_internal.cuh"
 #include "indexer_common.cuh"
+#include "mla_common.cuh"
 #include "select_common.cuh"
 #include "sm100.cuh"
 
@@ -45,16 +46,14 @@ __device__ __forceinline__ Layout layout_of(int kind) {
 // One block per (request, run of caches): the moves are worked out once, by a chain
 // of dependent loads (lengths, list, page table), and then applied cache by cache.
 // A warp moves one row at a time, 41 (KV) or 8 / 4 (index-K) pieces of 16 bytes; a
-// round reads up to 64 rows of as many whole caches as they make into registers, all
-// loads in flight, before the barrier and writes them after it, so a row may be
+// round reads up to 144 rows of as many whole caches as they make into shared memory,
+// all in flight at once, before the barrier and writes them after it, so a row may be
 // another row's target.  (A block per cache spent most of its time on the chain:
 // 128 requests x 99 caches took 45 us.)
 constexpr int kCommitWarps = kCopyThreads / 32;
-constexpr int kRowsPerWarp = kMaxAccept / kCommitWarps;    // of a round
-// Blocks of a launch: three times what is resident (two a SM).  A block with more
-// caches takes more rounds one after another, a block with fewer repeats the chain:
-// 128 requests x 99 caches took 32.8 / 24.2 / 20.9 / 21.6 / 22.9 us with 304 / 608 /
-// 912 / 1216 / 2432 blocks.
+constexpr int kCommitRows = 144;                           // of a round: 94 KB, two blocks a SM
+constexpr int kCommitSmem = kCommitRows * DSA_KV_TOKEN_BYTES;
+static_assert(DSA_KV_TOKEN_BYTES >= DSA_INDEX_HEAD_DIM + 4, "an index key and its scale word take a row's place");
 constexpr int kCommitBlocks = 912;
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -123,38 +122,33 @@ commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheLi
     __syncthreads();
     const int n = s_n;
     if (n == 0) return;
+    extern __shared__ __align__(16) uint8_t smem[];
     const int c_end = min(n_caches, (int)(blockIdx.y + 1) * per_block);
-    const int round = kMaxAccept / n;                      // caches of a round, at least one
+    const int round = kCommitRows / n;                     // caches of a round, at least two
     for (int c0 = blockIdx.y * per_block; c0 < c_end; c0 += round) {
         const int rows = min(round, c_end - c0) * n;
-        uint4 v0[kRowsPerWarp], v1[kRowsPerWarp];          // a lane's pieces of a row: lane and, in KV rows, 32 + lane
-        uint32_t word[kRowsPerWarp];                       // an index key's scale word
-#pragma unroll
-        for (int u = 0; u < kRowsPerWarp; ++u) {
-            const int x = u * kCommitWarps + warp;
-            if (x < rows) {
-                const int c = c0 + x / n, s = s_src[x % n];
-                const Layout lo = layout_of(cl.kind[c]);
-                const uint8_t* page = cl.data[c] + (int64_t)(s / kPage) * lo.page_bytes;
-                const uint4* from = reinterpret_cast<const uint4*>(page) + (s % kPage) * lo.row16;
-                if (lane < lo.row16) v0[u] = from[lane];
-                if (lane + 32 < lo.row16) v1[u] = from[lane + 32];
-                if (lo.scale_at && lane == 0) word[u] = *reinterpret_cast<const uint32_t*>(page + lo.scale_at + (s % kPage) * 4);
-            }
+        for (int x = warp; x < rows; x += kCommitWarps) {
+            const int c = c0 + x / n, s = s_src[x % n];
+            const Layout lo = layout_of(cl.kind[c]);
+            const uint8_t* page = cl.data[c] + (int64_t)(s / kPage) * lo.page_bytes;
+            const uint4* from = reinterpret_cast<const uint4*>(page) + (s % kPage) * lo.row16;
+            const uint32_t to = sm100::smem_addr(smem) + x * DSA_KV_TOKEN_BYTES;
+            if (lane < lo.row16) mlc::cp_async_16(to + lane * 16, from + lane);
+            if (lane + 32 < lo.row16) mlc::cp_async_16(to + (lane + 32) * 16, from + lane + 32);
+            if (lo.scale_at && lane == 0) mlc::cp_async_4(to + lo.row16 * 16, page + lo.scale_at + (s % kPage) * 4);
         }
+        mlc::cp_async_wait_all();                          // a lane stores what it has read
         __syncthreads();                                   // every source row of these caches has been read
-#pragma unroll
-        for (int u = 0; u < kRowsPerWarp; ++u) {
-            const int x = u * kCommitWarps + warp;
-            if (x < rows) {
-                const int c = c0 + x / n, d = s_dst[x % n];
-                const Layout lo = layout_of(cl.kind[c]);
-                uint8_t* page = cl.data[c] + (int64_t)(d / kPage) * lo.page_bytes;
-                uint4* to = reinterpret_cast<uint4*>(page) + (d % kPage) * lo.row16;
-                if (lane < lo.row16) to[lane] = v0[u];
-                if (lane + 32 < lo.row16) to[lane + 32] = v1[u];
-                if (lo.scale_at && lane == 0) *reinterpret_cast<uint32_t*>(page + lo.scale_at + (d % kPage) * 4) = word[u];
-            }
+        for (int x = warp; x < rows; x += kCommitWarps) {
+            const int c = c0 + x / n, d = s_dst[x % n];
+            const Layout lo = layout_of(cl.kind[c]);
+            uint8_t* page = cl.data[c] + (int64_t)(d / kPage) * lo.page_bytes;
+            uint4* to = reinterpret_cast<uint4*>(page) + (d % kPage) * lo.row16;
+            const uint4* from = reinterpret_cast<const uint4*>(smem + x * DSA_KV_TOKEN_BYTES);
+            if (lane < lo.row16) to[lane] = from[lane];
+            if (lane + 32 < lo.row16) to[lane + 32] = from[lane + 32];
+            if (lo.scale_at && lane == 0)
+                *reinterpret_cast<uint32_t*>(page + lo.scale_at + (d % kPage) * 4) = *reinterpret_cast<const uint32_t*>(from + lo.row16);
         }
     }
 }
@@ -195,9 +189,20 @@ release_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
 // One cluster of up to eight blocks walks the counts.  Each round covers 16 counts
 // per thread and block, a block's next round in flight while the blocks tell one
 // another how many free pages they hold; the ranks follow from a scan inside the
-// block, so every block knows where its pages belong and takes them at once.
+// block.  A block lists its free pages, so that its threads take them side by side:
+// the threads that found them would each take up to 16 one after the other, a round
+// trip each.
 constexpr int kPoolBlocks = 8;                             // the largest cluster every launch may have
 constexpr int kStep = 16 * kPoolThreads;                   // counts of a block's round
+
+// Dynamic shared memory of the calls that take pages.
+struct PoolShared {
+    int32_t a[kMaxRows];                                   // 16-byte aligned: lists that among() reads
+    int32_t cnt[kMaxRows + 4];                             // entries before each request
+    uint16_t free_at[kStep];                               // the block's free pages, from the round's first one
+    int scratch[32];
+    int total[2][kPoolBlocks];                             // free pages of each block's round
+};
 
 struct Counts {
     int4 v[4];
@@ -222,8 +227,8 @@ __device__ __forceinline__ int64_t first_count() { return (int64_t)blockIdx.x * 
 // returns how many there were (at most want), the same in every block.  c: the
 // counts from first_count() on, loaded by the caller.
 template <typename Take>
-__device__ __forceinline__ int walk_free(Counts c, const int32_t* ref, int64_t num_pages, int want, int* scratch, Take take) {
-    __shared__ int s_tot[2][kPoolBlocks];                  // free pages of each block's round
+__device__ __forceinline__ int walk_free(Counts c, const int32_t* ref, int64_t num_pages, int want, PoolShared& sh, Take take) {
+    static_assert(kStep <= 1 << 16, "pages of a round as 16-bit numbers");
     const int tid = threadIdx.x, blocks = gridDim.x;
     const int64_t round = (int64_t)blocks * kStep;
     int found = 0, turn = 0;
@@ -234,27 +239,33 @@ __device__ __forceinline__ int walk_free(Counts c, const int32_t* ref, int64_t n
         int n = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) n += (c.v[u].x == 0) + (c.v[u].y == 0) + (c.v[u].z == 0) + (c.v[u].w == 0);
-        int tot, rank = found + sel::excl_scan<kPoolThreads, 0>(n, tid, scratch, &tot), all = tot;
-        if (blocks > 1) {
-            if (tid < blocks) sm100::st_cluster_u32(sm100::mapa_shared(sm100::smem_addr(&s_tot[turn][blockIdx.x]), tid), (uint32_t)tot);
-            sm100::cluster_sync();                         // a block is never two rounds ahead: two sets of slots do
-            all = 0;
-            for (int b = 0; b < blocks; ++b) {
-                if (b == (int)blockIdx.x) rank += all;
-                all += s_tot[turn][b];
-            }
-        }
+        int mine;                                          // free pages of this block's round
+        int place = sel::excl_scan<kPoolThreads, 0>(n, tid, sh.scratch, &mine);
+        if (blocks > 1 && tid < blocks)
+            sm100::st_cluster_u32(sm100::mapa_shared(sm100::smem_addr(&sh.total[turn][blockIdx.x]), tid), (uint32_t)mine);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int x[4] = {c.v[u].x, c.v[u].y, c.v[u].z, c.v[u].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (x[e] == 0) {
-                    if (rank < want) take(rank, at + 4 * u + e);
-                    ++rank;
-                }
+                if (x[e] == 0) sh.free_at[place++] = (uint16_t)(tid * 16 + 4 * u + e);
         }
-        found += all;
+        int rank0 = found;                                 // of the block's first free page
+        if (blocks > 1) {
+            sm100::cluster_sync();                         // a block is never two rounds ahead: two sets of slots do
+            for (int b = 0; b < blocks; ++b) {
+                if (b < (int)blockIdx.x) rank0 += sh.total[turn][b];
+                found += sh.total[turn][b];
+            }
+        } else {
+            __syncthreads();
+            found += mine;
+        }
+        const int64_t page0 = base + (int64_t)blockIdx.x * kStep;
+        const int takes = min(mine, want - rank0);
+#pragma unroll 4
+        for (int e = tid; e < takes; e += kPoolThreads) take(rank0 + e, page0 + sh.free_at[e]);
+        __syncthreads();                                   // the list may be written again
         c = next;
     }
     return min(found, want);
@@ -314,9 +325,9 @@ __global__ void __launch_bounds__(kPoolThreads)
 reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict__ table, int rows, int max_pages,
                const int32_t* __restrict__ row, const int32_t* __restrict__ have, const int32_t* __restrict__ want, int n,
                int32_t* __restrict__ st) {
-    // s_at: the requests' rows, then their first entries in the table; s_cnt: entries before each
-    __shared__ __align__(16) int32_t s_at[kMaxRows], s_cnt[kMaxRows + 1];
-    __shared__ int scratch[32];
+    extern __shared__ __align__(16) uint8_t smem[];
+    PoolShared& sh = *reinterpret_cast<PoolShared*>(smem);
+    int32_t *const s_at = sh.a, *const s_cnt = sh.cnt;     // the requests' rows, then their first entries in the table
     if (gridDim.x > 1) sm100::cluster_sync();              // the others' shared memory is there from here on
     pdl_wait();
     pdl_trigger();
@@ -353,12 +364,12 @@ reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
 #pragma unroll
     for (int u = 0; u < kPerThread; ++u)
         if (tid + u * kPoolThreads < n) s_at[tid + u * kPoolThreads] = at[u];
-    const int total = prefix_in_place(s_cnt, n, scratch);
+    const int total = prefix_in_place(s_cnt, n, sh.scratch);
     auto entry = [&](int e) {
         const int i = owner_of(s_cnt, n, e);
         return table + s_at[i] + (e - s_cnt[i]);
     };
-    const int found = walk_free(c, ref, num_pages, total, scratch, [&](int rank, int64_t page) {
+    const int found = walk_free(c, ref, num_pages, total, sh, [&](int rank, int64_t page) {
         int32_t* t = entry(rank);
         if (*t < 0) {
             *t = (int32_t)page;
@@ -390,9 +401,9 @@ __global__ void __launch_bounds__(kPoolThreads)
 fork_take_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict__ table, int rows, int max_pages,
                  const int32_t* __restrict__ src, const int32_t* __restrict__ dst, const int32_t* __restrict__ length,
                  int n, int32_t* __restrict__ st) {
-    // s_cnt: the source rows, then the pages taken before each child
-    __shared__ __align__(16) int32_t s_dst[kMaxRows], s_cnt[kMaxRows + 1];
-    __shared__ int scratch[32];
+    extern __shared__ __align__(16) uint8_t smem[];
+    PoolShared& sh = *reinterpret_cast<PoolShared*>(smem);
+    int32_t *const s_dst = sh.a, *const s_cnt = sh.cnt;    // s_cnt: the source rows, then the pages taken before each child
     if (gridDim.x > 1) sm100::cluster_sync();              // the others' shared memory is there from here on
     pdl_wait();
     pdl_trigger();
@@ -429,9 +440,9 @@ fork_take_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restri
     for (int u = 0; u < kPerThread; ++u)
         if (tid + u * kPoolThreads < n) s_cnt[tid + u * kPoolThreads] = take[u];
     __syncthreads();
-    const int total = prefix_in_place(s_cnt, n, scratch);
+    const int total = prefix_in_place(s_cnt, n, sh.scratch);
     auto last = [&](int i) { return table + (int64_t)s_dst[i] * max_pages + fork_len(length[i], max_pages) / kPage; };
-    const int found = walk_free(c, ref, num_pages, total, scratch, [&](int rank, int64_t page) {
+    const int found = walk_free(c, ref, num_pages, total, sh, [&](int rank, int64_t page) {
         *last(owner_of(s_cnt, n, rank)) = (int32_t)page;
         ref[page] = 1;
     });
@@ -549,13 +560,14 @@ extern "C" dsa_status dsa_tree_commit(const int32_t* accept, int32_t width, cons
     if (width > pages::kMaxAccept || b->num_pages * kPage > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
     if (width > 0 && !accept) return DSA_ERR_INVALID_ARGUMENT;
     if (n_caches == 0 && !new_seq_len) return DSA_OK;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(&pages::commit_kernel), pages::kCommitSmem) != DSA_OK) return DSA_ERR_CUDA;
     int32_t at = 0;
     do {                                                   // 128 caches a launch; the first writes the lengths
         const int32_t n = n_caches - at < pages::kMaxCaches ? n_caches - at : pages::kMaxCaches;
         const int32_t want = std::min(std::max(1, pages::kCommitBlocks / b->batch), std::max(1, n));
         const int32_t per = std::max(1, (n + want - 1) / want);
         DSA_CHECK(launch_pdl(pages::commit_kernel, dim3((unsigned)b->batch, (unsigned)std::max(1, (n + per - 1) / per)),
-                             dim3(pages::kCopyThreads), 0, as_stream(stream), 1, accept, (int)width, to_dev(b),
+                             dim3(pages::kCopyThreads), pages::kCommitSmem, as_stream(stream), 1, accept, (int)width, to_dev(b),
                              pages::list_of(caches, at, n), (int)n, (int)per, at == 0 ? new_seq_len : nullptr,
                              at == 0 ? dev_status : nullptr));
         at += n;
@@ -571,7 +583,8 @@ extern "C" dsa_status dsa_pages_reserve(int32_t* page_ref, int64_t num_pages, in
     if (!row || !have_len || !want_len) return DSA_ERR_INVALID_ARGUMENT;
     if (n > pages::kMaxRows) return DSA_ERR_UNSUPPORTED;
     const unsigned blocks = pages::pool_blocks(num_pages);
-    DSA_CHECK(launch_pdl(pages::reserve_kernel, dim3(blocks), dim3(pages::kPoolThreads), 0, as_stream(stream), blocks,
+    if (ensure_smem_limit(reinterpret_cast<const void*>(&pages::reserve_kernel), sizeof(pages::PoolShared)) != DSA_OK) return DSA_ERR_CUDA;
+    DSA_CHECK(launch_pdl(pages::reserve_kernel, dim3(blocks), dim3(pages::kPoolThreads), sizeof(pages::PoolShared), as_stream(stream), blocks,
                          page_ref, num_pages, page_table, (int)rows, (int)max_pages, row, have_len, want_len, (int)n,
                          dev_status));
     return DSA_OK;
@@ -600,7 +613,8 @@ extern "C" dsa_status dsa_pages_fork(int32_t* page_ref, int64_t num_pages, int32
     if (!src_row || !dst_row || !length) return DSA_ERR_INVALID_ARGUMENT;
     if (n > pages::kMaxRows) return DSA_ERR_UNSUPPORTED;
     const unsigned blocks = pages::pool_blocks(num_pages);
-    DSA_CHECK(launch_pdl(pages::fork_take_kernel, dim3(blocks), dim3(pages::kPoolThreads), 0, as_stream(stream), blocks,
+    if (ensure_smem_limit(reinterpret_cast<const void*>(&pages::fork_take_kernel), sizeof(pages::PoolShared)) != DSA_OK) return DSA_ERR_CUDA;
+    DSA_CHECK(launch_pdl(pages::fork_take_kernel, dim3(blocks), dim3(pages::kPoolThreads), sizeof(pages::PoolShared), as_stream(stream), blocks,
                          page_ref, num_pages, page_table, (int)rows, (int)max_pages, src_row, dst_row, length, (int)n,
                          dev_status));
     const int chunks = (max_pages + pages::kCopyThreads - 1) / pages::kCopyThreads;
