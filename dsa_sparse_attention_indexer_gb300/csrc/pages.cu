@@ -195,11 +195,16 @@ release_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
 constexpr int kPoolBlocks = 8;                             // the largest cluster every launch may have
 constexpr int kStep = 16 * kPoolThreads;                   // counts of a block's round
 
+constexpr int kSlots = 4 * kMaxRows;                       // of the table of rows, at most half of them in use
+
 // Dynamic shared memory of the calls that take pages.
 struct PoolShared {
-    int32_t a[kMaxRows];                                   // 16-byte aligned: lists that among() reads
+    int32_t a[kMaxRows];
     int32_t cnt[kMaxRows + 4];                             // entries before each request
-    uint16_t free_at[kStep];                               // the block's free pages, from the round's first one
+    union {
+        uint32_t slot[kSlots];                             // rows mentioned (struct Mentions), before the walk
+        uint16_t free_at[kStep];                           // the block's free pages, from the round's first one
+    };
     int scratch[32];
     int total[2][kPoolBlocks];                             // free pages of each block's round
 };
@@ -223,11 +228,17 @@ __device__ __forceinline__ void load_counts(Counts& c, const int32_t* ref, int64
 // Where this thread's counts of the block's first round begin.
 __device__ __forceinline__ int64_t first_count() { return (int64_t)blockIdx.x * kStep + (int64_t)threadIdx.x * 16; }
 
-// Calls take(rank, page) for the first `want` free pages in ascending order and
-// returns how many there were (at most want), the same in every block.  c: the
-// counts from first_count() on, loaded by the caller.
-template <typename Take>
-__device__ __forceinline__ int walk_free(Counts c, const int32_t* ref, int64_t num_pages, int want, PoolShared& sh, Take take) {
+// Where a block's e-th free page is listed.  Threads that found 16 pages write 32 bytes
+// apart; turned by the groups of 64, they hit 32 banks.
+__device__ __forceinline__ int listed(int e) { return e ^ (e >> 6 & 7) << 1; }
+
+// The first `want` free pages in ascending order go to entry(0, i), entry(1, i), .. (i: the
+// caller's hint, 0 at first); an entry that holds a page keeps it if `keep`.  Returns how many pages there were (at most
+// want), the same in every block.  c: the counts from first_count() on, loaded by the
+// caller.
+template <typename Entry>
+__device__ __forceinline__ int walk_free(Counts c, int32_t* ref, int64_t num_pages, int want, bool keep, PoolShared& sh,
+                                         Entry entry) {
     static_assert(kStep <= 1 << 16, "pages of a round as 16-bit numbers");
     const int tid = threadIdx.x, blocks = gridDim.x;
     const int64_t round = (int64_t)blocks * kStep;
@@ -248,7 +259,7 @@ __device__ __forceinline__ int walk_free(Counts c, const int32_t* ref, int64_t n
             const int x[4] = {c.v[u].x, c.v[u].y, c.v[u].z, c.v[u].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (x[e] == 0) sh.free_at[place++] = (uint16_t)(tid * 16 + 4 * u + e);
+                if (x[e] == 0) sh.free_at[listed(place++)] = (uint16_t)(tid * 16 + 4 * u + e);
         }
         int rank0 = found;                                 // of the block's first free page
         if (blocks > 1) {
@@ -263,25 +274,60 @@ __device__ __forceinline__ int walk_free(Counts c, const int32_t* ref, int64_t n
         }
         const int64_t page0 = base + (int64_t)blockIdx.x * kStep;
         const int takes = min(mine, want - rank0);
-#pragma unroll 4
-        for (int e = tid; e < takes; e += kPoolThreads) take(rank0 + e, page0 + sh.free_at[e]);
+        // a warp takes consecutive pages for consecutive entries, four round trips at a time
+        const int chunk = (takes + kPoolThreads - 1) / kPoolThreads * 32, end = min(takes, ((tid >> 5) + 1) * chunk);
+        int owner = 0;
+        for (int e0 = (tid >> 5) * chunk + (tid & 31); e0 < end; e0 += 4 * 32) {
+            int32_t* t[4];
+            bool ours[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                t[u] = e0 + u * 32 < end ? entry(rank0 + e0 + u * 32, owner) : nullptr;
+                ours[u] = t[u] != nullptr && (!keep || *t[u] < 0);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (ours[u]) {
+                    const int64_t page = page0 + sh.free_at[listed(e0 + u * 32)];
+                    *t[u] = (int32_t)page;
+                    ref[page] = 1;
+                }
+        }
         __syncthreads();                                   // the list may be written again
         c = next;
     }
     return min(found, want);
 }
 
-// Whether d is among s[0 .. n); s is 16-byte aligned.
-__device__ __forceinline__ bool among(const int32_t* s, int n, int d) {
-    bool hit = false;
-    int j = 0;
-#pragma unroll 4
-    for (; j + 4 <= n; j += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(s + j);
-        hit |= (v.x == d) | (v.y == d) | (v.z == d) | (v.w == d);
+// The rows that a call names, each with its least mention: an open hash table.
+// row_of(m) is the row of mention m.
+template <typename RowOf>
+struct Mentions {
+    uint32_t* slot;                                        // [kSlots]: mention + 1, 0 where free
+    RowOf row_of;
+    __device__ __forceinline__ uint32_t first_slot(int row) const { return (uint32_t)row * 0x9e3779b1u >> 18; }
+    __device__ __forceinline__ void add(int m) {
+        static_assert(kSlots == 1 << 14, "hash bits");
+        const int row = row_of(m);
+        for (uint32_t at = first_slot(row);; at = (at + 1) % kSlots) {
+            const uint32_t was = atomicCAS(slot + at, 0u, m + 1u);
+            if (was == 0) return;
+            if (row_of(was - 1) == row) {
+                atomicMin(slot + at, m + 1u);
+                return;
+            }
+        }
     }
-    for (; j < n; ++j) hit |= s[j] == d;
-    return hit;
+    __device__ __forceinline__ int least(int row) const {  // of a row that has been added
+        uint32_t at = first_slot(row);
+        while (row_of(slot[at] - 1) != row) at = (at + 1) % kSlots;
+        return (int)slot[at] - 1;
+    }
+};
+template <typename RowOf>
+__device__ __forceinline__ Mentions<RowOf> no_mentions(uint32_t* slot, RowOf row_of) {   // a barrier must follow
+    for (int i = threadIdx.x; i < kSlots / 4; i += kPoolThreads) reinterpret_cast<uint4*>(slot)[i] = make_uint4(0, 0, 0, 0);
+    return {slot, row_of};
 }
 
 // Exclusive prefix sums of cnt[0 .. n) in place, cnt[n] = their total; n <= kMaxRows.
@@ -308,9 +354,12 @@ __device__ __forceinline__ int prefix_in_place(int32_t* cnt, int n, int* scratch
     return tot;
 }
 
-// The request whose entries hold rank e: the last i with cnt[i] <= e.
-__device__ __forceinline__ int owner_of(const int32_t* cnt, int n, int e) {
-    int lo = 0, hi = n - 1;
+// The request whose entries hold rank e, which is `from` or one after it: the last i
+// with cnt[i] <= e, cnt[n] > e.  Mostly `from` or the next; else a binary search.
+__device__ __forceinline__ int owner_of(const int32_t* cnt, int n, int e, int from = 0) {
+    int lo = from, hi = n - 1;
+    if (e < cnt[lo + 1]) return lo;
+    if (e < cnt[min(lo + 2, n)]) return lo + 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (cnt[mid] <= e) lo = mid; else hi = mid - 1;
@@ -335,6 +384,7 @@ reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
     const bool speaks = blockIdx.x == 0;                   // every block works the same requests out, one records
     Counts c;
     load_counts(c, ref, num_pages, first_count());
+    auto named = no_mentions(sh.slot, [&](int m) { return s_at[m]; });
     int at[kPerThread], cnt[kPerThread];
 #pragma unroll
     for (int u = 0; u < kPerThread; ++u) {
@@ -349,12 +399,14 @@ reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
         at[u] = lo;
     }
     __syncthreads();
+    for (int i = tid; i < n; i += kPoolThreads) named.add(i);
+    __syncthreads();
 #pragma unroll
     for (int u = 0; u < kPerThread; ++u) {
         const int i = tid + u * kPoolThreads;
         if (i >= n) continue;
         const int r = s_at[i];
-        const bool ok = r >= 0 && r < rows && !among(s_at, i, r);   // a row's first mention counts
+        const bool ok = r >= 0 && r < rows && named.least(r) == i;   // a row's first mention counts
         if (!ok) s_cnt[i] = 0;
         if (speaks && !ok) record_error(st, DSA_DEVERR_INDEX_RANGE, r);
         if (speaks && ok && cnt[u] < 0) record_error(st, DSA_DEVERR_INDEX_RANGE, -1 - cnt[u]);
@@ -365,20 +417,14 @@ reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
     for (int u = 0; u < kPerThread; ++u)
         if (tid + u * kPoolThreads < n) s_at[tid + u * kPoolThreads] = at[u];
     const int total = prefix_in_place(s_cnt, n, sh.scratch);
-    auto entry = [&](int e) {
-        const int i = owner_of(s_cnt, n, e);
+    auto entry = [&](int e, int& i) {                      // i: the owner of an earlier entry, then this one's
+        i = owner_of(s_cnt, n, e, i);
         return table + s_at[i] + (e - s_cnt[i]);
     };
-    const int found = walk_free(c, ref, num_pages, total, sh, [&](int rank, int64_t page) {
-        int32_t* t = entry(rank);
-        if (*t < 0) {
-            *t = (int32_t)page;
-            ref[page] = 1;
-        }
-    });
+    const int found = walk_free(c, ref, num_pages, total, true, sh, entry);
     if (speaks)                                            // what the pool does not hold
-        for (int e = found + tid; e < total; e += kPoolThreads)
-            if (*entry(e) < 0) record_error(st, DSA_DEVERR_PAGE_POOL, row[owner_of(s_cnt, n, e)]);
+        for (int e = found + tid, i = 0; e < total; e += kPoolThreads)
+            if (*entry(e, i) < 0) record_error(st, DSA_DEVERR_PAGE_POOL, row[i]);
 }
 
 // ---------------------------------------------------------------- fork
@@ -411,10 +457,13 @@ fork_take_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restri
     const bool speaks = blockIdx.x == 0;                   // every block works the same children out, one records
     Counts c;
     load_counts(c, ref, num_pages, first_count());
+    auto named = no_mentions(sh.slot, [&](int m) { return m < n ? s_cnt[m] : s_dst[m - n]; });   // as a source, then as a child
     for (int i = tid; i < n; i += kPoolThreads) {
         s_dst[i] = dst[i];
         s_cnt[i] = src[i];
     }
+    __syncthreads();
+    for (int i = tid; i < 2 * n; i += kPoolThreads) named.add(i);
     __syncthreads();
     int take[kPerThread];
 #pragma unroll
@@ -423,7 +472,7 @@ fork_take_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restri
         take[u] = 0;
         if (i >= n) continue;
         const int s = s_cnt[i], d = s_dst[i];
-        if (s < 0 || s >= rows || d < 0 || d >= rows || among(s_cnt, n, d) || among(s_dst, i, d)) {
+        if (s < 0 || s >= rows || d < 0 || d >= rows || named.least(d) != n + i) {   // no source, and no earlier child
             if (speaks) record_error(st, DSA_DEVERR_INDEX_RANGE, d);
             continue;
         }
@@ -442,10 +491,7 @@ fork_take_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restri
     __syncthreads();
     const int total = prefix_in_place(s_cnt, n, sh.scratch);
     auto last = [&](int i) { return table + (int64_t)s_dst[i] * max_pages + fork_len(length[i], max_pages) / kPage; };
-    const int found = walk_free(c, ref, num_pages, total, sh, [&](int rank, int64_t page) {
-        *last(owner_of(s_cnt, n, rank)) = (int32_t)page;
-        ref[page] = 1;
-    });
+    const int found = walk_free(c, ref, num_pages, total, false, sh, [&](int e, int& i) { return last(i = owner_of(s_cnt, n, e, i)); });
     if (speaks)                                            // children that the pool holds no page for
         for (int e = found + tid; e < total; e += kPoolThreads) {
             const int i = owner_of(s_cnt, n, e);
