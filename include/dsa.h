@@ -559,8 +559,8 @@ dsa_status dsa_tree_mla(const void* q, const uint64_t* tree_mask, const uint8_t*
  *   are passed over; both are recorded (DSA_DEVERR_INDEX_RANGE).  Lengths are
  *   cut to 64 * max_pages and recorded likewise.
  *     row, have_len, want_len, first_page, end_page, src_row, dst_row, length
- *                device int32 [n]; n <= 4096 for reserve and fork
- *                (DSA_ERR_UNSUPPORTED beyond)                                  */
+ *                device int32 [n]; n <= 4096 for reserve and fork, and
+ *                rows * max_pages < 2^31 (DSA_ERR_UNSUPPORTED beyond)          */
 #define DSA_CACHE_KV         0      /* latent rows,  DSA_KV_PAGE_BYTES             */
 #define DSA_CACHE_IDXK       1      /* FP8 index-K,  DSA_IDXK_PAGE_BYTES           */
 #define DSA_CACHE_IDXK_MXFP4 2      /* MXFP4 index-K, DSA_IDXK_MXFP4_PAGE_BYTES    */

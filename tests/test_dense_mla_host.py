@@ -121,6 +121,7 @@ def test_pool_argument_errors(L):
         assert call(ref=ODD) == ALIGN
         assert call(pages=1 << 25) == UNSUPPORTED
         assert call(ref=N, table=N, row=N, a=N, b=N, n=0) == OK
+        assert call(rows=1 << 20, width=1 << 11) == UNSUPPORTED       # 2^31 table entries
     assert reserve(n=4097) == UNSUPPORTED
     assert fork(n=4097) == UNSUPPORTED
     assert L.dsa_pages_fork(FK, 128, FK, 8, 64, FK, FK, FK, 2, _list((0x50000004, 1)), 1, N, N) == ALIGN

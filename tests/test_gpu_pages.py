@@ -200,6 +200,77 @@ def test_fork_refusals_and_an_empty_pool():
     assert np.array_equal(dtable.cpu().numpy(), table) and np.array_equal(dref.cpu().numpy(), ref)
 
 
+def test_reserve_of_many_rows_in_a_large_pool():
+    """As many requests as one call takes, rows named again among them, and so few free
+    pages up front that the walk goes round several times."""
+    rng = np.random.default_rng(77)
+    pages, rows, width, n = 400001, 4500, 6, 4096
+    ref = rng.integers(1, 4, pages).astype(np.int32)
+    ref[rng.permutation(pages)[:7000]] = 0
+    ref[-3:] = 0
+    table = np.full((rows, width), -1, np.int32)
+    table[::7, 1] = 5                                                # entries that hold a page keep it
+    row = rng.permutation(rows)[:n]
+    row[rng.permutation(n)[:200]] = row[rng.permutation(n)[:200]]
+    row[[3, 4000]] = [rows, -7]
+    have = rng.integers(0, 2 * 64, n)
+    want = np.minimum(have + rng.integers(-64, 5 * 64, n), width * 64)
+    dref, dtable = dev(ref), dev(table)
+    st = D.new_device_status(DEV)
+    D.dsa_pages_reserve(dref, dtable, dev(row), dev(have), dev(want), dev_status=st)
+    errors = O.pages_reserve(ref, table, row.tolist(), have.tolist(), want.tolist())
+    s = D.dsa_device_status_read(st)
+    assert s[1] == errors and s[0] == D.DEVERR_INDEX_RANGE | D.DEVERR_PAGE_POOL
+    assert np.array_equal(dtable.cpu().numpy(), table) and np.array_equal(dref.cpu().numpy(), ref)
+
+
+def test_fork_of_many_rows():
+    """Children named again, and named as sources, in a call of as many as there may be."""
+    rng = np.random.default_rng(78)
+    rows, width, n = 4300, 3, 4096
+    ref, table = pool_state(rng, 20000, rows, width, [width if r < 100 else 0 for r in range(rows)])
+    src = rng.integers(0, 100, n)
+    dst = 100 + rng.permutation(rows - 100)[:n]
+    dst[rng.permutation(n)[:50]] = dst[rng.permutation(n)[:50]]
+    dst[[7, 9, 4095]] = [src[0], -1, rows]
+    length = rng.integers(0, width * 64 + 1, n)
+    host = raw_caches(rng, 20000, [D.CACHE_IDXK_MXFP4])
+    t, caches = device_caches(host, [D.CACHE_IDXK_MXFP4], 20000)
+    dref, dtable = dev(ref), dev(table)
+    st = D.new_device_status(DEV)
+    D.dsa_pages_fork(dref, dtable, dev(src), dev(dst), dev(length), caches, dev_status=st)
+    errors, copies = O.pages_fork(ref, table, src.tolist(), dst.tolist(), length.tolist())
+    s = D.dsa_device_status_read(st)
+    assert (s[0], s[1]) == (D.DEVERR_INDEX_RANGE, errors)
+    assert np.array_equal(dtable.cpu().numpy(), table) and np.array_equal(dref.cpu().numpy(), ref)
+    want = token_rows(host[0], D.CACHE_IDXK_MXFP4)
+    for a, b, m in copies:
+        want[b, :m] = want[a, :m]
+    assert np.array_equal(token_rows(t[0].cpu().numpy(), D.CACHE_IDXK_MXFP4), want)
+
+
+def test_commit_of_whole_lists_in_many_caches():
+    """63 moves a request: the rows of two caches at most fit one round."""
+    rng = np.random.default_rng(79)
+    kinds = [D.CACHE_KV, D.CACHE_IDXK, D.CACHE_IDXK_MXFP4] * 3
+    B, pages = 3, 12
+    host = raw_caches(rng, pages, kinds)
+    t, caches = device_caches(host, kinds, pages)
+    table = rng.permutation(pages).reshape(B, 4).astype(np.int32)
+    seq, accept = [200, 64, 130], np.stack([rng.permutation(64) for _ in range(B)]).astype(np.int32)
+    batch = D.Batch(dev(seq), dev([0, 64, 128, 192]), dev(table), pages, max_seq_len=256, max_q_len=64, total_q=192)
+    st = D.new_device_status(DEV)
+    got = D.dsa_tree_commit(dev(accept), batch, caches, dev_status=st)
+    assert D.dsa_device_status_read(st)[0] == 0 and got.cpu().tolist() == seq
+    for i, kind in enumerate(kinds):
+        before, want = token_rows(host[i], kind), token_rows(host[i], kind).copy()
+        for r in range(B):
+            for k, u in enumerate(accept[r]):
+                a, b = seq[r] - 64 + u, seq[r] - 64 + k
+                want[table[r, b // 64], b % 64] = before[table[r, a // 64], a % 64]
+        assert np.array_equal(token_rows(t[i].cpu().numpy(), kind), want), f"cache {i}"
+
+
 def test_binding_refuses_mixed_lists():
     ref, table, one = dev([0] * 8), dev([[-1] * 4]), dev([0])
     with pytest.raises(ValueError):
