@@ -31,13 +31,25 @@
 //               128-byte-swizzled tile (exact for scales in [2^-15, 2^7]), each
 //               part as soon as it is free.  Rows that are not seen become zeros or
 //               another row, with probability 0;
-//   next row    its Q, scaled by the power of two that puts its largest |q| in
-//               [2^14, 2^15), while the last P.V runs; then the epilogue, while
-//               the first S^T of the next row runs.
+//   next row    its Q, copied into its place as bf16 during the softmax, then scaled
+//               by the power of two that puts its largest |q| in [2^14, 2^15), while
+//               the last P.V runs; then the epilogue, while the first S^T of the
+//               next row runs.
 // Warp 16 issues the MMAs.  Warp 17 lays out the tiles of the CTA's share up to four
 // ahead: pages, masks of what is seen, where a row's piece begins and ends; it also
 // prefetches the pages into L2.
 // Every wait is time-bounded; a timeout is recorded and the CTA winds down.
+//
+// What bounds it (64 tree rows in each of 8 requests, 32K tokens: 2.94 ms, 795 TFLOP/s;
+// 2048 rows with a window of 2048: 0.96 ms; one row in each of 4 requests with a window of
+// 131072: 136 us, 2.5 TB/s): the workers' issue slots.  A tile takes about 7,500 cycles,
+// of which the tensor core is busy 3,300; without the MMAs it takes 4 % less, without the
+// loads 10 %.  Of about 675 instructions per warp and tile most are conversions and fp16
+// products of the dequantisation, at half rate or less.
+//
+// One row of 512 tokens takes 16 us, all of it latency: the share 2, tile and page 1.5,
+// Q 2, tile 1.5, S^T 0.5, softmax 1.5, P.V 1, the partial's 131 KB at 30 bytes a cycle 2.5,
+// the merge 3.
 #include <algorithm>
 #include <type_traits>
 
@@ -777,24 +789,9 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                     for (int c = 0; c < kHeads; ++c) to[c * 512] = __uint_as_float(o[c]);
                     continue;
                 }
-                // bf16: four lanes turn their 16 heads x 1 dim into 4 heads x 4 dims each, so
-                // that a store is 8 bytes (2 bytes a store were bound by their number)
-                uint32_t x[8], y[8];
+                __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at + d;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) x[c] = pack_bf16x2(__uint_as_float(o[c]), __uint_as_float(o[c + 8]));   // heads c, c + 8
-                const bool odd = lane & 1, high = lane & 2;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {                          // dims of an even lane and the next: heads 0-7 | 8-15
-                    const uint32_t z = __shfl_xor_sync(0xffffffffu, x[c], 1);
-                    y[c] = odd ? __byte_perm(z, x[c], 0x7632) : __byte_perm(x[c], z, 0x5410);
-                }
-                uint16_t* to = static_cast<uint16_t*>(a.out) + at + (mb * 128 + q4 * 32 + (lane & ~3)) +
-                               ((odd ? 8 : 0) + (high ? 4 : 0)) * 512;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {                          // dims of four lanes: heads 0-3 | 4-7 of those
-                    const uint32_t z = __shfl_xor_sync(0xffffffffu, high ? y[c] : y[c + 4], 2);
-                    *reinterpret_cast<uint2*>(to + c * 512) = high ? make_uint2(z, y[c + 4]) : make_uint2(y[c], z);
-                }
+                for (int c = 0; c < kHeads; ++c) to[c * 512] = __float2bfloat16_rn(__uint_as_float(o[c]));
             }
             tc_fence_before();
             if (tid < 64) {
@@ -823,8 +820,9 @@ dense_mla_kernel(const __grid_constant__ Args a) {
 
 // ---------------------------------------------------------------- merge
 // Blocks of a row that was cut, four heads and 128 dims at a time.  Where there are
-// more shares than rows, block x looks after row x; else after the row that share
-// x + 1 begins inside, if it is the first to do so.  Per head over the pieces u:
+// more shares than rows, block x looks after row x (8 rows x 17 pieces 21.8 us; by
+// boundary, most of whose blocks have nothing to do, 28.0); else after the row that
+// share x + 1 begins inside, if it is the first to do so.  Per head over the pieces u:
 //   M = max m_u,  w_u = 2^(m_u - M),  L = sum w_u l_u,
 //   out = sum_u w_u O_u / L,  lse = (M + log2 L) ln 2.
 // Every warp works the weights out by itself, eight pieces x four heads a step, the
@@ -974,6 +972,9 @@ static dsa_status launch(const void* q, const uint8_t* kv, const dsa_batch* b, V
     const cudaStream_t s = as_stream(stream);
     DSA_CHECK(launch_pdl(dense_mla_kernel, dim3((unsigned)G), dim3(kThreads), kSmemAlloc, s, 1, a));
     if (G > 1) {
+        // A block per part of a row where few rows can be cut, which may have many pieces (4
+        // rows x 38 pieces 137 us, with four parts a block 150), four parts a block where many
+        // can (200 rows 127 us, with one part a block 137).
         const bool by_row = b->total_q < G;
         DSA_CHECK(launch_pdl(dense_merge_kernel, dim3(by_row ? (unsigned)b->total_q : (unsigned)(G - 1), b->total_q < 32 ? 64 : 16),
                              dim3(kMergeThreads), 0, s, 1, a, G, (int)by_row));
