@@ -40,12 +40,15 @@
 // prefetches the pages into L2.
 // Every wait is time-bounded; a timeout is recorded and the CTA winds down.
 //
-// What bounds it (64 tree rows in each of 8 requests, 32K tokens: 2.94 ms, 795 TFLOP/s;
-// 2048 rows with a window of 2048: 0.96 ms; one row in each of 4 requests with a window of
-// 131072: 136 us, 2.5 TB/s): the workers' issue slots.  A tile takes about 7,500 cycles,
-// of which the tensor core is busy 3,300; without the MMAs it takes 4 % less, without the
-// loads 10 %.  Of about 675 instructions per warp and tile most are conversions and fp16
-// products of the dequantisation, at half rate or less.
+// What bounds it (64 tree rows in each of 8 requests of up to 32K tokens: 2.94 ms, 671
+// TFLOP/s; 2048 rows with a window of 2048: 0.96 ms, 613 TFLOP/s; one row in each of 4
+// requests with a window of 131072: 136 us, 2.5 TB/s): the workers' issue slots.  A tile
+// takes about 7,500 cycles, of which the tensor core is busy 3,300; without the MMAs it
+// takes 4 % less, without the loads 10 %.  Of about 675 instructions per warp and tile
+// most are conversions and fp16 products of the dequantisation, at half rate or less.
+// Neighbouring rows of a request read the same tiles, but two rows' O^T (2 x 256
+// columns) leave no TMEM for S^T; two CTAs that dequantise half a tile each and copy
+// it to one another move in step, and wait more than they save (2.94 -> 3.93 ms).
 //
 // One row of 512 tokens takes 16 us, all of it latency: the share 2, tile and page 1.5,
 // Q 2, tile 1.5, S^T 0.5, softmax 1.5, P.V 1, the partial's 131 KB at 30 bytes a cycle 2.5,

@@ -2,9 +2,13 @@
 // to the front of its tokens, requests that share or give back pages, and the
 // pool of page counts behind them.  No call reads anything back to the host.
 //
-// All of it is copying and counting: a move is bound by HBM (row bytes read and
-// written once), the pool calls by latency (one pass over the counts up to the
-// last page taken).
+// All of it is copying and counting: a large move is bound by HBM (row bytes read
+// and written once), the rest by latency: chains of dependent loads (lengths, lists,
+// page table, counts, entries) of 0.6 to 1 us each.  Measured: 64 children of
+// 8,229 tokens with a partial page in each of 99 caches 37 us (6.9 TB/s, the reads
+// mostly from the L2: one source page a cache); 128 accepted paths of 16 tokens in 99
+// caches 16.6 us (4.3 TB/s); one path in 5 caches 2.6 us; 256 rows giving back and
+// taking about 100,000 of 131,072 pages 17 us; 8 rows of a pool of 1,024 6.8 us.
 #include <algorithm>
 
 #include "dsa_internal.cuh"
@@ -48,12 +52,15 @@ __device__ __forceinline__ Layout layout_of(int kind) {
 // A warp moves one row at a time, 41 (KV) or 8 / 4 (index-K) pieces of 16 bytes; a
 // round reads up to 144 rows of as many whole caches as they make into shared memory,
 // all in flight at once, before the barrier and writes them after it, so a row may be
-// another row's target.  (A block per cache spent most of its time on the chain:
-// 128 requests x 99 caches took 45 us.)
+// another row's target.  128 requests x 99 caches: 45 us with a block per cache, most
+// of it the chain; 20.5 with the rows in registers, which allow 64 a round; 16.6 so.
 constexpr int kCommitWarps = kCopyThreads / 32;
 constexpr int kCommitRows = 144;                           // of a round: 94 KB, two blocks a SM
 constexpr int kCommitSmem = kCommitRows * DSA_KV_TOKEN_BYTES;
 static_assert(DSA_KV_TOKEN_BYTES >= DSA_INDEX_HEAD_DIM + 4, "an index key and its scale word take a row's place");
+// Blocks of a launch: three times what is resident.  More caches a block take more
+// rounds one after another, fewer repeat the chain: 24.3 / 18.8 / 16.6 / 17.8 / 18.2 us
+// with 304 / 608 / 912 / 1216 / 1824 blocks.
 constexpr int kCommitBlocks = 912;
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -191,7 +198,9 @@ release_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
 // another how many free pages they hold; the ranks follow from a scan inside the
 // block.  A block lists its free pages, so that its threads take them side by side:
 // the threads that found them would each take up to 16 one after the other, a round
-// trip each.
+// trip each.  (About 100,000 pages from 131,072 counts with the release before it:
+// 131 us with one block, 27 with eight, 21 with the list, 17 with a warp's entries next
+// to one another, whose owner is then mostly known.)
 constexpr int kPoolBlocks = 8;                             // the largest cluster every launch may have
 constexpr int kStep = 16 * kPoolThreads;                   // counts of a block's round
 
