@@ -599,6 +599,8 @@ class CacheSet:
                 raise ValueError(f"cache {i} has unknown kind {kind}")
             _need(t, torch.uint8, f"cache {i}", self.device, self.num_pages * _CACHE_PAGE_BYTES[kind])
             self.c[i] = DsaCache(t.data_ptr(), kind, 0)
+        if len({t.data_ptr() for t in self.tensors}) < len(self.tensors):
+            raise ValueError("a cache is named twice")
 
     def __len__(self) -> int:
         return len(self.tensors)

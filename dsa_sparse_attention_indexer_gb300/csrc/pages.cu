@@ -614,6 +614,10 @@ extern "C" dsa_status dsa_tree_commit(const int32_t* accept, int32_t width, cons
     if (vs != DSA_OK) return vs;
     if (width > pages::kMaxAccept || b->num_pages * kPage > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
     if (width > 0 && !accept) return DSA_ERR_INVALID_ARGUMENT;
+    // several blocks read a request's seq_len, one writes its new length
+    const uintptr_t from = reinterpret_cast<uintptr_t>(b->seq_len), to = reinterpret_cast<uintptr_t>(new_seq_len);
+    const uintptr_t lens = sizeof(int32_t) * (uintptr_t)b->batch;
+    if (new_seq_len && to < from + lens && from < to + lens) return DSA_ERR_INVALID_ARGUMENT;
     if (n_caches == 0 && !new_seq_len) return DSA_OK;
     if (ensure_smem_limit(reinterpret_cast<const void*>(&pages::commit_kernel), pages::kCommitSmem) != DSA_OK) return DSA_ERR_CUDA;
     int32_t at = 0;

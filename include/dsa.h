@@ -516,7 +516,7 @@ dsa_status dsa_tree_mla(const void* q, const uint64_t* tree_mask, const uint8_t*
  *
  * A cache list names every layer's caches that one page table serves; a call
  * treats them all alike, in one launch per 128 caches.  The list itself lives
- * on the host and is read before the call returns.
+ * on the host and is read before the call returns.  It names no cache twice.
  *
  * dsa_tree_commit: after a verify step, the tokens of the accepted path move to
  *   the front of the request's new tokens: with P = seq_len[r] - q_len[r], the
@@ -527,7 +527,7 @@ dsa_status dsa_tree_mla(const void* q, const uint64_t* tree_mask, const uint8_t*
  *   new_seq_len[r] = P + (entries kept).  The new tokens' pages must belong to
  *   one request only.  A position without a page is skipped and recorded.
  *     accept      device int32 [B, width], 0 <= width <= 64
- *     new_seq_len device int32 [B] or NULL
+ *     new_seq_len device int32 [B] or NULL; no part of the batch's seq_len
  *
  * The pool of pages is an array of counts, one per page: how many page-table
  * entries hold it.  A page whose count is 0 is free.  A pool starts as zeros and

@@ -102,6 +102,13 @@ def test_commit_argument_errors(L):
     assert L.dsa_tree_commit(N, 0, _batch(), N, 0, N, N, N) == OK     # nothing to move, no lengths asked for
 
 
+def test_commit_refuses_to_write_the_lengths_it_reads(L):
+    one = _list((0x50000000, 0))
+    for at in (0x10000000, 0x10000004):                               # the batch's seq_len, two requests
+        assert L.dsa_tree_commit(FK, 4, _batch(), one, 1, ctypes.c_void_p(at), N, N) == INVALID
+    assert L.dsa_tree_commit(FK, 4, _batch(), N, 0, ctypes.c_void_p(0x10000000), N, N) == INVALID
+
+
 def test_pool_argument_errors(L):
     one = _list((0x50000000, 1))
 

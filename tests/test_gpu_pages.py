@@ -271,6 +271,21 @@ def test_commit_of_whole_lists_in_many_caches():
         assert np.array_equal(token_rows(t[i].cpu().numpy(), kind), want), f"cache {i}"
 
 
+def test_a_cache_is_named_once():
+    t = torch.zeros(2 * D.KV_PAGE_BYTES, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError):
+        D.CacheSet([(t, D.CACHE_KV), (t[:D.KV_PAGE_BYTES], D.CACHE_KV)], 1)
+    D.CacheSet([(t[:D.KV_PAGE_BYTES], D.CACHE_KV), (t[D.KV_PAGE_BYTES:], D.CACHE_KV)], 1)
+
+
+def test_commit_does_not_take_the_lengths_it_reads():
+    seq = dev([8])
+    batch = D.Batch(seq, dev([0, 4]), dev([[0]]), 1, max_seq_len=64, max_q_len=4, total_q=4)
+    with pytest.raises(D.DsaError):
+        D.dsa_tree_commit(dev([[0, 2]]), batch, D.CacheSet([], 1), new_seq_len=seq)
+    assert D.dsa_tree_commit(dev([[0, 2]]), batch, D.CacheSet([], 1)).tolist() == [6]
+
+
 def test_binding_refuses_mixed_lists():
     ref, table, one = dev([0] * 8), dev([[-1] * 4]), dev([0])
     with pytest.raises(ValueError):
