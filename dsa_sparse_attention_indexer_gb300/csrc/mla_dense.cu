@@ -40,12 +40,14 @@
 // prefetches the pages into L2.
 // Every wait is time-bounded; a timeout is recorded and the CTA winds down.
 //
-// What bounds it (64 tree rows in each of 8 requests of up to 32K tokens: 2.94 ms, 671
-// TFLOP/s; 2048 rows with a window of 2048: 0.96 ms, 613 TFLOP/s; one row in each of 4
-// requests with a window of 131072: 136 us, 2.5 TB/s): the workers' issue slots.  A tile
-// takes about 7,500 cycles, of which the tensor core is busy 3,300; without the MMAs it
-// takes 4 % less, without the loads 10 %.  Of about 675 instructions per warp and tile
-// most are conversions and fp16 products of the dequantisation, at half rate or less.
+// What bounds it (64 tree rows in each of 8 requests of up to 32K tokens: 2.86 ms, 690
+// TFLOP/s; 2048 rows with a window of 2048: 0.94 ms, 624 TFLOP/s; one row in each of 4
+// requests with a window of 131072: 132 us, 2.6 TB/s): the workers.  A tile takes about
+// 7,000 cycles, of which the tensor core is busy 3,300.  The workers issue 695
+// instructions per warp and tile, mostly conversions and fp16 products of the
+// dequantisation at half rate, and 4,300 passes through the load/store pipe (1,400 for
+// the fp16 tile's stores, 1,900 for the rows' loads), one phase after the other: without
+// the MMAs a tile takes 4 % less, without the loads 10 %.
 // Neighbouring rows of a request read the same tiles, but two rows' O^T (2 x 256
 // columns) leave no TMEM for S^T; two CTAs that dequantise half a tile each and copy
 // it to one another move in step, and wait more than they save (2.94 -> 3.93 ms).
