@@ -766,7 +766,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             if (tid < 64) {
                 const float l = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
                 l_acc[tid] = l;
-                alpha[tid] = l > 0.f ? 1.f / l : 0.f;
+                alpha[tid] = l > 0.f ? 1.f / l : 0.f;       // its place is free until the next references
             }
             work_sync();
             const int64_t unit = 2 * (int64_t)blockIdx.x + (piece++ == 0 ? 0 : 1);   // a share's first piece, or its last

@@ -282,7 +282,7 @@ __device__ __forceinline__ int walk_free(Counts c, int32_t* ref, int64_t num_pag
             found += mine;
         }
         const int64_t page0 = base + (int64_t)blockIdx.x * kStep;
-        const int takes = min(mine, want - rank0);
+        const int takes = max(0, min(mine, want - rank0));
         // a warp takes consecutive pages for consecutive entries, four round trips at a time
         const int chunk = (takes + kPoolThreads - 1) / kPoolThreads * 32, end = min(takes, ((tid >> 5) + 1) * chunk);
         int owner = 0;
