@@ -40,10 +40,10 @@
 // prefetches the pages into L2.
 // Every wait is time-bounded; a timeout is recorded and the CTA winds down.
 //
-// What bounds it (64 tree rows in each of 8 requests of up to 32K tokens: 2.86 ms, 690
-// TFLOP/s; 2048 rows with a window of 2048: 0.94 ms, 624 TFLOP/s; one row in each of 4
-// requests with a window of 131072: 132 us, 2.6 TB/s): the workers.  A tile takes about
-// 7,000 cycles, of which the tensor core is busy 3,300.  The workers issue 695
+// What bounds it (64 tree rows in each of 8 requests of up to 32K tokens: 2.78 ms, 709
+// TFLOP/s; 2048 rows with a window of 2048: 0.93 ms, 632 TFLOP/s; one row in each of 4
+// requests with a window of 131072: 129 us, 2.7 TB/s): the workers.  A tile takes about
+// 6,800 cycles, of which the tensor core is busy 3,300.  The workers issue 695
 // instructions per warp and tile, mostly conversions and fp16 products of the
 // dequantisation at half rate, and 4,300 passes through the load/store pipe (1,400 for
 // the fp16 tile's stores, 1,900 for the rows' loads), one phase after the other: without
