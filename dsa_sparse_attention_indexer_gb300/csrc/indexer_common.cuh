@@ -15,7 +15,7 @@ struct BatchDev {
     const int32_t* seq_len;
     const int32_t* q_start;
     const int32_t* page_table;
-    uint64_t wait_ns;      // limit of the decode score kernel's pipeline waits (normally 2 s)
+    uint64_t wait_ns;      // limit of the pipeline waits of the decode score and the dense MLA kernel (normally 2 s)
 };
 
 inline BatchDev to_dev(const dsa_batch* b) {

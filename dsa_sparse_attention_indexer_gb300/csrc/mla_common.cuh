@@ -24,12 +24,14 @@ __device__ __forceinline__ bool bar_any(bool pred) {
 }
 
 // mbarrier wait that also gives up when another role has set the abort flag.
-__device__ __forceinline__ bool wait_ab(uint64_t* bar, uint32_t parity, const volatile int32_t* abort_flag) {
+__device__ __forceinline__ bool wait_ab(uint64_t* bar, uint32_t parity, const volatile int32_t* abort_flag,
+                                        uint64_t limit_ns = 2000000000ull) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (limit_ns == 0) return false;                       // no waiting at all
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-        if ((it & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > 2000000000ull)) return false;
+        if ((it & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > limit_ns)) return false;
     }
 }
 

@@ -340,6 +340,8 @@ dense_mla_kernel(const __grid_constant__ Args a) {
         }
         mbar_init(&bars[B_DRAIN], 1);
         misc->abort = 0;
+        // what a worker finds whose wait for a tile ran out: pages of the cache or none, at any time
+        for (int i = 0; i < kAhead; ++i) misc->tile[i] = Tile{{0, 0}, {-1, -1}, 0};
         fence_barrier_init();
     }
     if (warp == 0) {
@@ -369,6 +371,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
         record_error(a.st, DSA_DEVERR_TIMEOUT, where);
         *abort_flag = 1;
     };
+    auto wait = [&](int bar, uint32_t parity) { return wait_ab(&bars[bar], parity, abort_flag, b.wait_ns); };
 
     if (warp >= kMmaWarp) {
         fewer_registers<kMmaRegs>();
@@ -385,12 +388,12 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                 const uint32_t ph = (uint32_t)(n & 1);
                 bool first = false;
                 if (lane == 0) {
-                    ok = wait_ab(&bars[B_AIM0 + n % kAhead], (uint32_t)(n / kAhead & 1), abort_flag);
-                    first = reinterpret_cast<volatile Tile*>(misc->tile)[n % kAhead].row & T_FIRST;
+                    ok = ok && wait(B_AIM0 + n % kAhead, (uint32_t)(n / kAhead & 1));
+                    if (ok) first = reinterpret_cast<volatile Tile*>(misc->tile)[n % kAhead].row & T_FIRST;
                     mbar_arrive(&bars[B_FREE0 + n % kAhead]);
-                    if (ok && first) ok = wait_ab(&bars[B_QFULL], (uint32_t)(k++ & 1), abort_flag);
+                    if (ok && first) ok = wait(B_QFULL, (uint32_t)(k++ & 1));
                     auto next = [&](int bar) {
-                        if (ok) ok = wait_ab(&bars[bar], ph, abort_flag);
+                        ok = ok && wait(bar, ph);
                         tc_fence_after();
                         return ok;
                     };
@@ -431,7 +434,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             for (int n = 0; n < n_mine; ++n) {
                 // until the workers and the MMA warp have read the slot's last tile (a phase that
                 // counts as over the first time round)
-                ok = __all_sync(0xffffffffu, wait_ab(&bars[B_FREE0 + n % kAhead], (uint32_t)(n / kAhead + 1 & 1), abort_flag));
+                ok = __all_sync(0xffffffffu, wait(B_FREE0 + n % kAhead, (uint32_t)(n / kAhead + 1 & 1)));
                 if (!ok) break;
                 Tile* tile = &misc->tile[n % kAhead];
                 const int u = 2 * t + lane;
@@ -501,7 +504,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
         const uint8_t* src[2] = {};                        // of the tile in flight
         int32_t slot_next[2] = {};                         // of the one after it, as cache slots
         auto aim = [&](int x) {                            // lays slot_next, row_next, .. on tile x
-            ok = wait_ab(&bars[B_AIM0 + x % kAhead], (uint32_t)(x / kAhead & 1), abort_flag) && ok;
+            ok = wait(B_AIM0 + x % kAhead, (uint32_t)(x / kAhead & 1)) && ok;   // if not: an older tile, or none
             const Tile* tile = &misc->tile[x % kAhead];
             row_next = tile->row;
             valid_next = tile->seen[q4 >> 1] >> (st & 63) & 1u;
@@ -553,7 +556,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             };
             auto group = [&](auto gi) {
                 constexpr int gg = decltype(gi)::value;
-                ok = wait_ab(&bars[B_PV0 + gg], ph, abort_flag) && ok;
+                ok = wait(B_PV0 + gg, ph) && ok;
                 auto put_row = [&](auto hi) {
                     // 16 FP8 dims 128 gg + 16 c8 .. -> K-block 2 gg + c8 / 4, 16-byte chunks 2 (c8 % 4) + c8 / 4, and its neighbour
                     constexpr int h = decltype(hi)::value, kOff = 2 * gg * kBlk + h * kPage * 128;
@@ -657,7 +660,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
         for (;; ++n) {
             const uint32_t done = row;                      // row and flags of this tile
             // ---- softmax of tile n
-            ok = wait_ab(&bars[B_SFULL], (uint32_t)(n & 1), abort_flag) && ok;
+            ok = wait(B_SFULL, (uint32_t)(n & 1)) && ok;
             // a token that is not seen takes -inf for its references: every P is 0
             const float4* nr4 = reinterpret_cast<const float4*>(valid ? neg_ref + hh * kHeads : neg_inf);
             uint32_t most;                                  // largest P of the thread, as two fp16
@@ -705,6 +708,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                 tc_fence_after();
                 if (vote(!ok)) {
                     if (tid == 0) timeout(63);
+                    cp_async_wait_all();                    // a next row's Q may be on its way
                     break;
                 }
                 load_s(v);
@@ -756,7 +760,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             }
             if (!(done & T_LAST)) continue;
             // ---- the piece's output: O^T is final when its last P.V has completed
-            ok = wait_ab(&bars[B_PV3], (uint32_t)(n & 1), abort_flag) && ok;
+            ok = wait(B_PV3, (uint32_t)(n & 1)) && ok;
             if (n + 1 == n_mine) pdl_trigger();             // the merge's blocks may take their places
             xreduce16<false>(lsum, lane);
             if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = lsum[0];

@@ -318,3 +318,24 @@ def test_binding_refuses_short_and_foreign_tensors():
         D.dsa_tree_mla(c["dq"], torch.zeros(0, dtype=torch.int64, device=DEV), c["kv"], c["batch"])
     with pytest.raises(D.DsaError):
         D.dsa_window_mla(c["dq"], c["kv"], c["batch"], window=0)
+
+
+@pytest.mark.parametrize("seq,q_len,window", [([100], [1], 100), ([40000, 900], [1, 2], 39000), ([700, 0, 600], [300, 0, 64], 260)])
+def test_a_wait_that_runs_out_is_recorded_and_nothing_else_is_touched(seq, q_len, window):
+    """With no time to wait, the kernel winds down from its first tile on: it reads no tile that was not
+    laid out, leaves rows behind the last request alone, and the next call is right."""
+    c = window_case(81, seq, q_len, window, 0, pad_rows=3)
+    n = c["T"]
+    for _ in range(3):
+        st = D.new_device_status(DEV)
+        out = torch.full((n + 3, 64, 512), SENTINEL, device=DEV)
+        lse = torch.full((n + 3, 64), SENTINEL, device=DEV)
+        try:
+            D.dsa_debug_set_wait_limit_ns(0)
+            D.dsa_window_mla(c["dq"], c["kv"], c["batch"], window=window, out=out, out_dtype=D.DTYPE_F32, lse=lse, dev_status=st)
+            torch.cuda.synchronize()
+        finally:
+            D.dsa_debug_set_wait_limit_ns(2_000_000_000)
+        assert D.dsa_device_status_read(st)[0] == D.DEVERR_TIMEOUT
+        assert (out[n:] == SENTINEL).all() and (lse[n:] == SENTINEL).all()
+        compare(c, *run(c, window_call(window, 0)))
