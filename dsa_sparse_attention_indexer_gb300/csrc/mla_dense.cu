@@ -83,12 +83,12 @@ struct Args {
     const uint8_t* kv;          // latent cache
     BatchDev b;
     View view;
-    float scale_log2;
+    float scale;
     void* out;
     int out_f32;
     float* lse;
     float* part_o;              // [2 G, 16, 512, 4]: unnormalised outputs of cut rows, two pieces per share, four heads side by side
-    float2* part_ml;            // [2 G, 64]: reference (log2 units), sum
+    float2* part_ml;            // [2 G, 64]: log2 of what P was scaled by, sum
     Meta* meta;          // [G]
     int32_t* st;
 };
@@ -177,9 +177,9 @@ constexpr int kThreads = (kWorkWarps + 4) * 32;            // five warpgroups; t
 constexpr int kWorkBar = 1, kVoteBar = 2;                  // workers; workers and the MMA warp
 constexpr int kAhead = 4;                                  // tiles laid out ahead
 constexpr float kTau = 12.0f;                              // lazy-rescale threshold, log2 units
-constexpr float kShift = 3.0f;                             // P is scaled by 2^3 ..
-constexpr uint32_t kPMaxH = 0x7800;                        // .. so at most 2^(kTau + kShift) = 2^15, as fp16 bits
-constexpr float kNoRef = 0x1p100f;                         // minus the reference of a head without one: P of any score is inf
+constexpr float kShift = 3.0f;                             // P of a score at its reference is 2^3 ..
+constexpr uint32_t kPMaxH = 0x7800;                        // .. and of any at most 2^(kTau + kShift) = 2^15, as fp16 bits
+constexpr float kNoRef = INFINITY;                         // minus the reference of a head without one: P of any score is inf
 constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
 constexpr uint32_t kIdescPV = idesc_f16_f32(128, 64, true, true);
 constexpr uint32_t kColS = 0;                              // TMEM: S^T [128 x 64]
@@ -321,7 +321,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
     Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc);
     float* red = reinterpret_cast<float*>(smem + kOffRed);
-    float* neg_ref = reinterpret_cast<float*>(smem + kOffStat);   // minus the heads' references, log2 units
+    float* neg_ref = reinterpret_cast<float*>(smem + kOffStat);   // minus the heads' references, scores of the scaled Q
     float* l_acc = neg_ref + 64;
     float* alpha = l_acc + 64;
     float* neg_inf = alpha + 64;
@@ -639,7 +639,8 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_QFULL]);
-            return a.scale_log2 * __int_as_float((127 - kq) << 23);
+            // neither 0 nor inf: differences of scores are multiplied by it that may be inf or 0
+            return fminf(fmaxf(a.scale * __int_as_float((127 - kq) << 23) * 1.4426950408889634f, 0x1p-126f), 0x1.fffffep127f);
         };
 
         float lsum[kHeads];                                // this token lane's running sums of its heads
@@ -672,20 +673,27 @@ dense_mla_kernel(const __grid_constant__ Args a) {
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) v[h] = __uint_as_float(x[h]);
             };
-            // P of the current references, and its P^T row (heads 16 hh.. as fp16, MN-major swizzle)
+            // P of the current references, and its P^T row (heads 16 hh.. as fp16, MN-major swizzle).
+            // P = 2^((S - reference) sl2 + kShift), with references that are scores: the difference of
+            // near ones is exact however large they are.
             auto write_p = [&](float (&v)[kHeads]) {
                 most = 0;
                 auto eight = [&](auto ci) {
                     constexpr int c = decltype(ci)::value * 8;
                     const float4 m0 = nr4[c / 4], m1 = nr4[c / 4 + 1];
-                    v[c] = ex2_approx(fmaf(v[c], sl2, m0.x));
-                    v[c + 1] = ex2_approx(fmaf(v[c + 1], sl2, m0.y));
-                    v[c + 2] = ex2_approx(fmaf(v[c + 2], sl2, m0.z));
-                    v[c + 3] = ex2_approx(fmaf(v[c + 3], sl2, m0.w));
-                    v[c + 4] = ex2_approx(fmaf(v[c + 4], sl2, m1.x));
-                    v[c + 5] = ex2_approx(fmaf(v[c + 5], sl2, m1.y));
-                    v[c + 6] = ex2_approx(fmaf(v[c + 6], sl2, m1.z));
-                    v[c + 7] = ex2_approx(fmaf(v[c + 7], sl2, m1.w));
+                    const float2 s2 = make_float2(sl2, sl2), k2 = make_float2(kShift, kShift);
+                    const float2 x0 = add_scale2(make_float2(v[c], v[c + 1]), make_float2(m0.x, m0.y), s2, k2);
+                    const float2 x1 = add_scale2(make_float2(v[c + 2], v[c + 3]), make_float2(m0.z, m0.w), s2, k2);
+                    const float2 x2 = add_scale2(make_float2(v[c + 4], v[c + 5]), make_float2(m1.x, m1.y), s2, k2);
+                    const float2 x3 = add_scale2(make_float2(v[c + 6], v[c + 7]), make_float2(m1.z, m1.w), s2, k2);
+                    v[c] = ex2_approx(x0.x);
+                    v[c + 1] = ex2_approx(x0.y);
+                    v[c + 2] = ex2_approx(x1.x);
+                    v[c + 3] = ex2_approx(x1.y);
+                    v[c + 4] = ex2_approx(x2.x);
+                    v[c + 5] = ex2_approx(x2.y);
+                    v[c + 6] = ex2_approx(x3.x);
+                    v[c + 7] = ex2_approx(x3.y);
                     const uint32_t h0 = pack_h2(v[c], v[c + 1]), h1 = pack_h2(v[c + 2], v[c + 3]);
                     const uint32_t h2 = pack_h2(v[c + 4], v[c + 5]), h3 = pack_h2(v[c + 6], v[c + 7]);
                     st_shared_v4(p_at ^ (c * 2), h0, h1, h2, h3);
@@ -713,15 +721,15 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                 }
                 load_s(v);
 #pragma unroll
-                for (int c = 0; c < kHeads; ++c) v[c] = valid ? v[c] * sl2 : -INFINITY;
+                for (int c = 0; c < kHeads; ++c) v[c] = valid ? v[c] : -INFINITY;
                 xreduce16<true>(v, lane);                   // per-head tile max (consumes v)
                 if (lane < kHeads) red[q4 * 64 + hh * kHeads + lane] = v[0];
                 work_sync();
                 if (tid < 64) {
-                    const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid])) - kShift;
+                    const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
                     const float mo = -neg_ref[tid];
-                    const bool need = tm > mo + kTau;
-                    alpha[tid] = need ? exp2f(mo - tm) : 1.f;          // 0 for a first reference
+                    const bool need = (tm - mo) * sl2 > kTau;          // no: -inf, or NaN where both are -inf
+                    alpha[tid] = need ? exp2f((mo - tm) * sl2) : 1.f;  // 0 for a first reference
                     if (need) neg_ref[tid] = -tm;
                 }
                 work_sync();
@@ -806,8 +814,9 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             tc_fence_before();
             if (tid < 64) {
                 const float l = l_acc[tid];
-                if (!(done & T_WHOLE)) a.part_ml[unit * 64 + tid] = make_float2(-neg_ref[tid], l);
-                else if (a.lse) a.lse[(int64_t)(done >> 3) * 64 + tid] = l > 0.f ? (log2f(l) - neg_ref[tid]) * 0.69314718055994531f : -INFINITY;
+                const float ref = fmaf(-neg_ref[tid], sl2, -kShift);   // in log2 units; P was scaled by 2^-ref
+                if (!(done & T_WHOLE)) a.part_ml[unit * 64 + tid] = make_float2(ref, l);
+                else if (a.lse) a.lse[(int64_t)(done >> 3) * 64 + tid] = l > 0.f ? (log2f(l) + ref) * 0.69314718055994531f : -INFINITY;
                 neg_ref[tid] = kNoRef;
             }
             if (n + 1 == n_mine) {
@@ -971,7 +980,7 @@ static dsa_status launch(const void* q, const uint8_t* kv, const dsa_batch* b, V
     a.kv = kv;
     a.b = to_dev(b);
     a.view = view;
-    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.scale = softmax_scale;
     a.out = out;
     a.out_f32 = out_dtype == DSA_DTYPE_F32;
     a.lse = lse;

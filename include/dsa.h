@@ -480,7 +480,7 @@ dsa_status dsa_topk_share_mtp_end(dsa_topk_share* s);
  *   out_ih = sum_j softmax_j(S_hj) c_j,  lse_ih = log sum_j exp(S_hj)
  * A row that sees nothing gives out = 0 and lse = -inf.  Softmax statistics and
  * accumulation are fp32; probabilities are rounded to fp16 for the product with
- * the latents, as in sparse MLA.
+ * the latents, as in sparse MLA.  Scores may have any magnitude that fp32 holds.
  * dsa_window_mla: j <= p and (j < sinks or j > p - window): the last `window`
  *   positions up to the row's own, and the context's first `sinks`.
  *   window >= 1, sinks >= 0; window >= max_seq_len is causal attention over the

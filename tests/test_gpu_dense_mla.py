@@ -339,3 +339,39 @@ def test_a_wait_that_runs_out_is_recorded_and_nothing_else_is_touched(seq, q_len
         assert D.dsa_device_status_read(st)[0] == D.DEVERR_TIMEOUT
         assert (out[n:] == SENTINEL).all() and (lse[n:] == SENTINEL).all()
         compare(c, *run(c, window_call(window, 0)))
+
+
+LARGE = [(1.0 / 16, 1e8), (1.0 / 16, 1e9), (1.0 / 16, 1e12), (1.0 / 16, 1e30), (1.0 / 16, 1e33), (1.0 / 16, 1e36), (3e38, 1e-36), (1e30, 1e-6)]
+
+
+@pytest.mark.parametrize("scale,q_scale", LARGE)
+def test_large_scores_of_one_position(scale, q_scale):
+    """A row that sees one position gives its latent (P's fp16 rounding aside) and its score, however
+    large and of either sign: |S| up to 1e37."""
+    c = window_case(7, [90, 300], [1, 2], 1, 0, q_scale=q_scale)
+    out, lse = (f64(x) for x in run(c, window_call(1, 0), scale=scale))
+    for i, (_, kv) in enumerate(c["rows"]):
+        q = f64(c["q"][i])
+        s, mag = scale * (q @ kv[0]), scale * (np.abs(q) @ np.abs(kv[0]))
+        assert (np.abs(out[i] - kv[:, :512]) <= (2.0 ** -11 + 2.0 ** -18) * np.abs(kv[:, :512])).all(), f"row {i}"
+        assert (np.abs(lse[i] - s) <= 40 * 2.0 ** -23 * mag + 2.0 ** -22 * np.abs(s) + 2.0 ** -20).all(), f"row {i}"
+
+
+@pytest.mark.parametrize("scale,q_scale", LARGE)
+def test_large_scores_of_many_positions(scale, q_scale):
+    """Where the largest score leads by more than the scores' own error, its latent is the output, in
+    whole rows and in rows that several shares hold; no head is without a number."""
+    c = window_case(9, [700, 40000], [2, 1], 20000, 3, q_scale=q_scale)
+    out, lse = (f64(x) for x in run(c, window_call(20000, 3), scale=scale))
+    sure = 0
+    for i, (_, kv) in enumerate(c["rows"]):
+        q = f64(c["q"][i])
+        s = scale * (q @ kv.T)
+        dS = 40 * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(kv).T).max(1)
+        top = np.sort(s, 1)[:, -2:]
+        assert np.isfinite(out[i]).all() and (np.abs(lse[i] - top[:, 1]) <= dS + 2.0 ** -22 * np.abs(top[:, 1]) + 12).all(), f"row {i}"
+        for h in np.nonzero(top[:, 1] - top[:, 0] > 2 * dS + 60)[0]:
+            best = kv[s[h].argmax(), :512]
+            assert (np.abs(out[i, h] - best) <= (2.0 ** -11 + 2.0 ** -18) * np.abs(best) + 2.0 ** -60).all(), f"row {i}, head {h}"
+            sure += 1
+    assert sure > 100
