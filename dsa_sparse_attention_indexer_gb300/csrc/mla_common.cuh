@@ -67,13 +67,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
-// (a + b) * s + c for two values in two instructions.
-__device__ __forceinline__ float2 add_scale2(float2 a, float2 b, float2 s, float2 c) {
+// (a + b) * s for two values in two instructions.
+__device__ __forceinline__ float2 add_scale2(float2 a, float2 b, float2 s) {
     float2 r;
-    asm("{\n .reg .b64 a, b, s, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 s, {%6, %7};\n mov.b64 c, {%8, %9};\n"
-        " add.rn.f32x2 a, a, b;\n fma.rn.f32x2 a, a, s, c;\n mov.b64 {%0, %1}, a;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(s.x), "f"(s.y), "f"(c.x), "f"(c.y));
+    asm("{\n .reg .b64 a, b, s;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 s, {%6, %7};\n"
+        " add.rn.f32x2 a, a, b;\n mul.rn.f32x2 a, a, s;\n mov.b64 {%0, %1}, a;\n}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(s.x), "f"(s.y));
     return r;
 }
 

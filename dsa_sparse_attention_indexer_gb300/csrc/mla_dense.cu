@@ -24,9 +24,8 @@
 //
 // Warps 0-15 (workers) do what a tile's phases ask for one after the other:
 //   softmax     a thread owns one token (TMEM lane) and 16 heads.  P is formed
-//               against a reference that lags the maximum by up to 2^12 before
-//               O^T is rescaled, and shifted up by 2^3, so that fp16 holds
-//               probabilities down to 2^-28 of the reference;
+//               against a reference per head that is renewed, and O^T rescaled,
+//               only when a P passes 2^15, and once behind a piece's first tiles;
 //   next tile   its rows, read into registers two groups ahead, are dequantised into the
 //               128-byte-swizzled tile (exact for scales in [2^-15, 2^7]), each
 //               part as soon as it is free.  Rows that are not seen become zeros or
@@ -88,7 +87,7 @@ struct Args {
     int out_f32;
     float* lse;
     float* part_o;              // [2 G, 16, 512, 4]: unnormalised outputs of cut rows, two pieces per share, four heads side by side
-    float2* part_ml;            // [2 G, 64]: log2 of what P was scaled by, sum
+    float2* part_ml;            // [2 G, 64]: reference (log2 units), sum
     Meta* meta;          // [G]
     int32_t* st;
 };
@@ -176,9 +175,18 @@ constexpr int kAimWarp = kMmaWarp + 1;
 constexpr int kThreads = (kWorkWarps + 4) * 32;            // five warpgroups; the last one issues the MMAs and lays out the tiles
 constexpr int kWorkBar = 1, kVoteBar = 2;                  // workers; workers and the MMA warp
 constexpr int kAhead = 4;                                  // tiles laid out ahead
-constexpr float kTau = 12.0f;                              // lazy-rescale threshold, log2 units
-constexpr float kShift = 3.0f;                             // P of a score at its reference is 2^3 ..
-constexpr uint32_t kPMaxH = 0x7800;                        // .. and of any at most 2^(kTau + kShift) = 2^15, as fp16 bits
+// P is held in fp16 against a reference per head, renewed when a P passes 2^kTau.  A first
+// reference puts the largest P at 2^kFirst, which leaves a head room to grow.  Behind kSettle
+// tiles of a piece, references move down to where the sum of the P so far is 2^kSettled, so
+// that behind a dominating position the many small ones keep their bits: P is off by 2^-11 of
+// itself or by 2^-25, which is 2^-28 of the sum in the first tiles and 2^-34 in all others:
+// 4096 times 2^-28 and a million times 2^-34 are 2^-14 of the largest latent together.
+// (Settled after 8 tiles, prefill with 17 tiles a row takes 952 us instead of 917; with
+// references that put every tile's largest P at 2^9, or its sum at 2^8, flat heads
+// outgrow them tile after tile: 1077 and 993 us.)
+constexpr float kTau = 15.0f, kFirst = 3.0f, kSettled = 9.0f;
+constexpr int kSettle = 32;
+constexpr uint32_t kPMaxH = 0x7800;                        // 2^kTau as fp16 bits
 constexpr float kNoRef = INFINITY;                         // minus the reference of a head without one: P of any score is inf
 constexpr uint32_t kIdescQK = idesc_f16_f32(128, 64, false, false);
 constexpr uint32_t kIdescPV = idesc_f16_f32(128, 64, true, true);
@@ -207,9 +215,11 @@ static_assert(B_COUNT <= 24, "barrier block");
 struct Tile {
     uint64_t seen[2];
     int32_t page[2];            // -1: no position of the page is seen, or it is outside the cache
-    uint32_t row;               // row x 8 + FIRST, LAST tile of the piece; WHOLE: the piece is the whole row
+    uint32_t row;               // row << kRowShift | flags: FIRST, LAST tile of the piece; WHOLE: the piece is the whole row;
+                                // SETTLE: its tile kSettle, LATE: that one or a later one
 };
-enum { T_FIRST = 1, T_LAST = 2, T_WHOLE = 4 };
+enum { T_FIRST = 1, T_LAST = 2, T_WHOLE = 4, T_SETTLE = 8, T_LATE = 16 };
+constexpr int kRowShift = 5;
 
 struct Misc {
     uint32_t tmem_base;
@@ -430,7 +440,8 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             bool ok = true;
             int row = row_begin, t = tile_begin;
             Row w = row_view(b, a.view, row, lane == 0 ? a.st : nullptr);
-            bool first = true, cut = t > 0;                // the piece's first tile; the row began in an earlier share
+            bool cut = t > 0;                              // the row began in an earlier share
+            int at = 0;                                    // of the piece's tiles
             for (int n = 0; n < n_mine; ++n) {
                 // until the workers and the MMA warp have read the slot's last tile (a phase that
                 // counts as over the first time round)
@@ -458,11 +469,12 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                 }
                 if (lane == 0) {
                     const bool last = end_of_row || n + 1 == n_mine;
-                    tile->row = (uint32_t)row << 3 | (first ? T_FIRST : 0) | (last ? T_LAST : 0) | (last && end_of_row && !cut ? T_WHOLE : 0);
+                    tile->row = (uint32_t)row << kRowShift | (at == 0 ? T_FIRST : 0) | (last ? T_LAST : 0) |
+                                (last && end_of_row && !cut ? T_WHOLE : 0) | (at == kSettle ? T_SETTLE : 0) | (at >= kSettle ? T_LATE : 0);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_AIM0 + n % kAhead]);
-                first = end_of_row;
+                at = end_of_row ? 0 : at + 1;
                 ++t;
                 if (end_of_row && n + 1 < n_mine) {
                     ++row;
@@ -674,18 +686,18 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                 for (int h = 0; h < kHeads; ++h) v[h] = __uint_as_float(x[h]);
             };
             // P of the current references, and its P^T row (heads 16 hh.. as fp16, MN-major swizzle).
-            // P = 2^((S - reference) sl2 + kShift), with references that are scores: the difference of
-            // near ones is exact however large they are.
+            // P = 2^((S - reference) sl2), with references of the scores' kind: the difference of near
+            // ones is exact however large they are.
             auto write_p = [&](float (&v)[kHeads]) {
                 most = 0;
                 auto eight = [&](auto ci) {
                     constexpr int c = decltype(ci)::value * 8;
                     const float4 m0 = nr4[c / 4], m1 = nr4[c / 4 + 1];
-                    const float2 s2 = make_float2(sl2, sl2), k2 = make_float2(kShift, kShift);
-                    const float2 x0 = add_scale2(make_float2(v[c], v[c + 1]), make_float2(m0.x, m0.y), s2, k2);
-                    const float2 x1 = add_scale2(make_float2(v[c + 2], v[c + 3]), make_float2(m0.z, m0.w), s2, k2);
-                    const float2 x2 = add_scale2(make_float2(v[c + 4], v[c + 5]), make_float2(m1.x, m1.y), s2, k2);
-                    const float2 x3 = add_scale2(make_float2(v[c + 6], v[c + 7]), make_float2(m1.z, m1.w), s2, k2);
+                    const float2 s2 = make_float2(sl2, sl2);
+                    const float2 x0 = add_scale2(make_float2(v[c], v[c + 1]), make_float2(m0.x, m0.y), s2);
+                    const float2 x1 = add_scale2(make_float2(v[c + 2], v[c + 3]), make_float2(m0.z, m0.w), s2);
+                    const float2 x2 = add_scale2(make_float2(v[c + 4], v[c + 5]), make_float2(m1.x, m1.y), s2);
+                    const float2 x3 = add_scale2(make_float2(v[c + 6], v[c + 7]), make_float2(m1.z, m1.w), s2);
                     v[c] = ex2_approx(x0.x);
                     v[c + 1] = ex2_approx(x0.y);
                     v[c + 2] = ex2_approx(x1.x);
@@ -705,14 +717,14 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             };
             float v[kHeads];
             tc_fence_after();
-            if (n + 1 < n_mine && (row_next & T_FIRST)) fetch_q((int)(row_next >> 3));
+            if (n + 1 < n_mine && (row_next & T_FIRST)) fetch_q((int)(row_next >> kRowShift));
             load_s(v);
             write_p(v);
-            // ---- a score above its head's reference by more than 2^kTau (P above 2^(kTau + kShift))
+            // ---- a score above its head's reference by more than 2^kTau
             //      makes every warp take new references (always on the piece's first tile)
             const bool over = (most & 0xffffu) > kPMaxH || most >> 16 > kPMaxH;
             tc_fence_before();
-            if (vote(over || !ok)) {
+            if (vote(over || (done & T_SETTLE) || !ok)) {
                 tc_fence_after();
                 if (vote(!ok)) {
                     if (tid == 0) timeout(63);
@@ -724,13 +736,30 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                 for (int c = 0; c < kHeads; ++c) v[c] = valid ? v[c] : -INFINITY;
                 xreduce16<true>(v, lane);                   // per-head tile max (consumes v)
                 if (lane < kHeads) red[q4 * 64 + hh * kHeads + lane] = v[0];
+                if (done & T_SETTLE) {                      // the sums so far
+#pragma unroll
+                    for (int c = 0; c < kHeads; ++c) v[c] = lsum[c];
+                    xreduce16<false>(v, lane);
+                    if (lane < kHeads) red[256 + q4 * 64 + hh * kHeads + lane] = v[0];
+                }
                 work_sync();
                 if (tid < 64) {
                     const float tm = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
-                    const float mo = -neg_ref[tid];
-                    const bool need = (tm - mo) * sl2 > kTau;          // no: -inf, or NaN where both are -inf
-                    alpha[tid] = need ? exp2f((mo - tm) * sl2) : 1.f;  // 0 for a first reference
-                    if (need) neg_ref[tid] = -tm;
+                    const float mo = -neg_ref[tid], d = (tm - mo) * sl2;   // d: -inf where the tile saw nothing (NaN if none did)
+                    float from = mo, down = 0.f;            // a renewed reference is `from`, `down` log2 units lower
+                    if (d > kTau) {
+                        from = tm;
+                        down = (done & T_LATE) ? kSettled : kFirst;
+                    } else if ((done & T_SETTLE) && mo > -INFINITY) {
+                        const float l = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
+                        down = kSettled - fmaxf(log2f(l), d);   // this tile's P stay below 2^kSettled too
+                    }
+                    alpha[tid] = 1.f;
+                    if (down > 0.f) {                       // rounded up: never further down; finite for the smallest sl2
+                        const float mr = __fsub_ru(from, fminf(down / sl2, 0x1p64f));
+                        alpha[tid] = exp2f((mo - mr) * sl2);   // 0 for a first reference
+                        neg_ref[tid] = -mr;
+                    }
                 }
                 work_sync();
                 bool mine = false;                          // does a head of this warp have a new reference
@@ -763,7 +792,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             // ---- the next row's Q and the next tile
             float sl2_next = sl2;
             if (n + 1 < n_mine) {
-                if (row_next & T_FIRST) sl2_next = put_q((int)(row_next >> 3));
+                if (row_next & T_FIRST) sl2_next = put_q((int)(row_next >> kRowShift));
                 put_tile(n + 1);
             }
             if (!(done & T_LAST)) continue;
@@ -800,7 +829,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                     const float inv = alpha[hh * kHeads + c];
                     o[c] = inv > 0.f ? __float_as_uint(__uint_as_float(o[c]) * inv) : 0u;
                 }
-                const int64_t at = ((int64_t)(done >> 3) * 64 + hh * kHeads) * 512;
+                const int64_t at = ((int64_t)(done >> kRowShift) * 64 + hh * kHeads) * 512;
                 if (a.out_f32) {
                     float* to = static_cast<float*>(a.out) + at + d;
 #pragma unroll
@@ -814,9 +843,9 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             tc_fence_before();
             if (tid < 64) {
                 const float l = l_acc[tid];
-                const float ref = fmaf(-neg_ref[tid], sl2, -kShift);   // in log2 units; P was scaled by 2^-ref
+                const float ref = -neg_ref[tid] * sl2;                 // in log2 units
                 if (!(done & T_WHOLE)) a.part_ml[unit * 64 + tid] = make_float2(ref, l);
-                else if (a.lse) a.lse[(int64_t)(done >> 3) * 64 + tid] = l > 0.f ? (log2f(l) + ref) * 0.69314718055994531f : -INFINITY;
+                else if (a.lse) a.lse[(int64_t)(done >> kRowShift) * 64 + tid] = l > 0.f ? (log2f(l) + ref) * 0.69314718055994531f : -INFINITY;
                 neg_ref[tid] = kNoRef;
             }
             if (n + 1 == n_mine) {
@@ -967,8 +996,8 @@ static dsa_status launch(const void* q, const uint8_t* kv, const dsa_batch* b, V
     if (b->total_q == 0) return DSA_OK;
     if (!q || !kv || !out) return DSA_ERR_INVALID_ARGUMENT;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(out)) return DSA_ERR_ALIGNMENT;
-    // 32-bit tile counts of a share, rows with three flags in a word
-    if (b->total_q * most_tiles(b, view) / device_sm_count() > 0x7ffffff0LL || b->total_q > 0x1fffffffLL) return DSA_ERR_UNSUPPORTED;
+    // 32-bit tile counts of a share, rows with their flags in a word
+    if (b->total_q * most_tiles(b, view) / device_sm_count() > 0x7ffffff0LL || b->total_q >> (32 - kRowShift)) return DSA_ERR_UNSUPPORTED;
     if (!ws) return DSA_ERR_INVALID_ARGUMENT;
     if (bytes < ws_bytes(device_sm_count())) return DSA_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned16(ws)) return DSA_ERR_ALIGNMENT;

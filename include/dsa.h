@@ -479,8 +479,10 @@ dsa_status dsa_topk_share_mtp_end(dsa_topk_share* s);
  *   S_hj = softmax_scale * <q_ih, k_j>,  k_j = [c_j * scale | rope_j] (576 dims)
  *   out_ih = sum_j softmax_j(S_hj) c_j,  lse_ih = log sum_j exp(S_hj)
  * A row that sees nothing gives out = 0 and lse = -inf.  Softmax statistics and
- * accumulation are fp32; probabilities are rounded to fp16 for the product with
- * the latents, as in sparse MLA.  Scores may have any magnitude that fp32 holds.
+ * accumulation (16 positions a step) are fp32; probabilities are rounded to fp16
+ * for the product with the latents, as in sparse MLA: each is off by 2^-11 of
+ * itself, or, where it is small, by so little that a million of them make 2^-14
+ * of the largest latent.  Scores may have any magnitude that fp32 holds.
  * dsa_window_mla: j <= p and (j < sinks or j > p - window): the last `window`
  *   positions up to the row's own, and the context's first `sinks`.
  *   window >= 1, sinks >= 0; window >= max_seq_len is causal attention over the

@@ -375,3 +375,44 @@ def test_large_scores_of_many_positions(scale, q_scale):
             assert (np.abs(out[i, h] - best) <= (2.0 ** -11 + 2.0 ** -18) * np.abs(best) + 2.0 ** -60).all(), f"row {i}, head {h}"
             sure += 1
     assert sure > 100
+
+
+def test_a_long_tail_behind_a_dominating_sink():
+    """One position of zero latent whose score leads by 8 to 22 nats and 131,072 others, in so many rows
+    that a share holds whole ones: the output is the others'.  P of a position is off by 2^-11 of itself,
+    or by half of fp16's smallest step, 2^-25, against a sum of P of at least 2^3 in a piece's first 32
+    tiles of two pages and 2^9 behind them.  O is summed by the tensor core, 16 positions a step, each
+    off by at most 2^-23 of a partial sum: every latent is positive, so of the value, n / 16 times."""
+    g = torch.Generator(device=DEV).manual_seed(17)
+    rows, n = 304, 131072 + 304
+    lat = torch.randn(n, 512, generator=g, device=DEV).abs().to(torch.bfloat16)
+    rope = (0.05 * torch.randn(n, 64, generator=g, device=DEV)).to(torch.bfloat16)
+    lead = torch.where(torch.randn(64, generator=g, device=DEV) > 0, 1.0, -1.0)
+    lat[0], rope[0] = 0, lead.to(torch.bfloat16)
+    q = torch.zeros(rows, 64, 576, device=DEV)
+    q[:, :, 512:] = lead * torch.linspace(2.0, 5.5, 64, device=DEV)[:, None]    # times 64 / 16: 8 .. 22
+    q = q.to(torch.bfloat16)
+    pages = (n + 63) // 64
+    kv = torch.zeros(pages * D.KV_PAGE_BYTES, dtype=torch.uint8, device=DEV)
+    D.dsa_latent_kv_store(lat, rope, torch.arange(n, device=DEV), kv)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    batch = D.Batch(ints(n), ints(0, rows), table, pages, max_seq_len=n, max_q_len=rows, total_q=rows)
+    st = D.new_device_status(DEV)
+    lse = torch.empty(rows, 64, device=DEV)
+    out = D.dsa_window_mla(q, kv, batch, window=n, out_dtype=D.DTYPE_F32, lse=lse, dev_status=st).double()
+    assert D.dsa_device_status_read(st)[0] == 0
+    raw = kv.view(-1, 656)[:n]
+    k = raw[:, :512].contiguous().view(torch.float8_e4m3fn).double()
+    k = torch.cat([k * raw[:, 512:528].contiguous().view(torch.float32).double().repeat_interleave(128, 1), rope.double()], 1)
+    for i in (0, 1, 151, 302, 303):
+        kk = k[: n - rows + 1 + i]
+        s = q[i].double() @ kk.T / 16
+        z = torch.logsumexp(s, 1)
+        p = torch.exp(s - z[:, None])
+        want = p @ kk[:, :512]
+        dS = 40 * 2.0 ** -23 * (q[i].double().abs() @ kk.abs().T).amax(1) / 16
+        tol = want * (2.0 ** -11 + 2 * dS[:, None] + 2.0 ** -18 + n / 16 * 2.0 ** -23) + 2.0 ** -34 * kk[:, :512].sum(0) + 2.0 ** -28 * kk[:4096, :512].sum(0)
+        err = (out[i] - want).abs()
+        assert bool((err <= tol).all()), f"row {i}: worst {float((err / tol).max()):.1f} of the bound, {float((err / want).max()):.2%} of the value"
+        assert bool(((lse[i].double() - z).abs() <= dS + 2.0 ** -20 + 2.0 ** -22 * z.abs()).all())
