@@ -806,7 +806,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
             if (tid < 64) {
                 const float l = red[256 + tid] + red[320 + tid] + red[384 + tid] + red[448 + tid];
                 l_acc[tid] = l;
-                alpha[tid] = l > 0.f ? 1.f / l : 0.f;       // its place is free until the next references
+                alpha[tid] = l == 0.f ? 0.f : 1.f / l;      // its place is free until the next references
             }
             work_sync();
             const int64_t unit = 2 * (int64_t)blockIdx.x + (piece++ == 0 ? 0 : 1);   // a share's first piece, or its last
@@ -827,7 +827,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
 #pragma unroll
                 for (int c = 0; c < kHeads; ++c) {
                     const float inv = alpha[hh * kHeads + c];
-                    o[c] = inv > 0.f ? __float_as_uint(__uint_as_float(o[c]) * inv) : 0u;
+                    o[c] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);   // a NaN among what is seen stays one
                 }
                 const int64_t at = ((int64_t)(done >> kRowShift) * 64 + hh * kHeads) * 512;
                 if (a.out_f32) {
@@ -845,7 +845,7 @@ dense_mla_kernel(const __grid_constant__ Args a) {
                 const float l = l_acc[tid];
                 const float ref = -neg_ref[tid] * sl2;                 // in log2 units
                 if (!(done & T_WHOLE)) a.part_ml[unit * 64 + tid] = make_float2(ref, l);
-                else if (a.lse) a.lse[(int64_t)(done >> kRowShift) * 64 + tid] = l > 0.f ? (log2f(l) + ref) * 0.69314718055994531f : -INFINITY;
+                else if (a.lse) a.lse[(int64_t)(done >> kRowShift) * 64 + tid] = l == 0.f ? -INFINITY : (log2f(l) + ref) * 0.69314718055994531f;
                 neg_ref[tid] = kNoRef;
             }
             if (n + 1 == n_mine) {
@@ -929,7 +929,7 @@ dense_merge_kernel(const __grid_constant__ Args a, int G, int by_row) {
         auto load_ml = [&](int q0) {
             float2 ml = make_float2(-INFINITY, 0.f);
             if (q0 + (lane >> 2) < np) ml = __ldcg(a.part_ml + unit(q0 + (lane >> 2)) * 64 + h0 + (lane & 3));
-            if (!(ml.y > 0.f)) ml = make_float2(-INFINITY, 0.f);
+            if (ml.y == 0.f) ml.x = -INFINITY;
             return ml;
         };
         load_o(v, 0);
@@ -944,8 +944,8 @@ dense_merge_kernel(const __grid_constant__ Args a, int G, int by_row) {
         for (int q0 = 0; q0 < np; q0 += 8) {
             load_o(next, q0 + 8);
             ml_next = load_ml(q0 + 8);
-            const float w = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
-            L += w * ml.y;
+            const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
+            L += w * ml.y;                                 // NaN if any piece's sum is
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (q0 + j >= np) break;
@@ -962,7 +962,7 @@ dense_merge_kernel(const __grid_constant__ Args a, int G, int by_row) {
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        const float inv = L > 0.f ? 1.f / L : 0.f;         // lane % 4: head
+        const float inv = L == 0.f ? 0.f : 1.f / L;        // lane % 4: head
         const int64_t at = ((int64_t)row * 64 + h0) * 512 + d;
         const float x[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
@@ -972,7 +972,7 @@ dense_merge_kernel(const __grid_constant__ Args a, int G, int by_row) {
             else static_cast<__nv_bfloat16*>(a.out)[at + e * 512] = __float2bfloat16_rn(val);
         }
         if (a.lse && (part & 3) == 0 && tid < 4)
-            a.lse[(int64_t)row * 64 + h0 + tid] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+            a.lse[(int64_t)row * 64 + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
     }
 }
 

@@ -416,3 +416,22 @@ def test_a_long_tail_behind_a_dominating_sink():
         err = (out[i] - want).abs()
         assert bool((err <= tol).all()), f"row {i}: worst {float((err / tol).max()):.1f} of the bound, {float((err / want).max()):.2%} of the value"
         assert bool(((lse[i].double() - z).abs() <= dS + 2.0 ** -20 + 2.0 ** -22 * z.abs()).all())
+
+
+@pytest.mark.parametrize("what", ["latent", "rope"])
+@pytest.mark.parametrize("seq,window", [([300, 130], 200), ([30000, 130], 29000)])
+def test_a_nan_that_a_row_sees_shows(seq, window, what):
+    """Its row is NaN, in one share or several, never the zeros of a row that sees nothing."""
+    c = window_case(43, seq, [2, 1], window, 3)
+    at = seq[0] - 2 - window + 1                                     # the first row's first position, which the second does not see
+    kv = c["kv"].view(-1, 64, 656)
+    page = int(c["table"][0, at // 64])
+    if what == "latent":
+        kv[page, at % 64, 77] = 0x7f
+    else:
+        kv[page, at % 64, 528:530] = torch.tensor([0x7fc0], dtype=torch.int16).view(torch.uint8).to(DEV)
+    out, lse = run(c, window_call(window, 3), want_status=D.DEVERR_FP16_RANGE if what == "rope" else 0)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    for i in (1, 2):
+        ref, z, tol, ztol = reference(f64(c["q"][i]), c["rows"][i][1])
+        assert (np.abs(f64(out[i]) - ref) <= tol).all() and (np.abs(f64(lse[i]) - z) <= ztol).all()
