@@ -158,7 +158,8 @@ __device__ __forceinline__ Row row_view(const BatchDev& b, const View& v, int64_
     w.sink_end = min(v.sinks, end);
     w.sink_pages = w.sink_end / kPage + (w.sink_end % kPage != 0);
     w.first_page = max(w.sink_pages, w.first / kPage);
-    w.pages = max(1, w.sink_pages + max(0, (end + kPage - 1) / kPage - w.first_page));
+    const int last_page = end / kPage + (end % kPage != 0);        // end + 63 may pass 2^31
+    w.pages = max(1, w.sink_pages + max(0, last_page - w.first_page));
     return w;
 }
 

@@ -435,3 +435,19 @@ def test_a_nan_that_a_row_sees_shows(seq, window, what):
     for i in (1, 2):
         ref, z, tol, ztol = reference(f64(c["q"][i]), c["rows"][i][1])
         assert (np.abs(f64(out[i]) - ref) <= tol).all() and (np.abs(f64(lse[i]) - z) <= ztol).all()
+
+
+def test_contexts_up_to_the_largest_length():
+    """2^31 - 1 tokens, whose last page ends past what 32 bits hold, with all but the window's pages given back."""
+    L, window = 2 ** 31 - 1, 100
+    c = window_case(29, [200], [1], window, 0)                       # the positions 100 .. 199 of 200 become the last of L
+    kv = c["kv"].view(-1, 64, 656)
+    rows = torch.stack([kv[int(c["table"][0, j // 64]), j % 64] for j in range(100, 200)])
+    far = torch.full((3 * 64, 656), 0x7f, dtype=torch.uint8, device=DEV)
+    at = torch.arange(L - 100, L, device=DEV)
+    table = torch.full((1, 2 ** 25), -1, dtype=torch.int32, device=DEV)
+    table[0, 2 ** 25 - 2:] = torch.tensor([2, 0], dtype=torch.int32, device=DEV)
+    far[table[0, at // 64].long() * 64 + at % 64] = rows
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    c["kv"], c["batch"] = far.view(-1), D.Batch(ints(L), ints(0, 1), table, 3, max_seq_len=L, max_q_len=1, total_q=1)
+    compare(c, *run(c, window_call(window, 0)))
