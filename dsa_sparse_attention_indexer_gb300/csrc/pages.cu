@@ -216,6 +216,7 @@ struct PoolShared {
     };
     int scratch[32];
     int total[2][kPoolBlocks];                             // free pages of each block's round
+    int next;                                              // fill_rest: the first entry that got no page of the round's
 };
 
 struct Counts {
@@ -308,6 +309,46 @@ __device__ __forceinline__ int walk_free(Counts c, int32_t* ref, int64_t num_pag
     return min(found, want);
 }
 
+// Entries [e, total) that lack a page take, in order, the free pages that are left: those
+// that entries with a page of their own passed over.  By one block, behind a walk of all
+// that ended without a page for each entry.  Returns the first entry that was not looked at
+// with a page in hand.
+template <typename Entry>
+__device__ __noinline__ int fill_rest(int32_t* ref, int64_t num_pages, int e, int total, PoolShared& sh, Entry entry) {
+    const int tid = threadIdx.x;
+    for (int64_t base = 0; base < num_pages && e < total; base += kStep) {
+        uint32_t free = 0;                                 // of this thread's 16 counts
+        for (int u = 0; u < 16; ++u) {
+            const int64_t page = base + tid * 16 + u;
+            if (page < num_pages && __ldcg(ref + page) == 0) free |= 1u << u;
+        }
+        int mine;
+        int place = sel::excl_scan<kPoolThreads, 0>(__popc(free), tid, sh.scratch, &mine);
+        for (int u = 0; u < 16; ++u)
+            if (free >> u & 1u) sh.free_at[place++] = (uint16_t)(tid * 16 + u);
+        __syncthreads();
+        for (int used = 0; used < mine && e < total;) {
+            int owner = 0;
+            int32_t* t = e + tid < total ? entry(e + tid, owner) : nullptr;
+            const bool lacks = t != nullptr && __ldcg(t) < 0;
+            int n;
+            const int rank = sel::excl_scan<kPoolThreads, 0>(lacks, tid, sh.scratch, &n);
+            if (lacks && rank < mine - used) {
+                const int64_t page = base + sh.free_at[used + rank];
+                *t = (int32_t)page;
+                ref[page] = 1;
+            }
+            if (lacks && rank == mine - used) sh.next = e + tid;
+            __syncthreads();
+            e = n > mine - used ? sh.next : min(total, e + kPoolThreads);
+            used += min(n, mine - used);
+            __syncthreads();                               // sh.next may be written again
+        }
+        __syncthreads();                                   // the list may be written again
+    }
+    return e;
+}
+
 // The rows that a call names, each with its least mention: an open hash table.
 // row_of(m) is the row of mention m.
 template <typename RowOf>
@@ -378,7 +419,8 @@ __device__ __forceinline__ int owner_of(const int32_t* cnt, int n, int e, int fr
 
 __device__ __forceinline__ int pages_of(int len) { return len / kPage + (len % kPage != 0); }
 
-// The e-th entry of the call takes the e-th free page, unless it holds one already.
+// The e-th entry of the call takes the e-th free page, unless it holds one already; where
+// that leaves entries without a page, they take the pages passed over.
 __global__ void __launch_bounds__(kPoolThreads)
 reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict__ table, int rows, int max_pages,
                const int32_t* __restrict__ row, const int32_t* __restrict__ have, const int32_t* __restrict__ want, int n,
@@ -430,7 +472,11 @@ reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
         i = owner_of(s_cnt, n, e, i);
         return table + s_at[i] + (e - s_cnt[i]);
     };
-    const int found = walk_free(c, ref, num_pages, total, true, sh, entry);
+    int found = walk_free(c, ref, num_pages, total, true, sh, entry);
+    if (found < total) {                                   // the same in every block
+        if (gridDim.x > 1) sm100::cluster_sync();          // the others' entries and counts are written
+        if (speaks) found = fill_rest(ref, num_pages, found, total, sh, entry);
+    }
     if (speaks)                                            // what the pool does not hold
         for (int e = found + tid, i = 0; e < total; e += kPoolThreads)
             if (*entry(e, i) < 0) record_error(st, DSA_DEVERR_PAGE_POOL, row[i]);

@@ -546,7 +546,8 @@ dsa_status dsa_tree_mla(const void* q, const uint64_t* tree_mask, const uint8_t*
  *   it holds have_len[i]: the entries from ceil(have_len / 64) up to
  *   ceil(want_len / 64).  Entry e of the call (counted over its requests in
  *   order) takes the e-th free page; one that already holds a page keeps it.
- *   When the pool is used up the entry stays -1 and is recorded
+ *   Entries beyond the last free page take, in order, those that were so passed
+ *   over.  When the pool is used up the entry stays -1 and is recorded
  *   (DSA_DEVERR_PAGE_POOL).  Only the first mention of a row counts; others,
  *   rows outside [0, rows) and lengths above 64 * max_pages are recorded
  *   (DSA_DEVERR_INDEX_RANGE; a length is cut to 64 * max_pages).

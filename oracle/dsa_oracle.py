@@ -786,7 +786,8 @@ def pool_free(ref) -> list:
 
 
 def pages_reserve(ref, table, row, have_len, want_len):
-    """Entries in the call's order against the free pages in ascending order; returns the errors' count."""
+    """Entries in the call's order against the free pages in ascending order, then those that still
+    lack a page against the pages that held entries passed over; returns the errors' count."""
     entries, errors, named = [], 0, set()
     for r, h, w in zip(row, have_len, want_len):
         if not 0 <= r < table.shape[0] or r in named:
@@ -799,16 +800,20 @@ def pages_reserve(ref, table, row, have_len, want_len):
             errors += 1
             hi = table.shape[1]
         entries += [(r, k) for k in range(-(-max(h, 0) // PAGE_TOKENS), hi)]
-    free = pool_free(ref)
+    free, late = pool_free(ref), []
     for e, (r, k) in enumerate(entries):
         if table[r, k] >= 0:
             continue
         if e >= len(free):
-            errors += 1
+            late.append((r, k))
             continue
         table[r, k] = free[e]
         ref[free[e]] = 1
-    return errors
+    free = pool_free(ref)
+    for (r, k), p in zip(late, free):
+        table[r, k] = p
+        ref[p] = 1
+    return errors + max(0, len(late) - len(free))
 
 
 def pages_release(ref, table, row, first, end):

@@ -163,3 +163,12 @@ def test_oracle_positions_and_pool():
     assert table[1].tolist() == [-1] * 3 and ref.tolist() == [1, 0, 0, 0, 1]
     errors, copies = O.pages_fork(ref, table, [0, 0], [1, 1], [70, 70])
     assert errors == 1 and copies == [(4, 1, 6)] and table[1].tolist() == [0, 1, -1] and ref.tolist() == [2, 1, 0, 0, 1]
+
+
+def test_oracle_reserve_uses_the_pages_that_held_entries_pass_over():
+    ref, table = np.array([1, 0, 1, 0, 0]), np.array([[0, 2, -1, -1, -1]])
+    assert O.pages_reserve(ref, table, [0], [0], [5 * 64]) == 0
+    assert table.tolist() == [[0, 2, 4, 1, 3]] and ref.tolist() == [1] * 5
+    ref, table = np.array([1, 0, 1, 0, 1]), np.array([[0, 2, -1, -1, -1]])
+    assert O.pages_reserve(ref, table, [0], [0], [5 * 64]) == 1
+    assert table.tolist() == [[0, 2, 1, 3, -1]] and ref.tolist() == [1] * 5

@@ -405,3 +405,41 @@ def test_a_serving_loop():
     D.dsa_pages_release(ref, table, dev([1, 2, 3]), dev([0] * 3), dev([width] * 3), dev_status=st)
     assert D.dsa_device_status_read(st)[0] == 0
     assert (ref == 0).all() and (table == -1).all()
+
+
+def test_reserve_takes_every_free_page_before_it_gives_up():
+    """Entries that hold a page take none: the pages they passed over go to the entries that lack one."""
+    ref, table = np.ones(40, np.int32), np.full((3, 12), -1, np.int32)
+    table[1, :8] = range(8)
+    ref[[9, 13, 20, 21, 39]] = 0
+    for want in (10, 12):                                            # 2 and 4 missing entries behind 8 held ones, 5 free pages
+        r, t = ref.copy(), table.copy()
+        dref, dtable = dev(r), dev(t)
+        st = D.new_device_status(DEV)
+        D.dsa_pages_reserve(dref, dtable, dev([1]), dev([0]), dev([want * 64]), dev_status=st)
+        assert D.dsa_device_status_read(st)[0] == 0
+        assert O.pages_reserve(r, t, [1], [0], [want * 64]) == 0
+        assert np.array_equal(dtable.cpu().numpy(), t) and np.array_equal(dref.cpu().numpy(), r)
+        assert (t[1, :want] >= 0).all() and (r == 0).sum() == 5 - (want - 8)
+
+
+@pytest.mark.parametrize("pages,free", [(30, 6), (5000, 700), (40000, 20000), (300001, 3000), (300001, 12000)])
+def test_reserve_with_held_entries_in_a_short_pool(pages, free):
+    """Held entries anywhere among the call's, and fewer, as many and more free pages than missing entries."""
+    rng = np.random.default_rng(pages + free)
+    width = 9
+    rows = max(3, min(4000, 2 * free // width))
+    for missing in (free // 2, free, free + 5):
+        ref, table = np.ones(pages, np.int32), np.full((rows, width), -1, np.int32)
+        flat = rng.permutation(rows * width)
+        table.reshape(-1)[flat[min(missing, rows * width):]] = rng.integers(0, pages, max(0, rows * width - missing))
+        ref[rng.permutation(pages)[:free]] = 0
+        row = rng.permutation(rows)
+        dref, dtable = dev(ref), dev(table)
+        st = D.new_device_status(DEV)
+        D.dsa_pages_reserve(dref, dtable, dev(row), dev([0] * rows), dev([width * 64] * rows), dev_status=st)
+        errors = O.pages_reserve(ref, table, row.tolist(), [0] * rows, [width * 64] * rows)
+        s = D.dsa_device_status_read(st)
+        assert errors == max(0, min(missing, rows * width) - free)
+        assert (s[0], s[1]) == (D.DEVERR_PAGE_POOL if errors else 0, errors)
+        assert np.array_equal(dtable.cpu().numpy(), table) and np.array_equal(dref.cpu().numpy(), ref)
