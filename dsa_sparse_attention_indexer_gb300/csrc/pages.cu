@@ -91,11 +91,11 @@ commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheLi
             kept += n;
             open = open && !end;
         }
-        if (P < 0 && kept > 0) {                           // more new tokens than the request holds
+        if (P < 0) {                                       // more new tokens than the request holds
             if (lane == 0 && speaks) record_error(st, DSA_DEVERR_INDEX_RANGE, P);
             kept = 0;
         }
-        if (speaks && lane == 0 && new_len) new_len[r] = P + kept;
+        if (speaks && lane == 0 && new_len) new_len[r] = P < 0 ? L : P + kept;
         int n_moves = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

@@ -530,8 +530,10 @@ dsa_status dsa_tree_mla(const void* q, const uint64_t* tree_mask, const uint8_t*
  *   k = 0, 1, .. up to the first negative entry of accept[r].  Every row is read
  *   before any is written, so accept[r] may be in any order.  An entry at or
  *   above q_len[r] ends the list and is recorded (DSA_DEVERR_INDEX_RANGE).
- *   new_seq_len[r] = P + (entries kept).  The new tokens' pages must belong to
- *   one request only.  A position without a page is skipped and recorded.
+ *   new_seq_len[r] = P + (entries kept).  A request shorter than its new tokens
+ *   (P < 0) is recorded likewise, moves nothing and keeps its length.  The new
+ *   tokens' pages must belong to one request only.  A position without a page is
+ *   skipped and recorded.
  *     accept      device int32 [B, width], 0 <= width <= 64
  *     new_seq_len device int32 [B] or NULL; no part of the batch's seq_len
  *

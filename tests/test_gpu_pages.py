@@ -443,3 +443,17 @@ def test_reserve_with_held_entries_in_a_short_pool(pages, free):
         assert errors == max(0, min(missing, rows * width) - free)
         assert (s[0], s[1]) == (D.DEVERR_PAGE_POOL if errors else 0, errors)
         assert np.array_equal(dtable.cpu().numpy(), table) and np.array_equal(dref.cpu().numpy(), ref)
+
+
+def test_commit_of_a_request_shorter_than_its_new_tokens():
+    """Nothing moves, its length stays and it is recorded, whether anything was accepted or not."""
+    host = raw_caches(np.random.default_rng(2), 3, [D.CACHE_KV])
+    t, caches = device_caches(host, [D.CACHE_KV], 3)
+    batch = D.Batch(dev([3, 0, 70]), dev([0, 4, 7, 10]), dev([[0, -1], [1, -1], [2, -1]]), 3, max_seq_len=128, max_q_len=4, total_q=10)
+    for accept in ([[2], [1], [-1]], [[-1], [-1], [-1]]):
+        st = D.new_device_status(DEV)
+        got = D.dsa_tree_commit(dev(accept), batch, caches, dev_status=st)
+        s = D.dsa_device_status_read(st)
+        assert (s[0], s[1]) == (D.DEVERR_INDEX_RANGE, 2)
+        assert got.cpu().tolist() == [3, 0, 67]
+        assert np.array_equal(t[0].cpu().numpy(), host[0])
