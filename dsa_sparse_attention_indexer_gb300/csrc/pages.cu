@@ -442,9 +442,9 @@ reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
         const int i = tid + u * kPoolThreads;
         if (i >= n) continue;
         s_at[i] = at[u] = row[i];
-        const int w = want[i], lo = pages_of(max(have[i], 0));
+        const int h = have[i], w = want[i], lo = pages_of(max(h, 0));
         int hi = pages_of(max(w, 0));
-        cnt[u] = hi > max_pages ? -1 - w : max(0, hi - lo);
+        cnt[u] = hi > max_pages ? -1 - w : lo > max_pages ? -1 - h : 0;   // -1 - a length beyond the table
         if (hi > max_pages) hi = max_pages;
         s_cnt[i] = max(0, hi - lo);
         at[u] = lo;

@@ -551,8 +551,8 @@ dsa_status dsa_tree_mla(const void* q, const uint64_t* tree_mask, const uint8_t*
  *   Entries beyond the last free page take, in order, those that were so passed
  *   over.  When the pool is used up the entry stays -1 and is recorded
  *   (DSA_DEVERR_PAGE_POOL).  Only the first mention of a row counts; others,
- *   rows outside [0, rows) and lengths above 64 * max_pages are recorded
- *   (DSA_DEVERR_INDEX_RANGE; a length is cut to 64 * max_pages).
+ *   rows outside [0, rows) and requests with a length above 64 * max_pages are
+ *   recorded (DSA_DEVERR_INDEX_RANGE; a length is cut to 64 * max_pages).
  * dsa_pages_release: entries [first_page[i], end_page[i]) of request row[i] give
  *   their pages back and become -1; entries that are -1 already, or lie outside
  *   [0, max_pages), are passed over.  Whole requests, a rejected tail and the

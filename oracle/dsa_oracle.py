@@ -795,11 +795,9 @@ def pages_reserve(ref, table, row, have_len, want_len):
             named.add(r)
             continue
         named.add(r)
-        hi = -(-max(w, 0) // PAGE_TOKENS)
-        if hi > table.shape[1]:
-            errors += 1
-            hi = table.shape[1]
-        entries += [(r, k) for k in range(-(-max(h, 0) // PAGE_TOKENS), hi)]
+        lo, hi = -(-max(h, 0) // PAGE_TOKENS), -(-max(w, 0) // PAGE_TOKENS)
+        errors += max(lo, hi) > table.shape[1]
+        entries += [(r, k) for k in range(lo, min(hi, table.shape[1]))]
     free, late = pool_free(ref), []
     for e, (r, k) in enumerate(entries):
         if table[r, k] >= 0:

@@ -457,3 +457,15 @@ def test_commit_of_a_request_shorter_than_its_new_tokens():
         assert (s[0], s[1]) == (D.DEVERR_INDEX_RANGE, 2)
         assert got.cpu().tolist() == [3, 0, 67]
         assert np.array_equal(t[0].cpu().numpy(), host[0])
+
+
+def test_reserve_records_a_held_length_beyond_the_table():
+    ref, table = np.zeros(40, np.int32), np.full((3, 6), -1, np.int32)
+    dref, dtable = dev(ref), dev(table)
+    row, have, want = [0, 1, 2], [6 * 64 + 1, 6 * 64, 2 ** 31 - 1], [64, 64, 6 * 64]
+    st = D.new_device_status(DEV)
+    D.dsa_pages_reserve(dref, dtable, dev(row), dev(have), dev(want), dev_status=st)
+    errors = O.pages_reserve(ref, table, row, have, want)
+    s = D.dsa_device_status_read(st)
+    assert (s[0], s[1]) == (D.DEVERR_INDEX_RANGE, 2) and errors == 2
+    assert np.array_equal(dtable.cpu().numpy(), table) and np.array_equal(dref.cpu().numpy(), ref)
