@@ -599,8 +599,9 @@ class CacheSet:
                 raise ValueError(f"cache {i} has unknown kind {kind}")
             _need(t, torch.uint8, f"cache {i}", self.device, self.num_pages * _CACHE_PAGE_BYTES[kind])
             self.c[i] = DsaCache(t.data_ptr(), kind, 0)
-        if len({t.data_ptr() for t in self.tensors}) < len(self.tensors):
-            raise ValueError("a cache is named twice")
+        spans = sorted((t.data_ptr(), t.data_ptr() + self.num_pages * _CACHE_PAGE_BYTES[kind]) for t, kind in caches)
+        if any(end > begin for (_, end), (begin, _) in zip(spans, spans[1:])):
+            raise ValueError("two of the caches share memory")
 
     def __len__(self) -> int:
         return len(self.tensors)

@@ -522,7 +522,7 @@ dsa_status dsa_tree_mla(const void* q, const uint64_t* tree_mask, const uint8_t*
  *
  * A cache list names every layer's caches that one page table serves; a call
  * treats them all alike, in one launch per 128 caches.  The list itself lives
- * on the host and is read before the call returns.  It names no cache twice.
+ * on the host and is read before the call returns.  No two of its caches overlap.
  *
  * dsa_tree_commit: after a verify step, the tokens of the accepted path move to
  *   the front of the request's new tokens: with P = seq_len[r] - q_len[r], the

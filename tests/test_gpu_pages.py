@@ -469,3 +469,14 @@ def test_reserve_records_a_held_length_beyond_the_table():
     s = D.dsa_device_status_read(st)
     assert (s[0], s[1]) == (D.DEVERR_INDEX_RANGE, 2) and errors == 2
     assert np.array_equal(dtable.cpu().numpy(), table) and np.array_equal(dref.cpu().numpy(), ref)
+
+
+def test_caches_that_overlap_are_refused():
+    n = 3
+    t = torch.zeros(2 * n * D.KV_PAGE_BYTES + 64, dtype=torch.uint8, device=DEV)
+    for at in (16, D.KV_PAGE_BYTES, n * D.KV_PAGE_BYTES - 16):
+        with pytest.raises(ValueError):
+            D.CacheSet([(t, D.CACHE_KV), (t[at:], D.CACHE_KV)], n)
+        with pytest.raises(ValueError):
+            D.CacheSet([(t[at:], D.CACHE_IDXK), (t, D.CACHE_KV)], n)
+    D.CacheSet([(t[n * D.KV_PAGE_BYTES:], D.CACHE_IDXK), (t, D.CACHE_KV)], n)
