@@ -18,6 +18,9 @@
 #include "sm100.cuh"
 
 namespace dsa {
+
+int device_sm_count();
+
 namespace pages {
 
 constexpr int kMaxCaches = 128;                            // caches of one launch (passed by value)
@@ -58,10 +61,10 @@ constexpr int kCommitWarps = kCopyThreads / 32;
 constexpr int kCommitRows = 144;                           // of a round: 94 KB, two blocks a SM
 constexpr int kCommitSmem = kCommitRows * DSA_KV_TOKEN_BYTES;
 static_assert(DSA_KV_TOKEN_BYTES >= DSA_INDEX_HEAD_DIM + 4, "an index key and its scale word take a row's place");
-// Blocks of a launch: three times what is resident.  More caches a block take more
-// rounds one after another, fewer repeat the chain: 24.3 / 18.8 / 16.6 / 17.8 / 18.2 us
-// with 304 / 608 / 912 / 1216 / 1824 blocks.
-constexpr int kCommitBlocks = 912;
+// Blocks of a launch, per SM: three times what is resident.  More caches a block take
+// more rounds one after another, fewer repeat the chain: 24.3 / 18.8 / 16.6 / 17.8 /
+// 18.2 us with 2 / 4 / 6 / 8 / 12.
+constexpr int kCommitBlocks = 6;
 
 __global__ void __launch_bounds__(kCopyThreads)
 commit_kernel(const int32_t* __restrict__ accept, int width, BatchDev b, CacheList cl, int n_caches, int per_block,
@@ -669,7 +672,7 @@ extern "C" dsa_status dsa_tree_commit(const int32_t* accept, int32_t width, cons
     int32_t at = 0;
     do {                                                   // 128 caches a launch; the first writes the lengths
         const int32_t n = n_caches - at < pages::kMaxCaches ? n_caches - at : pages::kMaxCaches;
-        const int32_t want = std::min(std::max(1, pages::kCommitBlocks / b->batch), std::max(1, n));
+        const int32_t want = std::min(std::max(1, pages::kCommitBlocks * device_sm_count() / b->batch), std::max(1, n));
         const int32_t per = std::max(1, (n + want - 1) / want);
         DSA_CHECK(launch_pdl(pages::commit_kernel, dim3((unsigned)b->batch, (unsigned)std::max(1, (n + per - 1) / per)),
                              dim3(pages::kCopyThreads), pages::kCommitSmem, as_stream(stream), 1, accept, (int)width, to_dev(b),
