@@ -471,7 +471,7 @@ reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
     for (int u = 0; u < kPerThread; ++u)
         if (tid + u * kPoolThreads < n) s_at[tid + u * kPoolThreads] = at[u];
     const int total = prefix_in_place(s_cnt, n, sh.scratch);
-    auto entry = [&](int e, int& i) {                      // i: the owner of an earlier entry, then this one's
+    auto entry = [=](int e, int& i) {                      // i: the owner of an earlier entry, then this one's
         i = owner_of(s_cnt, n, e, i);
         return table + s_at[i] + (e - s_cnt[i]);
     };
