@@ -273,6 +273,18 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one) that the call's caller did not give.
+    It comes from that stream's memory, so that nothing enqueued elsewhere still uses it, and goes
+    back only when the work that the current stream does on it until then has ended."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def new_device_status(device) -> torch.Tensor:
     return torch.zeros(4, dtype=torch.int32, device=device)
 
@@ -387,11 +399,14 @@ def _indexer_args(q, w, idxk_cache, batch: Batch) -> int:
     return T
 
 
-def _ws(ws, nbytes, device):
-    """The call's workspace: allocated when not given, else a uint8 CUDA buffer."""
-    if ws is None:
+def _ws(ws, nbytes, device, stream):
+    """The call's workspace: allocated when not given, else a uint8 CUDA buffer.  An
+    allocated one is freed when the call returns, so it is memory of the call's stream:
+    only work that comes behind the call there may get it next."""
+    if ws is not None:
+        return _need(ws, torch.uint8, "ws", device)
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
         return workspace(nbytes, device)
-    return _need(ws, torch.uint8, "ws", device)
 
 
 def dsa_indexer_topk_workspace_size(batch: Batch) -> int:
@@ -403,11 +418,11 @@ def dsa_indexer_topk(q, w, idxk_cache, batch: Batch, *, topk=None, topk_scores=N
     """Indexer + top-2048.  Returns topk int32 [T, 2048] (allocated if not given)."""
     T = _indexer_args(q, w, idxk_cache, batch)
     if topk is None:
-        topk = torch.empty((T, TOPK), dtype=torch.int32, device=q.device)
+        topk = _empty((T, TOPK), torch.int32, q.device, stream)
     _need(topk, torch.int32, "topk", q.device, T * TOPK)
     _opt(topk_scores, torch.float32, "topk_scores", q.device, T * TOPK)
     _opt(dev_status, torch.int32, "dev_status", q.device, 4)
-    ws = _ws(ws, dsa_indexer_topk_workspace_size(batch) if ws is None else 0, q.device)
+    ws = _ws(ws, dsa_indexer_topk_workspace_size(batch) if ws is None else 0, q.device, stream)
     _call("dsa_indexer_topk", q.device,
         _ptr(q), _ptr(w), _ptr(idxk_cache), batch.ref(), _ptr(topk), _ptr(topk_scores),
         None if share is None else share.handle, layer_id, _ptr(ws), ws.numel(), _ptr(dev_status),
@@ -420,11 +435,11 @@ def dsa_indexer_topk_mxfp4(q, w, idxk_cache, batch: Batch, *, topk=None, topk_sc
     """dsa_indexer_topk over an MXFP4 index-K cache (at most 65535 query rows)."""
     T = _indexer_args(q, w, idxk_cache, batch)
     if topk is None:
-        topk = torch.empty((T, TOPK), dtype=torch.int32, device=q.device)
+        topk = _empty((T, TOPK), torch.int32, q.device, stream)
     _need(topk, torch.int32, "topk", q.device, T * TOPK)
     _opt(topk_scores, torch.float32, "topk_scores", q.device, T * TOPK)
     _opt(dev_status, torch.int32, "dev_status", q.device, 4)
-    ws = _ws(ws, dsa_indexer_topk_workspace_size(batch) if ws is None else 0, q.device)
+    ws = _ws(ws, dsa_indexer_topk_workspace_size(batch) if ws is None else 0, q.device, stream)
     _call("dsa_indexer_topk_mxfp4", q.device,
         _ptr(q), _ptr(w), _ptr(idxk_cache), batch.ref(), _ptr(topk), _ptr(topk_scores),
         None if share is None else share.handle, layer_id, _ptr(ws), ws.numel(), _ptr(dev_status),
@@ -437,7 +452,7 @@ def dsa_indexer_topk_noalloc(q, w, idxk_cache, batch: Batch, *, topk=None, topk_
     """dsa_indexer_topk for decode batches on the library's fixed scratch (no workspace)."""
     T = _indexer_args(q, w, idxk_cache, batch)
     if topk is None:
-        topk = torch.empty((T, TOPK), dtype=torch.int32, device=q.device)
+        topk = _empty((T, TOPK), torch.int32, q.device, stream)
     _need(topk, torch.int32, "topk", q.device, T * TOPK)
     _opt(topk_scores, torch.float32, "topk_scores", q.device, T * TOPK)
     _opt(dev_status, torch.int32, "dev_status", q.device, 4)
@@ -453,10 +468,10 @@ def dsa_indexer_scores(q, w, idxk_cache, batch: Batch, *, ld=None, scores=None, 
     T = _indexer_args(q, w, idxk_cache, batch)
     ld = batch.c.max_seq_len if ld is None else ld
     if scores is None:
-        scores = torch.empty((T, ld), dtype=torch.float32, device=q.device)
+        scores = _empty((T, ld), torch.float32, q.device, stream)
     _need(scores, torch.float32, "scores", q.device, T * ld)
     _opt(dev_status, torch.int32, "dev_status", q.device, 4)
-    ws = _ws(ws, _ws_size("dsa_indexer_scores_workspace_size", batch) if ws is None else 0, q.device)
+    ws = _ws(ws, _ws_size("dsa_indexer_scores_workspace_size", batch) if ws is None else 0, q.device, stream)
     _call("dsa_indexer_scores", q.device,
         _ptr(q), _ptr(w), _ptr(idxk_cache), batch.ref(), _ptr(scores), ld, _ptr(ws), ws.numel(),
         _ptr(dev_status), _stream(stream, q.device))
@@ -469,10 +484,10 @@ def dsa_indexer_scores_cuda_core(q, w, idxk_cache, batch: Batch, *, ld=None, sco
     T = _indexer_args(q, w, idxk_cache, batch)
     ld = batch.c.max_seq_len if ld is None else ld
     if scores is None:
-        scores = torch.empty((T, ld), dtype=torch.float32, device=q.device)
+        scores = _empty((T, ld), torch.float32, q.device, stream)
     _need(scores, torch.float32, "scores", q.device, T * ld)
     _opt(dev_status, torch.int32, "dev_status", q.device, 4)
-    ws = _ws(ws, T * (4096 + 128) if ws is None else 0, q.device)
+    ws = _ws(ws, T * (4096 + 128) if ws is None else 0, q.device, stream)
     _call("dsa_indexer_scores_cuda_core", q.device,
         _ptr(q), _ptr(w), _ptr(idxk_cache), batch.ref(), _ptr(scores), ld, _ptr(ws), ws.numel(),
         _ptr(dev_status), _stream(stream, q.device))
@@ -487,12 +502,12 @@ def dsa_topk_from_scores(scores, valid_len, *, max_len=None, topk=None, stream=N
     _need(valid_len, torch.int32, "valid_len", scores.device, rows)
     max_len = ld if max_len is None else max_len
     if topk is None:
-        topk = torch.empty((rows, TOPK), dtype=torch.int32, device=scores.device)
+        topk = _empty((rows, TOPK), torch.int32, scores.device, stream)
     _need(topk, torch.int32, "topk", scores.device, rows * TOPK)
     n = c_size_t(0)
     _check("dsa_topk_from_scores_workspace_size",
            lib().dsa_topk_from_scores_workspace_size(rows, max_len, ctypes.byref(n)))
-    ws = workspace(n.value, scores.device)
+    ws = _ws(None, n.value, scores.device, stream)
     _call("dsa_topk_from_scores", scores.device,
         _ptr(scores), ld, _ptr(valid_len), rows, max_len, _ptr(topk), _ptr(ws), ws.numel(), _stream(stream, scores.device))
     return topk
@@ -512,11 +527,11 @@ def _mla(fn, q, topk, kv_cache, batch, softmax_scale, out, out_dtype, lse, share
     _opt(topk, torch.int32, "topk", dev, T * TOPK)
     out_t = torch.float32 if out_dtype == DTYPE_F32 else torch.bfloat16
     if out is None:
-        out = torch.empty((T, MLA_HEADS, LATENT_DIM), dtype=out_t, device=dev)
+        out = _empty((T, MLA_HEADS, LATENT_DIM), out_t, dev, stream)
     _need(out, out_t, "out", dev, T * MLA_HEADS * LATENT_DIM)
     _opt(lse, torch.float32, "lse", dev, T * MLA_HEADS)
     _opt(dev_status, torch.int32, "dev_status", dev, 4)
-    ws = _ws(ws, dsa_sparse_mla_workspace_size(batch) if ws is None else 0, dev)
+    ws = _ws(ws, dsa_sparse_mla_workspace_size(batch) if ws is None else 0, dev, stream)
     _call(fn, dev,
           _ptr(q), _ptr(topk), None if share is None else share.handle, _ptr(kv_cache), batch.ref(),
           softmax_scale, _ptr(out), out_dtype, _ptr(lse), _ptr(ws), ws.numel(), _ptr(dev_status),
@@ -542,7 +557,7 @@ def dsa_dense_mla_workspace_size(batch: Batch) -> int:
     return _ws_size("dsa_dense_mla_workspace_size", batch)
 
 
-def _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status):
+def _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status, stream):
     _need(q, torch.bfloat16, "q")
     T, dev = batch.total_q, q.device
     _need(q, torch.bfloat16, "q", dev, T * MLA_HEADS * QK_DIM)
@@ -550,21 +565,22 @@ def _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status):
     _need(batch.seq_len, torch.int32, "batch.seq_len", dev)
     out_t = torch.float32 if out_dtype == DTYPE_F32 else torch.bfloat16
     if out is None:
-        out = torch.empty((T, MLA_HEADS, LATENT_DIM), dtype=out_t, device=dev)
+        out = _empty((T, MLA_HEADS, LATENT_DIM), out_t, dev, stream)
     _need(out, out_t, "out", dev, T * MLA_HEADS * LATENT_DIM)
     _opt(lse, torch.float32, "lse", dev, T * MLA_HEADS)
     _opt(dev_status, torch.int32, "dev_status", dev, 4)
+    nbytes = 0
     if ws is None:
         with torch.cuda.device(dev):
-            ws = workspace(dsa_dense_mla_workspace_size(batch), dev)
-    return out, _need(ws, torch.uint8, "ws", dev)
+            nbytes = dsa_dense_mla_workspace_size(batch)
+    return out, _ws(ws, nbytes, dev, stream)
 
 
 def dsa_window_mla(q, kv_cache, batch: Batch, *, window: int, sinks: int = 0, softmax_scale=1.0 / 16, out=None,
                    out_dtype=DTYPE_BF16, lse=None, ws=None, dev_status=None, stream=None):
     """Attention of every row over the last `window` positions up to its own and
     the context's first `sinks`.  Returns out [T, 64, 512] (allocated if not given)."""
-    out, ws = _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status)
+    out, ws = _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status, stream)
     _call("dsa_window_mla", q.device,
           _ptr(q), _ptr(kv_cache), batch.ref(), window, sinks, softmax_scale, _ptr(out), out_dtype, _ptr(lse), _ptr(ws),
           ws.numel(), _ptr(dev_status), _stream(stream, q.device))
@@ -575,7 +591,7 @@ def dsa_tree_mla(q, tree_mask, kv_cache, batch: Batch, *, softmax_scale=1.0 / 16
                  lse=None, ws=None, dev_status=None, stream=None):
     """Attention of a draft tree's rows: the cached prefix and the new tokens whose
     bit is set in the row's mask (int64 [T], taken as 64 bits)."""
-    out, ws = _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status)
+    out, ws = _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status, stream)
     _need(tree_mask, torch.int64, "tree_mask", q.device, batch.total_q)
     _call("dsa_tree_mla", q.device,
           _ptr(q), _ptr(tree_mask), _ptr(kv_cache), batch.ref(), softmax_scale, _ptr(out), out_dtype, _ptr(lse), _ptr(ws),
@@ -623,7 +639,7 @@ def dsa_tree_commit(accept, batch: Batch, caches: CacheSet, *, new_seq_len=None,
     _need(batch.seq_len, torch.int32, "batch.seq_len", dev)
     c, n = _caches(caches, batch.c.num_pages, dev)
     if new_seq_len is None:
-        new_seq_len = torch.empty(B, dtype=torch.int32, device=dev)
+        new_seq_len = _empty(B, torch.int32, dev, stream)
     _need(new_seq_len, torch.int32, "new_seq_len", dev, B)
     _opt(dev_status, torch.int32, "dev_status", dev, 4)
     _call("dsa_tree_commit", dev, _ptr(accept), accept.shape[1], batch.ref(), c, n, _ptr(new_seq_len), _ptr(dev_status),
@@ -786,7 +802,7 @@ def dsa_mtp_seed_write(topk, *, src_row=None, n=None, seed=None, width=None, dev
     if width is None:
         width = dsa_mtp_topk_width() if seed is None else seed.shape[1]
     if seed is None:
-        seed = torch.empty((n, width), dtype=torch.int32, device=topk.device)
+        seed = _empty((n, width), torch.int32, topk.device, stream)
     _need(seed, torch.int32, "seed", topk.device, n * width)
     _opt(dev_status, torch.int32, "dev_status", topk.device, 4)
     _call("dsa_mtp_seed_write", topk.device,
@@ -819,7 +835,7 @@ def dsa_cp_topk_merge(cand_pos, cand_scores, pos_offset, *, topk=None, topk_scor
     _need(cand_scores, torch.float32, "cand_scores", dev, G * rows * TOPK)
     _need(pos_offset, torch.int64, "pos_offset", dev, G * rows)
     if topk is None:
-        topk = torch.empty((rows, TOPK), dtype=torch.int32, device=dev)
+        topk = _empty((rows, TOPK), torch.int32, dev, stream)
     _need(topk, torch.int32, "topk", dev, rows * TOPK)
     _opt(topk_scores, torch.float32, "topk_scores", dev, rows * TOPK)
     _opt(dev_status, torch.int32, "dev_status", dev, 4)
@@ -836,7 +852,7 @@ def dsa_cp_topk_localize(topk, slice_start, slice_len, *, local_topk=None, strea
     _need(slice_start, torch.int64, "slice_start", dev, rows)
     _need(slice_len, torch.int64, "slice_len", dev, rows)
     if local_topk is None:
-        local_topk = torch.empty((rows, TOPK), dtype=torch.int32, device=dev)
+        local_topk = _empty((rows, TOPK), torch.int32, dev, stream)
     _need(local_topk, torch.int32, "local_topk", dev, rows * TOPK)
     _call("dsa_cp_topk_localize", dev, _ptr(topk), rows, _ptr(slice_start), _ptr(slice_len), _ptr(local_topk),
           _stream(stream, dev))
@@ -853,7 +869,7 @@ def dsa_cp_attention_merge(o_parts, lse_parts, *, out=None, out_dtype=DTYPE_BF16
     _need(lse_parts, torch.float32, "lse_parts", dev, G * rows * MLA_HEADS)
     out_t = torch.float32 if out_dtype == DTYPE_F32 else torch.bfloat16
     if out is None:
-        out = torch.empty((rows, MLA_HEADS, LATENT_DIM), dtype=out_t, device=dev)
+        out = _empty((rows, MLA_HEADS, LATENT_DIM), out_t, dev, stream)
     _need(out, out_t, "out", dev, rows * MLA_HEADS * LATENT_DIM)
     _opt(lse, torch.float32, "lse", dev, rows * MLA_HEADS)
     _call("dsa_cp_attention_merge", dev, _ptr(o_parts), _ptr(lse_parts), G, rows, _ptr(out), out_dtype, _ptr(lse),
@@ -866,8 +882,8 @@ class LibraryOps:
 
     def indexer_topk(self, q, w, idxk_cache, batch, ws=None, dev_status=None, stream=None):
         T = batch.total_q
-        topk = torch.empty((T, TOPK), dtype=torch.int32, device=q.device)
-        scores = torch.empty((T, TOPK), dtype=torch.float32, device=q.device)
+        topk = _empty((T, TOPK), torch.int32, q.device, stream)
+        scores = _empty((T, TOPK), torch.float32, q.device, stream)
         dsa_indexer_topk(q, w, idxk_cache, batch, topk=topk, topk_scores=scores, ws=ws, dev_status=dev_status,
                          stream=stream)
         return topk, scores
@@ -880,14 +896,14 @@ class LibraryOps:
 
     def sparse_mla(self, q, local_topk, kv_cache, batch, softmax_scale, ws=None, dev_status=None, stream=None):
         T = batch.total_q
-        lse = torch.empty((T, MLA_HEADS), dtype=torch.float32, device=q.device)
+        lse = _empty((T, MLA_HEADS), torch.float32, q.device, stream)
         out = dsa_sparse_mla_decode(q, local_topk, kv_cache, batch, softmax_scale=softmax_scale, out_dtype=DTYPE_F32,
                                     lse=lse, ws=ws, dev_status=dev_status, stream=stream)
         return out, lse
 
     def attention_merge(self, o_parts, lse_parts, out_dtype, stream=None):
         T = o_parts.shape[1]
-        lse = torch.empty((T, MLA_HEADS), dtype=torch.float32, device=o_parts.device)
+        lse = _empty((T, MLA_HEADS), torch.float32, o_parts.device, stream)
         out = dsa_cp_attention_merge(o_parts, lse_parts, out_dtype=out_dtype, lse=lse, stream=stream)
         return out, lse
 

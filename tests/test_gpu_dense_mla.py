@@ -451,3 +451,45 @@ def test_contexts_up_to_the_largest_length():
     ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
     c["kv"], c["batch"] = far.view(-1), D.Batch(ints(L), ints(0, 1), table, 3, max_seq_len=L, max_q_len=1, total_q=1)
     compare(c, *run(c, window_call(window, 0)))
+
+
+def test_what_a_call_allocates_is_memory_of_its_stream(monkeypatch):
+    """Outputs and workspaces that the caller does not give are allocated on the call's stream: a workspace
+    is free again when the call returns, and work of another stream must not get it before the kernels
+    have run.  The results are those of a call on the current stream."""
+    c = window_case(91, [3000, 70], [1, 1], 2500, 3)
+    mask = torch.ones(2, dtype=torch.int64, device=DEV)
+    topk = torch.full((2, D.TOPK), -1, dtype=torch.int32, device=DEV)
+    topk[:, :70] = torch.arange(70, device=DEV)
+    caches = D.CacheSet([], c["pages"])
+    qi, w = torch.randn(2, 32, 128, device=DEV).to(torch.bfloat16), torch.rand(2, 32, device=DEV)
+    idx = torch.zeros(c["pages"] * D.IDXK_PAGE_BYTES, dtype=torch.uint8, device=DEV)
+    scores = torch.randn(2, 3000, device=DEV)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    full = window_case(92, [300, 70], [1, 1], 300, 0, full_table=True)
+    b = full["batch"]
+    calls = {
+        "window": lambda s: D.dsa_window_mla(c["dq"], c["kv"], c["batch"], window=2500, sinks=3, stream=s),
+        "tree": lambda s: D.dsa_tree_mla(full["dq"], mask, full["kv"], b, stream=s),
+        "commit": lambda s: D.dsa_tree_commit(ints([0], [-1]), c["batch"], caches, stream=s),
+        "sparse": lambda s: D.dsa_sparse_mla_decode(full["dq"], topk, full["kv"], b, stream=s),
+        "topk": lambda s: D.dsa_indexer_topk(qi, w, idx, b, stream=s),
+        "from_scores": lambda s: D.dsa_topk_from_scores(scores, ints(3000, 70), stream=s),
+    }
+    want = {name: call(None) for name, call in calls.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    seen, real = [], torch.empty
+
+    def empty(*a, **k):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return real(*a, **k)
+
+    for name, call in calls.items():
+        del seen[:]
+        monkeypatch.setattr(torch, "empty", empty)
+        got = call(side)
+        monkeypatch.setattr(torch, "empty", real)
+        assert seen and all(x == side.cuda_stream for x in seen), name
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want[name]), name
