@@ -579,7 +579,9 @@ def _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status, str
 def dsa_window_mla(q, kv_cache, batch: Batch, *, window: int, sinks: int = 0, softmax_scale=1.0 / 16, out=None,
                    out_dtype=DTYPE_BF16, lse=None, ws=None, dev_status=None, stream=None):
     """Attention of every row over the last `window` positions up to its own and
-    the context's first `sinks`.  Returns out [T, 64, 512] (allocated if not given)."""
+    the context's first `sinks`; of either, 2^31 - 1 or more is the whole context.
+    Returns out [T, 64, 512] (allocated if not given)."""
+    window, sinks = (max(-1, min(int(n), 2 ** 31 - 1)) for n in (window, sinks))   # the library takes int32
     out, ws = _dense_mla_args(q, kv_cache, batch, out, out_dtype, lse, ws, dev_status, stream)
     _call("dsa_window_mla", q.device,
           _ptr(q), _ptr(kv_cache), batch.ref(), window, sinks, softmax_scale, _ptr(out), out_dtype, _ptr(lse), _ptr(ws),

@@ -493,3 +493,15 @@ def test_what_a_call_allocates_is_memory_of_its_stream(monkeypatch):
         assert seen and all(x == side.cuda_stream for x in seen), name
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(got, want[name]), name
+
+
+def test_windows_and_sinks_beyond_32_bits_are_the_whole_context():
+    c = window_case(95, [300, 129], [1, 2], 2 ** 40, 0)
+    whole = run(c, window_call(2 ** 31 - 1, 0))
+    compare(c, *whole)
+    for window, sinks in ((2 ** 31, 0), (2 ** 32 + 5, 0), (2 ** 63, 0), (1, 2 ** 32), (1, 2 ** 32 + 3)):
+        out, lse = run(c, window_call(window, sinks))
+        assert torch.equal(out, whole[0]) and torch.equal(lse, whole[1]), (window, sinks)
+    for window, sinks in ((0, 0), (-2 ** 32 + 5, 0), (5, -1), (5, -2 ** 32 + 1)):
+        with pytest.raises(D.DsaError):
+            D.dsa_window_mla(c["dq"], c["kv"], c["batch"], window=window, sinks=sinks)
