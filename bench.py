@@ -45,12 +45,12 @@ L2_BYTES = 129 * 1024 * 1024
 # (one pass): the sparse-MLA kernel of decode32k, the score kernel of the decode1m
 # and of the verify64k indexer call.
 NCU_TRAFFIC = {
-    ("decode32k", "sparse_mla_decode"): (105.2e6, "dsa_sparse_attention_indexer_gb300/csrc/mla_tc.cu",
-                                         "b578eccc9eb1936e"),
+    ("decode32k", "sparse_mla_decode"): (105.3e6, "dsa_sparse_attention_indexer_gb300/csrc/mla_tc.cu",
+                                         "3f00d9fd9138e828"),
     ("decode1m", "indexer_topk"): (554.1e6, "dsa_sparse_attention_indexer_gb300/csrc/indexer_tc.cu",
-                                   "705e9c579e52891d"),
-    ("verify64k", "indexer_topk"): (1403.4e6, "dsa_sparse_attention_indexer_gb300/csrc/indexer_mt.cu",
-                                    "27f628ac41f61059"),
+                                   "59ebcfa8bf066df8"),
+    ("verify64k", "indexer_topk"): (1405.3e6, "dsa_sparse_attention_indexer_gb300/csrc/indexer_mt.cu",
+                                    "4cb2e12e8acc6571"),
 }
 FP8_OVER_BF16 = 2.0          # nominal dense tensor rate ratio (4.5 / 2.25 PFLOP/s), used only if the
                              # FP8 GEMM measurement below cannot run

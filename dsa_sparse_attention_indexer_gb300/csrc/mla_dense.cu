@@ -39,14 +39,14 @@
 // prefetches the pages into L2.
 // Every wait is time-bounded; a timeout is recorded and the CTA winds down.
 //
-// What bounds it (64 tree rows in each of 8 requests of up to 32K tokens: 2.78 ms, 709
-// TFLOP/s; 2048 rows with a window of 2048: 0.93 ms, 632 TFLOP/s; one row in each of 4
-// requests with a window of 131072: 129 us, 2.7 TB/s): the workers.  A tile takes about
-// 6,800 cycles, of which the tensor core is busy 3,300.  The workers issue 695
+// What bounds it (64 tree rows in each of 8 requests of up to 32K tokens: 2.83 ms, 696
+// TFLOP/s; 2048 rows with a window of 2048: 0.95 ms, 618 TFLOP/s; one row in each of 4
+// requests with a window of 131072: 130 us, 2.7 TB/s): the workers.  A tile takes about
+// 6,950 cycles, of which the tensor core is busy 2,180.  The workers issue 700
 // instructions per warp and tile, mostly conversions and fp16 products of the
-// dequantisation at half rate, and 4,300 passes through the load/store pipe (1,400 for
-// the fp16 tile's stores, 1,900 for the rows' loads), one phase after the other: without
-// the MMAs a tile takes 4 % less, without the loads 10 %.
+// dequantisation at half rate, and 4,300 passes through the load/store pipe (1,430 for
+// shared stores, most of them the fp16 tile's, 1,900 for the rows' loads), one phase
+// after the other.
 // Neighbouring rows of a request read the same tiles, but two rows' O^T (2 x 256
 // columns) leave no TMEM for S^T; two CTAs that dequantise half a tile each and copy
 // it to one another move in step, and wait more than they save (2.94 -> 3.93 ms).
@@ -181,7 +181,7 @@ constexpr int kAhead = 4;                                  // tiles laid out ahe
 // tiles of a piece, references move down to where the sum of the P so far is 2^kSettled, so
 // that behind a dominating position the many small ones keep their bits: P is off by 2^-11 of
 // itself or by 2^-25, which is 2^-28 of the sum in the first tiles and 2^-34 in all others:
-// 4096 times 2^-28 and a million times 2^-34 are 2^-14 of the largest latent together.
+// 4096 times 2^-28 and a million times 2^-34 are less than 2^-13 of the largest latent.
 // (Settled after 8 tiles, prefill with 17 tiles a row takes 952 us instead of 917; with
 // references that put every tile's largest P at 2^9, or its sum at 2^8, flat heads
 // outgrow them tile after tile: 1077 and 993 us.)

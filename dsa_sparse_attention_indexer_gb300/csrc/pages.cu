@@ -5,10 +5,10 @@
 // All of it is copying and counting: a large move is bound by HBM (row bytes read
 // and written once), the rest by latency: chains of dependent loads (lengths, lists,
 // page table, counts, entries) of 0.6 to 1 us each.  Measured: 64 children of
-// 8,229 tokens with a partial page in each of 99 caches 37 us (6.9 TB/s, the reads
+// 8,229 tokens with a partial page in each of 99 caches 36 us (7.0 TB/s, the reads
 // mostly from the L2: one source page a cache); 128 accepted paths of 16 tokens in 99
-// caches 16.6 us (4.3 TB/s); one path in 5 caches 2.6 us; 256 rows giving back and
-// taking about 100,000 of 131,072 pages 17 us; 8 rows of a pool of 1,024 6.8 us.
+// caches 16.3 us (4.4 TB/s); one path in 5 caches 2.2 us; 256 rows giving back and
+// taking about 100,000 of 131,072 pages 16.6 us; 8 rows of a pool of 1,024 6.2 us.
 #include <algorithm>
 
 #include "dsa_internal.cuh"

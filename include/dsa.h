@@ -481,8 +481,8 @@ dsa_status dsa_topk_share_mtp_end(dsa_topk_share* s);
  * A row that sees nothing gives out = 0 and lse = -inf.  Softmax statistics and
  * accumulation (16 positions a step) are fp32; probabilities are rounded to fp16
  * for the product with the latents, as in sparse MLA: each is off by 2^-11 of
- * itself, or, where it is small, by so little that a million of them make 2^-14
- * of the largest latent.  Scores may have any magnitude that fp32 holds.  A NaN
+ * itself, or, where it is small, by so little that a million of them make less
+ * than 2^-13 of the largest latent.  Scores may have any magnitude that fp32 holds.  A NaN
  * in a latent or RoPE dim that a row sees makes its out and lse NaN (in a RoPE
  * dim it is recorded too, DSA_DEVERR_FP16_RANGE).
  * dsa_window_mla: j <= p and (j < sinks or j > p - window): the last `window`
