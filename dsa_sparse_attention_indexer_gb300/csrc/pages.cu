@@ -332,7 +332,7 @@ __device__ __noinline__ int fill_rest(int32_t* ref, int64_t num_pages, int e, in
         __syncthreads();
         for (int used = 0; used < mine && e < total;) {
             int owner = 0;
-            int32_t* t = e + tid < total ? entry(e + tid, owner) : nullptr;
+            int32_t* t = tid < total - e ? entry(e + tid, owner) : nullptr;   // there may be nearly 2^31 entries
             const bool lacks = t != nullptr && __ldcg(t) < 0;
             int n;
             const int rank = sel::excl_scan<kPoolThreads, 0>(lacks, tid, sh.scratch, &n);
@@ -343,7 +343,7 @@ __device__ __noinline__ int fill_rest(int32_t* ref, int64_t num_pages, int e, in
             }
             if (lacks && rank == mine - used) sh.next = e + tid;
             __syncthreads();
-            e = n > mine - used ? sh.next : min(total, e + kPoolThreads);
+            e = n > mine - used ? sh.next : e + min(total - e, kPoolThreads);
             used += min(n, mine - used);
             __syncthreads();                               // sh.next may be written again
         }
@@ -480,9 +480,10 @@ reserve_kernel(int32_t* __restrict__ ref, int64_t num_pages, int32_t* __restrict
         if (gridDim.x > 1) sm100::cluster_sync();          // the others' entries and counts are written
         if (speaks) found = fill_rest(ref, num_pages, found, total, sh, entry);
     }
-    if (speaks)                                            // what the pool does not hold
-        for (int e = found + tid, i = 0; e < total; e += kPoolThreads)
-            if (*entry(e, i) < 0) record_error(st, DSA_DEVERR_PAGE_POOL, row[i]);
+    int i = 0;
+    if (speaks)                                            // what the pool does not hold; e passes 2^31 - 1
+        for (int64_t e = (int64_t)found + tid; e < total; e += kPoolThreads)
+            if (*entry((int)e, i) < 0) record_error(st, DSA_DEVERR_PAGE_POOL, row[i]);
 }
 
 // ---------------------------------------------------------------- fork

@@ -480,3 +480,21 @@ def test_caches_that_overlap_are_refused():
         with pytest.raises(ValueError):
             D.CacheSet([(t[at:], D.CACHE_IDXK), (t, D.CACHE_KV)], n)
     D.CacheSet([(t[n * D.KV_PAGE_BYTES:], D.CACHE_IDXK), (t, D.CACHE_KV)], n)
+
+
+def test_reserve_of_nearly_2_to_31_entries_without_a_free_page():
+    """The last entries of the largest table are looked at, and nothing past them: 64 rows of 2^25 - 1 pages, all
+    of which hold page 0 but three."""
+    rows, width = 64, 2 ** 25 - 1
+    ref, table = dev([3] * 20), torch.zeros(rows, width, dtype=torch.int32, device=DEV)
+    table[0, 5] = table[rows - 1, width - 1] = table[rows - 1, width - 700] = -1
+    st = D.new_device_status(DEV)
+    D.dsa_pages_reserve(ref, table, dev(range(rows)), dev([0] * rows), dev([width * 64] * rows), dev_status=st)
+    s = D.dsa_device_status_read(st)
+    assert (s[0], s[1]) == (D.DEVERR_PAGE_POOL, 3)
+    assert int(torch.count_nonzero(table)) == 3 and (ref == 3).all()
+    ref[7], ref[12] = 0, 0                                           # two of the three can be served
+    st = D.new_device_status(DEV)
+    D.dsa_pages_reserve(ref, table[rows - 1:], dev([0]), dev([(width - 1000) * 64]), dev([width * 64]), dev_status=st)
+    assert D.dsa_device_status_read(st)[0] == 0
+    assert table[rows - 1, [width - 700, width - 1]].tolist() == [7, 12] and ref.tolist() == [3] * 7 + [1] + [3] * 4 + [1] + [3] * 7
