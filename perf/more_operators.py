@@ -21,7 +21,7 @@ own = False
 
 DEV = "cuda"
 PAGE, BLOCK = 64, 16
-E_MIN, E_MAX = -48, 48
+E_MIN, E_MAX = -24, 24
 BASE = 10000.0
 
 
