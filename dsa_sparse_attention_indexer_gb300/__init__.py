@@ -45,6 +45,11 @@ DEVERR_FP16_RANGE = 16
 DEVERR_PAGE_POOL = 32
 DEVERR_PAGE_COUNT = 64
 
+KV8_BLOCK = 16
+KV8_MAX_EXP = 24
+ROPE_INTERLEAVED = 0
+ROPE_HALVES = 1
+
 CACHE_KV = 0
 CACHE_IDXK = 1
 CACHE_IDXK_MXFP4 = 2
@@ -80,6 +85,10 @@ class DsaBatch(ctypes.Structure):
 
 class DsaCache(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("kind", c_int32), ("reserved", c_int32)]
+
+
+class DsaHeads(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("token_stride", c_int64), ("head_stride", c_int64)]
 
 
 _lib = None
@@ -146,6 +155,9 @@ _SIGS = {
                                     c_void_p, c_void_p]),
     "dsa_pages_fork": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
                                  POINTER(DsaCache), c_int32, c_void_p, c_void_p]),
+    "dsa_kv8_append": (c_int32, [POINTER(DsaHeads), POINTER(DsaHeads), POINTER(DsaHeads), POINTER(DsaBatch), c_int32, c_int32,
+                                 c_int32, c_int32, c_int32, c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p]),
     "dsa_cp_topk_merge": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p,
                                     c_void_p]),
     "dsa_cp_topk_localize": (c_int32, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -690,6 +702,80 @@ def dsa_pages_fork(page_ref, page_table, src_row, dst_row, length, caches: Cache
     c, n_caches = _caches(caches, page_ref.numel(), dev)
     _call("dsa_pages_fork", dev, _ptr(page_ref), page_ref.numel(), _ptr(page_table), rows, max_pages, _ptr(src_row),
           _ptr(dst_row), _ptr(length), n, c, n_caches, _ptr(dev_status), _stream(stream, dev))
+
+
+# ---------------------------------------------------------------------------
+# Grouped heads beside the latent ones: the KV8 cache and attention.
+def kv8_page_bytes(kv_heads: int, head_dim: int) -> int:
+    """Bytes of a KV8 cache's page: 64 tokens of every head."""
+    return kv_heads * (2 * PAGE_TOKENS * head_dim + 32)
+
+
+def kv8_views(cache: torch.Tensor, kv_heads: int, head_dim: int):
+    """Views of a KV8 cache: key codes [pages, kv_heads, 4, 16, head_dim] and value codes
+    [pages, kv_heads, 4, head_dim, 16] (float8_e4m3fn), scales fp32 [pages, kv_heads, 2, 4]
+    (keys', then values')."""
+    part = PAGE_TOKENS * head_dim
+    heads = cache.view(-1, kv_heads, 2 * part + 32)
+    blocks = PAGE_TOKENS // KV8_BLOCK
+    return (heads[..., :part].unflatten(-1, (blocks, KV8_BLOCK, head_dim)).view(torch.float8_e4m3fn),
+            heads[..., part:2 * part].unflatten(-1, (blocks, head_dim, KV8_BLOCK)).view(torch.float8_e4m3fn),
+            heads[..., 2 * part:].view(torch.float32).unflatten(-1, (2, blocks)))
+
+
+def _heads(t: torch.Tensor, name: str, device=None, rows=None):
+    """A dsa_heads of a bf16 [rows, heads, head_dim] CUDA tensor whose dims are neighbours."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}'s head_dim must be contiguous, its stride is {t.stride(2)}")
+    if rows is not None and t.shape[0] < rows:
+        raise ValueError(f"{name} holds {t.shape[0]} rows, the call needs {rows}")
+    # the stride of an axis of one entry says nothing
+    return DsaHeads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def dsa_kv8_append(k, v, cache, batch: Batch, *, q=None, rope_dims=None, rope_style: int = ROPE_HALVES, rope_base=10000.0,
+                   inv_freq=None, q_out=None, k_out=None, dev_status=None, stream=None):
+    """The batch's new keys and values (bf16 [total_q, kv_heads, head_dim], any strides of rows and
+    heads) enter the KV8 cache, keys rotated by their positions in dims [0, rope_dims) (None: all).
+    q (bf16 [total_q, heads, head_dim]) is rotated likewise into q_out, which is returned (allocated
+    if not given; None without q); k_out receives the rotated keys if given."""
+    dev, T = getattr(k, "device", None), batch.total_q
+    ck = _heads(k, "k", None, T)
+    kv_heads, dim = k.shape[1], k.shape[2]
+    cv = _heads(v, "v", dev, T)
+    if tuple(v.shape[1:]) != (kv_heads, dim):
+        raise ValueError(f"v must be [rows, {kv_heads}, {dim}], got {tuple(v.shape)}")
+    heads, cq = kv_heads, None
+    if q is not None:
+        cq = _heads(q, "q", dev, T)
+        heads = q.shape[1]
+        if q.shape[2] != dim:
+            raise ValueError(f"q must be [rows, heads, {dim}], got {tuple(q.shape)}")
+        if q_out is None:
+            q_out = _empty((T, heads, dim), torch.bfloat16, dev, stream)
+        _need(q_out, torch.bfloat16, "q_out", dev, T * heads * dim)
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    _opt(k_out, torch.bfloat16, "k_out", dev, T * kv_heads * dim)
+    _need(cache, torch.uint8, "cache", dev, batch.c.num_pages * kv8_page_bytes(kv_heads, dim))
+    _need(batch.seq_len, torch.int32, "batch.seq_len", dev)
+    rope_dims = dim if rope_dims is None else rope_dims
+    _opt(inv_freq, torch.float32, "inv_freq", dev, max(rope_dims, 0) // 2)
+    _opt(dev_status, torch.int32, "dev_status", dev, 4)
+    _call("dsa_kv8_append", dev, ctypes.byref(ck), ctypes.byref(cv), None if cq is None else ctypes.byref(cq), batch.ref(), heads,
+          kv_heads, dim, rope_dims, rope_style, rope_base, _ptr(inv_freq), _ptr(cache), _ptr(q_out), _ptr(k_out),
+          _ptr(dev_status), _stream(stream, dev))
+    return q_out
 
 
 # ---------------------------------------------------------------------------

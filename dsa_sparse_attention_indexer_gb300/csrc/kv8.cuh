@@ -1,0 +1,39 @@
+// The KV8 cache: grouped heads' keys and values in E4M3, one power-of-two scale
+// for each block of 16 tokens and head (layout in dsa.h).
+#pragma once
+#include "dsa_internal.cuh"
+#include "indexer_common.cuh"
+
+namespace dsa {
+namespace kv8 {
+
+constexpr int kBlock = DSA_KV8_BLOCK;
+constexpr int kBlocks = kPage / kBlock;                    // of a page
+constexpr int kMaxExp = DSA_KV8_MAX_EXP;
+
+// Bytes of one head in a page, and where its parts begin.
+__host__ __device__ constexpr int64_t head_bytes(int dim) { return 2 * kPage * dim + 32; }
+__host__ __device__ constexpr int v_at(int dim) { return kPage * dim; }
+__host__ __device__ constexpr int scale_at(int dim) { return 2 * kPage * dim; }
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // e in [-126, 127]
+// The exponent of a stored scale.  Whatever the word holds, it is one of the cache's.
+__device__ __forceinline__ int scale_exponent(float s) {
+    return max(-kMaxExp, min(kMaxExp, (int)((__float_as_uint(s) >> 23) & 0xffu) - 127));
+}
+
+// Checks that the calls on grouped heads share.
+inline dsa_status check_shape(int32_t heads, int32_t kv_heads, int32_t dim) {
+    if (heads < 1 || kv_heads < 1) return DSA_ERR_INVALID_ARGUMENT;
+    if (dim != 64 && dim != 128 && dim != 256) return DSA_ERR_UNSUPPORTED;
+    if (heads % kv_heads != 0 || heads / kv_heads > 128 || heads > 65535) return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
+inline dsa_status check_heads(const dsa_heads* h) {
+    if (!h->data || h->token_stride < 0 || h->head_stride < 0) return DSA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(h->data) || h->token_stride % 8 != 0 || h->head_stride % 8 != 0) return DSA_ERR_ALIGNMENT;
+    return DSA_OK;
+}
+
+}  // namespace kv8
+}  // namespace dsa

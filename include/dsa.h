@@ -591,6 +591,66 @@ dsa_status dsa_pages_fork(int32_t* page_ref, int64_t num_pages, int32_t* page_ta
                           const int32_t* length, int32_t n, const dsa_cache* caches, int32_t n_caches,
                           int32_t* dev_status, void* stream);
 
+/* ---- Grouped heads beside the latent ones ---------------------------------------
+ * The pages have no counterpart of these calls.  They serve layers, draft models
+ * and hybrid models with ordinary keys and values per head on the page tables and
+ * pools of the latent caches: `heads` query heads share `kv_heads` heads of keys
+ * and values, heads / kv_heads neighbouring query heads each, of head_dim 64, 128
+ * or 256; heads is a multiple of kv_heads, at most 128 times as many, and at most
+ * 65535.  Other shapes return DSA_ERR_UNSUPPORTED.
+ *
+ * A KV8 cache holds keys and values in FP8 E4M3 with one scale 2^e, e in
+ * [-24, 24], for each block of 16 tokens and head.  A page holds its kv_heads
+ * heads one after the other, 128 * head_dim + 32 bytes each:
+ *   keys   [64 tokens][head_dim]           E4M3
+ *   values [4 blocks][head_dim][16 tokens] E4M3 (a block's tokens side by side)
+ *   scales keys fp32 [4 blocks], values fp32 [4 blocks]
+ *
+ * A dsa_heads names bf16 rows of heads, so that parts of a projection's output
+ * are taken as they lie.  data is 16-byte aligned, the strides multiples of 8
+ * elements and at least 0 (DSA_ERR_ALIGNMENT, DSA_ERR_INVALID_ARGUMENT); a head's
+ * dims are neighbours. */
+#define DSA_KV8_BLOCK      16
+#define DSA_KV8_MAX_EXP    24
+#define DSA_KV8_PAGE_BYTES(kv_heads, head_dim) ((int64_t)(kv_heads) * (128 * (int64_t)(head_dim) + 32))
+#define DSA_ROPE_INTERLEAVED 0      /* pairs (2i, 2i + 1)                          */
+#define DSA_ROPE_HALVES      1      /* pairs (i, i + rope_dims / 2)                */
+typedef struct dsa_heads {
+    const void* data;           /* device bf16                                      */
+    int64_t token_stride;       /* elements from a token to the next                */
+    int64_t head_stride;        /* elements from a head to the next                 */
+} dsa_heads;
+
+/* dsa_kv8_append: the batch's new tokens (row t of request r is position
+ *   p = seq_len - q_len + t) enter the cache.  Dims [0, rope_dims) of keys and
+ *   queries are rotated: pair i by the angle p * f_i, f_i = inv_freq[i] or
+ *   rope_base^(-2i / rope_dims); the angle is reduced exactly, products are fp32.
+ *   Keys and values of a block and head are then rounded to E4M3 (nearest even,
+ *   from fp32) with the smallest scale, e >= -24, that holds the largest of the
+ *   call's new values, |x| <= 448 * 2^e, and is no smaller than the scale that
+ *   the block has when tokens before the new ones are in it: where such a scale
+ *   grows, those tokens' codes are rounded again to the new one (exact, except
+ *   for codes that become subnormal).  A value beyond 448 * 2^24, infinite or NaN
+ *   is stored as NaN and has no say in the scale.
+ *   Positions without a page (an entry outside the cache: DSA_DEVERR_PAGE_RANGE;
+ *   below 0 or at and above 64 * max_pages: DSA_DEVERR_INDEX_RANGE) are skipped
+ *   and recorded.  Bytes of positions that are not new stay as they are, but for
+ *   those codes and the block's scale.  A page that gets new tokens must belong to
+ *   one request only.  q_out and k_out get the rotated rows in bf16, those
+ *   of skipped positions too; rows at and above q_start[B] are left as they were.
+ *   k, v     kv_heads heads of total_q rows; q heads heads or NULL
+ *   rope_dims a multiple of 16, 0 <= rope_dims <= head_dim; rope_base > 0
+ *   inv_freq device fp32 [rope_dims / 2] or NULL
+ *   cache    device uint8 [num_pages * DSA_KV8_PAGE_BYTES], 16-byte aligned
+ *   q_out    device bf16 [T, heads, head_dim], exactly when q is given; may be q's
+ *            own memory where q lies like that
+ *   k_out    device bf16 [T, kv_heads, head_dim] or NULL; may be k's own memory
+ *            where k lies like that                                              */
+dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, const dsa_heads* q, const dsa_batch* b,
+                          int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t rope_dims,
+                          int32_t rope_style, float rope_base, const float* inv_freq, uint8_t* cache,
+                          void* q_out, void* k_out, int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -867,3 +867,69 @@ def pages_fork(ref, table, src, dst, length):
             table[d, full] = taken[f]
             copies.append((int(old[full]), taken[f], part))
     return errors, copies
+
+
+# ---------------------------------------------------------------------------
+# Grouped heads: the KV8 cache (E4M3, a scale for each block of 16 tokens and
+# head) and attention over it or over packed prompts.  The pages have no
+# counterpart of these calls; the definitions follow dsa.h.
+KV8_BLOCK, KV8_MAX_EXP = 16, 24
+
+
+def rope_pairs(x: np.ndarray, pos: np.ndarray, rope_dims: int, halves: bool, inv_freq=None, base: float = 10000.0) -> np.ndarray:
+    """x [T, heads, dim] with dims [0, rope_dims) rotated: pair i by pos * f_i."""
+    y = np.array(x, dtype=np.float64)
+    n = rope_dims // 2
+    i = np.arange(n)
+    f = base ** (-2.0 * i / rope_dims) if inv_freq is None else np.asarray(inv_freq, dtype=np.float64)
+    ang = np.asarray(pos, dtype=np.float64)[:, None, None] * f
+    a, b = (i, i + n) if halves else (2 * i, 2 * i + 1)
+    xa, xb = y[..., a].copy(), y[..., b].copy()
+    y[..., a] = xa * np.cos(ang) - xb * np.sin(ang)
+    y[..., b] = xa * np.sin(ang) + xb * np.cos(ang)
+    return y
+
+
+def kv8_exponent(amax: float) -> int:
+    """Smallest e in [-24, 24] with amax <= 448 * 2^e."""
+    e = -KV8_MAX_EXP
+    while e < KV8_MAX_EXP and amax > 448.0 * 2.0 ** e:
+        e += 1
+    return e
+
+
+def kv8_block_append(codes: np.ndarray, exponent: int, held: int, new: np.ndarray):
+    """A block of one head: codes uint8 [16, dim], the exponent of its scale, tokens held,
+    new fp64 [n, dim].  Returns (codes, exponent)."""
+    limit = 448.0 * 2.0 ** KV8_MAX_EXP
+    with np.errstate(invalid="ignore"):
+        good = np.abs(new) <= limit
+    e = kv8_exponent(float(np.max(np.abs(new[good]), initial=0.0)))
+    codes = codes.copy()
+    if held:
+        e = max(e, exponent)
+    if held and e > exponent:                              # a NaN code that is written again is 0x7f
+        old = codes[:held]
+        nan = (old & 0x7f) == 0x7f
+        codes[:held] = np.where(nan, 0x7f, e4m3_encode(np.where(nan, 0.0, e4m3_decode(old)) * 2.0 ** (exponent - e)))
+    codes[held:held + len(new)] = np.where(good, e4m3_encode(np.where(good, new, 0.0) * 2.0 ** -e), 0x7f)
+    return codes, e
+
+
+def grouped_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, first: int, scale: float):
+    """q [n, heads, dim]; k, v [L, kv_heads, dim], all fp64.  Row t sees keys j <= first + t.
+    Returns (out [n, heads, dim], lse [n, heads]); a row that sees nothing gives (0, -inf)."""
+    n, heads, dim = q.shape
+    G = heads // k.shape[1]
+    out, lse = np.zeros((n, heads, dim)), np.full((n, heads), -np.inf)
+    for t in range(n):
+        m = min(first + t + 1, len(k))
+        if m <= 0:
+            continue
+        for h in range(heads):
+            s = scale * (k[:m, h // G] @ q[t, h])
+            top = s.max()
+            w = np.exp(s - top)
+            out[t, h] = (w @ v[:m, h // G]) / w.sum()
+            lse[t, h] = top + np.log(w.sum())
+    return out, lse
