@@ -158,6 +158,9 @@ _SIGS = {
     "dsa_kv8_append": (c_int32, [POINTER(DsaHeads), POINTER(DsaHeads), POINTER(DsaHeads), POINTER(DsaBatch), c_int32, c_int32,
                                  c_int32, c_int32, c_int32, c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_void_p]),
+    "dsa_kv8_attention_workspace_size": (c_int32, [POINTER(DsaBatch), c_int32, c_int32, c_int32, POINTER(c_size_t)]),
+    "dsa_kv8_attention": (c_int32, [POINTER(DsaHeads), c_void_p, POINTER(DsaBatch), c_int32, c_int32, c_int32, c_float, c_void_p,
+                                    c_int32, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "dsa_cp_topk_merge": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p,
                                     c_void_p]),
     "dsa_cp_topk_localize": (c_int32, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -776,6 +779,46 @@ def dsa_kv8_append(k, v, cache, batch: Batch, *, q=None, rope_dims=None, rope_st
           kv_heads, dim, rope_dims, rope_style, rope_base, _ptr(inv_freq), _ptr(cache), _ptr(q_out), _ptr(k_out),
           _ptr(dev_status), _stream(stream, dev))
     return q_out
+
+
+def dsa_kv8_attention_workspace_size(batch: Batch, heads: int, kv_heads: int, head_dim: int) -> int:
+    n = c_size_t(0)
+    _check("dsa_kv8_attention_workspace_size",
+           lib().dsa_kv8_attention_workspace_size(batch.ref(), heads, kv_heads, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def _attention_args(q, T, heads, dim, softmax_scale, out, out_dtype, lse, dev_status, stream):
+    """Checks what the attention calls on grouped heads share; returns (softmax scale, out)."""
+    dev = q.device
+    out_t = torch.float32 if out_dtype == DTYPE_F32 else torch.bfloat16
+    if out is None:
+        out = _empty((T, heads, dim), out_t, dev, stream)
+    _need(out, out_t, "out", dev, T * heads * dim)
+    _opt(lse, torch.float32, "lse", dev, T * heads)
+    _opt(dev_status, torch.int32, "dev_status", dev, 4)
+    return dim ** -0.5 if softmax_scale is None else softmax_scale, out
+
+
+def dsa_kv8_attention(q, cache, batch: Batch, *, kv_heads: int, softmax_scale=None, out=None, out_dtype=DTYPE_BF16, lse=None,
+                      ws=None, dev_status=None, stream=None):
+    """Causal attention of the batch's new tokens (q bf16 [total_q, heads, head_dim], any strides of
+    rows and heads) over a KV8 cache.  softmax_scale defaults to head_dim ** -0.5.
+    Returns out [total_q, heads, head_dim] (allocated if not given)."""
+    T = batch.total_q
+    cq = _heads(q, "q", None, T)
+    dev, heads, dim = q.device, q.shape[1], q.shape[2]
+    _need(cache, torch.uint8, "cache", dev, batch.c.num_pages * kv8_page_bytes(kv_heads, dim))
+    _need(batch.seq_len, torch.int32, "batch.seq_len", dev)
+    softmax_scale, out = _attention_args(q, T, heads, dim, softmax_scale, out, out_dtype, lse, dev_status, stream)
+    nbytes = 0
+    if ws is None:
+        with torch.cuda.device(dev):
+            nbytes = dsa_kv8_attention_workspace_size(batch, heads, kv_heads, dim)
+    ws = _ws(ws, nbytes, dev, stream)
+    _call("dsa_kv8_attention", dev, ctypes.byref(cq), _ptr(cache), batch.ref(), heads, kv_heads, dim, softmax_scale, _ptr(out),
+          out_dtype, _ptr(lse), _ptr(ws), ws.numel(), _ptr(dev_status), _stream(stream, dev))
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -3,6 +3,7 @@
 #pragma once
 #include "dsa_internal.cuh"
 #include "indexer_common.cuh"
+#include "mla_common.cuh"
 
 namespace dsa {
 namespace kv8 {
@@ -20,6 +21,12 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // The exponent of a stored scale.  Whatever the word holds, it is one of the cache's.
 __device__ __forceinline__ int scale_exponent(float s) {
     return max(-kMaxExp, min(kMaxExp, (int)((__float_as_uint(s) >> 23) & 0xffu) - 127));
+}
+
+// A wait of these kernels' pipelines: within the limit, and not beyond another role's
+// timeout.  A limit of 0 takes what has happened already, and is not suspended for it.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int32_t* abort_flag, uint64_t limit_ns) {
+    return limit_ns == 0 ? sm100::mbar_test_wait(bar, parity) : mlc::wait_ab(bar, parity, abort_flag, limit_ns);
 }
 
 // Checks that the calls on grouped heads share.

@@ -143,8 +143,8 @@ dsa_status dsa_device_status_read(const int32_t* dev_status, void* stream, int32
 /* Testing hook for failure detection, process-wide: the limit, in ns, of the
  * pipeline waits of the decode indexer's score kernel (dsa_indexer_topk and
  * dsa_indexer_topk_mxfp4 on a batch of one row per request) and of the
- * attention kernel of dsa_window_mla and dsa_tree_mla, launched after
- * the call.  2e9 (2 s) by default; 0 makes every wait that is not already
+ * attention kernels of dsa_window_mla, dsa_tree_mla and dsa_kv8_attention,
+ * launched after the call.  2e9 (2 s) by default; 0 makes every wait that is not already
  * satisfied give up at once.  A wait that gives up records
  * DSA_DEVERR_TIMEOUT; the kernel then lets its copies and MMAs in flight
  * finish, releases its tensor memory and returns, the merge sees only what
@@ -650,6 +650,36 @@ dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, const dsa_head
                           int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t rope_dims,
                           int32_t rope_style, float rope_base, const float* inv_freq, uint8_t* cache,
                           void* q_out, void* k_out, int32_t* dev_status, void* stream);
+
+/* dsa_kv8_attention: causal attention of the batch's new tokens over a KV8 cache that
+ *   holds them (dsa_kv8_append).  For query row i (request r, position
+ *   p = seq_len - q_len + t) and head h, with keys and values of head
+ *   h * kv_heads / heads as the codes times their scales, over the positions j <= p:
+ *     S_hj = softmax_scale * <q_ih, k_j>,  out_ih = sum_j softmax_j(S_hj) v_j,
+ *     lse_ih = log sum_j exp(S_hj)
+ *   q_len is 1 for decoding, any for verify and prefill.  A row that sees nothing
+ *   (p < 0) gives out = 0 and lse = -inf.  q is scaled per row by a power of two
+ *   and rounded to fp16 (exact, but for values more than 2^39 below the row's
+ *   largest), E4M3 is exact in fp16; softmax statistics and accumulation are
+ *   fp32; probabilities are rounded to fp16 for the product with the values, each
+ *   off by 2^-11 of itself, or by less than 2^-32 of the largest.  A NaN in a key
+ *   or in a value that a row sees makes its outputs NaN, and no other row's.
+ *   Cache rows that no row sees may hold anything.  A page id outside the cache
+ *   is recorded (DSA_DEVERR_PAGE_RANGE) and its positions are not seen; a negative
+ *   p and positions at and above 64 * max_pages likewise (DSA_DEVERR_INDEX_RANGE).
+ *   Rows at and above q_start[B] are left as they were.  total_q * heads / kv_heads
+ *   above 2^31 - 256 returns DSA_ERR_UNSUPPORTED.
+ *   q        heads heads of total_q rows, rotated
+ *   out      device [T, heads, head_dim], bf16 or fp32 per out_dtype
+ *   lse      device fp32 [T, heads] or NULL
+ *   ws       device workspace of dsa_kv8_attention_workspace_size() bytes, sized for
+ *            the SM count of the device current at the size call; nothing in it has
+ *            to start at zero or is kept between calls                             */
+dsa_status dsa_kv8_attention_workspace_size(const dsa_batch* b, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                            size_t* bytes);
+dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache, const dsa_batch* b, int32_t heads,
+                             int32_t kv_heads, int32_t head_dim, float softmax_scale, void* out, int32_t out_dtype,
+                             float* lse, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

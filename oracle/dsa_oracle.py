@@ -916,20 +916,48 @@ def kv8_block_append(codes: np.ndarray, exponent: int, held: int, new: np.ndarra
     return codes, e
 
 
-def grouped_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, first: int, scale: float):
-    """q [n, heads, dim]; k, v [L, kv_heads, dim], all fp64.  Row t sees keys j <= first + t.
-    Returns (out [n, heads, dim], lse [n, heads]); a row that sees nothing gives (0, -inf)."""
-    n, heads, dim = q.shape
-    G = heads // k.shape[1]
-    out, lse = np.zeros((n, heads, dim)), np.full((n, heads), -np.inf)
-    for t in range(n):
-        m = min(first + t + 1, len(k))
-        if m <= 0:
+def kv8_read(cache: np.ndarray, kv_heads: int, dim: int, table_row, length: int, num_pages: int):
+    """Keys and values [length, kv_heads, dim] (fp64) of a request, and which positions have a page."""
+    heads = cache.reshape(num_pages, kv_heads, 128 * dim + 32)
+    k, v = np.zeros((length, kv_heads, dim)), np.zeros((length, kv_heads, dim))
+    ok = np.zeros(length, dtype=bool)
+    for p0 in range(0, length, 64):
+        pg = int(table_row[p0 // 64]) if p0 // 64 < len(table_row) else -1
+        if not 0 <= pg < num_pages:
             continue
-        for h in range(heads):
-            s = scale * (k[:m, h // G] @ q[t, h])
-            top = s.max()
-            w = np.exp(s - top)
-            out[t, h] = (w @ v[:m, h // G]) / w.sum()
-            lse[t, h] = top + np.log(w.sum())
-    return out, lse
+        n = min(64, length - p0)
+        for h in range(kv_heads):
+            raw = heads[pg, h]
+            scales = raw[128 * dim:].copy().view(np.float32).astype(np.float64)
+            keys = e4m3_decode(raw[:64 * dim].reshape(64, dim)) * np.repeat(scales[:4], 16)[:, None]
+            vals = e4m3_decode(raw[64 * dim:128 * dim].reshape(4, dim, 16)).transpose(0, 2, 1) * scales[4:, None, None]
+            k[p0:p0 + n, h], v[p0:p0 + n, h] = keys[:n], vals.reshape(64, dim)[:n]
+        ok[p0:p0 + n] = True
+    return k, v, ok
+
+
+def grouped_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, first: int, scale: float, ok=None):
+    """q [n, heads, dim]; k, v [L, kv_heads, dim], all fp64.  Row t sees keys j <= first + t
+    (with ok: those of them that are ok).  Returns (out [n, heads, dim], lse [n, heads],
+    weight [n, heads, dim]: the sums of |softmax * v|); a row that sees nothing gives (0, -inf, 0)."""
+    n, heads, dim = q.shape
+    kv = k.shape[1]
+    G = heads // kv
+    out, size, lse = np.zeros((n, heads, dim)), np.zeros((n, heads, dim)), np.full((n, heads), -np.inf)
+    see = np.arange(len(k)) <= first + np.arange(n)[:, None]
+    if ok is not None:
+        see = see & ok
+    for h in range(heads):
+        with np.errstate(invalid="ignore"):
+            s = scale * (q[:, h] @ k[:, h // G].T)
+        for t in range(n):
+            at = see[t]
+            if not at.any():
+                continue
+            with np.errstate(invalid="ignore", over="ignore"):
+                top = s[t, at].max()
+                w = np.exp(s[t, at] - top)
+                lse[t, h] = top + np.log(w.sum())
+                out[t, h] = (w @ v[at, h // G]) / w.sum()
+                size[t, h] = (w @ np.abs(v[at, h // G])) / w.sum()
+    return out, lse, size

@@ -1,0 +1,232 @@
+"""dsa_kv8_attention against the 64-bit oracle, at the bounds derived in tests/grouped.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import dsa_sparse_attention_indexer_gb300 as D
+from tests.grouped import DEV, cache_case, check, expected, place
+
+pytestmark = pytest.mark.gpu
+
+
+def _run(c, dtype=D.DTYPE_BF16, scale=None, ws=None, stream=None, q=None):
+    T = c["T"] + c["pad"]
+    out = torch.full((T, c["heads"], c["dim"]), 7.0, dtype=torch.float32 if dtype == D.DTYPE_F32 else torch.bfloat16, device=DEV)
+    lse = torch.full((T, c["heads"]), 7.0, device=DEV)
+    st = D.new_device_status(DEV)
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    D.dsa_kv8_attention(c["q"] if q is None else q, c["dev_cache"], c["batch"], kv_heads=c["kv"], softmax_scale=scale, out=out, out_dtype=dtype, lse=lse,
+                        ws=ws, dev_status=st, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.all(out[c["T"]:] == 7.0) and torch.all(lse[c["T"]:] == 7.0)           # rows behind the last request
+    return out, lse, D.dsa_device_status_read(st)[0]
+
+
+SHAPES = [
+    # seq_len, q_len, kv_heads, group, dim
+    ([1], [1], 1, 1, 64),
+    ([1, 15, 16, 17, 31], [1] * 5, 2, 8, 128),
+    ([63, 64, 65, 127, 128, 129], [1] * 6, 2, 4, 64),
+    ([100, 700, 3], [1] * 3, 1, 2, 256),
+    ([1000, 33, 512], [1] * 3, 8, 8, 128),
+    ([20000], [1], 1, 8, 128),
+    ([5000, 7000], [1, 1], 1, 64, 128),
+    ([300, 129, 64], [1] * 3, 2, 7, 128),
+    ([300, 129, 64], [1] * 3, 2, 12, 64),
+    ([300, 129], [1] * 2, 2, 16, 256),
+    ([200, 64, 130, 77], [6, 1, 0, 3], 2, 4, 128),
+    ([200, 64, 6], [6, 6, 6], 4, 4, 256),
+    ([65, 66], [2, 2], 3, 5, 64),
+    ([190, 100], [33, 100], 2, 3, 128),
+    ([150], [70], 1, 5, 256),
+    ([128, 127], [128, 3], 2, 1, 64),
+    ([257], [140], 2, 8, 128),
+    ([40], [3], 1, 128, 64),
+]
+
+
+@pytest.mark.parametrize("seq,n,kv,group,dim", SHAPES)
+def test_attention(seq, n, kv, group, dim):
+    c = cache_case(seq, n, kv, group, dim, seed=len(seq) + dim, pad_rows=2)
+    want = expected(c)
+    for dtype in (D.DTYPE_F32, D.DTYPE_BF16):
+        out, lse, bits = _run(c, dtype)
+        check(out, lse, want)
+        assert bits == 0
+
+
+def test_many_requests_of_all_lengths():
+    """More requests than threads plan at once, lengths 1 .. 400; shares that begin and end anywhere."""
+    seq = [1 + (37 * i) % 400 for i in range(500)]
+    c = cache_case(seq, [1] * 500, 1, 4, 64, seed=5)
+    out, lse, bits = _run(c)
+    check(out, lse, expected(c))
+    assert bits == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_shares_of_many_pages(dim):
+    """Shares of more pages than a CTA holds at once, several times over, of an odd number of pages each."""
+    seq = [7000 + 333 * (i % 7) for i in range(40)]
+    c = cache_case(seq, [1] * 40, 1, 2, dim, seed=dim)
+    out, lse, bits = _run(c)
+    check(out, lse, expected(c))
+    assert bits == 0
+
+
+def test_scales_far_apart():
+    """Blocks' scales from 2^-24 to 2^24 side by side, in any order: each output to its own precision."""
+    for seed in range(3):
+        c = cache_case([600, 90], [3, 1], 2, 4, 128, seed=seed)
+        s = D.kv8_views(c["cache"], 2, 128)[2]
+        g = torch.Generator().manual_seed(seed)
+        s[:, :, 1] = torch.exp2(torch.randint(-24, 25, s[:, :, 1].shape, generator=g).float())
+        place(c)
+        for scale in (None, 1.0):
+            out, lse, _ = _run(c, D.DTYPE_F32, scale)
+            check(out, lse, expected(c, scale))
+
+
+def test_large_scores_and_a_dominating_token():
+    c = cache_case([4000], [1], 1, 8, 128, seed=3, q_size=300.0)
+    check(*_run(c, D.DTYPE_F32)[:2], expected(c))
+    # one key far above the others, first, in the middle and last, then the sum of many small ones behind it
+    for at in (0, 2000, 3999):
+        c = cache_case([4000], [1], 1, 8, 128, seed=4, q_size=0.05)
+        k = D.kv8_views(c["cache"], 1, 128)[0]
+        pg, blk, tok = int(c["table"][0, at // 64]), at % 64 // 16, at % 16
+        k[pg, 0, blk, tok] = (torch.sign(c["q"][0, 3].float().cpu()) * 448).to(torch.float8_e4m3fn)
+        place(c)
+        check(*_run(c, D.DTYPE_F32)[:2], expected(c))
+
+
+def test_a_context_of_equal_scores():
+    c = cache_case([9000], [1], 1, 8, 128, seed=6)
+    c["q"].zero_()
+    check(*_run(c, D.DTYPE_F32)[:2], expected(c))
+
+
+def test_unseen_rows_may_hold_anything():
+    """NaN codes and scales of any bits behind every request's end and in pages that no one holds."""
+    c = cache_case([50, 17, 64, 130], [3, 1, 2, 5], 2, 4, 128, seed=8)
+    want = expected(c)
+    k, v, s = (x.view(torch.uint8) if x.dtype != torch.float32 else x for x in D.kv8_views(c["cache"], 2, 128))
+    used = torch.zeros(c["pages"], dtype=torch.bool)
+    for r, L in enumerate(c["seq"]):
+        for p in range((L + 63) // 64):
+            pg = int(c["table"][r, p])
+            used[pg] = True
+            for blk in range(4):
+                left = min(16, max(0, L - p * 64 - blk * 16))
+                k[pg, :, blk, left:] = 0x7f
+                v[pg, :, blk, :, left:] = 0xff
+                if left == 0:
+                    s[pg, :, :, blk] = float("nan")
+    c["cache"][~used] = 0xff
+    place(c)
+    out, lse, bits = _run(c)
+    check(out, lse, want)
+    assert bits == 0
+
+
+def test_nan_reaches_the_rows_that_see_it():
+    for dim, group, n in ((128, 4, 5), (64, 1, 40), (256, 2, 9)):
+        c = cache_case([100, 90], [n, 1], 2, group, dim, seed=9)
+        k, v, _ = D.kv8_views(c["cache"], 2, dim)
+        for p, what in ((98, v), (97, k), (20, None)):
+            pg, blk, tok = int(c["table"][0, p // 64]), p % 64 // 16, p % 16
+            if what is v:
+                v.view(torch.uint8)[pg, 0, blk, 5, tok] = 0x7f
+                v.view(torch.uint8)[pg, 1, blk, dim - 1, tok] = 0xff
+            elif what is k:
+                k.view(torch.uint8)[pg, 1, blk, tok, 3] = 0xff
+        pg = int(c["table"][1, 0])
+        v.view(torch.uint8)[pg, 0, 0, 7, 0] = 0x7f          # every row of request 1 sees this one
+        place(c)
+        out, lse, _ = _run(c, D.DTYPE_F32)
+        want = expected(c)
+        assert np.isnan(want[0]).any() and not np.isnan(want[0]).all()
+        # a NaN score makes the whole row NaN
+        bad = np.isnan(want[1])
+        want[0][bad] = np.nan
+        check(out, lse, want)
+
+
+def test_pages_outside_the_cache_and_lengths_outside_the_table():
+    c = cache_case([300, 200, 100, 5], [2, 1, 3, 9], 2, 3, 128, seed=10)
+    c["table"][0, 2], c["table"][1, 0], c["table"][1, 3] = c["pages"], -1, -7
+    place(c)
+    out, lse, bits = _run(c)
+    check(out, lse, expected(c))                            # request 3 has 9 new tokens and holds 5: its first rows see nothing
+    assert bits == D.DEVERR_PAGE_RANGE | D.DEVERR_INDEX_RANGE
+    c = cache_case([128, 64], [1, 1], 1, 2, 64, seed=11)
+    c["seq"] = [500, 64]                                    # two pages of the table: positions from 128 on are not seen
+    place(c)
+    out, lse, bits = _run(c)
+    want = expected(dict(c, seq=[128, 64]))
+    check(out, lse, want)
+    assert bits == D.DEVERR_INDEX_RANGE
+    c["seq"] = [-3, 0]
+    place(c)
+    out, lse, bits = _run(c)
+    assert torch.all(out == 0) and torch.all(lse == -float("inf")) and bits == D.DEVERR_INDEX_RANGE
+
+
+def test_strides_scale_stream_graph_and_workspace():
+    c = cache_case([400, 70, 1000], [2, 1, 4], 2, 4, 128, seed=12)
+    want = expected(c)
+    out, lse, _ = _run(c)
+    check(out, lse, want)
+    # q as a part of wider rows, and with its heads in front
+    wide = torch.randn(c["T"], c["heads"] + 4, 128, device=DEV).to(torch.bfloat16)
+    wide[:, 2:2 + c["heads"]] = c["q"]
+    turned = c["q"].transpose(0, 1).contiguous().transpose(0, 1)
+    for q in (wide[:, 2:2 + c["heads"]], turned):
+        o2, l2, _ = _run(c, q=q)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    # the same bits with a dirty workspace, on another stream and from a graph
+    nbytes = D.dsa_kv8_attention_workspace_size(c["batch"], c["heads"], c["kv"], 128)
+    for fill in (0, 0xff, 0xab):
+        ws = torch.full((nbytes,), fill, dtype=torch.uint8, device=DEV)
+        o2, l2, _ = _run(c, ws=ws, stream=torch.cuda.Stream())
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    o2, l2 = torch.zeros_like(out), torch.zeros_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        D.dsa_kv8_attention(c["q"], c["dev_cache"], c["batch"], kv_heads=2, out=o2, lse=l2, ws=ws)
+    for _ in range(2):
+        o2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    check(*_run(c, scale=0.7)[:2], expected(c, 0.7))
+
+
+def test_extreme_queries():
+    """Rows whose q is far above and below fp16's range, zero, and NaN."""
+    c = cache_case([90, 90], [1, 2], 1, 8, 64, seed=13)
+    c["q"][0, 0] *= 1e6
+    c["q"][0, 1] *= 1e-20
+    c["q"][0, 2] = 0
+    c["q"][1, 3, 5] = float("nan")
+    out, lse, _ = _run(c, D.DTYPE_F32)
+    want = expected(c)
+    want[0][np.isnan(want[1])] = np.nan
+    check(out, lse, want)
+
+
+def test_timeout_is_recorded_and_the_next_call_is_right():
+    c = cache_case([3000, 800], [1, 2], 2, 8, 128, seed=14)
+    long = cache_case([100000], [1], 2, 8, 128, seed=15)   # a dozen pages and more for every SM: they cannot all be there at once
+    try:
+        D.dsa_debug_set_wait_limit_ns(0)
+        for _ in range(3):
+            _, _, bits = _run(long)
+            assert bits & D.DEVERR_TIMEOUT
+    finally:
+        D.dsa_debug_set_wait_limit_ns(2_000_000_000)
+    out, lse, bits = _run(c)
+    check(out, lse, expected(c))
+    assert bits == 0

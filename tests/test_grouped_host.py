@@ -69,6 +69,38 @@ def test_append_refusals(L):
     assert _append(L, b=_batch(T=0), k=N, v=N, q=N, cache=N, q_out=N) == OK          # nothing to do
 
 
+def _attention(L, q=_h(), cache=FK, b=None, heads=16, kv=4, dim=128, scale=0.0625, out=FK, dtype=0, ws=WSP, n=1 << 40):
+    return L.dsa_kv8_attention(q, cache, b or _batch(), heads, kv, dim, scale, out, dtype, N, ws, n, N, N)
+
+
+def _attention_errors(L, call):
+    _shapes(L, call)
+    for name in ("q", "out", "ws"):
+        assert call(L, **{name: N}) == INVALID
+    assert call(L, q=_h(data=None)) == INVALID and call(L, q=_h(data=0x30000008)) == ALIGN
+    assert call(L, q=_h(tok=-8)) == INVALID and call(L, q=_h(head=-8)) == INVALID
+    assert call(L, q=_h(tok=1020)) == ALIGN and call(L, q=_h(head=12)) == ALIGN
+    for name in ("out", "ws"):
+        assert call(L, **{name: ODD}) == ALIGN
+    assert call(L, dtype=2) == INVALID and call(L, dtype=-1) == INVALID
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(L, scale=scale) == INVALID
+    assert call(L, n=1024) == WS
+
+
+def test_kv8_attention_refusals(L):
+    _attention_errors(L, _attention)
+    assert _attention(L, cache=N) == INVALID and _attention(L, cache=ODD) == ALIGN
+    assert _attention(L, b=_batch(max_pages=1)) == INVALID
+    assert _attention(L, b=_batch(T=0), q=N, cache=N, out=N, ws=N) == OK
+    assert _attention(L, b=_batch(T=1 << 28, max_q=1 << 27), heads=128, kv=1) == UNSUPPORTED
+    n = ctypes.c_size_t(0)
+    assert L.dsa_kv8_attention_workspace_size(_batch(), 16, 4, 128, ctypes.byref(n)) == OK and n.value > 0
+    assert L.dsa_kv8_attention_workspace_size(_batch(), 16, 4, 128, N) == INVALID
+    assert L.dsa_kv8_attention_workspace_size(N, 16, 4, 128, ctypes.byref(n)) == INVALID
+    assert L.dsa_kv8_attention_workspace_size(_batch(), 16, 5, 128, ctypes.byref(n)) == UNSUPPORTED
+
+
 def test_kv8_page_bytes_and_views():
     kv, dim = 3, 64
     page = D.kv8_page_bytes(kv, dim)
@@ -112,10 +144,11 @@ def test_oracle_grouped_attention():
     """The oracle against torch's definition of softmax over a dense mask."""
     g = torch.Generator().manual_seed(5)
     q, k, v = (torch.randn(s, generator=g, dtype=torch.float64) for s in ((6, 6, 16), (9, 2, 16), (9, 2, 16)))
-    out, lse = O.grouped_attention(q.numpy(), k.numpy(), v.numpy(), -2, 0.3)
+    out, lse, size = O.grouped_attention(q.numpy(), k.numpy(), v.numpy(), -2, 0.3)
     kk, vv = k.repeat_interleave(3, 1), v.repeat_interleave(3, 1)
     s = 0.3 * torch.einsum("nhd,lhd->nhl", q, kk)
     s = s.masked_fill(torch.arange(9) > torch.arange(6)[:, None, None] - 2, -float("inf"))
     assert np.all(out[:2] == 0) and np.all(lse[:2] == -np.inf)
     want = torch.einsum("nhl,lhd->nhd", torch.softmax(s[2:], -1), vv)
+    assert np.allclose(size[2:], torch.einsum("nhl,lhd->nhd", torch.softmax(s[2:], -1), vv.abs()).numpy())
     assert np.allclose(out[2:], want.numpy()) and np.allclose(lse[2:], torch.logsumexp(s[2:], -1).numpy())
