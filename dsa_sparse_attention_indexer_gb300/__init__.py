@@ -91,6 +91,11 @@ class DsaHeads(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("token_stride", c_int64), ("head_stride", c_int64)]
 
 
+class DsaPrompt(ctypes.Structure):
+    _fields_ = [("batch", c_int32), ("max_q_len", c_int32), ("max_k_len", c_int32), ("reserved", c_int32),
+                ("total_q", c_int64), ("total_k", c_int64), ("q_start", c_void_p), ("k_start", c_void_p)]
+
+
 _lib = None
 
 _SIGS = {
@@ -161,6 +166,9 @@ _SIGS = {
     "dsa_kv8_attention_workspace_size": (c_int32, [POINTER(DsaBatch), c_int32, c_int32, c_int32, POINTER(c_size_t)]),
     "dsa_kv8_attention": (c_int32, [POINTER(DsaHeads), c_void_p, POINTER(DsaBatch), c_int32, c_int32, c_int32, c_float, c_void_p,
                                     c_int32, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "dsa_prompt_attention_workspace_size": (c_int32, [POINTER(DsaPrompt), c_int32, c_int32, c_int32, POINTER(c_size_t)]),
+    "dsa_prompt_attention": (c_int32, [POINTER(DsaHeads), POINTER(DsaHeads), POINTER(DsaHeads), POINTER(DsaPrompt), c_int32, c_int32,
+                                       c_int32, c_float, c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "dsa_cp_topk_merge": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p,
                                     c_void_p]),
     "dsa_cp_topk_localize": (c_int32, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -818,6 +826,73 @@ def dsa_kv8_attention(q, cache, batch: Batch, *, kv_heads: int, softmax_scale=No
     ws = _ws(ws, nbytes, dev, stream)
     _call("dsa_kv8_attention", dev, ctypes.byref(cq), _ptr(cache), batch.ref(), heads, kv_heads, dim, softmax_scale, _ptr(out),
           out_dtype, _ptr(lse), _ptr(ws), ws.numel(), _ptr(dev_status), _stream(stream, dev))
+    return out
+
+
+class PromptBatch:
+    """Owns the device tensors of a batch of packed sequences and the dsa_prompt struct over them.
+
+    q_start int32 [B+1] and k_start int32 [B+1] (device; None: q_start).  Host bounds default to
+    the tensors' values (read once, with a device sync).
+    """
+
+    def __init__(self, q_start, k_start=None, *, max_q_len=None, max_k_len=None, total_q=None, total_k=None):
+        self.q_start = _need(q_start, torch.int32, "q_start")
+        self.k_start = self.q_start if k_start is None else _need(k_start, torch.int32, "k_start", q_start.device, q_start.numel())
+        if q_start.numel() < 2:
+            raise ValueError(f"q_start must hold at least 2 entries, got {q_start.numel()}")
+        known = {}
+        for name, t, longest, total in (("q", self.q_start, max_q_len, total_q), ("k", self.k_start, max_k_len, total_k)):
+            if longest is None or total is None:
+                s = t.cpu()
+                longest = int((s[1:] - s[:-1]).max()) if longest is None else longest
+                total = int(s[-1]) if total is None else total
+            known[name] = int(longest), int(total)
+        (max_q, n_q), (max_k, n_k) = known["q"], known["k"]
+        self.c = DsaPrompt(q_start.numel() - 1, max_q, max_k, 0, n_q, n_k, self.q_start.data_ptr(), self.k_start.data_ptr())
+
+    @property
+    def total_q(self) -> int:
+        return self.c.total_q
+
+    @property
+    def total_k(self) -> int:
+        return self.c.total_k
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def dsa_prompt_attention_workspace_size(batch: PromptBatch, heads: int, kv_heads: int, head_dim: int) -> int:
+    n = c_size_t(0)
+    _check("dsa_prompt_attention_workspace_size",
+           lib().dsa_prompt_attention_workspace_size(batch.ref(), heads, kv_heads, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def dsa_prompt_attention(q, k, v, batch: PromptBatch, *, softmax_scale=None, out=None, out_dtype=DTYPE_BF16, lse=None, ws=None,
+                         dev_status=None, stream=None):
+    """Causal attention of packed sequences: q bf16 [total_q, heads, head_dim], k and v bf16 [total_k,
+    kv_heads, head_dim], any strides of rows and heads; a sequence's queries are its last tokens.
+    softmax_scale defaults to head_dim ** -0.5.  Returns out [total_q, heads, head_dim]
+    (allocated if not given)."""
+    T = batch.total_q
+    cq = _heads(q, "q", None, T)
+    dev, heads, dim = q.device, q.shape[1], q.shape[2]
+    ck, cv = _heads(k, "k", dev, batch.total_k), _heads(v, "v", dev, batch.total_k)
+    kv_heads = k.shape[1]
+    for name, t in (("k", k), ("v", v)):
+        if tuple(t.shape[1:]) != (kv_heads, dim):
+            raise ValueError(f"{name} must be [rows, {kv_heads}, {dim}], got {tuple(t.shape)}")
+    _need(batch.q_start, torch.int32, "batch.q_start", dev)
+    softmax_scale, out = _attention_args(q, T, heads, dim, softmax_scale, out, out_dtype, lse, dev_status, stream)
+    nbytes = 0
+    if ws is None:
+        with torch.cuda.device(dev):
+            nbytes = dsa_prompt_attention_workspace_size(batch, heads, kv_heads, dim)
+    ws = _ws(ws, nbytes, dev, stream)
+    _call("dsa_prompt_attention", dev, ctypes.byref(cq), ctypes.byref(ck), ctypes.byref(cv), batch.ref(), heads, kv_heads, dim,
+          softmax_scale, _ptr(out), out_dtype, _ptr(lse), _ptr(ws), ws.numel(), _ptr(dev_status), _stream(stream, dev))
     return out
 
 

@@ -143,8 +143,8 @@ dsa_status dsa_device_status_read(const int32_t* dev_status, void* stream, int32
 /* Testing hook for failure detection, process-wide: the limit, in ns, of the
  * pipeline waits of the decode indexer's score kernel (dsa_indexer_topk and
  * dsa_indexer_topk_mxfp4 on a batch of one row per request) and of the
- * attention kernels of dsa_window_mla, dsa_tree_mla and dsa_kv8_attention,
- * launched after the call.  2e9 (2 s) by default; 0 makes every wait that is not already
+ * attention kernels of dsa_window_mla, dsa_tree_mla, dsa_kv8_attention and
+ * dsa_prompt_attention, launched after the call.  2e9 (2 s) by default; 0 makes every wait that is not already
  * satisfied give up at once.  A wait that gives up records
  * DSA_DEVERR_TIMEOUT; the kernel then lets its copies and MMAs in flight
  * finish, releases its tensor memory and returns, the merge sees only what
@@ -680,6 +680,46 @@ dsa_status dsa_kv8_attention_workspace_size(const dsa_batch* b, int32_t heads, i
 dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache, const dsa_batch* b, int32_t heads,
                              int32_t kv_heads, int32_t head_dim, float softmax_scale, void* out, int32_t out_dtype,
                              float* lse, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* dsa_prompt_attention: causal attention of packed prompts on their fresh keys and
+ *   values, no cache involved (prefill of ordinary heads, and of latent attention
+ *   with its keys and values written out, "GLM-5.3 推理全链路(一)", 第五阶段).  Sequence r
+ *   holds rows q_start[r] .. q_start[r+1] - 1 of q and k_start[r] .. k_start[r+1] - 1 of
+ *   k and v; with q_len and k_len their numbers, row t of q sees keys
+ *   j <= k_len - q_len + t: the queries are the sequence's last tokens.
+ *     S_hj = softmax_scale * <q_th, k_j>,  out_th = sum_j softmax_j(S_hj) v_j,
+ *     lse_th = log sum_j exp(S_hj)
+ *   with keys and values of head h * kv_heads / heads.  A row that sees nothing
+ *   gives out = 0 and lse = -inf.  Products of bf16 are exact; softmax statistics and
+ *   accumulation are fp32; probabilities are rounded to bf16 for the product with
+ *   the values, each off by 2^-8 of itself.  Scores up to 2^30 in magnitude.
+ *   Infinite and NaN keys and values count for the rows that see them alone.  Rows at
+ *   and above q_start[B] are left as they were; rows of k and v at and above
+ *   k_start[B] may hold anything.
+ *   q        heads heads of total_q rows; k, v  kv_heads heads of total_k rows, bf16;
+ *            strides as in a dsa_heads, below 2^38 and, along an axis of several
+ *            entries, not 0 (DSA_ERR_UNSUPPORTED)
+ *   out      device [T, heads, head_dim], bf16 or fp32 per out_dtype
+ *   lse      device fp32 [T, heads] or NULL
+ *   ws       device workspace of dsa_prompt_attention_workspace_size() bytes; nothing
+ *            in it has to start at zero or is kept between calls
+ *   total_q and total_k above 2^31 - 256 return DSA_ERR_UNSUPPORTED.               */
+typedef struct dsa_prompt {
+    int32_t batch;              /* B >= 1 sequences                                 */
+    int32_t max_q_len;          /* host upper bound on every q_len                  */
+    int32_t max_k_len;          /* host upper bound on every k_len                  */
+    int32_t reserved;           /* 0                                                */
+    int64_t total_q;            /* rows of q, at least q_start[B]                   */
+    int64_t total_k;            /* rows of k and v, at least k_start[B]             */
+    const int32_t* q_start;     /* device [B+1], q_start[0] = 0                     */
+    const int32_t* k_start;     /* device [B+1], k_start[0] = 0; may be q_start     */
+} dsa_prompt;
+dsa_status dsa_prompt_attention_workspace_size(const dsa_prompt* b, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                               size_t* bytes);
+dsa_status dsa_prompt_attention(const dsa_heads* q, const dsa_heads* k, const dsa_heads* v, const dsa_prompt* b,
+                                int32_t heads, int32_t kv_heads, int32_t head_dim, float softmax_scale, void* out,
+                                int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                void* stream);
 
 #ifdef __cplusplus
 }

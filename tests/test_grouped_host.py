@@ -101,6 +101,34 @@ def test_kv8_attention_refusals(L):
     assert L.dsa_kv8_attention_workspace_size(_batch(), 16, 5, 128, ctypes.byref(n)) == UNSUPPORTED
 
 
+def _prompt_batch(B=2, max_q=64, max_k=64, T=100, K=100, qs=0x10000000, ks=0x10000100, reserved=0):
+    return ctypes.byref(D.DsaPrompt(B, max_q, max_k, reserved, T, K, qs, ks))
+
+
+def _prompt(L, q=_h(), k=_h(), v=_h(), b=None, heads=16, kv=4, dim=128, scale=0.0625, out=FK, dtype=0, ws=WSP, n=1 << 40):
+    return L.dsa_prompt_attention(q, k, v, b or _prompt_batch(), heads, kv, dim, scale, out, dtype, N, ws, n, N, N)
+
+
+def test_prompt_attention_refusals(L):
+    _attention_errors(L, lambda L, n=1 << 40, **kw: _prompt(L, n=min(n, 255) if n < 1 << 40 else n, **kw))
+    for name in ("k", "v"):
+        assert _prompt(L, **{name: N}) == INVALID
+        assert _prompt(L, **{name: _h(data=0x30000002)}) == ALIGN and _prompt(L, **{name: _h(tok=-8)}) == INVALID
+    for name in ("q", "k", "v"):
+        assert _prompt(L, **{name: _h(tok=0)}) == UNSUPPORTED and _prompt(L, **{name: _h(head=0)}) == UNSUPPORTED
+        assert _prompt(L, **{name: _h(tok=1 << 38)}) == UNSUPPORTED
+    for kw in (dict(B=0), dict(max_q=-1), dict(max_k=-1), dict(T=-1), dict(K=-1), dict(qs=None), dict(ks=None), dict(reserved=1), dict(T=129), dict(K=129)):
+        assert _prompt(L, b=_prompt_batch(**kw)) == INVALID
+    assert _prompt(L, b=_prompt_batch(B=65536)) == UNSUPPORTED
+    assert _prompt(L, b=_prompt_batch(max_q=1 << 30, T=(1 << 31) - 1)) == UNSUPPORTED
+    assert _prompt(L, b=_prompt_batch(T=0), q=N, k=N, v=N, out=N, ws=N) == OK
+    n = ctypes.c_size_t(0)
+    assert L.dsa_prompt_attention_workspace_size(_prompt_batch(), 16, 4, 128, ctypes.byref(n)) == OK and n.value > 0
+    assert L.dsa_prompt_attention_workspace_size(_prompt_batch(), 16, 4, 128, N) == INVALID
+    assert L.dsa_prompt_attention_workspace_size(N, 16, 4, 128, ctypes.byref(n)) == INVALID
+    assert L.dsa_prompt_attention_workspace_size(_prompt_batch(), 16, 4, 192, ctypes.byref(n)) == UNSUPPORTED
+
+
 def test_kv8_page_bytes_and_views():
     kv, dim = 3, 64
     page = D.kv8_page_bytes(kv, dim)
