@@ -18,6 +18,8 @@ __host__ __device__ constexpr int v_at(int dim) { return kPage * dim; }
 __host__ __device__ constexpr int scale_at(int dim) { return 2 * kPage * dim; }
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // e in [-126, 127]
+// 2^-d for a whole d in [-126, 126].
+__device__ __forceinline__ float minus_pow2(float d) { return __int_as_float(__float_as_int(8388608.0f + 127.0f - d) << 23); }
 // The exponent of a stored scale.  Whatever the word holds, it is one of the cache's.
 __device__ __forceinline__ int scale_exponent(float s) {
     return max(-kMaxExp, min(kMaxExp, (int)((__float_as_uint(s) >> 23) & 0xffu) - 127));

@@ -50,6 +50,7 @@ struct Args {
     const uint8_t* cache;
     BatchDev b;
     int kv_heads, group;
+    int max_rows;               // requests with more query rows are not this kernel's
     float scale;                // softmax scale * log2(e)
     void* out;
     int out_f32;
@@ -113,7 +114,7 @@ __device__ __forceinline__ Request request(const Args& a, int r) {
     w.row0 = b.q_start[r];
     const int n = (int)max((int64_t)0, end - w.row0);
     w.prefix = b.seq_len[r] - (b.q_start[r + 1] - b.q_start[r]);
-    w.rows = n * a.group;
+    w.rows = n * a.group > a.max_rows ? 0 : n * a.group;
     w.blocks = (w.rows + COLS - 1) / COLS;
     w.room = (int64_t)b.max_pages * kPage;
     return w;
@@ -231,8 +232,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ void e4m3x4_h2(uint32_t four, uint32_t& lo, uint32_t& hi) {
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(four));
 }
-// 2^-d for a whole d in [-126, 126].
-__device__ __forceinline__ float minus_pow2(float d) { return __int_as_float(__float_as_int(8388608.0f + 127.0f - d) << 23); }
 // The bytes of a word that are NaN codes, as 4 bits.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     const uint32_t m = __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x01010101u;
@@ -697,6 +696,11 @@ kv8_merge_kernel(const __grid_constant__ Args a, int G) {
     }
 }
 
+dsa_status launch_prefill(const dsa_heads* q, const uint8_t* cache, const dsa_batch* b, int32_t heads, int32_t kv_heads, int32_t dim,
+                          int32_t min_rows, float scale_log2, void* out, int out_f32, float* lse, int32_t* st, cudaStream_t s);
+// Requests with more query rows than this are the prefill kernel's.
+constexpr int kTcRows = 64;
+
 // Query rows of a row block.
 static int columns(int64_t max_rows, int dim) {
     if (max_rows <= 8) return 8;
@@ -766,7 +770,19 @@ extern "C" dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache
     a.lse = lse;
     a.part_o = static_cast<float*>(ws);
     a.st = dev_status;
-    const int64_t max_rows = (int64_t)b->max_q_len * a.group;
+    const cudaStream_t s = as_stream(stream);
+    const int64_t longest = std::min<int64_t>(b->max_q_len, b->total_q) * a.group;
+    a.max_rows = 0x7fffffff;
+    // q's strides as a tensor map takes them; a q that does not lie so has its rows taken one by one
+    const bool mapped = (heads == 1 || q->head_stride > 0) && (b->total_q == 1 || q->token_stride > 0) && q->head_stride < 1LL << 38 && q->token_stride < 1LL << 38;
+    if (longest > kv8::kTcRows && mapped) {
+        // a single request is the prefill kernel's however few of its rows there turn out to be
+        const bool all = b->batch == 1;
+        a.max_rows = kv8::kTcRows;
+        vs = kv8::launch_prefill(q, cache, b, heads, kv_heads, head_dim, all ? 0 : kv8::kTcRows + 1, a.scale, out, a.out_f32, lse, dev_status, s);
+        if (vs != DSA_OK || all) return vs;
+    }
+    const int64_t max_rows = std::min<int64_t>(longest, a.max_rows);
     const int cols = kv8::columns(max_rows, head_dim);
     // the pages of a CTA's share are counted in 32 bits
     if ((b->total_q * a.group / cols + b->batch) * kv_heads > 0x7fffffffLL * sms / (((int64_t)b->max_seq_len + kPage - 1) / kPage) / 2)
@@ -775,7 +791,6 @@ extern "C" dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache
     const int64_t blocks = std::min<int64_t>(b->total_q * a.group / cols + b->batch, b->total_q * a.group);
     const int64_t pages = ((int64_t)b->max_seq_len + kPage - 1) / kPage;
     const int G = (int)std::min<int64_t>(sms, std::max<int64_t>(1, blocks) * kv_heads * pages);
-    const cudaStream_t s = as_stream(stream);
     switch (head_dim / 64 * 64 + cols) {
         case 64 + 8: return kv8::launch<64, 1>(a, sms, G, s);
         case 64 + 16: return kv8::launch<64, 2>(a, sms, G, s);

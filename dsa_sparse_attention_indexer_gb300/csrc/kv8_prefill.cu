@@ -1,0 +1,512 @@
+// Attention of grouped heads over the KV8 cache, for requests with many query rows
+// (prefill chunks): the tiles, the pipeline and the softmax of the packed prompts' kernel,
+// on fp16 operands.
+//   S = Q K^T      tcgen05.mma kind::f16, M = 128 rows (tokens x the group's heads), N = 128 keys
+//   O += P V       P from TMEM, V as it lies in the cache, with a block's tokens side by side:
+//                  a K-major operand
+// Converter warps turn a step's 128 keys (two pages) into the 128-byte-swizzled stages that
+// the MMAs read: 16 codes are one load, two stores of 16 bytes, and conversions only, as
+// E4M3 is exact in fp16; a code's load for the next stage is under way while the others of
+// this one are converted.  The blocks' scales stay out of the operands: the softmax takes a
+// block's 16 scores times 2^ek, and P carries 2^ev.  With t = score + ev (log2 units), R
+// the row's reference, a whole number, so that ev - R is exact,
+//   P = 2^(t - R) <= 2^kTop in fp16,  O = sum P code_v,  l = sum 2^-ev P,  out = O / l
+//
+// Q comes by TMA as bf16 and is turned, in place, into fp16 by the softmax threads, each its
+// own row: times the power of two that puts its largest |q| in [2^14, 2^15).
+//
+// Warps: softmax as there; then a warpgroup with one warp each for the MMAs, the items and
+// Q's copies; then the converters.
+#include <algorithm>
+
+#include "grouped_tc.cuh"
+#include "kv8.cuh"
+
+namespace dsa {
+
+int device_sm_count();
+
+namespace kv8 {
+
+using namespace sm100;
+using namespace mlc;
+using namespace gtc;
+
+struct PrefillArgs {
+    const uint8_t* cache;
+    BatchDev b;
+    int kv_heads, group, tokens;
+    int min_rows;               // requests with fewer query rows are not this kernel's
+    float scale;                // softmax scale * log2(e)
+    void* out;
+    int out_f32;
+    float* lse;
+    int32_t* st;
+};
+
+namespace {
+
+constexpr float kFirst = 7.0f, kTop = 15.0f;               // log2 of a new reference's P, and of the largest
+constexpr int kMeta = 8;                                   // steps whose scales are kept: more than the ring holds
+
+template <int D> struct TcShape {
+    static constexpr int kDim = D;
+    static constexpr int kTiles = D <= 128 ? 2 : 1;
+    static constexpr int kSoft = kTiles * 4;
+    static constexpr int kConv = D <= 128 ? 4 : 8;         // converter warps
+    static constexpr int kConv0 = kSoft + 4;               // the first of them
+    static constexpr int kThreads = 512;
+    static constexpr int kPart = D < 128 ? D : 128;
+    static constexpr int kParts = D / kPart;
+    static constexpr int kStage = kBox * kPart / 64;
+    static constexpr int kQ = kTiles * kBox * (D / 64);
+    static constexpr int kStages = (232448 - 1024 - 2048 - kQ) / kStage < 10 ? (232448 - 1024 - 2048 - kQ) / kStage : 10;
+    static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
+    static constexpr uint32_t kIdQK = idesc_f16_f32(128, kKeys, false, false), kIdPV = idesc_f16_f32(128, kPart, false, false);
+    static constexpr bool kValuesMn = false, kCleans = false;
+    static constexpr uint32_t s(int i) { return 128 * i; }
+    static constexpr uint32_t o(int i) { return 256 + 128 * i; }
+};
+
+struct Block {
+    Pipe pipe;
+    uint64_t q_raw;             // Q has come as bf16
+    float k2[kMeta][8];         // scales of a step's blocks' keys
+    float ev[kMeta][8];         // exponents of their values'
+    uint32_t here[kMeta];       // bit h: the step's page h is in the cache
+};
+static_assert(sizeof(Block) <= 2048, "the block behind the ring");
+
+__device__ __forceinline__ void codes4_h2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(four));
+}
+__device__ __forceinline__ uint32_t nan_of(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
+kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap qmap) {
+    using S = TcShape<D>;
+    constexpr int kMmaWarp = S::kSoft, kItemWarp = kMmaWarp + 1, kQWarp = kMmaWarp + 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t* q_smem = smem;
+    uint8_t* ring = smem + S::kQ;
+    Block* blk = reinterpret_cast<Block*>(ring + S::kStages * S::kStage);
+    Pipe* pipe = &blk->pipe;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(&blk->q_raw, 1);
+        mbar_init(&pipe->q_full, S::kSoft);
+        mbar_init(&pipe->q_empty, 1);
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&pipe->kv_full[i], S::kConv);
+            mbar_init(&pipe->kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&pipe->s_full[i], 1);
+            mbar_init(&pipe->p_full[i], 4);
+            mbar_init(&pipe->o_done[i], 1);
+        }
+        mbar_init(&pipe->drain, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&pipe->item_full[i], 1);
+            mbar_init(&pipe->item_empty[i], S::kSoft + 2 + S::kConv);   // softmax, MMAs, Q's copies, converters
+        }
+        pipe->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&pipe->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = pipe->tmem_base;
+    pdl_wait();
+    pdl_trigger();
+    const BatchDev& b = a.b;
+    const Role me = {pipe, b.wait_ns, a.st, warp, lane};
+
+    // registers: 128 a thread at launch; 256 x 200 + 256 x 56, at 256 dims 128 x 200 + 384 x 104 = 512 x 128
+    if (warp < S::kSoft) more_registers<200>();
+    else fewer_registers<S::kTiles == 2 ? 56 : 104>();
+
+    if (warp < S::kSoft) {
+        // ======================================================== softmax: a thread a row
+        const int x = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int tok_of = row / a.group, head_of = row % a.group;
+        const int heads = a.kv_heads * a.group;
+        uint32_t t = 0, q_items = 0, u0 = 0;               // the tile's steps, items with a Q and steps of the CTA so far
+        Item it;
+        bool ok = true;
+        for (int k = 0; ok && me.take(k, it); ++k) {
+            const int count = it.count(x, a.tokens), steps = it.steps(x, a.tokens);
+            const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0);
+            const int tok = it.tok0 + x * a.tokens + tok_of;
+            const bool live = tok_of < count;
+            const int see = live ? it.see(tok) : INT32_MAX;
+            float c = 0.f;                                 // log2 units of a score
+            if (most > 0) {
+                ok = me.wait_all(&blk->q_raw, q_items++);
+                if (!ok) break;
+                if (steps > 0) {
+                    // the row's chunks of 8 dims, swizzled
+                    uint8_t* mine = q_smem + x * (D / 64) * kBox + row * 128;
+                    uint32_t top = 0;
+#pragma unroll 4
+                    for (int j = 0; j < D / 8; ++j) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(mine + j / 8 * kBox + ((j ^ row) & 7) * 16);
+                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t lo = v[e] & 0x7fffu, hi = v[e] >> 16 & 0x7fffu;
+                            if (lo < 0x7f80u) top = max(top, lo);          // of finite ones
+                            if (hi < 0x7f80u) top = max(top, hi);
+                        }
+                    }
+                    const int e = max(-100, min(100, top ? 14 - ((int)(top >> 7) - 127) : 0));
+                    const float up = pow2(e);
+                    c = a.scale * pow2(-e);
+#pragma unroll 4
+                    for (int j = 0; j < D / 8; ++j) {
+                        uint4* p = reinterpret_cast<uint4*>(mine + j / 8 * kBox + ((j ^ row) & 7) * 16);
+                        uint4 w = *p;
+                        w.x = bf16x2_scaled_to_h2(w.x, up), w.y = bf16x2_scaled_to_h2(w.y, up);
+                        w.z = bf16x2_scaled_to_h2(w.z, up), w.w = bf16x2_scaled_to_h2(w.w, up);
+                        *p = w;
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pipe->q_full);
+            }
+            float ref = 0.f, sum = 0.f;                    // R, l
+            for (int i = 0; ok && i < steps; ++i, ++t) {
+                const int s = S::kTiles == 2 ? x : t & 1;
+                ok = me.wait_all(&pipe->s_full[s], S::kTiles == 2 ? t : t >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t w[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(tmem + lanes + S::s(s) + 32 * q, w[q]);
+                const int u = (u0 + i) % kMeta;
+                float ck[8], ev[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 y = *reinterpret_cast<const float4*>(&blk->k2[u][4 * h]), z = *reinterpret_cast<const float4*>(&blk->ev[u][4 * h]);
+                    ck[4 * h] = y.x * c, ck[4 * h + 1] = y.y * c, ck[4 * h + 2] = y.z * c, ck[4 * h + 3] = y.w * c;
+                    ev[4 * h] = z.x, ev[4 * h + 1] = z.y, ev[4 * h + 2] = z.z, ev[4 * h + 3] = z.w;
+                }
+                const uint32_t here = blk->here[u];
+                tmem_ld_wait();
+                const int lim = see - i * kKeys;           // keys of the step that the row sees
+                if (__any_sync(0xffffffffu, lim < kKeys) || here != 3u) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * q + j >= lim || !(here >> (q >> 1) & 1)) w[q][j] = 0xff800000u;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const uint32_t* v = &w[g >> 1][16 * (g & 1)];
+                    float m = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+#pragma unroll
+                    for (int j = 2; j < 16; j += 2) m = max3(m, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                    top = fmaxf(top, fmaf(m, ck[g], ev[g]));
+                }
+                const float fresh = top == -INFINITY ? 0.f : rintf(top) - kFirst;
+                if (i == 0) {
+                    ref = fresh;
+                } else if (__any_sync(0xffffffffu, top > ref + kTop)) {
+                    const float to = top > ref + kTop ? fresh : ref, f = exp2f(ref - to);
+                    ok = me.wait_all(&pipe->o_done[x], t - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    rescale_o<D>(tmem + lanes + S::o(x), f);
+                    sum *= f;
+                    ref = to;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int g = 4 * h; g < 4 * h + 4; ++g) {
+                        const float2 c2 = make_float2(ck[g], ck[g]), r2 = make_float2(ev[g] - ref, ev[g] - ref);
+                        float2 sums = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t* v = &w[g >> 1][16 * (g & 1) + 2 * j];
+                            float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, r2);
+                            y.x = ex2_approx(y.x);
+                            y.y = ex2_approx(y.y);
+                            sums = add2(sums, y);
+                            p[8 * (g & 3) + j] = pack_h2(y.x, y.y);
+                        }
+                        sum = fmaf(sums.x + sums.y, minus_pow2(ev[g]), sum);
+                    }
+                    tmem_st_32x32b_x32(tmem + lanes + S::s(s) + 32 * h, p);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pipe->p_full[s]);
+            }
+            u0 += most;
+            // ---- the rows' outputs
+            if (ok && steps > 0) {
+                // each phase in turn, as one could be taken for the one after the next
+                ok = S::kTiles == 2 || steps == 1 || me.wait(&pipe->o_done[x], t - 2);
+                ok = __all_sync(0xffffffffu, ok && me.wait(&pipe->o_done[x], t - 1));
+                tc_fence_after();
+            }
+            if (ok && count > 0) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int64_t at = (int64_t)(it.q_row + tok) * heads + it.h * a.group + head_of;
+                const bool odd = pipe->any_odd[k % kItems] != 0;
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    if (steps > 0) {
+                        tmem_ld_32x32b_x32(tmem + lanes + S::o(x) + d, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0;
+                    }
+                    if (live) {
+                        float y[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(o[j]) * inv;
+                        if (odd) {
+                            // NaN values of masked steps that this row sees
+                            for (int e = 0; e < kMasked * kKeys; ++e) {
+                                const int key = it.masked_from() * kKeys + e;
+                                if (!(pipe->odd[k % kItems][e / kKeys][e % kKeys / 32] >> (e & 31) & 1) || key >= see) continue;
+                                const int64_t page = b.page_table[(int64_t)it.k_row * b.max_pages + key / kPage];
+                                const uint8_t* v = a.cache + (page * a.kv_heads + it.h) * head_bytes(D) + v_at(D) + key % kPage / kBlock * (kBlock * D) +
+                                                   d * kBlock + key % kBlock;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if ((v[j * kBlock] & 0x7f) == 0x7f) y[j] = __int_as_float(0x7fc00000);
+                            }
+                        }
+                        write_32(a.out, a.out_f32, at * D + d, y);
+                    }
+                    __syncwarp();
+                }
+                if (live && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+            }
+            tc_fence_before();                             // O is read before the next item's first P says so
+            me.done_with(k);
+        }
+    } else if (warp == kMmaWarp) {
+        issue_mmas<S>(me, tmem, smem_addr(q_smem), smem_addr(ring), a.tokens);
+    } else if (warp == kItemWarp) {
+        lay_out_items(
+            me, b.batch, a.kv_heads, a.tokens * S::kTiles,
+            [&](int r, int& qs, int& qn) {
+                qs = b.q_start[r];
+                qn = (int)max((int64_t)0, min((int64_t)b.q_start[r + 1], b.total_q) - qs);
+                if ((int64_t)qn * a.group < a.min_rows) qn = 0;
+            },
+            [&](int r, Item& it) {
+                const int len = b.seq_len[r];
+                const int64_t room = (int64_t)b.max_pages * kPage;
+                it.k_row = r;
+                it.len = len - (b.q_start[r + 1] - it.q_row) + it.n;
+                it.cap = (int)min((int64_t)INT32_MAX, room);
+                if (lane == 0 && it.h == 0 && it.tok0 == 0) {
+                    if (it.len < it.n) record_error(a.st, DSA_DEVERR_INDEX_RANGE, it.len - it.n);
+                    else if (len > room) record_error(a.st, DSA_DEVERR_INDEX_RANGE, len);
+                }
+            });
+    } else if (warp == kQWarp) {
+        // ======================================================== Q's copies, by one thread
+        uint32_t items = 0;
+        bool ok = true;
+        Item it;
+        for (int k = 0; me.take(k, it); ++k) {
+            me.done_with(k);
+            const int steps[2] = {it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0};
+            if (lane == 0 && ok && max(steps[0], steps[1]) > 0) {
+                if (items > 0) ok = me.wait(&pipe->q_empty, items - 1);
+                if (ok) {
+                    int tiles = 0;
+                    for (int x = 0; x < S::kTiles; ++x) tiles += steps[x] > 0;
+                    mbar_arrive_expect_tx(&blk->q_raw, (uint32_t)(tiles * D * 2 * a.tokens * a.group));
+                    for (int x = 0; x < S::kTiles; ++x)
+                        for (int c = 0; c < D / 64 && steps[x] > 0; ++c)
+                            tma_load_3d(q_smem + (x * (D / 64) + c) * kBox, &qmap, 64 * c, it.h * a.group, it.q_row + it.tok0 + x * a.tokens, &blk->q_raw);
+                    ++items;
+                }
+            }
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        }
+        if (lane == 0 && items > 0) mbar_wait(&blk->q_raw, (items - 1) & 1);   // copies in flight end before the CTA does
+    } else if (warp >= S::kConv0) {
+        // ======================================================== converters
+        constexpr int kThr = S::kConv * 32;
+        constexpr int kUnits = kKeys * S::kPart / 16 / kThr;                   // 16-byte pieces of a stage, a thread
+        const int ct = tid - S::kConv0 * 32;
+        uint32_t n = 0, u = 0;                             // stages and steps so far
+        bool ok = true;
+        Item it;
+        for (int k = 0; ok && me.take(k, it); ++k) {
+            const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0), masked = it.masked_from();
+            int last = it.n - 1;                           // the item's last token
+            last = min(last, it.tok0 + a.tokens * S::kTiles - 1);
+            const int top = it.see(last);                  // keys that some row of the item sees
+            const bool tells = it.h == 0 && last == it.n - 1 && ct == 0;       // one item of a request records its pages
+            const int32_t* table = b.page_table + (int64_t)it.k_row * b.max_pages;
+            // the step's pages' parts of the head, NULL where there is none to see
+            auto page = [&](int i, int h) -> const uint8_t* {
+                const int64_t p = 2 * (int64_t)i + h;
+                if (p * kPage >= top) return nullptr;
+                const int64_t id = table[p];
+                if (id < 0 || id >= b.num_pages) {
+                    if (tells) record_error(a.st, DSA_DEVERR_PAGE_RANGE, id);
+                    return nullptr;
+                }
+                return a.cache + (id * a.kv_heads + it.h) * head_bytes(D);
+            };
+            // Piece e of part p of a step's keys (v = 0): 16 dims of a token, or values: a block's 16 tokens
+            // of a dim.  Neighbouring threads take neighbouring pieces.
+            auto piece = [&](const uint8_t* h0, const uint8_t* h1, int v, int p, int e) {
+                const int g = ct + e * kThr;
+                const uint8_t* from;
+                int off;
+                if (!v) {
+                    constexpr int kPer = S::kPart / 16;
+                    const int token = g / kPer;
+                    from = token < kPage ? h0 : h1;
+                    off = token % kPage * D + p * S::kPart + g % kPer * 16;
+                } else {
+                    const int block = g / S::kPart;
+                    from = block < kBlocks ? h0 : h1;
+                    off = v_at(D) + block % kBlocks * (kBlock * D) + (p * S::kPart + g % S::kPart) * 16;
+                }
+                return from ? ldg_pinned(reinterpret_cast<const uint4*>(from + off)) : make_uint4(0, 0, 0, 0);
+            };
+            const uint8_t *h0 = nullptr, *h1 = nullptr, *n0 = nullptr, *n1 = nullptr;
+            uint4 w[kUnits];
+            if (most > 0) {
+                h0 = page(0, 0), h1 = page(0, 1);
+#pragma unroll
+                for (int e = 0; e < kUnits; ++e) w[e] = piece(h0, h1, 0, 0, e);
+            }
+            for (int i = 0; ok && i < most; ++i, ++u) {
+                if (ct < 8) {
+                    // the step's scales
+                    const uint8_t* head = ct < kBlocks ? h0 : h1;
+                    const float* sc = reinterpret_cast<const float*>(head + scale_at(D)) + ct % kBlocks;
+                    blk->k2[u % kMeta][ct] = head ? pow2(scale_exponent(sc[0])) : 1.f;
+                    blk->ev[u % kMeta][ct] = head ? (float)scale_exponent(sc[kBlocks]) : 0.f;
+                    if (ct == 0) blk->here[u % kMeta] = (h0 ? 1u : 0u) | (h1 || (2 * (int64_t)i + 1) * kPage >= top ? 2u : 0u);
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int p = 0; p < S::kParts; ++p) {
+                        if (!ok) break;
+                        const int s = n % S::kStages;
+                        if (n >= S::kStages) ok = me.wait_all(&pipe->kv_empty[s], n / S::kStages - 1);
+                        if (!ok) break;
+                        // what comes next: the step's next part, its values, the next step's keys
+                        const bool more = !(v == 1 && p == S::kParts - 1) || i + 1 < most;
+                        if (v == 1 && p == 0 && i + 1 < most) n0 = page(i + 1, 0), n1 = page(i + 1, 1);
+                        const int nv = p + 1 < S::kParts ? v : 1 - v, np = p + 1 < S::kParts ? p + 1 : 0;
+                        const bool step = v == 1 && p == S::kParts - 1;
+                        uint8_t* stage = ring + s * S::kStage;
+#pragma unroll
+                        for (int e = 0; e < kUnits; ++e) {
+                            const int g = ct + e * kThr;
+                            uint4 c = w[e];
+                            uint32_t to;                   // the piece's first 16 bytes; the others are its neighbour's place
+                            if (v == 0) {
+                                constexpr int kPer = S::kPart / 16;
+                                const int token = g / kPer, j = g % kPer;
+                                to = j / 4 * kBox + token * 128 + ((2 * (j % 4)) ^ (token & 7)) * 16;
+                            } else {
+                                const int block = g / S::kPart, d = g % S::kPart;
+                                to = block / 4 * (S::kPart * 128) + d * 128 + ((2 * (block % 4)) ^ (d & 7)) * 16;
+                                if (i >= masked) {
+                                    // tokens that no row sees become zeros; a NaN joins the rows that see it in the end
+                                    const int seen = top - i * kKeys - block * kBlock;
+                                    uint32_t* q = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) {
+                                        const int left = seen - 4 * y;
+                                        q[y] &= left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+                                        const uint32_t nan = nan_of(q[y]);
+                                        if (nan) {
+                                            q[y] &= ~nan;
+                                            for (int z = 0; z < 4; ++z)
+                                                if (nan >> (8 * z) & 1) {
+                                                    const int key = block * kBlock + 4 * y + z;
+                                                    atomicOr(&pipe->odd[k % kItems][i - masked][key >> 5], 1u << (key & 31));
+                                                }
+                                            pipe->any_odd[k % kItems] = 1;
+                                        }
+                                    }
+                                }
+                            }
+                            uint32_t h[8];
+                            codes4_h2(c.x, h[0], h[1]);
+                            codes4_h2(c.y, h[2], h[3]);
+                            codes4_h2(c.z, h[4], h[5]);
+                            codes4_h2(c.w, h[6], h[7]);
+                            if (more) w[e] = step ? piece(n0, n1, 0, 0, e) : piece(h0, h1, nv, np, e);
+                            const uint32_t base = smem_addr(stage);
+                            st_shared_v4(base + to, h[0], h[1], h[2], h[3]);
+                            st_shared_v4(base + (to ^ 16), h[4], h[5], h[6], h[7]);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pipe->kv_full[s]);
+                        ++n;
+                        if (step) h0 = n0, h1 = n1;
+                    }
+            }
+            me.done_with(k);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+static dsa_status launch_tc(const PrefillArgs& a, const CUtensorMap& q, cudaStream_t s) {
+    using S = TcShape<D>;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(&kv8_prefill_kernel<D>), S::kSmem) != DSA_OK) return DSA_ERR_CUDA;
+    const int64_t most = std::min(a.b.total_q, a.b.total_q / (a.tokens * S::kTiles) + a.b.batch) * a.kv_heads;
+    const unsigned G = (unsigned)std::min<int64_t>(device_sm_count(), most);
+    DSA_CHECK(launch_pdl(kv8_prefill_kernel<D>, dim3(G), dim3(S::kThreads), S::kSmem, s, 1, a, q));
+    return DSA_OK;
+}
+
+// The requests of the batch with at least min_rows query rows.
+dsa_status launch_prefill(const dsa_heads* q, const uint8_t* cache, const dsa_batch* b, int32_t heads, int32_t kv_heads, int32_t dim,
+                          int32_t min_rows, float scale_log2, void* out, int out_f32, float* lse, int32_t* st, cudaStream_t s) {
+    PrefillArgs a = {};
+    a.cache = cache;
+    a.b = to_dev(b);
+    a.kv_heads = kv_heads, a.group = heads / kv_heads, a.tokens = 128 / a.group;
+    a.min_rows = min_rows;
+    a.scale = scale_log2;
+    a.out = out, a.out_f32 = out_f32, a.lse = lse, a.st = st;
+    CUtensorMap qm;
+    if (!make_heads_map(q, dim, heads, b->total_q, (unsigned)a.group, (unsigned)a.tokens, &qm)) return DSA_ERR_CUDA;
+    if (dim == 64) return launch_tc<64>(a, qm, s);
+    if (dim == 128) return launch_tc<128>(a, qm, s);
+    return launch_tc<256>(a, qm, s);
+}
+
+}  // namespace kv8
+}  // namespace dsa

@@ -26,18 +26,31 @@
 
 #include <cudaTypedefs.h>
 
+#include "grouped_tc.cuh"
 #include "kv8.cuh"
-#include "mla_common.cuh"
-#include "sm100.cuh"
 
 namespace dsa {
 
 int device_sm_count();
 
+namespace gtc {
+bool make_heads_map(const dsa_heads* h, int dim, int64_t heads, int64_t rows, unsigned bh, unsigned br, CUtensorMap* out) {
+    const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    // the stride of an axis of one entry says nothing
+    const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? h->head_stride : dim) * 2, (cuuint64_t)(rows > 1 ? h->token_stride : dim * heads) * 2};
+    const cuuint32_t box[3] = {64, bh, br}, estr[3] = {1, 1, 1};
+    return encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(h->data), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace gtc
+
 namespace prompt {
 
 using namespace sm100;
 using namespace mlc;
+using namespace gtc;
 using kv8::wait_for;
 
 struct Args {
@@ -55,14 +68,13 @@ struct Args {
     int32_t* st;
 };
 
-constexpr int kKeys = 128;                                 // of a step
-constexpr int kBox = kKeys * 128;                          // bytes of 128 rows of 64 dims
 constexpr float kGrow = 8.0f;                              // log2 of how far a score may pass its reference
-constexpr int kItems = 2;                                  // laid out ahead
-constexpr int kCleaned = 8;                                // masked steps that may be looked through before their MMA: more than the ring holds
-constexpr int kMasked = 4;                                 // steps of an item that some rows see in part, at most
+
+// kind::f16 with bf16 operands, fp32 sums.
+constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) { return idesc_f16_f32(M, N, false, b_mn) | (1u << 7) | (1u << 10); }
 
 template <int D> struct Shape {
+    static constexpr int kDim = D;
     static constexpr int kTiles = D <= 128 ? 2 : 1;        // tiles of rows of a CTA
     static constexpr int kSoft = kTiles * 4;               // softmax warps
     static constexpr int kThreads = (kSoft + 4) * 32;
@@ -72,84 +84,17 @@ template <int D> struct Shape {
     static constexpr int kQ = kTiles * kBox * (D / 64);
     static constexpr int kStages = (232448 - 1024 - 2048 - kQ) / kStage < 10 ? (232448 - 1024 - 2048 - kQ) / kStage : 10;
     static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
+    static constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, kPart, true);
+    static constexpr bool kValuesMn = true, kCleans = true;
     // TMEM columns
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
 };
 
-struct Item {
-    int32_t q_row, tok0, n;     // the sequence's first row of q, the item's first token, the sequence's tokens; n < 0: no more items
-    int32_t k_row, len, h;      // its first row of k, its keys, the key head
-    int32_t pad[2];
-    // keys that token t sees
-    __device__ __forceinline__ int see(int t) const { return max(0, min(len, len - n + t + 1)); }
-    // tokens of tile x, and its steps
-    __device__ __forceinline__ int count(int x, int tokens) const { return max(0, min(tokens, n - tok0 - x * tokens)); }
-    __device__ __forceinline__ int steps(int x, int tokens) const {
-        const int c = count(x, tokens);
-        return c ? (see(tok0 + x * tokens + c - 1) + kKeys - 1) / kKeys : 0;
-    }
-    // the first step that some row of the item sees in part or not at all
-    __device__ __forceinline__ int masked_from() const { return see(tok0) / kKeys; }
-};
+static_assert(sizeof(Pipe) <= 2048, "the block behind the ring");
 
-struct Misc {
-    uint64_t q_full, q_empty;
-    uint64_t kv_full[10], kv_empty[10];
-    uint64_t s_full[2], p_full[2], o_done[2];
-    uint64_t v_clean[kCleaned], drain;
-    uint64_t item_full[kItems], item_empty[kItems];
-    Item item[kItems];
-    uint32_t odd[kItems][kMasked][4];                      // keys of an item's masked steps whose values are not all finite
-    uint32_t any_odd[kItems];
-    uint32_t tmem_base;
-    int32_t abort;
-};
-static_assert(sizeof(Misc) <= 2048, "misc block");
-
-// D[tmem] (+)= A[tmem] B[smem]: A holds two 16-bit values a column.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)) : "memory");
-}
-// kind::f16 with bf16 operands, fp32 sums.
-constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) { return idesc_f16_f32(M, N, false, b_mn) | (1u << 7) | (1u << 10); }
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-        " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
 // A 16-bit pair of bf16 holds an infinity or a NaN.
 __device__ __forceinline__ uint32_t odd2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
-
-template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
@@ -161,9 +106,8 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* q_smem = smem;
     uint8_t* ring = smem + S::kQ;
-    Misc* misc = reinterpret_cast<Misc*>(ring + S::kStages * S::kStage);
+    Pipe* misc = reinterpret_cast<Pipe*>(ring + S::kStages * S::kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    volatile int32_t* abort_flag = &misc->abort;
     if (tid == 0) {
         mbar_init(&misc->q_full, 1);
         mbar_init(&misc->q_empty, 1);
@@ -195,25 +139,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
     const uint32_t tmem = misc->tmem_base;
     pdl_wait();
     pdl_trigger();
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (wait_for(bar, parity & 1, abort_flag, a.wait_ns)) return true;
-        record_error(a.st, DSA_DEVERR_TIMEOUT, warp);
-        *abort_flag = 1;
-        return false;
-    };
-    // Item k of the CTA, read by one role's warp; false when there is none (or a wait gave up).
-    auto take = [&](int k, Item& it) {
-        bool ok = wait(&misc->item_full[k % kItems], k / kItems);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
-        it = misc->item[k % kItems];
-        return it.n >= 0;
-    };
-    auto done_with = [&](int k) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&misc->item_empty[k % kItems]);
-    };
-
+    const Role me = {misc, a.wait_ns, a.st, warp, lane};
 
     if constexpr (S::kTiles == 2) {
         // registers: 168 a thread at launch (65,536 / 384, in eights); 256 x 208 + 128 x 88 = 384 x 168
@@ -230,7 +156,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         uint32_t t = 0;                                    // steps so far
         Item it;
         bool ok = true;
-        for (int k = 0; ok && take(k, it); ++k) {
+        for (int k = 0; ok && me.take(k, it); ++k) {
             const int count = it.count(x, a.tokens), steps = it.steps(x, a.tokens);
             const int tok = it.tok0 + x * a.tokens + tok_of;
             const bool live = tok_of < count;              // tok_of < a.tokens too
@@ -238,7 +164,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             float refc = 0.f, sum = 0.f;                   // reference in log2 units, sum of P
             for (int i = 0; ok && i < steps; ++i, ++t) {
                 const int s = S::kTiles == 2 ? x : t & 1;
-                ok = __all_sync(0xffffffffu, wait(&misc->s_full[s], S::kTiles == 2 ? t : t >> 1));
+                ok = me.wait_all(&misc->s_full[s], S::kTiles == 2 ? t : t >> 1);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t w[4][32];
@@ -266,18 +192,10 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                 } else if (__any_sync(0xffffffffu, top > refc + kGrow)) {
                     // O counts from a new reference
                     const float to = top > refc + kGrow ? top : refc, f = exp2f(refc - to);
-                    ok = __all_sync(0xffffffffu, wait(&misc->o_done[x], t - 1));
+                    ok = me.wait_all(&misc->o_done[x], t - 1);
                     if (!ok) break;
                     tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(tmem + lanes + S::o(x) + c, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st_32x32b_x32(tmem + lanes + S::o(x) + c, o);
-                    }
+                    rescale_o<D>(tmem + lanes + S::o(x), f);
                     sum *= f;
                     refc = to;
                 }
@@ -308,8 +226,8 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             if (ok && steps > 0) {
                 // With two S the last step's products began before the ones of the step before had
                 // ended: each phase is waited for, so that none is taken for the one after it.
-                ok = S::kTiles == 2 || steps == 1 || wait(&misc->o_done[x], t - 2);
-                ok = __all_sync(0xffffffffu, ok && wait(&misc->o_done[x], t - 1));
+                ok = S::kTiles == 2 || steps == 1 || me.wait(&misc->o_done[x], t - 2);
+                ok = __all_sync(0xffffffffu, ok && me.wait(&misc->o_done[x], t - 1));
                 tc_fence_after();
             }
             if (ok && count > 0) {
@@ -343,143 +261,24 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                                 }
                             }
                         }
-                        if (a.out_f32) {
-                            float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + c);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) out[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-                        } else {
-                            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + c);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                out[j] = make_uint4(pack_bf2(y[8 * j], y[8 * j + 1]), pack_bf2(y[8 * j + 2], y[8 * j + 3]),
-                                                    pack_bf2(y[8 * j + 4], y[8 * j + 5]), pack_bf2(y[8 * j + 6], y[8 * j + 7]));
-                        }
+                        write_32(a.out, a.out_f32, at * D + c, y);
                     }
                     __syncwarp();
                 }
                 if (live && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (refc + log2f(sum)) * 0.69314718055994531f;
             }
             tc_fence_before();                             // O is read before the next item's first P says so
-            done_with(k);
+            me.done_with(k);
         }
     } else if (warp == kMmaWarp) {
-        // ======================================================== the MMAs, by one thread
-        const uint32_t q0 = smem_addr(q_smem), r0 = smem_addr(ring);
-        constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, S::kPart, true);
-        uint32_t n = 0, cleaned = 0, t[2] = {0, 0};        // stages, masked steps and the tiles' steps so far
-        uint32_t items = 0;                                // with a Q
-        bool ok = true;
-        Item it;
-        for (int k = 0; take(k, it); ++k) {
-            done_with(k);
-            const int steps[2] = {it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0};
-            const int most = max(steps[0], steps[1]), masked = it.masked_from();
-            if (lane == 0 && most > 0 && ok) {
-                // stage of part p of step i's keys (v = 0) or values (v = 1)
-                auto stage = [&](int i, int v, int p) { return (n + (2 * i + v) * S::kParts + p) % S::kStages; };
-                auto full = [&](int i, int v) {
-#pragma unroll
-                    for (int p = 0; p < S::kParts; ++p)
-                        ok = ok && wait(&misc->kv_full[stage(i, v, p)], (n + (2 * i + v) * S::kParts + p) / S::kStages);
-                    tc_fence_after();
-                };
-                // What a failed wait was for may still be under way: nothing is freed behind it.
-                auto free_stages = [&](int i, int v) {
-#pragma unroll
-                    for (int p = 0; p < S::kParts && ok; ++p) mma_commit(&misc->kv_empty[stage(i, v, p)]);
-                };
-                auto free_q = [&]() {
-                    if (ok) mma_commit(&misc->q_empty);
-                };
-                auto qk = [&](int x, int s, int i) {       // S[s] = Q[x] K_i^T
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        const uint64_t dq = desc_kmajor_sw128(q0 + (x * (D / 64) + c) * kBox);
-                        const uint64_t dk = desc_kmajor_sw128(r0 + stage(i, 0, c * 64 / S::kPart) * S::kStage + c * 64 % S::kPart / 64 * kBox);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + S::s(s), dq + (uint64_t)(kk * 32 >> 4), dk + (uint64_t)(kk * 32 >> 4), kIdQK, c + kk > 0);
-                    }
-                    mma_commit(&misc->s_full[s]);
-                };
-                auto pv = [&](int x, int s, int i) {       // O[x] += P[s] V_i
-#pragma unroll
-                    for (int p = 0; p < S::kParts; ++p) {
-                        const uint64_t dv = desc_mnmajor_sw128(r0 + stage(i, 1, p) * S::kStage, kBox);
-#pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_f16_ts(tmem + S::o(x) + p * S::kPart, tmem + S::s(s) + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), kIdPV,
-                                       i > 0 || kk > 0);
-                    }
-                    mma_commit(&misc->o_done[x]);
-                };
-                auto values = [&](int i) {
-                    full(i, 1);
-                    if (i >= masked) {
-                        ok = ok && wait(&misc->v_clean[cleaned % kCleaned], cleaned / kCleaned);
-                        ++cleaned;
-                    }
-                };
-                ok = ok && wait(&misc->q_full, items++);
-                full(0, 0);
-                if constexpr (S::kTiles == 2) {
-                    for (int x = 0; x < 2 && ok; ++x)
-                        if (steps[x] > 0) qk(x, x, 0);
-                    free_stages(0, 0);
-                    if (most == 1) free_q();
-                    for (int i = 0; i < most && ok; ++i) {
-                        values(i);
-                        bool have = false;                 // the next keys
-                        for (int x = 0; x < 2 && ok; ++x) {
-                            if (i >= steps[x]) continue;
-                            ok = ok && wait(&misc->p_full[x], t[x]++);
-                            tc_fence_after();
-                            if (ok) pv(x, x, i);
-                            if (ok && i + 1 < steps[x]) {
-                                if (!have) full(i + 1, 0);
-                                have = true;
-                                if (ok) qk(x, x, i + 1);
-                            }
-                        }
-                        if (!ok) break;
-                        free_stages(i, 1);
-                        if (i + 1 < most) free_stages(i + 1, 0);
-                        if (i + 2 == most) free_q();
-                    }
-                } else {
-                    if (ok) qk(0, t[0] & 1, 0);
-                    free_stages(0, 0);
-                    if (most == 1) free_q();
-                    for (int i = 0; i < most && ok; ++i) {
-                        const uint32_t u = t[0]++;
-                        if (i + 1 < most) {
-                            full(i + 1, 0);
-                            if (ok) qk(0, (u + 1) & 1, i + 1);
-                            free_stages(i + 1, 0);
-                            if (i + 2 == most) free_q();
-                        }
-                        values(i);
-                        ok = ok && wait(&misc->p_full[u & 1], u >> 1);
-                        tc_fence_after();
-                        if (ok) pv(0, u & 1, i);
-                        free_stages(i, 1);
-                    }
-                }
-                n += 2 * most * S::kParts;
-            }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        }
-        if (lane == 0) {                                   // MMAs in flight end before TMEM is given back
-            mma_commit(&misc->drain);
-            mbar_wait(&misc->drain, 0);
-        }
+        issue_mmas<S>(me, tmem, smem_addr(q_smem), smem_addr(ring), a.tokens);
     } else if (warp == kTmaWarp) {
         // ======================================================== copies, by one thread
         uint32_t n = 0, items = 0;
         bool ok = true;
         Item it;
-        for (int k = 0; take(k, it); ++k) {
-            done_with(k);
+        for (int k = 0; me.take(k, it); ++k) {
+            me.done_with(k);
             const int steps[2] = {it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0};
             const int most = max(steps[0], steps[1]);
             if (lane == 0 && ok) {
@@ -487,7 +286,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                     for (int v = 0; v < 2 && ok; ++v) {
                         for (int p = 0; p < S::kParts && ok; ++p, ++n) {
                             const int s = n % S::kStages;
-                            if (n >= S::kStages) ok = wait(&misc->kv_empty[s], n / S::kStages - 1);
+                            if (n >= S::kStages) ok = me.wait(&misc->kv_empty[s], n / S::kStages - 1);
                             if (!ok) break;
                             mbar_arrive_expect_tx(&misc->kv_full[s], S::kStage);
 #pragma unroll
@@ -496,7 +295,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                                             it.k_row + i * kKeys, &misc->kv_full[s]);
                         }
                         if (i == 0 && v == 0 && ok) {      // Q behind the first keys, which have room earlier
-                            if (items > 0) ok = wait(&misc->q_empty, items - 1);
+                            if (items > 0) ok = me.wait(&misc->q_empty, items - 1);
                             if (!ok) break;
                             int tiles = 0;
                             for (int x = 0; x < S::kTiles; ++x) tiles += steps[x] > 0;
@@ -517,71 +316,28 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             if (items > 0) mbar_wait(&misc->q_full, (items - 1) & 1);
         }
     } else if (warp == kItemWarp) {
-        // ======================================================== items: 32 requests at a time, one a lane
-        const int per = a.tokens * S::kTiles;              // tokens of an item
-        int c0 = -32;
-        int64_t base = 0, all = 0;                         // items before the 32 requests, and theirs
-        int64_t upto = 0;                                  // and of those up to the lane's
-        int qs = 0, qn = 0, blocks = 0;
-        bool ok = true;
-        for (int k = 0; ok; ++k) {
-            // there and back over the CTAs: items of a request come longest first
-            const int64_t i = (int64_t)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            while (i >= base + all && c0 + 32 < a.batch) {
-                base += all;
-                c0 += 32;
-                const int r = c0 + lane;
-                qs = qn = blocks = 0;
-                if (r < a.batch) {
-                    qs = a.q_start[r];
-                    qn = (int)max((int64_t)0, min((int64_t)a.q_start[r + 1], a.total_q) - qs);
-                    blocks = (qn + per - 1) / per;
-                }
-                upto = (int64_t)blocks * a.kv_heads;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
-                }
-                all = __shfl_sync(0xffffffffu, upto, 31);
-            }
-            Item it = {};
-            it.n = -1;
-            const uint32_t past = __ballot_sync(0xffffffffu, i < base + upto);
-            if (past) {
-                const int at = __ffs(past) - 1, r = c0 + at;
-                const int b = __shfl_sync(0xffffffffu, blocks, at);
-                const int64_t j = i - base - __shfl_sync(0xffffffffu, upto - (int64_t)blocks * a.kv_heads, at);
-                it.q_row = __shfl_sync(0xffffffffu, qs, at);
-                it.n = __shfl_sync(0xffffffffu, qn, at);
-                it.tok0 = (b - 1 - (int)(j / a.kv_heads)) * per;
-                it.h = (int)(j % a.kv_heads);
+        lay_out_items(
+            me, a.batch, a.kv_heads, a.tokens * S::kTiles,
+            [&](int r, int& qs, int& qn) {
+                qs = a.q_start[r];
+                qn = (int)max((int64_t)0, min((int64_t)a.q_start[r + 1], a.total_q) - qs);
+            },
+            [&](int r, Item& it) {
                 it.k_row = a.k_start[r];
-                it.len = (int)max((int64_t)0, min((int64_t)a.k_start[r + 1], a.total_k) - it.k_row);
-            }
-            if (k >= kItems) ok = __all_sync(0xffffffffu, wait(&misc->item_empty[k % kItems], k / kItems - 1));
-            if (!ok) break;
-            if (lane == 0) {
-                misc->item[k % kItems] = it;
-                misc->any_odd[k % kItems] = 0;
-                mbar_arrive(&misc->item_full[k % kItems]);
-            }
-            if (it.n < 0) break;
-        }
+                it.len = it.cap = (int)max((int64_t)0, min((int64_t)a.k_start[r + 1], a.total_k) - it.k_row);
+            });
     } else {
         // ======================================================== values of masked steps
         uint32_t n = 0, cleaned = 0;
         bool ok = true;
         Item it;
-        for (int k = 0; ok && take(k, it); ++k) {
+        for (int k = 0; ok && me.take(k, it); ++k) {
             const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0), masked = it.masked_from();
-            if (lane < kMasked * 4) misc->odd[k % kItems][lane >> 2][lane & 3] = 0;
-            __syncwarp();
             for (int i = 0; ok && i < most; ++i)
                 for (int v = 0; ok && v < 2; ++v) {
                     for (int p = 0; ok && p < S::kParts; ++p, ++n) {
                         const int s = n % S::kStages;
-                        ok = __all_sync(0xffffffffu, wait(&misc->kv_full[s], n / S::kStages));
+                        ok = me.wait_all(&misc->kv_full[s], n / S::kStages);
                         if (!ok) break;
                         if (v && i >= masked) {
                             uint8_t* part = ring + s * S::kStage;
@@ -613,24 +369,12 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                         if (lane == 0) mbar_arrive(&misc->kv_empty[s]);
                     }
                 }
-            done_with(k);
+            me.done_with(k);
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 512);
-}
-
-// bf16 rows of heads as [rows, heads, dim], boxes of 64 dims x bh heads x br rows.
-static bool make_map(const dsa_heads* h, int dim, int64_t heads, int64_t rows, unsigned bh, unsigned br, CUtensorMap* out) {
-    const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
-    if (!encode) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
-    // the stride of an axis of one entry says nothing
-    const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? h->head_stride : dim) * 2, (cuuint64_t)(rows > 1 ? h->token_stride : dim * heads) * 2};
-    const cuuint32_t box[3] = {64, bh, br}, estr[3] = {1, 1, 1};
-    return encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(h->data), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
@@ -705,8 +449,8 @@ extern "C" dsa_status dsa_prompt_attention(const dsa_heads* q, const dsa_heads* 
     a.st = dev_status;
     CUtensorMap qm, km, vm;
     const int64_t rows = std::max<int64_t>(1, b->total_k);
-    if (!prompt::make_map(q, head_dim, heads, b->total_q, (unsigned)a.group, (unsigned)a.tokens, &qm) ||
-        !prompt::make_map(kk, head_dim, kv_heads, rows, 1, prompt::kKeys, &km) || !prompt::make_map(vv, head_dim, kv_heads, rows, 1, prompt::kKeys, &vm))
+    if (!gtc::make_heads_map(q, head_dim, heads, b->total_q, (unsigned)a.group, (unsigned)a.tokens, &qm) ||
+        !gtc::make_heads_map(kk, head_dim, kv_heads, rows, 1, gtc::kKeys, &km) || !gtc::make_heads_map(vv, head_dim, kv_heads, rows, 1, gtc::kKeys, &vm))
         return DSA_ERR_CUDA;
     const cudaStream_t s = as_stream(stream);
     if (head_dim == 64) return prompt::launch<64>(a, qm, km, vm, s);

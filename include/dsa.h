@@ -662,7 +662,7 @@ dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, const dsa_head
  *   and rounded to fp16 (exact, but for values more than 2^39 below the row's
  *   largest), E4M3 is exact in fp16; softmax statistics and accumulation are
  *   fp32; probabilities are rounded to fp16 for the product with the values, each
- *   off by 2^-11 of itself, or by less than 2^-32 of the largest.  A NaN in a key
+ *   off by 2^-11 of itself, or by less than 2^-30 of the largest.  A NaN in a key
  *   or in a value that a row sees makes its outputs NaN, and no other row's.
  *   Cache rows that no row sees may hold anything.  A page id outside the cache
  *   is recorded (DSA_DEVERR_PAGE_RANGE) and its positions are not seen; a negative

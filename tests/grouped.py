@@ -2,10 +2,11 @@
 
 With A the largest sum of a row's products |q_d k_d| times the softmax scale, a score is off by at most D steps of its
 fp32 sum, 2 D 2^-24 A for a sum that cuts off, and 2^-22 of the score in the exponent (log2 units and the power of
-two's approximation): at most OFF = (2 D 2^-24 + 2^-21) A.  A probability is off by that, by its rounding P and, where it
-is small, by 2^-32 of the largest; sums over n positions and their merge are off by (n + 64) 2^-23 of the sum of sizes W.
+two's approximation): at most OFF = (2 D 2^-24 + 2^-21) A.  A probability is off by that, by its rounding P and, in fp16
+and where it is small, by 2^-25: with the largest contribution at 2^6.5 or more, and codes of up to twice its block's largest
+one, by less than 2^-30 of the largest value; sums over n positions and their merge are off by (n + 64) 2^-23 of the sum of sizes W.
 Numerator and denominator both count the scores' error:
-  |out - exact| <= W (P + 2 OFF + (n + 64) 2^-23) + n 2^-32 max|v| (+ half a step of the output)
+  |out - exact| <= W (P + 2 OFF + (n + 64) 2^-23) + n 2^-30 max|v| (+ half a step of the output)
   |lse - exact| <= 2 OFF + (n + 64) 2^-23 + 2^-21 (1 + |lse|)
 """
 
@@ -88,7 +89,7 @@ def bounds(q, k, v, first, scale, P, ok=None):
             A[:, h] = scale * (np.abs(q[:, h]) @ fine[:, h // G].T).max(1)
             top[h] = fv[:, h // G].max()
     off = (2 * dim * 2.0 ** -24 + 2.0 ** -21) * A
-    tol = W * (P + 2 * off + (L + 64) * 2.0 ** -23)[..., None] + (L * 2.0 ** -32 if P < 2.0 ** -10 else 0.0) * top
+    tol = W * (P + 2 * off + (L + 64) * 2.0 ** -23)[..., None] + (L * 2.0 ** -30 if P < 2.0 ** -10 else 0.0) * top
     lse_tol = 2 * off + (L + 64) * 2.0 ** -23 + 2.0 ** -21 * (1 + np.abs(np.where(np.isfinite(lse), lse, 0)))
     return out, lse, tol, lse_tol
 

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import dsa_sparse_attention_indexer_gb300 as D
-from tests.grouped import DEV, cache_case, check, expected, place
+from oracle import dsa_oracle as O
+from tests.grouped import DEV, bounds, cache_case, check, expected, f64, place
 
 pytestmark = pytest.mark.gpu
 
@@ -44,6 +45,14 @@ SHAPES = [
     ([128, 127], [128, 3], 2, 1, 64),
     ([257], [140], 2, 8, 128),
     ([40], [3], 1, 128, 64),
+    # many rows a request, alone and beside few
+    ([300], [300], 1, 1, 128),
+    ([300], [129], 2, 1, 64),
+    ([520, 77], [260, 77], 2, 2, 256),
+    ([700, 1000, 64, 200], [200, 1, 64, 0], 2, 8, 128),
+    ([500, 100], [90, 33], 2, 7, 64),
+    ([1100], [700], 1, 5, 128),
+    ([260, 129, 90], [17, 5, 40], 1, 64, 256),
 ]
 
 
@@ -132,7 +141,7 @@ def test_unseen_rows_may_hold_anything():
 
 
 def test_nan_reaches_the_rows_that_see_it():
-    for dim, group, n in ((128, 4, 5), (64, 1, 40), (256, 2, 9)):
+    for dim, group, n in ((128, 4, 5), (64, 1, 40), (256, 2, 9), (128, 8, 70), (64, 2, 90), (256, 8, 80)):
         c = cache_case([100, 90], [n, 1], 2, group, dim, seed=9)
         k, v, _ = D.kv8_views(c["cache"], 2, dim)
         for p, what in ((98, v), (97, k), (20, None)):
@@ -215,6 +224,80 @@ def test_extreme_queries():
     want = expected(c)
     want[0][np.isnan(want[1])] = np.nan
     check(out, lse, want)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_long_chunks_beside_decode_rows(dim):
+    """Chunks whose items are more than the CTAs, a page that is not there, and rows behind the last request."""
+    c = cache_case([900, 1500, 65, 700, 333], [300, 1, 65, 640, 2], 4, 4, dim, seed=dim, pad_rows=2)
+    c["table"][0, 3] = -1
+    c["table"][3, 10] = c["pages"] + 5
+    place(c)
+    out, lse, bits = _run(c)
+    check(out, lse, expected(c))
+    assert bits == D.DEVERR_PAGE_RANGE
+
+
+def test_prefill_scales_far_apart_and_large_scores():
+    for seed, size in ((0, 1.0), (1, 300.0)):
+        c = cache_case([600], [150], 2, 4, 128, seed=seed, q_size=size)
+        s = D.kv8_views(c["cache"], 2, 128)[2]
+        g = torch.Generator().manual_seed(seed)
+        s[:, :, 1] = torch.exp2(torch.randint(-24, 25, s[:, :, 1].shape, generator=g).float())
+        place(c)
+        check(*_run(c, D.DTYPE_F32)[:2], expected(c))
+
+
+def test_prefill_unseen_rows_and_lengths():
+    c = cache_case([150, 130], [100, 130], 2, 2, 128, seed=20)
+    want = expected(c)
+    k, v, s = (x.view(torch.uint8) if x.dtype != torch.float32 else x for x in D.kv8_views(c["cache"], 2, 128))
+    for r, L in enumerate(c["seq"]):
+        for blk in range(L // 16, 12):
+            pg, at = int(c["table"][r, blk // 4]), blk % 4
+            left = max(0, L - blk * 16)
+            k[pg, :, at, left:] = 0x7f
+            v[pg, :, at, :, left:] = 0xff
+            if left == 0:
+                s[pg, :, :, at] = float("nan")
+    place(c)
+    out, lse, bits = _run(c)
+    check(out, lse, want)
+    assert bits == 0
+    # fewer tokens held than new ones: rows that see nothing; more than the table has: positions that no one sees
+    for seq, n in (([60], [100]), ([500], [120])):
+        c = cache_case([128], n, 1, 4, 64, seed=21)
+        c["seq"] = seq
+        place(c)
+        out, lse, bits = _run(c)
+        L = min(seq[0], 128)
+        k, v, ok = O.kv8_read(c["cache"].numpy().reshape(-1), 1, 64, c["table"][0].numpy(), L, c["pages"])
+        check(out, lse, bounds(f64(c["q"]), k, v, seq[0] - n[0], 64 ** -0.5, 2.0 ** -11, ok))
+        assert bits == D.DEVERR_INDEX_RANGE
+
+
+def test_queries_that_a_tensor_map_does_not_take():
+    """One row of q for all tokens: a stride of 0."""
+    c = cache_case([300], [100], 2, 4, 64, seed=22)
+    one = c["q"][:1]
+    c["q"] = one.expand(100, 8, 64).contiguous()
+    want = expected(c)
+    out, lse, bits = _run(c, q=one.expand(100, 8, 64))
+    check(out, lse, want)
+
+
+def test_prefill_timeout_is_recorded_and_the_next_call_is_right():
+    c = cache_case([3000], [500], 2, 4, 128, seed=23)
+    try:
+        D.dsa_debug_set_wait_limit_ns(0)
+        for _ in range(3):
+            _, _, bits = _run(c)
+            assert bits & D.DEVERR_TIMEOUT
+    finally:
+        D.dsa_debug_set_wait_limit_ns(2_000_000_000)
+    out, lse, bits = _run(c)
+    check(out, lse, expected(c))
+    assert bits == 0
 
 
 def test_timeout_is_recorded_and_the_next_call_is_right():
