@@ -1,6 +1,8 @@
 // Device helpers that the tensor-core attention kernels on grouped heads share:
 // their items of work, MMAs with an operand in TMEM, packed fp32 arithmetic.
 #pragma once
+#include <algorithm>
+
 #include "dsa_internal.cuh"
 #include "kv8.cuh"
 #include "mla_common.cuh"
@@ -32,12 +34,28 @@ struct Item {
     __device__ __forceinline__ int masked_from() const { return see(tok0) / kKeys; }
 };
 
-// D[tmem] (+)= A[tmem] B[smem]: A holds two 16-bit values a column.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// MMAs and commits of one lane, `lead`, of a warp that runs them together: in control flow
+// that the whole warp takes, the operands are kept and added to in uniform registers, and an
+// MMA is issued every 64 cycles (128 x 128 x 16, as fast as it runs).  Behind a branch that
+// one lane takes each operand is moved there for each MMA: 100 cycles, and the thread that
+// issues bounds the kernel (1 x 8192 tokens of 64 heads: 938 us).
+// D[tmem] (+)= A[smem] B[smem].
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]: A holds two 16-bit values a column.
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+                 ::"r"(smem_addr(bar)), "r"(lead) : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -67,18 +85,37 @@ __device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-// 32 dims of an output row.
-__device__ __forceinline__ void write_32(void* out, int f32, int64_t at, const float (&y)[32]) {
-    if (f32) {
-        float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) to[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+// 32 bytes, a sector of memory: in one store where the address allows it.
+__device__ __forceinline__ void store_32_bytes(void* to, bool wide, const uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
     } else {
-        uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+        static_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+// 32 dims of an output row, of outputs that begin at a multiple of 16 bytes.  A thread holds a
+// row, so that a warp's stores go to 32 places: half as many as with 16 bytes each.
+__device__ __forceinline__ void write_32(void* out, int f32, int64_t at, const float (&y)[32]) {
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+    uint32_t w[8];
+    if (f32) {
+        float* to = static_cast<float*>(out) + at;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            to[j] = make_uint4(pack_bf2(y[8 * j], y[8 * j + 1]), pack_bf2(y[8 * j + 2], y[8 * j + 3]),
-                               pack_bf2(y[8 * j + 4], y[8 * j + 5]), pack_bf2(y[8 * j + 6], y[8 * j + 7]));
+        for (int j = 0; j < 32; j += 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[j + e]);
+            store_32_bytes(to + j, wide, w);
+        }
+    } else {
+        uint16_t* to = static_cast<uint16_t*>(out) + at;
+#pragma unroll
+        for (int j = 0; j < 32; j += 16) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = pack_bf2(y[j + 2 * e], y[j + 2 * e + 1]);
+            store_32_bytes(to + j, wide, w);
+        }
     }
 }
 // O's TMEM columns [o, o + D) of the warp's rows times f.
@@ -95,6 +132,9 @@ __device__ __forceinline__ void rescale_o(uint32_t o_tmem, float f) {
     }
 }
 
+// Items of a call, at most; the kernels count them in 32 bits.
+inline int64_t most_items(int64_t total_q, int batch, int kv_heads, int per) { return std::min(total_q, total_q / per + batch) * kv_heads; }
+
 // bf16 rows of heads as [rows, heads, dim], boxes of 64 dims x bh heads x br rows.
 bool make_heads_map(const dsa_heads* h, int dim, int64_t heads, int64_t rows, unsigned bh, unsigned br, CUtensorMap* out);
 
@@ -106,14 +146,14 @@ template <int R> __device__ __forceinline__ void fewer_registers() { asm volatil
 // step's keys or values; the stages of an item are its steps' keys and values in turn.
 constexpr int kMaxStages = 10;
 constexpr int kItems = 2;                                  // laid out ahead
-constexpr int kCleaned = 8;                                // masked steps that may be looked through before their MMA: more than the ring holds
 constexpr int kMasked = 4;                                 // steps of an item that some rows see in part, at most
 
 struct Pipe {
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];                        // by tile
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
-    uint64_t s_full[2], p_full[2], o_done[2];
-    uint64_t v_clean[kCleaned], drain;
+    uint64_t s_full[2], o_done[2];                         // by S, by tile
+    uint64_t p_full[2][2];                                 // by S: the first 64 keys' P, the others'
+    uint64_t drain[2];
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
     uint32_t odd[kItems][kMasked][4];                      // keys of an item's masked steps whose values are not all finite
@@ -149,121 +189,135 @@ struct Role {
     }
 };
 
-// S: kDim, kTiles, kPart, kParts, kStage, kStages, s(i) and o(i) (TMEM columns), kIdQK and
-// kIdPV, kValuesMn (values lie with their dims side by side: an MN-major operand; else their
-// tokens), kCleans (masked steps' values are looked through first).
+// A place in the ring: stage and the parity of its phase.
 template <class S>
-__device__ __forceinline__ void issue_mmas(const Role& me, uint32_t tmem, uint32_t q0, uint32_t r0, int tokens) {
+struct Place {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void next(int by = 1) {
+        stage += by;
+        if (stage >= S::kStages) stage -= S::kStages, phase ^= 1;
+    }
+    __device__ __forceinline__ Place then(int by) const {
+        Place p = *this;
+        p.next(by);
+        return p;
+    }
+};
+
+// The warp that issues tile x's MMAs.  S: kDim, kTiles, kPart, kParts, kStage, kStages, s(i) and
+// o(i) (TMEM columns), kIdQK and kIdPV, kValuesMn (values lie with their dims side by side: an
+// MN-major operand; else their tokens).  A warp a tile, as its own waits and the time that
+// operands take to uniform registers (an MMA of 128 x 128 x 16 runs 64 cycles and is issued in
+// 80 to 100) would bound the kernel if one warp issued for both.
+// TMEM is the kernel's alone: all 512 columns, from column 0.
+template <class S>
+__device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, uint32_t r0, int tokens) {
+    static_assert(S::kStages <= kMaxStages && 2 * S::kParts < S::kStages, "a step's values and the next one's keys are held at once");
     Pipe* m = me.m;
-    uint32_t n = 0, cleaned = 0, t[2] = {0, 0};            // stages, masked steps and the tiles' steps so far
-    uint32_t items = 0;                                    // with a Q
+    const uint32_t lead = me.lane == 0;
+    uint32_t t = 0, items = 0;                             // the tile's steps, and items with a Q, so far
+    Place<S> kp;                                           // where the step's keys are; its values follow
     bool ok = true;
     Item it;
-    for (int k = 0; me.take(k, it); ++k) {
+    for (int k = 0; ok && me.take(k, it); ++k) {
         me.done_with(k);
-        const int steps[2] = {it.steps(0, tokens), S::kTiles == 2 ? it.steps(1, tokens) : 0};
-        const int most = max(steps[0], steps[1]), masked = it.masked_from();
-        if (me.lane == 0 && most > 0 && ok) {
-            // stage of part p of step i's keys (v = 0) or values (v = 1)
-            auto stage = [&](int i, int v, int p) { return (n + (2 * i + v) * S::kParts + p) % S::kStages; };
-            auto full = [&](int i, int v) {
+        auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };      // so that the compiler knows it for the warp's
+        const int steps = same(it.steps(x, tokens));
+        const int most = S::kTiles == 2 ? same(max(it.steps(0, tokens), it.steps(1, tokens))) : steps;
+        auto full = [&](Place<S> p) {
 #pragma unroll
-                for (int p = 0; p < S::kParts; ++p)
-                    ok = ok && me.wait(&m->kv_full[stage(i, v, p)], (n + (2 * i + v) * S::kParts + p) / S::kStages);
-                tc_fence_after();
-            };
-            auto free_stages = [&](int i, int v) {
+            for (int i = 0; i < S::kParts; ++i, p.next()) ok = ok && me.wait_all(&m->kv_full[p.stage], p.phase);
+            tc_fence_after();
+        };
+        auto free_stages = [&](Place<S> p) {
 #pragma unroll
-                for (int p = 0; p < S::kParts && ok; ++p) mma_commit(&m->kv_empty[stage(i, v, p)]);
-            };
-            auto free_q = [&]() {
-                if (ok) mma_commit(&m->q_empty);
-            };
-            auto qk = [&](int x, int s, int i) {           // S[s] = Q[x] K_i^T
+            for (int i = 0; i < S::kParts; ++i, p.next())
+                if (ok) commit(lead, &m->kv_empty[p.stage]);
+        };
+        auto qk = [&](int s, Place<S> p) {                 // S[s] = Q[x] K^T
+            uint32_t part[S::kParts];
 #pragma unroll
-                for (int c = 0; c < S::kDim / 64; ++c) {
-                    const uint64_t dq = desc_kmajor_sw128(q0 + (x * (S::kDim / 64) + c) * kBox);
-                    const uint64_t dk = desc_kmajor_sw128(r0 + stage(i, 0, c * 64 / S::kPart) * S::kStage + c * 64 % S::kPart / 64 * kBox);
+            for (int i = 0; i < S::kParts; ++i, p.next()) part[i] = r0 + p.stage * S::kStage;
+            const uint32_t d = S::s(0) + 128 * s;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + S::s(s), dq + (uint64_t)(kk * 32 >> 4), dk + (uint64_t)(kk * 32 >> 4), S::kIdQK, c + kk > 0);
-                }
-                mma_commit(&m->s_full[s]);
-            };
-            auto pv = [&](int x, int s, int i) {           // O[x] += P[s] V_i
+            for (int c = 0; c < S::kDim / 64; ++c) {
+                const uint64_t dq = desc_kmajor_sw128(q0 + (x * (S::kDim / 64) + c) * kBox);
+                const uint64_t dk = desc_kmajor_sw128(part[c * 64 / S::kPart] + c * 64 % S::kPart / 64 * kBox);
 #pragma unroll
-                for (int p = 0; p < S::kParts; ++p) {
-                    const uint32_t v0 = r0 + stage(i, 1, p) * S::kStage;
-                    const uint64_t dv = S::kValuesMn ? desc_mnmajor_sw128(v0, kBox) : desc_kmajor_sw128(v0);
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk) {
-                        // 16 keys on: 16 rows of 128 bytes, or 32 bytes in the rows of 64 keys
-                        const uint64_t at = S::kValuesMn ? kk * 2048 : kk / 4 * (S::kPart * 128) + kk % 4 * 32;
-                        mma_f16_ts(tmem + S::o(x) + p * S::kPart, tmem + S::s(s) + kk * 8, dv + (at >> 4), S::kIdPV, i > 0 || kk > 0);
-                    }
-                }
-                mma_commit(&m->o_done[x]);
-            };
-            auto values = [&](int i) {
-                full(i, 1);
-                if (S::kCleans && i >= masked) {
-                    ok = ok && me.wait(&m->v_clean[cleaned % kCleaned], cleaned / kCleaned);
-                    ++cleaned;
-                }
-            };
-            ok = ok && me.wait(&m->q_full, items++);
-            full(0, 0);
-            if constexpr (S::kTiles == 2) {
-                for (int x = 0; x < 2 && ok; ++x)
-                    if (steps[x] > 0) qk(x, x, 0);
-                free_stages(0, 0);
-                if (most == 1) free_q();
-                for (int i = 0; i < most && ok; ++i) {
-                    values(i);
-                    bool have = false;                     // the next keys
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        if (i >= steps[x]) continue;
-                        ok = ok && me.wait(&m->p_full[x], t[x]++);
-                        tc_fence_after();
-                        if (ok) pv(x, x, i);
-                        if (ok && i + 1 < steps[x]) {
-                            if (!have) full(i + 1, 0);
-                            have = true;
-                            if (ok) qk(x, x, i + 1);
-                        }
-                    }
-                    if (!ok) break;
-                    free_stages(i, 1);
-                    if (i + 1 < most) free_stages(i + 1, 0);
-                    if (i + 2 == most) free_q();
-                }
-            } else {
-                if (ok) qk(0, t[0] & 1, 0);
-                free_stages(0, 0);
-                if (most == 1) free_q();
-                for (int i = 0; i < most && ok; ++i) {
-                    const uint32_t u = t[0]++;
-                    if (i + 1 < most) {
-                        full(i + 1, 0);
-                        if (ok) qk(0, (u + 1) & 1, i + 1);
-                        free_stages(i + 1, 0);
-                        if (i + 2 == most) free_q();
-                    }
-                    values(i);
-                    ok = ok && me.wait(&m->p_full[u & 1], u >> 1);
-                    tc_fence_after();
-                    if (ok) pv(0, u & 1, i);
-                    free_stages(i, 1);
-                }
+                for (int kk = 0; kk < 4; ++kk) mma_ss(lead, d, dq + (uint64_t)(kk * 32 >> 4), dk + (uint64_t)(kk * 32 >> 4), S::kIdQK, c + kk > 0);
             }
-            n += 2 * most * S::kParts;
+            commit(lead, &m->s_full[s]);
+        };
+        // 64 keys of O[x] (+)= P[s] V: half h
+        auto pv = [&](int s, Place<S> p, int h, bool first) {
+            const uint32_t a = S::s(0) + 128 * s + 32 * h;
+#pragma unroll
+            for (int i = 0; i < S::kParts; ++i, p.next()) {
+                // 16 keys on: 16 rows of 128 bytes, or 32 bytes in the rows of 64 keys
+                const uint32_t v0 = r0 + p.stage * S::kStage + h * (S::kValuesMn ? 4 * 2048 : S::kPart * 128);
+                const uint64_t dv = S::kValuesMn ? desc_mnmajor_sw128(v0, kBox) : desc_kmajor_sw128(v0);
+                const uint32_t d = S::o(0) + 128 * x + i * S::kPart;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(lead, d, a + kk * 8, dv + (uint64_t)((S::kValuesMn ? kk * 2048 : kk * 32) >> 4), S::kIdPV, kk > 0 || !first);
+            }
+        };
+        if (steps > 0) ok = ok && me.wait_all(&m->q_full[x], items++);
+        // The second tile begins when the first one's first P is there: out of step, one's softmax runs
+        // beside the other's MMAs; in step both leave the tensor core idle together.
+        if (S::kTiles == 2 && x == 1 && k == 0 && same(it.steps(0, tokens)) > 0) ok = ok && me.wait_all(&m->p_full[0][0], 0);
+        if (ok && most > 0) {
+            full(kp);
+            if (ok && steps > 0) qk(S::kTiles == 2 ? x : t & 1, kp);
+            free_stages(kp);
+            if (ok && steps == 1) commit(lead, &m->q_empty[x]);
         }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        for (int i = 0; i < most && ok; ++i) {
+            const Place<S> vp = kp.then(S::kParts), np = kp.then(2 * S::kParts);
+            const bool more = i + 1 < most;
+            if constexpr (S::kTiles == 2) {
+                full(vp);
+                if (more) full(np);
+                if (i < steps) {
+                    ok = ok && me.wait_all(&m->p_full[x][0], t);
+                    tc_fence_after();
+                    if (ok) pv(x, vp, 0, i == 0);
+                    ok = ok && me.wait_all(&m->p_full[x][1], t);
+                    tc_fence_after();
+                    if (ok) {
+                        pv(x, vp, 1, false);
+                        commit(lead, &m->o_done[x]);
+                        if (i + 1 < steps) qk(x, np);
+                    }
+                    ++t;
+                }
+                // a tile with fewer steps than the other lets the stages go by
+                free_stages(vp);
+                if (more) free_stages(np);
+            } else {
+                // with two S, the next step's is formed while this one's P is
+                if (more) {
+                    full(np);
+                    if (ok) qk((t + 1) & 1, np);
+                    free_stages(np);
+                }
+                full(vp);
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && me.wait_all(&m->p_full[t & 1][h], t >> 1);
+                    tc_fence_after();
+                    if (ok) pv(t & 1, vp, h, i == 0 && h == 0);
+                }
+                if (ok) commit(lead, &m->o_done[x]);
+                free_stages(vp);
+                ++t;
+            }
+            if (ok && i + 2 == steps) commit(lead, &m->q_empty[x]);
+            kp = np;
+        }
     }
-    if (me.lane == 0) {                                    // MMAs in flight end before TMEM is given back
-        mma_commit(&m->drain);
-        mbar_wait(&m->drain, 0);
-    }
+    __syncwarp();
+    commit(lead, &m->drain[x]);                            // MMAs in flight end before TMEM is given back
+    mbar_wait(&m->drain[x], 0);
 }
 
 // Lays out the CTA's items, `per` tokens each, 32 requests at a time, one a lane: `rows(r, qs,
@@ -273,21 +327,21 @@ template <class Rows, class Keys>
 __device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_heads, int per, Rows rows, Keys keys) {
     Pipe* m = me.m;
     int c0 = -32;
-    int64_t base = 0, all = 0;                             // items before the 32 requests, and theirs
-    int64_t upto = 0;                                      // and of those up to the lane's
+    uint32_t base = 0, all = 0;                            // items before the 32 requests, and theirs (the host bounds them)
+    uint32_t upto = 0;                                     // and of those up to the lane's
     int qs = 0, qn = 0, blocks = 0;
     for (int k = 0;; ++k) {
-        const int64_t i = (int64_t)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const uint32_t i = (uint32_t)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         while (i >= base + all && c0 + 32 < batch) {
             base += all;
             c0 += 32;
             qs = qn = 0;
             if (c0 + me.lane < batch) rows(c0 + me.lane, qs, qn);
             blocks = (qn + per - 1) / per;
-            upto = (int64_t)blocks * kv_heads;
+            upto = (uint32_t)(blocks * kv_heads);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
                 if (me.lane >= o) upto += y;
             }
             all = __shfl_sync(0xffffffffu, upto, 31);
@@ -298,11 +352,11 @@ __device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_
         if (past) {
             const int at = __ffs(past) - 1;
             const int b = __shfl_sync(0xffffffffu, blocks, at);
-            const int64_t j = i - base - __shfl_sync(0xffffffffu, upto - (int64_t)blocks * kv_heads, at);
+            const uint32_t j = i - base - __shfl_sync(0xffffffffu, upto - (uint32_t)(blocks * kv_heads), at);
             it.q_row = __shfl_sync(0xffffffffu, qs, at);
             it.n = __shfl_sync(0xffffffffu, qn, at);
-            it.tok0 = (b - 1 - (int)(j / kv_heads)) * per;
-            it.h = (int)(j % kv_heads);
+            it.tok0 = (b - 1 - (int)(j / (uint32_t)kv_heads)) * per;
+            it.h = (int)(j % (uint32_t)kv_heads);
             keys(c0 + at, it);
         }
         if (k >= kItems && !me.wait_all(&m->item_empty[k % kItems], k / kItems - 1)) break;

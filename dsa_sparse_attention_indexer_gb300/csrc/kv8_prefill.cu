@@ -56,6 +56,8 @@ template <int D> struct TcShape {
     static constexpr int kConv = D <= 128 ? 4 : 8;         // converter warps
     static constexpr int kConv0 = kSoft + 4;               // the first of them
     static constexpr int kThreads = 512;
+    static constexpr int kSoftRegs = kTiles == 2 ? 200 : 232, kMmaRegs = 40, kConvRegs = kTiles == 2 ? 72 : 104;
+    static_assert(kSoft * 32 * kSoftRegs + 128 * kMmaRegs + kConv * 32 * kConvRegs <= kThreads * 128, "more registers than the launch holds");
     static constexpr int kPart = D < 128 ? D : 128;
     static constexpr int kParts = D / kPart;
     static constexpr int kStage = kBox * kPart / 64;
@@ -63,16 +65,16 @@ template <int D> struct TcShape {
     static constexpr int kStages = (232448 - 1024 - 2048 - kQ) / kStage < 10 ? (232448 - 1024 - 2048 - kQ) / kStage : 10;
     static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
     static constexpr uint32_t kIdQK = idesc_f16_f32(128, kKeys, false, false), kIdPV = idesc_f16_f32(128, kPart, false, false);
-    static constexpr bool kValuesMn = false, kCleans = false;
+    static constexpr bool kValuesMn = false;
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
 };
 
 struct Block {
     Pipe pipe;
-    uint64_t q_raw;             // Q has come as bf16
-    float k2[kMeta][8];         // scales of a step's blocks' keys
-    float ev[kMeta][8];         // exponents of their values'
+    uint64_t q_raw[2];          // by tile: Q has come as bf16
+    alignas(16) float k2[kMeta][8];   // scales of a step's blocks' keys
+    alignas(16) float ev[kMeta][8];   // exponents of their values'
     uint32_t here[kMeta];       // bit h: the step's page h is in the cache
 };
 static_assert(sizeof(Block) <= 2048, "the block behind the ring");
@@ -88,31 +90,32 @@ template <int D>
 __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
 kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap qmap) {
     using S = TcShape<D>;
-    constexpr int kMmaWarp = S::kSoft, kItemWarp = kMmaWarp + 1, kQWarp = kMmaWarp + 2;
+    constexpr int kMmaWarp = S::kSoft, kItemWarp = kMmaWarp + 2, kQWarp = kMmaWarp + 3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* q_smem = smem;
     uint8_t* ring = smem + S::kQ;
     Block* blk = reinterpret_cast<Block*>(ring + S::kStages * S::kStage);
     Pipe* pipe = &blk->pipe;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (a warp's number that the compiler knows for the warp's: its operands stay in uniform registers)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
-        mbar_init(&blk->q_raw, 1);
-        mbar_init(&pipe->q_full, S::kSoft);
-        mbar_init(&pipe->q_empty, 1);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&pipe->kv_full[i], S::kConv);
-            mbar_init(&pipe->kv_empty[i], 1);
+            mbar_init(&pipe->kv_empty[i], S::kTiles);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&blk->q_raw[i], 1);
+            mbar_init(&pipe->q_full[i], 4);
+            mbar_init(&pipe->q_empty[i], 1);
             mbar_init(&pipe->s_full[i], 1);
-            mbar_init(&pipe->p_full[i], 4);
             mbar_init(&pipe->o_done[i], 1);
+            mbar_init(&pipe->drain[i], 1);
+            for (int h = 0; h < 2; ++h) mbar_init(&pipe->p_full[i][h], 4);
         }
-        mbar_init(&pipe->drain, 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&pipe->item_full[i], 1);
-            mbar_init(&pipe->item_empty[i], S::kSoft + 2 + S::kConv);   // softmax, MMAs, Q's copies, converters
+            mbar_init(&pipe->item_empty[i], S::kSoft + S::kTiles + 1 + S::kConv);   // softmax, MMAs, Q's copies, converters
         }
         pipe->abort = 0;
         fence_barrier_init();
@@ -124,17 +127,16 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = pipe->tmem_base;
+    const uint32_t tmem = 0;                               // all 512 columns are the CTA's
     pdl_wait();
     pdl_trigger();
     const BatchDev& b = a.b;
     const Role me = {pipe, b.wait_ns, a.st, warp, lane};
 
-    // registers: 128 a thread at launch; 256 x 200 + 256 x 56, at 256 dims 128 x 200 + 384 x 104 = 512 x 128
-    if (warp < S::kSoft) more_registers<200>();
-    else fewer_registers<S::kTiles == 2 ? 56 : 104>();
-
+    // Registers by warpgroup, of 128 a thread at launch: a converter holds a stage's pieces of codes.
+    // (Set within the roles' branches: behind a join, all roles get the fewest.)
     if (warp < S::kSoft) {
+        more_registers<S::kSoftRegs>();
         // ======================================================== softmax: a thread a row
         const int x = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -150,10 +152,10 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             const bool live = tok_of < count;
             const int see = live ? it.see(tok) : INT32_MAX;
             float c = 0.f;                                 // log2 units of a score
-            if (most > 0) {
-                ok = me.wait_all(&blk->q_raw, q_items++);
+            if (steps > 0) {
+                ok = me.wait_all(&blk->q_raw[x], q_items++);
                 if (!ok) break;
-                if (steps > 0) {
+                {
                     // the row's chunks of 8 dims, swizzled
                     uint8_t* mine = q_smem + x * (D / 64) * kBox + row * 128;
                     uint32_t top = 0;
@@ -182,7 +184,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pipe->q_full);
+                if (lane == 0) mbar_arrive(&pipe->q_full[x]);
             }
             float ref = 0.f, sum = 0.f;                    // R, l
             for (int i = 0; ok && i < steps; ++i, ++t) {
@@ -251,11 +253,11 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                         sum = fmaf(sums.x + sums.y, minus_pow2(ev[g]), sum);
                     }
                     tmem_st_32x32b_x32(tmem + lanes + S::s(s) + 32 * h, p);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pipe->p_full[s][h]);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&pipe->p_full[s]);
             }
             u0 += most;
             // ---- the rows' outputs
@@ -305,51 +307,54 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             tc_fence_before();                             // O is read before the next item's first P says so
             me.done_with(k);
         }
-    } else if (warp == kMmaWarp) {
-        issue_mmas<S>(me, tmem, smem_addr(q_smem), smem_addr(ring), a.tokens);
-    } else if (warp == kItemWarp) {
-        lay_out_items(
-            me, b.batch, a.kv_heads, a.tokens * S::kTiles,
-            [&](int r, int& qs, int& qn) {
-                qs = b.q_start[r];
-                qn = (int)max((int64_t)0, min((int64_t)b.q_start[r + 1], b.total_q) - qs);
-                if ((int64_t)qn * a.group < a.min_rows) qn = 0;
-            },
-            [&](int r, Item& it) {
-                const int len = b.seq_len[r];
-                const int64_t room = (int64_t)b.max_pages * kPage;
-                it.k_row = r;
-                it.len = len - (b.q_start[r + 1] - it.q_row) + it.n;
-                it.cap = (int)min((int64_t)INT32_MAX, room);
-                if (lane == 0 && it.h == 0 && it.tok0 == 0) {
-                    if (it.len < it.n) record_error(a.st, DSA_DEVERR_INDEX_RANGE, it.len - it.n);
-                    else if (len > room) record_error(a.st, DSA_DEVERR_INDEX_RANGE, len);
+    } else if (warp < S::kConv0) {
+        fewer_registers<S::kMmaRegs>();
+        if (warp < kItemWarp) {
+            if (warp - kMmaWarp < S::kTiles) issue_mmas<S>(me, warp - kMmaWarp, smem_addr(q_smem), smem_addr(ring), a.tokens);
+        } else if (warp == kItemWarp) {
+            lay_out_items(
+                me, b.batch, a.kv_heads, a.tokens * S::kTiles,
+                [&](int r, int& qs, int& qn) {
+                    qs = b.q_start[r];
+                    qn = (int)max((int64_t)0, min((int64_t)b.q_start[r + 1], b.total_q) - qs);
+                    if ((int64_t)qn * a.group < a.min_rows) qn = 0;
+                },
+                [&](int r, Item& it) {
+                    const int len = b.seq_len[r];
+                    const int64_t room = (int64_t)b.max_pages * kPage;
+                    it.k_row = r;
+                    it.len = len - (b.q_start[r + 1] - it.q_row) + it.n;
+                    it.cap = (int)min((int64_t)INT32_MAX, room);
+                    if (lane == 0 && it.h == 0 && it.tok0 == 0) {
+                        if (it.len < it.n) record_error(a.st, DSA_DEVERR_INDEX_RANGE, it.len - it.n);
+                        else if (len > room) record_error(a.st, DSA_DEVERR_INDEX_RANGE, len);
+                    }
+                });
+        } else if (warp == kQWarp) {
+            // ======================================================== Q's copies, by one thread
+            uint32_t items[2] = {0, 0};
+            bool ok = true;
+            Item it;
+            for (int k = 0; me.take(k, it); ++k) {
+                me.done_with(k);
+#pragma unroll
+                for (int x = 0; x < S::kTiles; ++x) {
+                    if (lane != 0 || !ok || it.steps(x, a.tokens) == 0) continue;
+                    if (items[x] > 0) ok = me.wait(&pipe->q_empty[x], items[x] - 1);
+                    if (!ok) continue;
+                    ++items[x];
+                    mbar_arrive_expect_tx(&blk->q_raw[x], (uint32_t)(D * 2 * a.tokens * a.group));
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(q_smem + (x * (D / 64) + c) * kBox, &qmap, 64 * c, it.h * a.group, it.q_row + it.tok0 + x * a.tokens, &blk->q_raw[x]);
                 }
-            });
-    } else if (warp == kQWarp) {
-        // ======================================================== Q's copies, by one thread
-        uint32_t items = 0;
-        bool ok = true;
-        Item it;
-        for (int k = 0; me.take(k, it); ++k) {
-            me.done_with(k);
-            const int steps[2] = {it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0};
-            if (lane == 0 && ok && max(steps[0], steps[1]) > 0) {
-                if (items > 0) ok = me.wait(&pipe->q_empty, items - 1);
-                if (ok) {
-                    int tiles = 0;
-                    for (int x = 0; x < S::kTiles; ++x) tiles += steps[x] > 0;
-                    mbar_arrive_expect_tx(&blk->q_raw, (uint32_t)(tiles * D * 2 * a.tokens * a.group));
-                    for (int x = 0; x < S::kTiles; ++x)
-                        for (int c = 0; c < D / 64 && steps[x] > 0; ++c)
-                            tma_load_3d(q_smem + (x * (D / 64) + c) * kBox, &qmap, 64 * c, it.h * a.group, it.q_row + it.tok0 + x * a.tokens, &blk->q_raw);
-                    ++items;
-                }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            if (lane == 0)                                 // copies in flight end before the CTA does
+                for (int x = 0; x < S::kTiles; ++x)
+                    if (items[x] > 0) mbar_wait(&blk->q_raw[x], (items[x] - 1) & 1);
         }
-        if (lane == 0 && items > 0) mbar_wait(&blk->q_raw, (items - 1) & 1);   // copies in flight end before the CTA does
-    } else if (warp >= S::kConv0) {
+    } else {
+        fewer_registers<S::kConvRegs>();
         // ======================================================== converters
         constexpr int kThr = S::kConv * 32;
         constexpr int kUnits = kKeys * S::kPart / 16 / kThr;                   // 16-byte pieces of a stage, a thread
@@ -478,14 +483,15 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == 0) tmem_dealloc(pipe->tmem_base, 512);
 }
 
 template <int D>
 static dsa_status launch_tc(const PrefillArgs& a, const CUtensorMap& q, cudaStream_t s) {
     using S = TcShape<D>;
     if (ensure_smem_limit(reinterpret_cast<const void*>(&kv8_prefill_kernel<D>), S::kSmem) != DSA_OK) return DSA_ERR_CUDA;
-    const int64_t most = std::min(a.b.total_q, a.b.total_q / (a.tokens * S::kTiles) + a.b.batch) * a.kv_heads;
+    const int64_t most = most_items(a.b.total_q, a.b.batch, a.kv_heads, a.tokens * S::kTiles);
+    if (most > 0x7fff0000LL) return DSA_ERR_UNSUPPORTED;
     const unsigned G = (unsigned)std::min<int64_t>(device_sm_count(), most);
     DSA_CHECK(launch_pdl(kv8_prefill_kernel<D>, dim3(G), dim3(S::kThreads), S::kSmem, s, 1, a, q));
     return DSA_OK;

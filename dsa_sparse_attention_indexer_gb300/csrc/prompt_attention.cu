@@ -85,7 +85,7 @@ template <int D> struct Shape {
     static constexpr int kStages = (232448 - 1024 - 2048 - kQ) / kStage < 10 ? (232448 - 1024 - 2048 - kQ) / kStage : 10;
     static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
     static constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, kPart, true);
-    static constexpr bool kValuesMn = true, kCleans = true;
+    static constexpr bool kValuesMn = true;
     // TMEM columns
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
@@ -96,35 +96,66 @@ static_assert(sizeof(Pipe) <= 2048, "the block behind the ring");
 // A 16-bit pair of bf16 holds an infinity or a NaN.
 __device__ __forceinline__ uint32_t odd2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
 
+// Takes infinite and NaN values of a masked step's keys from `from` on out of its stages and
+// notes their keys; by the 128 threads of a tile, before their P says that the step's values
+// may be read.  The other tile's threads do the same, to the same end.
+template <class S>
+__device__ __noinline__ bool clean_values(const Role& me, uint8_t* ring, Place<S> vp, int from, int masked, int k, int thread) {
+    Pipe* m = me.m;
+    for (int p = 0; p < S::kParts; ++p, vp.next()) {
+        if (!me.wait_all(&m->kv_full[vp.stage], vp.phase)) return false;
+        uint8_t* stage = ring + vp.stage * S::kStage;
+        bool found = false;
+#pragma unroll 4
+        for (int e = thread; e < (kKeys - from) * (S::kPart / 8); e += 128) {  // a key's 8 pieces of 16 bytes of each 64 dims
+            const int key = from + (e >> 3) % (kKeys - from), box = (e >> 3) / (kKeys - from);
+            uint4* at = reinterpret_cast<uint4*>(stage + box * kBox + key * 128 + (e & 7) * 16);
+            const uint4 w = *at;
+            const uint4 o = make_uint4(odd2(w.x), odd2(w.y), odd2(w.z), odd2(w.w));
+            if (o.x | o.y | o.z | o.w) {
+                *at = make_uint4(w.x & ~o.x, w.y & ~o.y, w.z & ~o.z, w.w & ~o.w);
+                if (masked < kMasked) atomicOr(&m->odd[k % kItems][masked][key >> 5], 1u << (key & 31));
+                found = true;
+            }
+        }
+        if (found) {
+            fence_proxy_async_smem();
+            m->any_odd[k % kItems] = 1;
+        }
+    }
+    __syncwarp();
+    return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
               const __grid_constant__ CUtensorMap vmap) {
     using S = Shape<D>;
-    constexpr int kMmaWarp = S::kSoft, kTmaWarp = kMmaWarp + 1, kItemWarp = kMmaWarp + 2;
+    constexpr int kMmaWarp = S::kSoft, kTmaWarp = kMmaWarp + 2, kItemWarp = kMmaWarp + 3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* q_smem = smem;
     uint8_t* ring = smem + S::kQ;
     Pipe* misc = reinterpret_cast<Pipe*>(ring + S::kStages * S::kStage);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (a warp's number that the compiler knows for the warp's: its operands stay in uniform registers)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
-        mbar_init(&misc->q_full, 1);
-        mbar_init(&misc->q_empty, 1);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&misc->kv_full[i], 1);
-            mbar_init(&misc->kv_empty[i], 2);              // the MMAs, and the warp that looks through values
+            mbar_init(&misc->kv_empty[i], S::kTiles);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&misc->q_full[i], 1);
+            mbar_init(&misc->q_empty[i], 1);
             mbar_init(&misc->s_full[i], 1);
-            mbar_init(&misc->p_full[i], 4);
             mbar_init(&misc->o_done[i], 1);
+            mbar_init(&misc->drain[i], 1);
+            for (int h = 0; h < 2; ++h) mbar_init(&misc->p_full[i][h], 4);
         }
-        for (int i = 0; i < kCleaned; ++i) mbar_init(&misc->v_clean[i], 1);
-        mbar_init(&misc->drain, 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&misc->item_full[i], 1);
-            mbar_init(&misc->item_empty[i], S::kSoft + 3);  // the softmax warps and those of the MMAs, the copies and the values
+            mbar_init(&misc->item_empty[i], S::kSoft + S::kTiles + 1);  // the softmax warps and those of the MMAs and the copies
         }
         misc->abort = 0;
         fence_barrier_init();
@@ -136,34 +167,38 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc->tmem_base;
+    const uint32_t tmem = 0;                               // all 512 columns are the CTA's
     pdl_wait();
     pdl_trigger();
     const Role me = {misc, a.wait_ns, a.st, warp, lane};
 
-    if constexpr (S::kTiles == 2) {
-        // registers: 168 a thread at launch (65,536 / 384, in eights); 256 x 208 + 128 x 88 = 384 x 168
-        if (warp < S::kSoft) more_registers<208>();
-        else fewer_registers<88>();
-    }
-
+    // Registers: 168 a thread at launch (65,536 / 384, in eights); 256 x 216 + 128 x 72 = 384 x 168.
+    // (Set within the roles' branches: behind a join, all roles get the fewest.)
     if (warp < S::kSoft) {
+        if constexpr (S::kTiles == 2) more_registers<216>();
         // ======================================================== softmax: a thread a row
         const int x = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const int tok_of = row / a.group, head_of = row % a.group;
         const int heads = a.kv_heads * a.group;
         uint32_t t = 0;                                    // steps so far
+        Place<S> kp;                                       // where the step's keys are
         Item it;
         bool ok = true;
         for (int k = 0; ok && me.take(k, it); ++k) {
+            const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0);
+            const int all_see = it.see(it.tok0 + x * a.tokens);        // keys that all of the tile's rows see
             const int count = it.count(x, a.tokens), steps = it.steps(x, a.tokens);
             const int tok = it.tok0 + x * a.tokens + tok_of;
             const bool live = tok_of < count;              // tok_of < a.tokens too
             const int see = live ? it.see(tok) : INT32_MAX;
             float refc = 0.f, sum = 0.f;                   // reference in log2 units, sum of P
-            for (int i = 0; ok && i < steps; ++i, ++t) {
+            for (int i = 0; ok && i < steps; ++i, ++t, kp.next(2 * S::kParts)) {
                 const int s = S::kTiles == 2 ? x : t & 1;
+                if (all_see < (i + 1) * kKeys) {
+                    ok = clean_values<S>(me, ring, kp.then(S::kParts), max(0, all_see - i * kKeys), i - it.masked_from(), k, (warp & 3) * 32 + lane);
+                    if (!ok) break;
+                }
                 ok = me.wait_all(&misc->s_full[s], S::kTiles == 2 ? t : t >> 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -214,14 +249,15 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                         p[j] = pack_bf2(y.x, y.y);
                     }
                     tmem_st_32x32b_x32(tmem + lanes + S::s(s) + 32 * h, p);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&misc->p_full[s][h]);
                 }
                 sums[0] = add2(sums[0], sums[1]);
                 sum += sums[0].x + sums[0].y;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&misc->p_full[s]);
             }
+            for (int i = steps; i < most; ++i) kp.next(2 * S::kParts);
             // ---- the rows' outputs
             if (ok && steps > 0) {
                 // With two S the last step's products began before the ones of the step before had
@@ -270,118 +306,78 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             tc_fence_before();                             // O is read before the next item's first P says so
             me.done_with(k);
         }
-    } else if (warp == kMmaWarp) {
-        issue_mmas<S>(me, tmem, smem_addr(q_smem), smem_addr(ring), a.tokens);
-    } else if (warp == kTmaWarp) {
-        // ======================================================== copies, by one thread
-        uint32_t n = 0, items = 0;
-        bool ok = true;
-        Item it;
-        for (int k = 0; me.take(k, it); ++k) {
-            me.done_with(k);
-            const int steps[2] = {it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0};
-            const int most = max(steps[0], steps[1]);
-            if (lane == 0 && ok) {
-                for (int i = 0; i < most && ok; ++i)
-                    for (int v = 0; v < 2 && ok; ++v) {
-                        for (int p = 0; p < S::kParts && ok; ++p, ++n) {
-                            const int s = n % S::kStages;
-                            if (n >= S::kStages) ok = me.wait(&misc->kv_empty[s], n / S::kStages - 1);
-                            if (!ok) break;
-                            mbar_arrive_expect_tx(&misc->kv_full[s], S::kStage);
-#pragma unroll
-                            for (int c = 0; c < S::kPart / 64; ++c)
-                                tma_load_3d(ring + s * S::kStage + c * kBox, v ? &vmap : &kmap, p * S::kPart + 64 * c, it.h,
-                                            it.k_row + i * kKeys, &misc->kv_full[s]);
-                        }
-                        if (i == 0 && v == 0 && ok) {      // Q behind the first keys, which have room earlier
-                            if (items > 0) ok = me.wait(&misc->q_empty, items - 1);
-                            if (!ok) break;
-                            int tiles = 0;
-                            for (int x = 0; x < S::kTiles; ++x) tiles += steps[x] > 0;
-                            mbar_arrive_expect_tx(&misc->q_full, (uint32_t)(tiles * D * 2 * a.tokens * a.group));
-                            for (int x = 0; x < S::kTiles; ++x)
-                                for (int c = 0; c < D / 64 && steps[x] > 0; ++c)
-                                    tma_load_3d(q_smem + (x * (D / 64) + c) * kBox, &qmap, 64 * c, it.h * a.group,
-                                                it.q_row + it.tok0 + x * a.tokens, &misc->q_full);
-                            ++items;
-                        }
-                    }
-            }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        }
-        if (lane == 0) {                                   // copies in flight end before the CTA does
-            for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
-                if (!mbar_wait(&misc->kv_full[i % S::kStages], i / S::kStages & 1)) break;
-            if (items > 0) mbar_wait(&misc->q_full, (items - 1) & 1);
-        }
-    } else if (warp == kItemWarp) {
-        lay_out_items(
-            me, a.batch, a.kv_heads, a.tokens * S::kTiles,
-            [&](int r, int& qs, int& qn) {
-                qs = a.q_start[r];
-                qn = (int)max((int64_t)0, min((int64_t)a.q_start[r + 1], a.total_q) - qs);
-            },
-            [&](int r, Item& it) {
-                it.k_row = a.k_start[r];
-                it.len = it.cap = (int)max((int64_t)0, min((int64_t)a.k_start[r + 1], a.total_k) - it.k_row);
-            });
     } else {
-        // ======================================================== values of masked steps
-        uint32_t n = 0, cleaned = 0;
-        bool ok = true;
-        Item it;
-        for (int k = 0; ok && me.take(k, it); ++k) {
-            const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0), masked = it.masked_from();
-            for (int i = 0; ok && i < most; ++i)
-                for (int v = 0; ok && v < 2; ++v) {
-                    for (int p = 0; ok && p < S::kParts; ++p, ++n) {
-                        const int s = n % S::kStages;
-                        ok = me.wait_all(&misc->kv_full[s], n / S::kStages);
-                        if (!ok) break;
-                        if (v && i >= masked) {
-                            uint8_t* part = ring + s * S::kStage;
-                            bool found = false;
-                            for (int e = lane * 16; e < S::kStage; e += 32 * 16 * 4) {
-                                uint4 w[4];
+        if constexpr (S::kTiles == 2) fewer_registers<72>();
+        if (warp < kTmaWarp) {
+            if (warp - kMmaWarp < S::kTiles) issue_mmas<S>(me, warp - kMmaWarp, smem_addr(q_smem), smem_addr(ring), a.tokens);
+        } else if (warp == kTmaWarp) {
+            // ======================================================== copies, by one thread
+            uint32_t n = 0, items[2] = {0, 0};             // stages, and items with a Q of each tile, so far
+            bool ok = true;
+            Item it;
+            for (int k = 0; me.take(k, it); ++k) {
+                me.done_with(k);
+                const int steps[2] = {it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0};
+                const int most = max(steps[0], steps[1]);
+                if (lane == 0 && ok) {
+                    for (int i = 0; i < most && ok; ++i)
+                        for (int v = 0; v < 2 && ok; ++v) {
+                            for (int p = 0; p < S::kParts && ok; ++p, ++n) {
+                                const int s = n % S::kStages;
+                                if (n >= S::kStages) ok = me.wait(&misc->kv_empty[s], n / S::kStages - 1);
+                                if (!ok) break;
+                                mbar_arrive_expect_tx(&misc->kv_full[s], S::kStage);
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) w[u] = *reinterpret_cast<const uint4*>(part + e + u * 512);
+                                for (int c = 0; c < S::kPart / 64; ++c)
+                                    tma_load_3d(ring + s * S::kStage + c * kBox, v ? &vmap : &kmap, p * S::kPart + 64 * c, it.h,
+                                                it.k_row + i * kKeys, &misc->kv_full[s]);
+                            }
+                            if (i == 0 && v == 0)          // Q behind the first keys, which have room earlier
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const uint4 o = make_uint4(odd2(w[u].x), odd2(w[u].y), odd2(w[u].z), odd2(w[u].w));
-                                    if (o.x | o.y | o.z | o.w) {
-                                        *reinterpret_cast<uint4*>(part + e + u * 512) = make_uint4(w[u].x & ~o.x, w[u].y & ~o.y, w[u].z & ~o.z, w[u].w & ~o.w);
-                                        const int key = (e + u * 512) % kBox / 128;        // a key's dims are a row of 128 bytes
-                                        if (i - masked < kMasked) atomicOr(&misc->odd[k % kItems][i - masked][key >> 5], 1u << (key & 31));
-                                        found = true;
-                                    }
+                                for (int x = 0; x < S::kTiles; ++x) {
+                                    if (!ok || steps[x] == 0) continue;
+                                    if (items[x] > 0) ok = me.wait(&misc->q_empty[x], items[x] - 1);
+                                    if (!ok) continue;
+                                    ++items[x];
+                                    mbar_arrive_expect_tx(&misc->q_full[x], (uint32_t)(D * 2 * a.tokens * a.group));
+                                    for (int c = 0; c < D / 64; ++c)
+                                        tma_load_3d(q_smem + (x * (D / 64) + c) * kBox, &qmap, 64 * c, it.h * a.group,
+                                                    it.q_row + it.tok0 + x * a.tokens, &misc->q_full[x]);
                                 }
-                            }
-                            if (found) {
-                                fence_proxy_async_smem();
-                                misc->any_odd[k % kItems] = 1;
-                            }
-                            __syncwarp();
-                            if (lane == 0 && p == S::kParts - 1) mbar_arrive(&misc->v_clean[cleaned % kCleaned]);
-                            if (p == S::kParts - 1) ++cleaned;
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&misc->kv_empty[s]);
-                    }
                 }
-            me.done_with(k);
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            }
+            if (lane == 0) {                                   // copies in flight end before the CTA does
+                for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
+                    if (!mbar_wait(&misc->kv_full[i % S::kStages], i / S::kStages & 1)) break;
+                for (int x = 0; x < S::kTiles; ++x)
+                    if (items[x] > 0) mbar_wait(&misc->q_full[x], (items[x] - 1) & 1);
+            }
+        } else if (warp == kItemWarp) {
+            lay_out_items(
+                me, a.batch, a.kv_heads, a.tokens * S::kTiles,
+                [&](int r, int& qs, int& qn) {
+                    qs = a.q_start[r];
+                    qn = (int)max((int64_t)0, min((int64_t)a.q_start[r + 1], a.total_q) - qs);
+                },
+                [&](int r, Item& it) {
+                    it.k_row = a.k_start[r];
+                    it.len = it.cap = (int)max((int64_t)0, min((int64_t)a.k_start[r + 1], a.total_k) - it.k_row);
+                });
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == 0) tmem_dealloc(misc->tmem_base, 512);
 }
 
 template <int D>
 static dsa_status launch(const Args& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
     using S = Shape<D>;
     if (ensure_smem_limit(reinterpret_cast<const void*>(&prompt_kernel<D>), S::kSmem) != DSA_OK) return DSA_ERR_CUDA;
-    const int64_t most = std::min(a.total_q, a.total_q / (a.tokens * S::kTiles) + a.batch) * a.kv_heads;
+    const int64_t most = most_items(a.total_q, a.batch, a.kv_heads, a.tokens * S::kTiles);
+    if (most > 0x7fff0000LL) return DSA_ERR_UNSUPPORTED;
     const unsigned G = (unsigned)std::min<int64_t>(device_sm_count(), most);
     DSA_CHECK(launch_pdl(prompt_kernel<D>, dim3(G), dim3(S::kThreads), S::kSmem, s, 1, a, q, k, v));
     return DSA_OK;

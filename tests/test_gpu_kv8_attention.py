@@ -276,6 +276,20 @@ def test_prefill_unseen_rows_and_lengths():
         assert bits == D.DEVERR_INDEX_RANGE
 
 
+def test_outputs_that_begin_at_16_bytes():
+    """Outputs, their log-sums and the cache at the least alignment that the calls ask for."""
+    for n in (3, 100):
+        c = cache_case([300], [n], 2, 4, 64, seed=24)
+        want, _, _ = _run(c)
+        room = torch.zeros(n * 8 * 64 + 8, dtype=torch.bfloat16, device=DEV)
+        out = room[8:].view(n, 8, 64)
+        lse = torch.empty(n * 8 + 1, device=DEV)[1:].view(n, 8)
+        cache = torch.empty(c["dev_cache"].numel() + 16, dtype=torch.uint8, device=DEV)[16:]
+        cache.copy_(c["dev_cache"].flatten())
+        D.dsa_kv8_attention(c["q"], cache, c["batch"], kv_heads=2, out=out, lse=lse)
+        assert torch.equal(out, want)
+
+
 def test_queries_that_a_tensor_map_does_not_take():
     """One row of q for all tokens: a stride of 0."""
     c = cache_case([300], [100], 2, 4, 64, seed=22)

@@ -163,6 +163,22 @@ def test_strides_stream_graph_and_workspace():
     check(*_run(c, scale=0.5)[:2], _expected(c, 0.5))
 
 
+def test_inputs_and_outputs_that_begin_at_16_bytes():
+    c = _case([150, 20], 0, 2, 4, 64, seed=7)
+    want, _, _ = _run(c)
+
+    def moved(x):
+        room = torch.zeros(x.numel() + 8, dtype=x.dtype, device=DEV)
+        y = room[8:].view(x.shape)
+        y.copy_(x)
+        return y
+
+    out = moved(want) * 0
+    out = moved(out)
+    D.dsa_prompt_attention(moved(c["q"]), moved(c["k"]), moved(c["v"]), c["batch"], out=out)
+    assert torch.equal(out, want)
+
+
 def test_without_keys():
     c = _case([5, 3], [-5, -3], 1, 2, 64, seed=5)
     out, lse, bits = _run(c)
