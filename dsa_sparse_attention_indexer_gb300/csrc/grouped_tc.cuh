@@ -153,6 +153,7 @@ struct Pipe {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
     uint64_t s_full[2], o_done[2];                         // by S, by tile
     uint64_t p_full[2][2];                                 // by S: the first 64 keys' P, the others'
+    uint64_t turn[2];                                      // by tile: its warp may issue a step's last MMAs
     uint64_t drain[2];
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
@@ -208,14 +209,15 @@ struct Place {
 // o(i) (TMEM columns), kIdQK and kIdPV, kValuesMn (values lie with their dims side by side: an
 // MN-major operand; else their tokens).  A warp a tile, as its own waits and the time that
 // operands take to uniform registers (an MMA of 128 x 128 x 16 runs 64 cycles and is issued in
-// 80 to 100) would bound the kernel if one warp issued for both.
+// 80 to 100) would bound the kernel if one warp issued for both.  The tiles take turns with a
+// step's last MMAs, which keeps them out of step: one's softmax runs beside the other's MMAs.
 // TMEM is the kernel's alone: all 512 columns, from column 0.
 template <class S>
 __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, uint32_t r0, int tokens) {
     static_assert(S::kStages <= kMaxStages && 2 * S::kParts < S::kStages, "a step's values and the next one's keys are held at once");
     Pipe* m = me.m;
     const uint32_t lead = me.lane == 0;
-    uint32_t t = 0, items = 0;                             // the tile's steps, and items with a Q, so far
+    uint32_t t = 0, items = 0, turns = 0;                  // the tile's steps, items with a Q, and turns, so far
     Place<S> kp;                                           // where the step's keys are; its values follow
     bool ok = true;
     Item it;
@@ -263,9 +265,6 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
             }
         };
         if (steps > 0) ok = ok && me.wait_all(&m->q_full[x], items++);
-        // The second tile begins when the first one's first P is there: out of step, one's softmax runs
-        // beside the other's MMAs; in step both leave the tensor core idle together.
-        if (S::kTiles == 2 && x == 1 && k == 0 && same(it.steps(0, tokens)) > 0) ok = ok && me.wait_all(&m->p_full[0][0], 0);
         if (ok && most > 0) {
             full(kp);
             if (ok && steps > 0) qk(S::kTiles == 2 ? x : t & 1, kp);
@@ -284,13 +283,18 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
                     if (ok) pv(x, vp, 0, i == 0);
                     ok = ok && me.wait_all(&m->p_full[x][1], t);
                     tc_fence_after();
+                    ok = ok && me.wait_all(&m->turn[x], turns);
                     if (ok) {
                         pv(x, vp, 1, false);
                         commit(lead, &m->o_done[x]);
                         if (i + 1 < steps) qk(x, np);
                     }
                     ++t;
+                } else {
+                    ok = ok && me.wait_all(&m->turn[x], turns);
                 }
+                ++turns;
+                if (ok && lead) mbar_arrive(&m->turn[1 - x]);
                 // a tile with fewer steps than the other lets the stages go by
                 free_stages(vp);
                 if (more) free_stages(np);

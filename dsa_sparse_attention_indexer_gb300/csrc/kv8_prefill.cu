@@ -111,6 +111,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             mbar_init(&pipe->s_full[i], 1);
             mbar_init(&pipe->o_done[i], 1);
             mbar_init(&pipe->drain[i], 1);
+            mbar_init(&pipe->turn[i], 1);
             for (int h = 0; h < 2; ++h) mbar_init(&pipe->p_full[i][h], 4);
         }
         for (int i = 0; i < kItems; ++i) {
@@ -118,6 +119,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             mbar_init(&pipe->item_empty[i], S::kSoft + S::kTiles + 1 + S::kConv);   // softmax, MMAs, Q's copies, converters
         }
         pipe->abort = 0;
+        mbar_arrive(&pipe->turn[0]);                         // the first tile begins
         fence_barrier_init();
     }
     if (warp == 0) {

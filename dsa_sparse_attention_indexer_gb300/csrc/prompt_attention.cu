@@ -151,6 +151,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             mbar_init(&misc->s_full[i], 1);
             mbar_init(&misc->o_done[i], 1);
             mbar_init(&misc->drain[i], 1);
+            mbar_init(&misc->turn[i], 1);
             for (int h = 0; h < 2; ++h) mbar_init(&misc->p_full[i][h], 4);
         }
         for (int i = 0; i < kItems; ++i) {
@@ -158,6 +159,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             mbar_init(&misc->item_empty[i], S::kSoft + S::kTiles + 1);  // the softmax warps and those of the MMAs and the copies
         }
         misc->abort = 0;
+        mbar_arrive(&misc->turn[0]);                         // the first tile begins
         fence_barrier_init();
     }
     if (warp == 0) {
