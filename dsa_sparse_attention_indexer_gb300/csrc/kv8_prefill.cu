@@ -371,51 +371,65 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             const int top = it.see(last);                  // keys that some row of the item sees
             const bool tells = it.h == 0 && last == it.n - 1 && ct == 0;       // one item of a request records its pages
             const int32_t* table = b.page_table + (int64_t)it.k_row * b.max_pages;
-            // the step's pages' parts of the head, NULL where there is none to see
-            auto page = [&](int i, int h) -> const uint8_t* {
+            // Page h of step i: its id as the table has it, kBeyond behind what the item sees; then its
+            // part of the head, NULL where there is none.  Ids are loaded two steps ahead, scales one
+            // step and codes one stage ahead of their use.
+            constexpr int32_t kBeyond = INT32_MIN;
+            auto id_of = [&](int i, int h) {
                 const int64_t p = 2 * (int64_t)i + h;
-                if (p * kPage >= top) return nullptr;
-                const int64_t id = table[p];
-                if (id < 0 || id >= b.num_pages) {
-                    if (tells) record_error(a.st, DSA_DEVERR_PAGE_RANGE, id);
-                    return nullptr;
-                }
-                return a.cache + (id * a.kv_heads + it.h) * head_bytes(D);
+                return p * kPage < top ? __ldg(table + p) : kBeyond;
             };
-            // Piece e of part p of a step's keys (v = 0): 16 dims of a token, or values: a block's 16 tokens
-            // of a dim.  Neighbouring threads take neighbouring pieces.
-            auto piece = [&](const uint8_t* h0, const uint8_t* h1, int v, int p, int e) {
-                const int g = ct + e * kThr;
-                const uint8_t* from;
-                int off;
-                if (!v) {
-                    constexpr int kPer = S::kPart / 16;
-                    const int token = g / kPer;
-                    from = token < kPage ? h0 : h1;
-                    off = token % kPage * D + p * S::kPart + g % kPer * 16;
-                } else {
-                    const int block = g / S::kPart;
-                    from = block < kBlocks ? h0 : h1;
-                    off = v_at(D) + block % kBlocks * (kBlock * D) + (p * S::kPart + g % S::kPart) * 16;
-                }
-                return from ? ldg_pinned(reinterpret_cast<const uint4*>(from + off)) : make_uint4(0, 0, 0, 0);
+            auto head_of_page = [&](int32_t id) -> const uint8_t* {
+                if (id >= 0 && id < b.num_pages) return a.cache + ((int64_t)id * a.kv_heads + it.h) * head_bytes(D);
+                if (id != kBeyond && tells) record_error(a.st, DSA_DEVERR_PAGE_RANGE, id);
+                return nullptr;
+            };
+            // Piece e of part p of a step's keys (v = 0): 16 dims of a token, or values: a block's 16 tokens of
+            // a dim.  Neighbouring threads take neighbouring pieces, the first half of a thread's are of the
+            // first page.
+            constexpr int kHalf = kUnits / 2;
+            constexpr int kPer = S::kPart / 16, kTokens = kThr / kPer;         // pieces of a token, tokens of a piece of all threads
+            constexpr int kDims = kThr / S::kPart;                             // blocks of a piece of all threads
+            const uint32_t k_from = ct / kPer * D + ct % kPer * 16, v_from = v_at(D) + ct / S::kPart * (kBlock * D) + ct % S::kPart * 16;
+            auto piece = [&](const uint8_t* x0, const uint8_t* x1, int v, int p, int e) {
+                const uint8_t* x = e < kHalf ? x0 : x1;
+                const uint32_t off = v ? v_from + e % kHalf * kDims * (kBlock * D) + p * S::kPart * 16 : k_from + e % kHalf * kTokens * D + p * S::kPart;
+                return x ? ldg_pinned(reinterpret_cast<const uint4*>(x + off)) : make_uint4(0, 0, 0, 0);
+            };
+            // ... and its place: the first 16 of its 32 bytes; the others' is the neighbour's
+            const uint32_t k_to = ct % kPer / 4 * kBox + ct / kPer * 128 + ((2 * (ct % kPer % 4)) ^ (ct / kPer & 7)) * 16;
+            auto place = [&](int v, int e) -> uint32_t {
+                if (!v) return k_to + e * kTokens * 128;
+                const int block = ct / S::kPart + e * kDims, d = ct % S::kPart;
+                return block / 4 * (S::kPart * 128) + d * 128 + ((2 * (block % 4)) ^ (d & 7)) * 16;
+            };
+            static_assert(kTokens % 8 == 0 && kUnits % 2 == 0, "a thread's pieces have one swizzle and are half of each page's");
+            // scales of block ct of a step: keys', values'
+            auto scales_of = [&](const uint8_t* x0, const uint8_t* x1) {
+                const uint8_t* x = ct < kBlocks ? x0 : x1;
+                if (ct >= 8 || !x) return make_float2(1.f, 1.f);
+                const float* sc = reinterpret_cast<const float*>(x + scale_at(D)) + ct % kBlocks;
+                return make_float2(__ldg(sc), __ldg(sc + kBlocks));
             };
             const uint8_t *h0 = nullptr, *h1 = nullptr, *n0 = nullptr, *n1 = nullptr;
             uint4 w[kUnits];
+            float2 sc;
             if (most > 0) {
-                h0 = page(0, 0), h1 = page(0, 1);
+                const int32_t i0 = id_of(0, 0), i1 = id_of(0, 1), j0 = id_of(1, 0), j1 = id_of(1, 1);
+                h0 = head_of_page(i0), h1 = head_of_page(i1);
 #pragma unroll
                 for (int e = 0; e < kUnits; ++e) w[e] = piece(h0, h1, 0, 0, e);
+                sc = scales_of(h0, h1);
+                n0 = head_of_page(j0), n1 = head_of_page(j1);
             }
             for (int i = 0; ok && i < most; ++i, ++u) {
                 if (ct < 8) {
-                    // the step's scales
-                    const uint8_t* head = ct < kBlocks ? h0 : h1;
-                    const float* sc = reinterpret_cast<const float*>(head + scale_at(D)) + ct % kBlocks;
-                    blk->k2[u % kMeta][ct] = head ? pow2(scale_exponent(sc[0])) : 1.f;
-                    blk->ev[u % kMeta][ct] = head ? (float)scale_exponent(sc[kBlocks]) : 0.f;
+                    blk->k2[u % kMeta][ct] = pow2(scale_exponent(sc.x));
+                    blk->ev[u % kMeta][ct] = (float)scale_exponent(sc.y);
                     if (ct == 0) blk->here[u % kMeta] = (h0 ? 1u : 0u) | (h1 || (2 * (int64_t)i + 1) * kPage >= top ? 2u : 0u);
                 }
+                const int32_t r0 = id_of(i + 2, 0), r1 = id_of(i + 2, 1);
+                sc = scales_of(n0, n1);
 #pragma unroll
                 for (int v = 0; v < 2; ++v)
 #pragma unroll
@@ -425,41 +439,32 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                         if (n >= S::kStages) ok = me.wait_all(&pipe->kv_empty[s], n / S::kStages - 1);
                         if (!ok) break;
                         // what comes next: the step's next part, its values, the next step's keys
-                        const bool more = !(v == 1 && p == S::kParts - 1) || i + 1 < most;
-                        if (v == 1 && p == 0 && i + 1 < most) n0 = page(i + 1, 0), n1 = page(i + 1, 1);
-                        const int nv = p + 1 < S::kParts ? v : 1 - v, np = p + 1 < S::kParts ? p + 1 : 0;
                         const bool step = v == 1 && p == S::kParts - 1;
-                        uint8_t* stage = ring + s * S::kStage;
+                        const int nv = p + 1 < S::kParts ? v : 1 - v, np = p + 1 < S::kParts ? p + 1 : 0;
+                        const uint8_t *x0 = step ? n0 : h0, *x1 = step ? n1 : h1;
+                        const uint32_t base = smem_addr(ring + s * S::kStage);
 #pragma unroll
                         for (int e = 0; e < kUnits; ++e) {
-                            const int g = ct + e * kThr;
                             uint4 c = w[e];
-                            uint32_t to;                   // the piece's first 16 bytes; the others are its neighbour's place
-                            if (v == 0) {
-                                constexpr int kPer = S::kPart / 16;
-                                const int token = g / kPer, j = g % kPer;
-                                to = j / 4 * kBox + token * 128 + ((2 * (j % 4)) ^ (token & 7)) * 16;
-                            } else {
-                                const int block = g / S::kPart, d = g % S::kPart;
-                                to = block / 4 * (S::kPart * 128) + d * 128 + ((2 * (block % 4)) ^ (d & 7)) * 16;
-                                if (i >= masked) {
-                                    // tokens that no row sees become zeros; a NaN joins the rows that see it in the end
-                                    const int seen = top - i * kKeys - block * kBlock;
-                                    uint32_t* q = reinterpret_cast<uint32_t*>(&c);
+                            w[e] = piece(x0, x1, nv, np, e);
+                            if (v == 1 && i >= masked) {
+                                // tokens that no row sees become zeros; a NaN joins the rows that see it in the end
+                                const int block = ct / S::kPart + e * kDims;
+                                const int seen = top - i * kKeys - block * kBlock;
+                                uint32_t* q = reinterpret_cast<uint32_t*>(&c);
 #pragma unroll
-                                    for (int y = 0; y < 4; ++y) {
-                                        const int left = seen - 4 * y;
-                                        q[y] &= left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-                                        const uint32_t nan = nan_of(q[y]);
-                                        if (nan) {
-                                            q[y] &= ~nan;
-                                            for (int z = 0; z < 4; ++z)
-                                                if (nan >> (8 * z) & 1) {
-                                                    const int key = block * kBlock + 4 * y + z;
-                                                    atomicOr(&pipe->odd[k % kItems][i - masked][key >> 5], 1u << (key & 31));
-                                                }
-                                            pipe->any_odd[k % kItems] = 1;
-                                        }
+                                for (int y = 0; y < 4; ++y) {
+                                    const int left = seen - 4 * y;
+                                    q[y] &= left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+                                    const uint32_t nan = nan_of(q[y]);
+                                    if (nan) {
+                                        q[y] &= ~nan;
+                                        for (int z = 0; z < 4; ++z)
+                                            if (nan >> (8 * z) & 1) {
+                                                const int key = block * kBlock + 4 * y + z;
+                                                atomicOr(&pipe->odd[k % kItems][i - masked][key >> 5], 1u << (key & 31));
+                                            }
+                                        pipe->any_odd[k % kItems] = 1;
                                     }
                                 }
                             }
@@ -468,17 +473,17 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                             codes4_h2(c.y, h[2], h[3]);
                             codes4_h2(c.z, h[4], h[5]);
                             codes4_h2(c.w, h[6], h[7]);
-                            if (more) w[e] = step ? piece(n0, n1, 0, 0, e) : piece(h0, h1, nv, np, e);
-                            const uint32_t base = smem_addr(stage);
-                            st_shared_v4(base + to, h[0], h[1], h[2], h[3]);
-                            st_shared_v4(base + (to ^ 16), h[4], h[5], h[6], h[7]);
+                            const uint32_t to = base + place(v, e);
+                            st_shared_v4(to, h[0], h[1], h[2], h[3]);
+                            st_shared_v4(to ^ 16, h[4], h[5], h[6], h[7]);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&pipe->kv_full[s]);
                         ++n;
-                        if (step) h0 = n0, h1 = n1;
                     }
+                h0 = n0, h1 = n1;
+                n0 = head_of_page(r0), n1 = head_of_page(r1);
             }
             me.done_with(k);
         }
