@@ -56,7 +56,7 @@ template <int D> struct TcShape {
     static constexpr int kConv = D <= 128 ? 4 : 8;         // converter warps
     static constexpr int kConv0 = kSoft + 4;               // the first of them
     static constexpr int kThreads = 512;
-    static constexpr int kSoftRegs = kTiles == 2 ? 200 : 232, kMmaRegs = 40, kConvRegs = kTiles == 2 ? 72 : 104;
+    static constexpr int kSoftRegs = kTiles == 2 ? 184 : 232, kMmaRegs = 40, kConvRegs = 104;
     static_assert(kSoft * 32 * kSoftRegs + 128 * kMmaRegs + kConv * 32 * kConvRegs <= kThreads * 128, "more registers than the launch holds");
     static constexpr int kPart = D < 128 ? D : 128;
     static constexpr int kParts = D / kPart;
@@ -372,8 +372,8 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             const bool tells = it.h == 0 && last == it.n - 1 && ct == 0;       // one item of a request records its pages
             const int32_t* table = b.page_table + (int64_t)it.k_row * b.max_pages;
             // Page h of step i: its id as the table has it, kBeyond behind what the item sees; then its
-            // part of the head, NULL where there is none.  Ids are loaded two steps ahead, scales one
-            // step and codes one stage ahead of their use.
+            // part of the head, NULL where there is none.  Ids are loaded two steps ahead, scales and
+            // codes one step ahead of their use.
             constexpr int32_t kBeyond = INT32_MIN;
             auto id_of = [&](int i, int h) {
                 const int64_t p = 2 * (int64_t)i + h;
@@ -412,13 +412,16 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 return make_float2(__ldg(sc), __ldg(sc + kBlocks));
             };
             const uint8_t *h0 = nullptr, *h1 = nullptr, *n0 = nullptr, *n1 = nullptr;
-            uint4 w[kUnits];
+            // pieces under way: the keys' and the values' of a part each, loaded again as soon as they are used
+            uint4 w[2][kUnits];
             float2 sc;
             if (most > 0) {
                 const int32_t i0 = id_of(0, 0), i1 = id_of(0, 1), j0 = id_of(1, 0), j1 = id_of(1, 1);
                 h0 = head_of_page(i0), h1 = head_of_page(i1);
 #pragma unroll
-                for (int e = 0; e < kUnits; ++e) w[e] = piece(h0, h1, 0, 0, e);
+                for (int e = 0; e < kUnits; ++e) w[0][e] = piece(h0, h1, 0, 0, e);
+#pragma unroll
+                for (int e = 0; e < kUnits; ++e) w[1][e] = piece(h0, h1, 1, 0, e);
                 sc = scales_of(h0, h1);
                 n0 = head_of_page(j0), n1 = head_of_page(j1);
             }
@@ -438,15 +441,14 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                         const int s = n % S::kStages;
                         if (n >= S::kStages) ok = me.wait_all(&pipe->kv_empty[s], n / S::kStages - 1);
                         if (!ok) break;
-                        // what comes next: the step's next part, its values, the next step's keys
-                        const bool step = v == 1 && p == S::kParts - 1;
-                        const int nv = p + 1 < S::kParts ? v : 1 - v, np = p + 1 < S::kParts ? p + 1 : 0;
+                        // what comes next in this one's place: the step's next part, or the next step's first
+                        const bool step = p == S::kParts - 1;
                         const uint8_t *x0 = step ? n0 : h0, *x1 = step ? n1 : h1;
                         const uint32_t base = smem_addr(ring + s * S::kStage);
 #pragma unroll
                         for (int e = 0; e < kUnits; ++e) {
-                            uint4 c = w[e];
-                            w[e] = piece(x0, x1, nv, np, e);
+                            uint4 c = w[v][e];
+                            w[v][e] = piece(x0, x1, v, step ? 0 : p + 1, e);
                             if (v == 1 && i >= masked) {
                                 // tokens that no row sees become zeros; a NaN joins the rows that see it in the end
                                 const int block = ct / S::kPart + e * kDims;
