@@ -372,7 +372,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             const bool tells = it.h == 0 && last == it.n - 1 && ct == 0;       // one item of a request records its pages
             const int32_t* table = b.page_table + (int64_t)it.k_row * b.max_pages;
             // Page h of step i: its id as the table has it, kBeyond behind what the item sees; then its
-            // part of the head, NULL where there is none.  Ids are loaded two steps ahead, scales and
+            // part of the head, NULL where there is none.  Ids are loaded three steps ahead, scales and
             // codes one step ahead of their use.
             constexpr int32_t kBeyond = INT32_MIN;
             auto id_of = [&](int i, int h) {
@@ -411,82 +411,98 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 const float* sc = reinterpret_cast<const float*>(x + scale_at(D)) + ct % kBlocks;
                 return make_float2(__ldg(sc), __ldg(sc + kBlocks));
             };
-            const uint8_t *h0 = nullptr, *h1 = nullptr, *n0 = nullptr, *n1 = nullptr;
-            // pieces under way: the keys' and the values' of a part each, loaded again as soon as they are used
+            // Pages of this step, the next and the one after; pieces under way, of the keys and of the values
+            // to be converted next, loaded again as soon as they are used; the next keys' step's scales.
+            const uint8_t *h0 = nullptr, *h1 = nullptr, *n0 = nullptr, *n1 = nullptr, *m0 = nullptr, *m1 = nullptr;
             uint4 w[2][kUnits];
-            float2 sc;
-            if (most > 0) {
-                const int32_t i0 = id_of(0, 0), i1 = id_of(0, 1), j0 = id_of(1, 0), j1 = id_of(1, 1);
-                h0 = head_of_page(i0), h1 = head_of_page(i1);
+            float2 sc = make_float2(1.f, 1.f);
+            // Turns step i's keys (v = 0) or values, codes of pages x0 and x1, into their stages; the next ones
+            // are z0's and z1's.
+            auto convert = [&](auto kind, int i, const uint8_t* x0, const uint8_t* x1, const uint8_t* z0, const uint8_t* z1) {
+                constexpr int v = decltype(kind)::value;
 #pragma unroll
-                for (int e = 0; e < kUnits; ++e) w[0][e] = piece(h0, h1, 0, 0, e);
+                for (int p = 0; p < S::kParts; ++p) {
+                    const int s = n % S::kStages;
+                    if (ok && n >= S::kStages) ok = me.wait_all(&pipe->kv_empty[s], n / S::kStages - 1);
+                    if (!ok) return;
+                    const bool last_part = p == S::kParts - 1;
+                    const uint32_t base = smem_addr(ring + s * S::kStage);
 #pragma unroll
-                for (int e = 0; e < kUnits; ++e) w[1][e] = piece(h0, h1, 1, 0, e);
-                sc = scales_of(h0, h1);
-                n0 = head_of_page(j0), n1 = head_of_page(j1);
-            }
-            for (int i = 0; ok && i < most; ++i, ++u) {
-                if (ct < 8) {
-                    blk->k2[u % kMeta][ct] = pow2(scale_exponent(sc.x));
-                    blk->ev[u % kMeta][ct] = (float)scale_exponent(sc.y);
-                    if (ct == 0) blk->here[u % kMeta] = (h0 ? 1u : 0u) | (h1 || (2 * (int64_t)i + 1) * kPage >= top ? 2u : 0u);
+                    for (int e = 0; e < kUnits; ++e) {
+                        uint4 c = w[v][e];
+                        w[v][e] = last_part ? piece(z0, z1, v, 0, e) : piece(x0, x1, v, p + 1, e);
+                        if (v == 1 && i >= masked) {
+                            // tokens that no row sees become zeros; a NaN joins the rows that see it in the end
+                            const int block = ct / S::kPart + e * kDims;
+                            const int seen = top - i * kKeys - block * kBlock;
+                            uint32_t* q = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int left = seen - 4 * y;
+                                q[y] &= left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+                                const uint32_t nan = nan_of(q[y]);
+                                if (nan) {
+                                    q[y] &= ~nan;
+                                    for (int z = 0; z < 4; ++z)
+                                        if (nan >> (8 * z) & 1) {
+                                            const int key = block * kBlock + 4 * y + z;
+                                            atomicOr(&pipe->odd[k % kItems][i - masked][key >> 5], 1u << (key & 31));
+                                        }
+                                    pipe->any_odd[k % kItems] = 1;
+                                }
+                            }
+                        }
+                        uint32_t h[8];
+                        codes4_h2(c.x, h[0], h[1]);
+                        codes4_h2(c.y, h[2], h[3]);
+                        codes4_h2(c.z, h[4], h[5]);
+                        codes4_h2(c.w, h[6], h[7]);
+                        const uint32_t to = base + place(v, e);
+                        st_shared_v4(to, h[0], h[1], h[2], h[3]);
+                        st_shared_v4(to ^ 16, h[4], h[5], h[6], h[7]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pipe->kv_full[s]);
+                    ++n;
                 }
-                const int32_t r0 = id_of(i + 2, 0), r1 = id_of(i + 2, 1);
-                sc = scales_of(n0, n1);
+            };
+            // Step i's keys, of pages x0 and x1, and what the softmax has to know of it.
+            auto keys = [&](int i, const uint8_t* x0, const uint8_t* x1, const uint8_t* z0, const uint8_t* z1) {
+                if (ct < 8) {
+                    const int at = (u + i) % kMeta;
+                    blk->k2[at][ct] = pow2(scale_exponent(sc.x));
+                    blk->ev[at][ct] = (float)scale_exponent(sc.y);
+                    if (ct == 0) blk->here[at] = (x0 ? 1u : 0u) | (x1 || (2 * (int64_t)i + 1) * kPage >= top ? 2u : 0u);
+                }
+                sc = scales_of(z0, z1);
+                convert(Constant<0>(), i, x0, x1, z0, z1);
+            };
+            if (most > 0) {
+                const int32_t i0 = id_of(0, 0), i1 = id_of(0, 1), j0 = id_of(1, 0), j1 = id_of(1, 1), k0 = id_of(2, 0), k1 = id_of(2, 1);
+                h0 = head_of_page(i0), h1 = head_of_page(i1);
 #pragma unroll
                 for (int v = 0; v < 2; ++v)
 #pragma unroll
-                    for (int p = 0; p < S::kParts; ++p) {
-                        if (!ok) break;
-                        const int s = n % S::kStages;
-                        if (n >= S::kStages) ok = me.wait_all(&pipe->kv_empty[s], n / S::kStages - 1);
-                        if (!ok) break;
-                        // what comes next in this one's place: the step's next part, or the next step's first
-                        const bool step = p == S::kParts - 1;
-                        const uint8_t *x0 = step ? n0 : h0, *x1 = step ? n1 : h1;
-                        const uint32_t base = smem_addr(ring + s * S::kStage);
-#pragma unroll
-                        for (int e = 0; e < kUnits; ++e) {
-                            uint4 c = w[v][e];
-                            w[v][e] = piece(x0, x1, v, step ? 0 : p + 1, e);
-                            if (v == 1 && i >= masked) {
-                                // tokens that no row sees become zeros; a NaN joins the rows that see it in the end
-                                const int block = ct / S::kPart + e * kDims;
-                                const int seen = top - i * kKeys - block * kBlock;
-                                uint32_t* q = reinterpret_cast<uint32_t*>(&c);
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    const int left = seen - 4 * y;
-                                    q[y] &= left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-                                    const uint32_t nan = nan_of(q[y]);
-                                    if (nan) {
-                                        q[y] &= ~nan;
-                                        for (int z = 0; z < 4; ++z)
-                                            if (nan >> (8 * z) & 1) {
-                                                const int key = block * kBlock + 4 * y + z;
-                                                atomicOr(&pipe->odd[k % kItems][i - masked][key >> 5], 1u << (key & 31));
-                                            }
-                                        pipe->any_odd[k % kItems] = 1;
-                                    }
-                                }
-                            }
-                            uint32_t h[8];
-                            codes4_h2(c.x, h[0], h[1]);
-                            codes4_h2(c.y, h[2], h[3]);
-                            codes4_h2(c.z, h[4], h[5]);
-                            codes4_h2(c.w, h[6], h[7]);
-                            const uint32_t to = base + place(v, e);
-                            st_shared_v4(to, h[0], h[1], h[2], h[3]);
-                            st_shared_v4(to ^ 16, h[4], h[5], h[6], h[7]);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&pipe->kv_full[s]);
-                        ++n;
-                    }
-                h0 = n0, h1 = n1;
-                n0 = head_of_page(r0), n1 = head_of_page(r1);
+                    for (int e = 0; e < kUnits; ++e) w[v][e] = piece(h0, h1, v, 0, e);
+                sc = scales_of(h0, h1);
+                n0 = head_of_page(j0), n1 = head_of_page(j1);
+                m0 = head_of_page(k0), m1 = head_of_page(k1);
+                keys(0, h0, h1, n0, n1);
             }
+            for (int i = 0; ok && i < most; ++i) {
+                const int32_t r0 = id_of(i + 3, 0), r1 = id_of(i + 3, 1);
+                if (S::kTiles == 1 && i + 1 < most) keys(i + 1, n0, n1, m0, m1);
+                convert(Constant<1>(), i, h0, h1, n0, n1);
+                if (S::kTiles == 2 && i + 1 < most) keys(i + 1, n0, n1, m0, m1);
+                h0 = n0, h1 = n1;
+                n0 = m0, n1 = m1;
+                m0 = head_of_page(r0), m1 = head_of_page(r1);
+                // (1128 us without: what other CTAs have not read yet comes from DRAM)
+                if (ct == 0 && m0) prefetch_l2(m0, (uint32_t)head_bytes(D));
+                if (ct == 32 && m1) prefetch_l2(m1, (uint32_t)head_bytes(D));
+            }
+            u += most;
             me.done_with(k);
         }
     }

@@ -184,7 +184,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         const int tok_of = row / a.group, head_of = row % a.group;
         const int heads = a.kv_heads * a.group;
         uint32_t t = 0;                                    // steps so far
-        Place<S> kp;                                       // where the step's keys are
+        Ring<S> at;                                        // where the steps' values are
         Item it;
         bool ok = true;
         for (int k = 0; ok && me.take(k, it); ++k) {
@@ -195,10 +195,13 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             const bool live = tok_of < count;              // tok_of < a.tokens too
             const int see = live ? it.see(tok) : INT32_MAX;
             float refc = 0.f, sum = 0.f;                   // reference in log2 units, sum of P
-            for (int i = 0; ok && i < steps; ++i, ++t, kp.next(2 * S::kParts)) {
+            Place<S> vp, np;
+            if (most > 0) at.take();
+            for (int i = 0; ok && i < steps; ++i, ++t) {
+                at.step(i + 1 < most, vp, np);
                 const int s = S::kTiles == 2 ? x : t & 1;
                 if (all_see < (i + 1) * kKeys) {
-                    ok = clean_values<S>(me, ring, kp.then(S::kParts), max(0, all_see - i * kKeys), i - it.masked_from(), k, (warp & 3) * 32 + lane);
+                    ok = clean_values<S>(me, ring, vp, max(0, all_see - i * kKeys), i - it.masked_from(), k, (warp & 3) * 32 + lane);
                     if (!ok) break;
                 }
                 ok = me.wait_all(&misc->s_full[s], S::kTiles == 2 ? t : t >> 1);
@@ -259,7 +262,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                 sums[0] = add2(sums[0], sums[1]);
                 sum += sums[0].x + sums[0].y;
             }
-            for (int i = steps; i < most; ++i) kp.next(2 * S::kParts);
+            for (int i = steps; i < most; ++i) at.step(i + 1 < most, vp, np);
             // ---- the rows' outputs
             if (ok && steps > 0) {
                 // With two S the last step's products began before the ones of the step before had
@@ -322,31 +325,35 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                 const int steps[2] = {it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0};
                 const int most = max(steps[0], steps[1]);
                 if (lane == 0 && ok) {
-                    for (int i = 0; i < most && ok; ++i)
-                        for (int v = 0; v < 2 && ok; ++v) {
-                            for (int p = 0; p < S::kParts && ok; ++p, ++n) {
-                                const int s = n % S::kStages;
-                                if (n >= S::kStages) ok = me.wait(&misc->kv_empty[s], n / S::kStages - 1);
-                                if (!ok) break;
-                                mbar_arrive_expect_tx(&misc->kv_full[s], S::kStage);
+                    auto load = [&](int i, int v) {        // a step's keys or values
+                        for (int p = 0; p < S::kParts && ok; ++p, ++n) {
+                            const int s = n % S::kStages;
+                            if (n >= S::kStages) ok = me.wait(&misc->kv_empty[s], n / S::kStages - 1);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(&misc->kv_full[s], S::kStage);
 #pragma unroll
-                                for (int c = 0; c < S::kPart / 64; ++c)
-                                    tma_load_3d(ring + s * S::kStage + c * kBox, v ? &vmap : &kmap, p * S::kPart + 64 * c, it.h,
-                                                it.k_row + i * kKeys, &misc->kv_full[s]);
-                            }
-                            if (i == 0 && v == 0)          // Q behind the first keys, which have room earlier
-#pragma unroll
-                                for (int x = 0; x < S::kTiles; ++x) {
-                                    if (!ok || steps[x] == 0) continue;
-                                    if (items[x] > 0) ok = me.wait(&misc->q_empty[x], items[x] - 1);
-                                    if (!ok) continue;
-                                    ++items[x];
-                                    mbar_arrive_expect_tx(&misc->q_full[x], (uint32_t)(D * 2 * a.tokens * a.group));
-                                    for (int c = 0; c < D / 64; ++c)
-                                        tma_load_3d(q_smem + (x * (D / 64) + c) * kBox, &qmap, 64 * c, it.h * a.group,
-                                                    it.q_row + it.tok0 + x * a.tokens, &misc->q_full[x]);
-                                }
+                            for (int c = 0; c < S::kPart / 64; ++c)
+                                tma_load_3d(ring + s * S::kStage + c * kBox, v ? &vmap : &kmap, p * S::kPart + 64 * c, it.h,
+                                            it.k_row + i * kKeys, &misc->kv_full[s]);
                         }
+                    };
+                    if (most > 0) load(0, 0);
+#pragma unroll
+                    for (int x = 0; x < S::kTiles; ++x) {  // Q behind the first keys, which have room earlier
+                        if (!ok || steps[x] == 0) continue;
+                        if (items[x] > 0) ok = me.wait(&misc->q_empty[x], items[x] - 1);
+                        if (!ok) continue;
+                        ++items[x];
+                        mbar_arrive_expect_tx(&misc->q_full[x], (uint32_t)(D * 2 * a.tokens * a.group));
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(q_smem + (x * (D / 64) + c) * kBox, &qmap, 64 * c, it.h * a.group,
+                                        it.q_row + it.tok0 + x * a.tokens, &misc->q_full[x]);
+                    }
+                    for (int i = 0; i < most && ok; ++i) {
+                        if (S::kTiles == 1 && i + 1 < most) load(i + 1, 0);
+                        if (ok) load(i, 1);
+                        if (S::kTiles == 2 && ok && i + 1 < most) load(i + 1, 0);
+                    }
                 }
                 if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             }
