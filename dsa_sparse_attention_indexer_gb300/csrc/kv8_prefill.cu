@@ -58,6 +58,7 @@ template <int D> struct TcShape {
     static constexpr int kThreads = 512;
     static constexpr int kSoftRegs = kTiles == 2 ? 184 : 232, kMmaRegs = 40, kConvRegs = 104;
     static_assert(kSoft * 32 * kSoftRegs + 128 * kMmaRegs + kConv * 32 * kConvRegs <= kThreads * 128, "more registers than the launch holds");
+    static_assert(kSoftRegs >= 128 && kMmaRegs <= 128 && kConvRegs <= 128, "who takes and who gives");
     static constexpr int kPart = D < 128 ? D : 128;
     static constexpr int kParts = D / kPart;
     static constexpr int kStage = kBox * kPart / 64;
@@ -66,6 +67,7 @@ template <int D> struct TcShape {
     static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
     static constexpr uint32_t kIdQK = idesc_f16_f32(128, kKeys, false, false), kIdPV = idesc_f16_f32(128, kPart, false, false);
     static constexpr bool kValuesMn = false;
+    static constexpr bool kTurns = false;                  // 1147 us without, 1171 with: what the converters make comes in step
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
 };
@@ -198,13 +200,6 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(tmem + lanes + S::s(s) + 32 * q, w[q]);
                 const int u = (u0 + i) % kMeta;
-                float ck[8], ev[8];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 y = *reinterpret_cast<const float4*>(&blk->k2[u][4 * h]), z = *reinterpret_cast<const float4*>(&blk->ev[u][4 * h]);
-                    ck[4 * h] = y.x * c, ck[4 * h + 1] = y.y * c, ck[4 * h + 2] = y.z * c, ck[4 * h + 3] = y.w * c;
-                    ev[4 * h] = z.x, ev[4 * h + 1] = z.y, ev[4 * h + 2] = z.z, ev[4 * h + 3] = z.w;
-                }
                 const uint32_t here = blk->here[u];
                 tmem_ld_wait();
                 const int lim = see - i * kKeys;           // keys of the step that the row sees
@@ -222,7 +217,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                     float m = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
 #pragma unroll
                     for (int j = 2; j < 16; j += 2) m = max3(m, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                    top = fmaxf(top, fmaf(m, ck[g], ev[g]));
+                    top = fmaxf(top, fmaf(m, blk->k2[u][g] * c, blk->ev[u][g]));
                 }
                 const float fresh = top == -INFINITY ? 0.f : rintf(top) - kFirst;
                 if (i == 0) {
@@ -238,23 +233,27 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
 #pragma unroll
-                    for (int g = 4 * h; g < 4 * h + 4; ++g) {
-                        const float2 c2 = make_float2(ck[g], ck[g]), r2 = make_float2(ev[g] - ref, ev[g] - ref);
-                        float2 sums = make_float2(0.f, 0.f);
+                    for (int q = 2 * h; q < 2 * h + 2; ++q) {                  // 32 keys
+                        uint32_t p[16];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t* v = &w[g >> 1][16 * (g & 1) + 2 * j];
-                            float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, r2);
-                            y.x = ex2_approx(y.x);
-                            y.y = ex2_approx(y.y);
-                            sums = add2(sums, y);
-                            p[8 * (g & 3) + j] = pack_h2(y.x, y.y);
+                        for (int g = 2 * q; g < 2 * q + 2; ++g) {
+                            const float ev = blk->ev[u][g], ck = blk->k2[u][g] * c;
+                            const float2 c2 = make_float2(ck, ck), r2 = make_float2(ev - ref, ev - ref);
+                            float2 sums = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t* v = &w[q][16 * (g & 1) + 2 * j];
+                                float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, r2);
+                                y.x = ex2_approx(y.x);
+                                y.y = ex2_approx(y.y);
+                                sums = add2(sums, y);
+                                p[8 * (g & 1) + j] = pack_h2(y.x, y.y);
+                            }
+                            sum = fmaf(sums.x + sums.y, minus_pow2(ev), sum);
                         }
-                        sum = fmaf(sums.x + sums.y, minus_pow2(ev[g]), sum);
+                        tmem_st_32x32b_x16(tmem + lanes + S::s(s) + 16 * q, p);
                     }
-                    tmem_st_32x32b_x32(tmem + lanes + S::s(s) + 32 * h, p);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -488,19 +487,19 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 sc = scales_of(h0, h1);
                 n0 = head_of_page(j0), n1 = head_of_page(j1);
                 m0 = head_of_page(k0), m1 = head_of_page(k1);
-                keys(0, h0, h1, n0, n1);
+                if (S::kTiles == 1) keys(0, h0, h1, n0, n1);
             }
             for (int i = 0; ok && i < most; ++i) {
                 const int32_t r0 = id_of(i + 3, 0), r1 = id_of(i + 3, 1);
-                if (S::kTiles == 1 && i + 1 < most) keys(i + 1, n0, n1, m0, m1);
+                if (S::kTiles == 2) keys(i, h0, h1, n0, n1);
+                else if (i + 1 < most) keys(i + 1, n0, n1, m0, m1);
                 convert(Constant<1>(), i, h0, h1, n0, n1);
-                if (S::kTiles == 2 && i + 1 < most) keys(i + 1, n0, n1, m0, m1);
                 h0 = n0, h1 = n1;
                 n0 = m0, n1 = m1;
                 m0 = head_of_page(r0), m1 = head_of_page(r1);
                 // (1128 us without: what other CTAs have not read yet comes from DRAM)
-                if (ct == 0 && m0) prefetch_l2(m0, (uint32_t)head_bytes(D));
-                if (ct == 32 && m1) prefetch_l2(m1, (uint32_t)head_bytes(D));
+                if (ct == 0 && n0) prefetch_l2(n0, (uint32_t)head_bytes(D));
+                if (ct == 32 && n1) prefetch_l2(n1, (uint32_t)head_bytes(D));
             }
             u += most;
             me.done_with(k);

@@ -87,6 +87,7 @@ template <int D> struct Shape {
     static constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, kPart, true);
     static constexpr bool kValuesMn = true;
     // TMEM columns
+    static constexpr bool kTurns = true;
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
 };
