@@ -740,18 +740,19 @@ def _heads(t: torch.Tensor, name: str, device=None, rows=None):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
-    if t.numel() and t.stride(2) != 1:
-        raise ValueError(f"{name}'s head_dim must be contiguous, its stride is {t.stride(2)}")
-    if rows is not None and t.shape[0] < rows:
-        raise ValueError(f"{name} holds {t.shape[0]} rows, the call needs {rows}")
+    if stride[2] != 1 and t.numel():
+        raise ValueError(f"{name}'s head_dim must be contiguous, its stride is {stride[2]}")
+    if rows is not None and shape[0] < rows:
+        raise ValueError(f"{name} holds {shape[0]} rows, the call needs {rows}")
     # the stride of an axis of one entry says nothing
-    return DsaHeads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    return DsaHeads(t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
 
 
 def dsa_kv8_append(k, v, cache, batch: Batch, *, q=None, rope_dims=None, rope_style: int = ROPE_HALVES, rope_base=10000.0,

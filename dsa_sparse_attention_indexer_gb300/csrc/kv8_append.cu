@@ -235,7 +235,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int h, int64_t
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads<D>)
+__global__ void __launch_bounds__(kThreads<D>, 2)
 append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int kThreads = kv8::kThreads<D>, kWarps = kThreads / 32;
     __shared__ alignas(16) uint8_t tiles[kWarps][kBlock * D];
@@ -298,21 +298,33 @@ append_kernel(const __grid_constant__ AppendArgs a) {
             else append_block<D, false>(a, h, row, held, n, at, head, cs, tiles[warp], lane);
         }
         if (a.q) {
-            // queries: a thread takes 16 dims of a token and head at a time
+            // queries: a thread takes 16 dims of a head, of four tokens at a time
             constexpr int kItems = D / 16;
-            const int all = n * a.heads * kItems;
-            for (int i = blockIdx.y * kThreads + tid; i < all; i += gridDim.y * kThreads) {
-                const int item = i % kItems, h = i / kItems % a.heads, t = i / kItems / a.heads;
+            for (int i = blockIdx.y * kThreads + tid; i < a.heads * kItems; i += gridDim.y * kThreads) {
+                const int item = i % kItems, h = i / kItems;
                 int o1, o2;
                 item_dims<D>(item, a.rope, a.halves, o1, o2);
-                const uint16_t* src = a.q + (row + t) * a.q_tok + h * a.q_head;
-                float x[16];
-                unpack8(*reinterpret_cast<const uint4*>(src + o1), x);
-                unpack8(*reinterpret_cast<const uint4*>(src + o2), x + 8);
-                rotate(x, item, a.rope, a.halves, cs + t * pairs);
-                uint16_t* out = a.q_out + ((row + t) * a.heads + h) * D;
-                *reinterpret_cast<uint4*>(out + o1) = pack8(x);
-                *reinterpret_cast<uint4*>(out + o2) = pack8(x + 8);
+                const uint16_t* src = a.q + row * a.q_tok + h * a.q_head;
+                uint16_t* out = a.q_out + (row * a.heads + h) * D;
+                for (int t0 = 0; t0 < n; t0 += 4) {
+                    uint4 w[4][2];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t0 + t < n) {
+                            w[t][0] = *reinterpret_cast<const uint4*>(src + (t0 + t) * a.q_tok + o1);
+                            w[t][1] = *reinterpret_cast<const uint4*>(src + (t0 + t) * a.q_tok + o2);
+                        }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t0 + t < n) {
+                            float x[16];
+                            unpack8(w[t][0], x);
+                            unpack8(w[t][1], x + 8);
+                            rotate(x, item, a.rope, a.halves, cs + (t0 + t) * pairs);
+                            *reinterpret_cast<uint4*>(out + (int64_t)(t0 + t) * a.heads * D + o1) = pack8(x);
+                            *reinterpret_cast<uint4*>(out + (int64_t)(t0 + t) * a.heads * D + o2) = pack8(x + 8);
+                        }
+                }
             }
         }
         row += n;
@@ -358,19 +370,27 @@ extern "C" dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, con
     a.q_out = static_cast<uint16_t*>(q_out);
     a.k_out = static_cast<uint16_t*>(k_out);
     a.st = dev_status;
-    for (int i = 0; i < rope_dims / 2 && !inv_freq; ++i) {
-        const double x = std::pow((double)rope_base, -2.0 * i / rope_dims) * 0.15915494309189535;
-        a.turns.f[i] = (uint64_t)((x - std::floor(x)) * 18446744073709551616.0);
+    if (!inv_freq) {
+        // the last rotation's frequencies, by host thread: forming them takes longer than the rest of the call
+        static thread_local struct { int32_t dims = -1; float base = 0.f; kv8::Turns turns; } last;
+        if (last.dims != rope_dims || last.base != rope_base) {
+            for (int i = 0; i < rope_dims / 2; ++i) {
+                const double x = std::pow((double)rope_base, -2.0 * i / rope_dims) * 0.15915494309189535;
+                last.turns.f[i] = (uint64_t)((x - std::floor(x)) * 18446744073709551616.0);
+            }
+            last.dims = rope_dims, last.base = rope_base;
+        }
+        a.turns = last.turns;
     }
     // A thread block for each row where rows are few, so that a decode batch spreads over the
     // SMs (one that does not begin a block of tokens ends at once), for 16 rows where they are
-    // many; several share a block of tokens' heads while there are SMs without one.
+    // many; several share a block of tokens' heads, eight to an SM where there are heads enough.
     a.rows_per = b->total_q <= 2048 ? 1 : kv8::kBlock;
     const int64_t groups = (b->total_q + a.rows_per - 1) / a.rows_per;
     const int64_t blocks = std::min<int64_t>(groups, (b->total_q + kv8::kBlock - 1) / kv8::kBlock + b->batch);
     const int threads = head_dim == 256 ? kv8::kThreads<256> : kv8::kThreads<128>, warps = threads / 32;
     const int64_t jobs = std::max<int64_t>((2 * (int64_t)kv_heads + warps - 1) / warps, (int64_t)heads * head_dim / 16 / threads);
-    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(jobs, 2 * device_sm_count() / blocks));
+    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(jobs, (8 * device_sm_count() + blocks - 1) / blocks));
     const dim3 grid((unsigned)groups, (unsigned)std::min<int64_t>(share, 65535));
     auto* kernel = head_dim == 64 ? kv8::append_kernel<64> : head_dim == 128 ? kv8::append_kernel<128> : kv8::append_kernel<256>;
     DSA_CHECK(launch_pdl(kernel, grid, dim3((unsigned)threads), 0, as_stream(stream), 1, a));

@@ -652,6 +652,7 @@ kv8_merge_kernel(const __grid_constant__ Args a, int G) {
     const Meta me = a.meta[g], prev = a.meta[g - 1];
     auto same = [&](const Meta& m) { return m.r == me.r && m.rb == me.rb && m.h == me.h; };
     if (me.r < 0 || !me.inside || (prev.inside && same(prev))) return;
+    const Request w = request<COLS>(a, me.r);
     __shared__ int32_t s_end;
     if (threadIdx.x == 0) s_end = G;
     __syncthreads();
@@ -663,24 +664,41 @@ kv8_merge_kernel(const __grid_constant__ Args a, int G) {
     const int np = 1 + s_end - g;
     // the first piece is the last of the share before
     auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)(g - 1) + 1 : 2 * (int64_t)(g - 1 + i); };
-    const Request w = request<COLS>(a, me.r);
-    constexpr int kQuads = D / 4;
+    constexpr int kQuads = D / 4, kBatch = 8;
     for (int i = blockIdx.y * 128 + threadIdx.x; i < COLS * kQuads; i += gridDim.y * 128) {
         const int col = i / kQuads, d = i % kQuads * 4, row = me.rb * COLS + col;
         if (row >= w.rows) continue;
-        float base = -INFINITY;
-        for (int q = 0; q < np; ++q) base = fmaxf(base, __ldcg(&a.part_ml[slot(q) * COLS + col]).x);
-        float total = 0.f, c = 0.f;
+        // in one pass, eight pieces' loads at a time: {reference, sum, log2 units of a score}, four dims
+        float4 ml[kBatch], y[kBatch];
+        auto load = [&](int q0) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                ml[q] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                if (q0 + q < np) {
+                    ml[q] = __ldcg(&a.part_ml[slot(q0 + q) * COLS + col]);
+                    y[q] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + ((slot(q0 + q) * COLS + col) * D + d) / 4);
+                }
+            }
+        };
+        float base = -INFINITY, total = 0.f, c = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int q = 0; q < np; ++q) {
-            const float4 ml = __ldcg(&a.part_ml[slot(q) * COLS + col]);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o) + ((slot(q) * COLS + col) * D + d) / 4);
-            c = ml.z;
-            if (ml.y == 0.f) continue;                     // nothing seen
-            const float f = ml.y * (ml.x > -INFINITY ? exp2f((ml.x - base) * c) : 1.f);
-            total += f;
-            v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y), v.z = fmaf(f, y.z, v.z), v.w = fmaf(f, y.w, v.w);
+        for (int q0 = 0; q0 < np; q0 += kBatch) {
+            load(q0);
+            float top = base;
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) top = fmaxf(top, ml[q].x);
+            c = ml[0].z;
+            const float old = base > -INFINITY ? exp2f((base - top) * c) : 1.f;
+            total *= old;
+            v.x *= old, v.y *= old, v.z *= old, v.w *= old;
+            base = top;
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                if (ml[q].y == 0.f) continue;              // nothing seen, or no piece
+                const float f = ml[q].y * (ml[q].x > -INFINITY ? exp2f((ml[q].x - base) * c) : 1.f);
+                total += f;
+                v.x = fmaf(f, y[q].x, v.x), v.y = fmaf(f, y[q].y, v.y), v.z = fmaf(f, y[q].z, v.z), v.w = fmaf(f, y[q].w, v.w);
+            }
         }
         const float inv = total != 0.f ? 1.f / total : 0.f;
         v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
