@@ -16,7 +16,7 @@
 //   - tcgen05 would have the codes converted into shared memory and read back from
 //     there, 128 rows for the 8 that there are.
 //
-// Work split: row blocks of 8, 16 or 32 query rows (tokens x the group's heads) of a
+// Work split: row blocks of 8, 16, 32 or 64 query rows (tokens x the group's heads) of a
 // request and head form one line of pages, cut into equal shares, one per CTA.  The eight
 // consumer warps of a CTA take a share's blocks of tokens in turn, each with its own
 // reference, sum and O^T, and are joined behind the share's part of a row block; a row
@@ -70,15 +70,20 @@ static_assert(kConsumers * 32 * kConsRegs + 128 * kProdRegs <= kThreads * kLaunc
 constexpr int kConsBar = 1;
 constexpr float kFirst = 7.0f, kTop = 15.0f;               // log2 of a reference's P, and of the largest
 
-template <int D, int NB> struct Shape {
-    static constexpr int kCols = 8 * NB;                   // query rows of a row block
+// GR: halves of the consumer warps.  With one, the halves take alternate pages, each with all
+// columns of the row block; with two, each half takes every page with half of the columns, so
+// that a page is copied once for as many rows as the registers of all warps hold (O^T is
+// D / 4 * NB of them): 16 requests of 24 rows at 256 dims 182 us with two row blocks, 160 so.
+template <int D, int NB, int GR> struct Shape {
+    static constexpr int kCols = 8 * NB * GR;              // query rows of a row block
+    static constexpr int kReaders = kPage / kBlock * GR;   // warps that read a page
     static constexpr int kKSteps = D / 16;
     static constexpr bool kQRegs = NB * D <= 256;          // Q stays in registers
     static constexpr int kHead = (int)head_bytes(D);
     static constexpr int kRedStride = D + 4;
     static constexpr int kRedBytes = kConsumers * 8 * kRedStride * 4;
-    static constexpr int kQBytes = NB * kKSteps * 32 * 8;
-    static constexpr int kFixed = kRedBytes + kQBytes + 4096;
+    static constexpr int kQBytes = NB * GR * kKSteps * 32 * 8;
+    static constexpr int kFixed = kRedBytes + kQBytes + 5120;
     // An even number, so that a stage's pages are all one half's of the warps: a warp that waits for
     // a stage's next page has seen the last one there, whose phase it could take for the next one's.
     static constexpr int kStages = (232448 - 1024 - kFixed) / kHead < 16 ? (232448 - 1024 - kFixed) / kHead / 2 * 2 : 16;
@@ -92,11 +97,11 @@ struct Misc {
     int32_t r0, rb0, h0;        // where the share begins
     int64_t page0, mine, at;    // page of the row block, pages of the share, of the line before it
     int64_t scratch[kThreads / 32];
-    float c[32];                // log2 units of a column's score
-    float ref[kConsumers][32], exp[kConsumers][32], sum[kConsumers][32];
-    float join[32][3];          // per column: reference, factor of O, sum
+    float c[64];                // log2 units of a column's score
+    float ref[kConsumers][32], exp[kConsumers][32], sum[kConsumers][32];       // of a warp's columns
+    float join[64][3];          // per column: reference, factor of O, sum
 };
-static_assert(sizeof(Misc) <= 4096, "misc block");
+static_assert(sizeof(Misc) <= 5120, "misc block");
 
 // A request's rows as this call sees them.
 struct Request {
@@ -238,10 +243,10 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return (m | m >> 7 | m >> 14 | m >> 21) & 15u;
 }
 
-template <int D, int NB>
+template <int D, int NB, int GR>
 __global__ void __launch_bounds__(kThreads, 1)
 kv8_attention_kernel(const __grid_constant__ Args a) {
-    using S = Shape<D, NB>;
+    using S = Shape<D, NB, GR>;
     constexpr int COLS = S::kCols, KS = S::kKSteps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
@@ -253,7 +258,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&misc->full[i], 1);
-            mbar_init(&misc->empty[i], kPage / kBlock);
+            mbar_init(&misc->empty[i], S::kReaders);
         }
         misc->abort = 0;
         fence_barrier_init();
@@ -333,6 +338,9 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
     const int g = lane >> 2, t = lane & 3;
     const int tok0 = 4 * (g >> 1) + (g & 1);               // K rows g and g + 8 of the operand hold tokens tok0 and tok0 + 2
     const int blk = warp & 3;                              // block of the page
+    const int col0 = GR == 2 ? (warp >> 2) * 8 * NB : 0;   // the warp's first column
+    const int first_warp = GR == 2 ? warp & ~3 : 0;        // of those with the same columns
+    constexpr int kSame = kConsumers / GR;                 // warps with the same columns
     uint32_t n = 0;                                        // stages before the piece
     bool ok = true;
     do {
@@ -377,7 +385,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
         uint2 qr[S::kQRegs ? NB * KS : 1];
         if constexpr (S::kQRegs) {
 #pragma unroll
-            for (int i = 0; i < NB * KS; ++i) qr[i] = qf[i * 32 + lane];
+            for (int i = 0; i < NB * KS; ++i) qr[i] = qf[((col0 >> 3) * KS + i) * 32 + lane];
         }
         float o[NB][D / 16][4];                            // O^T: dims 16 i + g and + 8, columns 8 nb + 2 t and + 1
         float ref[NB][2], ex[NB][2], sum[NB][2], c[NB][2];
@@ -393,16 +401,17 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
                 ref[nb][j] = -INFINITY;
                 ex[nb][j] = 0.f;                           // kFirst - exponent of the reference's values
                 sum[nb][j] = 0.f;
-                c[nb][j] = misc->c[8 * nb + 2 * t + j];
+                c[nb][j] = misc->c[col0 + 8 * nb + 2 * t + j];
                 int tok, hd;
-                q_row(8 * nb + 2 * t + j, tok, hd);
+                q_row(col0 + 8 * nb + 2 * t + j, tok, hd);
                 see[nb][j] = k.w.prefix + tok + 1;
             }
         }
         const int32_t all_see = k.w.prefix + k.rb * COLS / a.group + 1;           // positions that every row of the block sees
 
-        for (int64_t p = k.page + ((warp >> 2 ^ n) & 1); p < k.end; p += 2) {
-            const uint32_t m = n + (uint32_t)(p - k.page);  // odd pages of the share are warps 4-7's
+        // with one half of columns, odd pages of the share are warps 4-7's
+        for (int64_t p = k.page + (GR == 1 ? (warp >> 2 ^ n) & 1 : 0); p < k.end; p += 3 - GR) {
+            const uint32_t m = n + (uint32_t)(p - k.page);
             const int s = m % S::kStages;
             if (ok && !wait_for(&misc->full[s], m / S::kStages & 1, abort_flag, a.b.wait_ns)) {
                 timeout(2);
@@ -436,7 +445,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
                         for (int nb = 0; nb < NB; ++nb) {
                             uint2 b;
                             if constexpr (S::kQRegs) b = qr[nb * KS + h * 4 + w];
-                            else b = qf[(nb * KS + h * 4 + w) * 32 + lane];
+                            else b = qf[(((col0 >> 3) + nb) * KS + h * 4 + w) * 32 + lane];
                             mma_16816(sc[nb], a0, a1, a2, a3, b.x, b.y);
                         }
                     }
@@ -576,19 +585,19 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
                 const int col = 8 * nb + 2 * t + j;
                 float base = -INFINITY, most = -INFINITY, total = 0.f;
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) base = fmaxf(base, misc->ref[w][col]);
+                for (int w = first_warp; w < first_warp + kSame; ++w) base = fmaxf(base, misc->ref[w][col]);
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
+                for (int w = first_warp; w < first_warp + kSame; ++w) {
                     const float by = (misc->ref[w][col] - base) * c[nb][j];
                     if (misc->ref[w][col] > -INFINITY) most = fmaxf(most, by + misc->exp[w][col]);
                     // a warp without a reference has seen nothing, or a NaN that is in its sum
                     if (misc->sum[w][col] != 0.f) total += misc->sum[w][col] * (misc->ref[w][col] > -INFINITY ? exp2f(by) : 1.f);
                 }
                 f[nb][j] = ref[nb][j] > -INFINITY ? exp2f((ref[nb][j] - base) * c[nb][j] + (kFirst - ex[nb][j]) - most) : 1.f;
-                if (warp == 0 && g == 0) {
-                    misc->join[col][0] = base;
-                    misc->join[col][1] = total != 0.f ? exp2f(most - kFirst) / total : 0.f;
-                    misc->join[col][2] = total;
+                if (warp == first_warp && g == 0) {
+                    misc->join[col0 + col][0] = base;
+                    misc->join[col0 + col][1] = total != 0.f ? exp2f(most - kFirst) / total : 0.f;
+                    misc->join[col0 + col][2] = total;
                 }
             }
         const bool whole = k.page == 0 && k.end == k.pages;
@@ -602,11 +611,11 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) mine[(j & 1) * S::kRedStride + 16 * i + (j >> 1) * 8] = o[nb][i][j] * f[nb][j & 1];
             bar_sync<kConsBar, kConsumers * 32>();
-            for (int i = tid; i < 8 * D / 4; i += kConsumers * 32) {
-                const int cc = i / (D / 4), d = i % (D / 4) * 4, col = 8 * nb + cc;
+            for (int i = tid; i < GR * 8 * D / 4; i += kConsumers * 32) {
+                const int gr = i / (8 * D / 4), cc = i / (D / 4) % 8, d = i % (D / 4) * 4, col = gr * 8 * NB + 8 * nb + cc;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
+                for (int w = gr * kSame; w < gr * kSame + kSame; ++w) {
                     const float4 y = *reinterpret_cast<const float4*>(red + (w * 8 + cc) * S::kRedStride + d);
                     v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
                 }
@@ -722,22 +731,22 @@ constexpr int kTcRows = 64;
 // Query rows of a row block.
 static int columns(int64_t max_rows, int dim) {
     if (max_rows <= 8) return 8;
-    if (max_rows <= 16 || dim == 256) return 16;
-    return 32;
+    if (max_rows <= 16) return 16;
+    return max_rows <= 32 || dim == 256 ? 32 : 64;
 }
 
 static size_t ws_bytes(int sms, int dim) {
-    const size_t cols = dim == 256 ? 16 : 32;
+    const size_t cols = dim == 256 ? 32 : 64;
     return ((size_t)2 * sms * cols * (dim * 4 + 16) + (size_t)sms * sizeof(Meta) + 255) / 256 * 256;
 }
 
-template <int D, int NB>
+template <int D, int NB, int GR>
 static dsa_status launch(Args a, int sms, int G, cudaStream_t s) {
-    using S = Shape<D, NB>;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(&kv8_attention_kernel<D, NB>), S::kSmem) != DSA_OK) return DSA_ERR_CUDA;
+    using S = Shape<D, NB, GR>;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(&kv8_attention_kernel<D, NB, GR>), S::kSmem) != DSA_OK) return DSA_ERR_CUDA;
     a.part_ml = reinterpret_cast<float4*>(a.part_o + (size_t)2 * sms * S::kCols * D);
     a.meta = reinterpret_cast<Meta*>(a.part_ml + (size_t)2 * sms * S::kCols);
-    DSA_CHECK(launch_pdl(kv8_attention_kernel<D, NB>, dim3((unsigned)G), dim3(kThreads), S::kSmem, s, 1, a));
+    DSA_CHECK(launch_pdl(kv8_attention_kernel<D, NB, GR>, dim3((unsigned)G), dim3(kThreads), S::kSmem, s, 1, a));
     if (G > 1)
         DSA_CHECK(launch_pdl(kv8_merge_kernel<D, S::kCols>, dim3((unsigned)(G - 1), (unsigned)(S::kCols * D / 4 / 128)), dim3(128), 0, s, 1, a, G));
     return DSA_OK;
@@ -809,14 +818,17 @@ extern "C" dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache
     const int64_t blocks = std::min<int64_t>(b->total_q * a.group / cols + b->batch, b->total_q * a.group);
     const int64_t pages = ((int64_t)b->max_seq_len + kPage - 1) / kPage;
     const int G = (int)std::min<int64_t>(sms, std::max<int64_t>(1, blocks) * kv_heads * pages);
-    switch (head_dim / 64 * 64 + cols) {
-        case 64 + 8: return kv8::launch<64, 1>(a, sms, G, s);
-        case 64 + 16: return kv8::launch<64, 2>(a, sms, G, s);
-        case 64 + 32: return kv8::launch<64, 4>(a, sms, G, s);
-        case 128 + 8: return kv8::launch<128, 1>(a, sms, G, s);
-        case 128 + 16: return kv8::launch<128, 2>(a, sms, G, s);
-        case 128 + 32: return kv8::launch<128, 4>(a, sms, G, s);
-        case 256 + 8: return kv8::launch<256, 1>(a, sms, G, s);
-        default: return kv8::launch<256, 2>(a, sms, G, s);
+    switch (1000 * head_dim + cols) {
+        case 64008: return kv8::launch<64, 1, 1>(a, sms, G, s);
+        case 64016: return kv8::launch<64, 2, 1>(a, sms, G, s);
+        case 64032: return kv8::launch<64, 4, 1>(a, sms, G, s);
+        case 64064: return kv8::launch<64, 4, 2>(a, sms, G, s);
+        case 128008: return kv8::launch<128, 1, 1>(a, sms, G, s);
+        case 128016: return kv8::launch<128, 2, 1>(a, sms, G, s);
+        case 128032: return kv8::launch<128, 4, 1>(a, sms, G, s);
+        case 128064: return kv8::launch<128, 4, 2>(a, sms, G, s);
+        case 256008: return kv8::launch<256, 1, 1>(a, sms, G, s);
+        case 256016: return kv8::launch<256, 2, 1>(a, sms, G, s);
+        default: return kv8::launch<256, 2, 2>(a, sms, G, s);
     }
 }

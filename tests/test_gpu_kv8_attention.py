@@ -45,6 +45,12 @@ SHAPES = [
     ([128, 127], [128, 3], 2, 1, 64),
     ([257], [140], 2, 8, 128),
     ([40], [3], 1, 128, 64),
+    # 17 to 64 rows: two halves of columns
+    ([100, 300], [5, 6], 2, 4, 256),
+    ([1000, 65], [8, 4], 1, 4, 256),
+    ([777, 200, 40], [6, 1, 5], 2, 8, 128),
+    ([130, 3000], [60, 33], 2, 1, 64),
+    ([90], [1], 1, 61, 128),
     # many rows a request, alone and beside few
     ([300], [300], 1, 1, 128),
     ([300], [129], 2, 1, 64),
@@ -75,11 +81,11 @@ def test_many_requests_of_all_lengths():
     assert bits == 0
 
 
-@pytest.mark.parametrize("dim", [64, 128, 256])
-def test_shares_of_many_pages(dim):
+@pytest.mark.parametrize("dim,n", [(64, 1), (128, 1), (256, 1), (64, 20), (128, 17), (256, 9)])
+def test_shares_of_many_pages(dim, n):
     """Shares of more pages than a CTA holds at once, several times over, of an odd number of pages each."""
     seq = [7000 + 333 * (i % 7) for i in range(40)]
-    c = cache_case(seq, [1] * 40, 1, 2, dim, seed=dim)
+    c = cache_case(seq, [n] * 40, 1, 2, dim, seed=dim)
     out, lse, bits = _run(c)
     check(out, lse, expected(c))
     assert bits == 0
