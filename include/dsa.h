@@ -605,6 +605,9 @@ dsa_status dsa_pages_fork(int32_t* page_ref, int64_t num_pages, int32_t* page_ta
  *   keys   [64 tokens][head_dim]           E4M3
  *   values [4 blocks][head_dim][16 tokens] E4M3 (a block's tokens side by side)
  *   scales keys fp32 [4 blocks], values fp32 [4 blocks]
+ * dsa_pages_reserve and dsa_pages_release serve its pages as they do the latent
+ * caches'; dsa_pages_fork shares its full pages (a length that is a multiple of 64,
+ * or a partial page that the caller copies), and a dsa_cache does not name one.
  *
  * A dsa_heads names bf16 rows of heads, so that parts of a projection's output
  * are taken as they lie.  data is 16-byte aligned, the strides multiples of 8
