@@ -21,17 +21,21 @@ constexpr int kBox = kKeys * 128;                          // bytes of 128 rows 
 struct Item {
     int32_t q_row, tok0, n;     // the sequence's first row of q, the item's first token, the sequence's tokens; n < 0: no more items
     int32_t k_row, len, h;      // its first row of k (of a paged cache: its request), the sequence's keys, the key head
-    int32_t cap, pad;           // keys that there are
+    int32_t cap;                // keys that there are
+    int32_t from, to;           // the steps of this piece of it: [from, to)
+    int32_t slot;               // of the piece's partial outputs; -1: it is whole
+    int32_t pad;
     // keys that token t sees
     __device__ __forceinline__ int see(int t) const { return max(0, min(cap, len - n + t + 1)); }
-    // tokens of tile x, and its steps
+    // tokens of tile x, and its steps, of the whole item and of this piece
     __device__ __forceinline__ int count(int x, int tokens) const { return max(0, min(tokens, n - tok0 - x * tokens)); }
-    __device__ __forceinline__ int steps(int x, int tokens) const {
+    __device__ __forceinline__ int all_steps(int x, int tokens) const {
         const int c = count(x, tokens);
         return c ? (see(tok0 + x * tokens + c - 1) + kKeys - 1) / kKeys : 0;
     }
-    // the first step that some row of the item sees in part or not at all
-    __device__ __forceinline__ int masked_from() const { return see(tok0) / kKeys; }
+    __device__ __forceinline__ int steps(int x, int tokens) const { return max(0, min(all_steps(x, tokens), to) - from); }
+    // the first step that some row of the item sees in part or not at all, counted from the piece's first
+    __device__ __forceinline__ int masked_from() const { return see(tok0) / kKeys - from; }
 };
 
 // MMAs and commits of one lane, `lead`, of a warp that runs them together: in control flow
@@ -186,9 +190,11 @@ struct Role {
     }
     __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) const { return __all_sync(0xffffffffu, wait(bar, parity)); }
     // Item k of the CTA, read by a whole warp; false when there is none.
-    __device__ __forceinline__ bool take(int k, Item& it) const {
+    // (Cut: items may be pieces.)
+    template <bool Cut> __device__ __forceinline__ bool take(int k, Item& it) const {
         if (!wait_all(&m->item_full[k % kItems], k / kItems)) return false;
         it = m->item[k % kItems];
+        if (!Cut) it.from = 0, it.to = INT32_MAX, it.slot = -1;
         return it.n >= 0;
     }
     __device__ __forceinline__ void done_with(int k) const {
@@ -236,7 +242,7 @@ struct Ring {
 
 // The warp that issues tile x's MMAs.  S: kDim, kTiles, kPart, kParts, kStage, kStages, s(i) and
 // o(i) (TMEM columns), kIdQK and kIdPV, kValuesMn (values lie with their dims side by side: an
-// MN-major operand; else their tokens), kTurns.  A warp a tile, as its own waits and the time that
+// MN-major operand; else their tokens), kTurns, kCut (items may be pieces).  A warp a tile, as its own waits and the time that
 // operands take to uniform registers (an MMA of 128 x 128 x 16 runs 64 cycles and is issued in
 // 80 to 100) would bound the kernel if one warp issued for both.  With kTurns the tiles take turns
 // with a step's last MMAs, which keeps them out of step: one's softmax runs beside the other's
@@ -251,7 +257,7 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
     Ring<S> ring;
     bool ok = true;
     Item it;
-    for (int k = 0; ok && me.take(k, it); ++k) {
+    for (int k = 0; ok && me.take<S::kCut>(k, it); ++k) {
         me.done_with(k);
         auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };      // so that the compiler knows it for the warp's
         const int steps = same(it.steps(x, tokens));
@@ -355,44 +361,131 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
     mbar_wait(&m->drain[x], 0);
 }
 
-// Lays out the CTA's items, `per` tokens each, 32 requests at a time, one a lane: `rows(r, qs,
-// qn)` gives a request's first row and tokens, `keys(r, it)` sets an item's keys.  The items of
-// a request come longest first, and go there and back over the CTAs.
-template <class Rows, class Keys>
-__device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_heads, int per, Rows rows, Keys keys) {
-    Pipe* m = me.m;
+// Items are dealt out to the CTAs in rounds.  The last round's, which would leave CTAs without
+// work, may be cut along the keys into equal pieces, as many as fill the CTAs best, that leave
+// partial outputs for a second kernel: one request's 512 items of 128 steps on 152 CTAs take
+// 3.4 rounds so and 4 else, and a chunk of 100 tokens over a long cache has few items at all.
+constexpr int kMinSteps = 8;                               // of a piece: beginning and end cost about five steps
+constexpr int kMaxPieces = 160;
+
+struct Split {
+    float* part_o;              // [slots][rows of an item][D]: normalised
+    float2* part_ml;            // [slots][rows of an item]: reference in log2 units, sum
+    struct Cut* cut;            // [CTAs]: the last round's items
+    int slots;                  // 0: no item is cut
+    int ctas;
+};
+struct Cut {
+    int32_t q_row, tok0, count, h, slot, pieces, pad[2];   // first row of q and token, tokens; pieces < 2: nothing to join
+};
+
+// How many pieces each of `rest` items is cut into: the smallest number of CTAs' turns, in
+// units of an item.  Asked of a whole warp.
+__device__ __forceinline__ uint32_t pieces_of(uint32_t rest, uint32_t ctas, uint32_t slots) {
+    if (rest == 0) return 1;
+    const uint32_t most = min(slots / rest, (uint32_t)kMaxPieces);
+    uint32_t best = 0xffffffffu;
+    for (uint32_t p = 1 + (threadIdx.x & 31); p <= most; p += 32) best = min(best, ((rest * p + ctas - 1) / ctas * 65536u / p) << 8 | p);
+    best = __reduce_min_sync(0xffffffffu, best);
+    return best == 0xffffffffu ? 1 : best & 255u;
+}
+static_assert(kMaxPieces < 256, "pieces in a byte");
+
+// The items of a call in order, 32 requests at a time, one a lane; asked of a whole warp, for
+// items in ascending order.
+template <class Rows>
+struct Finder {
+    Rows rows;
+    int batch, kv_heads, per, lane;
     int c0 = -32;
     uint32_t base = 0, all = 0;                            // items before the 32 requests, and theirs (the host bounds them)
     uint32_t upto = 0;                                     // and of those up to the lane's
     int qs = 0, qn = 0, blocks = 0;
-    for (int k = 0;; ++k) {
-        const uint32_t i = (uint32_t)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        while (i >= base + all && c0 + 32 < batch) {
-            base += all;
-            c0 += 32;
-            qs = qn = 0;
-            if (c0 + me.lane < batch) rows(c0 + me.lane, qs, qn);
-            blocks = (qn + per - 1) / per;
-            upto = (uint32_t)(blocks * kv_heads);
+    __device__ __forceinline__ bool next() {
+        if (c0 + 32 >= batch) return false;
+        base += all;
+        c0 += 32;
+        qs = qn = 0;
+        if (c0 + lane < batch) rows(c0 + lane, qs, qn);
+        blocks = (qn + per - 1) / per;
+        upto = (uint32_t)(blocks * kv_heads);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (me.lane >= o) upto += y;
-            }
-            all = __shfl_sync(0xffffffffu, upto, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        Item it = {};
+        all = __shfl_sync(0xffffffffu, upto, 31);
+        return true;
+    }
+    // Item i without its keys; returns its request, -1 when there is none.
+    __device__ __forceinline__ int find(uint32_t i, Item& it) {
+        it = Item{};
         it.n = -1;
-        const uint32_t past = __ballot_sync(0xffffffffu, i < base + upto);
-        if (past) {
-            const int at = __ffs(past) - 1;
-            const int b = __shfl_sync(0xffffffffu, blocks, at);
-            const uint32_t j = i - base - __shfl_sync(0xffffffffu, upto - (uint32_t)(blocks * kv_heads), at);
-            it.q_row = __shfl_sync(0xffffffffu, qs, at);
-            it.n = __shfl_sync(0xffffffffu, qn, at);
-            it.tok0 = (b - 1 - (int)(j / (uint32_t)kv_heads)) * per;
-            it.h = (int)(j % (uint32_t)kv_heads);
-            keys(c0 + at, it);
+        while (i >= base + all)
+            if (!next()) return -1;
+        const int at = __ffs(__ballot_sync(0xffffffffu, i < base + upto)) - 1;
+        const int b = __shfl_sync(0xffffffffu, blocks, at);
+        const uint32_t j = i - base - __shfl_sync(0xffffffffu, upto - (uint32_t)(blocks * kv_heads), at);
+        it.q_row = __shfl_sync(0xffffffffu, qs, at);
+        it.n = __shfl_sync(0xffffffffu, qn, at);
+        it.tok0 = (b - 1 - (int)(j / (uint32_t)kv_heads)) * per;
+        it.h = (int)(j % (uint32_t)kv_heads);
+        return c0 + at;
+    }
+};
+
+// Lays out the CTA's items, of `tiles` tiles of `tokens` tokens: `rows(r, qs, qn)` gives a
+// request's first row and tokens, `keys(r, it, first)` sets an item's keys (first: it is the
+// item's first piece).  The items of a request come longest first, and go there and back
+// over the CTAs.
+template <class Rows, class Keys>
+__device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_heads, int tokens, int tiles, const Split& split, Rows rows, Keys keys) {
+    Pipe* m = me.m;
+    const int per = tokens * tiles;
+    uint32_t whole = 0xffffffffu, pieces = 1;              // items before the last round; pieces of its items
+    auto pieces_now = [&](const Item& it) {                // of one of them
+        int most = it.all_steps(0, tokens);
+        if (tiles == 2) most = max(most, it.all_steps(1, tokens));
+        return max(1, min((int)pieces, most / kMinSteps));
+    };
+    if (split.slots > 0) {
+        Finder<Rows> count{rows, batch, kv_heads, per, me.lane};
+        while (count.next()) {}
+        const uint32_t items = count.base + count.all, rest = items % gridDim.x;
+        whole = items - rest;
+        pieces = pieces_of(rest, gridDim.x, (uint32_t)split.slots);
+        // The joining kernel's list: written before any wait, so that it is there whatever else happens.
+        Cut cut = {};
+        if (blockIdx.x < rest) {
+            Finder<Rows> one{rows, batch, kv_heads, per, me.lane};
+            Item it;
+            const int r = one.find(whole + blockIdx.x, it);
+            if (r >= 0) {
+                keys(r, it, false);
+                cut.q_row = it.q_row, cut.tok0 = it.tok0, cut.count = min(per, it.n - it.tok0), cut.h = it.h;
+                cut.slot = (int)(blockIdx.x * pieces), cut.pieces = pieces_now(it);
+            }
+        }
+        if (me.lane == 0) split.cut[blockIdx.x] = cut;
+    }
+    Finder<Rows> finder{rows, batch, kv_heads, per, me.lane};
+    for (uint32_t k = 0, turn = 0;; ++turn) {
+        const uint32_t i = turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const uint32_t piece = i < whole ? 0 : (i - whole) % pieces;
+        Item it;
+        const int r = finder.find(i < whole ? i : whole + (i - whole) / pieces, it);
+        it.from = 0, it.to = INT32_MAX, it.slot = -1;
+        if (r >= 0) {
+            keys(r, it, piece == 0);
+            if (i >= whole && pieces > 1) {
+                const int n = pieces_now(it);
+                if ((int)piece >= n) continue;
+                if (n > 1) {
+                    const int64_t most = max(it.all_steps(0, tokens), tiles == 2 ? it.all_steps(1, tokens) : 0);
+                    it.from = (int)(most * piece / n), it.to = (int)(most * (piece + 1) / n);
+                    it.slot = (int)(i - whole);
+                }
+            }
         }
         if (k >= kItems && !me.wait_all(&m->item_empty[k % kItems], k / kItems - 1)) break;
         if (me.lane < kMasked * 4) m->odd[k % kItems][me.lane >> 2][me.lane & 3] = 0;
@@ -402,7 +495,79 @@ __device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_
             m->any_odd[k % kItems] = 0;
             mbar_arrive(&m->item_full[k % kItems]);
         }
-        if (it.n < 0) break;
+        if (r < 0) break;
+        ++k;
+    }
+}
+
+// Joins the partial outputs of the items that were cut: (R, l) of a piece: out = sum 2^R l
+// out_piece / sum 2^R l.  Four warps a row, each a quarter of its pieces, as what bounds it
+// is the loads' latency (100 pieces one after another by one warp: 80 us for 100 tokens over
+// 100,000); a lane takes D / 32 dims.
+constexpr int kJoinRows = 2, kJoinWarps = 4;               // rows of a block at a time, warps of a row
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * kJoinWarps * 32)
+join_kernel(const __grid_constant__ Split split, int group, int kv_heads, int item_rows, void* out, int out_f32, float* lse) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ float part[kJoinRows][kJoinWarps][D + 1];
+    const Cut cut = split.cut[blockIdx.x];
+    if (cut.pieces < 2) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp / kJoinWarps, w = warp % kJoinWarps;
+    const int tokens = 128 / group;                        // of a tile
+    for (int row0 = blockIdx.y * kJoinRows; row0 < item_rows; row0 += gridDim.y * kJoinRows) {
+        const int row = row0 + mine, tok = row / 128 * tokens + row % 128 / group;
+        const bool live = row % 128 < tokens * group && tok < cut.count;
+        float top = -INFINITY, total = 0.f, v[D / 32];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) v[j] = 0.f;
+        if (live) {
+            const float2* ml_at = split.part_ml + (int64_t)cut.slot * item_rows + row;
+            const float* o_at = split.part_o + ((int64_t)cut.slot * item_rows + row) * D + lane * (D / 32);
+            for (int p = lane; p < cut.pieces; p += 32) {
+                const float2 ml = __ldcg(ml_at + (int64_t)p * item_rows);
+                if (ml.y != 0.f) top = fmaxf(top, ml.x);   // 0: the row sees nothing there
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll 8
+            for (int p = w; p < cut.pieces; p += kJoinWarps) {
+                const float2 ml = __ldcg(ml_at + (int64_t)p * item_rows);
+                float y[D / 32];
+#pragma unroll
+                for (int j = 0; j < D / 32; j += 2) {
+                    const float2 two = __ldcg(reinterpret_cast<const float2*>(o_at + (int64_t)p * item_rows * D + j));
+                    y[j] = two.x, y[j + 1] = two.y;
+                }
+                const float f = ml.y != 0.f ? ml.y * exp2f(ml.x - top) : 0.f;
+                total += f;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+                    if (ml.y != 0.f) v[j] = fmaf(f, y[j], v[j]);               // (a NaN counts whatever its share)
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) part[mine][w][lane + 32 * j] = v[j];
+        if (lane == 0) part[mine][w][D] = total;
+        __syncthreads();
+        if (live && w == 0) {
+#pragma unroll
+            for (int i = 1; i < kJoinWarps; ++i) {
+                total += part[mine][i][D];
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) v[j] += part[mine][i][lane + 32 * j];
+            }
+            const float inv = total != 0.f ? 1.f / total : 0.f;
+            const int64_t at = (int64_t)(cut.q_row + cut.tok0 + tok) * (kv_heads * group) + cut.h * group + row % 128 % group;
+#pragma unroll
+            for (int j = 0; j < D / 32; j += 2) {
+                const int64_t to = at * D + lane * (D / 32) + j;
+                if (out_f32) *reinterpret_cast<float2*>(static_cast<float*>(out) + to) = make_float2(v[j] * inv, v[j + 1] * inv);
+                else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + to) = pack_bf2(v[j] * inv, v[j + 1] * inv);
+            }
+            if (lse && lane == 0) lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
+        }
+        __syncthreads();
     }
 }
 

@@ -724,7 +724,8 @@ kv8_merge_kernel(const __grid_constant__ Args a, int G) {
 }
 
 dsa_status launch_prefill(const dsa_heads* q, const uint8_t* cache, const dsa_batch* b, int32_t heads, int32_t kv_heads, int32_t dim,
-                          int32_t min_rows, float scale_log2, void* out, int out_f32, float* lse, int32_t* st, cudaStream_t s);
+                          int32_t min_rows, float scale_log2, void* out, int out_f32, float* lse, void* ws, int32_t* st, cudaStream_t s);
+size_t prefill_ws_bytes(int sms, const dsa_batch* b, int dim);
 // Requests with more query rows than this are the prefill kernel's.
 constexpr int kTcRows = 64;
 
@@ -735,9 +736,15 @@ static int columns(int64_t max_rows, int dim) {
     return max_rows <= 32 || dim == 256 ? 32 : 64;
 }
 
-static size_t ws_bytes(int sms, int dim) {
+static int64_t longest_request(const dsa_batch* b, int group) { return std::min<int64_t>(b->max_q_len, b->total_q) * group; }
+
+// The two kernels' parts of the workspace, one behind the other.
+static size_t few_rows_ws_bytes(int sms, int dim) {
     const size_t cols = dim == 256 ? 32 : 64;
     return ((size_t)2 * sms * cols * (dim * 4 + 16) + (size_t)sms * sizeof(Meta) + 255) / 256 * 256;
+}
+static size_t ws_bytes(int sms, const dsa_batch* b, int group, int dim) {
+    return few_rows_ws_bytes(sms, dim) + (longest_request(b, group) > kTcRows ? prefill_ws_bytes(sms, b, dim) : 0);
 }
 
 template <int D, int NB, int GR>
@@ -764,7 +771,7 @@ extern "C" dsa_status dsa_kv8_attention_workspace_size(const dsa_batch* b, int32
     vs = kv8::check_shape(heads, kv_heads, head_dim);
     if (vs != DSA_OK) return vs;
     if (!bytes) return DSA_ERR_INVALID_ARGUMENT;
-    *bytes = kv8::ws_bytes(device_sm_count(), head_dim);
+    *bytes = kv8::ws_bytes(device_sm_count(), b, heads / kv_heads, head_dim);
     return DSA_OK;
 }
 
@@ -784,7 +791,7 @@ extern "C" dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache
     if ((vs = kv8::check_heads(q)) != DSA_OK) return vs;
     if (!aligned16(cache) || !aligned16(out) || !aligned16(ws)) return DSA_ERR_ALIGNMENT;
     const int sms = device_sm_count();
-    if (ws_bytes < kv8::ws_bytes(sms, head_dim)) return DSA_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < kv8::ws_bytes(sms, b, heads / kv_heads, head_dim)) return DSA_ERR_WORKSPACE_TOO_SMALL;
     kv8::Args a = {};
     a.q = static_cast<const uint16_t*>(q->data);
     a.q_tok = q->token_stride, a.q_head = q->head_stride;
@@ -798,7 +805,7 @@ extern "C" dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache
     a.part_o = static_cast<float*>(ws);
     a.st = dev_status;
     const cudaStream_t s = as_stream(stream);
-    const int64_t longest = std::min<int64_t>(b->max_q_len, b->total_q) * a.group;
+    const int64_t longest = kv8::longest_request(b, a.group);
     a.max_rows = 0x7fffffff;
     // q's strides as a tensor map takes them; a q that does not lie so has its rows taken one by one
     const bool mapped = (heads == 1 || q->head_stride > 0) && (b->total_q == 1 || q->token_stride > 0) && q->head_stride < 1LL << 38 && q->token_stride < 1LL << 38;
@@ -806,7 +813,8 @@ extern "C" dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache
         // a single request is the prefill kernel's however few of its rows there turn out to be
         const bool all = b->batch == 1;
         a.max_rows = kv8::kTcRows;
-        vs = kv8::launch_prefill(q, cache, b, heads, kv_heads, head_dim, all ? 0 : kv8::kTcRows + 1, a.scale, out, a.out_f32, lse, dev_status, s);
+        vs = kv8::launch_prefill(q, cache, b, heads, kv_heads, head_dim, all ? 0 : kv8::kTcRows + 1, a.scale, out, a.out_f32, lse,
+                                 static_cast<uint8_t*>(ws) + kv8::few_rows_ws_bytes(sms, head_dim), dev_status, s);
         if (vs != DSA_OK || all) return vs;
     }
     const int64_t max_rows = std::min<int64_t>(longest, a.max_rows);

@@ -42,10 +42,12 @@ struct PrefillArgs {
     int out_f32;
     float* lse;
     int32_t* st;
+    Split split;
 };
 
 namespace {
 
+constexpr float kNone = -1e30f;                            // reference of a row that has seen nothing so far
 constexpr float kFirst = 7.0f, kTop = 15.0f;               // log2 of a new reference's P, and of the largest
 constexpr int kMeta = 8;                                   // steps whose scales are kept: more than the ring holds
 
@@ -67,6 +69,7 @@ template <int D> struct TcShape {
     static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
     static constexpr uint32_t kIdQK = idesc_f16_f32(128, kKeys, false, false), kIdPV = idesc_f16_f32(128, kPart, false, false);
     static constexpr bool kValuesMn = false;
+    static constexpr bool kCut = true;
     static constexpr bool kTurns = false;                  // 1147 us without, 1171 with: what the converters make comes in step
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
@@ -149,7 +152,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
         uint32_t t = 0, q_items = 0, u0 = 0;               // the tile's steps, items with a Q and steps of the CTA so far
         Item it;
         bool ok = true;
-        for (int k = 0; ok && me.take(k, it); ++k) {
+        for (int k = 0; ok && me.take<S::kCut>(k, it); ++k) {
             const int count = it.count(x, a.tokens), steps = it.steps(x, a.tokens);
             const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0);
             const int tok = it.tok0 + x * a.tokens + tok_of;
@@ -202,7 +205,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 const int u = (u0 + i) % kMeta;
                 const uint32_t here = blk->here[u];
                 tmem_ld_wait();
-                const int lim = see - i * kKeys;           // keys of the step that the row sees
+                const int lim = see - (it.from + i) * kKeys;           // keys of the step that the row sees
                 if (__any_sync(0xffffffffu, lim < kKeys) || here != 3u) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -219,7 +222,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                     for (int j = 2; j < 16; j += 2) m = max3(m, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                     top = fmaxf(top, fmaf(m, blk->k2[u][g] * c, blk->ev[u][g]));
                 }
-                const float fresh = top == -INFINITY ? 0.f : rintf(top) - kFirst;
+                const float fresh = top == -INFINITY ? kNone : rintf(top) - kFirst;
                 if (i == 0) {
                     ref = fresh;
                 } else if (__any_sync(0xffffffffu, top > ref + kTop)) {
@@ -270,7 +273,9 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             }
             if (ok && count > 0) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const int64_t at = (int64_t)(it.q_row + tok) * heads + it.h * a.group + head_of;
+                const bool cut = it.slot >= 0;             // a piece's rows are its slot's
+                const int64_t at = cut ? (int64_t)it.slot * (S::kTiles * 128) + x * 128 + row : (int64_t)(it.q_row + tok) * heads + it.h * a.group + head_of;
+                void* const to = cut ? a.split.part_o : a.out;
                 const bool odd = pipe->any_odd[k % kItems] != 0;
 #pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
@@ -289,7 +294,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                         if (odd) {
                             // NaN values of masked steps that this row sees
                             for (int e = 0; e < kMasked * kKeys; ++e) {
-                                const int key = it.masked_from() * kKeys + e;
+                                const int key = (it.from + it.masked_from()) * kKeys + e;
                                 if (!(pipe->odd[k % kItems][e / kKeys][e % kKeys / 32] >> (e & 31) & 1) || key >= see) continue;
                                 const int64_t page = b.page_table[(int64_t)it.k_row * b.max_pages + key / kPage];
                                 const uint8_t* v = a.cache + (page * a.kv_heads + it.h) * head_bytes(D) + v_at(D) + key % kPage / kBlock * (kBlock * D) +
@@ -299,11 +304,12 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                                     if ((v[j * kBlock] & 0x7f) == 0x7f) y[j] = __int_as_float(0x7fc00000);
                             }
                         }
-                        write_32(a.out, a.out_f32, at * D + d, y);
+                        write_32(to, cut || a.out_f32, at * D + d, y);
                     }
                     __syncwarp();
                 }
-                if (live && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+                if (live && cut) a.split.part_ml[at] = make_float2(ref, sum);
+                else if (live && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
             }
             tc_fence_before();                             // O is read before the next item's first P says so
             me.done_with(k);
@@ -314,19 +320,19 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             if (warp - kMmaWarp < S::kTiles) issue_mmas<S>(me, warp - kMmaWarp, smem_addr(q_smem), smem_addr(ring), a.tokens);
         } else if (warp == kItemWarp) {
             lay_out_items(
-                me, b.batch, a.kv_heads, a.tokens * S::kTiles,
+                me, b.batch, a.kv_heads, a.tokens, S::kTiles, a.split,
                 [&](int r, int& qs, int& qn) {
                     qs = b.q_start[r];
                     qn = (int)max((int64_t)0, min((int64_t)b.q_start[r + 1], b.total_q) - qs);
                     if ((int64_t)qn * a.group < a.min_rows) qn = 0;
                 },
-                [&](int r, Item& it) {
+                [&](int r, Item& it, bool first) {
                     const int len = b.seq_len[r];
                     const int64_t room = (int64_t)b.max_pages * kPage;
                     it.k_row = r;
                     it.len = len - (b.q_start[r + 1] - it.q_row) + it.n;
                     it.cap = (int)min((int64_t)INT32_MAX, room);
-                    if (lane == 0 && it.h == 0 && it.tok0 == 0) {
+                    if (first && lane == 0 && it.h == 0 && it.tok0 == 0) {
                         if (it.len < it.n) record_error(a.st, DSA_DEVERR_INDEX_RANGE, it.len - it.n);
                         else if (len > room) record_error(a.st, DSA_DEVERR_INDEX_RANGE, len);
                     }
@@ -336,7 +342,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             uint32_t items[2] = {0, 0};
             bool ok = true;
             Item it;
-            for (int k = 0; me.take(k, it); ++k) {
+            for (int k = 0; me.take<S::kCut>(k, it); ++k) {
                 me.done_with(k);
 #pragma unroll
                 for (int x = 0; x < S::kTiles; ++x) {
@@ -363,7 +369,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
         uint32_t n = 0, u = 0;                             // stages and steps so far
         bool ok = true;
         Item it;
-        for (int k = 0; ok && me.take(k, it); ++k) {
+        for (int k = 0; ok && me.take<S::kCut>(k, it); ++k) {
             const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0), masked = it.masked_from();
             int last = it.n - 1;                           // the item's last token
             last = min(last, it.tok0 + a.tokens * S::kTiles - 1);
@@ -375,7 +381,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             // codes one step ahead of their use.
             constexpr int32_t kBeyond = INT32_MIN;
             auto id_of = [&](int i, int h) {
-                const int64_t p = 2 * (int64_t)i + h;
+                const int64_t p = 2 * ((int64_t)it.from + i) + h;
                 return p * kPage < top ? __ldg(table + p) : kBeyond;
             };
             auto head_of_page = [&](int32_t id) -> const uint8_t* {
@@ -433,7 +439,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                         if (v == 1 && i >= masked) {
                             // tokens that no row sees become zeros; a NaN joins the rows that see it in the end
                             const int block = ct / S::kPart + e * kDims;
-                            const int seen = top - i * kKeys - block * kBlock;
+                            const int seen = top - (it.from + i) * kKeys - block * kBlock;
                             uint32_t* q = reinterpret_cast<uint32_t*>(&c);
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
@@ -472,7 +478,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                     const int at = (u + i) % kMeta;
                     blk->k2[at][ct] = pow2(scale_exponent(sc.x));
                     blk->ev[at][ct] = (float)scale_exponent(sc.y);
-                    if (ct == 0) blk->here[at] = (x0 ? 1u : 0u) | (x1 || (2 * (int64_t)i + 1) * kPage >= top ? 2u : 0u);
+                    if (ct == 0) blk->here[at] = (x0 ? 1u : 0u) | (x1 || (2 * ((int64_t)it.from + i) + 1) * kPage >= top ? 2u : 0u);
                 }
                 sc = scales_of(z0, z1);
                 convert(Constant<0>(), i, x0, x1, z0, z1);
@@ -516,14 +522,30 @@ static dsa_status launch_tc(const PrefillArgs& a, const CUtensorMap& q, cudaStre
     if (ensure_smem_limit(reinterpret_cast<const void*>(&kv8_prefill_kernel<D>), S::kSmem) != DSA_OK) return DSA_ERR_CUDA;
     const int64_t most = most_items(a.b.total_q, a.b.batch, a.kv_heads, a.tokens * S::kTiles);
     if (most > 0x7fff0000LL) return DSA_ERR_UNSUPPORTED;
-    const unsigned G = (unsigned)std::min<int64_t>(device_sm_count(), most);
+    const unsigned G = a.split.slots ? (unsigned)a.split.ctas : (unsigned)std::min<int64_t>(a.split.ctas, most);
     DSA_CHECK(launch_pdl(kv8_prefill_kernel<D>, dim3(G), dim3(S::kThreads), S::kSmem, s, 1, a, q));
+    if (a.split.slots) {
+        // items of the last round, at most; a block for every two rows, as long as the blocks are few
+        const unsigned x = (unsigned)std::min<int64_t>(G, most), rows = S::kTiles * 128;
+        const unsigned y = std::max(rows / 16, std::min(rows / kJoinRows, 2048 / x));
+        DSA_CHECK(launch_pdl(join_kernel<D>, dim3(x, y), dim3(kJoinRows * kJoinWarps * 32), 0, s, 1, a.split, a.group, a.kv_heads, (int)rows, a.out,
+                             a.out_f32, a.lse));
+    }
     return DSA_OK;
+}
+
+// Slots of partial outputs: two a CTA where some request may be long enough for two pieces of an item.
+static int slots(int sms, const dsa_batch* b) { return b->max_seq_len >= 2 * kMinSteps * kKeys ? 2 * sms : 0; }
+static int64_t item_rows(int dim) { return dim <= 128 ? 256 : 128; }
+
+size_t prefill_ws_bytes(int sms, const dsa_batch* b, int dim) {
+    const size_t n = slots(sms, b);
+    return n ? (n * item_rows(dim) * (dim * 4 + 8) + sms * sizeof(Cut) + 255) / 256 * 256 : 0;
 }
 
 // The requests of the batch with at least min_rows query rows.
 dsa_status launch_prefill(const dsa_heads* q, const uint8_t* cache, const dsa_batch* b, int32_t heads, int32_t kv_heads, int32_t dim,
-                          int32_t min_rows, float scale_log2, void* out, int out_f32, float* lse, int32_t* st, cudaStream_t s) {
+                          int32_t min_rows, float scale_log2, void* out, int out_f32, float* lse, void* ws, int32_t* st, cudaStream_t s) {
     PrefillArgs a = {};
     a.cache = cache;
     a.b = to_dev(b);
@@ -531,6 +553,12 @@ dsa_status launch_prefill(const dsa_heads* q, const uint8_t* cache, const dsa_ba
     a.min_rows = min_rows;
     a.scale = scale_log2;
     a.out = out, a.out_f32 = out_f32, a.lse = lse, a.st = st;
+    a.split.ctas = device_sm_count();
+    a.split.slots = slots(a.split.ctas, b);
+    const size_t rows = a.split.slots * item_rows(dim);
+    a.split.part_o = static_cast<float*>(ws);
+    a.split.part_ml = reinterpret_cast<float2*>(a.split.part_o + rows * dim);
+    a.split.cut = reinterpret_cast<Cut*>(a.split.part_ml + rows);
     CUtensorMap qm;
     if (!make_heads_map(q, dim, heads, b->total_q, (unsigned)a.group, (unsigned)a.tokens, &qm)) return DSA_ERR_CUDA;
     if (dim == 64) return launch_tc<64>(a, qm, s);

@@ -87,6 +87,7 @@ template <int D> struct Shape {
     static constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, kPart, true);
     static constexpr bool kValuesMn = true;
     // TMEM columns
+    static constexpr bool kCut = false;
     static constexpr bool kTurns = true;
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
@@ -188,7 +189,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         Ring<S> at;                                        // where the steps' values are
         Item it;
         bool ok = true;
-        for (int k = 0; ok && me.take(k, it); ++k) {
+        for (int k = 0; ok && me.take<S::kCut>(k, it); ++k) {
             const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0);
             const int all_see = it.see(it.tok0 + x * a.tokens);        // keys that all of the tile's rows see
             const int count = it.count(x, a.tokens), steps = it.steps(x, a.tokens);
@@ -229,7 +230,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                 }
                 const float top = max3(fmaxf(m[0], m[1]), m[2], m[3]) * a.scale;
                 if (i == 0) {
-                    refc = top == -INFINITY ? 0.f : top;
+                    refc = top == -INFINITY ? -1e30f : top;      // (no score so far: whatever comes is above)
                 } else if (__any_sync(0xffffffffu, top > refc + kGrow)) {
                     // O counts from a new reference
                     const float to = top > refc + kGrow ? top : refc, f = exp2f(refc - to);
@@ -321,7 +322,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             uint32_t n = 0, items[2] = {0, 0};             // stages, and items with a Q of each tile, so far
             bool ok = true;
             Item it;
-            for (int k = 0; me.take(k, it); ++k) {
+            for (int k = 0; me.take<S::kCut>(k, it); ++k) {
                 me.done_with(k);
                 const int steps[2] = {it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0};
                 const int most = max(steps[0], steps[1]);
@@ -366,12 +367,12 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             }
         } else if (warp == kItemWarp) {
             lay_out_items(
-                me, a.batch, a.kv_heads, a.tokens * S::kTiles,
+                me, a.batch, a.kv_heads, a.tokens, S::kTiles, Split{},
                 [&](int r, int& qs, int& qn) {
                     qs = a.q_start[r];
                     qn = (int)max((int64_t)0, min((int64_t)a.q_start[r + 1], a.total_q) - qs);
                 },
-                [&](int r, Item& it) {
+                [&](int r, Item& it, bool) {
                     it.k_row = a.k_start[r];
                     it.len = it.cap = (int)max((int64_t)0, min((int64_t)a.k_start[r + 1], a.total_k) - it.k_row);
                 });

@@ -282,6 +282,91 @@ def test_prefill_unseen_rows_and_lengths():
         assert bits == D.DEVERR_INDEX_RANGE
 
 
+@pytest.mark.parametrize("seq,n,kv,group,dim", [
+    ([5000], [100], 1, 8, 128),                    # few items of many steps
+    ([5000], [70], 1, 1, 64),                      # one tile of two
+    ([2047], [65], 1, 2, 256),
+    ([2048], [65], 1, 2, 256),
+    ([20000], [17], 1, 5, 64),
+    ([3000], [800], 8, 8, 128),                    # one round of items and some
+    ([4000, 300, 2500, 1024], [200, 130, 1, 90], 2, 4, 128),      # long and short ones, and some that are not cut
+    ([3000, 2100], [1300, 90], 1, 16, 256),
+    ([1500], [1500], 2, 4, 64),                    # pieces that some rows see nothing of
+])
+def test_items_cut_along_the_keys(seq, n, kv, group, dim):
+    c = cache_case(seq, n, kv, group, dim, seed=dim + len(seq), pad_rows=3)
+    want = expected(c)
+    for dtype in (D.DTYPE_F32, D.DTYPE_BF16):
+        out, lse, bits = _run(c, dtype)
+        check(out, lse, want)
+        assert bits == 0
+
+
+def test_cut_items_with_nan_and_pages_that_are_not_there():
+    c = cache_case([4000], [100], 1, 4, 128, seed=40)
+    k, v, _ = (x.view(torch.uint8) if x.dtype != torch.float32 else x for x in D.kv8_views(c["cache"], 1, 128))
+    at = 3950                                              # rows from 50 on see it
+    v[int(c["table"][0, at // 64]), 0, at % 64 // 16, 5, at % 16] = 0x7f
+    v[int(c["table"][0, 10]), 0, 2, 77, 3] = 0xff           # all rows do
+    c["table"][0, 20] = -1
+    c["table"][0, 60] = c["pages"]
+    place(c)
+    out, lse, bits = _run(c)
+    check(out, lse, expected(c))
+    assert bits == D.DEVERR_PAGE_RANGE
+    # whole pieces whose pages are not there, and whole requests
+    for gone in (slice(0, 20), slice(16, 48), slice(0, 63)):
+        c = cache_case([4000], [100], 1, 4, 128, seed=41)
+        c["table"][0, gone] = -1
+        place(c)
+        out, lse, bits = _run(c)
+        check(out, lse, expected(c))
+        assert bits == D.DEVERR_PAGE_RANGE
+
+
+@pytest.mark.parametrize("n", [3, 100])
+def test_low_scores_behind_pages_that_are_not_there(n):
+    """What a row has not seen sets no reference: the first scores that it sees may be far below 0."""
+    c = cache_case([600], [n], 1, 4, 64, seed=42)
+    k = D.kv8_views(c["cache"], 1, 64)[0]
+    k.copy_(k.float().abs().clamp(min=16).to(torch.float8_e4m3fn))
+    c["q"] = -(c["q"].abs() + 1) * 64
+    c["table"][0, :3] = -1
+    place(c)
+    want = expected(c)
+    assert want[1].max() < -104                           # exp of it is below the smallest fp32
+    out, lse, bits = _run(c, D.DTYPE_F32)
+    check(out, lse, want)
+    assert bits == D.DEVERR_PAGE_RANGE
+
+
+def test_cut_items_from_a_graph_and_on_two_streams():
+    """Calls that share a workspace one after the other, and calls with their own beside each other."""
+    c = cache_case([5000, 900], [120, 90], 1, 8, 128, seed=43)
+    want, _, _ = _run(c)
+    size = D.dsa_kv8_attention_workspace_size(c["batch"], c["heads"], c["kv"], c["dim"])
+    shared = torch.full((size,), 0xff, dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(want) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    torch.cuda.synchronize()
+    for g, out in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            D.dsa_kv8_attention(c["q"], c["dev_cache"], c["batch"], kv_heads=1, out=out, ws=shared)
+    for g in graphs * 2:
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    streams, own = [torch.cuda.Stream() for _ in range(2)], [torch.full((size,), 0xff, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, o, w in zip(streams, outs, own):
+            D.dsa_kv8_attention(c["q"], c["dev_cache"], c["batch"], kv_heads=1, out=o, ws=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def test_outputs_that_begin_at_16_bytes():
     """Outputs, their log-sums and the cache at the least alignment that the calls ask for."""
     for n in (3, 100):

@@ -134,6 +134,20 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(dim, group):
     assert np.array_equal(np.isnan(z), np.isnan(want[1]))
 
 
+def test_low_scores_behind_infinite_keys():
+    """Keys whose scores are minus infinity set no reference: the first others may be far below 0."""
+    c = _case([100], [300], 1, 4, 64, seed=42)
+    c["k"].copy_(c["k"].abs() + 1)
+    c["k"][:260, :, 0] = -float("inf")
+    c["q"].copy_(-(c["q"].abs() + 1) * 8)
+    c["q"][..., 0] = 1.0
+    want = _expected(c)
+    assert np.isfinite(want[0]).all() and want[1].max() < -104        # exp of it is below the smallest fp32
+    out, lse, bits = _run(c, D.DTYPE_F32)
+    check(out, lse, want)
+    assert bits == 0
+
+
 def test_strides_stream_graph_and_workspace():
     c = _case([200, 77], [0, 40], 2, 4, 128, seed=4)
     want = _expected(c)
