@@ -139,6 +139,29 @@ __device__ __forceinline__ void rescale_o(uint32_t o_tmem, float f) {
 // Items of a call, at most; the kernels count them in 32 bits.
 inline int64_t most_items(int64_t total_q, int batch, int kv_heads, int per) { return std::min(total_q, total_q / per + batch) * kv_heads; }
 
+// Key heads whose items are laid out together: as many as have their keys and values in half of
+// the L2, where the CTAs that work on them find them.  2 x 4096 tokens of 64 key heads of 256
+// dims (270 MB a prompt) 1039 us with all heads together, which read 2.0 GB of 0.4 from DRAM,
+// 939 in runs of 64 MB, 951 of 32, 965 of 16; 8 key heads of 128 dims on 8192 tokens (34 MB)
+// 797 in one run and 807 in runs of 16 MB.
+constexpr int64_t kRunBytes = 64 << 20;
+inline int heads_of_run(int kv_heads, int64_t bytes) { return (int)std::max<int64_t>(1, std::min<int64_t>(kv_heads, kRunBytes / std::max<int64_t>(1, bytes))); }
+
+// Which calls deal their items out as they go: those of many rounds, and those whose CTAs have
+// many steps each.  The launch that clears the count takes 2 us, and an item that is known late
+// has its first copies late.  Dealt and not, in us: 16 prompts of up to 512 tokens (14 rounds)
+// 76.4, 81.9; 2 x 4096 tokens of 256 dims (27 rounds) 939, 972; 2048 tokens over 16384 in the cache (3.4
+// rounds, 430 steps a CTA) 993, 1041; 4 x 2048 tokens of 64 dims (3.5 rounds, 55 steps) 68.8, 64.8.
+constexpr int kDealtRounds = 4, kDealtSteps = 100;
+inline bool deals(int64_t items, int64_t longest, int64_t ctas) {
+    return items > ctas && (items > kDealtRounds * ctas || items * (longest / kKeys) > kDealtSteps * ctas);
+}
+static __global__ void clear_count(uint32_t* dealt) {
+    pdl_wait();
+    pdl_trigger();
+    *dealt = 0;
+}
+
 // bf16 rows of heads as [rows, heads, dim], boxes of 64 dims x bh heads x br rows.
 bool make_heads_map(const dsa_heads* h, int dim, int64_t heads, int64_t rows, unsigned bh, unsigned br, CUtensorMap* out);
 
@@ -396,7 +419,7 @@ static_assert(kMaxPieces < 256, "pieces in a byte");
 template <class Rows>
 struct Finder {
     Rows rows;
-    int batch, kv_heads, per, lane;
+    int batch, kv_heads, run, per, lane;
     int c0 = -32;
     uint32_t base = 0, all = 0;                            // items before the 32 requests, and theirs (the host bounds them)
     uint32_t upto = 0;                                     // and of those up to the lane's
@@ -428,18 +451,22 @@ struct Finder {
         const uint32_t j = i - base - __shfl_sync(0xffffffffu, upto - (uint32_t)(blocks * kv_heads), at);
         it.q_row = __shfl_sync(0xffffffffu, qs, at);
         it.n = __shfl_sync(0xffffffffu, qn, at);
-        it.tok0 = (b - 1 - (int)(j / (uint32_t)kv_heads)) * per;
-        it.h = (int)(j % (uint32_t)kv_heads);
+        const int first = (int)(j / (uint32_t)(b * run)) * run, heads = min(run, kv_heads - first);
+        const uint32_t e = j - (uint32_t)(b * first);
+        it.tok0 = (b - 1 - (int)(e / (uint32_t)heads)) * per;
+        it.h = first + (int)(e % (uint32_t)heads);
         return c0 + at;
     }
 };
 
 // Lays out the CTA's items, of `tiles` tiles of `tokens` tokens: `rows(r, qs, qn)` gives a
 // request's first row and tokens, `keys(r, it, first)` sets an item's keys (first: it is the
-// item's first piece).  The items of a request come longest first, and go there and back
-// over the CTAs.
+// item's first piece).  The items of a request come in runs of `run` heads, longest first.  A
+// CTA's first item is its number's; the others go to the CTAs as they get there, by the count
+// `dealt` (0 at the start), or, without one, there and back over them.  What an item's outputs
+// are does not depend on who takes it.
 template <class Rows, class Keys>
-__device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_heads, int tokens, int tiles, const Split& split, Rows rows, Keys keys) {
+__device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_heads, int run, int tokens, int tiles, const Split& split, uint32_t* dealt, Rows rows, Keys keys) {
     Pipe* m = me.m;
     const int per = tokens * tiles;
     uint32_t whole = 0xffffffffu, pieces = 1;              // items before the last round; pieces of its items
@@ -449,7 +476,7 @@ __device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_
         return max(1, min((int)pieces, most / kMinSteps));
     };
     if (split.slots > 0) {
-        Finder<Rows> count{rows, batch, kv_heads, per, me.lane};
+        Finder<Rows> count{rows, batch, kv_heads, run, per, me.lane};
         while (count.next()) {}
         const uint32_t items = count.base + count.all, rest = items % gridDim.x;
         whole = items - rest;
@@ -457,7 +484,7 @@ __device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_
         // The joining kernel's list: written before any wait, so that it is there whatever else happens.
         Cut cut = {};
         if (blockIdx.x < rest) {
-            Finder<Rows> one{rows, batch, kv_heads, per, me.lane};
+            Finder<Rows> one{rows, batch, kv_heads, run, per, me.lane};
             Item it;
             const int r = one.find(whole + blockIdx.x, it);
             if (r >= 0) {
@@ -468,26 +495,36 @@ __device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_
         }
         if (me.lane == 0) split.cut[blockIdx.x] = cut;
     }
-    Finder<Rows> finder{rows, batch, kv_heads, per, me.lane};
-    for (uint32_t k = 0, turn = 0;; ++turn) {
-        const uint32_t i = turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        const uint32_t piece = i < whole ? 0 : (i - whole) % pieces;
+    Finder<Rows> finder{rows, batch, kv_heads, run, per, me.lane};
+    uint32_t turn = 0;
+    for (uint32_t k = 0;; ++k) {
+        if (k >= kItems && !me.wait_all(&m->item_empty[k % kItems], k / kItems - 1)) break;
         Item it;
-        const int r = finder.find(i < whole ? i : whole + (i - whole) / pieces, it);
-        it.from = 0, it.to = INT32_MAX, it.slot = -1;
-        if (r >= 0) {
+        int r;
+        bool nothing;
+        do {
+            uint32_t i = blockIdx.x;
+            if (turn > 0) {
+                if (dealt) i = __shfl_sync(0xffffffffu, me.lane == 0 ? gridDim.x + atomicAdd(dealt, 1u) : 0u, 0);
+                else i = turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            }
+            ++turn;
+            const uint32_t piece = i < whole ? 0 : (i - whole) % pieces;
+            r = finder.find(i < whole ? i : whole + (i - whole) / pieces, it);
+            it.from = 0, it.to = INT32_MAX, it.slot = -1;
+            nothing = false;
+            if (r < 0) break;
             keys(r, it, piece == 0);
             if (i >= whole && pieces > 1) {
                 const int n = pieces_now(it);
-                if ((int)piece >= n) continue;
+                nothing = (int)piece >= n;
                 if (n > 1) {
                     const int64_t most = max(it.all_steps(0, tokens), tiles == 2 ? it.all_steps(1, tokens) : 0);
                     it.from = (int)(most * piece / n), it.to = (int)(most * (piece + 1) / n);
                     it.slot = (int)(i - whole);
                 }
             }
-        }
-        if (k >= kItems && !me.wait_all(&m->item_empty[k % kItems], k / kItems - 1)) break;
+        } while (nothing);
         if (me.lane < kMasked * 4) m->odd[k % kItems][me.lane >> 2][me.lane & 3] = 0;
         __syncwarp();
         if (me.lane == 0) {
@@ -496,7 +533,6 @@ __device__ __forceinline__ void lay_out_items(const Role& me, int batch, int kv_
             mbar_arrive(&m->item_full[k % kItems]);
         }
         if (r < 0) break;
-        ++k;
     }
 }
 

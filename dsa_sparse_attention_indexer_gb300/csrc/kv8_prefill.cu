@@ -36,6 +36,8 @@ struct PrefillArgs {
     const uint8_t* cache;
     BatchDev b;
     int kv_heads, group, tokens;
+    int run;                    // key heads laid out together
+    uint32_t* dealt;            // items taken
     int min_rows;               // requests with fewer query rows are not this kernel's
     float scale;                // softmax scale * log2(e)
     void* out;
@@ -320,7 +322,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             if (warp - kMmaWarp < S::kTiles) issue_mmas<S>(me, warp - kMmaWarp, smem_addr(q_smem), smem_addr(ring), a.tokens);
         } else if (warp == kItemWarp) {
             lay_out_items(
-                me, b.batch, a.kv_heads, a.tokens, S::kTiles, a.split,
+                me, b.batch, a.kv_heads, a.run, a.tokens, S::kTiles, a.split, a.dealt,
                 [&](int r, int& qs, int& qn) {
                     qs = b.q_start[r];
                     qn = (int)max((int64_t)0, min((int64_t)b.q_start[r + 1], b.total_q) - qs);
@@ -517,12 +519,14 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
 }
 
 template <int D>
-static dsa_status launch_tc(const PrefillArgs& a, const CUtensorMap& q, cudaStream_t s) {
+static dsa_status launch_tc(PrefillArgs a, int64_t longest, const CUtensorMap& q, cudaStream_t s) {
     using S = TcShape<D>;
     if (ensure_smem_limit(reinterpret_cast<const void*>(&kv8_prefill_kernel<D>), S::kSmem) != DSA_OK) return DSA_ERR_CUDA;
     const int64_t most = most_items(a.b.total_q, a.b.batch, a.kv_heads, a.tokens * S::kTiles);
     if (most > 0x7fff0000LL) return DSA_ERR_UNSUPPORTED;
     const unsigned G = a.split.slots ? (unsigned)a.split.ctas : (unsigned)std::min<int64_t>(a.split.ctas, most);
+    if (!deals(most, longest, G)) a.dealt = nullptr;
+    else DSA_CHECK(launch_pdl(clear_count, dim3(1), dim3(1), 0, s, 1, a.dealt));
     DSA_CHECK(launch_pdl(kv8_prefill_kernel<D>, dim3(G), dim3(S::kThreads), S::kSmem, s, 1, a, q));
     if (a.split.slots) {
         // items of the last round, at most; a block for every two rows, as long as the blocks are few
@@ -540,7 +544,7 @@ static int64_t item_rows(int dim) { return dim <= 128 ? 256 : 128; }
 
 size_t prefill_ws_bytes(int sms, const dsa_batch* b, int dim) {
     const size_t n = slots(sms, b);
-    return n ? (n * item_rows(dim) * (dim * 4 + 8) + sms * sizeof(Cut) + 255) / 256 * 256 : 0;
+    return (n * item_rows(dim) * (dim * 4 + 8) + sms * sizeof(Cut) + sizeof(uint32_t) + 255) / 256 * 256;
 }
 
 // The requests of the batch with at least min_rows query rows.
@@ -550,6 +554,7 @@ dsa_status launch_prefill(const dsa_heads* q, const uint8_t* cache, const dsa_ba
     a.cache = cache;
     a.b = to_dev(b);
     a.kv_heads = kv_heads, a.group = heads / kv_heads, a.tokens = 128 / a.group;
+    a.run = heads_of_run(kv_heads, b->max_seq_len * (int64_t)dim * 2);
     a.min_rows = min_rows;
     a.scale = scale_log2;
     a.out = out, a.out_f32 = out_f32, a.lse = lse, a.st = st;
@@ -559,11 +564,12 @@ dsa_status launch_prefill(const dsa_heads* q, const uint8_t* cache, const dsa_ba
     a.split.part_o = static_cast<float*>(ws);
     a.split.part_ml = reinterpret_cast<float2*>(a.split.part_o + rows * dim);
     a.split.cut = reinterpret_cast<Cut*>(a.split.part_ml + rows);
+    a.dealt = reinterpret_cast<uint32_t*>(a.split.cut + a.split.ctas);
     CUtensorMap qm;
     if (!make_heads_map(q, dim, heads, b->total_q, (unsigned)a.group, (unsigned)a.tokens, &qm)) return DSA_ERR_CUDA;
-    if (dim == 64) return launch_tc<64>(a, qm, s);
-    if (dim == 128) return launch_tc<128>(a, qm, s);
-    return launch_tc<256>(a, qm, s);
+    if (dim == 64) return launch_tc<64>(a, b->max_seq_len, qm, s);
+    if (dim == 128) return launch_tc<128>(a, b->max_seq_len, qm, s);
+    return launch_tc<256>(a, b->max_seq_len, qm, s);
 }
 
 }  // namespace kv8

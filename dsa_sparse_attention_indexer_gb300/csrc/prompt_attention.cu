@@ -59,6 +59,8 @@ struct Args {
     const int32_t *q_start, *k_start;
     int64_t total_q, total_k;
     int batch, kv_heads, group;
+    int run;                    // key heads laid out together
+    uint32_t* dealt;            // items taken
     int tokens;                 // of a tile: 128 / group
     float scale;                // softmax scale * log2(e)
     void* out;
@@ -367,7 +369,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             }
         } else if (warp == kItemWarp) {
             lay_out_items(
-                me, a.batch, a.kv_heads, a.tokens, S::kTiles, Split{},
+                me, a.batch, a.kv_heads, a.run, a.tokens, S::kTiles, Split{}, a.dealt,
                 [&](int r, int& qs, int& qn) {
                     qs = a.q_start[r];
                     qn = (int)max((int64_t)0, min((int64_t)a.q_start[r + 1], a.total_q) - qs);
@@ -384,12 +386,14 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
 }
 
 template <int D>
-static dsa_status launch(const Args& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+static dsa_status launch(Args a, int64_t longest, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
     using S = Shape<D>;
     if (ensure_smem_limit(reinterpret_cast<const void*>(&prompt_kernel<D>), S::kSmem) != DSA_OK) return DSA_ERR_CUDA;
     const int64_t most = most_items(a.total_q, a.batch, a.kv_heads, a.tokens * S::kTiles);
     if (most > 0x7fff0000LL) return DSA_ERR_UNSUPPORTED;
     const unsigned G = (unsigned)std::min<int64_t>(device_sm_count(), most);
+    if (!deals(most, longest, G)) a.dealt = nullptr;
+    else DSA_CHECK(launch_pdl(clear_count, dim3(1), dim3(1), 0, s, 1, a.dealt));
     DSA_CHECK(launch_pdl(prompt_kernel<D>, dim3(G), dim3(S::kThreads), S::kSmem, s, 1, a, q, k, v));
     return DSA_OK;
 }
@@ -448,10 +452,12 @@ extern "C" dsa_status dsa_prompt_attention(const dsa_heads* q, const dsa_heads* 
     a.batch = b->batch;
     a.kv_heads = kv_heads, a.group = heads / kv_heads;
     a.tokens = 128 / a.group;
+    a.run = gtc::heads_of_run(kv_heads, (int64_t)b->max_k_len * head_dim * 4);
     a.scale = softmax_scale * 1.44269504088896341f;
     a.out = out;
     a.out_f32 = out_dtype == DSA_DTYPE_F32;
     a.lse = lse;
+    a.dealt = static_cast<uint32_t*>(ws);
     a.wait_ns = wait_limit_ns();
     a.st = dev_status;
     CUtensorMap qm, km, vm;
@@ -460,7 +466,7 @@ extern "C" dsa_status dsa_prompt_attention(const dsa_heads* q, const dsa_heads* 
         !gtc::make_heads_map(kk, head_dim, kv_heads, rows, 1, gtc::kKeys, &km) || !gtc::make_heads_map(vv, head_dim, kv_heads, rows, 1, gtc::kKeys, &vm))
         return DSA_ERR_CUDA;
     const cudaStream_t s = as_stream(stream);
-    if (head_dim == 64) return prompt::launch<64>(a, qm, km, vm, s);
-    if (head_dim == 128) return prompt::launch<128>(a, qm, km, vm, s);
-    return prompt::launch<256>(a, qm, km, vm, s);
+    if (head_dim == 64) return prompt::launch<64>(a, b->max_k_len, qm, km, vm, s);
+    if (head_dim == 128) return prompt::launch<128>(a, b->max_k_len, qm, km, vm, s);
+    return prompt::launch<256>(a, b->max_k_len, qm, km, vm, s);
 }

@@ -302,6 +302,26 @@ def test_items_cut_along_the_keys(seq, n, kv, group, dim):
         assert bits == 0
 
 
+@pytest.mark.parametrize("pages,dim", [(4000, 64), (2000, 128), (4096, 128), (1000, 256)])
+def test_runs_of_heads_and_items_dealt_out(pages, dim):
+    """A wide page table lays the heads out in runs, the last one shorter, and has the items dealt out as the CTAs get there."""
+    c = cache_case([900, 2300, 100, 40], [700, 200, 90, 1], 7, 2, dim, seed=dim, pad_rows=2, max_pages=pages)
+    want = expected(c)
+    ws = torch.full((D.dsa_kv8_attention_workspace_size(c["batch"], c["heads"], 7, dim),), 0xff, dtype=torch.uint8, device=DEV)
+    out, lse, bits = _run(c, ws=ws)
+    check(out, lse, want)
+    assert bits == 0
+    again = torch.zeros_like(out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        D.dsa_kv8_attention(c["q"], c["dev_cache"], c["batch"], kv_heads=7, out=again, ws=ws)
+    for _ in range(3):
+        again.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again[:c["T"]], out[:c["T"]])
+
+
 def test_cut_items_with_nan_and_pages_that_are_not_there():
     c = cache_case([4000], [100], 1, 4, 128, seed=40)
     k, v, _ = (x.view(torch.uint8) if x.dtype != torch.float32 else x for x in D.kv8_views(c["cache"], 1, 128))

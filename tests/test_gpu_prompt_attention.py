@@ -134,6 +134,31 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(dim, group):
     assert np.array_equal(np.isnan(z), np.isnan(want[1]))
 
 
+@pytest.mark.parametrize("bound,dim", [(100_000, 64), (200_000, 64), (60_000, 128), (40_000, 256)])
+def test_runs_of_heads_and_items_dealt_out(bound, dim):
+    """A large bound on the keys lays the heads out in runs of one or two, the last one shorter, and has the items dealt out
+    as the CTAs get there: the same from a workspace of any content, replayed from a graph, and without it."""
+    c = _case([700, 300, 1, 90], [5, 400, 0, 0], 7, 2, dim, seed=dim, pad=2)
+    want = _expected(c)
+    plain, _, _ = _run(c)
+    check(*_run(c)[:2], want)
+    b = c["batch"]
+    c["batch"] = D.PromptBatch(b.q_start, b.k_start, max_q_len=b.c.max_q_len, max_k_len=bound, total_q=b.total_q, total_k=b.total_k)
+    ws = torch.full((max(256, D.dsa_prompt_attention_workspace_size(c["batch"], c["heads"], 7, dim)),), 0xff, dtype=torch.uint8, device=DEV)
+    out, lse, bits = _run(c, ws=ws)
+    check(out, lse, want)
+    assert bits == 0 and torch.equal(out[:c["T"]], plain[:c["T"]])
+    again = torch.zeros_like(out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        D.dsa_prompt_attention(c["q"], c["k"], c["v"], c["batch"], out=again, ws=ws)
+    for _ in range(3):
+        again.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again[:c["T"]], plain[:c["T"]])
+
+
 def test_low_scores_behind_infinite_keys():
     """Keys whose scores are minus infinity set no reference: the first others may be far below 0."""
     c = _case([100], [300], 1, 4, 64, seed=42)
