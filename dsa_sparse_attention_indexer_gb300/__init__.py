@@ -324,8 +324,8 @@ def dsa_device_status_read(dev_status: torch.Tensor, stream=None):
 
 
 def dsa_debug_set_wait_limit_ns(ns: int) -> None:
-    """Testing hook: limit (ns) of the pipeline waits of the decode score and the
-    dense MLA kernel for later launches, process-wide (2e9 by default; 0 = give up at once)."""
+    """Testing hook: limit (ns) of the pipeline waits of the decode score, the dense MLA and
+    the grouped-head attention kernels for later launches, process-wide (2e9 by default; 0 = give up at once)."""
     _check("dsa_debug_set_wait_limit_ns", lib().dsa_debug_set_wait_limit_ns(int(ns)))
 
 def dsa_device_status_reset(dev_status: torch.Tensor, stream=None):

@@ -13,6 +13,10 @@
 // by side in the cache; a warp turns them over in shared memory and writes (or, where
 // the block is not all new, reads, mends and writes) them as whole 16-byte pieces.
 //
+// What bounds it: 7 x 1024 tokens of 64 + 8 + 8 heads take 62 us, 4.5 TB/s, 67 % of a copy's
+// rate: two thread blocks an SM, each loading, then computing, then storing.  One token takes
+// 4.9 us on the GPU, 128 of as many requests 6.2: a chain of loads (length, page, scale, codes).
+//
 // An angle is a whole number: f_i / 2 pi as a 64-bit fraction of a turn, times the
 // position, modulo 2^64.  That is exact to 2^-30 of a turn at any position, and takes
 // four integer products where fp64 would take twice as long (two fp64 operations a

@@ -22,6 +22,11 @@
 // reference, sum and O^T, and are joined behind the share's part of a row block; a row
 // block that several shares hold leaves one partial each, joined by a second kernel.
 //
+// Measured: 64 rows of 8 x 8 heads of 128 dims on 32768 tokens 682 us (6.3 TB/s, 93 % of a copy);
+// one row on 8192 16.7 us, two launches and a chain of loads; 16 x 6 tokens of 16 heads
+// of 256 dims on 16381 160 us (3.3 TB/s, half of a copy): the chain of 24 rows' products and their
+// softmax, 2,900 cycles a page of 33 KB, with the tensor pipe 37 % busy.
+//
 // P is held in fp16 against a reference per column and warp: a score and the exponent of
 // its block's values, such that that position's P is 2^kFirst; it is renewed, and O^T
 // rescaled, when a P passes 2^kTop.  P carries the block's 2^ev; its sum does not.
