@@ -814,19 +814,20 @@ extern "C" dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache
     a.max_rows = 0x7fffffff;
     // q's strides as a tensor map takes them; a q that does not lie so has its rows taken one by one
     const bool mapped = (heads == 1 || q->head_stride > 0) && (b->total_q == 1 || q->token_stride > 0) && q->head_stride < 1LL << 38 && q->token_stride < 1LL << 38;
-    if (longest > kv8::kTcRows && mapped) {
-        // a single request is the prefill kernel's however few of its rows there turn out to be
-        const bool all = b->batch == 1;
-        a.max_rows = kv8::kTcRows;
+    const bool prefill = longest > kv8::kTcRows && mapped;
+    // a single request is the prefill kernel's however few of its rows there turn out to be
+    const bool all = prefill && b->batch == 1;
+    if (prefill) a.max_rows = kv8::kTcRows;
+    const int64_t max_rows = std::min<int64_t>(longest, a.max_rows);
+    const int cols = kv8::columns(max_rows, head_dim);
+    // the pages of a CTA's share are counted in 32 bits
+    if (!all && (b->total_q * a.group / cols + b->batch) * kv_heads > 0x7fffffffLL * sms / (((int64_t)b->max_seq_len + kPage - 1) / kPage) / 2)
+        return DSA_ERR_UNSUPPORTED;
+    if (prefill) {
         vs = kv8::launch_prefill(q, cache, b, heads, kv_heads, head_dim, all ? 0 : kv8::kTcRows + 1, a.scale, out, a.out_f32, lse,
                                  static_cast<uint8_t*>(ws) + kv8::few_rows_ws_bytes(sms, head_dim), dev_status, s);
         if (vs != DSA_OK || all) return vs;
     }
-    const int64_t max_rows = std::min<int64_t>(longest, a.max_rows);
-    const int cols = kv8::columns(max_rows, head_dim);
-    // the pages of a CTA's share are counted in 32 bits
-    if ((b->total_q * a.group / cols + b->batch) * kv_heads > 0x7fffffffLL * sms / (((int64_t)b->max_seq_len + kPage - 1) / kPage) / 2)
-        return DSA_ERR_UNSUPPORTED;
     // no more CTAs than pages
     const int64_t blocks = std::min<int64_t>(b->total_q * a.group / cols + b->batch, b->total_q * a.group);
     const int64_t pages = ((int64_t)b->max_seq_len + kPage - 1) / kPage;

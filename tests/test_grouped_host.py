@@ -94,6 +94,8 @@ def test_kv8_attention_refusals(L):
     assert _attention(L, b=_batch(max_pages=1)) == INVALID
     assert _attention(L, b=_batch(T=0), q=N, cache=N, out=N, ws=N) == OK
     assert _attention(L, b=_batch(T=1 << 28, max_q=1 << 27), heads=128, kv=1) == UNSUPPORTED
+    # refused before either of its kernels runs
+    assert _attention(L, b=_batch(B=2, T=1 << 27, max_q=1 << 26, max_seq=0x7fffff00, max_pages=1 << 25)) == UNSUPPORTED
     n = ctypes.c_size_t(0)
     assert L.dsa_kv8_attention_workspace_size(_batch(), 16, 4, 128, ctypes.byref(n)) == OK and n.value > 0
     assert L.dsa_kv8_attention_workspace_size(_batch(), 16, 4, 128, N) == INVALID
