@@ -272,7 +272,7 @@ append_kernel(const __grid_constant__ AppendArgs a) {
             row = min(row + kBlock - held, (int64_t)b.q_start[r + 1]);
             continue;
         }
-        const int n = (int)min((int64_t)(kBlock - held), b.q_start[r + 1] - row);
+        const int n = (int)min((int64_t)(kBlock - held), min((int64_t)b.q_start[r + 1], rows) - row);
         __syncthreads();                                   // turn is complete; the last block's cosines have been read
         for (int i = tid; i < n * pairs; i += kThreads) {
             const uint64_t angle = turn[i % pairs] * (uint64_t)(p + i / pairs);

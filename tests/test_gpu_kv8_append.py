@@ -244,6 +244,21 @@ def test_append_padded_batch_and_skipped_positions():
     assert D.dsa_device_status_read(st)[0] == D.DEVERR_PAGE_RANGE | D.DEVERR_INDEX_RANGE
 
 
+def test_append_takes_no_row_behind_total_q():
+    """A total_q that ends inside a block of new tokens: what is behind it is neither read nor written."""
+    kv, dim = 2, 64
+    c = _case([70, 40], [5, 20], kv, 2, dim, seed=60)
+    got, want = c["cache"].clone(), c["cache"].clone()
+    short = D.Batch(c["batch"].seq_len, c["batch"].q_start, c["batch"].page_table, c["pages"], max_seq_len=128, max_q_len=20, total_q=15)
+    exact = D.Batch(torch.tensor([70, 30], dtype=torch.int32, device=DEV), torch.tensor([0, 5, 15], dtype=torch.int32, device=DEV),
+                    c["batch"].page_table, c["pages"], max_seq_len=128, max_q_len=10, total_q=15)
+    c["k"][15:], c["v"][15:] = 1e30, float("inf")
+    q_out = torch.full((25, c["heads"], dim), 7.0, dtype=torch.bfloat16, device=DEV)
+    D.dsa_kv8_append(c["k"], c["v"], want, exact, q=c["q"])
+    D.dsa_kv8_append(c["k"], c["v"], got, short, q=c["q"], q_out=q_out)
+    assert torch.equal(got, want) and torch.all(q_out[15:] == 7.0)
+
+
 def test_append_in_place_on_a_stream_and_in_a_graph():
     kv, dim, rope = 2, 64, 64
     c = _case([33, 90], [3, 40], kv, 3, dim)
