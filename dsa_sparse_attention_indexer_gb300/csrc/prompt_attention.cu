@@ -125,15 +125,16 @@ __device__ __noinline__ bool clean_values(const Role& me, uint8_t* ring, Place<S
             const uint4 w = *at;
             const uint4 o = make_uint4(odd2(w.x), odd2(w.y), odd2(w.z), odd2(w.w));
             if (o.x | o.y | o.z | o.w) {
-                *at = make_uint4(w.x & ~o.x, w.y & ~o.y, w.z & ~o.z, w.w & ~o.w);
+                // noted before it is taken out: the other tile's MMAs, which may see all of the step, read
+                // the stage as it is by then, and its rows join what they did not find there
                 if (masked < kMasked) atomicOr(&m->odd[k % kItems][masked][key >> 5], 1u << (key & 31));
+                m->any_odd[k % kItems] = 1;
+                __threadfence_block();
+                *at = make_uint4(w.x & ~o.x, w.y & ~o.y, w.z & ~o.z, w.w & ~o.w);
                 found = true;
             }
         }
-        if (found) {
-            fence_proxy_async_smem();
-            m->any_odd[k % kItems] = 1;
-        }
+        if (found) fence_proxy_async_smem();
     }
     __syncwarp();
     return true;
