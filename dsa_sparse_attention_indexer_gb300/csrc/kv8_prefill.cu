@@ -18,8 +18,8 @@
 // Warps: softmax as there; then a warpgroup with one warp each for a tile's MMAs, the items and
 // Q's copies; then the converters.
 //
-// What bounds it: 2048 tokens of 64 heads of 128 dims over 16384 take 994 us (1.04 PFLOP/s, 54 % of
-// a library's product).  A step of both tiles is 4,300 cycles: of them 2,048 MMAs, 2,440 a tile's
+// What bounds it: 2048 tokens of 64 heads of 128 dims over 16384 take 1017 us (1.02 PFLOP/s, 53 % of
+// a library's product).  A step of both tiles is 4,400 cycles: of them 2,048 MMAs, 2,440 a tile's
 // softmax (traced with the clock), and the converters, four warps with a stage's codes in their registers, are busy
 // for 3,700.  Without their work the kernel takes 12 % less.  (Half of them for keys and half
 // for values, each with half a stage's codes under way: 1532 us.)
@@ -55,8 +55,12 @@ struct PrefillArgs {
 
 namespace {
 
-constexpr float kNone = -1e30f;                            // reference of a row that has seen nothing so far
+constexpr float kNone = -3e38f;                            // reference of a row that has seen nothing so far: below any score
 constexpr float kFirst = 7.0f, kTop = 15.0f;               // log2 of a new reference's P, and of the largest
+// Scores (log2 units) up to here.  A score's product with its units is rounded once with the
+// reference taken off, the reference on its own: they differ by half a step of the score, 1/2
+// below 2^24, and P stays below 2^(kTop + 1/2), which fp16 holds.
+constexpr float kMostScore = 16777216.0f;
 constexpr int kMeta = 8;                                   // steps whose scales are kept: more than the ring holds
 
 template <int D> struct TcShape {
@@ -88,6 +92,7 @@ struct Block {
     uint64_t q_raw[2];          // by tile: Q has come as bf16
     alignas(16) float k2[kMeta][8];   // scales of a step's blocks' keys
     alignas(16) float ev[kMeta][8];   // exponents of their values'
+    int32_t far;                // some row's scores are beyond kMostScore
     uint32_t here[kMeta];       // bit h: the step's page h is in the cache
 };
 static_assert(sizeof(Block) <= 2048, "the block behind the ring");
@@ -132,6 +137,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             mbar_init(&pipe->item_empty[i], S::kSoft + S::kTiles + 1 + S::kConv);   // softmax, MMAs, Q's copies, converters
         }
         pipe->abort = 0;
+        blk->far = 0;
         mbar_arrive(&pipe->turn[0]);                         // the first tile begins
         fence_barrier_init();
     }
@@ -202,6 +208,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 if (lane == 0) mbar_arrive(&pipe->q_full[x]);
             }
             float ref = 0.f, sum = 0.f;                    // R, l
+            float low = 0.f;                               // the first R: they only rise
             for (int i = 0; ok && i < steps; ++i, ++t) {
                 const int s = S::kTiles == 2 ? x : t & 1;
                 ok = me.wait_all(&pipe->s_full[s], S::kTiles == 2 ? t : t >> 1);
@@ -232,7 +239,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 }
                 const float fresh = top == -INFINITY ? kNone : rintf(top) - kFirst;
                 if (i == 0) {
-                    ref = fresh;
+                    ref = low = fresh;
                 } else if (__any_sync(0xffffffffu, top > ref + kTop)) {
                     const float to = top > ref + kTop ? fresh : ref, f = exp2f(ref - to);
                     ok = me.wait_all(&pipe->o_done[x], t - 1);
@@ -240,6 +247,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                     tc_fence_after();
                     rescale_o<D>(tmem + lanes + S::o(x), f);
                     sum *= f;
+                    if (ref == kNone) low = to;
                     ref = to;
                 }
 #pragma unroll
@@ -272,6 +280,9 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 }
             }
             u0 += most;
+            // (asked here, of the first and the last reference: 1017 us; of each in the loop 1115, in the outputs'
+            // part 1023, not at all 996)
+            if (live && ref != kNone && fmaxf(fabsf(low), fabsf(ref)) > kMostScore) blk->far = 1;
             // ---- the rows' outputs
             if (ok && steps > 0) {
                 // each phase in turn, as one could be taken for the one after the next
@@ -522,6 +533,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
     }
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && blk->far) record_error(a.st, DSA_DEVERR_FP16_RANGE, 0);
     if (warp == 0) tmem_dealloc(pipe->tmem_base, 512);
 }
 

@@ -241,7 +241,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                 }
                 const float top = max3(fmaxf(m[0], m[1]), m[2], m[3]) * a.scale;
                 if (i == 0) {
-                    refc = top == -INFINITY ? -1e30f : top;      // (no score so far: whatever comes is above)
+                    refc = top == -INFINITY ? -3e38f : top;      // (no score so far: whatever comes is above)
                 } else if (__any_sync(0xffffffffu, top > refc + kGrow)) {
                     // O counts from a new reference
                     const float to = top > refc + kGrow ? top : refc, f = exp2f(refc - to);

@@ -105,7 +105,8 @@ typedef int32_t dsa_status;
                                         value with |r| >= 2^16 (clamped) or an
                                         inf / NaN in q makes an operand inexact.
                                         q itself is scaled per row by a power of
-                                        two, so any finite q is in range        */
+                                        two, so any finite q is in range.  Of
+                                        dsa_kv8_attention: scores beyond 2^23   */
 #define DSA_DEVERR_PAGE_POOL    32   /* no free page was left for a request       */
 #define DSA_DEVERR_PAGE_COUNT   64   /* a released page's count was not positive  */
 
@@ -665,7 +666,10 @@ dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, const dsa_head
  *   and rounded to fp16 (exact, but for values more than 2^39 below the row's
  *   largest), E4M3 is exact in fp16; softmax statistics and accumulation are
  *   fp32; probabilities are rounded to fp16 for the product with the values, each
- *   off by 2^-11 of itself, or by less than 2^-30 of the largest.  A NaN in a key
+ *   off by 2^-11 of itself, or by less than 2^-30 of the largest.  Scores beyond 2^23
+ *   in magnitude (each known to a whole unit only) may be recorded
+ *   (DSA_DEVERR_FP16_RANGE) by a request of several rows, whose outputs are then
+ *   undefined.  A NaN in a key
  *   or in a value that a row sees makes its outputs NaN, and no other row's.
  *   Cache rows that no row sees may hold anything.  A page id outside the cache
  *   is recorded (DSA_DEVERR_PAGE_RANGE) and its positions are not seen; a negative

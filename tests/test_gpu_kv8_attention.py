@@ -358,6 +358,35 @@ def test_low_scores_behind_pages_that_are_not_there(n):
     out, lse, bits = _run(c, D.DTYPE_F32)
     check(out, lse, want)
     assert bits == D.DEVERR_PAGE_RANGE
+    # as far below as the scale can put them: one position has all of the weight, and its log-sum is finite; or, where
+    # there are many rows, it is recorded that such scores' probabilities are not to be had
+    out, lse, bits = _run(c, D.DTYPE_F32, 1e30)
+    if bits & D.DEVERR_FP16_RANGE:
+        assert n == 100
+    else:
+        check(out, lse, expected(c, 1e30))
+        assert torch.isfinite(lse[:n]).all() and out[:n].abs().amax(2).min() > 0
+
+
+def test_the_largest_scores_of_many_rows():
+    """Scores up to 2^23 are right, and beyond 2^24 they are recorded: here of keys that differ from a row's best by 2^-4 and more of it."""
+    c = cache_case([700], [100], 1, 2, 64, seed=44)
+    k = D.kv8_views(c["cache"], 1, 64)[0]
+    k.fill_(0)
+    k[..., 0] = 1.0
+    best = k[int(c["table"][0, 500 // 64]), 0, 500 % 64 // 16, 500 % 16]
+    best[0] = 2.0
+    D.kv8_views(c["cache"], 1, 64)[2][:, :, 0] = 1.0
+    c["q"].zero_()
+    c["q"][..., 0] = 1.0
+    place(c)
+    for scale, far in ((2.0 ** 22 - 1, False), (2.0 ** 26, True)):
+        out, lse, bits = _run(c, D.DTYPE_F32, scale)
+        assert bits == (D.DEVERR_FP16_RANGE if far else 0)
+        if not far:
+            _, v, _ = O.kv8_read(c["cache"].numpy().reshape(-1), 1, 64, c["table"][0].numpy(), 700, c["pages"])
+            assert np.allclose(f64(out[:100]), v[500], rtol=2.0 ** -10, atol=0)              # P and a sum of one
+            assert np.allclose(f64(lse[:100]), 2 * scale, rtol=2.0 ** -22)
 
 
 def test_cut_items_from_a_graph_and_on_two_streams():
