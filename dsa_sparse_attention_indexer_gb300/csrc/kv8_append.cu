@@ -276,10 +276,14 @@ append_kernel(const __grid_constant__ AppendArgs a) {
         __syncthreads();                                   // turn is complete; the last block's cosines have been read
         for (int i = tid; i < n * pairs; i += kThreads) {
             const uint64_t angle = turn[i % pairs] * (uint64_t)(p + i / pairs);
-            // the top 32 bits as a signed fraction of half a turn
+            // The nearest quarter of a turn is taken off in whole numbers: what is left, at most a
+            // quarter of half a turn, keeps 2^-27 of one as fp32, where the whole angle would keep 2^-25.
+            const uint32_t quarter = (uint32_t)((angle + (1ull << 61)) >> 62);
+            const int32_t rest = (int32_t)((int64_t)(angle - ((uint64_t)quarter << 62)) >> 30);
             float s, c;
-            sincospif((float)(int32_t)(angle >> 32) * 4.656612873077393e-10f, &s, &c);
-            cs[i] = make_float2(c, s);
+            sincospif((float)rest * 1.1641532182693481e-10f, &s, &c);          // 2^-33
+            const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;       // cos(a + 90) = -sin a, sin(a + 90) = cos a
+            cs[i] = make_float2(quarter + 1 & 2 ? -x : x, quarter & 2 ? -y : y);
         }
         __syncthreads();
         uint8_t* page = nullptr;
