@@ -25,6 +25,11 @@ __device__ __forceinline__ int scale_exponent(float s) {
     return max(-kMaxExp, min(kMaxExp, (int)((__float_as_uint(s) >> 23) & 0xffu) - 127));
 }
 
+// Four codes -> their values as fp16, exactly.
+__device__ __forceinline__ void e4m3x4_h2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(four));
+}
+
 // A wait of these kernels' pipelines: within the limit, and not beyond another role's
 // timeout.  A limit of 0 takes what has happened already, and is not suspended for it.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int32_t* abort_flag, uint64_t limit_ns) {

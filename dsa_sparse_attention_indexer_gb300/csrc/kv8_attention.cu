@@ -238,10 +238,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Four codes -> their values as fp16, exactly.
-__device__ __forceinline__ void e4m3x4_h2(uint32_t four, uint32_t& lo, uint32_t& hi) {
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(four));
-}
 // The bytes of a word that are NaN codes, as 4 bits.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     const uint32_t m = __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x01010101u;

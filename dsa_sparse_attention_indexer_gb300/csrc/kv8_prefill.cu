@@ -97,9 +97,6 @@ struct Block {
 };
 static_assert(sizeof(Block) <= 2048, "the block behind the ring");
 
-__device__ __forceinline__ void codes4_h2(uint32_t four, uint32_t& lo, uint32_t& hi) {
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(four));
-}
 __device__ __forceinline__ uint32_t nan_of(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
 }  // namespace
@@ -438,7 +435,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             // Pages of this step, the next and the one after; pieces under way, of the keys and of the values
             // to be converted next, loaded again as soon as they are used; the next keys' step's scales.
             const uint8_t *h0 = nullptr, *h1 = nullptr, *n0 = nullptr, *n1 = nullptr, *m0 = nullptr, *m1 = nullptr;
-            uint4 w[2][kUnits];
+            uint4 w[2][S::kParts * kUnits];
             float2 sc = make_float2(1.f, 1.f);
             // Turns step i's keys (v = 0) or values, codes of pages x0 and x1, into their stages; the next ones
             // are z0's and z1's.
@@ -449,12 +446,10 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                     const int s = n % S::kStages;
                     if (ok && n >= S::kStages) ok = me.wait_all(&pipe->kv_empty[s], n / S::kStages - 1);
                     if (!ok) return;
-                    const bool last_part = p == S::kParts - 1;
                     const uint32_t base = smem_addr(ring + s * S::kStage);
 #pragma unroll
                     for (int e = 0; e < kUnits; ++e) {
-                        uint4 c = w[v][e];
-                        w[v][e] = last_part ? piece(z0, z1, v, 0, e) : piece(x0, x1, v, p + 1, e);
+                        uint4 c = w[v][p * kUnits + e];
                         if (v == 1 && i >= masked) {
                             // tokens that no row sees become zeros; a NaN joins the rows that see it in the end
                             const int block = ct / S::kPart + e * kDims;
@@ -477,10 +472,10 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                             }
                         }
                         uint32_t h[8];
-                        codes4_h2(c.x, h[0], h[1]);
-                        codes4_h2(c.y, h[2], h[3]);
-                        codes4_h2(c.z, h[4], h[5]);
-                        codes4_h2(c.w, h[6], h[7]);
+                        e4m3x4_h2(c.x, h[0], h[1]);
+                        e4m3x4_h2(c.y, h[2], h[3]);
+                        e4m3x4_h2(c.z, h[4], h[5]);
+                        e4m3x4_h2(c.w, h[6], h[7]);
                         const uint32_t to = base + place(v, e);
                         st_shared_v4(to, h[0], h[1], h[2], h[3]);
                         st_shared_v4(to ^ 16, h[4], h[5], h[6], h[7]);
@@ -488,6 +483,8 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&pipe->kv_full[s]);
+#pragma unroll
+                    for (int e = 0; e < kUnits; ++e) w[v][p * kUnits + e] = piece(z0, z1, v, p, e);
                     ++n;
                 }
             };
@@ -508,7 +505,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
 #pragma unroll
                 for (int v = 0; v < 2; ++v)
 #pragma unroll
-                    for (int e = 0; e < kUnits; ++e) w[v][e] = piece(h0, h1, v, 0, e);
+                    for (int e = 0; e < S::kParts * kUnits; ++e) w[v][e] = piece(h0, h1, v, e / kUnits, e % kUnits);
                 sc = scales_of(h0, h1);
                 n0 = head_of_page(j0), n1 = head_of_page(j1);
                 m0 = head_of_page(k0), m1 = head_of_page(k1);
