@@ -18,11 +18,13 @@
 // Warps: softmax as there; then a warpgroup with one warp each for a tile's MMAs, the items and
 // Q's copies; then the converters.
 //
-// What bounds it: 2048 tokens of 64 heads of 128 dims over 16384 take 1017 us (1.02 PFLOP/s, 53 % of
-// a library's product).  A step of both tiles is 4,400 cycles: of them 2,048 MMAs, 2,440 a tile's
+// What bounds it: 2048 tokens of 64 heads of 128 dims over 16384 take 990 us (1.04 PFLOP/s, 54 % of
+// a library's product).  A step of both tiles is 4,300 cycles: of them 2,048 MMAs, 2,440 a tile's
 // softmax (traced with the clock), and the converters, four warps with a stage's codes in their registers, are busy
 // for 3,700.  Without their work the kernel takes 12 % less.  (Half of them for keys and half
-// for values, each with half a stage's codes under way: 1532 us.)
+// for values: 1563 us, as registers spill and a stage is held for a whole step while it is
+// written.)  At 256 dims the converters bound it, 7,000 cycles a step: 512 rows of 32 heads over
+// 32768 take 938 us (290 TFLOP/s).
 #include <algorithm>
 
 #include "grouped_tc.cuh"
@@ -82,7 +84,7 @@ template <int D> struct TcShape {
     static constexpr uint32_t kIdQK = idesc_f16_f32(128, kKeys, false, false), kIdPV = idesc_f16_f32(128, kPart, false, false);
     static constexpr bool kValuesMn = false;
     static constexpr bool kCut = true;
-    static constexpr bool kTurns = false;                  // 994 us without, 1069 with: what the converters make comes in step
+    static constexpr bool kTurns = false;                  // 994 us without, 1069 with it: what the converters make comes in step
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
 };
@@ -277,8 +279,8 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 }
             }
             u0 += most;
-            // (asked here, of the first and the last reference: 1017 us; of each in the loop 1115, in the outputs'
-            // part 1023, not at all 996)
+            // (asked here, of the first and the last reference: 1017 us when not asking took 996; of each in the
+            // loop 1115, in the outputs' part 1023)
             if (live && ref != kNone && fmaxf(fabsf(low), fabsf(ref)) > kMostScore) blk->far = 1;
             // ---- the rows' outputs
             if (ok && steps > 0) {
