@@ -23,8 +23,8 @@
 // softmax (traced with the clock), and the converters, four warps with a stage's codes in their registers, are busy
 // for 3,700.  Without their work the kernel takes 12 % less.  (Half of them for keys and half
 // for values: 1563 us, as registers spill and a stage is held for a whole step while it is
-// written.)  At 256 dims the converters bound it, 7,000 cycles a step: 512 rows of 32 heads over
-// 32768 take 938 us (290 TFLOP/s).
+// written.)  At 256 dims the converters bound it, 6,600 cycles a step: 512 rows of 32 heads over
+// 32768 take 887 us (614 TFLOP/s; 936 with 104 registers a converter, which spill).
 #include <algorithm>
 
 #include "grouped_tc.cuh"
@@ -72,7 +72,7 @@ template <int D> struct TcShape {
     static constexpr int kConv = D <= 128 ? 4 : 8;         // converter warps
     static constexpr int kConv0 = kSoft + 4;               // the first of them
     static constexpr int kThreads = 512;
-    static constexpr int kSoftRegs = kTiles == 2 ? 184 : 232, kMmaRegs = 40, kConvRegs = 104;
+    static constexpr int kSoftRegs = kTiles == 2 ? 184 : 232, kMmaRegs = 40, kConvRegs = kTiles == 2 ? 104 : 120;
     static_assert(kSoft * 32 * kSoftRegs + 128 * kMmaRegs + kConv * 32 * kConvRegs <= kThreads * 128, "more registers than the launch holds");
     static_assert(kSoftRegs >= 128 && kMmaRegs <= 128 && kConvRegs <= 128, "who takes and who gives");
     static constexpr int kPart = D < 128 ? D : 128;

@@ -27,9 +27,9 @@
 // part.  1 x 8192 tokens of 64 heads of 128 dims take 787 to 802 us (1.38 PFLOP/s, 72 % of a
 // library's product), a step of both tiles about 3,300 cycles of which 2,048 are MMAs
 // (tensor pipe 57 % busy).  At 256 dims there is one tile, whose softmax and MMAs follow one
-// another but for S of the next step; 2 x 4096 tokens of 64 heads 939 to 953 us (1.09 PFLOP/s).
+// another but for S of the next step; 2 x 4096 tokens of 64 heads 939 to 966 us (1.07 PFLOP/s).
 // Short prompts are bound by an item's two ends, about 4,000 cycles: 16 of up to 512 tokens
-// 76 us, one of 129 9.6 on the GPU.
+// 76 to 79 us, one of 129 9.6 on the GPU.
 #include <algorithm>
 
 #include <cudaTypedefs.h>
