@@ -30,6 +30,15 @@ __device__ __forceinline__ void e4m3x4_h2(uint32_t four, uint32_t& lo, uint32_t&
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
+// The power of two by which a row of q becomes fp16: it puts its largest |q| (`top`, bf16 bits of a finite
+// number) in [2^14, 2^15), or a number below 2^-112 as near to that as 2^126 takes it.
+__device__ __forceinline__ int q_exponent(uint32_t top) { return top ? min(126, 14 - ((int)(top >> 7) - 127)) : 0; }
+// Log2 units of a score of such a row, neither 0 nor infinite, as scores of -inf and differences of 0 are
+// multiplied by them.  A score without its units is below 2^56, so with 2^-102 or less it is nothing beside 1;
+// two of them differ by 2^-57 or not at all, so with 2^100 or more a row's best has all of the weight.
+// `most`: what the caller's products allow.
+__device__ __forceinline__ float q_units(float scale, int e, float most) { return fminf(fmaxf(scale * pow2(-e), 0x1p-102f), most); }
+
 // A wait of these kernels' pipelines: within the limit, and not beyond another role's
 // timeout.  A limit of 0 takes what has happened already, and is not suspended for it.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int32_t* abort_flag, uint64_t limit_ns) {

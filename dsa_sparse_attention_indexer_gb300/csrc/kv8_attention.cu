@@ -370,7 +370,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
                 for (int j = 0; j < 4; ++j) top = max(top, m[j] < 0x7f80u ? m[j] : 0u);
             }
             top = __reduce_max_sync(0xffffffffu, top);
-            const int e = max(-100, min(100, top ? 14 - ((int)(top >> 7) - 127) : 0));
+            const int e = q_exponent(top);
             const float up = pow2(e);
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
@@ -380,7 +380,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
                     qf[((col >> 3) * KS + ks) * 32 + to] = make_uint2(bf16x2_scaled_to_h2(w[i].x, up), bf16x2_scaled_to_h2(w[i].y, up));
                 }
             }
-            if (lane == 0) misc->c[col] = a.scale * pow2(-e);
+            if (lane == 0) misc->c[col] = q_units(a.scale, e, 0x1.fffffep127f);
         }
         bar_sync<kConsBar, kConsumers * 32>();
         uint2 qr[S::kQRegs ? NB * KS : 1];

@@ -190,9 +190,9 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                             if (hi < 0x7f80u) top = max(top, hi);
                         }
                     }
-                    const int e = max(-100, min(100, top ? 14 - ((int)(top >> 7) - 127) : 0));
+                    const int e = q_exponent(top);
                     const float up = pow2(e);
-                    c = a.scale * pow2(-e);
+                    c = q_units(a.scale, e, 0x1p100f);     // times a key's scale, up to 2^24, it is finite
 #pragma unroll 4
                     for (int j = 0; j < D / 8; ++j) {
                         uint4* p = reinterpret_cast<uint4*>(mine + j / 8 * kBox + ((j ^ row) & 7) * 16);
