@@ -31,7 +31,8 @@ struct Item {
     __device__ __forceinline__ int count(int x, int tokens) const { return max(0, min(tokens, n - tok0 - x * tokens)); }
     __device__ __forceinline__ int all_steps(int x, int tokens) const {
         const int c = count(x, tokens);
-        return c ? (see(tok0 + x * tokens + c - 1) + kKeys - 1) / kKeys : 0;
+        const int last = c ? see(tok0 + x * tokens + c - 1) : 0;
+        return last / kKeys + (last % kKeys != 0);         // (rounding up first would pass 2^31 with the longest contexts)
     }
     __device__ __forceinline__ int steps(int x, int tokens) const { return max(0, min(all_steps(x, tokens), to) - from); }
     // the first step that some row of the item sees in part or not at all, counted from the piece's first

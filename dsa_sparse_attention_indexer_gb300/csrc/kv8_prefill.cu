@@ -312,7 +312,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                         if (odd) {
                             // NaN values of masked steps that this row sees
                             for (int e = 0; e < kMasked * kKeys; ++e) {
-                                const int key = (it.from + it.masked_from()) * kKeys + e;
+                                const int64_t key = ((int64_t)it.from + it.masked_from()) * kKeys + e;
                                 if (!(pipe->odd[k % kItems][e / kKeys][e % kKeys / 32] >> (e & 31) & 1) || key >= see) continue;
                                 const int64_t page = b.page_table[(int64_t)it.k_row * b.max_pages + key / kPage];
                                 const uint8_t* v = a.cache + (page * a.kv_heads + it.h) * head_bytes(D) + v_at(D) + key % kPage / kBlock * (kBlock * D) +

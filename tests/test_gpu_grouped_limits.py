@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import dsa_sparse_attention_indexer_gb300 as D
-from tests.grouped import DEV, cache_case, check, expected, f64
+from oracle import dsa_oracle as O
+from tests.grouped import DEV, bounds, cache_case, check, expected, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,40 @@ def test_scores_beyond_all_range():
         want = expected(c, 1e30)
         err = np.abs(f64(out) - want[0])
         assert np.all(err <= 2.0 ** -11 * np.abs(want[0]) + 2.0 ** -22 * np.abs(want[0]))
+
+
+def _long_context(L, n, group, dim, seed):
+    """A context of L tokens: its last two pages are their own, all others are one page whose scores lie so far below (by 250
+    of a logarithm and more) that their probabilities, 2^31 of them together, are below 2^-300 of the others'.  Places of the
+    last page behind the context hold keys that outdo all others."""
+    width = (L + 63) // 64
+    c = cache_case([192], [n], 1, group, dim, seed=seed)
+    c["q"][..., 0] = 8.0
+    k, v, s = D.kv8_views(c["cache"], 1, dim)
+    first, own = int(c["table"][0, 0]), [int(x) for x in c["table"][0, 1:3]]
+    k[first] = 0
+    k[first, ..., 0] = -256.0
+    s[first, :, 0] = dim ** 0.5 / 8                        # a score of -256 / sqrt(dim) * sqrt(dim)
+    for pg in own:
+        k[pg, ..., 0] = 0
+    left = L - (width - 1) * 64
+    for t in range(left, 64):
+        k[own[1], 0, t // 16, t % 16] = 0
+        k[own[1], 0, t // 16, t % 16, 0] = 448.0
+        v[own[1], 0, t // 16, :, t % 16] = 448.0
+    c["dev_cache"] = c["cache"].to(DEV)
+    table = torch.full((1, width), first, dtype=torch.int32, device=DEV)
+    table[0, -2:] = torch.tensor(own, dtype=torch.int32, device=DEV)
+    c["batch"] = D.Batch(torch.tensor([L], dtype=torch.int32, device=DEV), torch.tensor([0, n], dtype=torch.int32, device=DEV), table, c["pages"],
+                         max_seq_len=L, max_q_len=n, total_q=n)
+    behind = 64 + left                                     # tokens of the two pages
+    kk, vv, ok = O.kv8_read(c["cache"].numpy().reshape(-1), 1, dim, np.array(own), behind, c["pages"])
+    return c, bounds(f64(c["q"]), kk, vv, behind - n, dim ** -0.5, 2.0 ** -11, ok)
+
+
+@pytest.mark.parametrize("L", [2 ** 31 - 1, 2 ** 31 - 127])
+def test_many_rows_of_the_longest_contexts(L):
+    c, want = _long_context(L, 9, 8, 64, 1)
+    out, lse, bits = _attention(c)
+    check(out, lse, want)
+    assert bits == 0
