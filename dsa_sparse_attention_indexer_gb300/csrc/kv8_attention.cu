@@ -390,7 +390,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
         }
         float o[NB][D / 16][4];                            // O^T: dims 16 i + g and + 8, columns 8 nb + 2 t and + 1
         float ref[NB][2], ex[NB][2], sum[NB][2], c[NB][2];
-        int32_t see[NB][2];                                // positions that the column sees
+        uint32_t see[NB][2];                               // positions that the column sees
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -405,10 +405,10 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
                 c[nb][j] = misc->c[col0 + 8 * nb + 2 * t + j];
                 int tok, hd;
                 q_row(col0 + 8 * nb + 2 * t + j, tok, hd);
-                see[nb][j] = k.w.prefix + tok + 1;
+                see[nb][j] = (uint32_t)max((int64_t)0, (int64_t)k.w.prefix + tok + 1);
             }
         }
-        const int32_t all_see = k.w.prefix + k.rb * COLS / a.group + 1;           // positions that every row of the block sees
+        const uint32_t all_see = (uint32_t)max((int64_t)0, (int64_t)k.w.prefix + k.rb * COLS / a.group + 1);      // positions that every row of the block sees
 
         // with one half of columns, odd pages of the share are warps 4-7's
         for (int64_t p = k.page + (GR == 1 ? (warp >> 2 ^ n) & 1 : 0); p < k.end; p += 3 - GR) {
@@ -420,7 +420,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
             }
             ok = __all_sync(0xffffffffu, ok);
             if (ok && misc->valid[s] && p * kPage + blk * kBlock < k.top) {
-                const int32_t pos = (int32_t)p * kPage + blk * kBlock;      // of the block's first token; below seq_len
+                const uint32_t pos = (uint32_t)p * kPage + blk * kBlock;    // of the block's first token; below seq_len (the block's last may not fit 31 bits)
                 const uint8_t* head = ring + s * S::kHead;
                 const float* scales = reinterpret_cast<const float*>(head + scale_at(D));
                 const float k2 = pow2(scale_exponent(scales[blk]));
@@ -453,7 +453,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
                 }
                 // ---- P^T: positions pos + tok0 (elements 0, 1) and + 2 (elements 2, 3)
                 const bool masked = pos + kBlock > all_see;
-                const int32_t at = pos + tok0;
+                const uint32_t at = pos + tok0;
                 bool outgrown = false;
                 float x[NB][4];
 #pragma unroll
@@ -542,7 +542,7 @@ kv8_attention_kernel(const __grid_constant__ Args a) {
                             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    const int32_t u = see[nb][j] - pos;             // the column's tokens of the block
+                                    const int64_t u = (int64_t)see[nb][j] - pos;    // the column's tokens of the block
                                     const uint32_t mine = u <= 0 ? 0u : u >= 16 ? 0xffffu : (1u << u) - 1;
                                     if (nan & mine) o[nb][i][2 * e + j] = __int_as_float(0x7fc00000);
                                 }

@@ -96,3 +96,11 @@ def test_many_rows_of_the_longest_contexts(L):
     out, lse, bits = _attention(c)
     check(out, lse, want)
     assert bits == 0
+
+
+@pytest.mark.parametrize("L,n", [(2 ** 31 - 1, 1), (2 ** 31 - 10, 1), (2 ** 31 - 3, 6)])
+def test_few_rows_of_the_longest_contexts(L, n):
+    c, want = _long_context(L, n, 8, 64, 2)
+    out, lse, bits = _attention(c)
+    check(out, lse, want)
+    assert bits == 0
