@@ -394,17 +394,17 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             const int top = it.see(last);                  // keys that some row of the item sees
             const bool tells = it.h == 0 && last == it.n - 1 && ct == 0;       // one item of a request records its pages
             const int32_t* table = b.page_table + (int64_t)it.k_row * b.max_pages;
-            // Page h of step i: its id as the table has it, kBeyond behind what the item sees; then its
+            // Page h of step i: its id as the table has it, -1 behind what the item sees; then its
             // part of the head, NULL where there is none.  Ids are loaded three steps ahead, scales and
             // codes one step ahead of their use.
-            constexpr int32_t kBeyond = INT32_MIN;
+            auto page_at = [&](int i, int h) { return 2 * ((int64_t)it.from + i) + h; };
             auto id_of = [&](int i, int h) {
-                const int64_t p = 2 * ((int64_t)it.from + i) + h;
-                return p * kPage < top ? __ldg(table + p) : kBeyond;
+                const int64_t p = page_at(i, h);
+                return p * kPage < top ? __ldg(table + p) : -1;
             };
-            auto head_of_page = [&](int32_t id) -> const uint8_t* {
+            auto head_of_page = [&](int32_t id, int i, int h) -> const uint8_t* {
                 if (id >= 0 && id < b.num_pages) return a.cache + ((int64_t)id * a.kv_heads + it.h) * head_bytes(D);
-                if (id != kBeyond && tells) record_error(a.st, DSA_DEVERR_PAGE_RANGE, id);
+                if (tells && page_at(i, h) * kPage < top) record_error(a.st, DSA_DEVERR_PAGE_RANGE, id);
                 return nullptr;
             };
             // Piece e of part p of a step's keys (v = 0): 16 dims of a token, or values: a block's 16 tokens of
@@ -503,14 +503,14 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
             };
             if (most > 0) {
                 const int32_t i0 = id_of(0, 0), i1 = id_of(0, 1), j0 = id_of(1, 0), j1 = id_of(1, 1), k0 = id_of(2, 0), k1 = id_of(2, 1);
-                h0 = head_of_page(i0), h1 = head_of_page(i1);
+                h0 = head_of_page(i0, 0, 0), h1 = head_of_page(i1, 0, 1);
 #pragma unroll
                 for (int v = 0; v < 2; ++v)
 #pragma unroll
                     for (int e = 0; e < S::kParts * kUnits; ++e) w[v][e] = piece(h0, h1, v, e / kUnits, e % kUnits);
                 sc = scales_of(h0, h1);
-                n0 = head_of_page(j0), n1 = head_of_page(j1);
-                m0 = head_of_page(k0), m1 = head_of_page(k1);
+                n0 = head_of_page(j0, 1, 0), n1 = head_of_page(j1, 1, 1);
+                m0 = head_of_page(k0, 2, 0), m1 = head_of_page(k1, 2, 1);
                 if (S::kTiles == 1) keys(0, h0, h1, n0, n1);
             }
             for (int i = 0; ok && i < most; ++i) {
@@ -520,7 +520,7 @@ kv8_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant_
                 convert(Constant<1>(), i, h0, h1, n0, n1);
                 h0 = n0, h1 = n1;
                 n0 = m0, n1 = m1;
-                m0 = head_of_page(r0), m1 = head_of_page(r1);
+                m0 = head_of_page(r0, i + 3, 0), m1 = head_of_page(r1, i + 3, 1);
                 // (8 x 96 tokens over 60,000, more than the L2 holds: 1487 us without, 1393 with; 2048 over
                 // 16384, which it holds: 984 without, 994 with)
                 if (ct == 0 && n0) prefetch_l2(n0, (uint32_t)head_bytes(D));

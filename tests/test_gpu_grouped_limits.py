@@ -7,7 +7,7 @@ import torch
 
 import dsa_sparse_attention_indexer_gb300 as D
 from oracle import dsa_oracle as O
-from tests.grouped import DEV, bounds, cache_case, check, expected, f64
+from tests.grouped import DEV, bounds, cache_case, check, expected, f64, place
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,13 @@ def test_few_rows_of_the_longest_contexts(L, n):
     out, lse, bits = _attention(c)
     check(out, lse, want)
     assert bits == 0
+
+
+def test_a_page_id_of_the_lowest_number_is_recorded():
+    for n in (1, 100):
+        c = cache_case([300], [n], 1, 4, 64, seed=62)
+        c["table"][0, 1] = -2 ** 31
+        place(c)
+        out, lse, bits = _attention(c)
+        check(out, lse, expected(c))
+        assert bits == D.DEVERR_PAGE_RANGE
