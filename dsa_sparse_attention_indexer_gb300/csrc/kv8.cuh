@@ -45,6 +45,9 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const v
     return limit_ns == 0 ? sm100::mbar_test_wait(bar, parity) : mlc::wait_ab(bar, parity, abort_flag, limit_ns);
 }
 
+// The largest softmax scale of the attention calls: log2(e) times it is finite.
+constexpr float kMostScale = 2.0e38f;
+
 // Checks that the calls on grouped heads share.
 inline dsa_status check_shape(int32_t heads, int32_t kv_heads, int32_t dim) {
     if (heads < 1 || kv_heads < 1) return DSA_ERR_INVALID_ARGUMENT;

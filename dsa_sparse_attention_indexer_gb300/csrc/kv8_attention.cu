@@ -785,7 +785,7 @@ extern "C" dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache
     vs = kv8::check_shape(heads, kv_heads, head_dim);
     if (vs != DSA_OK) return vs;
     if (out_dtype != DSA_DTYPE_BF16 && out_dtype != DSA_DTYPE_F32) return DSA_ERR_INVALID_ARGUMENT;
-    if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f) return DSA_ERR_INVALID_ARGUMENT;
+    if (!(softmax_scale > 0.f) || softmax_scale > kv8::kMostScale) return DSA_ERR_INVALID_ARGUMENT;
     if (b->total_q * (heads / kv_heads) > 0x7fffff00LL) return DSA_ERR_UNSUPPORTED;          // 32-bit query rows of a request
     if (b->total_q == 0) return DSA_OK;
     if (!q || !cache || !out || !ws) return DSA_ERR_INVALID_ARGUMENT;

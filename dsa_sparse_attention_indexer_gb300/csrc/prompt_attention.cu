@@ -440,7 +440,7 @@ extern "C" dsa_status dsa_prompt_attention(const dsa_heads* q, const dsa_heads* 
     vs = kv8::check_shape(heads, kv_heads, head_dim);
     if (vs != DSA_OK) return vs;
     if (out_dtype != DSA_DTYPE_BF16 && out_dtype != DSA_DTYPE_F32) return DSA_ERR_INVALID_ARGUMENT;
-    if (!(softmax_scale > 0.f) || softmax_scale > 2.0e38f) return DSA_ERR_INVALID_ARGUMENT;
+    if (!(softmax_scale > 0.f) || softmax_scale > kv8::kMostScale) return DSA_ERR_INVALID_ARGUMENT;
     if (b->total_q == 0) return DSA_OK;
     if (!q || !out || !ws || (b->total_k > 0 && (!k || !v))) return DSA_ERR_INVALID_ARGUMENT;
     const dsa_heads* kk = b->total_k > 0 ? k : q;           // without keys nothing is read of them

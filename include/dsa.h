@@ -675,7 +675,8 @@ dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, const dsa_head
  *   is recorded (DSA_DEVERR_PAGE_RANGE) and its positions are not seen; a negative
  *   p and positions at and above 64 * max_pages likewise (DSA_DEVERR_INDEX_RANGE).
  *   Rows at and above q_start[B] are left as they were.  total_q * heads / kv_heads
- *   above 2^31 - 256 returns DSA_ERR_UNSUPPORTED.
+ *   above 2^31 - 256 returns DSA_ERR_UNSUPPORTED, a softmax_scale that is not above 0, or
+ *   above 2e38, DSA_ERR_INVALID_ARGUMENT.
  *   q        heads heads of total_q rows, rotated
  *   out      device [T, heads, head_dim], bf16 or fp32 per out_dtype
  *   lse      device fp32 [T, heads] or NULL
@@ -710,7 +711,8 @@ dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache, const dsa
  *   lse      device fp32 [T, heads] or NULL
  *   ws       device workspace of dsa_prompt_attention_workspace_size() bytes; nothing
  *            in it has to start at zero or is kept between calls
- *   total_q and total_k above 2^31 - 256 return DSA_ERR_UNSUPPORTED.               */
+ *   total_q and total_k above 2^31 - 256 return DSA_ERR_UNSUPPORTED, a softmax_scale that
+ *   is not above 0, or above 2e38, DSA_ERR_INVALID_ARGUMENT.                        */
 typedef struct dsa_prompt {
     int32_t batch;              /* B >= 1 sequences                                 */
     int32_t max_q_len;          /* host upper bound on every q_len                  */
