@@ -110,14 +110,15 @@ __device__ __forceinline__ uint32_t odd2(uint32_t w) { return __vcmpeq2(w & 0x7f
 
 // Takes infinite and NaN values of a masked step's keys from `from` on out of its stages and
 // notes their keys; by the 128 threads of a tile, before their P says that the step's values
-// may be read.  The other tile's threads do the same, to the same end.
+// may be read.  Masked is what some row of the item does not see, whichever tile it is in, and
+// the other tile's threads do the same, to the same end: no MMA of the step reads what has not
+// been taken out, and a row gets such a value in the end whether its P was 0 or not.
 template <class S>
 __device__ __noinline__ bool clean_values(const Role& me, uint8_t* ring, Place<S> vp, int from, int masked, int k, int thread) {
     Pipe* m = me.m;
     for (int p = 0; p < S::kParts; ++p, vp.next()) {
         if (!me.wait_all(&m->kv_full[vp.stage], vp.phase)) return false;
         uint8_t* stage = ring + vp.stage * S::kStage;
-        bool found = false;
 #pragma unroll 4
         for (int e = thread; e < (kKeys - from) * (S::kPart / 8); e += 128) {  // a key's 8 pieces of 16 bytes of each 64 dims
             const int key = from + (e >> 3) % (kKeys - from), box = (e >> 3) / (kKeys - from);
@@ -125,16 +126,14 @@ __device__ __noinline__ bool clean_values(const Role& me, uint8_t* ring, Place<S
             const uint4 w = *at;
             const uint4 o = make_uint4(odd2(w.x), odd2(w.y), odd2(w.z), odd2(w.w));
             if (o.x | o.y | o.z | o.w) {
-                // noted before it is taken out: the other tile's MMAs, which may see all of the step, read
-                // the stage as it is by then, and its rows join what they did not find there
+                // (noted before it is taken out: who does not find it any more has it noted)
                 if (masked < kMasked) atomicOr(&m->odd[k % kItems][masked][key >> 5], 1u << (key & 31));
                 m->any_odd[k % kItems] = 1;
                 __threadfence_block();
                 *at = make_uint4(w.x & ~o.x, w.y & ~o.y, w.z & ~o.z, w.w & ~o.w);
-                found = true;
             }
         }
-        if (found) fence_proxy_async_smem();
+        fence_proxy_async_smem();                          // of a thread that found one taken out as well
     }
     __syncwarp();
     return true;
@@ -202,7 +201,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         bool ok = true;
         for (int k = 0; ok && me.take<S::kCut>(k, it); ++k) {
             const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0);
-            const int all_see = it.see(it.tok0 + x * a.tokens);        // keys that all of the tile's rows see
+            const int all_see = it.see(it.tok0);           // keys that all of the item's rows see
             const int count = it.count(x, a.tokens), steps = it.steps(x, a.tokens);
             const int tok = it.tok0 + x * a.tokens + tok_of;
             const bool live = tok_of < count;              // tok_of < a.tokens too

@@ -701,9 +701,11 @@ dsa_status dsa_kv8_attention(const dsa_heads* q, const uint8_t* cache, const dsa
  *   gives out = 0 and lse = -inf.  Products of bf16 are exact; softmax statistics and
  *   accumulation are fp32; probabilities are rounded to bf16 for the product with
  *   the values, each off by 2^-8 of itself.  Scores up to 2^30 in magnitude.
- *   Infinite and NaN keys and values count for the rows that see them alone.  Rows at
- *   and above q_start[B] are left as they were; rows of k and v at and above
- *   k_start[B] may hold anything.
+ *   Infinite and NaN keys and values count for the rows that see them alone; an infinite
+ *   value whose probability is below 2^-126 of the row's largest makes an output
+ *   infinite or NaN, which of the two depends on the lengths alone.  Rows at and
+ *   above q_start[B] are left as they were; rows of k and v at and above k_start[B]
+ *   may hold anything.
  *   q        heads heads of total_q rows; k, v  kv_heads heads of total_k rows, bf16;
  *            strides as in a dsa_heads, below 2^38 and, along an axis of several
  *            entries, not 0 (DSA_ERR_UNSUPPORTED)

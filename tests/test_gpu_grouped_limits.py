@@ -114,3 +114,57 @@ def test_a_page_id_of_the_lowest_number_is_recorded():
         out, lse, bits = _attention(c)
         check(out, lse, expected(c))
         assert bits == D.DEVERR_PAGE_RANGE
+
+
+def _prompt(n, kv, group, dim, seed):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(n, kv * group, dim, generator=g).to(torch.bfloat16)
+    k, v = (torch.randn(n, kv, dim, generator=g).to(torch.bfloat16) for _ in range(2))
+    q[..., 0] = 16.0
+    batch = D.PromptBatch(torch.tensor([0, n], dtype=torch.int32, device=DEV))
+
+    def call(k, v):
+        out, lse = torch.empty(n, kv * group, dim, device=DEV), torch.empty(n, kv * group, device=DEV)
+        D.dsa_prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), batch, out=out, out_dtype=D.DTYPE_F32, lse=lse)
+        torch.cuda.synchronize()
+        return out, lse
+
+    return q, k, v, call
+
+
+@pytest.mark.parametrize("n,kv,group,dim", [(256, 2, 1, 64), (256, 1, 1, 128), (64, 2, 4, 128), (128, 1, 1, 256), (40, 1, 8, 64)])
+def test_infinite_values_behind_probabilities_of_zero(n, kv, group, dim):
+    """Keys whose scores are so far below a row's best that their P is 0, with values that are not finite: rows of an item (two
+    tiles of 128 rows, one at 256 dims) get them whole where some row of it does not see the key, whichever tile each is in;
+    rows of items behind it, all of which see it, get them or a NaN."""
+    q, k, v, call = _prompt(n, kv, group, dim, 90 + dim)
+    k[5, :, 0], k[n // 2, :, 0] = -150.0, -150.0
+    v[5, 0, 3], v[n // 2, 0, dim - 1], v[5, kv - 1, 9], v[n // 2, kv - 1, 11] = float("inf"), -float("inf"), float("nan"), float("inf")
+    want = bounds(f64(q), f64(k), f64(v), 0, dim ** -0.5, 2.0 ** -8)
+    first, lse = call(k, v)
+    got, exact = f64(first), want[0].copy()
+    rest = slice(128 // group * (2 if dim <= 128 else 1), n)
+    exact[rest][np.isnan(got[rest]) & np.isinf(exact[rest])] = np.nan
+    for kind in (np.isnan, np.isposinf, np.isneginf):
+        assert np.array_equal(kind(got), kind(exact)) and kind(exact).any()
+    f = np.isfinite(exact)
+    assert np.all(np.abs(got[f] - exact[f]) <= (want[2] * (1 + 2.0 ** -24) + 2.0 ** -24 * np.abs(exact))[f])
+    assert np.all(np.abs(f64(lse) - want[1]) <= want[3])
+    for _ in range(10):
+        assert torch.equal(call(k, v)[0].view(torch.int32), first.view(torch.int32))
+
+
+def test_infinite_values_behind_probabilities_of_zero_in_long_prompts():
+    """Where rows see all of a step's keys: infinite or NaN, the same in every call, and nothing else changes."""
+    n, kv, group, dim = 1000, 2, 2, 64
+    q, k, v, call = _prompt(n, kv, group, dim, 95)
+    k[100, :, 0] = -150.0
+    plain, _ = call(k, v)
+    v[100, :, 7] = float("inf")
+    first, _ = call(k, v)
+    assert torch.equal(first[:100], plain[:100]) and not torch.isfinite(first[100:, :, 7]).any() and not torch.isneginf(first[100:, :, 7]).any()
+    first[100:, :, 7] = plain[100:, :, 7]
+    assert torch.equal(first, plain)
+    v[100, :, 7] = float("inf")
+    again = [call(k, v)[0].view(torch.int32) for _ in range(10)]
+    assert all(torch.equal(x, again[0]) for x in again)
