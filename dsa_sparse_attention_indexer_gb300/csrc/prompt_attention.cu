@@ -59,7 +59,6 @@ namespace prompt {
 using namespace sm100;
 using namespace mlc;
 using namespace gtc;
-using kv8::wait_for;
 
 struct Args {
     const uint16_t* v;          // for values that are not finite
