@@ -18,9 +18,11 @@
 // 4.9 us on the GPU, 128 of as many requests 6.2: a chain of loads (length, page, scale, codes).
 //
 // An angle is a whole number: f_i / 2 pi as a 64-bit fraction of a turn, times the
-// position, modulo 2^64.  That is exact to 2^-30 of a turn at any position, and takes
-// four integer products where fp64 would take twice as long (two fp64 operations a
-// cycle and SM).
+// position, modulo 2^64.  The fraction is formed from 106 bits of f_i / 2 pi, so that it
+// is right to 2^-63 of a turn for any f_i up to 2^32, and the angle to 2^-32 at any
+// position (an fp64 quotient's 53 bits would leave 2^-25 at position 2^31, 2^-15 with
+// f_i = 1000).  It takes four integer products where fp64 would take twice as long
+// (two fp64 operations a cycle and SM).
 #include <algorithm>
 #include <cmath>
 
@@ -39,6 +41,36 @@ constexpr int kMaxPairs = 128;
 struct Turns {
     uint64_t f[kMaxPairs];      // f_i / 2 pi in units of 2^-64 turns
 };
+
+// 1 / 2 pi as a sum of two fp64 numbers.
+constexpr double kTurnHi = 0x1.45f306dc9c883p-3, kTurnLo = -0x1.6b01ec5417056p-57;
+
+// A number of turns, less its whole ones, in units of 2^-64.
+__host__ __device__ inline uint64_t turn_fraction(double x) {
+    const double rest = x - rint(x);                        // exact, in [-1/2, 1/2]
+    return rest == 0.5 ? 1ull << 63 : (uint64_t)(int64_t)rint(rest * 18446744073709551616.0);
+}
+__host__ __device__ inline uint64_t turn_fraction(double hi, double lo) { return turn_fraction(hi) + turn_fraction(lo); }
+
+// x y, x and y sums of two fp64 numbers, to 2^-103 of itself.
+struct Two { double hi, lo; };
+inline Two times(Two x, Two y) {
+    const double p = x.hi * y.hi, e = std::fma(x.hi, y.hi, -p) + std::fma(x.hi, y.lo, x.lo * y.hi);
+    const double hi = p + e;
+    return {hi, e - (hi - p)};
+}
+// f_i = base^(-2i / dims) = q^i with q^(dims / 2) = 1 / base: q is fp64's power and one step of
+// Newton's method, q + q (1 - base q^n) / n, whose error is the square of fp64's.
+inline void turns_of_base(double base, int dims, uint64_t* f) {
+    const int n = dims / 2;
+    const double q0 = std::pow(base, -1.0 / n);
+    Two power = {base, 0.0};
+    for (int i = 0; i < n; ++i) power = times(power, Two{q0, 0.0});
+    const double step = q0 * ((1.0 - power.hi) - power.lo) / n;
+    const Two q = {q0 + step, step - ((q0 + step) - q0)};
+    Two x = {kTurnHi, kTurnLo};
+    for (int i = 0; i < n; ++i, x = times(x, q)) f[i] = turn_fraction(x.hi, x.lo);
+}
 
 struct AppendArgs {
     const uint16_t *k, *v, *q;
@@ -254,11 +286,10 @@ append_kernel(const __grid_constant__ AppendArgs a) {
     const int64_t begin = (int64_t)blockIdx.x * a.rows_per, end = min(begin + a.rows_per, rows);
     if (begin >= end) return;
     for (int i = tid; i < pairs; i += kThreads) {
-        // 2^64 f / 2 pi; an inverse frequency above 1 turns by its fraction alone
         uint64_t f = a.turns.f[i];
         if (a.inv_freq) {
-            const double x = (double)a.inv_freq[i] * 0.15915494309189535;
-            f = (uint64_t)((x - floor(x)) * 18446744073709551616.0);
+            const double x = a.inv_freq[i], hi = x * kTurnHi;
+            f = turn_fraction(hi, fma(x, kTurnLo, fma(x, kTurnHi, -hi)));
         }
         turn[i] = f;
     }
@@ -382,10 +413,7 @@ extern "C" dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, con
         // the last rotation's frequencies, by host thread: forming them takes longer than the rest of the call
         static thread_local struct { int32_t dims = -1; float base = 0.f; kv8::Turns turns; } last;
         if (last.dims != rope_dims || last.base != rope_base) {
-            for (int i = 0; i < rope_dims / 2; ++i) {
-                const double x = std::pow((double)rope_base, -2.0 * i / rope_dims) * 0.15915494309189535;
-                last.turns.f[i] = (uint64_t)((x - std::floor(x)) * 18446744073709551616.0);
-            }
+            kv8::turns_of_base(rope_base, rope_dims, last.turns.f);
             last.dims = rope_dims, last.base = rope_base;
         }
         a.turns = last.turns;

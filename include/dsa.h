@@ -628,7 +628,8 @@ typedef struct dsa_heads {
 /* dsa_kv8_append: the batch's new tokens (row t of request r is position
  *   p = seq_len - q_len + t) enter the cache.  Dims [0, rope_dims) of keys and
  *   queries are rotated: pair i by the angle p * f_i, f_i = inv_freq[i] or
- *   rope_base^(-2i / rope_dims); the angle is reduced exactly, products are fp32.
+ *   rope_base^(-2i / rope_dims), up to 2^32 in magnitude; the angle is reduced to
+ *   within 2^-32 of a turn at any position, products are fp32.
  *   Keys and values of a block and head are then rounded to E4M3 (nearest even,
  *   from fp32) with the smallest scale, e >= -24, that holds the largest of the
  *   call's new values, |x| <= 448 * 2^e, and is no smaller than the scale that

@@ -1,6 +1,8 @@
 """The calls on grouped heads at the ends of what they take.  Bounds are those of tests/grouped.py; where a test needs
 another it is derived beside it."""
 
+from decimal import Decimal, getcontext
+
 import numpy as np
 import pytest
 import torch
@@ -168,3 +170,45 @@ def test_infinite_values_behind_probabilities_of_zero_in_long_prompts():
     v[100, :, 7] = float("inf")
     again = [call(k, v)[0].view(torch.int32) for _ in range(10)]
     assert all(torch.equal(x, again[0]) for x in again)
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+def _turned(x, positions, freqs, halves):
+    """x [rows, heads, dim] with the pairs of its first 2 len(freqs) dims turned by position * freq, angles from 70 digits."""
+    getcontext().prec = 70
+    ang = np.array([[float(Decimal(int(p)) * f / (2 * PI) % 1 * 2 * PI) for f in freqs] for p in positions])[:, None]
+    n = len(freqs)
+    i = np.arange(n)
+    a, b = (i, i + n) if halves else (2 * i, 2 * i + 1)
+    y, size = x.copy(), np.abs(x)
+    y[..., a], y[..., b] = x[..., a] * np.cos(ang) - x[..., b] * np.sin(ang), x[..., a] * np.sin(ang) + x[..., b] * np.cos(ang)
+    size[..., a] = size[..., b] = np.abs(x[..., a]) + np.abs(x[..., b])
+    return y, size
+
+
+@pytest.mark.parametrize("given,halves", [(True, True), (True, False), (False, True)])
+def test_angles_at_the_farthest_positions(given, halves):
+    """Positions up to 2^31 - 2, frequencies far above 1 (given, or of a base below 1).  The bound is that of the tests of the
+    append: 2^-21 of a pair's size and half a step of bf16; an angle's turn is known to 2^-32."""
+    kv, dim, rope, n, L = 1, 64, 32, 5, 2 ** 31 - 1
+    g = torch.Generator().manual_seed(80)
+    q, k, v = (torch.randn(n, h, dim, generator=g).to(torch.bfloat16).to(DEV) for h in (2, kv, kv))
+    table = torch.zeros(1, 2 ** 25, dtype=torch.int32, device=DEV)
+    batch = D.Batch(torch.tensor([L], dtype=torch.int32, device=DEV), torch.tensor([0, n], dtype=torch.int32, device=DEV), table, 1,
+                    max_seq_len=L, max_q_len=n, total_q=n)
+    cache = torch.zeros(D.kv8_page_bytes(kv, dim), dtype=torch.uint8, device=DEV)
+    if given:
+        f = torch.tensor([1000.0, 1e6, 37654321.0, 4e9, 1.5, -2.5e5, 1e-3, 0.0] * 2, dtype=torch.float32)
+        freqs, kw = [Decimal(float(x)) for x in f], dict(inv_freq=f.to(DEV))
+    else:
+        base = float(np.float32(2.0 ** -31 * 1.37))
+        freqs, kw = [Decimal(base) ** (Decimal(-2 * i) / rope) for i in range(rope // 2)], dict(rope_base=base)
+    k_out = torch.empty_like(k)
+    q_out = D.dsa_kv8_append(k, v, cache, batch, q=q, rope_dims=rope, rope_style=D.ROPE_HALVES if halves else D.ROPE_INTERLEAVED, k_out=k_out, **kw)
+    for got, x in ((q_out, q), (k_out, k)):
+        want, size = _turned(f64(x), range(L - n, L), freqs, halves)
+        off = 2.0 ** -21 * size
+        off[..., rope:] = 0
+        assert np.all(np.abs(f64(got) - want) <= 2.0 ** -8 * np.abs(want) + off * (1 + 2.0 ** -8))
