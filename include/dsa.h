@@ -640,7 +640,9 @@ typedef struct dsa_heads {
  *   Positions without a page (an entry outside the cache: DSA_DEVERR_PAGE_RANGE;
  *   below 0 or at and above 64 * max_pages: DSA_DEVERR_INDEX_RANGE) are skipped
  *   and recorded.  Bytes of positions that are not new stay as they are, but for
- *   those codes and the block's scale.  A page that gets new tokens must belong to
+ *   those codes and the block's scale: a token that is taken back later (a rejected
+ *   draft) leaves behind the scale that it has raised and the earlier codes as they
+ *   were rounded for it.  A page that gets new tokens must belong to
  *   one request only.  q_out and k_out get the rotated rows in bf16, those
  *   of skipped positions too; rows at and above q_start[B] are left as they were.
  *   k, v     kv_heads heads of total_q rows; q heads heads or NULL
@@ -667,7 +669,10 @@ dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, const dsa_head
  *   and rounded to fp16 (exact, but for values more than 2^39 below the row's
  *   largest), E4M3 is exact in fp16; softmax statistics and accumulation are
  *   fp32; probabilities are rounded to fp16 for the product with the values, each
- *   off by 2^-11 of itself, or by less than 2^-30 of the largest.  Scores beyond 2^23
+ *   times its value's scale 2^e: with M the row's largest p_j 2^e_j, p_j 2^e_j is off
+ *   by 2^-11 of itself or, where it is small, by less than 2^-31 M.  So where blocks'
+ *   scales are more than 2^20 apart, dims that only the blocks of small scales hold are
+ *   known to 2^-22 M a position, not to a part of their own size.  Scores beyond 2^23
  *   in magnitude (each known to a whole unit only) may be recorded
  *   (DSA_DEVERR_FP16_RANGE) by a request of several rows, whose outputs are then
  *   undefined.  A NaN in a key

@@ -212,3 +212,59 @@ def test_angles_at_the_farthest_positions(given, halves):
         off = 2.0 ** -21 * size
         off[..., rope:] = 0
         assert np.all(np.abs(f64(got) - want) <= 2.0 ** -8 * np.abs(want) + off * (1 + 2.0 ** -8))
+
+
+def _bounds_by_scale(c, scale=None):
+    """Outputs and bounds per dim for blocks whose scales 2^e are far apart.  A probability is rounded to fp16 times its block's
+    2^e, against a reference among the row's largest of these products, which stands at 2^6.5 or more (2^7, or a whole number
+    next to it); fp16 rounds a number by 2^-11 of itself, or, below its normal range, by 2^-25: with M the largest p_j 2^e_j,
+    p_j 2^e_j is off by max(2^-11 of itself, 2^-31.5 M), and an output by the sum of that times its dim's codes."""
+    scale = c["dim"] ** -0.5 if scale is None else scale
+    L, n, G = c["seq"][0], c["n"][0], c["group"]
+    k, v, ok = O.kv8_read(c["cache"].numpy().reshape(-1), c["kv"], c["dim"], c["table"][0].numpy(), L, c["pages"])
+    q = f64(c["q"])
+    out, lse, W = O.grouped_attention(q, k, v, L - n, scale, ok)
+    s = D.kv8_views(c["cache"], c["kv"], c["dim"])[2].double().numpy()
+    e = np.stack([s[c["table"][0, j // 64], :, 1, j % 64 // 16] for j in range(L)])          # [L, kv]
+    tol, lse_tol = np.zeros_like(out), np.zeros_like(lse)
+    for h in range(c["heads"]):
+        g = h // G
+        a = scale * q[:, h] @ k[:, g].T
+        a[np.arange(L)[None] > (L - n + np.arange(n))[:, None]] = -np.inf
+        pe = np.exp(a - lse[:, h:h + 1]) * e[:, g]
+        rounding = np.where(pe > 0, np.maximum(2.0 ** -11 * pe, 2.0 ** -31.5 * pe.max(1, keepdims=True)), 0.0)
+        off = (2 * c["dim"] * 2.0 ** -24 + 2.0 ** -21) * scale * (np.abs(q[:, h]) @ np.abs(k[:, g]).T).max(1)
+        tol[:, h] = rounding @ np.abs(v[:, g] / e[:, g, None]) + W[:, h] * (2 * off + (L + 64) * 2.0 ** -23)[:, None]
+        lse_tol[:, h] = 2 * off + (L + 64) * 2.0 ** -23 + 2.0 ** -21 * (1 + np.abs(lse[:, h]))
+    return out, lse, tol, lse_tol
+
+
+@pytest.mark.parametrize("n", [3, 100])
+@pytest.mark.parametrize("low", [-6, -12, -20, -24])
+def test_dims_that_only_blocks_of_small_scales_hold(n, low):
+    """Half of the dims are zero in every block of a large scale: what they get comes from the blocks of small ones."""
+    c = cache_case([500], [n], 2, 4, 128, seed=70)
+    k, v, s = D.kv8_views(c["cache"], 2, 128)
+    v[:, :, ::2, ::2] = 0
+    s[:, :, 1, ::2], s[:, :, 1, 1::2] = 1.0, 2.0 ** low
+    place(c)
+    out, lse, bits = _attention(c)
+    want = _bounds_by_scale(c)
+    assert np.abs(want[0][..., ::2]).min() > 0
+    check(out, lse, want)
+    assert bits == 0
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_a_scale_that_a_token_taken_back_has_left(n):
+    """A block whose scale is 2^14 times what its values need, its codes far below the largest."""
+    c = cache_case([400], [n], 1, 4, 64, seed=71)
+    k, v, s = D.kv8_views(c["cache"], 1, 64)
+    pg = int(c["table"][0, 2])
+    x = v[pg, 0, 1].float()
+    v[pg, 0, 1] = (x * 2.0 ** -14).to(torch.float8_e4m3fn)
+    s[pg, 0, 1, 1] *= 2.0 ** 14
+    place(c)
+    out, lse, bits = _attention(c)
+    check(out, lse, _bounds_by_scale(c))
+    assert bits == 0
