@@ -175,6 +175,10 @@ template <int R> __device__ __forceinline__ void fewer_registers() { asm volatil
 constexpr int kMaxStages = 10;
 constexpr int kItems = 2;                                  // laid out ahead
 constexpr int kMasked = 4;                                 // steps of an item that some rows see in part, at most
+// Barriers of the first tile's masked steps, in turn.  Its softmax does a step's once the step before is done, whose S
+// is issued two turns after the second tile's MMAs were three steps behind: it is at most two steps ahead of them, and
+// a barrier comes to its next phase when the last one has been seen.
+constexpr int kCleans = 4;
 
 struct Pipe {
     uint64_t q_full[2], q_empty[2];                        // by tile
@@ -182,6 +186,7 @@ struct Pipe {
     uint64_t s_full[2], o_done[2];                         // by S, by tile
     uint64_t p_full[2][2];                                 // by S: the first 64 keys' P, the others'
     uint64_t turn[2];                                      // by tile: its warp may issue a step's last MMAs
+    uint64_t clean[kCleans];                               // a masked step's values are finite
     uint64_t drain[2];
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
@@ -266,18 +271,20 @@ struct Ring {
 
 // The warp that issues tile x's MMAs.  S: kDim, kTiles, kPart, kParts, kStage, kStages, s(i) and
 // o(i) (TMEM columns), kIdQK and kIdPV, kValuesMn (values lie with their dims side by side: an
-// MN-major operand; else their tokens), kTurns, kCut (items may be pieces).  A warp a tile, as its own waits and the time that
-// operands take to uniform registers (an MMA of 128 x 128 x 16 runs 64 cycles and is issued in
-// 80 to 100) would bound the kernel if one warp issued for both.  With kTurns the tiles take turns
-// with a step's last MMAs, which keeps them out of step: one's softmax runs beside the other's
-// MMAs (1 x 8192 tokens: 892 us without, 812 with).
+// MN-major operand; else their tokens), kTurns, kCut (items may be pieces), kCleans (the first
+// tile's threads take values that are not finite out of the steps that they mask, before either
+// tile's MMAs read them).  A warp a tile, as its own waits and the time that operands take to
+// uniform registers (an MMA of 128 x 128 x 16 runs 64 cycles and is issued in 80 to 100) would
+// bound the kernel if one warp issued for both.  With kTurns the tiles take turns with a step's
+// last MMAs, which keeps them out of step: one's softmax runs beside the other's MMAs (1 x 8192
+// tokens: 892 us without, 812 with).
 // TMEM is the kernel's alone: all 512 columns, from column 0.
 template <class S>
 __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, uint32_t r0, int tokens) {
     static_assert(S::kStages <= kMaxStages && 2 * S::kParts < S::kStages, "a step's values and the next one's keys are held at once");
     Pipe* m = me.m;
     const uint32_t lead = me.lane == 0;
-    uint32_t t = 0, items = 0, turns = 0;                  // the tile's steps, items with a Q, and turns, so far
+    uint32_t t = 0, items = 0, turns = 0, cleaned = 0;     // the tile's steps, items with a Q, turns and the first tile's masked steps, so far
     Ring<S> ring;
     bool ok = true;
     Item it;
@@ -286,6 +293,7 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
         auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };      // so that the compiler knows it for the warp's
         const int steps = same(it.steps(x, tokens));
         const int most = S::kTiles == 2 ? same(max(it.steps(0, tokens), it.steps(1, tokens))) : steps;
+        const int clean_from = S::kCleans && x == 1 ? same(it.masked_from()) : INT32_MAX, clean_to = S::kCleans ? same(it.steps(0, tokens)) : 0;
         auto full = [&](Place<S> p) {
 #pragma unroll
             for (int i = 0; i < S::kParts; ++i, p.next()) ok = ok && me.wait_all(&m->kv_full[p.stage], p.phase);
@@ -339,6 +347,10 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
             if constexpr (S::kTiles == 2) {
                 full(vp);
                 if (more) full(np);
+                if (S::kCleans && i >= clean_from && i < clean_to) {
+                    ok = ok && me.wait_all(&m->clean[cleaned % kCleans], cleaned / kCleans);
+                    ++cleaned;
+                }
                 if (i < steps) {
                     ok = ok && me.wait_all(&m->p_full[x][0], t);
                     tc_fence_after();

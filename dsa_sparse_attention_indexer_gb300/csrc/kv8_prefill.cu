@@ -83,6 +83,7 @@ template <int D> struct TcShape {
     static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
     static constexpr uint32_t kIdQK = idesc_f16_f32(128, kKeys, false, false), kIdPV = idesc_f16_f32(128, kPart, false, false);
     static constexpr bool kValuesMn = false;
+    static constexpr bool kCleans = false;                 // the converters do
     static constexpr bool kCut = true;
     static constexpr bool kTurns = false;                  // 994 us without, 1069 with it: what the converters make comes in step
     static constexpr uint32_t s(int i) { return 128 * i; }

@@ -95,6 +95,7 @@ template <int D> struct Shape {
     static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
     static constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, kPart, true);
     static constexpr bool kValuesMn = true;
+    static constexpr bool kCleans = kTiles == 2;
     // TMEM columns
     static constexpr bool kCut = false;
     static constexpr bool kTurns = true;
@@ -109,15 +110,16 @@ __device__ __forceinline__ uint32_t odd2(uint32_t w) { return __vcmpeq2(w & 0x7f
 
 // Takes infinite and NaN values of a masked step's keys from `from` on out of its stages and
 // notes their keys; by the 128 threads of a tile, before their P says that the step's values
-// may be read.  Masked is what some row of the item does not see, whichever tile it is in, and
-// the other tile's threads do the same, to the same end: no MMA of the step reads what has not
-// been taken out, and a row gets such a value in the end whether its P was 0 or not.
+// may be read.  Masked is what some row of the item does not see.  The steps that the first
+// tile sees are its threads' work, for which both tiles' MMAs wait: none reads what has not been
+// taken out, and a row gets such a value in the end whether its P was 0 or not.
 template <class S>
 __device__ __noinline__ bool clean_values(const Role& me, uint8_t* ring, Place<S> vp, int from, int masked, int k, int thread) {
     Pipe* m = me.m;
     for (int p = 0; p < S::kParts; ++p, vp.next()) {
         if (!me.wait_all(&m->kv_full[vp.stage], vp.phase)) return false;
         uint8_t* stage = ring + vp.stage * S::kStage;
+        bool found = false;
 #pragma unroll 4
         for (int e = thread; e < (kKeys - from) * (S::kPart / 8); e += 128) {  // a key's 8 pieces of 16 bytes of each 64 dims
             const int key = from + (e >> 3) % (kKeys - from), box = (e >> 3) / (kKeys - from);
@@ -125,14 +127,13 @@ __device__ __noinline__ bool clean_values(const Role& me, uint8_t* ring, Place<S
             const uint4 w = *at;
             const uint4 o = make_uint4(odd2(w.x), odd2(w.y), odd2(w.z), odd2(w.w));
             if (o.x | o.y | o.z | o.w) {
-                // (noted before it is taken out: who does not find it any more has it noted)
                 if (masked < kMasked) atomicOr(&m->odd[k % kItems][masked][key >> 5], 1u << (key & 31));
                 m->any_odd[k % kItems] = 1;
-                __threadfence_block();
                 *at = make_uint4(w.x & ~o.x, w.y & ~o.y, w.z & ~o.z, w.w & ~o.w);
+                found = true;
             }
         }
-        fence_proxy_async_smem();                          // of a thread that found one taken out as well
+        if (found) fence_proxy_async_smem();
     }
     __syncwarp();
     return true;
@@ -165,6 +166,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             mbar_init(&misc->turn[i], 1);
             for (int h = 0; h < 2; ++h) mbar_init(&misc->p_full[i][h], 4);
         }
+        for (int i = 0; i < kCleans; ++i) mbar_init(&misc->clean[i], 4);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&misc->item_full[i], 1);
             mbar_init(&misc->item_empty[i], S::kSoft + S::kTiles + 1);  // the softmax warps and those of the MMAs and the copies
@@ -194,7 +196,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const int tok_of = row / a.group, head_of = row % a.group;
         const int heads = a.kv_heads * a.group;
-        uint32_t t = 0;                                    // steps so far
+        uint32_t t = 0, cleaned = 0;                       // steps, and of them masked ones of the first tile, so far
         Ring<S> at;                                        // where the steps' values are
         Item it;
         bool ok = true;
@@ -202,6 +204,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0);
             const int all_see = it.see(it.tok0);           // keys that all of the item's rows see
             const int count = it.count(x, a.tokens), steps = it.steps(x, a.tokens);
+            const int others = x == 0 ? 0 : it.steps(0, a.tokens);     // steps that the first tile cleans
             const int tok = it.tok0 + x * a.tokens + tok_of;
             const bool live = tok_of < count;              // tok_of < a.tokens too
             const int see = live ? it.see(tok) : INT32_MAX;
@@ -211,9 +214,13 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             for (int i = 0; ok && i < steps; ++i, ++t) {
                 at.step(i + 1 < most, vp, np);
                 const int s = S::kTiles == 2 ? x : t & 1;
-                if (all_see < (i + 1) * kKeys) {
+                if (i >= others && all_see < (i + 1) * kKeys) {
                     ok = clean_values<S>(me, ring, vp, max(0, all_see - i * kKeys), i - it.masked_from(), k, (warp & 3) * 32 + lane);
                     if (!ok) break;
+                    if (S::kCleans && x == 0) {
+                        if (lane == 0) mbar_arrive(&misc->clean[cleaned % kCleans]);
+                        ++cleaned;
+                    }
                 }
                 ok = me.wait_all(&misc->s_full[s], S::kTiles == 2 ? t : t >> 1);
                 if (!ok) break;
