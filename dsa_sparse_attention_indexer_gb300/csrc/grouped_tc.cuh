@@ -37,6 +37,8 @@ struct Item {
     __device__ __forceinline__ int steps(int x, int tokens) const { return max(0, min(all_steps(x, tokens), to) - from); }
     // the first step that some row of the item sees in part or not at all, counted from the piece's first
     __device__ __forceinline__ int masked_from() const { return see(tok0) / kKeys - from; }
+    // The first step whose values tile x's threads clean: of masked steps, the first tile's that it has, the second's the others.
+    __device__ __forceinline__ int cleans_from(int x, int tokens) const { return x == 0 ? masked_from() : max(masked_from(), steps(0, tokens)); }
 };
 
 // MMAs and commits of one lane, `lead`, of a warp that runs them together: in control flow
@@ -175,9 +177,8 @@ template <int R> __device__ __forceinline__ void fewer_registers() { asm volatil
 constexpr int kMaxStages = 10;
 constexpr int kItems = 2;                                  // laid out ahead
 constexpr int kMasked = 4;                                 // steps of an item that some rows see in part, at most
-// Barriers of the first tile's masked steps, in turn.  Its softmax does a step's once the step before is done, whose S
-// is issued two turns after the second tile's MMAs were three steps behind: it is at most two steps ahead of them, and
-// a barrier comes to its next phase when the last one has been seen.
+// Barriers of the first tile's masked steps, in turn: its softmax is up to two steps ahead of the second tile's MMAs,
+// and a barrier must not be in its next but one phase when a wait for one is made.
 constexpr int kCleans = 4;
 
 struct Pipe {
@@ -186,7 +187,8 @@ struct Pipe {
     uint64_t s_full[2], o_done[2];                         // by S, by tile
     uint64_t p_full[2][2];                                 // by S: the first 64 keys' P, the others'
     uint64_t turn[2];                                      // by tile: its warp may issue a step's last MMAs
-    uint64_t clean[kCleans];                               // a masked step's values are finite
+    uint64_t here;                                         // with one tile: a masked step's values are there
+    uint64_t clean[kCleans];                               // with two: ... and are finite
     uint64_t drain[2];
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
@@ -271,13 +273,12 @@ struct Ring {
 
 // The warp that issues tile x's MMAs.  S: kDim, kTiles, kPart, kParts, kStage, kStages, s(i) and
 // o(i) (TMEM columns), kIdQK and kIdPV, kValuesMn (values lie with their dims side by side: an
-// MN-major operand; else their tokens), kTurns, kCut (items may be pieces), kCleans (the first
-// tile's threads take values that are not finite out of the steps that they mask, before either
-// tile's MMAs read them).  A warp a tile, as its own waits and the time that operands take to
-// uniform registers (an MMA of 128 x 128 x 16 runs 64 cycles and is issued in 80 to 100) would
-// bound the kernel if one warp issued for both.  With kTurns the tiles take turns with a step's
-// last MMAs, which keeps them out of step: one's softmax runs beside the other's MMAs (1 x 8192
-// tokens: 892 us without, 812 with).
+// MN-major operand; else their tokens), kTurns, kCut (items may be pieces), kCleans (the
+// softmax threads take values that are not finite out of masked steps, before MMAs read them).
+// A warp a tile, as its own waits and the time that operands take to uniform registers (an MMA of
+// 128 x 128 x 16 runs 64 cycles and is issued in 80 to 100) would bound the kernel if one warp
+// issued for both.  With kTurns the tiles take turns with a step's last MMAs, which keeps them out
+// of step: one's softmax runs beside the other's MMAs (1 x 8192 tokens: 892 us without, 812 with).
 // TMEM is the kernel's alone: all 512 columns, from column 0.
 template <class S>
 __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, uint32_t r0, int tokens) {
@@ -293,7 +294,7 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
         auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };      // so that the compiler knows it for the warp's
         const int steps = same(it.steps(x, tokens));
         const int most = S::kTiles == 2 ? same(max(it.steps(0, tokens), it.steps(1, tokens))) : steps;
-        const int clean_from = S::kCleans && x == 1 ? same(it.masked_from()) : INT32_MAX, clean_to = S::kCleans ? same(it.steps(0, tokens)) : 0;
+        const int masked = S::kCleans ? same(it.masked_from()) : 0, cleaned_to = S::kCleans && S::kTiles == 2 && x == 1 ? same(it.steps(0, tokens)) : 0;
         auto full = [&](Place<S> p) {
 #pragma unroll
             for (int i = 0; i < S::kParts; ++i, p.next()) ok = ok && me.wait_all(&m->kv_full[p.stage], p.phase);
@@ -347,7 +348,7 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
             if constexpr (S::kTiles == 2) {
                 full(vp);
                 if (more) full(np);
-                if (S::kCleans && i >= clean_from && i < clean_to) {
+                if (S::kCleans && i >= masked && i < cleaned_to) {     // the second tile's, by the first one's threads
                     ok = ok && me.wait_all(&m->clean[cleaned % kCleans], cleaned / kCleans);
                     ++cleaned;
                 }
@@ -380,6 +381,7 @@ __device__ __forceinline__ void issue_mmas(const Role& me, int x, uint32_t q0, u
                     free_stages(np);
                 }
                 full(vp);
+                if (S::kCleans && i >= masked && ok && lead) mbar_arrive(&m->here);
                 for (int h = 0; h < 2; ++h) {
                     ok = ok && me.wait_all(&m->p_full[t & 1][h], t >> 1);
                     tc_fence_after();

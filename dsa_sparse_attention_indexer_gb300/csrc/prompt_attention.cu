@@ -95,7 +95,7 @@ template <int D> struct Shape {
     static constexpr int kSmem = kQ + kStages * kStage + 2048 + 1024;
     static constexpr uint32_t kIdQK = idesc_bf16(128, kKeys, false), kIdPV = idesc_bf16(128, kPart, true);
     static constexpr bool kValuesMn = true;
-    static constexpr bool kCleans = kTiles == 2;
+    static constexpr bool kCleans = true;
     // TMEM columns
     static constexpr bool kCut = false;
     static constexpr bool kTurns = true;
@@ -114,10 +114,8 @@ __device__ __forceinline__ uint32_t odd2(uint32_t w) { return __vcmpeq2(w & 0x7f
 // tile sees are its threads' work, for which both tiles' MMAs wait: none reads what has not been
 // taken out, and a row gets such a value in the end whether its P was 0 or not.
 template <class S>
-__device__ __noinline__ bool clean_values(const Role& me, uint8_t* ring, Place<S> vp, int from, int masked, int k, int thread) {
-    Pipe* m = me.m;
+__device__ __noinline__ void clean_values(Pipe* m, uint8_t* ring, Place<S> vp, int from, int masked, int k, int thread) {
     for (int p = 0; p < S::kParts; ++p, vp.next()) {
-        if (!me.wait_all(&m->kv_full[vp.stage], vp.phase)) return false;
         uint8_t* stage = ring + vp.stage * S::kStage;
         bool found = false;
 #pragma unroll 4
@@ -136,7 +134,6 @@ __device__ __noinline__ bool clean_values(const Role& me, uint8_t* ring, Place<S
         if (found) fence_proxy_async_smem();
     }
     __syncwarp();
-    return true;
 }
 
 template <int D>
@@ -166,6 +163,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             mbar_init(&misc->turn[i], 1);
             for (int h = 0; h < 2; ++h) mbar_init(&misc->p_full[i][h], 4);
         }
+        mbar_init(&misc->here, 1);
         for (int i = 0; i < kCleans; ++i) mbar_init(&misc->clean[i], 4);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&misc->item_full[i], 1);
@@ -196,15 +194,14 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const int tok_of = row / a.group, head_of = row % a.group;
         const int heads = a.kv_heads * a.group;
-        uint32_t t = 0, cleaned = 0;                       // steps, and of them masked ones of the first tile, so far
+        uint32_t t = 0, cleaned = 0;                       // steps, and of them those whose values its threads clean, so far
         Ring<S> at;                                        // where the steps' values are
         Item it;
         bool ok = true;
         for (int k = 0; ok && me.take<S::kCut>(k, it); ++k) {
             const int most = max(it.steps(0, a.tokens), S::kTiles == 2 ? it.steps(1, a.tokens) : 0);
-            const int all_see = it.see(it.tok0);           // keys that all of the item's rows see
+            const int all_see = it.see(it.tok0), clean_from = it.cleans_from(x, a.tokens);       // keys that all of the item's rows see
             const int count = it.count(x, a.tokens), steps = it.steps(x, a.tokens);
-            const int others = x == 0 ? 0 : it.steps(0, a.tokens);     // steps that the first tile cleans
             const int tok = it.tok0 + x * a.tokens + tok_of;
             const bool live = tok_of < count;              // tok_of < a.tokens too
             const int see = live ? it.see(tok) : INT32_MAX;
@@ -214,13 +211,22 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
             for (int i = 0; ok && i < steps; ++i, ++t) {
                 at.step(i + 1 < most, vp, np);
                 const int s = S::kTiles == 2 ? x : t & 1;
-                if (i >= others && all_see < (i + 1) * kKeys) {
-                    ok = clean_values<S>(me, ring, vp, max(0, all_see - i * kKeys), i - it.masked_from(), k, (warp & 3) * 32 + lane);
-                    if (!ok) break;
-                    if (S::kCleans && x == 0) {
-                        if (lane == 0) mbar_arrive(&misc->clean[cleaned % kCleans]);
-                        ++cleaned;
+                if (i >= clean_from) {
+                    // The step's values have to be there.  A wait for some of a stage's phases only takes the one before the
+                    // last for the one that it is for, unless the last one has been.  With two tiles it has when the
+                    // scores of the step before, or of the first, are there: the MMA warp has waited for every stage up
+                    // to their keys.  With one tile the last phase may be the values of the step before, of which no
+                    // score tells; the MMA warp, which waits for each phase, does.
+                    if (S::kTiles == 1) {
+                        ok = me.wait_all(&misc->here, cleaned);
+                    } else {
+                        static_assert(S::kTiles == 1 || (S::kParts == 1 && S::kStages >= 3), "a step's values are three stages behind the keys of the step before");
+                        ok = (i > 0 || me.wait_all(&misc->s_full[s], t)) && me.wait_all(&misc->kv_full[vp.stage], vp.phase);
                     }
+                    if (!ok) break;
+                    clean_values<S>(misc, ring, vp, max(0, all_see - i * kKeys), i - it.masked_from(), k, (warp & 3) * 32 + lane);
+                    if (S::kTiles == 2 && x == 0 && lane == 0) mbar_arrive(&misc->clean[cleaned % kCleans]);
+                    ++cleaned;
                 }
                 ok = me.wait_all(&misc->s_full[s], S::kTiles == 2 ? t : t >> 1);
                 if (!ok) break;

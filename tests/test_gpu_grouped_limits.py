@@ -172,6 +172,37 @@ def test_infinite_values_behind_probabilities_of_zero_in_long_prompts():
     assert all(torch.equal(x, again[0]) for x in again)
 
 
+@pytest.mark.parametrize("n,past,heads,dim", [
+    ([96, 1, 7], [5, 1205, 984], 64, 256),                  # one tile of rows: a step's values come behind the next one's keys
+    ([1] * 30, [0, 253, 0, 161, 282, 316, 140, 186, 859, 357] * 3, 64, 256),
+    ([200, 100, 130, 40, 300], [1000, 0, 700, 30, 5], 32, 256),
+    ([300, 60, 129, 257, 40] * 6, [700, 0, 5, 300, 0] * 6, 8, 128),            # second tiles without rows between others
+    ([300, 130, 129, 257, 140] * 6, [900, -130, 500, -120, -10] * 6, 16, 64),  # and first tiles that see nothing
+])
+def test_what_lies_behind_a_sequence_reaches_none_of_its_rows(n, past, heads, dim):
+    """Every other sequence, and the rows behind the last one, of NaN keys and infinite or NaN values: the rows of the sequences
+    between them get the same bits as with finite ones there, call after call."""
+    g = torch.Generator().manual_seed(97)
+    L = [max(0, a + b) for a, b in zip(n, past)]
+    T, K = sum(n), sum(L)
+    q, k, v = (torch.randn(rows, heads, dim, generator=g).to(torch.bfloat16).to(DEV) for rows in (T, K + 5, K + 5))
+    starts, ends = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (n, L))
+    batch = D.PromptBatch(torch.tensor(starts, device=DEV), torch.tensor(ends, device=DEV), max_q_len=max(n), max_k_len=max(L) + 5, total_q=T,
+                          total_k=K + 5)
+    row, key = (torch.repeat_interleave(torch.arange(len(n)), torch.tensor(x)).to(DEV) for x in (n, L))
+    behind = torch.full((5,), len(n), device=DEV)
+    key = torch.cat([key, behind])
+    plain = D.dsa_prompt_attention(q, k, v, batch, out_dtype=D.DTYPE_F32)
+    assert torch.isfinite(plain).all()
+    for odd in (0, 1):
+        bad = (key % 2 == odd) | (key == len(n))
+        for fill in (float("inf"), float("nan")):
+            kk, vv = k.masked_fill(bad[:, None, None], float("nan")), v.masked_fill(bad[:, None, None], fill)
+            for _ in range(25):
+                out = D.dsa_prompt_attention(q, kk, vv, batch, out_dtype=D.DTYPE_F32)
+                assert torch.equal(out[row % 2 != odd], plain[row % 2 != odd])
+
+
 PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
 
 
