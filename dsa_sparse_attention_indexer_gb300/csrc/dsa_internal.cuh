@@ -122,7 +122,7 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Limit of the pipeline waits of later launches that take it (the decode
-// score and the dense MLA kernel); 2 s unless dsa_debug_set_wait_limit_ns changed it.
+// score, dense MLA and grouped-head attention kernels); 2 s unless dsa_debug_set_wait_limit_ns changed it.
 uint64_t wait_limit_ns();
 
 // Programmatic dependent launch.  A kernel launched by launch_pdl may begin

@@ -155,6 +155,9 @@ inline int heads_of_run(int kv_heads, int64_t bytes) { return (int)std::max<int6
 // has its first copies late.  Dealt and not, in us: 16 prompts of up to 512 tokens (14 rounds)
 // 76.4, 81.9; 2 x 4096 tokens of 256 dims (27 rounds) 939, 972; 2048 tokens over 16384 in the cache (3.4
 // rounds, 430 steps a CTA) 993, 1041; 4 x 2048 tokens of 64 dims (3.5 rounds, 55 steps) 68.8, 64.8.
+// Between these, in a graph: 2 x 4096 of 2 key heads (3.4 rounds, 108 steps) 129, 148; 8 x 512 (6.7
+// rounds) 68.8, 69.5; 2 x 1024 (3.4, 27) 48.7, 52.1 and 4 x 2048 of 64 dims of equal lengths (3.4, 54) 72.4,
+// 78.4, which the rule has wrong; 1 x 4096 of 2 key heads (1.7, 54) 77.0, 57.8.
 constexpr int kDealtRounds = 4, kDealtSteps = 100;
 inline bool deals(int64_t items, int64_t longest, int64_t ctas) {
     return items > ctas && (items > kDealtRounds * ctas || items * (longest / kKeys) > kDealtSteps * ctas);

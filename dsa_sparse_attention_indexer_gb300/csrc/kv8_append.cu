@@ -14,8 +14,10 @@
 // the block is not all new, reads, mends and writes) them as whole 16-byte pieces.
 //
 // What bounds it: 7 x 1024 tokens of 64 + 8 + 8 heads take 62 us, 4.5 TB/s, 67 % of a copy's
-// rate: two thread blocks an SM, each loading, then computing, then storing.  One token takes
-// 4.9 us on the GPU, 128 of as many requests 6.2: a chain of loads (length, page, scale, codes).
+// rate: two thread blocks an SM, each loading, then computing, then storing, with the load and
+// store pipe's wavefronts at 68 % of their peak (at 128 dims 60 bytes a thread spill at the 128
+// registers that two blocks leave).  One token takes 5.0 us on the GPU, 128 of as many requests
+// 6.2: a chain of loads (length, page, scale, codes).
 //
 // An angle is a whole number: f_i / 2 pi as a 64-bit fraction of a turn, times the
 // position, modulo 2^64.  The fraction is formed from 106 bits of f_i / 2 pi, so that it

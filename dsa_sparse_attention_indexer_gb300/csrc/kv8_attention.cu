@@ -22,10 +22,12 @@
 // reference, sum and O^T, and are joined behind the share's part of a row block; a row
 // block that several shares hold leaves one partial each, joined by a second kernel.
 //
-// Measured: 64 rows of 8 x 8 heads of 128 dims on 32768 tokens 682 us (6.3 TB/s, 93 % of a copy);
-// one row on 8192 16.7 us, two launches and a chain of loads; 16 x 6 tokens of 16 heads
-// of 256 dims on 16381 160 us (3.3 TB/s, half of a copy): the chain of 24 rows' products and their
-// softmax, 2,900 cycles a page of 33 KB, with the tensor pipe 37 % busy.
+// Measured: 64 rows of 8 x 8 heads of 128 dims on 32768 tokens 680 us (6.3 TB/s, 93 % of a copy), of
+// 64 dims 621 (3.5 TB/s); one row on 8192 16.7 us, two launches and a chain of loads; 16 x 6 tokens
+// of 16 heads of 256 dims on 16381 162 us (3.2 TB/s, half of a copy): the chain of 24 rows' products and
+// their softmax, 2,900 cycles a page of 33 KB, with the tensor pipe 37 % busy.  The shapes of 128
+// and 256 dims spill 72 to 164 bytes a thread, but for <128, 2, 1>.  All requests of a call have
+// the columns of its longest: 63 rows on 32768 beside a chunk, whose columns are 64, take 2.2 ms.
 //
 // P is held in fp16 against a reference per column and warp: a score and the exponent of
 // its block's values, such that that position's P is 2^kFirst; it is renewed, and O^T

@@ -18,13 +18,14 @@
 // Warps: softmax as there; then a warpgroup with one warp each for a tile's MMAs, the items and
 // Q's copies; then the converters.
 //
-// What bounds it: 2048 tokens of 64 heads of 128 dims over 16384 take 990 us (1.04 PFLOP/s, 54 % of
+// What bounds it: 2048 tokens of 64 heads of 128 dims over 16384 take 984 to 993 us (1.05 PFLOP/s, 55 % of
 // a library's product).  A step of both tiles is 4,300 cycles: of them 2,048 MMAs, 2,440 a tile's
 // softmax (traced with the clock), and the converters, four warps with a stage's codes in their registers, are busy
 // for 3,700.  Without their work the kernel takes 12 % less.  (Half of them for keys and half
 // for values: 1563 us, as registers spill and a stage is held for a whole step while it is
 // written.)  At 256 dims the converters bound it, 6,600 cycles a step: 512 rows of 32 heads over
-// 32768 take 887 us (614 TFLOP/s; 936 with 104 registers a converter, which spill).
+// 32768 take 874 to 887 us (614 to 624 TFLOP/s; 936 with 104 registers a converter, which spill).  At 64
+// dims 2048 tokens over 16384 take 770 us, no unit being more than 43 % busy.
 #include <algorithm>
 
 #include "grouped_tc.cuh"
@@ -85,7 +86,7 @@ template <int D> struct TcShape {
     static constexpr bool kValuesMn = false;
     static constexpr bool kCleans = false;                 // the converters do
     static constexpr bool kCut = true;
-    static constexpr bool kTurns = false;                  // 994 us without, 1069 with it: what the converters make comes in step
+    static constexpr bool kTurns = false;                  // 2048 over 16384: 979 us without, 993 with it, 1024 over 8192 288 and 280, at 64 dims 769 and 719
     static constexpr uint32_t s(int i) { return 128 * i; }
     static constexpr uint32_t o(int i) { return 256 + 128 * i; }
 };

@@ -19,17 +19,22 @@
 // and tile pair's rows).  A row's probability of a key that it does not see is 0, and 0
 // times an infinite or NaN value would not be: in a step that some rows see in part the
 // softmax threads take those values out of shared memory before the MMA, and they join
-// the rows that see them in the end.
+// the rows that see them in the end.  (The first tile's threads do it for both tiles, 4 x ~2048
+// tokens of 64 dims 66 us; each tile for itself 71.  They wait for the values' copy themselves
+// where there are two tiles; told by the MMA warp, as with one, 72.)
 //
 // O is rescaled only when a row's largest score passes its reference by 2^8.
 //
 // What bounds it: the chain of a tile's softmax and MMAs, which overlaps the other tile's in
-// part.  1 x 8192 tokens of 64 heads of 128 dims take 787 to 802 us (1.38 PFLOP/s, 72 % of a
+// part.  1 x 8192 tokens of 64 heads of 128 dims take 781 to 786 us (1.40 PFLOP/s, 73 % of a
 // library's product), a step of both tiles about 3,300 cycles of which 2,048 are MMAs
-// (tensor pipe 57 % busy).  At 256 dims there is one tile, whose softmax and MMAs follow one
-// another but for S of the next step; 2 x 4096 tokens of 64 heads 939 to 966 us (1.07 PFLOP/s).
-// Short prompts are bound by an item's two ends, about 4,000 cycles: 16 of up to 512 tokens
-// 76 to 79 us, one of 129 9.6 on the GPU.
+// (tensor pipe 57 % busy).  At 64 dims a step's softmax is as long beside half of the MMAs: 4 x
+// ~2048 tokens of 16 heads 66 us (tensor pipe and exponentials 26 % busy each).  At 256 dims
+// there is one tile, whose softmax and MMAs follow one another but for S of the next step; 2 x
+// ~4096 tokens of 64 heads 975 to 987 us (1.05 PFLOP/s).  Short prompts are bound by an item's two
+// ends, about 4,000 cycles: 16 of up to 512 tokens 81 us, one of 129 10.0 on the GPU.  A few
+// queries behind long keys leave SMs idle, as items are not cut along the keys: one query of 8
+// key heads behind 8192 keys 87 us.
 #include <algorithm>
 
 #include <cudaTypedefs.h>

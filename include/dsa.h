@@ -664,7 +664,10 @@ dsa_status dsa_kv8_append(const dsa_heads* k, const dsa_heads* v, const dsa_head
  *   h * kv_heads / heads as the codes times their scales, over the positions j <= p:
  *     S_hj = softmax_scale * <q_ih, k_j>,  out_ih = sum_j softmax_j(S_hj) v_j,
  *     lse_ih = log sum_j exp(S_hj)
- *   q_len is 1 for decoding, any for verify and prefill.  A row that sees nothing
+ *   q_len is 1 for decoding, any for verify and prefill.  Requests of at most 64 query
+ *   rows (q_len * heads / kv_heads) and longer ones have a kernel each; beside a longer
+ *   one the short ones take as long as if they had 64 rows (32 of 256 dims), so that
+ *   chunks and decode rows are faster in a call each.  A row that sees nothing
  *   (p < 0) gives out = 0 and lse = -inf.  q is scaled per row by a power of two
  *   and rounded to fp16 (exact, but for values more than 2^39 below the row's
  *   largest), E4M3 is exact in fp16; softmax statistics and accumulation are
