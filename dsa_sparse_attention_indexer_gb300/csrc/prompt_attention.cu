@@ -321,7 +321,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                         if (odd) {
                             // infinite and NaN values of masked steps that this row sees
                             for (int e = 0; e < kMasked * kKeys; ++e) {
-                                const int key = it.masked_from() * kKeys + e;
+                                const int64_t key = (int64_t)it.masked_from() * kKeys + e;
                                 if (!(misc->odd[k % kItems][e / kKeys][e % kKeys / 32] >> (e & 31) & 1) || key >= see) continue;
                                 const uint16_t* v = a.v + (it.k_row + key) * a.v_tok + it.h * a.v_head + c;
 #pragma unroll
